@@ -12,6 +12,7 @@ Build the library with ``python -m delta_rule_memory_gb300.build``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -23,13 +24,16 @@ __all__ = [
     "sdm_scan_noalloc", "sdm_forward_host", "sdm_forward_host_workspace_size", "sdm_scan_train",
     "sdm_scan_backward", "sdm_scan_backward_workspace_size", "sdm_address_backward", "sdm_scan_chunked",
     "sdm_scan_chunked_workspace_size",
-    "gdn_scan", "gdn_scan_workspace_size", "gdn2_scan", "gdn2_scan_workspace_size", "sse_scan", "sse_scan_workspace_size", "SDM_RESID_SHARED", "SDM_RESID_PERSLOT", "SSE_WRITE_ADDITIVE", "SSE_WRITE_DELTA",
+    "gdn_scan", "gdn_scan_workspace_size", "gdn2_scan", "gdn2_scan_workspace_size", "sse_scan", "sse_scan_workspace_size",
+    "glr_scan", "glr_scan_train", "glr_scan_carry_size", "glr_scan_backward", "glr_scan_backward_workspace_size",
+    "ckpt8_pack", "ckpt8_unpack", "SDM_RESID_SHARED", "SDM_RESID_PERSLOT", "SSE_WRITE_ADDITIVE", "SSE_WRITE_DELTA",
     "SDM_RESID_ADDITIVE", "SDM_DEVERR_INDEX_RANGE", "SDM_DEVERR_INDEX_REPEAT", "SDM_DEVERR_NONFINITE",
-    "SDM_DEVERR_TIMEOUT", "SDM_ERR_DEVICE",
+    "SDM_DEVERR_TIMEOUT", "SDM_DEVERR_RATE", "SDM_ERR_DEVICE",
 ]
 
 SDM_OK, SDM_ERR_INVALID_ARG, SDM_ERR_SHAPE, SDM_ERR_ALIGN, SDM_ERR_UNSUPPORTED, SDM_ERR_CUDA, SDM_ERR_DEVICE = range(7)
 SDM_DEVERR_INDEX_RANGE, SDM_DEVERR_INDEX_REPEAT, SDM_DEVERR_NONFINITE, SDM_DEVERR_TIMEOUT = 1, 2, 4, 8
+SDM_DEVERR_RATE = 16
 SDM_DTYPE_F32, SDM_DTYPE_BF16 = 0, 1
 SDM_RESID_SHARED, SDM_RESID_PERSLOT, SDM_RESID_ADDITIVE = 0, 1, 2
 SSE_WRITE_ADDITIVE, SSE_WRITE_DELTA = 0, 1
@@ -39,7 +43,7 @@ library_path = os.path.join(_HERE, "libsdm.so")
 _lock = threading.Lock()
 _lib = None
 
-_P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _SZ, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 _SIGNATURES = {
     "sdm_version": (_I, []),
     "sdm_last_error": (ctypes.c_char_p, []),
@@ -66,6 +70,14 @@ _SIGNATURES = {
     "gdn2_scan": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P, _P]),
     "sse_scan_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "sse_scan": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P, _P]),
+    "glr_scan": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "glr_scan_carry_size": (_SZ, [_I, _I, _I]),
+    "glr_scan_train": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "glr_scan_backward_workspace_size": (_SZ, [_I, _I, _I]),
+    "glr_scan_backward": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P,
+                               _L, _P, _P, _SZ, _P, _P]),
+    "ckpt8_pack": (_I, [_P, _L, _I, _L, _I, _P, _P, _P, _P]),
+    "ckpt8_unpack": (_I, [_P, _P, _L, _I, _P, _L, _I, _P]),
 }
 
 
@@ -534,3 +546,233 @@ def sse_scan(state, route_logits, topk: int, k_logits, q, v, alpha, y=None, sel_
                         workspace.data_ptr(), workspace.numel(), _ptr(dev_err), _stream(stream))
     _check("sse_scan", rc)
     return y
+
+
+_DTYPES = {torch.float32: SDM_DTYPE_F32, torch.bfloat16: SDM_DTYPE_BF16}
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """The device of the call's tensors and its stream (None: that device's
+    current one) as the current ones, so that what the call allocates belongs
+    to the stream that uses it.  Yields the stream's handle."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    if stream is None and device.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream().cuda_stream
+        return
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
+    """Check an activation [..., rows, D] whose channels are contiguous and
+    whose rows lie at one distance (a column slice of a wider contiguous
+    tensor will do); returns that distance in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    D = t.shape[-1]
+    ld = D
+    if t.numel():
+        if D > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}'s channels must be contiguous")
+        rows = 1            # rows that the dimensions walked so far hold
+        for n, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if n == 1:
+                continue
+            if rows == 1:
+                ld = step
+            if step != rows * ld or ld < D:
+                raise ValueError(f"{name}'s rows must lie at one distance of at least {D} elements")
+            rows *= n
+    return ld
+
+
+def _glr_checks(state, x, r, g, rate, reset, lens, like=None):
+    """Common checks of the glr_scan calls; returns B, T, D, the dtype and the
+    row distances of x, r and g (`like`: [B,T,D] tensor in their place)."""
+    first = x if like is None else like
+    _act(first, "x" if like is None else "dy")
+    if first.dim() != 3:
+        raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
+    B, T, D = first.shape
+    lds = (0, 0, 0)
+    if x is not None or like is None:
+        lds = tuple(_act(t, n, first.dtype, (B, T, D), first.device) for t, n in ((x, "x"), (r, "r"), (g, "g")))
+    _req(state, "state" if like is None else "dstate", torch.float32, (B, D))
+    _req(rate, "rate", torch.float32, (D,))
+    if reset is not None:
+        if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
+            reset = reset.view(torch.uint8)
+        _req(reset, "reset", torch.uint8, (B, T))
+    if lens is not None:
+        _req(lens, "lens", torch.int32, (B,))
+    _same_device(first.device, state=state, rate=rate, reset=reset, lens=lens)
+    return B, T, D, first.dtype, lds
+
+
+def _same_device(device, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{n} must be on {device}, got {t.device}")
+
+
+def _err_word(dev_err, device):
+    if dev_err is not None:
+        _req(dev_err, "dev_err", torch.int32)
+        _same_device(device, dev_err=dev_err)
+
+
+def _out(t, name: str, dtype, shape, device):
+    """An output the caller gave, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _req(t, name, dtype, shape)
+    _same_device(device, **{name: t})
+    return t
+
+
+def glr_scan(state, x, r, g, rate, reset=None, lens=None, y=None, state_out=None, dev_err=None, stream=None):
+    """Gated linear recurrence, one state per channel: h_t = a_t h_{t-1} +
+    sqrt(1 - a_t^2) sigmoid(g_t) x_t with a_t = exp(-rate sigmoid(r_t)).
+    x, r, g: bf16 or fp32 [B,T,D], channels contiguous (column slices of one
+    projection will do); rate: fp32 [D], >= 0; reset: uint8 or bool [B,T], 1
+    where a new sequence starts inside a row; lens: int32 [B], tokens that
+    exist.  Updates `state` fp32 [B,D] in place, or leaves it and writes
+    `state_out` where that is given.  Returns y [B,T,D] of x's dtype (rows
+    behind lens are not written).  T = 1 is the step of a decoding loop."""
+    B, T, D, dt, lds = _glr_checks(state, x, r, g, rate, reset, lens)
+    dev = x.device
+    _err_word(dev_err, dev)
+    with _on(dev, stream) as st:
+        y = _out(y, "y", dt, (B, T, D), dev)
+        state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
+        rc = lib().glr_scan(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lds[0], r.data_ptr(), lds[1],
+                            g.data_ptr(), lds[2], _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
+                            y.data_ptr(), _ptr(dev_err), st)
+    _check("glr_scan", rc)
+    return y
+
+
+def glr_scan_carry_size(B: int, T: int, D: int) -> int:
+    return int(lib().glr_scan_carry_size(B, T, D))
+
+
+def glr_scan_train(state, x, r, g, rate, reset=None, lens=None, keep8=False, y=None, state_out=None, carry=None,
+                   ckpt=None, dev_err=None, stream=None):
+    """glr_scan that also returns what glr_scan_backward needs: (y, carry),
+    carry fp32 [B,ceil(T/8),D] being the states before every 8th token; with
+    keep8 (or ckpt, a pair of buffers) (y, carry, (codes, exps)), the 8-bit
+    checkpoints of x, r and g, int8 [3,B,T,D] and uint8 [3,B,T,ceil(D/64)],
+    which the backward takes in place of x, r and g."""
+    B, T, D, dt, lds = _glr_checks(state, x, r, g, rate, reset, lens)
+    dev = x.device
+    _err_word(dev_err, dev)
+    with _on(dev, stream) as st:
+        y = _out(y, "y", dt, (B, T, D), dev)
+        state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
+        carry = _out(carry, "carry", torch.float32, (B, -(-T // 8), D), dev)
+        codes = exps = None
+        if keep8 or ckpt is not None:
+            codes, exps = (None, None) if ckpt is None else ckpt
+            codes = _out(codes, "codes", torch.int8, (3, B, T, D), dev)
+            exps = _out(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)), dev)
+        rc = lib().glr_scan_train(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lds[0], r.data_ptr(), lds[1],
+                                  g.data_ptr(), lds[2], _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
+                                  y.data_ptr(), carry.data_ptr(), _ptr(codes), _ptr(exps), _ptr(dev_err), st)
+    _check("glr_scan_train", rc)
+    return (y, carry) if codes is None else (y, carry, (codes, exps))
+
+
+def glr_scan_backward_workspace_size(B: int, T: int, D: int) -> int:
+    return int(lib().glr_scan_backward_workspace_size(B, T, D))
+
+
+def glr_scan_backward(dstate, x, r, g, rate, carry, dy, reset=None, lens=None, ckpt=None, grads=None,
+                      dstate_out=None, workspace=None, dev_err=None, stream=None):
+    """Gradients of glr_scan_train.  x, r, g as it was given, or None with
+    `ckpt` = the (codes, exps) that it returned; dy [B,T,D] of x's dtype.
+    `dstate` fp32 [B,D] holds dL/dh_T and becomes dL/dh_0 (or stays, with
+    `dstate_out` given).  `grads`: optional (dx, dr, dg) to write, which may be
+    column slices of one buffer.  Returns (dx, dr, dg, drate), drate fp32 [D]."""
+    if ckpt is not None and not (x is None and r is None and g is None):
+        raise ValueError("give x, r and g or ckpt, not both")
+    if ckpt is None and x is None:
+        raise ValueError("x, r and g, or ckpt, are needed")
+    B, T, D, dt, lds = _glr_checks(dstate, x, r, g, rate, reset, lens, like=dy)
+    dev = dy.device
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    _req(carry, "carry", torch.float32, (B, -(-T // 8), D))
+    _same_device(dev, carry=carry)
+    codes = exps = None
+    if ckpt is not None:
+        codes, exps = ckpt
+        _req(codes, "codes", torch.int8, (3, B, T, D))
+        _req(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)))
+        _same_device(dev, codes=codes, exps=exps)
+    _err_word(dev_err, dev)
+    with _on(dev, stream) as st:
+        if grads is None:
+            grads = tuple(torch.empty((B, T, D), dtype=dt, device=dev) for _ in range(3))
+        ld = {_act(t, n, dt, (B, T, D), dev) for t, n in zip(grads, ("dx", "dr", "dg"))}
+        if len(ld) != 1:
+            raise ValueError("dx, dr and dg must have their rows at the same distance")
+        dstate_out = dstate if dstate_out is None else _out(dstate_out, "dstate_out", torch.float32, (B, D), dev)
+        drate = torch.empty((D,), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(glr_scan_backward_workspace_size(B, T, D), 1), dtype=torch.uint8, device=dev)
+        _req(workspace, "workspace", torch.uint8)
+        rc = lib().glr_scan_backward(dstate.data_ptr(), dstate_out.data_ptr(), _ptr(x), lds[0], _ptr(r), lds[1],
+                                     _ptr(g), lds[2], _ptr(codes), _ptr(exps), _DTYPES[dt], rate.data_ptr(),
+                                     _ptr(reset), _ptr(lens), carry.data_ptr(), dy.data_ptr(), B, T, D,
+                                     grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), ld.pop(),
+                                     drate.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_err), st)
+    _check("glr_scan_backward", rc)
+    return (*grads, drate)
+
+
+def ckpt8_pack(x, codes=None, exps=None, dev_err=None, stream=None):
+    """8-bit checkpoint of x, bf16 or fp32 [..., D] (rows at one distance):
+    (codes int8 [..., D], exps uint8 [..., ceil(D/64)]).  Every 64 channels of
+    a row share the smallest power-of-two step that fits them in [-127, 127]."""
+    ld = _act(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    _err_word(dev_err, x.device)
+    with _on(x.device, stream) as st:
+        codes = _out(codes, "codes", torch.int8, x.shape, x.device)
+        exps = _out(exps, "exps", torch.uint8, (*x.shape[:-1], -(-D // 64)), x.device)
+        rc = lib().ckpt8_pack(x.data_ptr(), ld, _DTYPES[x.dtype], rows, D, codes.data_ptr(), exps.data_ptr(),
+                              _ptr(dev_err), st)
+    _check("ckpt8_pack", rc)
+    return codes, exps
+
+
+def ckpt8_unpack(codes, exps, dtype=torch.bfloat16, x=None, stream=None):
+    """The values that a ckpt8_pack checkpoint stands for, as bf16 or fp32
+    (exact in both)."""
+    _req(codes, "codes", torch.int8)
+    if codes.dim() < 1:
+        raise ValueError("codes must be [..., D]")
+    D = codes.shape[-1]
+    _req(exps, "exps", torch.uint8, (*codes.shape[:-1], -(-D // 64)))
+    _same_device(codes.device, exps=exps)
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    with _on(codes.device, stream) as st:
+        if x is None:
+            x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        ld = _act(x, "x", dtype, codes.shape, codes.device)
+        rc = lib().ckpt8_unpack(codes.data_ptr(), exps.data_ptr(), codes.numel() // D if D else 0, D, x.data_ptr(), ld,
+                                _DTYPES[dtype], st)
+    _check("ckpt8_unpack", rc)
+    return x

@@ -47,10 +47,11 @@ extern "C" int sdm_check(const int32_t *dev_err, void *stream) {
   if (rc == SDM_OK) rc = sdm::sticky_sse_chunk(&bits);
   if (rc != SDM_OK) return rc;
   if (bits == 0) return SDM_OK;
-  return sdm::set_error(SDM_ERR_DEVICE, "device error bits 0x%x:%s%s%s%s", static_cast<unsigned>(bits),
+  return sdm::set_error(SDM_ERR_DEVICE, "device error bits 0x%x:%s%s%s%s%s", static_cast<unsigned>(bits),
                         (bits & SDM_DEVERR_INDEX_RANGE) ? " index out of range;" : "",
                         (bits & SDM_DEVERR_INDEX_REPEAT) ? " repeated write slot;" : "",
                         (bits & SDM_DEVERR_NONFINITE) ? " non-finite score or logit;" : "",
                         (bits & SDM_DEVERR_TIMEOUT) ? " a bounded on-device wait gave up (outputs and state invalid);"
-                                                    : "");
+                                                    : "",
+                        (bits & SDM_DEVERR_RATE) ? " a decay rate below zero or not finite;" : "");
 }

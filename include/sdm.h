@@ -64,6 +64,7 @@ extern "C" {
 #define SDM_DEVERR_INDEX_REPEAT 2 /* a slot repeated within one token's write list */
 #define SDM_DEVERR_NONFINITE 4    /* a NaN or infinite score or logit */
 #define SDM_DEVERR_TIMEOUT 8      /* a bounded on-device wait gave up; outputs invalid */
+#define SDM_DEVERR_RATE 16        /* a decay rate of glr_scan below zero or not finite (taken as 0) */
 
 /*
  * A timeout (SDM_DEVERR_TIMEOUT) leaves that call's y AND the state it updated
@@ -89,7 +90,7 @@ extern "C" {
  *       CUDA context stays usable).  Never set in normal use.
  */
 
-/* Element types of the value input of sdm_scan. */
+/* Element types: the value input of sdm_scan; the activations of glr_scan and ckpt8_pack. */
 #define SDM_DTYPE_F32 0
 #define SDM_DTYPE_BF16 1
 
@@ -496,6 +497,132 @@ SDM_API size_t sse_scan_workspace_size(int B, int T, int H, int N, int topk, int
 SDM_API int sse_scan(float *state, const float *route_logits, int topk, const float *k_logits, const uint16_t *q,
              const uint16_t *v, const float *alpha, int write_mode, int B, int T, int H, int N, int c, int d,
              float *y, int32_t *sel_out, void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/*
+ * glr_scan - gated linear recurrence with one state per channel, the scan that
+ * stands beside gdn_scan and sse_scan where a layer keeps no key dimension
+ * (the papers have no counterpart; the formulas are stated here in full).
+ * For every channel c, tokens in order:
+ *   L_t = -rate sigmoid(r_t),  a_t = exp(L_t),  m_t = sqrt(1 - a_t^2)
+ *   h_t = a_t h_{t-1} + m_t sigmoid(g_t) x_t,   y_t = h_t
+ * r is the logit of the recurrence gate, g of the input gate; m_t keeps the
+ * state's variance at that of the input whatever the decay.
+ *
+ * state    : fp32 [B,D], h_0.   state_out : fp32 [B,D], h_T; may be `state`
+ *            itself (the state continues in place), must not overlap it else.
+ * x, r, g  : [B,T,D] of `dtype` (SDM_DTYPE_F32 or SDM_DTYPE_BF16).  Channels
+ *            are contiguous; token t of sequence b starts ld * (b T + t)
+ *            elements behind the pointer, with its own ld >= D for each of the
+ *            three, so they may be column slices of one projection's output.
+ * rate     : fp32 [D], >= 0 and finite; any other value counts as 0 and sets
+ *            SDM_DEVERR_RATE.
+ * reset    : optional uint8 [B,T]; where it is not 0, h_{t-1} is taken as 0 (a
+ *            new document starts at token t of a packed row).
+ * lens     : optional int32 [B], 0 <= lens[b] <= T: only the first lens[b]
+ *            tokens of sequence b exist.  The others are neither read nor
+ *            written (rows of y behind them keep their bits), and h_T is the
+ *            state after the last one that exists.  A value outside [0, T] is
+ *            clamped to it and sets SDM_DEVERR_INDEX_RANGE.
+ * y        : [B,T,D] of `dtype`, contiguous; must not overlap the inputs.
+ * dev_err  : optional.
+ * NaN and infinite x, r, g are not looked for: they run through the
+ * arithmetic, into the states of their channel only.  The state, its
+ * decays and their products are fp32; y is rounded once, to nearest even.
+ * Limits: B, T, D >= 0, B < 65536, T < 2^30, D < 2^24; ld >= D.  x, r, g, y
+ *         aligned to their element; state, rate 4-byte.  Any B, T or D of 0
+ *         is allowed (T = 0 copies the state).
+ */
+SDM_API int glr_scan(const float *state, float *state_out, const void *x, int64_t ld_x, const void *r, int64_t ld_r,
+                     const void *g, int64_t ld_g, int dtype, const float *rate, const uint8_t *reset,
+                     const int32_t *lens, int B, int T, int D, void *y, int32_t *dev_err, void *stream);
+
+/*
+ * Bytes of the states that glr_scan_train keeps for the backward pass: fp32
+ * [B, ceil(T/8), D], the state before every 8th token.  0 for invalid sizes.
+ */
+SDM_API size_t glr_scan_carry_size(int B, int T, int D);
+
+/*
+ * glr_scan_train - glr_scan that also keeps what glr_scan_backward needs: the
+ * states at the start of every segment of 8 tokens, from which the backward
+ * recomputes the others, and, if asked, the inputs in 8 bits.
+ *
+ * Arguments as glr_scan, plus
+ * carry  : fp32 [B, ceil(T/8), D] out, 4-byte aligned; carry[b,s] is the state
+ *          before token 8s (segments that begin at lens[b] or later keep their bits).
+ * codes, exps : both NULL, or both given: int8 [3,B,T,D] and uint8
+ *          [3,B,T,ceil(D/64)] out, the 8-bit checkpoints of x, r and g (planes
+ *          in that order) in the format of ckpt8_pack.  glr_scan_backward then
+ *          takes them in place of x, r and g.  y and h_T do not depend on them.
+ *          SDM_DEVERR_NONFINITE if a group unpacks to NaN.
+ * y, h_T and the error codes are identical to glr_scan's.
+ */
+SDM_API int glr_scan_train(const float *state, float *state_out, const void *x, int64_t ld_x, const void *r,
+                           int64_t ld_r, const void *g, int64_t ld_g, int dtype, const float *rate,
+                           const uint8_t *reset, const int32_t *lens, int B, int T, int D, void *y, float *carry,
+                           int8_t *codes, uint8_t *exps, int32_t *dev_err, void *stream);
+
+/* Scratch bytes glr_scan_backward needs: fp32 partial sums of drate. */
+SDM_API size_t glr_scan_backward_workspace_size(int B, int T, int D);
+
+/*
+ * glr_scan_backward - gradients of glr_scan_train.  With s_r = sigmoid(r_t),
+ * s_g = sigmoid(g_t), tokens last to first:
+ *   dh_t = dy_t + a_{t+1} dh_{t+1}     (dh_T: dy_T + dstate; the second term is
+ *                                       0 where token t+1 resets)
+ *   dx = dh m s_g,   dg = dh m s_g (1 - s_g) x
+ *   dL = a dh (h_{t-1} - (a / m) s_g x),  dr = -rate s_r (1 - s_r) dL
+ *   drate = sum over b and t of -s_r dL,   dL/dh_0 = a_1 dh_1
+ * (h_{t-1} as the forward used it: 0 where token t resets).  Where m_t^2
+ * underflows (rate 0, say) the term with a / m, which has no limit there, is
+ * left out.
+ *
+ * dstate   : fp32 [B,D], dL/dh_T (NULL: zero).  dstate_out : fp32 [B,D],
+ *            dL/dh_0; may be `dstate` itself.
+ * x, r, g, dtype, rate, reset, lens, sizes : as given to glr_scan_train; or,
+ *            with codes and exps as it wrote them, x = r = g = NULL: every
+ *            formula above then takes the values that the checkpoints stand for, and the
+ *            states inside a segment are recomputed from them (its first
+ *            state is the forward's own).
+ * carry    : as glr_scan_train wrote it.
+ * dy       : [B,T,D] of `dtype`, contiguous.
+ * dx,dr,dg : [B,T,D] of `dtype` out, token t of sequence b at ld_d * (b T + t)
+ *            elements, ld_d >= D: they may be column slices of one buffer.
+ *            Rows behind lens[b] keep their bits.
+ * drate    : fp32 [D] out (overwritten).
+ * workspace: glr_scan_backward_workspace_size() bytes, 16-byte aligned;
+ *            contents need no initialisation.  Calls that share one must not
+ *            overlap on the GPU.
+ * Deterministic: sums are formed in a fixed order.
+ */
+SDM_API int glr_scan_backward(const float *dstate, float *dstate_out, const void *x, int64_t ld_x, const void *r,
+                              int64_t ld_r, const void *g, int64_t ld_g, const int8_t *codes, const uint8_t *exps,
+                              int dtype, const float *rate, const uint8_t *reset, const int32_t *lens,
+                              const float *carry, const void *dy, int B, int T, int D, void *dx, void *dr, void *dg,
+                              int64_t ld_d, float *drate, void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                              void *stream);
+
+/*
+ * ckpt8_pack, ckpt8_unpack - activation checkpoints in 8 bits.  Every group of
+ * 64 neighbouring channels of a row (the last one of a row may be shorter)
+ * shares one step 2^e, the smallest power of two with max|x| <= 127 * 2^e and
+ * e >= -126; an element is kept as code = x / 2^e rounded to nearest even, a
+ * whole number in [-127, 127].  The division is exact, so a code is off by at
+ * most half a step and the same on every machine, and the value that it stands
+ * for, code * 2^e, is exact in bf16 and in fp32.  The exponent is kept as
+ * e + 127 (1 .. 248); 255 marks a group that held a NaN, an infinity or a
+ * magnitude above 127 * 2^121 = 3.376e38 (its step would leave fp32's range),
+ * which unpacks to NaN (SDM_DEVERR_NONFINITE).
+ *
+ * x     : [rows, D] of `dtype`, row i at ld * i elements (ld >= D for more
+ *         than one row); aligned to its element.  Unpacked rows may lie apart too.
+ * codes : int8 [rows, D], contiguous.   exps : uint8 [rows, ceil(D/64)].
+ * Limits: rows >= 0, 0 <= D < 2^24.
+ */
+SDM_API int ckpt8_pack(const void *x, int64_t ld, int dtype, int64_t rows, int D, int8_t *codes, uint8_t *exps,
+                       int32_t *dev_err, void *stream);
+SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows, int D, void *x, int64_t ld, int dtype,
+                         void *stream);
 
 #ifdef __cplusplus
 }
