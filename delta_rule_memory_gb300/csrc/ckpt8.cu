@@ -18,8 +18,7 @@ __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = static_cast<
 
 template <class E>
 __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const E *x, int64_t ld, int64_t rows, int D, int G,
-                                                         const int32_t *lens, int T, int8_t *codes, uint8_t *exps,
-                                                         int32_t *err) {
+                                                         int8_t *codes, uint8_t *exps, int32_t *err) {
   const int lane = threadIdx.x & 31;
   const int64_t total = rows * G;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -27,7 +26,6 @@ __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const E *x, int64_t ld,
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); w < total; w += warps) {
     const int64_t row = w / G;
     const int grp = static_cast<int>(w - row * G);
-    if (lens && row % T >= lens[row / T]) continue;  // warp-uniform
     const int c = grp * kGroup + 2 * lane;
     const E *p = x + row * ld + c;
     const float v0 = c < D ? load1(p) : 0.f, v1 = c + 1 < D ? load1(p + 1) : 0.f;
@@ -80,19 +78,6 @@ int check(const char *fn, const void *x, int64_t ld, int dtype, int64_t rows, in
 }
 
 }  // namespace
-
-int launch_ckpt8_pack(const void *x, int64_t ld, int dtype, int64_t rows, int D, const int32_t *lens, int T,
-                      int8_t *codes, uint8_t *exps, int32_t *err, cudaStream_t st) {
-  const int G = ckpt8::groups(D);
-  const unsigned grid = grid_for(rows * G);
-  if (dtype == SDM_DTYPE_F32)
-    ckpt8_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const float *>(x), ld, rows, D, G, lens, T, codes, exps, err);
-  else
-    ckpt8_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(x), ld, rows, D, G, lens, T, codes, exps,
-                                            err);
-  return check_launch("ckpt8_pack");
-}
-
 }  // namespace sdm
 
 using namespace sdm;
@@ -102,7 +87,14 @@ extern "C" int ckpt8_pack(const void *x, int64_t ld, int dtype, int64_t rows, in
   const int rc = check("ckpt8_pack", x, ld, dtype, rows, D, codes, exps);
   if (rc != SDM_OK || rows == 0 || D == 0) return rc;
   if (dev_err && !aligned(dev_err, 4)) return set_error(SDM_ERR_ALIGN, "ckpt8_pack: dev_err must be 4-byte aligned");
-  return launch_ckpt8_pack(x, ld, dtype, rows, D, nullptr, 0, codes, exps, dev_err, static_cast<cudaStream_t>(stream));
+  const int G = ckpt8::groups(D);
+  const unsigned grid = grid_for(rows * G);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SDM_DTYPE_F32)
+    ckpt8_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const float *>(x), ld, rows, D, G, codes, exps, dev_err);
+  else
+    ckpt8_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(x), ld, rows, D, G, codes, exps, dev_err);
+  return check_launch("ckpt8_pack");
 }
 
 extern "C" int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows, int D, void *x, int64_t ld,

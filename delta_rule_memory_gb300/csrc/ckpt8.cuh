@@ -35,10 +35,4 @@ __device__ __forceinline__ uint32_t code_bits(float x, float inv) {
 }
 
 }  // namespace ckpt8
-
-// ckpt8.cu: pack rows of `dtype`; with lens, row i is token i % T of sequence
-// i / T, and rows at lens[b] or behind it are neither read nor written.
-int launch_ckpt8_pack(const void *x, int64_t ld, int dtype, int64_t rows, int D, const int32_t *lens, int T,
-                      int8_t *codes, uint8_t *exps, int32_t *err, cudaStream_t st);
-
 }  // namespace sdm

@@ -14,6 +14,13 @@ reciprocal are good to 2^-22 and 2^-23 (relative).
 Along the recurrence every token adds a's error and a product's and a sum's
 rounding on top of the decayed one; a split over time multiplies decays with
 one another first, one more rounding a token: 4 E a token covers each order.
+What those are relative to: a split forms what the tokens of a run leave and
+what the state before the run leaves as two numbers and adds them at the end,
+a (h + u') as a h + a u', so each rounds by itself and their sum may cancel:
+with h = -u' (1 + d) the exact result is a d u', while the two products are off
+by E |a u'| each, however small d is.  The roundings are therefore relative to
+the same recurrence over absolute values, G_t = a_t G_{t-1} + |u_t|, which
+bounds every partial sum of every split, and not to |h_t|.
 """
 import numpy as np
 
@@ -52,12 +59,15 @@ def forward(h0, x, r, g, rate, reset=None, lens=None):
     y, before = np.zeros((B, T, D)), np.zeros((B, T, D))
     e_y, e_b = np.zeros((B, T, D)), np.zeros((B, T, D))
     h, e = h0.astype(np.float64).copy(), np.zeros((B, D))
+    G = np.abs(h)
     for t in range(T):
         live = np.ones(B, bool) if lens is None else t < lens
         keep = np.ones((B, 1)) if reset is None else (reset[:, t] == 0)[:, None].astype(float)
         before[:, t], e_b[:, t] = h, e
         hn = a[:, t] * h * keep + u[:, t]
-        en = keep * a[:, t] * (e + np.abs(h) * (d_a[:, t] + 4 * E)) + e_u[:, t] + 2 * E * np.abs(hn)
+        Gn = a[:, t] * G * keep + np.abs(u[:, t])
+        en = keep * a[:, t] * (e + G * (d_a[:, t] + 4 * E)) + e_u[:, t] + 2 * E * Gn
+        G = np.where(live[:, None], Gn, G)
         h, e = np.where(live[:, None], hn, h), np.where(live[:, None], en, e)
         y[:, t], e_y[:, t] = h, e
     return dict(y=y, hT=h, before=before, e_y=e_y, e_hT=e, e_before=e_b)
@@ -83,11 +93,14 @@ def backward(f, dhT, x, r, g, rate, dy, reset=None, lens=None, seg=None):
     before, e_b = before * keep, e_b * keep
     dh, e_dh = np.zeros((B, T, D)), np.zeros((B, T, D))
     c, e = dhT.astype(np.float64).copy(), np.zeros((B, D))
+    G = np.abs(c)
     for t in range(T - 1, -1, -1):
         lv = live[:, t] > 0
         dh[:, t] = dy[:, t] + c
-        e_dh[:, t] = e + 2 * E * np.abs(dh[:, t])
-        e = np.where(lv, keep[:, t] * a[:, t] * (e_dh[:, t] + np.abs(dh[:, t]) * (d_a[:, t] + 4 * E)), e)
+        H = G + np.abs(dy[:, t])
+        e_dh[:, t] = e + 2 * E * H
+        e = np.where(lv, keep[:, t] * a[:, t] * (e_dh[:, t] + H * (d_a[:, t] + 4 * E)), e)
+        G = np.where(lv, keep[:, t] * a[:, t] * H, G)
         c = np.where(lv, keep[:, t] * a[:, t] * dh[:, t], c)
     with np.errstate(divide="ignore", invalid="ignore"):
         am = np.where(m > 0, a / m, 0.0)
