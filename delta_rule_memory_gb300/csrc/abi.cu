@@ -20,6 +20,7 @@ int set_error(int code, const char *fmt, ...) {
 
 int sticky_gdn_chunk(int32_t *bits);
 int sticky_sse_chunk(int32_t *bits);
+int sticky_glr(int32_t *bits);
 
 int check_launch(const char *what) {
   cudaError_t e = cudaGetLastError();
@@ -45,6 +46,7 @@ extern "C" int sdm_check(const int32_t *dev_err, void *stream) {
   }
   int rc = sdm::sticky_gdn_chunk(&bits);
   if (rc == SDM_OK) rc = sdm::sticky_sse_chunk(&bits);
+  if (rc == SDM_OK) rc = sdm::sticky_glr(&bits);
   if (rc != SDM_OK) return rc;
   if (bits == 0) return SDM_OK;
   return sdm::set_error(SDM_ERR_DEVICE, "device error bits 0x%x:%s%s%s%s%s", static_cast<unsigned>(bits),

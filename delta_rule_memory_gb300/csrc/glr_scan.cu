@@ -8,8 +8,8 @@
 // that splits the sequence.  A warp owns 64 channels (a pair per lane) of 8
 // tokens: it forms its run's (P, H), takes the state in front of it from the
 // runs before, and steps its tokens through once more with the gates still in
-// registers.  Eight warps make a CTA (64 tokens), up to eight CTAs a cluster
-// (512 tokens, runs exchanged through distributed shared memory), and the
+// registers.  Four warps make a CTA (32 tokens), up to eight CTAs a cluster
+// (256 tokens, runs exchanged through distributed shared memory), and the
 // cluster walks the sequence.  Every input is read once and every output
 // written once, no CTA waits for another outside its cluster, and the order of
 // every sum is fixed by the sizes.
@@ -17,16 +17,25 @@
 #include <type_traits>
 
 #include "ckpt8.cuh"
+#include "umma.cuh"
 
 namespace sdm {
+
+int test_drop_signal();  // gdn_chunk.cu: the SDM_TEST_DROP_SIGNAL test hook
+SDM_STICKY_ACCESSOR(sticky_glr)
+
 namespace {
 
 constexpr int kSeg = 8;          // tokens of a warp's run, and between the states that the training forward keeps
-constexpr int kWarps = 8;        // runs of a CTA
+constexpr int kWarps = 4;        // runs of a CTA
 constexpr int kTile = kSeg * kWarps;
 constexpr int kChan = 64;        // channels of a CTA, and of a checkpoint's group
 constexpr int kMaxCluster = 8;
-constexpr int kResident = 152 * 3;  // CTAs that run at once
+constexpr int kSMs = 152;
+// CTAs that run at once on an SM: bound by registers, for fp32 rows by shared memory
+inline int forward_ctas(int dtype) { return dtype == SDM_DTYPE_F32 ? 3 : 5; }
+inline int backward_ctas(int dtype) { return dtype == SDM_DTYPE_F32 ? 2 : 3; }
+constexpr uint32_t kWaitPolls = 1u << 20;
 static_assert(kChan == ckpt8::kGroup, "a warp's channels are one checkpoint group");
 
 struct GlrArgs {
@@ -41,6 +50,7 @@ struct GlrArgs {
   const int32_t *lens;
   int B, T, D, S;
   int cs;               // CTAs of a cluster
+  int drop;             // test hook: the last CTA of a cluster sends nothing
   void *y;              // or dy
   float *carry;
   void *dx, *dr, *dg;
@@ -83,9 +93,14 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 }
 
 // The decay and its complement: a = 2^l with l = -rate log2(e) sigmoid(r),
-// m2 = 1 - a^2.  Near a = 1 the difference cancels, so for w = -2 ln a <= 1/4
-// the series w (1 - w/2 (1 - w/3 (...))) takes over, whose first term left out
-// is below 5e-8 of it there; above, 1 - a^2 loses two bits at most.
+// m2 = 1 - a^2.  Near a = 1 the difference cancels, and the series w (1 - w/2
+// (1 - w/3 (... (1 - w/6)))) in w = -2 ln a takes over.  It ends with a
+// negative term, so it is never above 1 - a^2, and below it by w^7 / 5040 at
+// first.  The difference is taken from 1 - 6e-7 in place of 1, which is more than
+// a^2's error (2 * 2^-22, ex2.approx) can make up for, so it is never above
+// 1 - a^2 either, and the larger of the two is the right one: off by 2.5e-6 of
+// it where they meet (w = 0.45), by less elsewhere.
+constexpr float kBelow1 = 0.9999994f;
 __device__ __forceinline__ float2 decay(float2 l) { return make_float2(ex2(l.x), ex2(l.y)); }
 __device__ __forceinline__ float2 complement(float2 l, float2 a) {
   const float2 w = mul2(l, dup(-2.f * kLn2));
@@ -95,7 +110,7 @@ __device__ __forceinline__ float2 complement(float2 l, float2 a) {
   p = fma2(w, p, dup(-0.5f));
   p = fma2(w, p, dup(1.f));
   p = mul2(w, p);
-  return make_float2(w.x <= 0.25f ? p.x : __fmaf_rn(-a.x, a.x, 1.f), w.y <= 0.25f ? p.y : __fmaf_rn(-a.y, a.y, 1.f));
+  return make_float2(fmaxf(p.x, __fmaf_rn(-a.x, a.x, kBelow1)), fmaxf(p.y, __fmaf_rn(-a.y, a.y, kBelow1)));
 }
 // 1 / sqrt(m2), and 0 where m2 underflows
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
@@ -226,12 +241,16 @@ struct Run {
   float2 P, H;
   bool cut;
 };
-__device__ __forceinline__ float2 apply(const Run &q, float2 v) { return q.cut ? q.H : fma2(q.P, v, q.H); }
+template <bool CUTS>
+__device__ __forceinline__ float2 apply(const Run &q, float2 v) {
+  return CUTS && q.cut ? q.H : fma2(q.P, v, q.H);
+}
 
 struct Runs {
   float4 warp[2][kWarps][32];
   float4 cta[2][kMaxCluster][32];
   uint32_t warp_cut[2][kWarps], cta_cut[2][kMaxCluster];
+  uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in cta[half]
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
@@ -241,21 +260,59 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
   return d;
 }
+// asynchronous stores into a CTA of the cluster, counted by its mbarrier
+__device__ __forceinline__ void send(uint32_t dst, float4 v, uint32_t mbar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];\n" ::"r"(dst),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mbar)
+               : "memory");
+}
+__device__ __forceinline__ void send(uint32_t dst, uint32_t v, uint32_t mbar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];\n" ::"r"(dst), "r"(v), "r"(mbar)
+               : "memory");
+}
+// false: the phase did not complete within the bound
+__device__ __forceinline__ bool wait_runs(uint32_t mbar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (i > 64) __nanosleep(64);
+  }
+  return false;
+}
 
-// Every warp of the cluster gives its run of this step; returns the value in
-// front of this warp's run and moves v (the value in front of the step, the same in
-// every warp) behind the step.  Runs follow one another by warp and CTA rank,
-// upwards, or (REVERSE) downwards.  The two halves of `s` alternate by step, so
-// that one barrier a step is enough: a half is written again two steps on,
-// when every reader has passed the barrier between.
-template <bool REVERSE>
-__device__ __forceinline__ float2 compose(Runs &s, int half, int warp, int lane, int rank, int cs, const Run &mine,
-                                          float2 &v) {
+// Where a warp stands in its cluster, and whether a wait of its gave up.
+struct Place {
+  int warp, lane, rank, cs;
+  bool drop;  // test hook: do not send
+  bool lost;
+};
+
+// Every warp of the cluster gives its run of a step; returns the value in front
+// of this warp's run and moves v (the value in front of the step, the same in every
+// warp) behind the step.  Runs follow one another by warp and CTA rank, upwards,
+// or (REVERSE) downwards.  k counts the calls: the halves of `s` alternate, so
+// that one CTA barrier a step is enough (a half is written again two steps on,
+// when every reader has passed the barrier between).  Between CTAs a run travels
+// by st.async, which needs no fence and no cluster barrier: a fence would wait
+// for the warp's stores to global memory as well.  A CTA sends its run of step k + 2
+// once it has every run of step k + 1, each sent after its sender had done with
+// step k, so a half in use is not overwritten.  CUTS: runs may be cut.
+template <bool REVERSE, bool CUTS>
+__device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &mine, float2 &v) {
+  const int half = k & 1, warp = at.warp, lane = at.lane, cs = at.cs;
   s.warp[half][warp][lane] = make_float4(mine.P.x, mine.P.y, mine.H.x, mine.H.y);
-  if (lane == 0) s.warp_cut[half][warp] = mine.cut;
+  if (CUTS && lane == 0) s.warp_cut[half][warp] = mine.cut;
+  if (cs > 1 && threadIdx.x == 0) umma::mbar_expect_tx(smem_u32(&s.full[half]), cs * (CUTS ? 516 : 512));
   __syncthreads();
-  auto run = [&](const float4 &q, uint32_t cut) {
-    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), cut != 0};
+  auto run = [&](const float4 &q, const uint32_t *cut) {
+    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && *cut != 0};
   };
   float2 front;
   if (cs == 1) {
@@ -264,7 +321,7 @@ __device__ __forceinline__ float2 compose(Runs &s, int half, int warp, int lane,
     for (int i = 0; i < kWarps; ++i) {
       const int j = REVERSE ? kWarps - 1 - i : i;
       if (j == warp) front = v;
-      v = apply(run(s.warp[half][j][lane], s.warp_cut[half][j]), v);
+      v = apply<CUTS>(run(s.warp[half][j][lane], &s.warp_cut[half][j]), v);
     }
     return front;
   }
@@ -273,29 +330,45 @@ __device__ __forceinline__ float2 compose(Runs &s, int half, int warp, int lane,
   for (int i = 0; i < kWarps; ++i) {
     const int j = REVERSE ? kWarps - 1 - i : i;
     if (j == warp) before = all;
-    const Run q = run(s.warp[half][j][lane], s.warp_cut[half][j]);
-    all.H = apply(q, all.H);
+    const Run q = run(s.warp[half][j][lane], &s.warp_cut[half][j]);
+    all.H = apply<CUTS>(q, all.H);
     all.P = mul2(all.P, q.P);
-    all.cut |= q.cut;
+    if (CUTS) all.cut |= q.cut;
   }
-  if (warp < cs) {  // warp i hands the CTA's run to CTA i of the cluster
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(in_cta(&s.cta[half][rank][lane], warp)),
-                 "f"(all.P.x), "f"(all.P.y), "f"(all.H.x), "f"(all.H.y)
-                 : "memory");
-    if (lane == 0)
-      asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(in_cta(&s.cta_cut[half][rank], warp)),
-                   "r"(static_cast<uint32_t>(all.cut))
-                   : "memory");
-  }
-  cluster_arrive();
-  cluster_wait();
+  if (!at.drop)
+    for (int i = warp; i < cs; i += kWarps) {  // the warps share out the CTAs that the run goes to
+      const uint32_t mbar = in_cta(&s.full[half], i);
+      send(in_cta(&s.cta[half][at.rank][lane], i), make_float4(all.P.x, all.P.y, all.H.x, all.H.y), mbar);
+      if (CUTS && lane == 0) send(in_cta(&s.cta_cut[half][at.rank], i), static_cast<uint32_t>(all.cut), mbar);
+    }
+  if (!at.lost) at.lost = !wait_runs(smem_u32(&s.full[half]), k >> 1 & 1);
   front = v;
   for (int i = 0; i < cs; ++i) {
     const int j = REVERSE ? cs - 1 - i : i;
-    if (j == rank) front = v;
-    v = apply(run(s.cta[half][j][lane], s.cta_cut[half][j]), v);
+    if (j == at.rank) front = v;
+    v = apply<CUTS>(run(s.cta[half][j][lane], &s.cta_cut[half][j]), v);
   }
-  return apply(before, front);
+  return apply<CUTS>(before, front);
+}
+
+// Before the first compose, and at the kernel's end.  A CTA whose waits all
+// ended well has received everything that is sent to it and may leave; the
+// cluster barrier at the end covers those whose wait gave up.
+__device__ __forceinline__ void open_runs(Runs &s, const Place &at) {
+  if (at.cs == 1) return;
+  if (threadIdx.x == 0) {
+    umma::mbar_init(smem_u32(&s.full[0]), 1);
+    umma::mbar_init(smem_u32(&s.full[1]), 1);
+    umma::fence_mbar_init();
+  }
+  cluster_arrive();
+}
+__device__ __forceinline__ void close_runs(const Place &at, int32_t *err) {
+  if (at.cs == 1) return;
+  if (at.lost) report_timeout(err);
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
 }
 
 // reset flags of tokens [0, n) as bits; the same in every lane
@@ -304,8 +377,8 @@ __device__ __forceinline__ uint32_t reset_bits(const uint8_t *reset, int64_t row
 }
 
 // ---- forward ----
-// K8: also the 8-bit checkpoints of x, r and g.
-template <class E, bool VEC, bool K8>
+// K8: also the 8-bit checkpoints of x, r and g.  CUTS: with reset flags.
+template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
@@ -313,9 +386,10 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned char *mine = smem + sizeof(Runs) + warp * 2 * kStage;
   const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
+  Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
-  if (cs > 1) cluster_arrive();
+  open_runs(runs, at);
   const int len = load_len(a, b);
   const int64_t row0 = static_cast<int64_t>(b) * a.T;
   const float2 rate2 = make_float2(one ? -kLog2e * load_rate(a, c) : 0.f, two ? -kLog2e * load_rate(a, c + 1) : 0.f);
@@ -343,7 +417,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
     __syncwarp();
     const int t0 = first(step), n = count(t0);
     const unsigned char *d = mine + (step & 1) * kStage;
-    const uint32_t cut = a.reset ? reset_bits(a.reset, row0 + t0, n, lane) : 0;
+    const uint32_t cut = CUTS ? reset_bits(a.reset, row0 + t0, n, lane) : 0;
     float2 f[kSeg], u[kSeg];
 #pragma unroll
     for (int i = 0; i < kSeg; ++i) {
@@ -382,7 +456,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
         if (i >= n) f[i] = dup(1.f), u[i] = dup(0.f);
     }
     Run q{f[0], u[0], cut != 0};
-    if (cut) {
+    if (CUTS && cut) {
 #pragma unroll
       for (int i = 1; i < kSeg; ++i) q.H = cut >> i & 1 ? u[i] : fma2(f[i], q.H, u[i]);
       q.P = dup(0.f);
@@ -390,7 +464,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
 #pragma unroll
       for (int i = 1; i < kSeg; ++i) q.P = mul2(q.P, f[i]), q.H = fma2(f[i], q.H, u[i]);
     }
-    float2 h = compose<false>(runs, step & 1, warp, lane, rank, cs, q, v);
+    float2 h = compose<false, CUTS>(runs, step, at, q, v);
     if (n > 0 && one) {
       if (a.carry) {
         float *k = a.carry + (static_cast<int64_t>(b) * a.S + t0 / kSeg) * a.D + c;
@@ -399,7 +473,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
       E *y = static_cast<E *>(a.y) + (row0 + t0) * a.D + c;
 #pragma unroll
       for (int i = 0; i < kSeg; ++i) {
-        h = cut >> i & 1 ? u[i] : fma2(f[i], h, u[i]);
+        h = CUTS && cut >> i & 1 ? u[i] : fma2(f[i], h, u[i]);
         if (i < n) store2<VEC>(y + static_cast<int64_t>(i) * a.D, h, two);
       }
     }
@@ -408,6 +482,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
     a.state_out[sc] = v.x;
     if (two) a.state_out[sc + 1] = v.y;
   }
+  close_runs(at, a.err);
   if (K8 && bad && lane == 0 && a.err) atomicOr(a.err, SDM_DEVERR_NONFINITE);
 }
 
@@ -415,7 +490,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
 // The same walk from the last token to the first; what runs through it is
 // e_t = a_t dh_t, the gradient that reaches h_{t-1}: dh_t = dy_t + e_{t+1}.
 // K8: x, r and g come from their checkpoints.
-template <class E, bool VEC, bool K8>
+template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
@@ -424,9 +499,10 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned char *mine = smem + sizeof(Runs) + warp * 2 * kStage;
   const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
+  Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
-  if (cs > 1) cluster_arrive();
+  open_runs(runs, at);
   const int len = load_len(a, b);
   const int64_t row0 = static_cast<int64_t>(b) * a.T, rows = static_cast<int64_t>(a.B) * a.T;
   const int G = ckpt8::groups(a.D);
@@ -460,7 +536,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
   for (int step = steps - 1; step >= 0; --step) {
     fetch(step - 1);
     const int t0 = first(step), n = count(t0);
-    const uint32_t cut = a.reset ? reset_bits(a.reset, row0 + t0, n, lane) : 0;
+    const uint32_t cut = CUTS ? reset_bits(a.reset, row0 + t0, n, lane) : 0;
     float2 h = dup(0.f);
     uint32_t exps = 0;  // lane 8 k + i: plane k, token i
     if (n > 0) {
@@ -500,7 +576,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
       cx[i] = mul2(m, sg);
       const float2 u = mul2(m, sx);
       cg[i] = mul2(u, fma2(sg, dup(-1.f), dup(1.f)));
-      if (cut >> i & 1) h = dup(0.f);
+      if (CUTS && cut >> i & 1) h = dup(0.f);
       const float2 nf = mul2(f[i], dup(-1.f));
       cr[i] = mul2(mul2(sr, nf), fma2(mul2(nf, rs), sx, h));
       ck[i] = mul2(rate, fma2(sr, dup(-1.f), dup(1.f)));
@@ -512,7 +588,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
         if (i >= n) f[i] = dup(1.f), dy[i] = dup(0.f);
     }
     Run q{dup(1.f), dup(0.f), cut != 0};
-    if (cut) {
+    if (CUTS && cut) {
 #pragma unroll
       for (int i = kSeg - 1; i >= 0; --i) q.H = cut >> i & 1 ? dup(0.f) : mul2(f[i], add2(dy[i], q.H));
       q.P = dup(0.f);
@@ -520,7 +596,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
 #pragma unroll
       for (int i = kSeg - 1; i >= 0; --i) q.P = mul2(q.P, f[i]), q.H = mul2(f[i], add2(dy[i], q.H));
     }
-    float2 e = compose<true>(runs, step & 1, warp, lane, rank, cs, q, v);
+    float2 e = compose<true, CUTS>(runs, steps - 1 - step, at, q, v);
     if (n > 0) {
       const int64_t at = (row0 + t0) * a.ld_d + c;
 #pragma unroll
@@ -535,7 +611,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
             store2<VEC>(static_cast<E *>(a.dr) + o, mul2(w, ck[i]), two);
             store2<VEC>(static_cast<E *>(a.dg) + o, mul2(dh, cg[i]), two);
           }
-          e = cut >> i & 1 ? dup(0.f) : mul2(f[i], dh);
+          e = CUTS && cut >> i & 1 ? dup(0.f) : mul2(f[i], dh);
         }
       }
     }
@@ -556,6 +632,7 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
     if (one) p[0] = drate.x;
     if (two) p[1] = drate.y;
   }
+  close_runs(at, a.err);
 }
 
 // drate[c] = sum over the parts: 32 interleaved sums, then those in order
@@ -596,13 +673,18 @@ int check_words(const char *fn, std::initializer_list<const void *> ps) {
   return SDM_OK;
 }
 
-// CTAs of a cluster: as many as the sequence has tiles for and as keep the
-// whole grid on the GPU at once.
-int cluster_size(int B, int T, int D) {
+// CTAs of a cluster: the split of the sequence that leaves the least to the
+// busiest SM, in tiles, as long as the whole grid runs at once.
+int cluster_size(int B, int T, int D, int per_sm) {
   const int64_t columns = static_cast<int64_t>(B) * ((D + kChan - 1) / kChan);
-  int cs = 1;
-  while (cs < kMaxCluster && 2 * cs * columns <= kResident && cs * kTile < T) cs *= 2;
-  return cs;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int cs = 1; cs <= kMaxCluster; ++cs) {
+    if (cs > 1 && (columns * cs > int64_t(kSMs) * per_sm || (cs - 1) * kTile >= T)) break;
+    const int64_t load = (columns * cs + kSMs - 1) / kSMs * ((T + kTile * cs - 1) / (kTile * cs));
+    if (load < least) least = load, best = cs;
+  }
+  return best;
 }
 
 // 16-byte copies of rows, pairwise stores
@@ -631,14 +713,20 @@ int launch(const char *fn, K kernel, size_t smem, const GlrArgs &a, cudaStream_t
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
   const size_t smem = sizeof(Runs) + kWarps * 2 * 3 * Rows<E>::kBytes;
-  return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true>, smem, a, st)
-                 : launch(fn, glr_forward_kernel<E, VEC, false>, smem, a, st);
+  if (a.reset)
+    return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
+                   : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
+  return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, false>, smem, a, st)
+                 : launch(fn, glr_forward_kernel<E, VEC, false, false>, smem, a, st);
 }
 template <class E, bool VEC>
 int launch_backward(const char *fn, const GlrArgs &a, cudaStream_t st) {
   const size_t smem = sizeof(Runs) + kWarps * 2 * ((a.codes ? 3 * Rows<int8_t>::kBytes : 3 * Rows<E>::kBytes) + Rows<E>::kBytes);
-  return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true>, smem, a, st)
-                 : launch(fn, glr_backward_kernel<E, VEC, false>, smem, a, st);
+  if (a.reset)
+    return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, true>, smem, a, st)
+                   : launch(fn, glr_backward_kernel<E, VEC, false, true>, smem, a, st);
+  return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, false>, smem, a, st)
+                 : launch(fn, glr_backward_kernel<E, VEC, false, false>, smem, a, st);
 }
 
 int forward(const char *fn, GlrArgs &a, int dtype, int8_t *codes, uint8_t *exps, cudaStream_t st) {
@@ -654,7 +742,8 @@ int forward(const char *fn, GlrArgs &a, int dtype, int8_t *codes, uint8_t *exps,
   if ((rc = check_words(fn, {a.state, a.state_out, a.rate, a.lens, a.carry, a.err}))) return rc;
   if (codes && !aligned(codes, 16)) return set_error(SDM_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
   a.codes = codes, a.exps = exps;
-  a.cs = cluster_size(a.B, a.T, a.D);
+  a.drop = test_drop_signal();
+  a.cs = cluster_size(a.B, a.T, a.D, forward_ctas(dtype));
   const int es = dtype == SDM_DTYPE_F32 ? 4 : 2;
   const bool vec = rows_vec(a.x, a.ld_x, es) && rows_vec(a.r, a.ld_r, es) && rows_vec(a.g, a.ld_g, es) &&
                    pairs_vec(a.y, a.D, es) && (!a.carry || aligned(a.carry, 8));
@@ -701,7 +790,7 @@ extern "C" int glr_scan_train(const float *state, float *state_out, const void *
 
 extern "C" size_t glr_scan_backward_workspace_size(int B, int T, int D) {
   if (check_sizes("glr_scan_backward_workspace_size", SDM_DTYPE_F32, B, T, D) != SDM_OK) return 0;
-  return (sizeof(float) * B * cluster_size(B, T, D) * static_cast<size_t>(D) + 255) / 256 * 256;
+  return (sizeof(float) * B * kMaxCluster * static_cast<size_t>(D) + 255) / 256 * 256;
 }
 
 extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const void *x, int64_t ld_x, const void *r,
@@ -745,7 +834,8 @@ extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const v
   a.B = B, a.T = T, a.D = D, a.S = (T + kSeg - 1) / kSeg;
   a.y = const_cast<void *>(dy), a.carry = const_cast<float *>(carry);
   a.dx = dx, a.dr = dr, a.dg = dg, a.part = static_cast<float *>(workspace), a.err = dev_err;
-  a.cs = cluster_size(B, T, D);
+  a.drop = test_drop_signal();
+  a.cs = cluster_size(B, T, D, backward_ctas(dtype));
   if (B > 0) {
     const int es = dtype == SDM_DTYPE_F32 ? 4 : 2;
     const bool in = codes ? D % 16 == 0 : rows_vec(x, ld_x, es) && rows_vec(r, ld_r, es) && rows_vec(g, ld_g, es);

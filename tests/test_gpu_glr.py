@@ -375,6 +375,33 @@ def test_streams_and_graphs(B, T, D):
     assert all(torch.equal(p, q) for p, q in zip(held, want2))
 
 
+def test_a_wait_that_runs_out_is_reported(monkeypatch):
+    """SDM_TEST_DROP_SIGNAL=1: a CTA of each cluster keeps its runs to itself, the
+    others' bounded waits give up, the call reports it, and the next is exact."""
+    sdm = need_gpu()
+    c = Case(1, 600, 64, "bf16", seed=18)      # one channel block: split over a cluster
+    f = c.forward()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = c.h0.clone()
+    y, carry = sdm.glr_scan_train(s, *c.args(), dev_err=err)
+    sdm.sdm_check(err)
+    monkeypatch.setenv("SDM_TEST_DROP_SIGNAL", "1")
+    for call in (lambda e: sdm.glr_scan(c.h0.clone(), *c.args(), dev_err=e),
+                 lambda e: sdm.glr_scan_backward(c.dhT.clone(), c.x, c.r, c.g, c.rate, carry, c.dy, dev_err=e)):
+        call(err)
+        assert int(err.item()) == sdm.SDM_DEVERR_TIMEOUT
+        err.zero_()
+        with pytest.raises(sdm.SdmError, match="gave up"):
+            sdm.sdm_check()                     # the library's own record, without an error word
+        sdm.sdm_check()
+    monkeypatch.delenv("SDM_TEST_DROP_SIGNAL")
+    s2 = c.h0.clone()
+    assert torch.equal(sdm.glr_scan(s2, *c.args(), dev_err=err), y) and torch.equal(s, s2)
+    assert_within(y, f["y"], f["e_y"], c.dt, "y")
+    check_backward(sdm, c, f, carry, None)
+    sdm.sdm_check(err)
+
+
 def test_offsets_beyond_32_bits():
     """2.3e9 elements: the last tokens against a call on them alone that
     continues from the state before them."""
