@@ -551,18 +551,38 @@ def sse_scan(state, route_logits, topk: int, k_logits, q, v, alpha, y=None, sel_
 _DTYPES = {torch.float32: SDM_DTYPE_F32, torch.bfloat16: SDM_DTYPE_BF16}
 
 
+class _Here:
+    """The current device and stream, as they are."""
+
+    def __enter__(self):
+        if _raw_stream is not None:     # the handle alone, without a Stream object around it
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_NOW = _Here()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 @contextlib.contextmanager
+def _there(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield torch.cuda.current_stream().cuda_stream
+
+
 def _on(device: torch.device, stream):
     """The device of the call's tensors and its stream (None: that device's
     current one) as the current ones, so that what the call allocates belongs
-    to the stream that uses it.  Yields the stream's handle."""
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+    to the stream that uses it.  The context's value is the stream's handle."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return _HERE_NOW
+    elif not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-    if stream is None and device.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream().cuda_stream
+    return _there(device, stream)
 
 
 def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
@@ -573,13 +593,13 @@ def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     D = t.shape[-1]
     ld = D
-    if t.numel():
+    if not t.is_contiguous() and t.numel():
         if D > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name}'s channels must be contiguous")
         rows = 1            # rows that the dimensions walked so far hold
@@ -601,10 +621,11 @@ def _glr_checks(state, x, r, g, rate, reset, lens, like=None):
     _act(first, "x" if like is None else "dy")
     if first.dim() != 3:
         raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
-    B, T, D = first.shape
+    B, T, D = shape = first.shape
+    dt, dev = first.dtype, first.device
     lds = (0, 0, 0)
     if x is not None or like is None:
-        lds = tuple(_act(t, n, first.dtype, (B, T, D), first.device) for t, n in ((x, "x"), (r, "r"), (g, "g")))
+        lds = _act(x, "x", dt, shape, dev), _act(r, "r", dt, shape, dev), _act(g, "g", dt, shape, dev)
     _req(state, "state" if like is None else "dstate", torch.float32, (B, D))
     _req(rate, "rate", torch.float32, (D,))
     if reset is not None:
@@ -613,8 +634,9 @@ def _glr_checks(state, x, r, g, rate, reset, lens, like=None):
         _req(reset, "reset", torch.uint8, (B, T))
     if lens is not None:
         _req(lens, "lens", torch.int32, (B,))
-    _same_device(first.device, state=state, rate=rate, reset=reset, lens=lens)
-    return B, T, D, first.dtype, lds
+    if state.device != dev or rate.device != dev or reset is not None or lens is not None:
+        _same_device(dev, state=state, rate=rate, reset=reset, lens=lens)
+    return B, T, D, dt, lds
 
 
 def _same_device(device, **tensors):
@@ -625,8 +647,7 @@ def _same_device(device, **tensors):
 
 def _err_word(dev_err, device):
     if dev_err is not None:
-        _req(dev_err, "dev_err", torch.int32)
-        _same_device(device, dev_err=dev_err)
+        _out(dev_err, "dev_err", torch.int32, None, device)
 
 
 def _out(t, name: str, dtype, shape, device):
@@ -634,7 +655,8 @@ def _out(t, name: str, dtype, shape, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _req(t, name, dtype, shape)
-    _same_device(device, **{name: t})
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t
 
 

@@ -5,14 +5,14 @@
 //
 // A run of tokens acts on the state before it as h -> P h + H (P the product
 // of its decays, H what it leaves when it starts from 0), and runs compose:
-// that splits the sequence.  A warp owns 64 channels (a pair per lane) of 8
-// tokens: it forms its run's (P, H), takes the state in front of it from the
-// runs before, and steps its tokens through once more with the gates still in
-// registers.  Four warps make a CTA (32 tokens), up to eight CTAs a cluster
-// (256 tokens, runs exchanged through distributed shared memory), and the
-// cluster walks the sequence.  Every input is read once and every output
-// written once, no CTA waits for another outside its cluster, and the order of
-// every sum is fixed by the sizes.
+// that splits the sequence.  A warp owns 64 channels (a pair per lane) of a run
+// of 16 tokens (8 in the backward): it forms the run's (P, H), takes the state in
+// front of it from the runs before, and steps its tokens through once more with
+// the gates still in registers.  Up to eight warps make a CTA, up to eight CTAs a
+// cluster (runs travel through distributed shared memory), and the cluster
+// walks the sequence.  Every input is read once and every output written once,
+// no CTA waits for another outside its cluster, and the order of every sum is
+// fixed by the sizes.
 #include <initializer_list>
 #include <type_traits>
 
@@ -26,15 +26,14 @@ SDM_STICKY_ACCESSOR(sticky_glr)
 
 namespace {
 
-constexpr int kSeg = 8;          // tokens of a warp's run, and between the states that the training forward keeps
-constexpr int kWarps = 4;        // runs of a CTA
-constexpr int kTile = kSeg * kWarps;
+constexpr int kSeg = 8;          // tokens between the states that the training forward keeps
+constexpr int kForwardRun = 16;  // tokens of a warp's run
+constexpr int kBackwardRun = kSeg;
 constexpr int kChan = 64;        // channels of a CTA, and of a checkpoint's group
-constexpr int kMaxCluster = 8;
+constexpr int kWarps = 4;        // of a CTA
+constexpr int kMaxCluster = 16;
 constexpr int kSMs = 152;
-// CTAs that run at once on an SM: bound by registers, for fp32 rows by shared memory
-inline int forward_ctas(int dtype) { return dtype == SDM_DTYPE_F32 ? 3 : 5; }
-inline int backward_ctas(int dtype) { return dtype == SDM_DTYPE_F32 ? 2 : 3; }
+constexpr int kForwardRegs = 128, kBackwardRegs = 128;  // of a thread
 constexpr uint32_t kWaitPolls = 1u << 20;
 static_assert(kChan == ckpt8::kGroup, "a warp's channels are one checkpoint group");
 
@@ -73,16 +72,32 @@ __device__ __forceinline__ float rsq(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float root(float x) {
-  float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // pairs of channels: one instruction for two fp32 operations
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -93,36 +108,42 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 }
 
 // The decay and its complement: a = 2^l with l = -rate log2(e) sigmoid(r),
-// m2 = 1 - a^2.  Near a = 1 the difference cancels, and the series w (1 - w/2
-// (1 - w/3 (... (1 - w/6)))) in w = -2 ln a takes over.  It ends with a
-// negative term, so it is never above 1 - a^2, and below it by w^7 / 5040 at
-// first.  The difference is taken from 1 - 6e-7 in place of 1, which is more than
-// a^2's error (2 * 2^-22, ex2.approx) can make up for, so it is never above
-// 1 - a^2 either, and the larger of the two is the right one: off by 2.5e-6 of
-// it where they meet (w = 0.45), by less elsewhere.
+// m2 = 1 - a^2.  Near a = 1 the difference cancels, and a cubic times w = -2 ln a
+// takes over: the best one (in relative error, by linear programming) among
+// those that stay below 1 - e^-w, off by 7.6e-7 up to w = 0.28 and ever further
+// below behind that.  The difference is taken from 1 - 6e-7 in place of 1, which is
+// more than a^2's error (2 * 2^-22, ex2.approx) can make up for, so it is never
+// above 1 - a^2 either, and the larger of the two is the right one: off by 4.5e-6
+// of it where they meet, by less elsewhere.
 constexpr float kBelow1 = 0.9999994f;
 __device__ __forceinline__ float2 decay(float2 l) { return make_float2(ex2(l.x), ex2(l.y)); }
 __device__ __forceinline__ float2 complement(float2 l, float2 a) {
   const float2 w = mul2(l, dup(-2.f * kLn2));
-  float2 p = fma2(w, dup(-1.f / 720.f), dup(1.f / 120.f));
-  p = fma2(w, p, dup(-1.f / 24.f));
-  p = fma2(w, p, dup(1.f / 6.f));
-  p = fma2(w, p, dup(-0.5f));
-  p = fma2(w, p, dup(1.f));
+  float2 p = fma2(w, dup(-0.03725945f), dup(0.16590417f));
+  p = fma2(w, p, dup(-0.49995695f));
+  p = fma2(w, p, dup(0.99999924f));
   p = mul2(w, p);
   return make_float2(fmaxf(p.x, __fmaf_rn(-a.x, a.x, kBelow1)), fmaxf(p.y, __fmaf_rn(-a.y, a.y, kBelow1)));
 }
 // 1 / sqrt(m2), and 0 where m2 underflows
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
+// sqrt(m2): the added number keeps the root's inverse finite at 0 and is lost from 2^-100 on
+__device__ __forceinline__ float2 root2(float2 m2) {
+  const float2 q = add2(m2, dup(1.17549435e-38f));
+  return mul2(m2, make_float2(rsq(q.x), rsq(q.y)));
+}
 
 __device__ __forceinline__ uint32_t bf16_pair(float2 v) {  // nearest even, v.x in the lower half
   uint32_t u;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(v.y), "f"(v.x));
   return u;
 }
-// a pair of channels to global memory; `two`: both exist
+// A pair of channels to global memory, `at` bytes behind a row that is the same
+// for the whole warp (an address in two parts costs no 64-bit arithmetic per
+// lane); `two`: both channels exist.
 template <bool VEC>
-__device__ __forceinline__ void store2(float *p, float2 v, bool two) {
+__device__ __forceinline__ void store2(float *row, uint32_t at, float2 v, bool two) {
+  float *p = reinterpret_cast<float *>(reinterpret_cast<char *>(row) + at);
   if (VEC) {
     *reinterpret_cast<float2 *>(p) = v;
   } else {
@@ -131,7 +152,8 @@ __device__ __forceinline__ void store2(float *p, float2 v, bool two) {
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void store2(uint16_t *p, float2 v, bool two) {
+__device__ __forceinline__ void store2(uint16_t *row, uint32_t at, float2 v, bool two) {
+  uint16_t *p = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(row) + at);
   const uint32_t u = bf16_pair(v);
   if (VEC) {
     *reinterpret_cast<uint32_t *>(p) = u;
@@ -158,11 +180,12 @@ __device__ __forceinline__ int load_len(const GlrArgs &a, int b) {
 }
 
 // ---- a warp's tokens in shared memory ----
-// Rows of 64 channels of E, token i at i * 64 * sizeof(E).  A warp copies and
-// reads its own rows only, so no CTA barrier guards them.
-template <class E>
+// Rows of 64 channels of I (an activation type, or int8 codes), token i at
+// i * 64 * sizeof(I).  A warp copies and reads its own rows only, so no CTA
+// barrier guards them.
+template <class I>
 struct Rows {
-  static constexpr int kRow = kChan * static_cast<int>(sizeof(E));
+  static constexpr int kRow = kChan * static_cast<int>(sizeof(I));
   static constexpr int kBytes = kSeg * kRow;
 };
 
@@ -170,62 +193,72 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Start copying tokens [0, n) (n <= 8; rows `ld` elements apart, src at the
-// first one's first channel of this warp, `chan` of them in range).  VEC: rows
-// are 16-byte aligned, 16 bytes a copy, zeros behind the last channel; else
-// element by element.
-template <class E, bool VEC>
-__device__ __forceinline__ void copy_rows(unsigned char *dst, const E *src, int64_t ld, int n, int chan, int lane) {
-  if (VEC) {
-    constexpr int kPer = Rows<E>::kRow / 16;
-    const uint32_t d = smem_u32(dst) + lane * 16;
-    const int j = lane % kPer;
-    const int left = chan * static_cast<int>(sizeof(E)) - 16 * j;
-    const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-    const E *s = src + (lane / kPer) * ld + (bytes > 0 ? j * (16 / static_cast<int>(sizeof(E))) : 0);
+// A walk over one [tokens, channels] tensor: a warp copies 8 rows at a time and
+// moves on.  VEC: rows are 16-byte aligned, 16 bytes a copy, zeros behind the
+// last channel; else a channel pair a row, element by element, zeros likewise.
+template <class I, bool VEC>
+struct Walk {
+  static constexpr int kEs = static_cast<int>(sizeof(I));
+  static constexpr int kPer = VEC ? Rows<I>::kRow / 16 : 1;  // copies a row
+  static constexpr int kRows = VEC ? 32 / kPer : 1;          // rows a copy of the warp
+  static_assert(kSeg % kRows == 0, "a copy of the warp holds whole rows of a run");
+  const char *p;      // the first row's first channel of the warp, the same in every lane
+  uint32_t row;       // bytes between rows
+  uint32_t at;        // this lane's part of a copy, behind p
+  int row0, bytes;    // VEC: its row of a copy and its bytes; else the warp's (4-byte I) or its channels
+
+  // `chan` channels exist
+  __device__ __forceinline__ Walk(const I *first, int64_t ld, int chan, int lane) {
+    row = static_cast<uint32_t>(ld) * kEs;
+    p = reinterpret_cast<const char *>(first);
+    if (VEC) {
+      const int left = chan * kEs - 16 * (lane % kPer);
+      bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+      row0 = lane / kPer;
+      at = row0 * row + (bytes > 0 ? 16 * (lane % kPer) : 0);
+    } else {
+      row0 = 0, bytes = kEs == 4 ? chan : min(2, max(0, chan - 2 * lane));
+      at = bytes > 0 ? 2 * lane * kEs : 0;
+    }
+  }
+  // start copying rows [0, n)
+  __device__ __forceinline__ void copy(unsigned char *dst, int n, int lane) const {
+    if constexpr (VEC) {
+      const uint32_t d = smem_u32(dst) + lane * 16;
+      if (n == kSeg) {
 #pragma unroll
-    for (int k = 0; k < kSeg * kPer / 32; ++k)
-      if (lane / kPer + k * (32 / kPer) < n) cp16(d + k * 512, s + k * (32 / kPer) * ld, bytes);
-  } else {
-    const int c = 2 * lane;
-    if (sizeof(E) == 4) {
+        for (int k = 0; k < kSeg / kRows; ++k) cp16(d + k * 512, p + (at + k * kRows * row), bytes);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i) {
-        if (i < n && c < chan) cp_async<4>(dst + i * Rows<E>::kRow + lane * 8, src + i * ld + c);
-        if (i < n && c + 1 < chan) cp_async<4>(dst + i * Rows<E>::kRow + lane * 8 + 4, src + i * ld + c + 1);
+        for (int k = 0; k < kSeg / kRows; ++k)
+          if (row0 + k * kRows < n) cp16(d + k * 512, p + (at + k * kRows * row), bytes);
+      }
+    } else if constexpr (kEs == 4) {
+      float *d = reinterpret_cast<float *>(dst) + lane;
+      for (int i = 0; i < n; ++i, d += kChan) {
+        const float *q = reinterpret_cast<const float *>(p + i * row) + lane;
+        if (lane < bytes) cp_async<4>(d, q);
+        else d[0] = 0.f;
+        if (lane + 32 < bytes) cp_async<4>(d + 32, q + 32);
+        else d[32] = 0.f;
       }
     } else {
-      uint32_t v[kSeg];
+      using W = typename std::conditional<kEs == 2, uint32_t, uint16_t>::type;  // a pair
+      using H = typename std::conditional<kEs == 2, uint16_t, uint8_t>::type;
+      W v[kSeg];
 #pragma unroll
       for (int i = 0; i < kSeg; ++i) {
-        const uint16_t *s = reinterpret_cast<const uint16_t *>(src) + i * ld + c;
-        const uint32_t lo = i < n && c < chan ? s[0] : 0, hi = i < n && c + 1 < chan ? s[1] : 0;
-        v[i] = lo | hi << 16;
+        const H *q = reinterpret_cast<const H *>(p + (at + i * row));
+        const uint32_t lo = i < n && bytes > 0 ? q[0] : 0, hi = i < n && bytes > 1 ? q[1] : 0;
+        v[i] = static_cast<W>(lo | hi << (8 * kEs));
       }
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i) *reinterpret_cast<uint32_t *>(dst + i * Rows<E>::kRow + lane * 4) = v[i];
+      for (int i = 0; i < kSeg; ++i) reinterpret_cast<W *>(dst)[i * (kChan / 2) + lane] = v[i];
     }
   }
-}
-// the same for checkpoint codes: rows of 64 bytes
-template <bool VEC>
-__device__ __forceinline__ void copy_codes(unsigned char *dst, const int8_t *src, int64_t ld, int n, int chan, int lane) {
-  if (VEC) {  // a row is 4 copies, 8 rows 32: one a lane
-    const int i = lane >> 2, j = lane & 3, left = chan - 16 * j;
-    const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-    if (i < n) cp16(smem_u32(dst) + lane * 16, src + i * ld + (bytes > 0 ? 16 * j : 0), bytes);
-  } else {
-    const int c = 2 * lane;
-    uint32_t v[kSeg];
-#pragma unroll
-    for (int i = 0; i < kSeg; ++i) {
-      const uint8_t *s = reinterpret_cast<const uint8_t *>(src) + i * ld + c;
-      v[i] = (i < n && c < chan ? s[0] : 0) | (i < n && c + 1 < chan ? s[1] : 0) << 8;
-    }
-#pragma unroll
-    for (int i = 0; i < kSeg; ++i) *reinterpret_cast<uint16_t *>(dst + i * kChan + c) = static_cast<uint16_t>(v[i]);
-  }
-}
+  __device__ __forceinline__ void move(int rows) { p += static_cast<int64_t>(rows) * row; }
+};
+
 __device__ __forceinline__ float2 row_pair(const unsigned char *rows, int i, int lane, const float *) {
   return *reinterpret_cast<const float2 *>(rows + i * Rows<float>::kRow + lane * 8);
 }
@@ -287,67 +320,72 @@ __device__ __forceinline__ bool wait_runs(uint32_t mbar, uint32_t parity) {
   return false;
 }
 
-// Where a warp stands in its cluster, and whether a wait of its gave up.
+// Where a warp stands: its place among the CTA's runs of a step and the CTA's
+// place among the cluster's, both in the order in which runs follow one another.
 struct Place {
   int warp, lane, rank, cs;
   bool drop;  // test hook: do not send
-  bool lost;
+  bool lost;  // a wait gave up
 };
 
 // Every warp of the cluster gives its run of a step; returns the value in front
 // of this warp's run and moves v (the value in front of the step, the same in every
-// warp) behind the step.  Runs follow one another by warp and CTA rank, upwards,
-// or (REVERSE) downwards.  k counts the calls: the halves of `s` alternate, so
+// warp) behind the step.  k counts the calls: the halves of `s` alternate, so
 // that one CTA barrier a step is enough (a half is written again two steps on,
 // when every reader has passed the barrier between).  Between CTAs a run travels
 // by st.async, which needs no fence and no cluster barrier: a fence would wait
 // for the warp's stores to global memory as well.  A CTA sends its run of step k + 2
 // once it has every run of step k + 1, each sent after its sender had done with
-// step k, so a half in use is not overwritten.  CUTS: runs may be cut.
-template <bool REVERSE, bool CUTS>
+// step k, so a half in use is not overwritten.  A wait that gives up is the
+// thread's last: an mbarrier whose phase is still open takes no second arrival
+// (that faults), so nothing is armed, sent or waited for any more, and the walk
+// ends on whatever the buffers hold.  CUTS: runs may be cut.
+template <bool CUTS>
 __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &mine, float2 &v) {
-  const int half = k & 1, warp = at.warp, lane = at.lane, cs = at.cs;
-  s.warp[half][warp][lane] = make_float4(mine.P.x, mine.P.y, mine.H.x, mine.H.y);
-  if (CUTS && lane == 0) s.warp_cut[half][warp] = mine.cut;
-  if (cs > 1 && threadIdx.x == 0) umma::mbar_expect_tx(smem_u32(&s.full[half]), cs * (CUTS ? 516 : 512));
+  const int half = k & 1, lane = at.lane, cs = at.cs;
+  s.warp[half][at.warp][lane] = make_float4(mine.P.x, mine.P.y, mine.H.x, mine.H.y);
+  if (CUTS && lane == 0) s.warp_cut[half][at.warp] = mine.cut;
+  if (cs > 1 && threadIdx.x == 0 && !at.lost) umma::mbar_expect_tx(smem_u32(&s.full[half]), cs * (CUTS ? 516 : 512));
   __syncthreads();
-  auto run = [&](const float4 &q, const uint32_t *cut) {
-    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && *cut != 0};
+  auto warp_run = [&](int j) {
+    const float4 q = s.warp[half][j][lane];
+    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.warp_cut[half][j] != 0};
   };
-  float2 front;
+  auto cta_run = [&](int j) {
+    const float4 q = s.cta[half][j][lane];
+    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.cta_cut[half][j] != 0};
+  };
   if (cs == 1) {
-    front = v;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const int j = REVERSE ? kWarps - 1 - i : i;
-      if (j == warp) front = v;
-      v = apply<CUTS>(run(s.warp[half][j][lane], &s.warp_cut[half][j]), v);
-    }
+#pragma unroll 4
+    for (int j = 0; j < at.warp; ++j) v = apply<CUTS>(warp_run(j), v);
+    const float2 front = v;
+    v = apply<CUTS>(mine, v);
+#pragma unroll 4
+    for (int j = at.warp + 1; j < kWarps; ++j) v = apply<CUTS>(warp_run(j), v);
     return front;
   }
-  Run all{dup(1.f), dup(0.f), false}, before = all;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const int j = REVERSE ? kWarps - 1 - i : i;
-    if (j == warp) before = all;
-    const Run q = run(s.warp[half][j][lane], &s.warp_cut[half][j]);
-    all.H = apply<CUTS>(q, all.H);
-    all.P = mul2(all.P, q.P);
-    if (CUTS) all.cut |= q.cut;
+  Run before{dup(1.f), dup(0.f), false};
+#pragma unroll 4
+  for (int j = 0; j < at.warp; ++j) {
+    const Run q = warp_run(j);
+    before.H = apply<CUTS>(q, before.H);
+    before.P = mul2(before.P, q.P);
+    if (CUTS) before.cut |= q.cut;
   }
-  if (!at.drop)
-    for (int i = warp; i < cs; i += kWarps) {  // the warps share out the CTAs that the run goes to
+  if (at.warp == kWarps - 1 && !at.drop && !at.lost) {  // the last warp knows the CTA's run
+    const float2 P = mul2(before.P, mine.P), H = apply<CUTS>(mine, before.H);
+    for (int i = 0; i < cs; ++i) {
       const uint32_t mbar = in_cta(&s.full[half], i);
-      send(in_cta(&s.cta[half][at.rank][lane], i), make_float4(all.P.x, all.P.y, all.H.x, all.H.y), mbar);
-      if (CUTS && lane == 0) send(in_cta(&s.cta_cut[half][at.rank], i), static_cast<uint32_t>(all.cut), mbar);
+      send(in_cta(&s.cta[half][at.rank][lane], i), make_float4(P.x, P.y, H.x, H.y), mbar);
+      if (CUTS && lane == 0) send(in_cta(&s.cta_cut[half][at.rank], i), before.cut || mine.cut ? 1u : 0u, mbar);
     }
-  if (!at.lost) at.lost = !wait_runs(smem_u32(&s.full[half]), k >> 1 & 1);
-  front = v;
-  for (int i = 0; i < cs; ++i) {
-    const int j = REVERSE ? cs - 1 - i : i;
-    if (j == at.rank) front = v;
-    v = apply<CUTS>(run(s.cta[half][j][lane], &s.cta_cut[half][j]), v);
   }
+  if (!at.lost) at.lost = !wait_runs(smem_u32(&s.full[half]), k >> 1 & 1);
+#pragma unroll 4
+  for (int j = 0; j < at.rank; ++j) v = apply<CUTS>(cta_run(j), v);
+  const float2 front = v;
+#pragma unroll 4
+  for (int j = at.rank; j < cs; ++j) v = apply<CUTS>(cta_run(j), v);
   return apply<CUTS>(before, front);
 }
 
@@ -371,119 +409,250 @@ __device__ __forceinline__ void close_runs(const Place &at, int32_t *err) {
   cluster_wait();
 }
 
-// reset flags of tokens [0, n) as bits; the same in every lane
-__device__ __forceinline__ uint32_t reset_bits(const uint8_t *reset, int64_t row, int n, int lane) {
-  return __ballot_sync(kFull, lane < n && reset[row + lane] != 0);
+// lane i < n: token i's reset flag (loaded a step before it is needed)
+__device__ __forceinline__ uint32_t reset_flag(const uint8_t *reset, int64_t row, int n, int lane) {
+  return lane < n ? reset[row + lane] : 0;
+}
+
+// The larger magnitude's bits of a pair; a NaN's are above every number's.
+__device__ __forceinline__ uint32_t max_magnitude(float2 v) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+  return __float_as_uint(m);
+}
+
+// The checkpoint of 8 tokens from shared memory to global memory: token i's
+// codes are the first 64 bytes of its row in each of the three tensors' rows, the
+// exponents are `bytes`.  VEC: 16 bytes a lane.  Groups with a value that has no
+// code get zeros and 255.
+template <class E, bool VEC>
+__device__ __forceinline__ void put_codes(const GlrArgs &a, unsigned char *q, const unsigned char *bytes, int64_t row,
+                                          int n, int c0, int chan, int lane) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
+  __syncwarp();
+  const int k = lane >> 3, i = lane & 7;
+  uint32_t byte = lane < 24 ? bytes[lane] : 0;
+  for (uint32_t bad = __ballot_sync(kFull, lane < 24 && i < n && byte > ckpt8::kLast); bad; bad &= bad - 1) {
+    const int j = __ffs(bad) - 1;
+    *reinterpret_cast<uint16_t *>(q + (j >> 3) * Rows<E>::kBytes + (j & 7) * Rows<E>::kRow + 2 * lane) = 0;
+    if (lane == j) byte = 255;
+    __syncwarp();
+  }
+  if (lane < 24 && i < n) a.exps[(k * rows + row + i) * ckpt8::groups(a.D) + c0 / kChan] = static_cast<uint8_t>(byte);
+  if (VEC && a.D % 16 == 0) {
+    const int j = lane >> 2, at = 16 * (lane & 3);
+    if (j < n && at < chan) {
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<int4 *>(a.codes + (p * rows + row + j) * a.D + c0 + at) =
+            *reinterpret_cast<const int4 *>(q + p * Rows<E>::kBytes + j * Rows<E>::kRow + at);
+    }
+  } else {
+    for (int p = 0; p < 3; ++p)
+      for (int j = 0; j < n; ++j) {
+        int8_t *o = a.codes + (p * rows + row + j) * a.D + c0;
+        const unsigned char *s = q + p * Rows<E>::kBytes + j * Rows<E>::kRow;
+        if (2 * lane < chan) o[2 * lane] = static_cast<int8_t>(s[2 * lane]);
+        if (2 * lane + 1 < chan) o[2 * lane + 1] = static_cast<int8_t>(s[2 * lane + 1]);
+      }
+  }
 }
 
 // ---- forward ----
 // K8: also the 8-bit checkpoints of x, r and g.  CUTS: with reset flags.
 template <class E, bool VEC, bool K8, bool CUTS>
-__global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs a) {
+__global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
-  constexpr int kStage = 3 * Rows<E>::kBytes;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned char *mine = smem + sizeof(Runs) + warp * 2 * kStage;
+  constexpr int kBytes = Rows<E>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg, kOut = K8 ? 32 : 0;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+  unsigned char *mine = smem + sizeof(Runs) + warp * (kHalves * kHalf + kOut);
   const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
-  Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
-  open_runs(runs, at);
+  Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
   const int len = load_len(a, b);
-  const int64_t row0 = static_cast<int64_t>(b) * a.T;
   const float2 rate2 = make_float2(one ? -kLog2e * load_rate(a, c) : 0.f, two ? -kLog2e * load_rate(a, c + 1) : 0.f);
   const int64_t sc = static_cast<int64_t>(b) * a.D + c;
   float2 v = make_float2(one ? a.state[sc] : 0.f, two ? a.state[sc + 1] : 0.f);
-  const int steps = (len + kTile * cs - 1) / (kTile * cs);
-  auto first = [&](int step) { return (step * cs + rank) * kTile + warp * kSeg; };
-  auto count = [&](int t0) { return max(0, min(kSeg, len - t0)); };
-  auto fetch = [&](int step) {
-    const int t0 = first(step), n = step < steps ? count(t0) : 0;
+  open_runs(runs, at);  // behind the state's loads: another CTA may write it in place
+  const int tile = kForwardRun * kWarps, tokens = tile * cs;  // tokens of a CTA and of the cluster in a step
+  const int steps = (len + tokens - 1) / tokens;
+  int t0 = rank * tile + warp * kForwardRun;  // first token of the run
+  const int64_t first = static_cast<int64_t>(b) * a.T + t0;
+  Walk<E, VEC> wx(static_cast<const E *>(a.x) + first * a.ld_x + c0, a.ld_x, chan, lane);
+  Walk<E, VEC> wr(static_cast<const E *>(a.r) + first * a.ld_r + c0, a.ld_r, chan, lane);
+  Walk<E, VEC> wg(static_cast<const E *>(a.g) + first * a.ld_g + c0, a.ld_g, chan, lane);
+  E *y = static_cast<E *>(a.y) + first * a.D + c0;
+  float *carry = a.carry ? a.carry + (static_cast<int64_t>(b) * a.S + t0 / kSeg) * a.D + c0 : nullptr;
+  const uint32_t row_bytes = a.D * static_cast<uint32_t>(sizeof(E));
+  // the rows of the run's first or second 8 tokens, t the first of them
+  auto fetch = [&](int half, int t) {
+    const int n = min(kSeg, len - t), on = half == kHalves - 1 ? tokens - kForwardRun + kSeg : kSeg;
     if (n > 0) {
-      unsigned char *d = mine + (step & 1) * kStage;
-      copy_rows<E, VEC>(d, static_cast<const E *>(a.x) + (row0 + t0) * a.ld_x + c0, a.ld_x, n, chan, lane);
-      copy_rows<E, VEC>(d + Rows<E>::kBytes, static_cast<const E *>(a.r) + (row0 + t0) * a.ld_r + c0, a.ld_r, n, chan, lane);
-      copy_rows<E, VEC>(d + 2 * Rows<E>::kBytes, static_cast<const E *>(a.g) + (row0 + t0) * a.ld_g + c0, a.ld_g, n, chan, lane);
+      unsigned char *d = mine + half * kHalf;
+      wx.copy(d, n, lane);
+      wr.copy(d + kBytes, n, lane);
+      wg.copy(d + 2 * kBytes, n, lane);
+      wx.move(on), wr.move(on), wg.move(on);
     }
     cp_async_commit();
   };
-  fetch(0);
+  for (int half = 0; half < kHalves; ++half) fetch(half, t0 + kSeg * half);
   if (cs > 1) cluster_wait();  // every CTA of the cluster runs before one writes into another
-  int bad = 0;
-  for (int step = 0; step < steps; ++step) {
-    fetch(step + 1);
-    cp_async_wait<1>();
-    __syncwarp();
-    const int t0 = first(step), n = count(t0);
-    const unsigned char *d = mine + (step & 1) * kStage;
-    const uint32_t cut = CUTS ? reset_bits(a.reset, row0 + t0, n, lane) : 0;
-    float2 f[kSeg], u[kSeg];
+  uint32_t top = 0;            // K8: the largest magnitude's bits
+  const uint8_t *flags = CUTS ? a.reset + static_cast<int64_t>(b) * a.T : nullptr;
+  uint32_t flag = CUTS ? reset_flag(flags, t0, min(kForwardRun, len - t0), lane) : 0;
+  for (int step = 0; step < steps; ++step, t0 += tokens) {
+    const int n = max(0, min(kForwardRun, len - t0));
+    const uint32_t cut = CUTS ? __ballot_sync(kFull, flag != 0) : 0;
+    if (CUTS) flag = reset_flag(flags, t0 + tokens, min(kForwardRun, len - t0 - tokens), lane);
+    float2 f[kForwardRun], u[kForwardRun];
 #pragma unroll
-    for (int i = 0; i < kSeg; ++i) {
-      const float2 x = row_pair(d, i, lane, static_cast<const E *>(nullptr));
-      const float2 r = row_pair(d + Rows<E>::kBytes, i, lane, static_cast<const E *>(nullptr));
-      const float2 g = row_pair(d + 2 * Rows<E>::kBytes, i, lane, static_cast<const E *>(nullptr));
-      const float2 l = mul2(rate2, sigmoid2(r)), sg = sigmoid2(g);
-      f[i] = decay(l);
-      const float2 m2 = complement(l, f[i]);
-      u[i] = mul2(mul2(make_float2(root(m2.x), root(m2.y)), sg), x);
-      if (K8 && i < n) {
-        const int64_t row = row0 + t0 + i, rows = static_cast<int64_t>(a.B) * a.T;
-        const int G = ckpt8::groups(a.D);
-        const float2 in[3] = {x, r, g};
+    for (int half = 0; half < kHalves; ++half) {
+      cp_async_wait<kHalves - 1>();
+      __syncwarp();
+      unsigned char *d = mine + half * kHalf;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t ux = one ? __float_as_uint(in[k].x) & 0x7fffffffu : 0, uy = two ? __float_as_uint(in[k].y) & 0x7fffffffu : 0;
-          const uint32_t byte = ckpt8::exp_byte(__reduce_max_sync(kFull, max(ux, uy)));
-          const float inv = ckpt8::inv_step(byte);
-          const uint32_t q0 = byte == 255u ? 0 : ckpt8::code_bits(in[k].x, inv), q1 = byte == 255u ? 0 : ckpt8::code_bits(in[k].y, inv);
-          int8_t *q = a.codes + (k * rows + row) * a.D + c;
-          if (VEC) {
-            if (one) *reinterpret_cast<uint16_t *>(q) = static_cast<uint16_t>(__byte_perm(q0, q1, 0x0040));
-          } else {
-            if (one) q[0] = static_cast<int8_t>(q0);
-            if (two) q[1] = static_cast<int8_t>(q1);
+      for (int i = 0; i < kSeg; ++i) {
+        const float2 x = row_pair(d, i, lane, static_cast<const E *>(nullptr));
+        const float2 r = row_pair(d + kBytes, i, lane, static_cast<const E *>(nullptr));
+        const float2 g = row_pair(d + 2 * kBytes, i, lane, static_cast<const E *>(nullptr));
+        const float2 l = mul2(rate2, sigmoid2(r)), sg = sigmoid2(g);
+        const float2 fi = decay(l);
+        f[kSeg * half + i] = fi;
+        u[kSeg * half + i] = mul2(mul2(root2(complement(l, fi)), sg), x);
+        if (K8) {
+          // a code goes where the token's inputs were: every lane's are in the maximum below, so they have been read
+          const float2 in[3] = {x, r, g};
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t big = __reduce_max_sync(kFull, max_magnitude(in[k]));
+            const uint32_t step8 = ckpt8::step_bits(big);
+            const float2 code = fma2(in[k], dup(__uint_as_float((254u << 23) - step8)), dup(12582912.f));
+            *reinterpret_cast<uint16_t *>(d + k * kBytes + i * Rows<E>::kRow + 2 * lane) =
+                static_cast<uint16_t>(__byte_perm(__float_as_uint(code.x), __float_as_uint(code.y), 0x0040));
+            if (lane == 0) mine[kHalves * kHalf + 8 * k + i] = static_cast<unsigned char>(step8 >> 23);
+            top = kSeg * half + i < n ? max(top, big) : top;
           }
-          if (lane == 0) a.exps[(k * rows + row) * G + c0 / kChan] = static_cast<uint8_t>(byte);
-          bad |= byte == 255u;
         }
       }
+      if (K8 && n > kSeg * half)
+        put_codes<E, VEC>(a, d, mine + kHalves * kHalf, static_cast<int64_t>(b) * a.T + t0 + kSeg * half,
+                          min(kSeg, n - kSeg * half), c0, chan, lane);
+      __syncwarp();  // the copies go where these rows were read
+      fetch(half, t0 + tokens + kSeg * half);
     }
-    if (n < kSeg) {
+    if (n < kForwardRun) {
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i)
+      for (int i = 0; i < kForwardRun; ++i)
         if (i >= n) f[i] = dup(1.f), u[i] = dup(0.f);
     }
-    Run q{f[0], u[0], cut != 0};
+    Run q{f[0], u[0], CUTS && cut != 0};
     if (CUTS && cut) {
 #pragma unroll
-      for (int i = 1; i < kSeg; ++i) q.H = cut >> i & 1 ? u[i] : fma2(f[i], q.H, u[i]);
+      for (int i = 1; i < kForwardRun; ++i) q.H = cut >> i & 1 ? u[i] : fma2(f[i], q.H, u[i]);
       q.P = dup(0.f);
     } else {
 #pragma unroll
-      for (int i = 1; i < kSeg; ++i) q.P = mul2(q.P, f[i]), q.H = fma2(f[i], q.H, u[i]);
+      for (int i = 1; i < kForwardRun; ++i) q.P = mul2(q.P, f[i]), q.H = fma2(f[i], q.H, u[i]);
     }
-    float2 h = compose<false, CUTS>(runs, step, at, q, v);
+    float2 h = compose<CUTS>(runs, step, at, q, v);
     if (n > 0 && one) {
-      if (a.carry) {
-        float *k = a.carry + (static_cast<int64_t>(b) * a.S + t0 / kSeg) * a.D + c;
-        store2<VEC>(k, h, two);
-      }
-      E *y = static_cast<E *>(a.y) + (row0 + t0) * a.D + c;
+      uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E));
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i) {
+      for (int i = 0; i < kForwardRun; ++i, o += row_bytes) {
+        if (i % kSeg == 0 && i < n && carry) store2<VEC>(carry + (i ? a.D : 0), 8u * lane, h, two);
         h = CUTS && cut >> i & 1 ? u[i] : fma2(f[i], h, u[i]);
-        if (i < n) store2<VEC>(y + static_cast<int64_t>(i) * a.D, h, two);
+        if (i < n) store2<VEC>(y, o, h, two);
+      }
+      if (t0 + n == len) {  // the last token's state, as y has it
+        a.state_out[sc] = h.x;
+        if (two) a.state_out[sc + 1] = h.y;
       }
     }
+    y += static_cast<int64_t>(tokens) * a.D;
+    if (carry) carry += static_cast<int64_t>(tokens / kSeg) * a.D;
   }
-  if (rank == 0 && warp == 0 && one) {
+  if (len == 0 && rank == 0 && warp == 0 && one) {
     a.state_out[sc] = v.x;
     if (two) a.state_out[sc + 1] = v.y;
   }
   close_runs(at, a.err);
-  if (K8 && bad && lane == 0 && a.err) atomicOr(a.err, SDM_DEVERR_NONFINITE);
+  if (K8 && top > ckpt8::kTop && lane == 0 && a.err) atomicOr(a.err, SDM_DEVERR_NONFINITE);
+}
+
+// ---- a few tokens: decoding steps ----
+// N channels of one sequence a thread (N = 16 bytes of E, or 1 where rows are
+// not aligned to that), its tokens in order; the same operations as above, so the
+// same bits.  Bound by the launch and, for large batches, by memory.
+template <class E, int N>
+struct alignas(sizeof(E) * N) Pack {
+  E v[N];
+};
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ void narrow(float &o, float v) { o = v; }
+__device__ __forceinline__ void narrow(uint16_t &o, float v) { o = static_cast<uint16_t>(bf16_pair(make_float2(v, 0.f))); }
+
+template <class E, int N>
+__global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
+  const int per = a.D / N;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.B) * per) return;
+  const int b = static_cast<int>(i / per), c = static_cast<int>(i - static_cast<int64_t>(b) * per) * N;
+  const int len = load_len(a, b);
+  const int64_t sc = static_cast<int64_t>(b) * a.D + c;
+  using P = Pack<E, N>;
+  using S = Pack<float, N < 4 ? N : 4>;
+  constexpr int kS = N < 4 ? N : 4;
+  float h[N], rate2[N];
+#pragma unroll
+  for (int j = 0; j < N; j += kS) {
+    const S s = *reinterpret_cast<const S *>(a.state + sc + j), q = *reinterpret_cast<const S *>(a.rate + c + j);
+#pragma unroll
+    for (int l = 0; l < kS; ++l) h[j + l] = s.v[l], rate2[j + l] = q.v[l];
+  }
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const bool ok = rate2[j] >= 0.f && rate2[j] < __int_as_float(0x7f800000);
+    bad |= !ok;
+    rate2[j] = ok ? -kLog2e * rate2[j] : 0.f;
+  }
+  if (bad && a.err) atomicOr(a.err, SDM_DEVERR_RATE);
+  const int64_t row0 = static_cast<int64_t>(b) * a.T;
+  for (int t = 0; t < len; ++t) {
+    const int64_t row = row0 + t;
+    const P x = *reinterpret_cast<const P *>(static_cast<const E *>(a.x) + row * a.ld_x + c);
+    const P r = *reinterpret_cast<const P *>(static_cast<const E *>(a.r) + row * a.ld_r + c);
+    const P g = *reinterpret_cast<const P *>(static_cast<const E *>(a.g) + row * a.ld_g + c);
+    const bool cut = a.reset && a.reset[row] != 0;
+    P y;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const int k = N > 1 ? j + 1 : j;
+      const float2 sr = sigmoid2(make_float2(widen(r.v[j]), widen(r.v[k])));
+      const float2 sg = sigmoid2(make_float2(widen(g.v[j]), widen(g.v[k])));
+      const float2 l = mul2(make_float2(rate2[j], rate2[k]), sr), f = decay(l);
+      const float2 u = mul2(mul2(root2(complement(l, f)), sg), make_float2(widen(x.v[j]), widen(x.v[k])));
+      const float2 n = cut ? u : fma2(f, make_float2(h[j], h[k]), u);
+      h[j] = n.x;
+      narrow(y.v[j], n.x);
+      if (N > 1) {
+        h[k] = n.y;
+        narrow(y.v[k], n.y);
+      }
+    }
+    *reinterpret_cast<P *>(static_cast<E *>(a.y) + row * a.D + c) = y;
+  }
+#pragma unroll
+  for (int j = 0; j < N; j += kS) {
+    S s;
+#pragma unroll
+    for (int l = 0; l < kS; ++l) s.v[l] = h[j + l];
+    *reinterpret_cast<S *>(a.state_out + sc + j) = s;
+  }
 }
 
 // ---- backward ----
@@ -491,83 +660,102 @@ __global__ void __launch_bounds__(kWarps * 32) glr_forward_kernel(const GlrArgs 
 // e_t = a_t dh_t, the gradient that reaches h_{t-1}: dh_t = dy_t + e_{t+1}.
 // K8: x, r and g come from their checkpoints.
 template <class E, bool VEC, bool K8, bool CUTS>
-__global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs a) {
+__global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
   using I = typename std::conditional<K8, int8_t, E>::type;  // what x, r and g are held in
-  constexpr int kStage = 3 * Rows<I>::kBytes + Rows<E>::kBytes;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned char *mine = smem + sizeof(Runs) + warp * 2 * kStage;
+  constexpr int kBytes = Rows<I>::kBytes, kStage = 3 * kBytes + Rows<E>::kBytes, kOut = K8 ? 24 * sizeof(float) : 0;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+  unsigned char *mine = smem + sizeof(Runs) + warp * (kStage + kOut);
   const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
-  Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
-  open_runs(runs, at);
+  Place at{kWarps - 1 - warp, lane, cs - 1 - rank, cs, a.drop && rank == 0, false};
   const int len = load_len(a, b);
-  const int64_t row0 = static_cast<int64_t>(b) * a.T, rows = static_cast<int64_t>(a.B) * a.T;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
   const int G = ckpt8::groups(a.D);
   const float2 rate = make_float2(one ? load_rate(a, c) : 0.f, two ? load_rate(a, c + 1) : 0.f);
   const float2 rate2 = mul2(rate, dup(-kLog2e));
   const int64_t sc = static_cast<int64_t>(b) * a.D + c;
   float2 v = make_float2(one && a.state ? a.state[sc] : 0.f, two && a.state ? a.state[sc + 1] : 0.f);
+  open_runs(runs, at);
   float2 drate = dup(0.f);
-  const int steps = (len + kTile * cs - 1) / (kTile * cs);
-  auto first = [&](int step) { return (step * cs + rank) * kTile + warp * kSeg; };
-  auto count = [&](int t0) { return max(0, min(kSeg, len - t0)); };
-  auto fetch = [&](int step) {
-    const int t0 = first(max(step, 0)), n = step >= 0 ? count(t0) : 0;
+  const int tile = kBackwardRun * kWarps, tokens = tile * cs;
+  const int steps = (len + tokens - 1) / tokens;
+  int t0 = ((steps - 1) * cs + rank) * tile + warp * kBackwardRun;  // below 0 with no tokens: nothing is read then
+  const int64_t first = static_cast<int64_t>(b) * a.T + t0;
+  auto source = [&](const void *p, int64_t ld, int plane) {
+    return K8 ? reinterpret_cast<const I *>(a.codes) + (plane * rows + first) * a.D + c0
+              : static_cast<const I *>(p) + first * ld + c0;
+  };
+  Walk<I, VEC> wx(source(a.x, a.ld_x, 0), K8 ? a.D : a.ld_x, chan, lane);
+  Walk<I, VEC> wr(source(a.r, a.ld_r, 1), K8 ? a.D : a.ld_r, chan, lane);
+  Walk<I, VEC> wg(source(a.g, a.ld_g, 2), K8 ? a.D : a.ld_g, chan, lane);
+  Walk<E, VEC> wy(static_cast<const E *>(a.y) + first * a.D + c0, a.D, chan, lane);
+  int64_t out = first * a.ld_d + c0;
+  const uint32_t out_row = static_cast<uint32_t>(a.ld_d) * static_cast<uint32_t>(sizeof(E));
+  auto count = [&](int t) { return t < 0 ? 0 : max(0, min(kSeg, len - t)); };
+  auto fetch = [&](int n) {
     if (n > 0) {
-      unsigned char *d = mine + (step & 1) * kStage;
-      const int64_t row = row0 + t0;
-      if constexpr (K8) {
-        for (int k = 0; k < 3; ++k)
-          copy_codes<VEC>(d + k * Rows<I>::kBytes, a.codes + (k * rows + row) * a.D + c0, a.D, n, chan, lane);
-      } else {
-        copy_rows<E, VEC>(d, static_cast<const E *>(a.x) + row * a.ld_x + c0, a.ld_x, n, chan, lane);
-        copy_rows<E, VEC>(d + Rows<E>::kBytes, static_cast<const E *>(a.r) + row * a.ld_r + c0, a.ld_r, n, chan, lane);
-        copy_rows<E, VEC>(d + 2 * Rows<E>::kBytes, static_cast<const E *>(a.g) + row * a.ld_g + c0, a.ld_g, n, chan, lane);
-      }
-      copy_rows<E, VEC>(d + 3 * Rows<I>::kBytes, static_cast<const E *>(a.y) + row * a.D + c0, a.D, n, chan, lane);
+      wx.copy(mine, n, lane);
+      wr.copy(mine + kBytes, n, lane);
+      wg.copy(mine + 2 * kBytes, n, lane);
     }
+    wx.move(-tokens), wr.move(-tokens), wg.move(-tokens);
     cp_async_commit();
   };
-  fetch(steps - 1);
-  if (cs > 1) cluster_wait();
-  for (int step = steps - 1; step >= 0; --step) {
-    fetch(step - 1);
-    const int t0 = first(step), n = count(t0);
-    const uint32_t cut = CUTS ? reset_bits(a.reset, row0 + t0, n, lane) : 0;
-    float2 h = dup(0.f);
-    uint32_t exps = 0;  // lane 8 k + i: plane k, token i
+  auto fetch_dy = [&](int n) {
+    if (n > 0) wy.copy(mine + 3 * kBytes, n, lane);
+    wy.move(-tokens);
+    cp_async_commit();
+  };
+  // what a step needs besides its rows, loaded a step ahead: flags, the kept
+  // state, the checkpoint groups' exponents (lane 8 k + i: plane k, token i)
+  const uint8_t *flags = CUTS ? a.reset + static_cast<int64_t>(b) * a.T : nullptr;
+  uint32_t flag = 0, exps = 1;
+  float2 h0 = dup(0.f);
+  auto ahead = [&](int t) {
+    const int n = count(t);
+    if (CUTS) flag = reset_flag(flags, t, n, lane);
     if (n > 0) {
-      const float *k = a.carry + (static_cast<int64_t>(b) * a.S + t0 / kSeg) * a.D + c;
+      const float *k = a.carry + (static_cast<int64_t>(b) * a.S + t / kSeg) * a.D + c;
       if (VEC) {
-        if (one) h = *reinterpret_cast<const float2 *>(k);
+        if (one) h0 = *reinterpret_cast<const float2 *>(k);
       } else {
-        h = make_float2(one ? k[0] : 0.f, two ? k[1] : 0.f);
+        h0 = make_float2(one ? k[0] : 0.f, two ? k[1] : 0.f);
       }
       if (K8 && lane < 24 && (lane & 7) < n)
-        exps = a.exps[((lane >> 3) * rows + row0 + t0 + (lane & 7)) * G + c0 / kChan];
+        exps = a.exps[((lane >> 3) * rows + static_cast<int64_t>(b) * a.T + t + (lane & 7)) * G + c0 / kChan];
     }
+  };
+  ahead(t0);
+  fetch(count(t0));
+  fetch_dy(count(t0));
+  if (cs > 1) cluster_wait();
+  for (int step = 0; step < steps; ++step, t0 -= tokens) {
+    const int n = count(t0);
+    const uint32_t cut = CUTS ? __ballot_sync(kFull, flag != 0) : 0;
+    float2 h = h0;
+    if (K8 && lane < 24) reinterpret_cast<float *>(mine + kStage)[lane] = ckpt8::step(exps);
+    ahead(t0 - tokens);
     cp_async_wait<1>();
     __syncwarp();
-    const unsigned char *d = mine + (step & 1) * kStage;
+    const unsigned char *d = mine;
     auto input = [&](int k, int i) {
       if constexpr (K8) {
-        const uint16_t q = *reinterpret_cast<const uint16_t *>(d + k * Rows<I>::kBytes + i * kChan + 2 * lane);
-        const float s = ckpt8::step(__shfl_sync(kFull, exps, 8 * k + i));
-        return mul2(make_float2(static_cast<float>(static_cast<int8_t>(q & 0xff)), static_cast<float>(static_cast<int8_t>(q >> 8))), dup(s));
+        return ckpt8::decode2(*reinterpret_cast<const uint16_t *>(d + k * kBytes + i * kChan + 2 * lane),
+                              reinterpret_cast<const float *>(mine + kStage)[8 * k + i]);
       } else {
-        return row_pair(d + k * Rows<I>::kBytes, i, lane, static_cast<const E *>(nullptr));
+        return row_pair(d + k * kBytes, i, lane, static_cast<const E *>(nullptr));
       }
     };
     // per token: the decay; what dh is multiplied by in dx and dg; and -sr a
     // (h_{t-1} - (a / m) sg x), by which it is in drate (dr: that times rate (1 - sr))
-    float2 f[kSeg], cx[kSeg], cg[kSeg], cr[kSeg], ck[kSeg], dy[kSeg];
+    float2 f[kSeg], cx[kSeg], cg[kSeg], cr[kSeg], ck[kSeg];
+    auto dy = [&](int i) { return row_pair(d + 3 * kBytes, i, lane, static_cast<const E *>(nullptr)); };
 #pragma unroll
     for (int i = 0; i < kSeg; ++i) {
       const float2 x = input(0, i), sr = sigmoid2(input(1, i)), sg = sigmoid2(input(2, i));
-      dy[i] = row_pair(d + 3 * Rows<I>::kBytes, i, lane, static_cast<const E *>(nullptr));
       const float2 l = mul2(rate2, sr);
       f[i] = decay(l);
       const float2 m2 = complement(l, f[i]);
@@ -582,39 +770,43 @@ __global__ void __launch_bounds__(kWarps * 32) glr_backward_kernel(const GlrArgs
       ck[i] = mul2(rate, fma2(sr, dup(-1.f), dup(1.f)));
       h = fma2(f[i], h, u);
     }
-    if (n < kSeg) {
+    cp_async_wait<0>();
+    __syncwarp();  // dy is here, and the next inputs go where these were read
+    fetch(count(t0 - tokens));
+    Run q{dup(1.f), dup(0.f), CUTS && cut != 0};
+    if (n == kSeg && !(CUTS && cut)) {
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i)
-        if (i >= n) f[i] = dup(1.f), dy[i] = dup(0.f);
-    }
-    Run q{dup(1.f), dup(0.f), cut != 0};
-    if (CUTS && cut) {
-#pragma unroll
-      for (int i = kSeg - 1; i >= 0; --i) q.H = cut >> i & 1 ? dup(0.f) : mul2(f[i], add2(dy[i], q.H));
-      q.P = dup(0.f);
+      for (int i = kSeg - 1; i >= 0; --i) q.P = mul2(q.P, f[i]), q.H = mul2(f[i], add2(dy(i), q.H));
     } else {
 #pragma unroll
-      for (int i = kSeg - 1; i >= 0; --i) q.P = mul2(q.P, f[i]), q.H = mul2(f[i], add2(dy[i], q.H));
-    }
-    float2 e = compose<true, CUTS>(runs, steps - 1 - step, at, q, v);
-    if (n > 0) {
-      const int64_t at = (row0 + t0) * a.ld_d + c;
-#pragma unroll
-      for (int i = kSeg - 1; i >= 0; --i) {
+      for (int i = kSeg - 1; i >= 0; --i)
         if (i < n) {
-          const float2 dh = add2(dy[i], e);
+          q.P = mul2(q.P, f[i]);
+          q.H = CUTS && cut >> i & 1 ? dup(0.f) : mul2(f[i], add2(dy(i), q.H));
+        }
+    }
+    float2 e = compose<CUTS>(runs, step, at, q, v);
+    if (n > 0) {
+E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
+      uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
+#pragma unroll
+      for (int i = kSeg - 1; i >= 0; --i, o -= out_row) {
+        if (i < n) {
+          const float2 dh = add2(dy(i), e);
           const float2 w = mul2(dh, cr[i]);
           drate = add2(drate, w);
           if (one) {
-            const int64_t o = at + i * a.ld_d;
-            store2<VEC>(static_cast<E *>(a.dx) + o, mul2(dh, cx[i]), two);
-            store2<VEC>(static_cast<E *>(a.dr) + o, mul2(w, ck[i]), two);
-            store2<VEC>(static_cast<E *>(a.dg) + o, mul2(dh, cg[i]), two);
+            store2<VEC>(dx, o, mul2(dh, cx[i]), two);
+            store2<VEC>(dr, o, mul2(w, ck[i]), two);
+            store2<VEC>(dg, o, mul2(dh, cg[i]), two);
           }
           e = CUTS && cut >> i & 1 ? dup(0.f) : mul2(f[i], dh);
         }
       }
     }
+    out -= tokens * a.ld_d;
+    __syncwarp();  // the next dy goes where this was read
+    fetch_dy(count(t0 - tokens));
   }
   if (rank == 0 && warp == 0 && one) {
     a.state_out[sc] = v.x;
@@ -661,7 +853,7 @@ int check_sizes(const char *fn, int dtype, int B, int T, int D) {
 // [B,T,D] tensors of `dtype` with their distance between tokens
 int check_rows(const char *fn, const char *name, const void *p, int64_t ld, int dtype, int D) {
   if (!p) return set_error(SDM_ERR_INVALID_ARG, "%s: null pointer (%s)", fn, name);
-  if (ld < D || ld >= int64_t(1) << 31) return set_error(SDM_ERR_SHAPE, "%s: need D <= ld < 2^31 (%s)", fn, name);
+  if (ld < D || ld >= 1 << 27) return set_error(SDM_ERR_SHAPE, "%s: need D <= ld < 2^27 (%s)", fn, name);
   if (!aligned(p, dtype == SDM_DTYPE_F32 ? 4 : 2))
     return set_error(SDM_ERR_ALIGN, "%s: %s must be aligned to its element", fn, name);
   return SDM_OK;
@@ -673,18 +865,44 @@ int check_words(const char *fn, std::initializer_list<const void *> ps) {
   return SDM_OK;
 }
 
-// CTAs of a cluster: the split of the sequence that leaves the least to the
-// busiest SM, in tiles, as long as the whole grid runs at once.
-int cluster_size(int B, int T, int D, int per_sm) {
+// Shared memory of a CTA: the runs and, for each warp, its rows.
+size_t forward_smem(int dtype, bool keep8) {
+  const size_t rows = dtype == SDM_DTYPE_F32 ? Rows<float>::kBytes : Rows<uint16_t>::kBytes;
+  return sizeof(Runs) + kWarps * (kForwardRun / kSeg * 3 * rows + (keep8 ? 32 : 0));
+}
+size_t backward_smem(int dtype, bool keep8) {
+  const size_t rows = dtype == SDM_DTYPE_F32 ? Rows<float>::kBytes : Rows<uint16_t>::kBytes;
+  return sizeof(Runs) + kWarps * (3 * (keep8 ? Rows<int8_t>::kBytes : rows) + rows + (keep8 ? 24 * sizeof(float) : 0));
+}
+
+// CTAs of a cluster.  A walk takes its steps once while the whole grid runs at
+// once, however few CTAs an SM has (it then waits for memory and for the runs of others);
+// beyond that, between the grid's share of the GPU and whole waves of it times as long.
+// Clusters of more than two CTAs find room on 148 of the 152 SMs.  Measured for 8 x 4096 x 1920
+// in bf16, forward: 127 us with 2 CTAs (79% of one wave), 136 with 3 (two
+// waves), 115 with 4, 127 with 5; 1 x 32768 x 3840: 250 with 8, 229 with 9.
+int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
   const int64_t columns = static_cast<int64_t>(B) * ((D + kChan - 1) / kChan);
+  const int per_sm = min(65536 / (32 * regs) / kWarps, static_cast<int>((227 << 10) / (smem + 1024)));
+  const int tile = run * kWarps;
   int best = 1;
-  int64_t least = INT64_MAX;
+  double least = 1e300;
   for (int cs = 1; cs <= kMaxCluster; ++cs) {
-    if (cs > 1 && (columns * cs > int64_t(kSMs) * per_sm || (cs - 1) * kTile >= T)) break;
-    const int64_t load = (columns * cs + kSMs - 1) / kSMs * ((T + kTile * cs - 1) / (kTile * cs));
-    if (load < least) least = load, best = cs;
+    if (cs > 1 && (cs - 1) * tile >= T) break;
+    const int64_t room = (cs > 2 ? kSMs - 4 : kSMs) * per_sm, ctas = columns * cs;
+    if (cs > 8 && ctas > room) break;  // large clusters pay only where they fill the GPU
+    const int64_t waves = (ctas + room - 1) / room, steps = (T + tile * cs - 1) / (tile * cs);
+    const double share = static_cast<double>(ctas) / room;
+    const double time = steps * ((share < 1 ? 1 : share) + waves) / 2;
+    if (time < 0.95 * least) least = time, best = cs;
   }
   return best;
+}
+int forward_cluster(int B, int T, int D, int dtype) {
+  return cluster_size(B, T, D, kForwardRun, kForwardRegs, forward_smem(dtype, false));
+}
+int backward_cluster(int B, int T, int D, int dtype) {
+  return cluster_size(B, T, D, kBackwardRun, kBackwardRegs, backward_smem(dtype, false));
 }
 
 // 16-byte copies of rows, pairwise stores
@@ -695,6 +913,10 @@ template <class K>
 int launch(const char *fn, K kernel, size_t smem, const GlrArgs &a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  if (a.cs > 8) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((a.D + kChan - 1) / kChan * a.cs, a.B);
   cfg.blockDim = dim3(kWarps * 32);
@@ -710,9 +932,23 @@ int launch(const char *fn, K kernel, size_t smem, const GlrArgs &a, cudaStream_t
   return check_launch(fn);
 }
 
+// Up to kStepTokens tokens and nothing to keep: one thread walks them all.
+constexpr int kStepTokens = 8;
+template <class E>
+int launch_step(const char *fn, const GlrArgs &a, cudaStream_t st) {
+  constexpr int N = 16 / sizeof(E), es = sizeof(E);
+  const bool wide = a.D % N == 0 && rows_vec(a.x, a.ld_x, es) && rows_vec(a.r, a.ld_r, es) && rows_vec(a.g, a.ld_g, es) &&
+                    rows_vec(a.y, a.D, es) && aligned(a.state, 16) && aligned(a.state_out, 16) && aligned(a.rate, 16);
+  const int64_t threads = static_cast<int64_t>(a.B) * (wide ? a.D / N : a.D), blocks = (threads + 127) / 128;
+  if (blocks > INT32_MAX) return set_error(SDM_ERR_SHAPE, "%s: B * D too large", fn);
+  if (wide) glr_step_kernel<E, N><<<static_cast<unsigned>(blocks), 128, 0, st>>>(a);
+  else glr_step_kernel<E, 1><<<static_cast<unsigned>(blocks), 128, 0, st>>>(a);
+  return check_launch(fn);
+}
+
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = sizeof(Runs) + kWarps * 2 * 3 * Rows<E>::kBytes;
+  const size_t smem = forward_smem(sizeof(E) == 4 ? SDM_DTYPE_F32 : SDM_DTYPE_BF16, a.codes);
   if (a.reset)
     return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
@@ -721,7 +957,7 @@ int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
 }
 template <class E, bool VEC>
 int launch_backward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = sizeof(Runs) + kWarps * 2 * ((a.codes ? 3 * Rows<int8_t>::kBytes : 3 * Rows<E>::kBytes) + Rows<E>::kBytes);
+  const size_t smem = backward_smem(sizeof(E) == 4 ? SDM_DTYPE_F32 : SDM_DTYPE_BF16, a.codes);
   if (a.reset)
     return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_backward_kernel<E, VEC, false, true>, smem, a, st);
@@ -741,9 +977,11 @@ int forward(const char *fn, GlrArgs &a, int dtype, int8_t *codes, uint8_t *exps,
   }
   if ((rc = check_words(fn, {a.state, a.state_out, a.rate, a.lens, a.carry, a.err}))) return rc;
   if (codes && !aligned(codes, 16)) return set_error(SDM_ERR_ALIGN, "%s: codes must be 16-byte aligned", fn);
+  if (a.T <= kStepTokens && !a.carry)
+    return dtype == SDM_DTYPE_F32 ? launch_step<float>(fn, a, st) : launch_step<uint16_t>(fn, a, st);
   a.codes = codes, a.exps = exps;
   a.drop = test_drop_signal();
-  a.cs = cluster_size(a.B, a.T, a.D, forward_ctas(dtype));
+  a.cs = forward_cluster(a.B, a.T, a.D, dtype);
   const int es = dtype == SDM_DTYPE_F32 ? 4 : 2;
   const bool vec = rows_vec(a.x, a.ld_x, es) && rows_vec(a.r, a.ld_r, es) && rows_vec(a.g, a.ld_g, es) &&
                    pairs_vec(a.y, a.D, es) && (!a.carry || aligned(a.carry, 8));
@@ -835,7 +1073,7 @@ extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const v
   a.y = const_cast<void *>(dy), a.carry = const_cast<float *>(carry);
   a.dx = dx, a.dr = dr, a.dg = dg, a.part = static_cast<float *>(workspace), a.err = dev_err;
   a.drop = test_drop_signal();
-  a.cs = cluster_size(B, T, D, backward_ctas(dtype));
+  a.cs = backward_cluster(B, T, D, dtype);
   if (B > 0) {
     const int es = dtype == SDM_DTYPE_F32 ? 4 : 2;
     const bool in = codes ? D % 16 == 0 : rows_vec(x, ld_x, es) && rows_vec(r, ld_r, es) && rows_vec(g, ld_g, es);

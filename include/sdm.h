@@ -528,7 +528,7 @@ SDM_API int sse_scan(float *state, const float *route_logits, int topk, const fl
  * NaN and infinite x, r, g are not looked for: they run through the
  * arithmetic, into the states of their channel only.  The state, its
  * decays and their products are fp32; y is rounded once, to nearest even.
- * Limits: B, T, D >= 0, B < 65536, T < 2^30, D < 2^24; ld >= D.  x, r, g, y
+ * Limits: B, T, D >= 0, B < 65536, T < 2^30, D < 2^24; D <= ld < 2^27.  x, r, g, y
  *         aligned to their element; state, rate 4-byte.  Any B, T or D of 0
  *         is allowed (T = 0 copies the state).
  */
@@ -617,7 +617,7 @@ SDM_API int glr_scan_backward(const float *dstate, float *dstate_out, const void
  * x     : [rows, D] of `dtype`, row i at ld * i elements (ld >= D for more
  *         than one row); aligned to its element.  Unpacked rows may lie apart too.
  * codes : int8 [rows, D], contiguous.   exps : uint8 [rows, ceil(D/64)].
- * Limits: rows >= 0, 0 <= D < 2^24.
+ * Limits: 0 <= rows < 2^36, 0 <= D < 2^24, ld < 2^27.
  */
 SDM_API int ckpt8_pack(const void *x, int64_t ld, int dtype, int64_t rows, int D, int8_t *codes, uint8_t *exps,
                        int32_t *dev_err, void *stream);

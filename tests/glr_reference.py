@@ -8,13 +8,13 @@ reciprocal are good to 2^-22 and 2^-23 (relative).
       rel <= (1 - sigmoid) (2 |z| E + 2^-22) + 2^-23 + 2 E.
   a = 2^l: l = rate2 sigmoid(r) has three roundings and sigmoid's error,
       rel <= |L| (rel_sigmoid + 3 E) + 2^-22.
-  m = sqrt(1 - a^2), the larger of two forms.  The series in w = -2 L has w's
-      error (rel_sigmoid + 5 E), eight roundings and its first term left out,
-      w^7 / 5040 (an alternating sum: w^6 / 4000 of m^2 covers it while it is
-      the smaller of the two).  The difference 1 - 6e-7 - a^2 has a^2's error, 2 a^2 d_a,
-      and 6e-7 and a rounding.  The larger is below m^2 by the smaller of the two
-      shortfalls, and above it by what a^2's error is over 6e-7 (0.9 of it: the
-      constant is rounded); half of it, and the root's own 2^-22.
+  m = sqrt(1 - a^2), the larger of two forms, neither above it but by rounding.
+      The polynomial in w = -2 L has w's error (rel_sigmoid + 5 E), eight roundings,
+      and falls short by 8e-7 of m^2 up to w = 0.28, by more behind that.  The
+      difference 1 - 6e-7 - a^2 has a^2's error, 2 a^2 d_a, and 6e-7 and a
+      rounding.  The larger falls short by the smaller of the two, and is above
+      m^2 by what a^2's error is over 6e-7 (0.9 of it: the constant is rounded);
+      half of it, and the root's own 2^-22.
 Along the recurrence every token adds a's error and a product's and a sum's
 rounding on top of the decayed one; a split over time multiplies decays with
 one another first, one more rounding a token: 4 E a token covers each order.
@@ -49,7 +49,7 @@ def gates(x, r, g, rate):
     d_a = -L * (rel_sig(r) + 3 * E) + 2.0 ** -22                     # rel error of a
     w, a2 = -2 * L, 2 * a * a * d_a
     with np.errstate(divide="ignore", invalid="ignore"):
-        short = np.where(m2 > 0, np.minimum(w ** 6 / 4000, (a2 + 6.6e-7) / m2), 0)
+        short = np.where(m2 > 0, np.minimum(np.where(w <= 0.28, 8e-7, np.inf), (a2 + 6.6e-7) / m2), 0)
         over = np.where(m2 > 0, np.maximum(0, a2 - 5.4e-7) / m2, 0)
     d_m = 0.5 * (rel_sig(r) + 13 * E + short + over) + 2.0 ** -22
     return sr, sg, a, m, d_a, d_m
