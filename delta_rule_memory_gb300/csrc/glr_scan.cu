@@ -127,10 +127,16 @@ __device__ __forceinline__ float2 complement(float2 l, float2 a) {
 }
 // 1 / sqrt(m2), and 0 where m2 underflows
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
-// sqrt(m2): the added number keeps the root's inverse finite at 0 and is lost from 2^-100 on
-__device__ __forceinline__ float2 root2(float2 m2) {
-  const float2 q = add2(m2, dup(1.17549435e-38f));
-  return mul2(m2, make_float2(rsq(q.x), rsq(q.y)));
+// m sigmoid(g) x with one special function less than its factors take: sigmoid(g)
+// = 1 / d, d = 1 + e^-g, so m / d = m2 / sqrt(d^2 m2).  The number added to m2 keeps
+// the root's inverse finite at m2 = 0 and is lost in it from 2^-100 on.  (The
+// special functions bind: 8 x 4096 x 1920 with the reciprocal of d by itself
+// took 138 us on one CTA a column in place of 127.)
+__device__ __forceinline__ float2 input_term(float2 m2, float2 g, float2 x) {
+  const float2 z = mul2(g, dup(-kLog2e));
+  const float2 d = add2(make_float2(ex2(z.x), ex2(z.y)), dup(1.f));
+  const float2 q = mul2(mul2(d, d), add2(m2, dup(1.17549435e-38f)));
+  return mul2(mul2(m2, x), make_float2(rsq(q.x), rsq(q.y)));
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float2 v) {  // nearest even, v.x in the lower half
@@ -518,10 +524,9 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
         const float2 x = row_pair(d, i, lane, static_cast<const E *>(nullptr));
         const float2 r = row_pair(d + kBytes, i, lane, static_cast<const E *>(nullptr));
         const float2 g = row_pair(d + 2 * kBytes, i, lane, static_cast<const E *>(nullptr));
-        const float2 l = mul2(rate2, sigmoid2(r)), sg = sigmoid2(g);
-        const float2 fi = decay(l);
+        const float2 l = mul2(rate2, sigmoid2(r)), fi = decay(l);
         f[kSeg * half + i] = fi;
-        u[kSeg * half + i] = mul2(mul2(root2(complement(l, fi)), sg), x);
+        u[kSeg * half + i] = input_term(complement(l, fi), g, x);
         if (K8) {
           // a code goes where the token's inputs were: every lane's are in the maximum below, so they have been read
           const float2 in[3] = {x, r, g};
@@ -633,9 +638,9 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
     for (int j = 0; j < N; j += 2) {
       const int k = N > 1 ? j + 1 : j;
       const float2 sr = sigmoid2(make_float2(widen(r.v[j]), widen(r.v[k])));
-      const float2 sg = sigmoid2(make_float2(widen(g.v[j]), widen(g.v[k])));
       const float2 l = mul2(make_float2(rate2[j], rate2[k]), sr), f = decay(l);
-      const float2 u = mul2(mul2(root2(complement(l, f)), sg), make_float2(widen(x.v[j]), widen(x.v[k])));
+      const float2 u = input_term(complement(l, f), make_float2(widen(g.v[j]), widen(g.v[k])),
+                                  make_float2(widen(x.v[j]), widen(x.v[k])));
       const float2 n = cut ? u : fma2(f, make_float2(h[j], h[k]), u);
       h[j] = n.x;
       narrow(y.v[j], n.x);
