@@ -99,7 +99,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float2 sigmoid2(float2 v) {
   const float2 z = mul2(v, dup(-kLog2e));
@@ -107,23 +107,26 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
   return make_float2(rcp(d.x), rcp(d.y));
 }
 
-// The decay and its complement: a = 2^l with l = -rate log2(e) sigmoid(r),
-// m2 = 1 - a^2.  Near a = 1 the difference cancels, and a cubic times w = -2 ln a
-// takes over: the best one (in relative error, by linear programming) among
-// those that stay below 1 - e^-w, off by 7.6e-7 up to w = 0.28 and ever further
-// below behind that.  The difference is taken from 1 - 6e-7 in place of 1, which is
-// more than a^2's error (2 * 2^-22, ex2.approx) can make up for, so it is never
-// above 1 - a^2 either, and the larger of the two is the right one: off by 4.5e-6
-// of it where they meet, by less elsewhere.
-constexpr float kBelow1 = 0.9999994f;
-__device__ __forceinline__ float2 decay(float2 l) { return make_float2(ex2(l.x), ex2(l.y)); }
-__device__ __forceinline__ float2 complement(float2 l, float2 a) {
-  const float2 w = mul2(l, dup(-2.f * kLn2));
-  float2 p = fma2(w, dup(-0.03725945f), dup(0.16590417f));
-  p = fma2(w, p, dup(-0.49995695f));
-  p = fma2(w, p, dup(0.99999924f));
-  p = mul2(w, p);
-  return make_float2(fmaxf(p.x, __fmaf_rn(-a.x, a.x, kBelow1)), fmaxf(p.y, __fmaf_rn(-a.y, a.y, kBelow1)));
+// The decay a = e^-y, y = rate sigmoid(r), and m2 = 1 - a^2 = (1 - a) (2 - (1 - a)),
+// both from e = 1 - a.  Near a = 1 the exponential unit cannot give e (the difference
+// cancels, and its results near 1 are cut off, not rounded: a bias of 2^-25, which a
+// horizon of 1 / e tokens multiplies; sums of gradients lost a digit to it).
+// Up to y = 0.15, where a bias counts little, e = y q(y) with q the cubic next to
+// (1 - e^-y) / y there (by linear programming, q(0) = 1): off by 5e-8 at most.
+// a is off by 2^-25 at most by taking it as 1 - e, which below 1/2 is more than a
+// relative rounding, and nothing next to an input of the same token.
+struct Decay {
+  float2 a, m2;
+};
+__device__ __forceinline__ Decay decay(float2 y) {
+  const float2 l = mul2(y, dup(-kLog2e));
+  const float2 far = fma2(make_float2(ex2(l.x), ex2(l.y)), dup(-1.f), dup(1.f));
+  float2 q = fma2(y, dup(-0.0393375196f), dup(0.166465417f));
+  q = fma2(y, q, dup(-0.499995023f));
+  q = fma2(y, q, dup(1.f));
+  q = mul2(y, q);
+  const float2 e = make_float2(y.x <= 0.15f ? q.x : far.x, y.y <= 0.15f ? q.y : far.y);
+  return Decay{fma2(e, dup(-1.f), dup(1.f)), mul2(e, fma2(e, dup(-1.f), dup(2.f)))};
 }
 // 1 / sqrt(m2), and 0 where m2 underflows
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
@@ -478,7 +481,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   const bool one = c < a.D, two = c + 1 < a.D;
   Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
   const int len = load_len(a, b);
-  const float2 rate2 = make_float2(one ? -kLog2e * load_rate(a, c) : 0.f, two ? -kLog2e * load_rate(a, c + 1) : 0.f);
+  const float2 rate = make_float2(one ? load_rate(a, c) : 0.f, two ? load_rate(a, c + 1) : 0.f);
   const int64_t sc = static_cast<int64_t>(b) * a.D + c;
   float2 v = make_float2(one ? a.state[sc] : 0.f, two ? a.state[sc + 1] : 0.f);
   open_runs(runs, at);  // behind the state's loads: another CTA may write it in place
@@ -524,9 +527,9 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
         const float2 x = row_pair(d, i, lane, static_cast<const E *>(nullptr));
         const float2 r = row_pair(d + kBytes, i, lane, static_cast<const E *>(nullptr));
         const float2 g = row_pair(d + 2 * kBytes, i, lane, static_cast<const E *>(nullptr));
-        const float2 l = mul2(rate2, sigmoid2(r)), fi = decay(l);
-        f[kSeg * half + i] = fi;
-        u[kSeg * half + i] = input_term(complement(l, fi), g, x);
+        const Decay q = decay(mul2(rate, sigmoid2(r)));
+        f[kSeg * half + i] = q.a;
+        u[kSeg * half + i] = input_term(q.m2, g, x);
         if (K8) {
           // a code goes where the token's inputs were: every lane's are in the maximum below, so they have been read
           const float2 in[3] = {x, r, g};
@@ -611,19 +614,19 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
   using P = Pack<E, N>;
   using S = Pack<float, N < 4 ? N : 4>;
   constexpr int kS = N < 4 ? N : 4;
-  float h[N], rate2[N];
+  float h[N], rate[N];
 #pragma unroll
   for (int j = 0; j < N; j += kS) {
     const S s = *reinterpret_cast<const S *>(a.state + sc + j), q = *reinterpret_cast<const S *>(a.rate + c + j);
 #pragma unroll
-    for (int l = 0; l < kS; ++l) h[j + l] = s.v[l], rate2[j + l] = q.v[l];
+    for (int l = 0; l < kS; ++l) h[j + l] = s.v[l], rate[j + l] = q.v[l];
   }
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const bool ok = rate2[j] >= 0.f && rate2[j] < __int_as_float(0x7f800000);
+    const bool ok = rate[j] >= 0.f && rate[j] < __int_as_float(0x7f800000);
     bad |= !ok;
-    rate2[j] = ok ? -kLog2e * rate2[j] : 0.f;
+    rate[j] = ok ? rate[j] : 0.f;
   }
   if (bad && a.err) atomicOr(a.err, SDM_DEVERR_RATE);
   const int64_t row0 = static_cast<int64_t>(b) * a.T;
@@ -638,10 +641,10 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
     for (int j = 0; j < N; j += 2) {
       const int k = N > 1 ? j + 1 : j;
       const float2 sr = sigmoid2(make_float2(widen(r.v[j]), widen(r.v[k])));
-      const float2 l = mul2(make_float2(rate2[j], rate2[k]), sr), f = decay(l);
-      const float2 u = input_term(complement(l, f), make_float2(widen(g.v[j]), widen(g.v[k])),
+      const Decay q = decay(mul2(make_float2(rate[j], rate[k]), sr));
+      const float2 u = input_term(q.m2, make_float2(widen(g.v[j]), widen(g.v[k])),
                                   make_float2(widen(x.v[j]), widen(x.v[k])));
-      const float2 n = cut ? u : fma2(f, make_float2(h[j], h[k]), u);
+      const float2 n = cut ? u : fma2(q.a, make_float2(h[j], h[k]), u);
       h[j] = n.x;
       narrow(y.v[j], n.x);
       if (N > 1) {
@@ -680,7 +683,6 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
   const int G = ckpt8::groups(a.D);
   const float2 rate = make_float2(one ? load_rate(a, c) : 0.f, two ? load_rate(a, c + 1) : 0.f);
-  const float2 rate2 = mul2(rate, dup(-kLog2e));
   const int64_t sc = static_cast<int64_t>(b) * a.D + c;
   float2 v = make_float2(one && a.state ? a.state[sc] : 0.f, two && a.state ? a.state[sc + 1] : 0.f);
   open_runs(runs, at);
@@ -761,9 +763,9 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
 #pragma unroll
     for (int i = 0; i < kSeg; ++i) {
       const float2 x = input(0, i), sr = sigmoid2(input(1, i)), sg = sigmoid2(input(2, i));
-      const float2 l = mul2(rate2, sr);
-      f[i] = decay(l);
-      const float2 m2 = complement(l, f[i]);
+      const Decay q = decay(mul2(rate, sr));
+      f[i] = q.a;
+      const float2 m2 = q.m2;
       const float2 rs = make_float2(inv_m(m2.x), inv_m(m2.y));
       const float2 sx = mul2(sg, x), m = mul2(m2, rs);
       cx[i] = mul2(m, sg);

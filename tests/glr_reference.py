@@ -6,15 +6,15 @@ Bounds.  E = 2^-24 is fp32's half step.  The kernels' exponential and
 reciprocal are good to 2^-22 and 2^-23 (relative).
   sigmoid(z): the exponent z log2(e) is rounded twice (|z| 2 E), so
       rel <= (1 - sigmoid) (2 |z| E + 2^-22) + 2^-23 + 2 E.
-  a = 2^l: l = rate2 sigmoid(r) has three roundings and sigmoid's error,
-      rel <= |L| (rel_sigmoid + 3 E) + 2^-22.
-  m = sqrt(1 - a^2), the larger of two forms, neither above it but by rounding.
-      The polynomial in w = -2 L has w's error (rel_sigmoid + 5 E), eight roundings,
-      and falls short by 8e-7 of m^2 up to w = 0.28, by more behind that.  The
-      difference 1 - 6e-7 - a^2 has a^2's error, 2 a^2 d_a, and 6e-7 and a
-      rounding.  The larger falls short by the smaller of the two, and is above
-      m^2 by what a^2's error is over 6e-7 (0.9 of it: the constant is rounded);
-      half of it, and the root's own 2^-22.
+  y = rate sigmoid(r): sigmoid's error and a rounding, d_y.
+  1 - a = 1 - e^-y, two forms that meet at y = 0.15.  Below: a cubic times y, good
+      to 6e-8, with four roundings, so d_y y a / (1 - a) <= d_y, and 6e-8 + 5 E,
+      relative.  Above: the exponential's 2^-22 and two roundings of its argument
+      (2 E y), relative to a, and a rounding of the difference.
+  a itself: 1 less that, an absolute error e_a (E for the last rounding).
+  m = sqrt((1 - a) (1 + a)): half of 1 - a's relative error (and of 1 + a's, whose
+      absolute error is the same and whose size is between 1 and 2), three
+      roundings, and the root's own 2^-22.
 Along the recurrence every token adds a's error and a product's and a sum's
 rounding on top of the decayed one; a split over time multiplies decays with
 one another first, one more rounding a token: 4 E a token covers each order.
@@ -42,23 +42,25 @@ def rel_sig(z):
 
 
 def gates(x, r, g, rate):
+    """sigmoids, decay, m, and the bounds: of a (absolute), of m (relative)."""
     sr, sg = sig(r), sig(g)
-    L = -rate * sr
-    a, m2 = np.exp(L), -np.expm1(2 * L)
-    m = np.sqrt(m2)
-    d_a = -L * (rel_sig(r) + 3 * E) + 2.0 ** -22                     # rel error of a
-    w, a2 = -2 * L, 2 * a * a * d_a
+    y = rate * sr
+    a, c = np.exp(-y), -np.expm1(-y)                # the decay and 1 - a
+    m = np.sqrt(c * (1 + a))
+    d_y = rel_sig(r) + E
+    near = c * (d_y + 6e-8 + 5 * E)
+    far = a * (y * (d_y + 2 * E) + 2.0 ** -22) + E
+    e_c = np.where(y < 0.149, near, np.where(y > 0.151, far, np.maximum(near, far)))
+    e_a = e_c + E
     with np.errstate(divide="ignore", invalid="ignore"):
-        short = np.where(m2 > 0, np.minimum(np.where(w <= 0.28, 8e-7, np.inf), (a2 + 6.6e-7) / m2), 0)
-        over = np.where(m2 > 0, np.maximum(0, a2 - 5.4e-7) / m2, 0)
-    d_m = 0.5 * (rel_sig(r) + 13 * E + short + over) + 2.0 ** -22
-    return sr, sg, a, m, d_a, d_m
+        d_m = 0.5 * (np.where(c > 0, e_c / c, 0) + e_c) + 1.5 * E + 2.0 ** -22
+    return sr, sg, a, m, e_a, d_m
 
 
 def forward(h0, x, r, g, rate, reset=None, lens=None):
     """y, h_T, all states before each token, and the bounds of y and h_T."""
     B, T, D = x.shape
-    _, sg, a, m, d_a, d_m = gates(x, r, g, rate)
+    _, sg, a, m, e_a, d_m = gates(x, r, g, rate)
     u = m * sg * x
     e_u = np.abs(u) * (d_m + rel_sig(g) + 3 * E)
     y, before = np.zeros((B, T, D)), np.zeros((B, T, D))
@@ -71,7 +73,7 @@ def forward(h0, x, r, g, rate, reset=None, lens=None):
         before[:, t], e_b[:, t] = h, e
         hn = a[:, t] * h * keep + u[:, t]
         Gn = a[:, t] * G * keep + np.abs(u[:, t])
-        en = keep * a[:, t] * (e + G * (d_a[:, t] + 4 * E)) + e_u[:, t] + 2 * E * Gn
+        en = keep * (a[:, t] * (e + 4 * E * G) + e_a[:, t] * G) + e_u[:, t] + 2 * E * Gn
         G = np.where(live[:, None], Gn, G)
         h, e = np.where(live[:, None], hn, h), np.where(live[:, None], en, e)
         y[:, t], e_y[:, t] = h, e
@@ -83,7 +85,7 @@ def backward(f, dhT, x, r, g, rate, dy, reset=None, lens=None, seg=None):
     the true inputs.  seg: states inside a segment of that many tokens are
     recomputed from x, r, g (an 8-bit checkpoint's values) and its first one."""
     B, T, D = x.shape
-    sr, sg, a, m, d_a, d_m = gates(x, r, g, rate)
+    sr, sg, a, m, e_a, d_m = gates(x, r, g, rate)
     u = m * sg * x
     e_u = np.abs(u) * (d_m + rel_sig(g) + 3 * E)
     before, e_b = f["before"].copy(), f["e_before"].copy()
@@ -93,8 +95,8 @@ def backward(f, dhT, x, r, g, rate, dy, reset=None, lens=None, seg=None):
         for t in range(T):
             if t % seg:
                 before[:, t] = a[:, t - 1] * before[:, t - 1] * keep[:, t - 1] + u[:, t - 1]
-                e_b[:, t] = (keep[:, t - 1] * a[:, t - 1] * (e_b[:, t - 1] + np.abs(before[:, t - 1]) *
-                             (d_a[:, t - 1] + 4 * E)) + e_u[:, t - 1] + 2 * E * np.abs(before[:, t]))
+                e_b[:, t] = (keep[:, t - 1] * (a[:, t - 1] * (e_b[:, t - 1] + 4 * E * np.abs(before[:, t - 1])) +
+                                            e_a[:, t - 1] * np.abs(before[:, t - 1])) + e_u[:, t - 1] + 2 * E * np.abs(before[:, t]))
     before, e_b = before * keep, e_b * keep
     dh, e_dh = np.zeros((B, T, D)), np.zeros((B, T, D))
     c, e = dhT.astype(np.float64).copy(), np.zeros((B, D))
@@ -104,7 +106,7 @@ def backward(f, dhT, x, r, g, rate, dy, reset=None, lens=None, seg=None):
         dh[:, t] = dy[:, t] + c
         H = G + np.abs(dy[:, t])
         e_dh[:, t] = e + 2 * E * H
-        e = np.where(lv, keep[:, t] * a[:, t] * (e_dh[:, t] + H * (d_a[:, t] + 4 * E)), e)
+        e = np.where(lv, keep[:, t] * (a[:, t] * (e_dh[:, t] + 4 * E * H) + e_a[:, t] * H), e)
         G = np.where(lv, keep[:, t] * a[:, t] * H, G)
         c = np.where(lv, keep[:, t] * a[:, t] * dh[:, t], c)
     with np.errstate(divide="ignore", invalid="ignore"):
@@ -117,9 +119,11 @@ def backward(f, dhT, x, r, g, rate, dy, reset=None, lens=None, seg=None):
             np.abs(dh * m * sg * x) * (sg * rel_sig(g) + E))
     k = am * sg * x
     inner = before - k
-    e_in = e_b + np.abs(k) * (d_a + d_m + rel_sig(g) + 4 * E) + E * np.abs(inner)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        e_k = np.where(m > 0, np.abs(sg * x) * e_a / m, 0.0) + np.abs(k) * (d_m + rel_sig(g) + 4 * E)
+    e_in = e_b + e_k + E * np.abs(inner)
     dL = a * dh * inner
-    e_dL = np.abs(dL) * (d_a + 4 * E) + a * np.abs(inner) * e_dh + a * np.abs(dh) * e_in
+    e_dL = np.abs(dh * inner) * (e_a + 4 * E * a) + (a + e_a) * (np.abs(inner) * e_dh + np.abs(dh) * e_in)
     dr = -rate * sr * (1 - sr) * dL
     e_dr = (rate * sr * (1 - sr) * e_dL + np.abs(dr) * (rel_sig(r) + 4 * E) +
             rate * sr * np.abs(dL) * (sr * rel_sig(r) + E))
