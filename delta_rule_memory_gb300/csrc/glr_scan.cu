@@ -189,12 +189,13 @@ __device__ __forceinline__ int load_len(const GlrArgs &a, int b) {
 }
 
 // ---- a warp's tokens in shared memory ----
-// Rows of 64 channels of I (an activation type, or int8 codes), token i at
-// i * 64 * sizeof(I).  A warp copies and reads its own rows only, so no CTA
-// barrier guards them.
-template <class I>
+// 8 rows of 64 channels of I (an activation type, or int8 codes).  A warp
+// copies and reads its own rows only, so no CTA barrier guards them.  VEC: rows
+// are 16-byte aligned in global memory and dense here.  Else 16- and 8-bit rows
+// are copied by the 4-byte words that hold them, one word more than they fill.
+template <class I, bool VEC>
 struct Rows {
-  static constexpr int kRow = kChan * static_cast<int>(sizeof(I));
+  static constexpr int kRow = kChan * static_cast<int>(sizeof(I)) + (VEC || sizeof(I) == 4 ? 0 : 8);
   static constexpr int kBytes = kSeg * kRow;
 };
 
@@ -203,18 +204,19 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
 }
 
 // A walk over one [tokens, channels] tensor: a warp copies 8 rows at a time and
-// moves on.  VEC: rows are 16-byte aligned, 16 bytes a copy, zeros behind the
-// last channel; else a channel pair a row, element by element, zeros likewise.
+// moves on by multiples of 8, so a row's place in its first 4-byte word depends
+// on its place among the 8 only.  VEC: 16 bytes a copy, zeros behind the last
+// channel.
 template <class I, bool VEC>
 struct Walk {
-  static constexpr int kEs = static_cast<int>(sizeof(I));
-  static constexpr int kPer = VEC ? Rows<I>::kRow / 16 : 1;  // copies a row
-  static constexpr int kRows = VEC ? 32 / kPer : 1;          // rows a copy of the warp
+  static constexpr int kEs = static_cast<int>(sizeof(I)), kRow = Rows<I, VEC>::kRow;
+  static constexpr int kPer = VEC ? kRow / 16 : 1;   // copies a row
+  static constexpr int kRows = VEC ? 32 / kPer : 1;  // rows a copy of the warp
   static_assert(kSeg % kRows == 0, "a copy of the warp holds whole rows of a run");
-  const char *p;      // the first row's first channel of the warp, the same in every lane
-  uint32_t row;       // bytes between rows
-  uint32_t at;        // this lane's part of a copy, behind p
-  int row0, bytes;    // VEC: its row of a copy and its bytes; else the warp's (4-byte I) or its channels
+  const char *p;    // the first row's first channel of the warp, the same in every lane
+  uint32_t row;     // bytes between rows
+  uint32_t at;      // VEC: this lane's part of a copy, behind p
+  int row0, bytes;  // VEC: its row of a copy and its bytes; else the warp's channels
 
   // `chan` channels exist
   __device__ __forceinline__ Walk(const I *first, int64_t ld, int chan, int lane) {
@@ -226,9 +228,12 @@ struct Walk {
       row0 = lane / kPer;
       at = row0 * row + (bytes > 0 ? 16 * (lane % kPer) : 0);
     } else {
-      row0 = 0, bytes = kEs == 4 ? chan : min(2, max(0, chan - 2 * lane));
-      at = bytes > 0 ? 2 * lane * kEs : 0;
+      row0 = 0, at = 0, bytes = chan;
     }
+  }
+  // how far behind a 4-byte boundary row i begins
+  __device__ __forceinline__ uint32_t offset(int i) const {
+    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) + i * row) & 3u;
   }
   // start copying rows [0, n)
   __device__ __forceinline__ void copy(unsigned char *dst, int n, int lane) const {
@@ -242,39 +247,48 @@ struct Walk {
         for (int k = 0; k < kSeg / kRows; ++k)
           if (row0 + k * kRows < n) cp16(d + k * 512, p + (at + k * kRows * row), bytes);
       }
-    } else if constexpr (kEs == 4) {
-      float *d = reinterpret_cast<float *>(dst) + lane;
-      for (int i = 0; i < n; ++i, d += kChan) {
-        const float *q = reinterpret_cast<const float *>(p + i * row) + lane;
-        if (lane < bytes) cp_async<4>(d, q);
-        else d[0] = 0.f;
-        if (lane + 32 < bytes) cp_async<4>(d + 32, q + 32);
-        else d[32] = 0.f;
-      }
     } else {
-      using W = typename std::conditional<kEs == 2, uint32_t, uint16_t>::type;  // a pair
-      using H = typename std::conditional<kEs == 2, uint16_t, uint8_t>::type;
-      W v[kSeg];
+      // the words of each row, whole ones of the allocation at either end
+      constexpr int kWords = kRow / 4;
 #pragma unroll
       for (int i = 0; i < kSeg; ++i) {
-        const H *q = reinterpret_cast<const H *>(p + (at + i * row));
-        const uint32_t lo = i < n && bytes > 0 ? q[0] : 0, hi = i < n && bytes > 1 ? q[1] : 0;
-        v[i] = static_cast<W>(lo | hi << (8 * kEs));
-      }
+        if (i < n) {
+          const uint32_t o = offset(i);
+          const char *q = p + i * row - o;
+          const int words = (o + bytes * kEs + 3) / 4;
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i) reinterpret_cast<W *>(dst)[i * (kChan / 2) + lane] = v[i];
+          for (int w = 0; w < kWords; w += 32)
+            if (w + lane < words) cp_async<4>(dst + i * kRow + 4 * (w + lane), q + 4 * (w + lane));
+        }
+      }
     }
   }
   __device__ __forceinline__ void move(int rows) { p += static_cast<int64_t>(rows) * row; }
-};
 
-__device__ __forceinline__ float2 row_pair(const unsigned char *rows, int i, int lane, const float *) {
-  return *reinterpret_cast<const float2 *>(rows + i * Rows<float>::kRow + lane * 8);
-}
-__device__ __forceinline__ float2 row_pair(const unsigned char *rows, int i, int lane, const uint16_t *) {
-  const uint32_t u = *reinterpret_cast<const uint32_t *>(rows + i * Rows<uint16_t>::kRow + lane * 4);
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
+  // the lane's channel pair of row i: its bits (16- and 8-bit I); zeros where channels do not exist
+  __device__ __forceinline__ uint32_t bits(const unsigned char *rows, int i, int lane) const {
+    if constexpr (VEC) {
+      if constexpr (kEs == 2) return *reinterpret_cast<const uint32_t *>(rows + i * kRow + lane * 4);
+      else return *reinterpret_cast<const uint16_t *>(rows + i * kRow + lane * 2);
+    } else {
+      const uint32_t o = offset(i) + 2 * kEs * lane;
+      const uint32_t *w = reinterpret_cast<const uint32_t *>(rows + i * kRow) + o / 4;
+      const uint32_t v = __funnelshift_r(w[0], w[1], 8 * (o & 3u));
+      return 2 * lane >= bytes ? 0u : 2 * lane + 1 >= bytes ? v & ((1u << (8 * kEs)) - 1u) : v;
+    }
+  }
+  // the pair's values (activations)
+  __device__ __forceinline__ float2 pair(const unsigned char *rows, int i, int lane) const {
+    if constexpr (kEs == 4) {
+      const float2 v = *reinterpret_cast<const float2 *>(rows + i * kRow + lane * 8);
+      if constexpr (VEC) return v;
+      else return make_float2(2 * lane < bytes ? v.x : 0.f, 2 * lane + 1 < bytes ? v.y : 0.f);
+    } else {
+      const uint32_t u = bits(rows, i, lane);
+      return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+  }
+};
 
 // ---- the composition of runs ----
 // A run maps v to P v + H; `cut`: it does not depend on v at all (a reset), not
@@ -443,7 +457,7 @@ __device__ __forceinline__ void put_codes(const GlrArgs &a, unsigned char *q, co
   uint32_t byte = lane < 24 ? bytes[lane] : 0;
   for (uint32_t bad = __ballot_sync(kFull, lane < 24 && i < n && byte > ckpt8::kLast); bad; bad &= bad - 1) {
     const int j = __ffs(bad) - 1;
-    *reinterpret_cast<uint16_t *>(q + (j >> 3) * Rows<E>::kBytes + (j & 7) * Rows<E>::kRow + 2 * lane) = 0;
+    *reinterpret_cast<uint16_t *>(q + (j >> 3) * Rows<E, VEC>::kBytes + (j & 7) * Rows<E, VEC>::kRow + 2 * lane) = 0;
     if (lane == j) byte = 255;
     __syncwarp();
   }
@@ -454,13 +468,13 @@ __device__ __forceinline__ void put_codes(const GlrArgs &a, unsigned char *q, co
 #pragma unroll
       for (int p = 0; p < 3; ++p)
         *reinterpret_cast<int4 *>(a.codes + (p * rows + row + j) * a.D + c0 + at) =
-            *reinterpret_cast<const int4 *>(q + p * Rows<E>::kBytes + j * Rows<E>::kRow + at);
+            *reinterpret_cast<const int4 *>(q + p * Rows<E, VEC>::kBytes + j * Rows<E, VEC>::kRow + at);
     }
   } else {
     for (int p = 0; p < 3; ++p)
       for (int j = 0; j < n; ++j) {
         int8_t *o = a.codes + (p * rows + row + j) * a.D + c0;
-        const unsigned char *s = q + p * Rows<E>::kBytes + j * Rows<E>::kRow;
+        const unsigned char *s = q + p * Rows<E, VEC>::kBytes + j * Rows<E, VEC>::kRow;
         if (2 * lane < chan) o[2 * lane] = static_cast<int8_t>(s[2 * lane]);
         if (2 * lane + 1 < chan) o[2 * lane + 1] = static_cast<int8_t>(s[2 * lane + 1]);
       }
@@ -473,7 +487,7 @@ template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
-  constexpr int kBytes = Rows<E>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg, kOut = K8 ? 32 : 0;
+  constexpr int kBytes = Rows<E, VEC>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg, kOut = K8 ? 32 : 0;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   unsigned char *mine = smem + sizeof(Runs) + warp * (kHalves * kHalf + kOut);
   const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
@@ -524,9 +538,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
       unsigned char *d = mine + half * kHalf;
 #pragma unroll
       for (int i = 0; i < kSeg; ++i) {
-        const float2 x = row_pair(d, i, lane, static_cast<const E *>(nullptr));
-        const float2 r = row_pair(d + kBytes, i, lane, static_cast<const E *>(nullptr));
-        const float2 g = row_pair(d + 2 * kBytes, i, lane, static_cast<const E *>(nullptr));
+        const float2 x = wx.pair(d, i, lane), r = wr.pair(d + kBytes, i, lane), g = wg.pair(d + 2 * kBytes, i, lane);
         const Decay q = decay(mul2(rate, sigmoid2(r)));
         f[kSeg * half + i] = q.a;
         u[kSeg * half + i] = input_term(q.m2, g, x);
@@ -538,7 +550,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
             const uint32_t big = __reduce_max_sync(kFull, max_magnitude(in[k]));
             const uint32_t step8 = ckpt8::step_bits(big);
             const float2 code = fma2(in[k], dup(__uint_as_float((254u << 23) - step8)), dup(12582912.f));
-            *reinterpret_cast<uint16_t *>(d + k * kBytes + i * Rows<E>::kRow + 2 * lane) =
+            *reinterpret_cast<uint16_t *>(d + k * kBytes + i * Rows<E, VEC>::kRow + 2 * lane) =
                 static_cast<uint16_t>(__byte_perm(__float_as_uint(code.x), __float_as_uint(code.y), 0x0040));
             if (lane == 0) mine[kHalves * kHalf + 8 * k + i] = static_cast<unsigned char>(step8 >> 23);
             top = kSeg * half + i < n ? max(top, big) : top;
@@ -672,7 +684,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
   using I = typename std::conditional<K8, int8_t, E>::type;  // what x, r and g are held in
-  constexpr int kBytes = Rows<I>::kBytes, kStage = 3 * kBytes + Rows<E>::kBytes, kOut = K8 ? 24 * sizeof(float) : 0;
+  constexpr int kBytes = Rows<I, VEC>::kBytes, kStage = 3 * kBytes + Rows<E, VEC>::kBytes, kOut = K8 ? 24 * sizeof(float) : 0;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   unsigned char *mine = smem + sizeof(Runs) + warp * (kStage + kOut);
   const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
@@ -748,21 +760,20 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
     cp_async_wait<1>();
     __syncwarp();
     const unsigned char *d = mine;
-    auto input = [&](int k, int i) {
+    auto input = [&](const Walk<I, VEC> &w, int k, int i) {
       if constexpr (K8) {
-        return ckpt8::decode2(*reinterpret_cast<const uint16_t *>(d + k * kBytes + i * kChan + 2 * lane),
-                              reinterpret_cast<const float *>(mine + kStage)[8 * k + i]);
+        return ckpt8::decode2(w.bits(d + k * kBytes, i, lane), reinterpret_cast<const float *>(mine + kStage)[8 * k + i]);
       } else {
-        return row_pair(d + k * kBytes, i, lane, static_cast<const E *>(nullptr));
+        return w.pair(d + k * kBytes, i, lane);
       }
     };
     // per token: the decay; what dh is multiplied by in dx and dg; and -sr a
     // (h_{t-1} - (a / m) sg x), by which it is in drate (dr: that times rate (1 - sr))
     float2 f[kSeg], cx[kSeg], cg[kSeg], cr[kSeg], ck[kSeg];
-    auto dy = [&](int i) { return row_pair(d + 3 * kBytes, i, lane, static_cast<const E *>(nullptr)); };
+    auto dy = [&](int i) { return wy.pair(d + 3 * kBytes, i, lane); };
 #pragma unroll
     for (int i = 0; i < kSeg; ++i) {
-      const float2 x = input(0, i), sr = sigmoid2(input(1, i)), sg = sigmoid2(input(2, i));
+      const float2 x = input(wx, 0, i), sr = sigmoid2(input(wr, 1, i)), sg = sigmoid2(input(wg, 2, i));
       const Decay q = decay(mul2(rate, sr));
       f[i] = q.a;
       const float2 m2 = q.m2;
@@ -873,13 +884,14 @@ int check_words(const char *fn, std::initializer_list<const void *> ps) {
 }
 
 // Shared memory of a CTA: the runs and, for each warp, its rows.
-size_t forward_smem(int dtype, bool keep8) {
-  const size_t rows = dtype == SDM_DTYPE_F32 ? Rows<float>::kBytes : Rows<uint16_t>::kBytes;
-  return sizeof(Runs) + kWarps * (kForwardRun / kSeg * 3 * rows + (keep8 ? 32 : 0));
+template <class E, bool VEC>
+constexpr size_t forward_smem(bool keep8) {
+  return sizeof(Runs) + kWarps * (kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes + (keep8 ? 32 : 0));
 }
-size_t backward_smem(int dtype, bool keep8) {
-  const size_t rows = dtype == SDM_DTYPE_F32 ? Rows<float>::kBytes : Rows<uint16_t>::kBytes;
-  return sizeof(Runs) + kWarps * (3 * (keep8 ? Rows<int8_t>::kBytes : rows) + rows + (keep8 ? 24 * sizeof(float) : 0));
+template <class E, bool VEC>
+constexpr size_t backward_smem(bool keep8) {
+  return sizeof(Runs) + kWarps * (3 * (keep8 ? Rows<int8_t, VEC>::kBytes : Rows<E, VEC>::kBytes) + Rows<E, VEC>::kBytes +
+                                  (keep8 ? 24 * sizeof(float) : 0));
 }
 
 // CTAs of a cluster.  A walk takes its steps once while the whole grid runs at
@@ -906,10 +918,12 @@ int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
   return best;
 }
 int forward_cluster(int B, int T, int D, int dtype) {
-  return cluster_size(B, T, D, kForwardRun, kForwardRegs, forward_smem(dtype, false));
+  return cluster_size(B, T, D, kForwardRun, kForwardRegs,
+                      dtype == SDM_DTYPE_F32 ? forward_smem<float, true>(false) : forward_smem<uint16_t, true>(false));
 }
 int backward_cluster(int B, int T, int D, int dtype) {
-  return cluster_size(B, T, D, kBackwardRun, kBackwardRegs, backward_smem(dtype, false));
+  return cluster_size(B, T, D, kBackwardRun, kBackwardRegs,
+                      dtype == SDM_DTYPE_F32 ? backward_smem<float, true>(false) : backward_smem<uint16_t, true>(false));
 }
 
 // 16-byte copies of rows, pairwise stores
@@ -955,7 +969,7 @@ int launch_step(const char *fn, const GlrArgs &a, cudaStream_t st) {
 
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = forward_smem(sizeof(E) == 4 ? SDM_DTYPE_F32 : SDM_DTYPE_BF16, a.codes);
+  const size_t smem = forward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
@@ -964,7 +978,7 @@ int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
 }
 template <class E, bool VEC>
 int launch_backward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = backward_smem(sizeof(E) == 4 ? SDM_DTYPE_F32 : SDM_DTYPE_BF16, a.codes);
+  const size_t smem = backward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_backward_kernel<E, VEC, false, true>, smem, a, st);
