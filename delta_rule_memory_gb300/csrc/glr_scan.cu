@@ -302,12 +302,15 @@ __device__ __forceinline__ float2 apply(const Run &q, float2 v) {
   return CUTS && q.cut ? q.H : fma2(q.P, v, q.H);
 }
 
+// in front of a CTA's shared memory; behind it, in a cluster, the CTAs' runs
 struct Runs {
   float4 warp[2][kWarps][32];
-  float4 cta[2][kMaxCluster][32];
   uint32_t warp_cut[2][kWarps], cta_cut[2][kMaxCluster];
-  uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in cta[half]
+  uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in cta(half, .)
+
+  __device__ __forceinline__ float4 *cta(int half, int j) { return reinterpret_cast<float4 *>(this + 1) + (2 * j + half) * 32; }
 };
+__host__ __device__ constexpr uint32_t runs_bytes(int cs) { return sizeof(Runs) + (cs > 1 ? cs * 1024u : 0u); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
@@ -375,7 +378,7 @@ __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &
     return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.warp_cut[half][j] != 0};
   };
   auto cta_run = [&](int j) {
-    const float4 q = s.cta[half][j][lane];
+    const float4 q = s.cta(half, j)[lane];
     return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.cta_cut[half][j] != 0};
   };
   if (cs == 1) {
@@ -399,7 +402,7 @@ __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &
     const float2 P = mul2(before.P, mine.P), H = apply<CUTS>(mine, before.H);
     for (int i = 0; i < cs; ++i) {
       const uint32_t mbar = in_cta(&s.full[half], i);
-      send(in_cta(&s.cta[half][at.rank][lane], i), make_float4(P.x, P.y, H.x, H.y), mbar);
+      send(in_cta(s.cta(half, at.rank) + lane, i), make_float4(P.x, P.y, H.x, H.y), mbar);
       if (CUTS && lane == 0) send(in_cta(&s.cta_cut[half][at.rank], i), before.cut || mine.cut ? 1u : 0u, mbar);
     }
   }
@@ -489,8 +492,9 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   Runs &runs = *reinterpret_cast<Runs *>(smem);
   constexpr int kBytes = Rows<E, VEC>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg, kOut = K8 ? 32 : 0;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-  unsigned char *mine = smem + sizeof(Runs) + warp * (kHalves * kHalf + kOut);
-  const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
+  const int cs = a.cs;
+  unsigned char *mine = smem + runs_bytes(cs) + warp * (kHalves * kHalf + kOut);
+  const int rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
   Place at{warp, lane, rank, cs, a.drop && rank == cs - 1, false};
@@ -686,8 +690,9 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
   using I = typename std::conditional<K8, int8_t, E>::type;  // what x, r and g are held in
   constexpr int kBytes = Rows<I, VEC>::kBytes, kStage = 3 * kBytes + Rows<E, VEC>::kBytes, kOut = K8 ? 24 * sizeof(float) : 0;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-  unsigned char *mine = smem + sizeof(Runs) + warp * (kStage + kOut);
-  const int cs = a.cs, rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
+  const int cs = a.cs;
+  unsigned char *mine = smem + runs_bytes(cs) + warp * (kStage + kOut);
+  const int rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
   Place at{kWarps - 1 - warp, lane, cs - 1 - rank, cs, a.drop && rank == 0, false};
@@ -791,34 +796,38 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
     cp_async_wait<0>();
     __syncwarp();  // dy is here, and the next inputs go where these were read
     fetch(count(t0 - tokens));
+    // dh_i = dy_i + f dd with f and dd those of token i + 1
     Run q{dup(1.f), dup(0.f), CUTS && cut != 0};
+    float2 ff = dup(0.f), dd = dup(0.f);
     if (n == kSeg && !(CUTS && cut)) {
 #pragma unroll
-      for (int i = kSeg - 1; i >= 0; --i) q.P = mul2(q.P, f[i]), q.H = mul2(f[i], add2(dy(i), q.H));
+      for (int i = kSeg - 1; i >= 0; --i) q.P = mul2(q.P, f[i]), dd = fma2(ff, dd, dy(i)), ff = f[i];
     } else {
 #pragma unroll
       for (int i = kSeg - 1; i >= 0; --i)
         if (i < n) {
           q.P = mul2(q.P, f[i]);
-          q.H = CUTS && cut >> i & 1 ? dup(0.f) : mul2(f[i], add2(dy(i), q.H));
+          dd = fma2(ff, dd, dy(i)), ff = f[i];
+          if (CUTS && cut >> i & 1) ff = dup(0.f), dd = dup(0.f);
         }
     }
-    float2 e = compose<CUTS>(runs, step, at, q, v);
+    q.H = mul2(ff, dd);
+    dd = compose<CUTS>(runs, step, at, q, v), ff = dup(1.f);
     if (n > 0) {
 E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
 #pragma unroll
       for (int i = kSeg - 1; i >= 0; --i, o -= out_row) {
         if (i < n) {
-          const float2 dh = add2(dy(i), e);
-          const float2 w = mul2(dh, cr[i]);
-          drate = add2(drate, w);
+          const float2 dh = fma2(ff, dd, dy(i)), w = mul2(dh, cr[i]);
+          drate = fma2(dh, cr[i], drate);
           if (one) {
             store2<VEC>(dx, o, mul2(dh, cx[i]), two);
             store2<VEC>(dr, o, mul2(w, ck[i]), two);
             store2<VEC>(dg, o, mul2(dh, cg[i]), two);
           }
-          e = CUTS && cut >> i & 1 ? dup(0.f) : mul2(f[i], dh);
+          ff = f[i], dd = dh;
+          if (CUTS && cut >> i & 1) ff = dup(0.f), dd = dup(0.f);
         }
       }
     }
@@ -831,7 +840,7 @@ E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = 
     if (two) a.state_out[sc + 1] = v.y;
   }
   // drate over the CTA's warps, in their order
-  float2 *sum = reinterpret_cast<float2 *>(smem + sizeof(Runs));
+  float2 *sum = reinterpret_cast<float2 *>(smem + runs_bytes(cs));
   cp_async_wait<0>();
   __syncthreads();
   sum[warp * 32 + lane] = drate;
@@ -883,14 +892,14 @@ int check_words(const char *fn, std::initializer_list<const void *> ps) {
   return SDM_OK;
 }
 
-// Shared memory of a CTA: the runs and, for each warp, its rows.
+// Shared memory of a CTA's warps for their rows (the runs come on top).
 template <class E, bool VEC>
 constexpr size_t forward_smem(bool keep8) {
-  return sizeof(Runs) + kWarps * (kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes + (keep8 ? 32 : 0));
+  return kWarps * (kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes + (keep8 ? 32 : 0));
 }
 template <class E, bool VEC>
 constexpr size_t backward_smem(bool keep8) {
-  return sizeof(Runs) + kWarps * (3 * (keep8 ? Rows<int8_t, VEC>::kBytes : Rows<E, VEC>::kBytes) + Rows<E, VEC>::kBytes +
+  return kWarps * (3 * (keep8 ? Rows<int8_t, VEC>::kBytes : Rows<E, VEC>::kBytes) + Rows<E, VEC>::kBytes +
                                   (keep8 ? 24 * sizeof(float) : 0));
 }
 
@@ -902,14 +911,15 @@ constexpr size_t backward_smem(bool keep8) {
 // waves), 115 with 4, 127 with 5; 1 x 32768 x 3840: 250 with 8, 229 with 9.
 int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
   const int64_t columns = static_cast<int64_t>(B) * ((D + kChan - 1) / kChan);
-  const int per_sm = min(65536 / (32 * regs) / kWarps, static_cast<int>((227 << 10) / (smem + 1024)));
   const int tile = run * kWarps;
   int best = 1;
   double least = 1e300;
   for (int cs = 1; cs <= kMaxCluster; ++cs) {
     if (cs > 1 && (cs - 1) * tile >= T) break;
+    const int per_sm = min(65536 / (32 * regs) / kWarps, static_cast<int>((227 << 10) / (runs_bytes(cs) + smem + 1024)));
     const int64_t room = (cs > 2 ? kSMs - 4 : kSMs) * per_sm, ctas = columns * cs;
-    if (cs > 8 && ctas > room) break;  // large clusters pay only where they fill the GPU
+    // large clusters pay only where the walk is long and they fill the GPU
+    if (cs > 8 && (ctas > room || T <= 16 * 8 * tile)) break;
     const int64_t waves = (ctas + room - 1) / room, steps = (T + tile * cs - 1) / (tile * cs);
     const double share = static_cast<double>(ctas) / room;
     const double time = steps * ((share < 1 ? 1 : share) + waves) / 2;
@@ -969,7 +979,7 @@ int launch_step(const char *fn, const GlrArgs &a, cudaStream_t st) {
 
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = forward_smem<E, VEC>(a.codes != nullptr);
+  const size_t smem = runs_bytes(a.cs) + forward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
@@ -978,7 +988,7 @@ int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
 }
 template <class E, bool VEC>
 int launch_backward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = backward_smem<E, VEC>(a.codes != nullptr);
+  const size_t smem = runs_bytes(a.cs) + backward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_backward_kernel<E, VEC, false, true>, smem, a, st);
