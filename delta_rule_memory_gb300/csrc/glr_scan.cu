@@ -302,15 +302,13 @@ __device__ __forceinline__ float2 apply(const Run &q, float2 v) {
   return CUTS && q.cut ? q.H : fma2(q.P, v, q.H);
 }
 
-// in front of a CTA's shared memory; behind it, in a cluster, the CTAs' runs
+// In front of a CTA's shared memory; then the warps' rows; then, in a cluster, the CTAs' runs.
 struct Runs {
   float4 warp[2][kWarps][32];
   uint32_t warp_cut[2][kWarps], cta_cut[2][kMaxCluster];
-  uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in cta(half, .)
-
-  __device__ __forceinline__ float4 *cta(int half, int j) { return reinterpret_cast<float4 *>(this + 1) + (2 * j + half) * 32; }
+  uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in its half of the CTAs' runs
 };
-__host__ __device__ constexpr uint32_t runs_bytes(int cs) { return sizeof(Runs) + (cs > 1 ? cs * 1024u : 0u); }
+__host__ __device__ constexpr uint32_t cluster_bytes(int cs) { return cs > 1 ? cs * 1024u : 0u; }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
@@ -366,9 +364,11 @@ struct Place {
 // thread's last: an mbarrier whose phase is still open takes no second arrival
 // (that faults), so nothing is armed, sent or waited for any more, and the walk
 // ends on whatever the buffers hold.  CUTS: runs may be cut.
-template <bool CUTS>
+// kAt: where the CTAs' runs lie behind s.
+template <bool CUTS, int kAt>
 __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &mine, float2 &v) {
   const int half = k & 1, lane = at.lane, cs = at.cs;
+  auto slot = [&](int j) { return reinterpret_cast<float4 *>(reinterpret_cast<char *>(&s) + kAt) + (2 * j + half) * 32 + lane; };
   s.warp[half][at.warp][lane] = make_float4(mine.P.x, mine.P.y, mine.H.x, mine.H.y);
   if (CUTS && lane == 0) s.warp_cut[half][at.warp] = mine.cut;
   if (cs > 1 && threadIdx.x == 0 && !at.lost) umma::mbar_expect_tx(smem_u32(&s.full[half]), cs * (CUTS ? 516 : 512));
@@ -378,7 +378,7 @@ __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &
     return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.warp_cut[half][j] != 0};
   };
   auto cta_run = [&](int j) {
-    const float4 q = s.cta(half, j)[lane];
+    const float4 q = *slot(j);
     return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.cta_cut[half][j] != 0};
   };
   if (cs == 1) {
@@ -402,7 +402,7 @@ __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &
     const float2 P = mul2(before.P, mine.P), H = apply<CUTS>(mine, before.H);
     for (int i = 0; i < cs; ++i) {
       const uint32_t mbar = in_cta(&s.full[half], i);
-      send(in_cta(s.cta(half, at.rank) + lane, i), make_float4(P.x, P.y, H.x, H.y), mbar);
+      send(in_cta(slot(at.rank), i), make_float4(P.x, P.y, H.x, H.y), mbar);
       if (CUTS && lane == 0) send(in_cta(&s.cta_cut[half][at.rank], i), before.cut || mine.cut ? 1u : 0u, mbar);
     }
   }
@@ -493,7 +493,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   constexpr int kBytes = Rows<E, VEC>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg, kOut = K8 ? 32 : 0;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int cs = a.cs;
-  unsigned char *mine = smem + runs_bytes(cs) + warp * (kHalves * kHalf + kOut);
+  unsigned char *mine = smem + sizeof(Runs) + warp * (kHalves * kHalf + kOut);
   const int rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
@@ -581,7 +581,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
 #pragma unroll
       for (int i = 1; i < kForwardRun; ++i) q.P = mul2(q.P, f[i]), q.H = fma2(f[i], q.H, u[i]);
     }
-    float2 h = compose<CUTS>(runs, step, at, q, v);
+    float2 h = compose<CUTS, sizeof(Runs) + kWarps * (kHalves * kHalf + kOut)>(runs, step, at, q, v);
     if (n > 0 && one) {
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E));
 #pragma unroll
@@ -691,7 +691,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
   constexpr int kBytes = Rows<I, VEC>::kBytes, kStage = 3 * kBytes + Rows<E, VEC>::kBytes, kOut = K8 ? 24 * sizeof(float) : 0;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int cs = a.cs;
-  unsigned char *mine = smem + runs_bytes(cs) + warp * (kStage + kOut);
+  unsigned char *mine = smem + sizeof(Runs) + warp * (kStage + kOut);
   const int rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
@@ -812,7 +812,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
         }
     }
     q.H = mul2(ff, dd);
-    dd = compose<CUTS>(runs, step, at, q, v), ff = dup(1.f);
+    dd = compose<CUTS, sizeof(Runs) + kWarps * (kStage + kOut)>(runs, step, at, q, v), ff = dup(1.f);
     if (n > 0) {
 E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
@@ -840,7 +840,7 @@ E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = 
     if (two) a.state_out[sc + 1] = v.y;
   }
   // drate over the CTA's warps, in their order
-  float2 *sum = reinterpret_cast<float2 *>(smem + runs_bytes(cs));
+  float2 *sum = reinterpret_cast<float2 *>(smem + sizeof(Runs));
   cp_async_wait<0>();
   __syncthreads();
   sum[warp * 32 + lane] = drate;
@@ -892,14 +892,14 @@ int check_words(const char *fn, std::initializer_list<const void *> ps) {
   return SDM_OK;
 }
 
-// Shared memory of a CTA's warps for their rows (the runs come on top).
+// Shared memory of a CTA without its cluster's runs.
 template <class E, bool VEC>
 constexpr size_t forward_smem(bool keep8) {
-  return kWarps * (kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes + (keep8 ? 32 : 0));
+  return sizeof(Runs) + kWarps * (kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes + (keep8 ? 32 : 0));
 }
 template <class E, bool VEC>
 constexpr size_t backward_smem(bool keep8) {
-  return kWarps * (3 * (keep8 ? Rows<int8_t, VEC>::kBytes : Rows<E, VEC>::kBytes) + Rows<E, VEC>::kBytes +
+  return sizeof(Runs) + kWarps * (3 * (keep8 ? Rows<int8_t, VEC>::kBytes : Rows<E, VEC>::kBytes) + Rows<E, VEC>::kBytes +
                                   (keep8 ? 24 * sizeof(float) : 0));
 }
 
@@ -916,7 +916,7 @@ int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
   double least = 1e300;
   for (int cs = 1; cs <= kMaxCluster; ++cs) {
     if (cs > 1 && (cs - 1) * tile >= T) break;
-    const int per_sm = min(65536 / (32 * regs) / kWarps, static_cast<int>((227 << 10) / (runs_bytes(cs) + smem + 1024)));
+    const int per_sm = min(65536 / (32 * regs) / kWarps, static_cast<int>((227 << 10) / (cluster_bytes(cs) + smem + 1024)));
     const int64_t room = (cs > 2 ? kSMs - 4 : kSMs) * per_sm, ctas = columns * cs;
     // large clusters pay only where the walk is long and they fill the GPU
     if (cs > 8 && (ctas > room || T <= 16 * 8 * tile)) break;
@@ -979,7 +979,7 @@ int launch_step(const char *fn, const GlrArgs &a, cudaStream_t st) {
 
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = runs_bytes(a.cs) + forward_smem<E, VEC>(a.codes != nullptr);
+  const size_t smem = cluster_bytes(a.cs) + forward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
@@ -988,7 +988,7 @@ int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
 }
 template <class E, bool VEC>
 int launch_backward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = runs_bytes(a.cs) + backward_smem<E, VEC>(a.codes != nullptr);
+  const size_t smem = cluster_bytes(a.cs) + backward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_backward_kernel<E, VEC, false, true>, smem, a, st);
