@@ -92,6 +92,8 @@ class SdmError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libsdm.so.  Raises if it was not built: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):
@@ -585,6 +587,12 @@ def _on(device: torch.device, stream):
     return _there(device, stream)
 
 
+def _plain(t, dtype, shape, device) -> bool:
+    """A contiguous tensor of this type, shape and device: nothing more to check."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+            and t.is_contiguous())
+
+
 def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
     """Check an activation [..., rows, D] whose channels are contiguous and
     whose rows lie at one distance (a column slice of a wider contiguous
@@ -615,49 +623,50 @@ def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
 
 
 def _glr_checks(state, x, r, g, rate, reset, lens, like=None):
-    """Common checks of the glr_scan calls; returns B, T, D, the dtype and the
-    row distances of x, r and g (`like`: [B,T,D] tensor in their place)."""
+    """Common checks of the glr_scan calls; returns the shape [B,T,D], the
+    dtype, the device, the row distances of x, r and g, and reset as uint8
+    (`like`: a tensor of that shape in place of x, r and g)."""
     first = x if like is None else like
     _act(first, "x" if like is None else "dy")
     if first.dim() != 3:
         raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
-    B, T, D = shape = first.shape
-    dt, dev = first.dtype, first.device
+    shape, dt, dev = first.shape, first.dtype, first.device
+    B, T, D = shape
     lds = (0, 0, 0)
     if x is not None or like is None:
-        lds = _act(x, "x", dt, shape, dev), _act(r, "r", dt, shape, dev), _act(g, "g", dt, shape, dev)
-    _req(state, "state" if like is None else "dstate", torch.float32, (B, D))
-    _req(rate, "rate", torch.float32, (D,))
+        lds = tuple([D if _plain(t, dt, shape, dev) else _act(t, n, dt, shape, dev)
+                     for t, n in ((x, "x"), (r, "r"), (g, "g"))])
+    if not _plain(state, torch.float32, (B, D), dev):
+        _out_check(state, "state" if like is None else "dstate", torch.float32, (B, D), dev)
+    if not _plain(rate, torch.float32, (D,), dev):
+        _out_check(rate, "rate", torch.float32, (D,), dev)
     if reset is not None:
         if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
             reset = reset.view(torch.uint8)
-        _req(reset, "reset", torch.uint8, (B, T))
+        _out_check(reset, "reset", torch.uint8, (B, T), dev)
     if lens is not None:
-        _req(lens, "lens", torch.int32, (B,))
-    if state.device != dev or rate.device != dev or reset is not None or lens is not None:
-        _same_device(dev, state=state, rate=rate, reset=reset, lens=lens)
-    return B, T, D, dt, lds
+        _out_check(lens, "lens", torch.int32, (B,), dev)
+    return shape, dt, dev, lds, reset
 
 
-def _same_device(device, **tensors):
-    for n, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{n} must be on {device}, got {t.device}")
-
-
-def _err_word(dev_err, device):
-    if dev_err is not None:
-        _out(dev_err, "dev_err", torch.int32, None, device)
+def _out_check(t, name: str, dtype, shape, device):
+    _req(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _out(t, name: str, dtype, shape, device):
     """An output the caller gave, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _req(t, name, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not _plain(t, dtype, shape, device):
+        _out_check(t, name, dtype, shape, device)
     return t
+
+
+def _err_word(dev_err, device):
+    if dev_err is not None:
+        _out_check(dev_err, "dev_err", torch.int32, None, device)
 
 
 def glr_scan(state, x, r, g, rate, reset=None, lens=None, y=None, state_out=None, dev_err=None, stream=None):
@@ -669,11 +678,11 @@ def glr_scan(state, x, r, g, rate, reset=None, lens=None, y=None, state_out=None
     exist.  Updates `state` fp32 [B,D] in place, or leaves it and writes
     `state_out` where that is given.  Returns y [B,T,D] of x's dtype (rows
     behind lens are not written).  T = 1 is the step of a decoding loop."""
-    B, T, D, dt, lds = _glr_checks(state, x, r, g, rate, reset, lens)
-    dev = x.device
+    shape, dt, dev, lds, reset = _glr_checks(state, x, r, g, rate, reset, lens)
+    B, T, D = shape
     _err_word(dev_err, dev)
     with _on(dev, stream) as st:
-        y = _out(y, "y", dt, (B, T, D), dev)
+        y = _out(y, "y", dt, shape, dev)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
         rc = lib().glr_scan(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lds[0], r.data_ptr(), lds[1],
                             g.data_ptr(), lds[2], _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
@@ -693,11 +702,11 @@ def glr_scan_train(state, x, r, g, rate, reset=None, lens=None, keep8=False, y=N
     keep8 (or ckpt, a pair of buffers) (y, carry, (codes, exps)), the 8-bit
     checkpoints of x, r and g, int8 [3,B,T,D] and uint8 [3,B,T,ceil(D/64)],
     which the backward takes in place of x, r and g."""
-    B, T, D, dt, lds = _glr_checks(state, x, r, g, rate, reset, lens)
-    dev = x.device
+    shape, dt, dev, lds, reset = _glr_checks(state, x, r, g, rate, reset, lens)
+    B, T, D = shape
     _err_word(dev_err, dev)
     with _on(dev, stream) as st:
-        y = _out(y, "y", dt, (B, T, D), dev)
+        y = _out(y, "y", dt, shape, dev)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
         carry = _out(carry, "carry", torch.float32, (B, -(-T // 8), D), dev)
         codes = exps = None
@@ -727,24 +736,23 @@ def glr_scan_backward(dstate, x, r, g, rate, carry, dy, reset=None, lens=None, c
         raise ValueError("give x, r and g or ckpt, not both")
     if ckpt is None and x is None:
         raise ValueError("x, r and g, or ckpt, are needed")
-    B, T, D, dt, lds = _glr_checks(dstate, x, r, g, rate, reset, lens, like=dy)
-    dev = dy.device
+    shape, dt, dev, lds, reset = _glr_checks(dstate, x, r, g, rate, reset, lens, like=dy)
+    B, T, D = shape
     if not dy.is_contiguous():
         raise ValueError("dy must be contiguous")
-    _req(carry, "carry", torch.float32, (B, -(-T // 8), D))
-    _same_device(dev, carry=carry)
+    _out_check(carry, "carry", torch.float32, (B, -(-T // 8), D), dev)
     codes = exps = None
     if ckpt is not None:
         codes, exps = ckpt
-        _req(codes, "codes", torch.int8, (3, B, T, D))
-        _req(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)))
-        _same_device(dev, codes=codes, exps=exps)
+        _out_check(codes, "codes", torch.int8, (3, B, T, D), dev)
+        _out_check(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)), dev)
     _err_word(dev_err, dev)
     with _on(dev, stream) as st:
         if grads is None:
-            grads = tuple(torch.empty((B, T, D), dtype=dt, device=dev) for _ in range(3))
-        ld = {_act(t, n, dt, (B, T, D), dev) for t, n in zip(grads, ("dx", "dr", "dg"))}
-        if len(ld) != 1:
+            grads = tuple([torch.empty(shape, dtype=dt, device=dev) for _ in range(3)])
+        ld, *more = [D if _plain(t, dt, shape, dev) else _act(t, n, dt, shape, dev)
+                     for t, n in zip(grads, ("dx", "dr", "dg"), strict=True)]
+        if any(d != ld for d in more):
             raise ValueError("dx, dr and dg must have their rows at the same distance")
         dstate_out = dstate if dstate_out is None else _out(dstate_out, "dstate_out", torch.float32, (B, D), dev)
         drate = torch.empty((D,), dtype=torch.float32, device=dev)
@@ -754,7 +762,7 @@ def glr_scan_backward(dstate, x, r, g, rate, carry, dy, reset=None, lens=None, c
         rc = lib().glr_scan_backward(dstate.data_ptr(), dstate_out.data_ptr(), _ptr(x), lds[0], _ptr(r), lds[1],
                                      _ptr(g), lds[2], _ptr(codes), _ptr(exps), _DTYPES[dt], rate.data_ptr(),
                                      _ptr(reset), _ptr(lens), carry.data_ptr(), dy.data_ptr(), B, T, D,
-                                     grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), ld.pop(),
+                                     grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), ld,
                                      drate.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_err), st)
     _check("glr_scan_backward", rc)
     return (*grads, drate)
@@ -786,8 +794,7 @@ def ckpt8_unpack(codes, exps, dtype=torch.bfloat16, x=None, stream=None):
     if codes.dim() < 1:
         raise ValueError("codes must be [..., D]")
     D = codes.shape[-1]
-    _req(exps, "exps", torch.uint8, (*codes.shape[:-1], -(-D // 64)))
-    _same_device(codes.device, exps=exps)
+    _out_check(exps, "exps", torch.uint8, (*codes.shape[:-1], -(-D // 64)), codes.device)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
     with _on(codes.device, stream) as st:

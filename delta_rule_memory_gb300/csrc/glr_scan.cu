@@ -53,7 +53,7 @@ struct GlrArgs {
   void *y;              // or dy
   float *carry;
   void *dx, *dr, *dg;
-  float *part;          // [B * cs][D]: drate, summed over the tokens of a CTA
+  float *part;          // [B][D]: drate of each sequence
   int32_t *err;
 };
 
@@ -839,19 +839,29 @@ E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = 
     a.state_out[sc] = v.x;
     if (two) a.state_out[sc + 1] = v.y;
   }
-  // drate over the CTA's warps, in their order
+  // drate over the CTA's warps, then over the cluster's CTAs, in their order.  A CTA
+  // leaves its sum in CTA 0's slots of the half that the last step did not use:
+  // CTA 0 is at most one step behind.
   float2 *sum = reinterpret_cast<float2 *>(smem + sizeof(Runs));
   cp_async_wait<0>();
   __syncthreads();
   sum[warp * 32 + lane] = drate;
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 0)
     for (int i = 1; i < kWarps; ++i) drate = add2(drate, sum[i * 32 + lane]);
-    float *p = a.part + (static_cast<int64_t>(b) * cs + rank) * a.D + c;
+  auto slot = [&](int j) {
+    return reinterpret_cast<float2 *>(smem + sizeof(Runs) + kWarps * (kStage + kOut) + (2 * j + (steps & 1)) * 512) + lane;
+  };
+  if (cs > 1 && warp == 0 && rank > 0)
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(in_cta(slot(rank), 0)), "f"(drate.x), "f"(drate.y)
+                 : "memory");
+  close_runs(at, a.err);
+  if (warp == 0 && rank == 0) {
+    for (int i = 1; i < cs; ++i) drate = add2(drate, *slot(i));
+    float *p = a.part + static_cast<int64_t>(b) * a.D + c;
     if (one) p[0] = drate.x;
     if (two) p[1] = drate.y;
   }
-  close_runs(at, a.err);
 }
 
 // drate[c] = sum over the parts: 32 interleaved sums, then those in order
@@ -1059,7 +1069,7 @@ extern "C" int glr_scan_train(const float *state, float *state_out, const void *
 
 extern "C" size_t glr_scan_backward_workspace_size(int B, int T, int D) {
   if (check_sizes("glr_scan_backward_workspace_size", SDM_DTYPE_F32, B, T, D) != SDM_OK) return 0;
-  return (sizeof(float) * B * kMaxCluster * static_cast<size_t>(D) + 255) / 256 * 256;
+  return (sizeof(float) * B * static_cast<size_t>(D) + 255) / 256 * 256;
 }
 
 extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const void *x, int64_t ld_x, const void *r,
@@ -1102,7 +1112,7 @@ extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const v
   a.codes = const_cast<int8_t *>(codes), a.exps = const_cast<uint8_t *>(exps), a.rate = rate, a.reset = reset, a.lens = lens;
   a.B = B, a.T = T, a.D = D, a.S = (T + kSeg - 1) / kSeg;
   a.y = const_cast<void *>(dy), a.carry = const_cast<float *>(carry);
-  a.dx = dx, a.dr = dr, a.dg = dg, a.part = static_cast<float *>(workspace), a.err = dev_err;
+  a.dx = dx, a.dr = dr, a.dg = dg, a.part = B == 1 ? drate : static_cast<float *>(workspace), a.err = dev_err;
   a.drop = test_drop_signal();
   a.cs = backward_cluster(B, T, D, dtype);
   if (B > 0) {
@@ -1114,8 +1124,8 @@ extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const v
       rc = vec ? launch_backward<float, true>(fn, a, st) : launch_backward<float, false>(fn, a, st);
     else
       rc = vec ? launch_backward<uint16_t, true>(fn, a, st) : launch_backward<uint16_t, false>(fn, a, st);
-    if (rc) return rc;
+    if (rc || B == 1) return rc;
   }
-  glr_rate_kernel<<<(D + 31) / 32, dim3(32, 32), 0, st>>>(a.part, B * a.cs, D, drate);
+  glr_rate_kernel<<<(D + 31) / 32, dim3(32, 32), 0, st>>>(a.part, B, D, drate);
   return check_launch(fn);
 }
