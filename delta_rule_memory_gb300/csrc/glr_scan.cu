@@ -99,6 +99,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, dup(-1.f), a); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float2 sigmoid2(float2 v) {
@@ -703,7 +705,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
   const int64_t sc = static_cast<int64_t>(b) * a.D + c;
   float2 v = make_float2(one && a.state ? a.state[sc] : 0.f, two && a.state ? a.state[sc + 1] : 0.f);
   open_runs(runs, at);
-  float2 drate = dup(0.f);
+  float2 drate = dup(0.f), lost = dup(0.f);  // the sum so far, and what its roundings lost
   const int tile = kBackwardRun * kWarps, tokens = tile * cs;
   const int steps = (len + tokens - 1) / tokens;
   int t0 = ((steps - 1) * cs + rank) * tile + warp * kBackwardRun;  // below 0 with no tokens: nothing is read then
@@ -816,11 +818,12 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
     if (n > 0) {
 E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
+      float2 part = dup(0.f);
 #pragma unroll
       for (int i = kSeg - 1; i >= 0; --i, o -= out_row) {
         if (i < n) {
           const float2 dh = fma2(ff, dd, dy(i)), w = mul2(dh, cr[i]);
-          drate = fma2(dh, cr[i], drate);
+          part = fma2(dh, cr[i], part);
           if (one) {
             store2<VEC>(dx, o, mul2(dh, cx[i]), two);
             store2<VEC>(dr, o, mul2(w, ck[i]), two);
@@ -830,6 +833,10 @@ E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = 
           if (CUTS && cut >> i & 1) ff = dup(0.f), dd = dup(0.f);
         }
       }
+      // the run's sum joins without loss: thousands of them cancel to a little (two-sum)
+      const float2 sum = add2(drate, part), back = sub2(sum, drate);
+      lost = add2(lost, add2(sub2(drate, sub2(sum, back)), sub2(part, back)));
+      drate = sum;
     }
     out -= tokens * a.ld_d;
     __syncwarp();  // the next dy goes where this was read
@@ -842,6 +849,7 @@ E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = 
   // drate over the CTA's warps, then over the cluster's CTAs, in their order.  A CTA
   // leaves its sum in CTA 0's slots of the half that the last step did not use:
   // CTA 0 is at most one step behind.
+  drate = add2(drate, lost);
   float2 *sum = reinterpret_cast<float2 *>(smem + sizeof(Runs));
   cp_async_wait<0>();
   __syncthreads();
