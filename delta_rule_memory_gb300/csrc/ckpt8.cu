@@ -81,11 +81,16 @@ struct Step {
 Step step_of(int64_t rows, int G, int64_t on) {
   return Step{rows * G, on, on / G, static_cast<int>(on % G), G};
 }
+// DENSE: the groups are whole and follow one another in x and in codes, so a
+// group is as good as a row.
+template <bool DENSE>
 struct GroupWalk {
   int64_t row;
   int grp;
   __device__ __forceinline__ GroupWalk(int64_t first, const Step &s) {
-    if (s.groups <= 0xffffffffll) {
+    if (DENSE) {
+      row = first, grp = 0;
+    } else if (s.groups <= 0xffffffffll) {
       const uint32_t r = static_cast<uint32_t>(first) / static_cast<uint32_t>(s.G);
       row = r, grp = static_cast<int>(static_cast<uint32_t>(first) - r * s.G);
     } else {
@@ -93,8 +98,12 @@ struct GroupWalk {
     }
   }
   __device__ __forceinline__ void next(const Step &s) {
-    row += s.rows_on, grp += s.grps_on;
-    if (grp >= s.G) grp -= s.G, ++row;
+    if (DENSE) {
+      row += s.on;
+    } else {
+      row += s.rows_on, grp += s.grps_on;
+      if (grp >= s.G) grp -= s.G, ++row;
+    }
   }
 };
 
@@ -102,12 +111,13 @@ struct GroupWalk {
 // groups of a thread at a time
 // (bf16 32,768 x 3840: 74 us with four in flight a thread and six CTAs an SM, 88
 // with two, 78 with four CTAs).
-template <class E, int kFlight>
+template <class E, int kFlight, bool DENSE>
 __global__ void __launch_bounds__(256, sizeof(E) == 2 ? 6 : 4) pack8_kernel(const E *x, int64_t ld, int64_t rows, int D, const Step s,
                                                        int8_t *codes, uint8_t *exps, int32_t *err) {
   const int64_t thread = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int part = threadIdx.x & 7;
-  GroupWalk ahead(thread >> 3, s), w = ahead;
+  const int part = threadIdx.x & 7, G = DENSE ? 1 : s.G;
+  if (DENSE) rows = s.groups, D = kGroup, ld = kGroup;
+  GroupWalk<DENSE> ahead(thread >> 3, s), w = ahead;
   bool bad = false;
   // whole warps leave together: a warp's four groups are neighbours, and a group
   // behind the last row only skips its loads and stores
@@ -129,7 +139,10 @@ __global__ void __launch_bounds__(256, sizeof(E) == 2 ? 6 : 4) pack8_kernel(cons
       const Eight v = e[i].eight();
       uint32_t q[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = ckpt8::code_bits(v.v[j], inv);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 c = __ffma2_rn(make_float2(v.v[j], v.v[j + 1]), make_float2(inv, inv), make_float2(12582912.f, 12582912.f));
+        q[j] = __float_as_uint(c.x), q[j + 1] = __float_as_uint(c.y);
+      }
       uint2 u;
       u.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
       u.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
@@ -138,19 +151,20 @@ __global__ void __launch_bounds__(256, sizeof(E) == 2 ? 6 : 4) pack8_kernel(cons
       if (w.row < rows && c < D) {
         *reinterpret_cast<uint2 *>(codes + w.row * D + c) = u;
         bad |= byte == 255u;
-        if (part == 0) exps[w.row * s.G + w.grp] = static_cast<uint8_t>(byte);
+        if (part == 0) exps[w.row * G + w.grp] = static_cast<uint8_t>(byte);
       }
     }
   }
   if (bad && err) atomicOr(err, SDM_DEVERR_NONFINITE);
 }
 
-template <class E, int kFlight>
+template <class E, int kFlight, bool DENSE>
 __global__ void __launch_bounds__(256) unpack8_kernel(const int8_t *codes, const uint8_t *exps, int64_t rows, int D,
                                                       const Step st, E *x, int64_t ld) {
   const int64_t thread = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int part = threadIdx.x & 7;
-  GroupWalk w(thread >> 3, st);
+  const int part = threadIdx.x & 7, G = DENSE ? 1 : st.G;
+  if (DENSE) rows = st.groups, D = kGroup, ld = kGroup;
+  GroupWalk<DENSE> w(thread >> 3, st);
   while (w.row < rows) {
     uint2 u[kFlight];
     uint32_t byte[kFlight];
@@ -162,7 +176,7 @@ __global__ void __launch_bounds__(256) unpack8_kernel(const int8_t *codes, const
       row[i] = w.row, c[i] = w.grp * kGroup + 8 * part;
       in[i] = w.row < rows && c[i] < D;
       u[i] = make_uint2(0, 0), byte[i] = 1;
-      if (in[i]) u[i] = *reinterpret_cast<const uint2 *>(codes + row[i] * D + c[i]), byte[i] = exps[row[i] * st.G + w.grp];
+      if (in[i]) u[i] = *reinterpret_cast<const uint2 *>(codes + row[i] * D + c[i]), byte[i] = exps[row[i] * G + w.grp];
     }
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
@@ -181,7 +195,7 @@ __global__ void __launch_bounds__(256) pack1_kernel(const E *x, int64_t ld, int6
                                                     int8_t *codes, uint8_t *exps, int32_t *err) {
   const int lane = threadIdx.x & 31, G = ckpt8::groups(D);
   bool bad = false;
-  for (GroupWalk w((static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5, s); w.row < rows; w.next(s)) {
+  for (GroupWalk<false> w((static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5, s); w.row < rows; w.next(s)) {
     const int c = w.grp * kFour + lane, left = D - c;  // w is the same in the whole warp
     const E *p = x + w.row * ld + c;
     int8_t *q = codes + w.row * D + c;
@@ -210,7 +224,7 @@ template <class E>
 __global__ void __launch_bounds__(256) unpack1_kernel(const int8_t *codes, const uint8_t *exps, int64_t rows, int D,
                                                       const Step s, E *x, int64_t ld) {
   const int lane = threadIdx.x & 31, G = ckpt8::groups(D);
-  for (GroupWalk w((static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5, s); w.row < rows; w.next(s)) {
+  for (GroupWalk<false> w((static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5, s); w.row < rows; w.next(s)) {
     const int c = w.grp * kFour + lane, left = D - c;
     const int8_t *q = codes + w.row * D + c;
     E *p = x + w.row * ld + c;
@@ -254,17 +268,21 @@ bool wide(const void *x, int64_t ld, int dtype, int64_t rows, int D, const void 
   return D % 8 == 0 && aligned(x, 16) && aligned(codes, 8) && (rows == 1 || ld * (dtype == SDM_DTYPE_F32 ? 4 : 2) % 16 == 0);
 }
 
+bool dense(int64_t ld, int64_t rows, int D) { return D % kGroup == 0 && (rows == 1 || ld == D); }
+
 template <class E>
 void launch_pack(const void *x, int64_t ld, int dtype, int64_t rows, int D, int8_t *codes, uint8_t *exps, int32_t *err,
                  cudaStream_t st) {
   const int G = ckpt8::groups(D);
   const E *p = static_cast<const E *>(x);
   if (wide(x, ld, dtype, rows, D, codes)) {
-    const int flight = small(rows * G) ? 1 : 4;
-    const unsigned grid = grid_for(rows * G, 32, flight);
+    const bool one = small(rows * G), flat = dense(ld, rows, D);
+    const unsigned grid = grid_for(rows * G, 32, one ? 1 : 4);
     const Step s = step_of(rows, G, static_cast<int64_t>(grid) * 32);
-    if (flight == 1) pack8_kernel<E, 1><<<grid, 256, 0, st>>>(p, ld, rows, D, s, codes, exps, err);
-    else pack8_kernel<E, 4><<<grid, 256, 0, st>>>(p, ld, rows, D, s, codes, exps, err);
+    if (one && flat) pack8_kernel<E, 1, true><<<grid, 256, 0, st>>>(p, ld, rows, D, s, codes, exps, err);
+    else if (one) pack8_kernel<E, 1, false><<<grid, 256, 0, st>>>(p, ld, rows, D, s, codes, exps, err);
+    else if (flat) pack8_kernel<E, 4, true><<<grid, 256, 0, st>>>(p, ld, rows, D, s, codes, exps, err);
+    else pack8_kernel<E, 4, false><<<grid, 256, 0, st>>>(p, ld, rows, D, s, codes, exps, err);
   } else {
     const int U = (G + 3) / 4;
     const unsigned grid = grid_for(rows * U, 8, 1);
@@ -278,11 +296,13 @@ void launch_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows, int D
   const int G = ckpt8::groups(D);
   E *p = static_cast<E *>(x);
   if (wide(x, ld, dtype, rows, D, codes)) {
-    const int flight = small(rows * G) ? 1 : 2;
-    const unsigned grid = grid_for(rows * G, 32, flight);
+    const bool one = small(rows * G), flat = dense(ld, rows, D);
+    const unsigned grid = grid_for(rows * G, 32, one ? 1 : 2);
     const Step s = step_of(rows, G, static_cast<int64_t>(grid) * 32);
-    if (flight == 1) unpack8_kernel<E, 1><<<grid, 256, 0, st>>>(codes, exps, rows, D, s, p, ld);
-    else unpack8_kernel<E, 2><<<grid, 256, 0, st>>>(codes, exps, rows, D, s, p, ld);
+    if (one && flat) unpack8_kernel<E, 1, true><<<grid, 256, 0, st>>>(codes, exps, rows, D, s, p, ld);
+    else if (one) unpack8_kernel<E, 1, false><<<grid, 256, 0, st>>>(codes, exps, rows, D, s, p, ld);
+    else if (flat) unpack8_kernel<E, 2, true><<<grid, 256, 0, st>>>(codes, exps, rows, D, s, p, ld);
+    else unpack8_kernel<E, 2, false><<<grid, 256, 0, st>>>(codes, exps, rows, D, s, p, ld);
   } else {
     const int U = (G + 3) / 4;
     const unsigned grid = grid_for(rows * U, 8, 1);

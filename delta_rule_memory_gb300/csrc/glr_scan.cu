@@ -450,23 +450,24 @@ __device__ __forceinline__ uint32_t max_magnitude(float2 v) {
 }
 
 // The checkpoint of 8 tokens from shared memory to global memory: token i's
-// codes are the first 64 bytes of its row in each of the three tensors' rows, the
-// exponents are `bytes`.  VEC: 16 bytes a lane.  Groups with a value that has no
-// code get zeros and 255.
+// codes are the first 64 bytes of its row in each of the three tensors' rows; lane
+// 8 k + i holds the largest magnitude's bits of token i in tensor k.  VEC: 16
+// bytes a lane.  Groups with a value that has no code get zeros and 255; returns
+// whether there are any.
 template <class E, bool VEC>
-__device__ __forceinline__ void put_codes(const GlrArgs &a, unsigned char *q, const unsigned char *bytes, int64_t row,
-                                          int n, int c0, int chan, int lane) {
+__device__ __forceinline__ bool put_codes(const GlrArgs &a, unsigned char *q, uint32_t big, int64_t row, int n, int c0,
+                                          int chan, int lane) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
   __syncwarp();
   const int k = lane >> 3, i = lane & 7;
-  uint32_t byte = lane < 24 ? bytes[lane] : 0;
-  for (uint32_t bad = __ballot_sync(kFull, lane < 24 && i < n && byte > ckpt8::kLast); bad; bad &= bad - 1) {
+  const bool mine = lane < 24 && i < n;
+  const uint32_t all = __ballot_sync(kFull, mine && big > ckpt8::kTop);
+  for (uint32_t bad = all; bad; bad &= bad - 1) {
     const int j = __ffs(bad) - 1;
     *reinterpret_cast<uint16_t *>(q + (j >> 3) * Rows<E, VEC>::kBytes + (j & 7) * Rows<E, VEC>::kRow + 2 * lane) = 0;
-    if (lane == j) byte = 255;
     __syncwarp();
   }
-  if (lane < 24 && i < n) a.exps[(k * rows + row + i) * ckpt8::groups(a.D) + c0 / kChan] = static_cast<uint8_t>(byte);
+  if (mine) a.exps[(k * rows + row + i) * ckpt8::groups(a.D) + c0 / kChan] = static_cast<uint8_t>(ckpt8::exp_byte(big));
   if (VEC && a.D % 16 == 0) {
     const int j = lane >> 2, at = 16 * (lane & 3);
     if (j < n && at < chan) {
@@ -484,6 +485,7 @@ __device__ __forceinline__ void put_codes(const GlrArgs &a, unsigned char *q, co
         if (2 * lane + 1 < chan) o[2 * lane + 1] = static_cast<int8_t>(s[2 * lane + 1]);
       }
   }
+  return all != 0;
 }
 
 // ---- forward ----
@@ -492,10 +494,10 @@ template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   Runs &runs = *reinterpret_cast<Runs *>(smem);
-  constexpr int kBytes = Rows<E, VEC>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg, kOut = K8 ? 32 : 0;
+  constexpr int kBytes = Rows<E, VEC>::kBytes, kHalf = 3 * kBytes, kHalves = kForwardRun / kSeg;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int cs = a.cs;
-  unsigned char *mine = smem + sizeof(Runs) + warp * (kHalves * kHalf + kOut);
+  unsigned char *mine = smem + sizeof(Runs) + warp * kHalves * kHalf;
   const int rank = blockIdx.x % cs, c0 = (blockIdx.x / cs) * kChan, b = blockIdx.y;
   const int c = c0 + 2 * lane, chan = min(kChan, a.D - c0);
   const bool one = c < a.D, two = c + 1 < a.D;
@@ -529,7 +531,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   };
   for (int half = 0; half < kHalves; ++half) fetch(half, t0 + kSeg * half);
   if (cs > 1) cluster_wait();  // every CTA of the cluster runs before one writes into another
-  uint32_t top = 0;            // K8: the largest magnitude's bits
+  bool bad = false;            // K8: a group without codes
   const uint8_t *flags = CUTS ? a.reset + static_cast<int64_t>(b) * a.T : nullptr;
   uint32_t flag = CUTS ? reset_flag(flags, t0, min(kForwardRun, len - t0), lane) : 0;
   for (int step = 0; step < steps; ++step, t0 += tokens) {
@@ -542,6 +544,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
       cp_async_wait<kHalves - 1>();
       __syncwarp();
       unsigned char *d = mine + half * kHalf;
+      uint32_t kept = 0;  // K8, lane 8 k + i: the largest magnitude's bits of token i in tensor k
 #pragma unroll
       for (int i = 0; i < kSeg; ++i) {
         const float2 x = wx.pair(d, i, lane), r = wr.pair(d + kBytes, i, lane), g = wg.pair(d + 2 * kBytes, i, lane);
@@ -558,13 +561,12 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
             const float2 code = fma2(in[k], dup(__uint_as_float((254u << 23) - step8)), dup(12582912.f));
             *reinterpret_cast<uint16_t *>(d + k * kBytes + i * Rows<E, VEC>::kRow + 2 * lane) =
                 static_cast<uint16_t>(__byte_perm(__float_as_uint(code.x), __float_as_uint(code.y), 0x0040));
-            if (lane == 0) mine[kHalves * kHalf + 8 * k + i] = static_cast<unsigned char>(step8 >> 23);
-            top = kSeg * half + i < n ? max(top, big) : top;
+            if (lane == 8 * k + i) kept = big;
           }
         }
       }
       if (K8 && n > kSeg * half)
-        put_codes<E, VEC>(a, d, mine + kHalves * kHalf, static_cast<int64_t>(b) * a.T + t0 + kSeg * half,
+        bad |= put_codes<E, VEC>(a, d, kept, static_cast<int64_t>(b) * a.T + t0 + kSeg * half,
                           min(kSeg, n - kSeg * half), c0, chan, lane);
       __syncwarp();  // the copies go where these rows were read
       fetch(half, t0 + tokens + kSeg * half);
@@ -583,7 +585,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
 #pragma unroll
       for (int i = 1; i < kForwardRun; ++i) q.P = mul2(q.P, f[i]), q.H = fma2(f[i], q.H, u[i]);
     }
-    float2 h = compose<CUTS, sizeof(Runs) + kWarps * (kHalves * kHalf + kOut)>(runs, step, at, q, v);
+    float2 h = compose<CUTS, sizeof(Runs) + kWarps * kHalves * kHalf>(runs, step, at, q, v);
     if (n > 0 && one) {
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E));
 #pragma unroll
@@ -605,7 +607,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
     if (two) a.state_out[sc + 1] = v.y;
   }
   close_runs(at, a.err);
-  if (K8 && top > ckpt8::kTop && lane == 0 && a.err) atomicOr(a.err, SDM_DEVERR_NONFINITE);
+  if (K8 && bad && lane == 0 && a.err) atomicOr(a.err, SDM_DEVERR_NONFINITE);
 }
 
 // ---- a few tokens: decoding steps ----
@@ -912,8 +914,8 @@ int check_words(const char *fn, std::initializer_list<const void *> ps) {
 
 // Shared memory of a CTA without its cluster's runs.
 template <class E, bool VEC>
-constexpr size_t forward_smem(bool keep8) {
-  return sizeof(Runs) + kWarps * (kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes + (keep8 ? 32 : 0));
+constexpr size_t forward_smem() {
+  return sizeof(Runs) + kWarps * kForwardRun / kSeg * 3 * Rows<E, VEC>::kBytes;
 }
 template <class E, bool VEC>
 constexpr size_t backward_smem(bool keep8) {
@@ -947,7 +949,7 @@ int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
 }
 int forward_cluster(int B, int T, int D, int dtype) {
   return cluster_size(B, T, D, kForwardRun, kForwardRegs,
-                      dtype == SDM_DTYPE_F32 ? forward_smem<float, true>(false) : forward_smem<uint16_t, true>(false));
+                      dtype == SDM_DTYPE_F32 ? forward_smem<float, true>() : forward_smem<uint16_t, true>());
 }
 int backward_cluster(int B, int T, int D, int dtype) {
   return cluster_size(B, T, D, kBackwardRun, kBackwardRegs,
@@ -997,7 +999,7 @@ int launch_step(const char *fn, const GlrArgs &a, cudaStream_t st) {
 
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = cluster_bytes(a.cs) + forward_smem<E, VEC>(a.codes != nullptr);
+  const size_t smem = cluster_bytes(a.cs) + forward_smem<E, VEC>();
   if (a.reset)
     return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
