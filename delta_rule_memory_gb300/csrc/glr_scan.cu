@@ -8,11 +8,21 @@
 // that splits the sequence.  A warp owns 64 channels (a pair per lane) of a run
 // of 16 tokens (8 in the backward): it forms the run's (P, H), takes the state in
 // front of it from the runs before, and steps its tokens through once more with
-// the gates still in registers.  Up to eight warps make a CTA, up to eight CTAs a
+// the gates still in registers.  Four warps make a CTA, up to sixteen CTAs a
 // cluster (runs travel through distributed shared memory), and the cluster
 // walks the sequence.  Every input is read once and every output written once,
 // no CTA waits for another outside its cluster, and the order of every sum is
 // fixed by the sizes.
+//
+// What bounds it (8 x 4096 x 1920 in bf16, one GB300): the forward moves 8 bytes an
+// element and takes 117 us, 64% of the measured copy bandwidth; its walk over
+// memory alone takes 84 us, and without the exchange of runs it takes 108.  An
+// element pair costs about 62 instructions, ten of them special functions, and
+// 128 registers a thread leave four warps to an SM's scheduler, which issues in
+// 59% of the cycles: latency between dependent instructions, not memory, is
+// what is left.  Runs of 8 tokens in 64 to 80 registers have more warps, but
+// exchange twice as often: 125 us.  The backward (14.5 bytes) takes 220 us (61%)
+// for the same reason, at twice the instructions.
 #include <initializer_list>
 #include <type_traits>
 
@@ -34,7 +44,7 @@ constexpr int kWarps = 4;        // of a CTA
 constexpr int kMaxCluster = 16;
 constexpr int kSMs = 152;
 constexpr int kForwardRegs = 128, kBackwardRegs = 128;  // of a thread
-constexpr uint32_t kWaitPolls = 1u << 20;
+constexpr uint32_t kWaitPolls = 1u << 20;  // of a cluster's mbarrier, about 0.1 s, before the wait gives up
 static_assert(kChan == ckpt8::kGroup, "a warp's channels are one checkpoint group");
 
 struct GlrArgs {
@@ -113,8 +123,9 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 // both from e = 1 - a.  Near a = 1 the exponential unit cannot give e (the difference
 // cancels, and its results near 1 are cut off, not rounded: a bias of 2^-25, which a
 // horizon of 1 / e tokens multiplies; sums of gradients lost a digit to it).
-// Up to y = 0.15, where a bias counts little, e = y q(y) with q the cubic next to
-// (1 - e^-y) / y there (by linear programming, q(0) = 1): off by 5e-8 at most.
+// So up to y = 0.15, e = y q(y) with q the cubic next to (1 - e^-y) / y there (by
+// linear programming, q(0) = 1): off by 5e-8 at most.  Beyond, horizons are of a
+// few tokens and the unit's bias counts for little.
 // a is off by 2^-25 at most by taking it as 1 - e, which below 1/2 is more than a
 // relative rounding, and nothing next to an input of the same token.
 struct Decay {
@@ -134,9 +145,8 @@ __device__ __forceinline__ Decay decay(float2 y) {
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
 // m sigmoid(g) x with one special function less than its factors take: sigmoid(g)
 // = 1 / d, d = 1 + e^-g, so m / d = m2 / sqrt(d^2 m2).  The number added to m2 keeps
-// the root's inverse finite at m2 = 0 and is lost in it from 2^-100 on.  (The
-// special functions bind: 8 x 4096 x 1920 with the reciprocal of d by itself
-// took 138 us on one CTA a column in place of 127.)
+// the root's inverse finite at m2 = 0 and is lost in it from 2^-100 on.  (8 x 4096 x
+// 1920 on one CTA a column: 127 us, and 138 with the reciprocal of d by itself.)
 __device__ __forceinline__ float2 input_term(float2 m2, float2 g, float2 x) {
   const float2 z = mul2(g, dup(-kLog2e));
   const float2 d = add2(make_float2(ex2(z.x), ex2(z.y)), dup(1.f));
@@ -490,6 +500,11 @@ __device__ __forceinline__ bool put_codes(const GlrArgs &a, unsigned char *q, ui
 
 // ---- forward ----
 // K8: also the 8-bit checkpoints of x, r and g.  CUTS: with reset flags.
+// 8 x 4096 x 1920 in bf16: 117 us (64% of the measured copy bandwidth); with the
+// carry 120; with checkpoints as well 187 (11.55 bytes an element, 57%: their
+// maxima, codes and exponents nearly double the instructions).  1 x 32768 x 3840, one
+// sequence over clusters of 9: 228 us (65%); 2 x 8192 x 3840 with resets: 133
+// (56%); fp32, 4 x 4096 x 1920: 111 (67%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -613,7 +628,8 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
 // ---- a few tokens: decoding steps ----
 // N channels of one sequence a thread (N = 16 bytes of E, or 1 where rows are
 // not aligned to that), its tokens in order; the same operations as above, so the
-// same bits.  Bound by the launch and, for large batches, by memory.
+// same bits.  Bound by the launch and latency of one load after another: 6 us for a
+// sequence of 1920 channels, 9 for 256 of 3840 (10 MB with the states, which takes 2).
 template <class E, int N>
 struct alignas(sizeof(E) * N) Pack {
   E v[N];
@@ -686,7 +702,11 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
 // ---- backward ----
 // The same walk from the last token to the first; what runs through it is
 // e_t = a_t dh_t, the gradient that reaches h_{t-1}: dh_t = dy_t + e_{t+1}.
-// K8: x, r and g come from their checkpoints.
+// K8: x, r and g come from their checkpoints.  A run is the 8 tokens between two
+// kept states, so the states inside it are recomputed in registers and cost no
+// memory.  8 x 4096 x 1920 in bf16: 220 us (61% of the measured copy bandwidth),
+// from checkpoints 227 (11.55 bytes an element, 47%: decoding replaces the
+// bytes it saves); fp32, 4 x 4096 x 1920: 178 (74%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -818,7 +838,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
     q.H = mul2(ff, dd);
     dd = compose<CUTS, sizeof(Runs) + kWarps * (kStage + kOut)>(runs, step, at, q, v), ff = dup(1.f);
     if (n > 0) {
-E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
+      E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
       float2 part = dup(0.f);
 #pragma unroll
@@ -874,7 +894,8 @@ E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = 
   }
 }
 
-// drate[c] = sum over the parts: 32 interleaved sums, then those in order
+// drate[c] = sum over the sequences' parts: 32 interleaved sums, then those in
+// order.  A launch behind the backward's (about 2 us); one sequence needs none.
 __global__ void __launch_bounds__(1024) glr_rate_kernel(const float *part, int parts, int D, float *drate) {
   __shared__ float sum[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;

@@ -60,9 +60,9 @@ extern "C" {
 #define SDM_ERR_DEVICE 6       /* sdm_check: a device-side error was recorded */
 
 /* Device-side error bits (OR-ed into *dev_err when dev_err != NULL). */
-#define SDM_DEVERR_INDEX_RANGE 1  /* a slot index outside [0, N) (skipped) */
+#define SDM_DEVERR_INDEX_RANGE 1  /* a slot index outside [0, N) (skipped); a length of glr_scan outside [0, T] (clamped) */
 #define SDM_DEVERR_INDEX_REPEAT 2 /* a slot repeated within one token's write list */
-#define SDM_DEVERR_NONFINITE 4    /* a NaN or infinite score or logit */
+#define SDM_DEVERR_NONFINITE 4    /* a NaN or infinite score or logit; an 8-bit checkpoint group without codes */
 #define SDM_DEVERR_TIMEOUT 8      /* a bounded on-device wait gave up; outputs invalid */
 #define SDM_DEVERR_RATE 16        /* a decay rate of glr_scan below zero or not finite (taken as 0) */
 
@@ -85,7 +85,8 @@ extern "C" {
  *   SDM_SSE_PATH=recurrent|chunk    sse_scan: force the token-by-token or the
  *       chunked prefill path (shape rules permitting).
  *   SDM_TEST_DROP_SIGNAL=1          test hook: the chunked GDN, KDA, GDN2 and
- *       SSE chain kernels skip one internal signal, so a bounded on-device wait runs out
+ *       SSE chain kernels and the glr_scan kernels (where a sequence is split over a
+ *       cluster) skip one internal signal, so a bounded on-device wait runs out
  *       and the call reports SDM_DEVERR_TIMEOUT (its outputs are invalid; the
  *       CUDA context stays usable).  Never set in normal use.
  */
@@ -524,10 +525,11 @@ SDM_API int sse_scan(float *state, const float *route_logits, int topk, const fl
  *            state after the last one that exists.  A value outside [0, T] is
  *            clamped to it and sets SDM_DEVERR_INDEX_RANGE.
  * y        : [B,T,D] of `dtype`, contiguous; must not overlap the inputs.
- * dev_err  : optional.
- * NaN and infinite x, r, g are not looked for: they run through the
- * arithmetic, into the states of their channel only.  The state, its
- * decays and their products are fp32; y is rounded once, to nearest even.
+ * dev_err  : optional; also SDM_DEVERR_TIMEOUT if a bounded wait gave up (a
+ *            sequence split over a cluster of thread blocks).
+ * NaN and infinite x, r, g and states are not looked for: they run through the
+ * arithmetic, into the states of their channel and sequence only, up to the next
+ * reset (an infinite state may go on as a NaN).  The state, its decays and their products are fp32; y is rounded once, to nearest even.
  * Limits: B, T, D >= 0, B < 65536, T < 2^30, D < 2^24; D <= ld < 2^27.  x, r, g, y
  *         aligned to their element; state, rate 4-byte.  Any B, T or D of 0
  *         is allowed (T = 0 copies the state).
@@ -588,7 +590,7 @@ SDM_API size_t glr_scan_backward_workspace_size(int B, int T, int D);
  * dy       : [B,T,D] of `dtype`, contiguous.
  * dx,dr,dg : [B,T,D] of `dtype` out, token t of sequence b at ld_d * (b T + t)
  *            elements, ld_d >= D: they may be column slices of one buffer.
- *            Rows behind lens[b] keep their bits.
+ *            They must not overlap the inputs or one another.  Rows behind lens[b] keep their bits.
  * drate    : fp32 [D] out (overwritten).
  * workspace: glr_scan_backward_workspace_size() bytes, 16-byte aligned;
  *            contents need no initialisation.  Calls that share one must not

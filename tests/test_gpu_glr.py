@@ -64,6 +64,7 @@ class Case:
         return dict(reset=self.reset, lens=self.lens)
 
 
+# one run and less, a run and one, one CTA, several, clusters; a channel to several blocks; steps of up to 8 tokens
 SHAPES = [(1, 1, 1), (2, 1, 64), (3, 2, 66), (1, 7, 3), (2, 8, 65), (2, 9, 130), (1, 63, 64), (1, 64, 32), (2, 65, 67),
           (1, 513, 129), (2, 1100, 192), (5, 300, 63), (1, 4099, 64), (70, 3, 256), (1, 2048, 1920)]
 
@@ -278,6 +279,31 @@ def test_a_split_sequence_continues():
         y = torch.cat([sdm.glr_scan(s, *part(0, T1), c.rate), sdm.glr_scan(s, *part(T1, 300), c.rate)], 1)
         assert_within(y, f["y"], f["e_y"], c.dt, "y")
         assert_within(s, f["hT"], f["e_hT"], torch.float32, "h_T")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_many_short_sequences(dt):
+    """A batch at the limit of the grid, by the step kernel and by the training forward."""
+    sdm = need_gpu()
+    c = Case(65535, 2, 3, dt, seed=19)
+    f = c.forward()
+    s, s2 = c.h0.clone(), c.h0.clone()
+    y = sdm.glr_scan(s, *c.args())
+    y2, carry = sdm.glr_scan_train(s2, *c.args())
+    assert torch.equal(y, y2) and torch.equal(s, s2)
+    assert_within(y, f["y"], f["e_y"], c.dt, "y")
+    check_backward(sdm, c, f, carry, None)
+
+
+def test_one_tensor_as_several_inputs_and_a_state_that_is_kept():
+    sdm = need_gpu()
+    c = Case(2, 40, 64, "bf16", seed=20)
+    y = sdm.glr_scan(c.h0.clone(), c.x, c.x, c.x, c.rate)
+    assert torch.equal(y, sdm.glr_scan(c.h0.clone(), c.x, c.x.clone(), c.x.clone(), c.rate))
+    before = c.h0.clone()
+    out = torch.empty_like(c.h0)
+    sdm.glr_scan(c.h0, c.x, c.r, c.g, c.rate, state_out=out)
+    assert torch.equal(c.h0, before) and not torch.equal(out, before)
 
 
 def test_empty_calls():
