@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -553,20 +554,19 @@ def sse_scan(state, route_logits, topk: int, k_logits, q, v, alpha, y=None, sel_
 _DTYPES = {torch.float32: SDM_DTYPE_F32, torch.bfloat16: SDM_DTYPE_BF16}
 
 
+_Tensor = torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _Here:
     """The current device and stream, as they are."""
+    handle = None
 
     def __enter__(self):
-        if _raw_stream is not None:     # the handle alone, without a Stream object around it
-            return _raw_stream(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        return self.handle
 
     def __exit__(self, *exc):
         return False
-
-
-_HERE_NOW = _Here()
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 @contextlib.contextmanager
@@ -575,36 +575,42 @@ def _there(device, stream):
         yield torch.cuda.current_stream().cuda_stream
 
 
-def _on(device: torch.device, stream):
+def _on(index: int, stream):
     """The device of the call's tensors and its stream (None: that device's
     current one) as the current ones, so that what the call allocates belongs
     to the stream that uses it.  The context's value is the stream's handle."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return _HERE_NOW
+        if index == torch.cuda.current_device():
+            here = _Here()      # the handle alone, without a Stream object around it
+            here.handle = torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(index)
+            return here
     elif not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-    return _there(device, stream)
+        stream = torch.cuda.ExternalStream(_stream(stream), device=index)
+    return _there(index, stream)
 
 
-def _plain(t, dtype, shape, device) -> bool:
-    """A contiguous tensor of this type, shape and device: nothing more to check."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+# The checks below take most of a small call's time on the host, so the common
+# case (contiguous, as expected) is one expression, and what is wrong is looked
+# for only once something is.
+
+def _plain(t, dtype, shape, index: int) -> bool:
+    """A contiguous tensor of this type, shape and CUDA device: nothing more to check."""
+    return (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous())
 
 
-def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
+def _act(t, name: str, dtype=None, shape=None, index=None) -> int:
     """Check an activation [..., rows, D] whose channels are contiguous and
     whose rows lie at one distance (a column slice of a wider contiguous
     tensor will do); returns that distance in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     D = t.shape[-1]
     ld = D
     if not t.is_contiguous() and t.numel():
@@ -622,51 +628,49 @@ def _act(t, name: str, dtype=None, shape=None, device=None) -> int:
     return ld
 
 
-def _glr_checks(state, x, r, g, rate, reset, lens, like=None):
-    """Common checks of the glr_scan calls; returns the shape [B,T,D], the
-    dtype, the device, the row distances of x, r and g, and reset as uint8
-    (`like`: a tensor of that shape in place of x, r and g)."""
-    first = x if like is None else like
-    _act(first, "x" if like is None else "dy")
-    if first.dim() != 3:
-        raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
-    shape, dt, dev = first.shape, first.dtype, first.device
-    B, T, D = shape
-    lds = (0, 0, 0)
-    if x is not None or like is None:
-        lds = tuple([D if _plain(t, dt, shape, dev) else _act(t, n, dt, shape, dev)
-                     for t, n in ((x, "x"), (r, "r"), (g, "g"))])
-    if not _plain(state, torch.float32, (B, D), dev):
-        _out_check(state, "state" if like is None else "dstate", torch.float32, (B, D), dev)
-    if not _plain(rate, torch.float32, (D,), dev):
-        _out_check(rate, "rate", torch.float32, (D,), dev)
-    if reset is not None:
-        if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
-            reset = reset.view(torch.uint8)
-        _out_check(reset, "reset", torch.uint8, (B, T), dev)
-    if lens is not None:
-        _out_check(lens, "lens", torch.int32, (B,), dev)
-    return shape, dt, dev, lds, reset
-
-
-def _out_check(t, name: str, dtype, shape, device):
+def _need(t, name: str, dtype, shape, index: int):
+    """A contiguous tensor; shape None: any."""
+    if isinstance(t, _Tensor) and _plain(t, dtype, t.shape if shape is None else shape, index):
+        return
     _req(t, name, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _out(t, name: str, dtype, shape, device):
+def _out(t, name: str, dtype, shape, index: int):
     """An output the caller gave, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not _plain(t, dtype, shape, device):
-        _out_check(t, name, dtype, shape, device)
+        return torch.empty(shape, dtype=dtype, device=index)
+    _need(t, name, dtype, shape, index)
     return t
 
 
-def _err_word(dev_err, device):
+def _glr_checks(state, x, r, g, rate, reset, lens, dev_err, like=None):
+    """Common checks of the glr_scan calls; returns the shape [B,T,D], the
+    dtype, the device's index, the row distances of x, r and g, and reset as
+    uint8 (`like`: a tensor of that shape in place of x, r and g)."""
+    first = x if like is None else like
+    _act(first, "x" if like is None else "dy")
+    shape = first.shape
+    if len(shape) != 3:
+        raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
+    dt, dev = first.dtype, first.get_device()
+    B, T, D = shape
+    lx = lr = lg = 0
+    if x is not None or like is None:
+        lx = D if _plain(x, dt, shape, dev) else _act(x, "x", dt, shape, dev)
+        lr = D if _plain(r, dt, shape, dev) else _act(r, "r", dt, shape, dev)
+        lg = D if _plain(g, dt, shape, dev) else _act(g, "g", dt, shape, dev)
+    _need(state, "state" if like is None else "dstate", torch.float32, (B, D), dev)
+    _need(rate, "rate", torch.float32, (D,), dev)
+    if reset is not None:
+        if isinstance(reset, _Tensor) and reset.dtype is torch.bool:
+            reset = reset.view(torch.uint8)
+        _need(reset, "reset", torch.uint8, (B, T), dev)
+    if lens is not None:
+        _need(lens, "lens", torch.int32, (B,), dev)
     if dev_err is not None:
-        _out_check(dev_err, "dev_err", torch.int32, None, device)
+        _need(dev_err, "dev_err", torch.int32, None, dev)
+    return B, T, D, shape, dt, dev, lx, lr, lg, reset
 
 
 def glr_scan(state, x, r, g, rate, reset=None, lens=None, y=None, state_out=None, dev_err=None, stream=None):
@@ -678,16 +682,15 @@ def glr_scan(state, x, r, g, rate, reset=None, lens=None, y=None, state_out=None
     exist.  Updates `state` fp32 [B,D] in place, or leaves it and writes
     `state_out` where that is given.  Returns y [B,T,D] of x's dtype (rows
     behind lens are not written).  T = 1 is the step of a decoding loop."""
-    shape, dt, dev, lds, reset = _glr_checks(state, x, r, g, rate, reset, lens)
-    B, T, D = shape
-    _err_word(dev_err, dev)
+    B, T, D, shape, dt, dev, lx, lr, lg, reset = _glr_checks(state, x, r, g, rate, reset, lens, dev_err)
     with _on(dev, stream) as st:
         y = _out(y, "y", dt, shape, dev)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
-        rc = lib().glr_scan(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lds[0], r.data_ptr(), lds[1],
-                            g.data_ptr(), lds[2], _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
+        rc = lib().glr_scan(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lx, r.data_ptr(), lr,
+                            g.data_ptr(), lg, _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
                             y.data_ptr(), _ptr(dev_err), st)
-    _check("glr_scan", rc)
+    if rc:
+        _check("glr_scan", rc)
     return y
 
 
@@ -702,9 +705,7 @@ def glr_scan_train(state, x, r, g, rate, reset=None, lens=None, keep8=False, y=N
     keep8 (or ckpt, a pair of buffers) (y, carry, (codes, exps)), the 8-bit
     checkpoints of x, r and g, int8 [3,B,T,D] and uint8 [3,B,T,ceil(D/64)],
     which the backward takes in place of x, r and g."""
-    shape, dt, dev, lds, reset = _glr_checks(state, x, r, g, rate, reset, lens)
-    B, T, D = shape
-    _err_word(dev_err, dev)
+    B, T, D, shape, dt, dev, lx, lr, lg, reset = _glr_checks(state, x, r, g, rate, reset, lens, dev_err)
     with _on(dev, stream) as st:
         y = _out(y, "y", dt, shape, dev)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
@@ -714,10 +715,11 @@ def glr_scan_train(state, x, r, g, rate, reset=None, lens=None, keep8=False, y=N
             codes, exps = (None, None) if ckpt is None else ckpt
             codes = _out(codes, "codes", torch.int8, (3, B, T, D), dev)
             exps = _out(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)), dev)
-        rc = lib().glr_scan_train(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lds[0], r.data_ptr(), lds[1],
-                                  g.data_ptr(), lds[2], _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
+        rc = lib().glr_scan_train(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lx, r.data_ptr(), lr,
+                                  g.data_ptr(), lg, _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
                                   y.data_ptr(), carry.data_ptr(), _ptr(codes), _ptr(exps), _ptr(dev_err), st)
-    _check("glr_scan_train", rc)
+    if rc:
+        _check("glr_scan_train", rc)
     return (y, carry) if codes is None else (y, carry, (codes, exps))
 
 
@@ -736,54 +738,61 @@ def glr_scan_backward(dstate, x, r, g, rate, carry, dy, reset=None, lens=None, c
         raise ValueError("give x, r and g or ckpt, not both")
     if ckpt is None and x is None:
         raise ValueError("x, r and g, or ckpt, are needed")
-    shape, dt, dev, lds, reset = _glr_checks(dstate, x, r, g, rate, reset, lens, like=dy)
-    B, T, D = shape
+    B, T, D, shape, dt, dev, lx, lr, lg, reset = _glr_checks(dstate, x, r, g, rate, reset, lens, dev_err, like=dy)
     if not dy.is_contiguous():
         raise ValueError("dy must be contiguous")
-    _out_check(carry, "carry", torch.float32, (B, -(-T // 8), D), dev)
+    _need(carry, "carry", torch.float32, (B, -(-T // 8), D), dev)
     codes = exps = None
     if ckpt is not None:
         codes, exps = ckpt
-        _out_check(codes, "codes", torch.int8, (3, B, T, D), dev)
-        _out_check(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)), dev)
-    _err_word(dev_err, dev)
+        _need(codes, "codes", torch.int8, (3, B, T, D), dev)
+        _need(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)), dev)
     with _on(dev, stream) as st:
         if grads is None:
-            grads = tuple([torch.empty(shape, dtype=dt, device=dev) for _ in range(3)])
-        ld, *more = [D if _plain(t, dt, shape, dev) else _act(t, n, dt, shape, dev)
-                     for t, n in zip(grads, ("dx", "dr", "dg"), strict=True)]
-        if any(d != ld for d in more):
-            raise ValueError("dx, dr and dg must have their rows at the same distance")
+            dx, dr, dg = [torch.empty(shape, dtype=dt, device=dev) for _ in range(3)]
+            ld = D
+        else:
+            dx, dr, dg = grads
+            ld = D if _plain(dx, dt, shape, dev) else _act(dx, "dx", dt, shape, dev)
+            if (ld != (D if _plain(dr, dt, shape, dev) else _act(dr, "dr", dt, shape, dev))
+                    or ld != (D if _plain(dg, dt, shape, dev) else _act(dg, "dg", dt, shape, dev))):
+                raise ValueError("dx, dr and dg must have their rows at the same distance")
         dstate_out = dstate if dstate_out is None else _out(dstate_out, "dstate_out", torch.float32, (B, D), dev)
         drate = torch.empty((D,), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(max(glr_scan_backward_workspace_size(B, T, D), 1), dtype=torch.uint8, device=dev)
-        _req(workspace, "workspace", torch.uint8)
-        rc = lib().glr_scan_backward(dstate.data_ptr(), dstate_out.data_ptr(), _ptr(x), lds[0], _ptr(r), lds[1],
-                                     _ptr(g), lds[2], _ptr(codes), _ptr(exps), _DTYPES[dt], rate.data_ptr(),
-                                     _ptr(reset), _ptr(lens), carry.data_ptr(), dy.data_ptr(), B, T, D,
-                                     grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), ld,
-                                     drate.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_err), st)
-    _check("glr_scan_backward", rc)
-    return (*grads, drate)
+        size = 0
+        if workspace is not None:
+            _need(workspace, "workspace", torch.uint8, None, dev)
+            size = workspace.numel()
+        elif B > 1:     # one sequence needs none
+            size = glr_scan_backward_workspace_size(B, T, D)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        rc = lib().glr_scan_backward(dstate.data_ptr(), dstate_out.data_ptr(), _ptr(x), lx, _ptr(r), lr, _ptr(g), lg,
+                                     _ptr(codes), _ptr(exps), _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens),
+                                     carry.data_ptr(), dy.data_ptr(), B, T, D, dx.data_ptr(), dr.data_ptr(),
+                                     dg.data_ptr(), ld, drate.data_ptr(), _ptr(workspace), size, _ptr(dev_err), st)
+    if rc:
+        _check("glr_scan_backward", rc)
+    return dx, dr, dg, drate
 
 
 def ckpt8_pack(x, codes=None, exps=None, dev_err=None, stream=None):
     """8-bit checkpoint of x, bf16 or fp32 [..., D] (rows at one distance):
     (codes int8 [..., D], exps uint8 [..., ceil(D/64)]).  Every 64 channels of
     a row share the smallest power-of-two step that fits them in [-127, 127]."""
-    ld = _act(x, "x")
-    if x.dim() < 1:
+    if isinstance(x, _Tensor) and x.dim() < 1:
         raise ValueError("x must be [..., D]")
-    D = x.shape[-1]
-    rows = x.numel() // D if D else 0
-    _err_word(dev_err, x.device)
-    with _on(x.device, stream) as st:
-        codes = _out(codes, "codes", torch.int8, x.shape, x.device)
-        exps = _out(exps, "exps", torch.uint8, (*x.shape[:-1], -(-D // 64)), x.device)
-        rc = lib().ckpt8_pack(x.data_ptr(), ld, _DTYPES[x.dtype], rows, D, codes.data_ptr(), exps.data_ptr(),
+    ld = _act(x, "x")
+    shape, dev = x.shape, x.get_device()
+    *rows, D = shape
+    if dev_err is not None:
+        _need(dev_err, "dev_err", torch.int32, None, dev)
+    with _on(dev, stream) as st:
+        codes = _out(codes, "codes", torch.int8, shape, dev)
+        exps = _out(exps, "exps", torch.uint8, (*rows, -(-D // 64)), dev)
+        rc = lib().ckpt8_pack(x.data_ptr(), ld, _DTYPES[x.dtype], math.prod(rows), D, codes.data_ptr(), exps.data_ptr(),
                               _ptr(dev_err), st)
-    _check("ckpt8_pack", rc)
+    if rc:
+        _check("ckpt8_pack", rc)
     return codes, exps
 
 
@@ -791,17 +800,20 @@ def ckpt8_unpack(codes, exps, dtype=torch.bfloat16, x=None, stream=None):
     """The values that a ckpt8_pack checkpoint stands for, as bf16 or fp32
     (exact in both)."""
     _req(codes, "codes", torch.int8)
-    if codes.dim() < 1:
+    shape, dev = codes.shape, codes.get_device()
+    if len(shape) < 1:
         raise ValueError("codes must be [..., D]")
-    D = codes.shape[-1]
-    _out_check(exps, "exps", torch.uint8, (*codes.shape[:-1], -(-D // 64)), codes.device)
+    *rows, D = shape
+    _need(exps, "exps", torch.uint8, (*rows, -(-D // 64)), dev)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    with _on(codes.device, stream) as st:
+    with _on(dev, stream) as st:
         if x is None:
-            x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-        ld = _act(x, "x", dtype, codes.shape, codes.device)
-        rc = lib().ckpt8_unpack(codes.data_ptr(), exps.data_ptr(), codes.numel() // D if D else 0, D, x.data_ptr(), ld,
-                                _DTYPES[dtype], st)
-    _check("ckpt8_unpack", rc)
+            x, ld = torch.empty(shape, dtype=dtype, device=dev), D
+        else:
+            ld = _act(x, "x", dtype, shape, dev)
+        rc = lib().ckpt8_unpack(codes.data_ptr(), exps.data_ptr(), math.prod(rows), D, x.data_ptr(), ld, _DTYPES[dtype],
+                                st)
+    if rc:
+        _check("ckpt8_unpack", rc)
     return x

@@ -983,8 +983,11 @@ bool pairs_vec(const void *p, int64_t ld, int es) { return aligned(p, 2 * es) &&
 
 template <class K>
 int launch(const char *fn, K kernel, size_t smem, const GlrArgs &a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  cudaError_t e;
+  if (smem > 48 << 10) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  }
   if (a.cs > 8) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
@@ -1100,7 +1103,7 @@ extern "C" int glr_scan_train(const float *state, float *state_out, const void *
 
 extern "C" size_t glr_scan_backward_workspace_size(int B, int T, int D) {
   if (check_sizes("glr_scan_backward_workspace_size", SDM_DTYPE_F32, B, T, D) != SDM_OK) return 0;
-  return (sizeof(float) * B * static_cast<size_t>(D) + 255) / 256 * 256;
+  return B < 2 ? 0 : (sizeof(float) * B * static_cast<size_t>(D) + 255) / 256 * 256;
 }
 
 extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const void *x, int64_t ld_x, const void *r,
@@ -1132,7 +1135,7 @@ extern "C" int glr_scan_backward(const float *dstate, float *dstate_out, const v
       if (!carry) return set_error(SDM_ERR_INVALID_ARG, "%s: null pointer (carry)", fn);
     }
     const size_t need = glr_scan_backward_workspace_size(B, T, D);
-    if (!workspace || workspace_bytes < need)
+    if (need > 0 && (!workspace || workspace_bytes < need))
       return set_error(SDM_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", fn, need);
     if (!aligned(workspace, 16)) return set_error(SDM_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   }

@@ -564,7 +564,7 @@ SDM_API int glr_scan_train(const float *state, float *state_out, const void *x, 
                            const uint8_t *reset, const int32_t *lens, int B, int T, int D, void *y, float *carry,
                            int8_t *codes, uint8_t *exps, int32_t *dev_err, void *stream);
 
-/* Scratch bytes glr_scan_backward needs: fp32 partial sums of drate. */
+/* Scratch bytes glr_scan_backward needs: fp32 partial sums of drate (0 for one sequence). */
 SDM_API size_t glr_scan_backward_workspace_size(int B, int T, int D);
 
 /*
@@ -592,8 +592,8 @@ SDM_API size_t glr_scan_backward_workspace_size(int B, int T, int D);
  *            elements, ld_d >= D: they may be column slices of one buffer.
  *            They must not overlap the inputs or one another.  Rows behind lens[b] keep their bits.
  * drate    : fp32 [D] out (overwritten).
- * workspace: glr_scan_backward_workspace_size() bytes, 16-byte aligned;
- *            contents need no initialisation.  Calls that share one must not
+ * workspace: glr_scan_backward_workspace_size() bytes, 16-byte aligned (NULL
+ *            where that is 0); contents need no initialisation.  Calls that share one must not
  *            overlap on the GPU.
  * Deterministic: sums are formed in a fixed order.
  */
