@@ -21,8 +21,8 @@
 // 128 registers a thread leave four warps to an SM's scheduler, which issues in
 // 59% of the cycles: latency between dependent instructions, not memory, is
 // what is left.  Runs of 8 tokens in 64 to 80 registers have more warps, but
-// exchange twice as often: 125 us.  The backward (14.5 bytes) takes 220 us (61%)
-// for the same reason, at twice the instructions.
+// exchange twice as often: 125 us.  The backward (14.5 bytes) takes 210 us (64%)
+// for the same reason, at 1.8 times the instructions.
 #include <initializer_list>
 #include <type_traits>
 
@@ -704,9 +704,9 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
 // e_t = a_t dh_t, the gradient that reaches h_{t-1}: dh_t = dy_t + e_{t+1}.
 // K8: x, r and g come from their checkpoints.  A run is the 8 tokens between two
 // kept states, so the states inside it are recomputed in registers and cost no
-// memory.  8 x 4096 x 1920 in bf16: 220 us (61% of the measured copy bandwidth),
-// from checkpoints 227 (11.55 bytes an element, 47%: decoding replaces the
-// bytes it saves); fp32, 4 x 4096 x 1920: 178 (74%).
+// memory.  8 x 4096 x 1920 in bf16: 210 us (64% of the measured copy bandwidth),
+// from checkpoints the same (11.55 bytes an element, 51%: decoding replaces the
+// bytes it saves); 1 x 32768 x 3840: 414 (65%); fp32, 4 x 4096 x 1920: 177 (75%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -841,20 +841,27 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
       E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
       float2 part = dup(0.f);
+      // `whole`: all 8 tokens exist (a run's only test of n then: 220 us in place
+      // of 210 with one per token)
+      auto put = [&](auto whole) {
 #pragma unroll
-      for (int i = kSeg - 1; i >= 0; --i, o -= out_row) {
-        if (i < n) {
-          const float2 dh = fma2(ff, dd, dy(i)), w = mul2(dh, cr[i]);
-          part = fma2(dh, cr[i], part);
-          if (one) {
-            store2<VEC>(dx, o, mul2(dh, cx[i]), two);
-            store2<VEC>(dr, o, mul2(w, ck[i]), two);
-            store2<VEC>(dg, o, mul2(dh, cg[i]), two);
+        for (int i = kSeg - 1; i >= 0; --i, o -= out_row) {
+          asm volatile("" : "+r"(o));  // keeps a row's offset one addition per lane
+          if (decltype(whole)::value || i < n) {
+            const float2 dh = fma2(ff, dd, dy(i)), w = mul2(dh, cr[i]);
+            part = fma2(dh, cr[i], part);
+            if (one) {
+              store2<VEC>(dx, o, mul2(dh, cx[i]), two);
+              store2<VEC>(dr, o, mul2(w, ck[i]), two);
+              store2<VEC>(dg, o, mul2(dh, cg[i]), two);
+            }
+            ff = f[i], dd = dh;
+            if (CUTS && cut >> i & 1) ff = dup(0.f), dd = dup(0.f);
           }
-          ff = f[i], dd = dh;
-          if (CUTS && cut >> i & 1) ff = dup(0.f), dd = dup(0.f);
         }
-      }
+      };
+      if (n == kSeg) put(std::true_type{});
+      else put(std::false_type{});
       // the run's sum joins without loss: thousands of them cancel to a little (two-sum)
       const float2 sum = add2(drate, part), back = sub2(sum, drate);
       lost = add2(lost, add2(sub2(drate, sub2(sum, back)), sub2(part, back)));
