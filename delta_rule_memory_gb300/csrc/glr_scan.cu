@@ -303,21 +303,32 @@ struct Walk {
 };
 
 // ---- the composition of runs ----
-// A run maps v to P v + H; `cut`: it does not depend on v at all (a reset), not
-// even where v is NaN.
+// A run maps v to P v + H.  A run with a reset does not depend on v at all, not
+// even where v is NaN: its P is -0, which no product of decays is.  (A flag of its
+// own beside P and H, stored, sent and tested apart, took the backward of 2 x 8192 x 3840
+// from OLD us to NEW.)
 struct Run {
   float2 P, H;
-  bool cut;
 };
+constexpr float kCut = -0.f;
+__device__ __forceinline__ bool is_cut(const Run &q) { return __float_as_uint(q.P.x) == 0x80000000u; }
 template <bool CUTS>
 __device__ __forceinline__ float2 apply(const Run &q, float2 v) {
-  return CUTS && q.cut ? q.H : fma2(q.P, v, q.H);
+  const float2 w = fma2(q.P, v, q.H);
+  if (!CUTS) return w;
+  return is_cut(q) ? q.H : w;
+}
+// p after q
+template <bool CUTS>
+__device__ __forceinline__ Run join(const Run &q, const Run &p) {
+  Run r{mul2(q.P, p.P), apply<CUTS>(p, q.H)};
+  if (CUTS && (is_cut(q) || is_cut(p))) r.P = dup(kCut);
+  return r;
 }
 
 // In front of a CTA's shared memory; then the warps' rows; then, in a cluster, the CTAs' runs.
 struct Runs {
   float4 warp[2][kWarps][32];
-  uint32_t warp_cut[2][kWarps], cta_cut[2][kMaxCluster];
   uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in its half of the CTAs' runs
 };
 __host__ __device__ constexpr uint32_t cluster_bytes(int cs) { return cs > 1 ? cs * 1024u : 0u; }
@@ -333,10 +344,6 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, int rank) {
 __device__ __forceinline__ void send(uint32_t dst, float4 v, uint32_t mbar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];\n" ::"r"(dst),
                "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mbar)
-               : "memory");
-}
-__device__ __forceinline__ void send(uint32_t dst, uint32_t v, uint32_t mbar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];\n" ::"r"(dst), "r"(v), "r"(mbar)
                : "memory");
 }
 // false: the phase did not complete within the bound
@@ -382,16 +389,15 @@ __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &
   const int half = k & 1, lane = at.lane, cs = at.cs;
   auto slot = [&](int j) { return reinterpret_cast<float4 *>(reinterpret_cast<char *>(&s) + kAt) + (2 * j + half) * 32 + lane; };
   s.warp[half][at.warp][lane] = make_float4(mine.P.x, mine.P.y, mine.H.x, mine.H.y);
-  if (CUTS && lane == 0) s.warp_cut[half][at.warp] = mine.cut;
-  if (cs > 1 && threadIdx.x == 0 && !at.lost) umma::mbar_expect_tx(smem_u32(&s.full[half]), cs * (CUTS ? 516 : 512));
+  if (cs > 1 && threadIdx.x == 0 && !at.lost) umma::mbar_expect_tx(smem_u32(&s.full[half]), cs * 512);
   __syncthreads();
   auto warp_run = [&](int j) {
     const float4 q = s.warp[half][j][lane];
-    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.warp_cut[half][j] != 0};
+    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w)};
   };
   auto cta_run = [&](int j) {
     const float4 q = *slot(j);
-    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w), CUTS && s.cta_cut[half][j] != 0};
+    return Run{make_float2(q.x, q.y), make_float2(q.z, q.w)};
   };
   if (cs == 1) {
 #pragma unroll 4
@@ -402,21 +408,13 @@ __device__ __forceinline__ float2 compose(Runs &s, int k, Place &at, const Run &
     for (int j = at.warp + 1; j < kWarps; ++j) v = apply<CUTS>(warp_run(j), v);
     return front;
   }
-  Run before{dup(1.f), dup(0.f), false};
+  Run before{dup(1.f), dup(0.f)};
 #pragma unroll 4
-  for (int j = 0; j < at.warp; ++j) {
-    const Run q = warp_run(j);
-    before.H = apply<CUTS>(q, before.H);
-    before.P = mul2(before.P, q.P);
-    if (CUTS) before.cut |= q.cut;
-  }
+  for (int j = 0; j < at.warp; ++j) before = join<CUTS>(before, warp_run(j));
   if (at.warp == kWarps - 1 && !at.drop && !at.lost) {  // the last warp knows the CTA's run
-    const float2 P = mul2(before.P, mine.P), H = apply<CUTS>(mine, before.H);
-    for (int i = 0; i < cs; ++i) {
-      const uint32_t mbar = in_cta(&s.full[half], i);
-      send(in_cta(slot(at.rank), i), make_float4(P.x, P.y, H.x, H.y), mbar);
-      if (CUTS && lane == 0) send(in_cta(&s.cta_cut[half][at.rank], i), before.cut || mine.cut ? 1u : 0u, mbar);
-    }
+    const Run q = join<CUTS>(before, mine);
+    for (int i = 0; i < cs; ++i)
+      send(in_cta(slot(at.rank), i), make_float4(q.P.x, q.P.y, q.H.x, q.H.y), in_cta(&s.full[half], i));
   }
   if (!at.lost) at.lost = !wait_runs(smem_u32(&s.full[half]), k >> 1 & 1);
 #pragma unroll 4
@@ -591,11 +589,11 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
       for (int i = 0; i < kForwardRun; ++i)
         if (i >= n) f[i] = dup(1.f), u[i] = dup(0.f);
     }
-    Run q{f[0], u[0], CUTS && cut != 0};
+    Run q{f[0], u[0]};
     if (CUTS && cut) {
 #pragma unroll
       for (int i = 1; i < kForwardRun; ++i) q.H = cut >> i & 1 ? u[i] : fma2(f[i], q.H, u[i]);
-      q.P = dup(0.f);
+      q.P = dup(kCut);
     } else {
 #pragma unroll
       for (int i = 1; i < kForwardRun; ++i) q.P = mul2(q.P, f[i]), q.H = fma2(f[i], q.H, u[i]);
@@ -821,7 +819,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
     __syncwarp();  // dy is here, and the next inputs go where these were read
     fetch(count(t0 - tokens));
     // dh_i = dy_i + f dd with f and dd those of token i + 1
-    Run q{dup(1.f), dup(0.f), CUTS && cut != 0};
+    Run q{dup(1.f), dup(0.f)};
     float2 ff = dup(0.f), dd = dup(0.f);
     if (n == kSeg && !(CUTS && cut)) {
 #pragma unroll
@@ -836,6 +834,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
         }
     }
     q.H = mul2(ff, dd);
+    if (CUTS && cut) q.P = dup(kCut);
     dd = compose<CUTS, sizeof(Runs) + kWarps * (kStage + kOut)>(runs, step, at, q, v), ff = dup(1.f);
     if (n > 0) {
       E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
