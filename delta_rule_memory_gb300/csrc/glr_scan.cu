@@ -15,14 +15,14 @@
 // fixed by the sizes.
 //
 // What bounds it (8 x 4096 x 1920 in bf16, one GB300): the forward moves 8 bytes an
-// element and takes 117 us, 64% of the measured copy bandwidth; its walk over
-// memory alone takes 84 us, and without the exchange of runs it takes 108.  An
-// element pair costs about 62 instructions, ten of them special functions, and
-// 128 registers a thread leave four warps to an SM's scheduler, which issues in
-// 59% of the cycles: latency between dependent instructions, not memory, is
-// what is left.  Runs of 8 tokens in 64 to 80 registers have more warps, but
-// exchange twice as often: 125 us.  The backward (14.5 bytes) takes 210 us (64%)
-// for the same reason, at 1.8 times the instructions.
+// element and takes 106.5 us, 70% of the measured copy bandwidth; its walk over
+// memory alone takes 84 us.  A pair of channels costs 72 instructions, ten of them
+// special functions, and 128 registers a thread leave four warps to an SM's
+// scheduler, which issues in 62% of the cycles: latency between dependent
+// instructions and in the exchange of runs, not memory, is what is left.  Runs of 8
+// tokens in 96 registers have more warps, but exchange twice as often: 108.5 us,
+// and 304 in place of 215 for one sequence of 32768 x 3840.  The backward (14.5
+// bytes) takes 201 us (67%) for the same reason, at 1.8 times the instructions.
 #include <initializer_list>
 #include <type_traits>
 
@@ -306,8 +306,8 @@ struct Walk {
 // ---- the composition of runs ----
 // A run maps v to P v + H.  A run with a reset does not depend on v at all, not
 // even where v is NaN: its P is -0, which no product of decays is.  (A flag of its
-// own beside P and H, stored, sent and tested apart, took the backward of 2 x 8192 x 3840
-// from OLD us to NEW.)
+// own beside P and H, stored, sent and tested apart, held the exchange up: the backward of
+// 2 x 8192 x 3840 took 285 us with it in place of 232.)
 struct Run {
   float2 P, H;
 };
@@ -501,11 +501,11 @@ __device__ __forceinline__ bool put_codes(const GlrArgs &a, unsigned char *q, ui
 
 // ---- forward ----
 // K8: also the 8-bit checkpoints of x, r and g.  CUTS: with reset flags.
-// 8 x 4096 x 1920 in bf16: 117 us (64% of the measured copy bandwidth); with the
-// carry 120; with checkpoints as well 187 (11.55 bytes an element, 57%: their
+// 8 x 4096 x 1920 in bf16: 106.5 us (70% of the measured copy bandwidth); with the
+// carry 108.5; with checkpoints as well 178 (11.55 bytes an element, 60%: their
 // maxima, codes and exponents nearly double the instructions).  1 x 32768 x 3840, one
-// sequence over clusters of 9: 228 us (65%); 2 x 8192 x 3840 with resets: 133
-// (56%); fp32, 4 x 4096 x 1920: 111 (67%).
+// sequence over clusters of 9: 215 us (69%); 2 x 8192 x 3840 with resets: 116
+// (64%); fp32, 4 x 4096 x 1920: 90 (82%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -705,9 +705,10 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
 // e_t = a_t dh_t, the gradient that reaches h_{t-1}: dh_t = dy_t + e_{t+1}.
 // K8: x, r and g come from their checkpoints.  A run is the 8 tokens between two
 // kept states, so the states inside it are recomputed in registers and cost no
-// memory.  8 x 4096 x 1920 in bf16: 210 us (64% of the measured copy bandwidth),
-// from checkpoints the same (11.55 bytes an element, 51%: decoding replaces the
-// bytes it saves); 1 x 32768 x 3840: 414 (65%); fp32, 4 x 4096 x 1920: 177 (75%).
+// memory.  8 x 4096 x 1920 in bf16: 201 us (67% of the measured copy bandwidth),
+// from checkpoints 207 (11.55 bytes an element, 52%: decoding takes the time of the
+// bytes it saves); 1 x 32768 x 3840: 396 (68%); 2 x 8192 x 3840 with resets: 228
+// (59%); fp32, 4 x 4096 x 1920: 156 (85%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -843,8 +844,8 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
       E *dx = static_cast<E *>(a.dx) + out, *dr = static_cast<E *>(a.dr) + out, *dg = static_cast<E *>(a.dg) + out;
       uint32_t o = 2 * lane * static_cast<uint32_t>(sizeof(E)) + (kSeg - 1) * out_row;
       float2 part = dup(0.f);
-      // `whole`: all 8 tokens exist (a run's only test of n then: 220 us in place
-      // of 210 with one per token)
+      // `whole`: all 8 tokens exist (a run's only test of n then; with one
+      // per token 8 x 4096 x 1920 took 10 us more)
       auto put = [&](auto whole) {
 #pragma unroll
         for (int i = kSeg - 1; i >= 0; --i, o -= out_row) {
@@ -957,8 +958,10 @@ constexpr size_t backward_smem(bool keep8) {
 // once, however few CTAs an SM has (it then waits for memory and for the runs of others);
 // beyond that, between the grid's share of the GPU and whole waves of it times as long.
 // Clusters of more than two CTAs find room on 148 of the 152 SMs.  Measured for 8 x 4096 x 1920
-// in bf16, forward: 127 us with 2 CTAs (79% of one wave), 136 with 3 (two
-// waves), 115 with 4, 127 with 5; 1 x 32768 x 3840: 250 with 8, 229 with 9.
+// in bf16, forward: 125 us with 2 CTAs (81% of one wave), 134 with 3, 117 with 4, 125
+// with 5, 122 with 6, 120 with 8, 136 with 9; backward: 220, 255, 208, 231, 220, 222 and 228;
+// 1 x 32768 x 3840, forward: 250 with 8, 229 with 9.  (Today's kernels are about 8%
+// faster at each.)
 int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
   const int64_t columns = static_cast<int64_t>(B) * ((D + kChan - 1) / kChan);
   const int tile = run * kWarps;
