@@ -204,12 +204,13 @@ __device__ __forceinline__ int load_len(const GlrArgs &a, int b) {
 // ---- a warp's tokens in shared memory ----
 // 8 rows of 64 channels of I (an activation type, or int8 codes).  A warp
 // copies and reads its own rows only, so no CTA barrier guards them.  VEC: rows
-// are 16-byte aligned in global memory and dense here.  Else 16- and 8-bit rows
-// are copied by the 4-byte words that hold them, one word more than they fill.
+// are 16-byte aligned in global memory and dense here.  Else they are copied by the
+// aligned 16 bytes that hold them, one piece more than they fill.
 template <class I, bool VEC>
 struct Rows {
-  static constexpr int kRow = kChan * static_cast<int>(sizeof(I)) + (VEC || sizeof(I) == 4 ? 0 : 8);
+  static constexpr int kRow = kChan * static_cast<int>(sizeof(I)) + (VEC ? 0 : 16);
   static constexpr int kBytes = kSeg * kRow;
+  static_assert(kBytes % 128 == 0, "the next rows begin on 128 bytes");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
@@ -217,36 +218,31 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
 }
 
 // A walk over one [tokens, channels] tensor: a warp copies 8 rows at a time and
-// moves on by multiples of 8, so a row's place in its first 4-byte word depends
-// on its place among the 8 only.  VEC: 16 bytes a copy, zeros behind the last
-// channel.
+// moves on by multiples of 16 bytes, so a row's place in its first piece depends
+// on its place among the 8 only.  VEC: zeros behind the last channel.
 template <class I, bool VEC>
 struct Walk {
   static constexpr int kEs = static_cast<int>(sizeof(I)), kRow = Rows<I, VEC>::kRow;
-  static constexpr int kPer = VEC ? kRow / 16 : 1;   // copies a row
-  static constexpr int kRows = VEC ? 32 / kPer : 1;  // rows a copy of the warp
+  static constexpr int kPer = kChan * kEs / 16;  // pieces a row
+  static constexpr int kRows = 32 / kPer;        // rows a copy of the warp
   static_assert(kSeg % kRows == 0, "a copy of the warp holds whole rows of a run");
-  const char *p;    // the first row's first channel of the warp, the same in every lane
-  uint32_t row;     // bytes between rows
-  uint32_t at;      // VEC: this lane's part of a copy, behind p
-  int row0, bytes;  // VEC: its row of a copy and its bytes; else the warp's channels
+  const char *p;   // the first row's first channel of the warp, the same in every lane
+  uint32_t row;    // bytes between rows
+  uint32_t at;     // this lane's part of a copy, behind p
+  int row0, part;  // its row of a copy, and where its piece lies in that row
+  int left;        // VEC: its piece's bytes; else the warp's channels
 
   // `chan` channels exist
   __device__ __forceinline__ Walk(const I *first, int64_t ld, int chan, int lane) {
     row = static_cast<uint32_t>(ld) * kEs;
     p = reinterpret_cast<const char *>(first);
-    if (VEC) {
-      const int left = chan * kEs - 16 * (lane % kPer);
-      bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-      row0 = lane / kPer;
-      at = row0 * row + (bytes > 0 ? 16 * (lane % kPer) : 0);
-    } else {
-      row0 = 0, at = 0, bytes = chan;
-    }
+    row0 = lane / kPer, part = 16 * (lane % kPer), left = chan;
+    if (VEC) left = max(0, min(16, chan * kEs - part));
+    at = row0 * row + (VEC && left == 0 ? 0 : part);
   }
-  // how far behind a 4-byte boundary row i begins
+  // how far behind a 16-byte boundary row i begins
   __device__ __forceinline__ uint32_t offset(int i) const {
-    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) + i * row) & 3u;
+    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) + i * row) & 15u;
   }
   // start copying rows [0, n)
   __device__ __forceinline__ void copy(unsigned char *dst, int n, int lane) const {
@@ -254,26 +250,22 @@ struct Walk {
       const uint32_t d = smem_u32(dst) + lane * 16;
       if (n == kSeg) {
 #pragma unroll
-        for (int k = 0; k < kSeg / kRows; ++k) cp16(d + k * 512, p + (at + k * kRows * row), bytes);
+        for (int k = 0; k < kSeg / kRows; ++k) cp16(d + k * 512, p + (at + k * kRows * row), left);
       } else {
 #pragma unroll
         for (int k = 0; k < kSeg / kRows; ++k)
-          if (row0 + k * kRows < n) cp16(d + k * 512, p + (at + k * kRows * row), bytes);
+          if (row0 + k * kRows < n) cp16(d + k * 512, p + (at + k * kRows * row), left);
       }
     } else {
-      // the words of each row, whole ones of the allocation at either end
-      constexpr int kWords = kRow / 4;
+      // pieces that hold a byte of the row at least, so they are the allocation's
+      // own (whole ones: it begins on 16 bytes and ends in none of another's)
+      auto piece = [&](int i, int behind, const char *q) {
+        const uint32_t o = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q)) & 15u;
+        if (i < n && behind < static_cast<int>(o) + left * kEs) cp16(smem_u32(dst) + i * kRow + behind, q - o, 16);
+      };
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i) {
-        if (i < n) {
-          const uint32_t o = offset(i);
-          const char *q = p + i * row - o;
-          const int words = (o + bytes * kEs + 3) / 4;
-#pragma unroll
-          for (int w = 0; w < kWords; w += 32)
-            if (w + lane < words) cp_async<4>(dst + i * kRow + 4 * (w + lane), q + 4 * (w + lane));
-        }
-      }
+      for (int k = 0; k < kSeg / kRows; ++k) piece(row0 + k * kRows, part, p + (at + k * kRows * row));
+      if (lane < kSeg) piece(lane, 16 * kPer, p + (lane * row + 16 * kPer));
     }
   }
   __device__ __forceinline__ void move(int rows) { p += static_cast<int64_t>(rows) * row; }
@@ -287,15 +279,18 @@ struct Walk {
       const uint32_t o = offset(i) + 2 * kEs * lane;
       const uint32_t *w = reinterpret_cast<const uint32_t *>(rows + i * kRow) + o / 4;
       const uint32_t v = __funnelshift_r(w[0], w[1], 8 * (o & 3u));
-      return 2 * lane >= bytes ? 0u : 2 * lane + 1 >= bytes ? v & ((1u << (8 * kEs)) - 1u) : v;
+      return 2 * lane >= left ? 0u : 2 * lane + 1 >= left ? v & ((1u << (8 * kEs)) - 1u) : v;
     }
   }
   // the pair's values (activations)
   __device__ __forceinline__ float2 pair(const unsigned char *rows, int i, int lane) const {
     if constexpr (kEs == 4) {
-      const float2 v = *reinterpret_cast<const float2 *>(rows + i * kRow + lane * 8);
-      if constexpr (VEC) return v;
-      else return make_float2(2 * lane < bytes ? v.x : 0.f, 2 * lane + 1 < bytes ? v.y : 0.f);
+      if constexpr (VEC) {
+        return *reinterpret_cast<const float2 *>(rows + i * kRow + lane * 8);
+      } else {
+        const float *v = reinterpret_cast<const float *>(rows + i * kRow + offset(i)) + 2 * lane;
+        return make_float2(2 * lane < left ? v[0] : 0.f, 2 * lane + 1 < left ? v[1] : 0.f);
+      }
     } else {
       const uint32_t u = bits(rows, i, lane);
       return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
