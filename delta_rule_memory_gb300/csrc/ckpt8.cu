@@ -61,7 +61,14 @@ struct Raw<uint16_t> {
     return max(t & 0xffff0000u, t << 16);
   }
 };
+// one 32-byte store where p allows it: two of 16 bytes write every sector in halves
 __device__ __forceinline__ void store8(float *p, const Eight &e) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(e.v[0]), "f"(e.v[1]),
+                 "f"(e.v[2]), "f"(e.v[3]), "f"(e.v[4]), "f"(e.v[5]), "f"(e.v[6]), "f"(e.v[7])
+                 : "memory");
+    return;
+  }
   *reinterpret_cast<float4 *>(p) = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
   *reinterpret_cast<float4 *>(p + 4) = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
 }
