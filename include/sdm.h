@@ -515,6 +515,7 @@ SDM_API int sse_scan(float *state, const float *route_logits, int topk, const fl
  *            are contiguous; token t of sequence b starts ld * (b T + t)
  *            elements behind the pointer, with its own ld >= D for each of the
  *            three, so they may be column slices of one projection's output.
+ *            (Rows are read by the aligned 16 bytes that hold their elements.)
  * rate     : fp32 [D], >= 0 and finite; any other value counts as 0 and sets
  *            SDM_DEVERR_RATE.
  * reset    : optional uint8 [B,T]; where it is not 0, h_{t-1} is taken as 0 (a

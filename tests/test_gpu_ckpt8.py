@@ -79,6 +79,28 @@ def test_values_that_are_not_finite(bad, dt):
         assert np.array_equal(sdm.ckpt8_unpack(codes, exps, to).double().cpu().numpy(), ref.unpack8(q, e), equal_nan=True)
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_rows_at_every_boundary(dt):
+    """Rows that begin anywhere among 32 bytes: what lies between them stays out and is left alone."""
+    sdm = need_gpu()
+    rows, D = 9, 72
+    v = _values(rows, D, 3).to(dt)
+    q, e = ref.pack8(v.double().cpu().numpy())
+    want = ref.unpack8(q, e)
+    for shift in range(17):
+        for ld in (72, 73, 76, 80, 88):
+            buf = torch.full((shift + rows * ld + 1,), float("nan"), dtype=dt, device="cuda")
+            x = torch.as_strided(buf, (rows, D), (ld, 1), shift)
+            x.copy_(v)
+            codes, exps = sdm.ckpt8_pack(x)
+            assert np.array_equal(host(codes), q) and np.array_equal(host(exps), e)
+            buf.fill_(3.0)
+            sdm.ckpt8_unpack(codes, exps, dt, x=x)
+            assert np.array_equal(x.double().cpu().numpy(), want)
+            x.fill_(3.0)
+            assert torch.all(buf == 3.0)
+
+
 def test_shapes_and_refusals():
     sdm = need_gpu()
     x = torch.randn((2, 3, 5, 70), device="cuda")

@@ -295,6 +295,38 @@ def test_many_short_sequences(dt):
     check_backward(sdm, c, f, carry, None)
 
 
+def _apart(t, shift, ld):
+    """t's rows at `ld` elements, the first `shift` elements into a buffer of NaN."""
+    B, T, D = t.shape
+    buf = torch.full((shift + B * T * ld + 1,), float("nan"), dtype=t.dtype, device="cuda")
+    v = torch.as_strided(buf, (B, T, D), (T * ld, ld, 1), shift)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 70, 131])
+def test_rows_at_every_boundary(D, dt):
+    """Inputs and gradients that begin anywhere among 16 bytes, at odd and even
+    distances, between NaNs: the bits of the contiguous call."""
+    sdm = need_gpu()
+    c = Case(2, 75, D, dt, seed=23)
+    s0 = c.h0.clone()
+    y0, carry0, ckpt0 = sdm.glr_scan_train(s0, *c.args(), keep8=True)
+    ds0 = c.dhT.clone()
+    want = sdm.glr_scan_backward(ds0, *c.args(), carry0, c.dy)
+    for shift, more in [(0, 1), (1, 2), (2, 3), (3, 5), (4, 8), (5, 16 - D % 16), (6, 6), (7, 9), (8, 24 - D % 8)]:
+        x, r, g = _apart(c.x, shift, D + more), _apart(c.r, shift + 1, D + more + 1), _apart(c.g, 2 * shift, D + 2 * more)
+        s = c.h0.clone()
+        assert torch.equal(sdm.glr_scan(s, x, r, g, c.rate), y0) and torch.equal(s, s0)
+        y, carry, ckpt = sdm.glr_scan_train(c.h0.clone(), x, r, g, c.rate, keep8=True)
+        assert torch.equal(y, y0) and torch.equal(carry, carry0)
+        assert torch.equal(ckpt[0], ckpt0[0]) and torch.equal(ckpt[1], ckpt0[1])
+        ds, grads = c.dhT.clone(), [_apart(torch.zeros_like(c.x), shift + i, D + more) for i in range(3)]
+        out = sdm.glr_scan_backward(ds, x, r, g, c.rate, carry, c.dy, grads=grads)
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(ds, ds0)
+
+
 def test_one_tensor_as_several_inputs_and_a_state_that_is_kept():
     sdm = need_gpu()
     c = Case(2, 40, 64, "bf16", seed=20)
