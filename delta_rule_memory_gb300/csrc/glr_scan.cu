@@ -257,8 +257,8 @@ struct Walk {
           if (row0 + k * kRows < n) cp16(d + k * 512, p + (at + k * kRows * row), left);
       }
     } else {
-      // pieces that hold a byte of the row at least, so they are the allocation's
-      // own (whole ones: it begins on 16 bytes and ends in none of another's)
+      // only pieces that hold a byte of the row: allocations begin on 16 bytes and
+      // more, so such a piece never reaches into unmapped memory
       auto piece = [&](int i, int behind, const char *q) {
         const uint32_t o = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q)) & 15u;
         if (i < n && behind < static_cast<int>(o) + left * kEs) cp16(smem_u32(dst) + i * kRow + behind, q - o, 16);
