@@ -991,16 +991,27 @@ int backward_cluster(int B, int T, int D, int dtype) {
 bool rows_vec(const void *p, int64_t ld, int es) { return aligned(p, 16) && ld * es % 16 == 0; }
 bool pairs_vec(const void *p, int64_t ld, int es) { return aligned(p, 2 * es) && ld % 2 == 0; }
 
+// A call that CUDA refused, taken off the thread's own record too: it is not the next launch's.
+int refused(const char *fn, cudaError_t e) {
+  cudaGetLastError();
+  return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+// layout: the kernel's shared memory without its cluster's runs.  The limit that
+// is set is the kernel's, for the largest cluster, and not the call's: between
+// here and the launch another thread's call of the same kernel may set it too.
 template <class K>
-int launch(const char *fn, K kernel, size_t smem, const GlrArgs &a, cudaStream_t st) {
+int launch(const char *fn, K kernel, size_t layout, const GlrArgs &a, cudaStream_t st) {
+  const size_t smem = layout + cluster_bytes(a.cs);
   cudaError_t e;
   if (smem > 48 << 10) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(layout + cluster_bytes(kMaxCluster)));
+    if (e != cudaSuccess) return refused(fn, e);
   }
   if (a.cs > 8) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    if (e != cudaSuccess) return refused(fn, e);
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((a.D + kChan - 1) / kChan * a.cs, a.B);
@@ -1013,8 +1024,7 @@ int launch(const char *fn, K kernel, size_t smem, const GlrArgs &a, cudaStream_t
   cfg.attrs = &at;
   cfg.numAttrs = a.cs > 1 ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-  return check_launch(fn);
+  return e == cudaSuccess ? SDM_OK : refused(fn, e);
 }
 
 // Up to kStepTokens tokens and nothing to keep: one thread walks them all.
@@ -1033,7 +1043,7 @@ int launch_step(const char *fn, const GlrArgs &a, cudaStream_t st) {
 
 template <class E, bool VEC>
 int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = cluster_bytes(a.cs) + forward_smem<E, VEC>();
+  const size_t smem = forward_smem<E, VEC>();
   if (a.reset)
     return a.codes ? launch(fn, glr_forward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_forward_kernel<E, VEC, false, true>, smem, a, st);
@@ -1042,7 +1052,7 @@ int launch_forward(const char *fn, const GlrArgs &a, cudaStream_t st) {
 }
 template <class E, bool VEC>
 int launch_backward(const char *fn, const GlrArgs &a, cudaStream_t st) {
-  const size_t smem = cluster_bytes(a.cs) + backward_smem<E, VEC>(a.codes != nullptr);
+  const size_t smem = backward_smem<E, VEC>(a.codes != nullptr);
   if (a.reset)
     return a.codes ? launch(fn, glr_backward_kernel<E, VEC, true, true>, smem, a, st)
                    : launch(fn, glr_backward_kernel<E, VEC, false, true>, smem, a, st);
