@@ -10,6 +10,12 @@ namespace sdm {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// Shared memory that a CTA may have on sm_103a.  A kernel whose need depends on
+// the call gets this as its limit in every call: the limit belongs to the kernel,
+// so one that followed the call's own need could be lowered by another thread's
+// call before the launch.
+constexpr int kMaxSmem = 227 << 10;
+
 // Set the thread-local error text (abi.cu) and return `code`.
 int set_error(int code, const char *fmt, ...);
 // Check the last launch; on failure record the CUDA error text.

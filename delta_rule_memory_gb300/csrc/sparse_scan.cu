@@ -470,8 +470,7 @@ int launch_scan(const ScanArgs &args, int wpc, cudaStream_t st) {
   const size_t smem = ScanLayout<P, SLOTS, TW>::kWarpBytes * wpc;
   auto kern =
       args.undo ? sparse_scan_kernel<P, SLOTS, TW, MODE, true> : sparse_scan_kernel<P, SLOTS, TW, MODE, false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
     return check_launch("sdm_scan: set shared memory");
   const long blocks = (args.total_warps + wpc - 1) / wpc;
   kern<<<static_cast<unsigned>(blocks), wpc * 32, smem, st>>>(args);

@@ -489,7 +489,7 @@ extern "C" int sse_scan(float *state, const float *route_logits, int topk, const
   args.rw = rec_words(topk);
   args.mode = write_mode;
   auto kern = write_mode == SSE_WRITE_DELTA ? sse_scan_kernel<SSE_WRITE_DELTA> : sse_scan_kernel<SSE_WRITE_ADDITIVE>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
     return check_launch("sse_scan: set shared memory");
   const long blocks = static_cast<long>(B) * H * args.tiles;
   kern<<<static_cast<unsigned>(blocks), kSseThreads, smem, st>>>(args);

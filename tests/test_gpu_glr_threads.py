@@ -120,3 +120,74 @@ def test_a_refused_launch_is_not_the_next_call_s_error():
     accepted(sdm, c.call(torch.cuda.current_stream().cuda_stream))
     torch.cuda.synchronize()
     assert c.right()
+
+
+class SparseScan:
+    """An sdm_scan call on buffers of its own, B H sequences of two tokens."""
+
+    def __init__(self, sdm, B, H, seed, N=64, T=2, W=4, dv=64):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        n = lambda *s: torch.rand(s, generator=gen, device="cuda")  # noqa: E731
+        idx = [n(B, T, H, N).argsort(-1)[..., :W].to(torch.int32).contiguous() for _ in range(2)]
+        w = [n(B, T, H, W) / W for _ in range(2)]
+        self.sdm, self.sizes = sdm, (B, T, H, N, dv)
+        self.args = (n(B, T, H, dv), n(B, T, H), n(B, T, H), idx[0], w[0], idx[1], w[1])
+        self.start = n(B, H, N, dv)
+        self.state, self.want_state = self.start.clone(), self.start.clone()
+        self.want = sdm.sdm_scan(self.want_state, *self.args)
+        self.y = torch.empty_like(self.want)
+        self.ws = torch.empty(sdm.sdm_scan_workspace_size(B, T, H, W, W), dtype=torch.uint8, device="cuda")
+
+    def call(self, stream):
+        v, al, be, iw, ww, ir, wr = (t.data_ptr() for t in self.args)
+        W = self.args[3].shape[-1]
+        return self.sdm.lib().sdm_scan(self.state.data_ptr(), v, self.sdm.SDM_DTYPE_F32, al, be, iw, ww, W, ir, wr, W,
+                                       *self.sizes, self.sdm.SDM_RESID_SHARED, self.y.data_ptr(), self.ws.data_ptr(),
+                                       self.ws.numel(), None, stream)
+
+    def right(self):
+        self.state.copy_(self.start)        # the loops went on with the state
+        accepted(self.sdm, self.call(torch.cuda.current_stream().cuda_stream))
+        return torch.equal(self.y, self.want) and torch.equal(self.state, self.want_state)
+
+
+class SseScan(SparseScan):
+    """An sse_scan call, token by token, N + 1 partitions in shared memory."""
+
+    def __init__(self, sdm, N, seed, B=1, T=3, H=2, c=128, d=32, topk=2):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        n = lambda *s: torch.rand(s, generator=gen, device="cuda")  # noqa: E731
+        self.sdm, self.sizes, self.topk = sdm, (B, T, H, N, c, d), topk
+        self.args = (n(B, T, H, N), n(B, T, H, c), n(B, T, H, c).bfloat16(), n(B, T, H, d).bfloat16(), n(B, T, H, c))
+        self.start = n(B, H, N + 1, c, d)
+        self.state, self.want_state = self.start.clone(), self.start.clone()
+        self.want = sdm.sse_scan(self.want_state, self.args[0], topk, *self.args[1:])
+        self.y = torch.empty_like(self.want)
+        self.ws = torch.empty(sdm.sse_scan_workspace_size(B, T, H, N, topk, c, d), dtype=torch.uint8, device="cuda")
+
+    def call(self, stream):
+        logits, k, q, v, al = (t.data_ptr() for t in self.args)
+        return self.sdm.lib().sse_scan(self.state.data_ptr(), logits, self.topk, k, q, v, al, self.sdm.SSE_WRITE_ADDITIVE,
+                                       *self.sizes, self.y.data_ptr(), None, self.ws.data_ptr(), self.ws.numel(), None,
+                                       stream)
+
+
+@pytest.mark.parametrize("kind,a,b", [(SparseScan, (8, 16), (10, 20)), (SseScan, (4,), (12,))], ids=["sdm", "sse"])
+def test_threads_with_scans_of_other_sizes(kind, a, b):
+    """sdm_scan with 128 and 200 (batch, head) pairs: 512 and 800 warps, which fit
+    the GPU at once with four and with two of them a CTA.  sse_scan with
+    tables of 5 and 13 partitions.  (Between setting a limit of the call's own
+    and the launch there are few instructions: one call in 48,000 was refused.)"""
+    sdm = need_gpu()
+    calls = [kind(sdm, *(b if i % 2 else a), i) for i in range(6)]
+
+    def work(c):
+        def run(stream):
+            for i in range(8000):
+                if i % 200 == 0:        # no thread waits long for room in its stream's queue
+                    torch.cuda.ExternalStream(stream).synchronize()
+                accepted(sdm, c.call(stream))
+        return run
+
+    assert not in_threads(*(work(c) for c in calls))
+    assert all(c.right() for c in calls)
