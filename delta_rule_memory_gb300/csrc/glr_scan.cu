@@ -121,26 +121,28 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 }
 
 // The decay a = e^-y, y = rate sigmoid(r), and m2 = 1 - a^2 = (1 - a) (2 - (1 - a)),
-// both from e = 1 - a.  Near a = 1 the exponential unit cannot give e (the difference
+// from e = 1 - a.  Near a = 1 the exponential unit cannot give e (the difference
 // cancels, and its results near 1 are cut off, not rounded: a bias of 2^-25, which a
 // horizon of 1 / e tokens multiplies; sums of gradients lost a digit to it).
 // So up to y = 0.15, e = y q(y) with q the cubic next to (1 - e^-y) / y there (by
-// linear programming, q(0) = 1): off by 5e-8 at most.  Beyond, horizons are of a
-// few tokens and the unit's bias counts for little.
-// a is off by 2^-25 at most by taking it as 1 - e, which below 1/2 is more than a
-// relative rounding, and nothing next to an input of the same token.
+// linear programming, q(0) = 1): off by 5e-8 at most, and a = 1 - e.  Beyond, horizons
+// are of a few tokens and the unit's bias counts for little; a is its result itself,
+// which keeps a's relative precision however small a is: dr and drate are
+// proportional to it, and so is y where a token has no input.
 struct Decay {
   float2 a, m2;
 };
 __device__ __forceinline__ Decay decay(float2 y) {
   const float2 l = mul2(y, dup(-kLog2e));
-  const float2 far = fma2(make_float2(ex2(l.x), ex2(l.y)), dup(-1.f), dup(1.f));
+  const float2 far = make_float2(ex2(l.x), ex2(l.y)), rest = fma2(far, dup(-1.f), dup(1.f));
   float2 q = fma2(y, dup(-0.0393375196f), dup(0.166465417f));
   q = fma2(y, q, dup(-0.499995023f));
   q = fma2(y, q, dup(1.f));
   q = mul2(y, q);
-  const float2 e = make_float2(y.x <= 0.15f ? q.x : far.x, y.y <= 0.15f ? q.y : far.y);
-  return Decay{fma2(e, dup(-1.f), dup(1.f)), mul2(e, fma2(e, dup(-1.f), dup(2.f)))};
+  const float2 near = fma2(q, dup(-1.f), dup(1.f));
+  const bool x = y.x <= 0.15f, z = y.y <= 0.15f;
+  const float2 e = make_float2(x ? q.x : rest.x, z ? q.y : rest.y);
+  return Decay{make_float2(x ? near.x : far.x, z ? near.y : far.y), mul2(e, fma2(e, dup(-1.f), dup(2.f)))};
 }
 // 1 / sqrt(m2), and 0 where m2 underflows
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
