@@ -120,8 +120,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
   return make_float2(rcp(d.x), rcp(d.y));
 }
 
-// The decay a = e^-y, y = rate sigmoid(r), and m2 = 1 - a^2 = (1 - a) (2 - (1 - a)),
-// from e = 1 - a.  Near a = 1 the exponential unit cannot give e (the difference
+// The decay a = e^-y, y = rate sigmoid(r), and e = 1 - a, of which m^2 = 1 - a^2 =
+// e (2 - e) is made.  Near a = 1 the exponential unit cannot give e (the difference
 // cancels, and its results near 1 are cut off, not rounded: a bias of 2^-25, which a
 // horizon of 1 / e tokens multiplies; sums of gradients lost a digit to it).
 // So up to y = 0.15, e = y q(y) with q the cubic next to (1 - e^-y) / y there (by
@@ -130,7 +130,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 // which keeps a's relative precision however small a is: dr and drate are
 // proportional to it, and so is y where a token has no input.
 struct Decay {
-  float2 a, m2;
+  float2 a, e;
 };
 __device__ __forceinline__ Decay decay(float2 y) {
   const float2 l = mul2(y, dup(-kLog2e));
@@ -141,20 +141,29 @@ __device__ __forceinline__ Decay decay(float2 y) {
   q = mul2(y, q);
   const float2 near = fma2(q, dup(-1.f), dup(1.f));
   const bool x = y.x <= 0.15f, z = y.y <= 0.15f;
-  const float2 e = make_float2(x ? q.x : rest.x, z ? q.y : rest.y);
-  return Decay{make_float2(x ? near.x : far.x, z ? near.y : far.y), mul2(e, fma2(e, dup(-1.f), dup(2.f)))};
+  return Decay{make_float2(x ? near.x : far.x, z ? near.y : far.y), make_float2(x ? q.x : rest.x, z ? q.y : rest.y)};
 }
 // 1 / sqrt(m2), and 0 where m2 underflows
 __device__ __forceinline__ float inv_m(float m2) { return m2 >= 1.17549435e-38f ? rsq(m2) : 0.f; }
+__device__ __forceinline__ float at_most(float v, float top) {  // NaN stays NaN
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(v), "f"(top));
+  return m;
+}
 // m sigmoid(g) x with one special function less than its factors take: sigmoid(g)
-// = 1 / d, d = 1 + e^-g, so m / d = m2 / sqrt(d^2 m2).  The number added to m2 keeps
-// the root's inverse finite at m2 = 0 and is lost in it from 2^-100 on.  (8 x 4096 x
-// 1920 on one CTA a column: 127 us, and 138 with the reciprocal of d by itself.)
-__device__ __forceinline__ float2 input_term(float2 m2, float2 g, float2 x) {
-  const float2 z = mul2(g, dup(-kLog2e));
-  const float2 d = add2(make_float2(ex2(z.x), ex2(z.y)), dup(1.f));
-  const float2 q = mul2(mul2(d, d), add2(m2, dup(1.17549435e-38f)));
-  return mul2(mul2(m2, x), make_float2(rsq(q.x), rsq(q.y)));
+// = w / d with w = e^g and d = 1 + w, and m / d = m2 / sqrt(d^2 m2).  From g = 26 on
+// sigmoid(g) is 1 in fp32, so g is stopped there and d^2 stays in range; a small w
+// keeps its digits down to e^-87.  m2 comes times 2^12, and times 2^24 under the
+// root, which keeps the root's digits down to m2 = 2^-126; the number added there
+// keeps its inverse finite at m2 = 0.  x comes last: nothing but the term itself
+// overflows.  (With 1 / d from e^-g, three instructions less a pair of channels, the
+// term was 0 from g = -44 on: 8 x 4096 x 1920 took 107.3 us in place of 110.6.)
+__device__ __forceinline__ float2 input_term(float2 e, float2 g, float2 x) {
+  const float2 z = mul2(make_float2(at_most(g.x, 26.f), at_most(g.y, 26.f)), dup(kLog2e));
+  const float2 w = make_float2(ex2(z.x), ex2(z.y)), d = add2(w, dup(1.f));
+  const float2 m2 = mul2(e, fma2(e, dup(-4096.f), dup(8192.f)));
+  const float2 q = mul2(mul2(d, d), fma2(m2, dup(4096.f), dup(1.17549435e-38f)));
+  return mul2(mul2(mul2(w, m2), make_float2(rsq(q.x), rsq(q.y))), x);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float2 v) {  // nearest even, v.x in the lower half
@@ -566,7 +575,7 @@ __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
         const float2 g = wg.template pair<K8>(d + 2 * kBytes, i, lane);
         const Decay q = decay(mul2(rate, sigmoid2(r)));
         f[kSeg * half + i] = q.a;
-        u[kSeg * half + i] = input_term(q.m2, g, x);
+        u[kSeg * half + i] = input_term(q.e, g, x);
         if (K8) {
           // a code goes where the token's inputs were: every lane's are in the maximum below, so they have been read
           const float2 in[3] = {x, r, g};
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
       const int k = N > 1 ? j + 1 : j;
       const float2 sr = sigmoid2(make_float2(widen(r.v[j]), widen(r.v[k])));
       const Decay q = decay(mul2(make_float2(rate[j], rate[k]), sr));
-      const float2 u = input_term(q.m2, make_float2(widen(g.v[j]), widen(g.v[k])),
+      const float2 u = input_term(q.e, make_float2(widen(g.v[j]), widen(g.v[k])),
                                   make_float2(widen(x.v[j]), widen(x.v[k])));
       const float2 n = cut ? u : fma2(q.a, make_float2(h[j], h[k]), u);
       h[j] = n.x;
@@ -807,7 +816,7 @@ __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) 
       const float2 x = input(wx, 0, i), sr = sigmoid2(input(wr, 1, i)), sg = sigmoid2(input(wg, 2, i));
       const Decay q = decay(mul2(rate, sr));
       f[i] = q.a;
-      const float2 m2 = q.m2;
+      const float2 m2 = mul2(q.e, fma2(q.e, dup(-1.f), dup(2.f)));
       const float2 rs = make_float2(inv_m(m2.x), inv_m(m2.y));
       const float2 sx = mul2(sg, x), m = mul2(m2, rs);
       cx[i] = mul2(m, sg);

@@ -1,5 +1,6 @@
-"""The gated linear recurrence where its decays are far below 1, within fp32's
-error relative to the decay itself.
+"""The gated linear recurrence where its factors are small: decays far below 1
+and gates that are nearly closed, within fp32's error relative to each factor
+itself.
 
 Where y = rate sigmoid(r) is above 0.15 the decay is the exponential unit's
 own result: relative error 2^-22 for the unit, 2 E y for the two roundings
@@ -83,6 +84,48 @@ def test_strong_decays_without_input(T, rate, dt):
     c = Case(2, T, 66, dt, seed=32, rate=rate)
     c.x.mul_((torch.arange(66, device="cuda") % 3 == 0) & (torch.arange(T, device="cuda")[:, None] % 4 == 3))
     check(sdm, c)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [1.0, 1e30])
+@pytest.mark.parametrize("T", [5, 100])
+def test_gates_that_are_nearly_closed(T, size, dt):
+    """Input gates of e^-44 to e^-86 into an empty state: the input term is all there is."""
+    sdm = need_gpu()
+    c = Case(2, T, 66, dt, seed=33)
+    c.h0.zero_()
+    c.g.copy_(-44 - 42 * torch.rand(c.g.shape, generator=torch.Generator().manual_seed(1)))
+    c.x.mul_(size)
+    f = c.forward()
+    s = c.h0.clone()
+    y = sdm.glr_scan(s, *c.args())
+    assert torch.all(y[c.x != 0].abs() > 0)
+    assert_within(y, f["y"], f["e_y"], c.dt, "y")
+    assert_within(s, f["hT"], f["e_hT"], torch.float32, "h_T")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_an_infinite_input_at_a_nearly_closed_gate(dt):
+    """m sigmoid(-60) is not 0, so an infinite x stays an infinity of its sign."""
+    sdm = need_gpu()
+    c = Case(1, 40, 64, dt, seed=34)
+    c.g[0, 20] = -60.0
+    c.x[0, 20, :32], c.x[0, 20, 32:] = float("inf"), -float("inf")
+    y = sdm.glr_scan(c.h0.clone(), *c.args())
+    assert torch.all(y[0, 20:, :32] == float("inf")) and torch.all(y[0, 20:, 32:] == -float("inf"))
+    assert torch.isfinite(y[0, :20]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_recurrence_gates_that_are_nearly_closed(dt):
+    """sigmoid(r) down to fp32's smallest normal numbers: m, its root, keeps its digits."""
+    sdm = need_gpu()
+    c = Case(2, 100, 66, dt, seed=35, rate=(0.5, 0.8))
+    c.h0.zero_()
+    c.r.copy_(-60 - 26 * torch.rand(c.r.shape, generator=torch.Generator().manual_seed(2)))
+    f = c.forward()
+    y = sdm.glr_scan(c.h0.clone(), *c.args())
+    assert_within(y, f["y"], f["e_y"], c.dt, "y")
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
