@@ -446,6 +446,7 @@ __device__ __forceinline__ void open_runs(Runs &s, const Place &at) {
     umma::mbar_init(smem_u32(&s.full[1]), 1);
     umma::fence_mbar_init();
   }
+  __syncwarp();  // the barrier is for whole warps (.aligned)
   cluster_arrive();
 }
 __device__ __forceinline__ void close_runs(const Place &at, int32_t *err) {
