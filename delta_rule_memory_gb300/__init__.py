@@ -585,7 +585,9 @@ def _on(index: int, stream):
             here.handle = torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(index)
             return here
     elif not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=index)
+        handle = _stream(stream)
+        # 0 and cudaStreamLegacy are the default stream (ExternalStream(0) is one of torch's pool)
+        stream = torch.cuda.default_stream(index) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=index)
     return _there(index, stream)
 
 
