@@ -588,6 +588,8 @@ def _on(index: int, stream):
         handle = _stream(stream)
         # 0 and cudaStreamLegacy are the default stream (ExternalStream(0) is one of torch's pool)
         stream = torch.cuda.default_stream(index) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream must be of cuda:{index}, the tensors' device, got {stream.device}")
     return _there(index, stream)
 
 

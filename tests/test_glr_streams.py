@@ -47,3 +47,13 @@ def test_other_streams(on):
     with call(0, mine) as handle:
         assert handle == 8192
     assert entered[-1] is mine
+
+
+def test_a_stream_of_another_device_is_refused(on):
+    """The kernel would run there, on this device's addresses."""
+    call, entered = on
+    with pytest.raises(ValueError, match="cuda:0"):
+        call(0, Stream(4096, device=1))
+    with pytest.raises(ValueError, match="cuda:1"):
+        call(1, Stream(4096))
+    assert not entered
