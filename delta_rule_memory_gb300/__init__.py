@@ -640,10 +640,11 @@ def _need(t, name: str, dtype, shape, index: int):
     raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _out(t, name: str, dtype, shape, index: int):
-    """An output the caller gave, checked, or a new one."""
+def _out(t, name: str, dtype, shape, index: int, lens=None):
+    """An output the caller gave, checked, or a new one; with lens, whose calls
+    do not write the rows behind them, a new one of zeros."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=index)
+        return (torch.empty if lens is None else torch.zeros)(shape, dtype=dtype, device=index)
     _need(t, name, dtype, shape, index)
     return t
 
@@ -684,11 +685,12 @@ def glr_scan(state, x, r, g, rate, reset=None, lens=None, y=None, state_out=None
     projection will do); rate: fp32 [D], >= 0; reset: uint8 or bool [B,T], 1
     where a new sequence starts inside a row; lens: int32 [B], tokens that
     exist.  Updates `state` fp32 [B,D] in place, or leaves it and writes
-    `state_out` where that is given.  Returns y [B,T,D] of x's dtype (rows
-    behind lens are not written).  T = 1 is the step of a decoding loop."""
+    `state_out` where that is given.  Returns y [B,T,D] of x's dtype; rows
+    behind lens are 0, or as they were in a `y` that was given.  T = 1 is the
+    step of a decoding loop."""
     B, T, D, shape, dt, dev, lx, lr, lg, reset = _glr_checks(state, x, r, g, rate, reset, lens, dev_err)
     with _on(dev, stream) as st:
-        y = _out(y, "y", dt, shape, dev)
+        y = _out(y, "y", dt, shape, dev, lens)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
         rc = lib().glr_scan(state.data_ptr(), state_out.data_ptr(), x.data_ptr(), lx, r.data_ptr(), lr,
                             g.data_ptr(), lg, _DTYPES[dt], rate.data_ptr(), _ptr(reset), _ptr(lens), B, T, D,
@@ -708,10 +710,11 @@ def glr_scan_train(state, x, r, g, rate, reset=None, lens=None, keep8=False, y=N
     carry fp32 [B,ceil(T/8),D] being the states before every 8th token; with
     keep8 (or ckpt, a pair of buffers) (y, carry, (codes, exps)), the 8-bit
     checkpoints of x, r and g, int8 [3,B,T,D] and uint8 [3,B,T,ceil(D/64)],
-    which the backward takes in place of x, r and g."""
+    which the backward takes in place of x, r and g (their rows behind lens are
+    not written, nor read by the backward)."""
     B, T, D, shape, dt, dev, lx, lr, lg, reset = _glr_checks(state, x, r, g, rate, reset, lens, dev_err)
     with _on(dev, stream) as st:
-        y = _out(y, "y", dt, shape, dev)
+        y = _out(y, "y", dt, shape, dev, lens)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, D), dev)
         carry = _out(carry, "carry", torch.float32, (B, -(-T // 8), D), dev)
         codes = exps = None
@@ -737,7 +740,8 @@ def glr_scan_backward(dstate, x, r, g, rate, carry, dy, reset=None, lens=None, c
     `ckpt` = the (codes, exps) that it returned; dy [B,T,D] of x's dtype.
     `dstate` fp32 [B,D] holds dL/dh_T and becomes dL/dh_0 (or stays, with
     `dstate_out` given).  `grads`: optional (dx, dr, dg) to write, which may be
-    column slices of one buffer.  Returns (dx, dr, dg, drate), drate fp32 [D]."""
+    column slices of one buffer.  Returns (dx, dr, dg, drate), drate fp32 [D];
+    rows of the gradients behind lens are 0, or as they were in given ones."""
     if ckpt is not None and not (x is None and r is None and g is None):
         raise ValueError("give x, r and g or ckpt, not both")
     if ckpt is None and x is None:
@@ -753,7 +757,7 @@ def glr_scan_backward(dstate, x, r, g, rate, carry, dy, reset=None, lens=None, c
         _need(exps, "exps", torch.uint8, (3, B, T, -(-D // 64)), dev)
     with _on(dev, stream) as st:
         if grads is None:
-            dx, dr, dg = [torch.empty(shape, dtype=dt, device=dev) for _ in range(3)]
+            dx, dr, dg = [_out(None, "", dt, shape, dev, lens) for _ in range(3)]
             ld = D
         else:
             dx, dr, dg = grads
