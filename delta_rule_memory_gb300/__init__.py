@@ -632,6 +632,12 @@ def _act(t, name: str, dtype=None, shape=None, index=None) -> int:
     return ld
 
 
+def _int32(*sizes):
+    """Refuse sizes that the C ABI's ints do not hold: ctypes would cut them off."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
+
+
 def _need(t, name: str, dtype, shape, index: int):
     """A contiguous tensor; shape None: any."""
     if isinstance(t, _Tensor) and _plain(t, dtype, t.shape if shape is None else shape, index):
@@ -660,6 +666,7 @@ def _glr_checks(state, x, r, g, rate, reset, lens, dev_err, like=None):
         raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
     dt, dev = first.dtype, first.get_device()
     B, T, D = shape
+    _int32(B, T, D)
     lx = lr = lg = 0
     if x is not None or like is None:
         lx = D if _plain(x, dt, shape, dev) else _act(x, "x", dt, shape, dev)
@@ -792,6 +799,7 @@ def ckpt8_pack(x, codes=None, exps=None, dev_err=None, stream=None):
     ld = _act(x, "x")
     shape, dev = x.shape, x.get_device()
     *rows, D = shape
+    _int32(D)
     if dev_err is not None:
         _need(dev_err, "dev_err", torch.int32, None, dev)
     with _on(dev, stream) as st:
@@ -812,6 +820,7 @@ def ckpt8_unpack(codes, exps, dtype=torch.bfloat16, x=None, stream=None):
     if len(shape) < 1:
         raise ValueError("codes must be [..., D]")
     *rows, D = shape
+    _int32(D)
     _need(exps, "exps", torch.uint8, (*rows, -(-D // 64)), dev)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
