@@ -812,9 +812,10 @@ def ckpt8_pack(x, codes=None, exps=None, dev_err=None, stream=None):
     return codes, exps
 
 
-def ckpt8_unpack(codes, exps, dtype=torch.bfloat16, x=None, stream=None):
+def ckpt8_unpack(codes, exps, dtype=None, x=None, stream=None):
     """The values that a ckpt8_pack checkpoint stands for, as bf16 or fp32
-    (exact in both)."""
+    (exact in both); without `dtype` in the type of `x`, the buffer to write,
+    or in bf16 where none is given."""
     _req(codes, "codes", torch.int8)
     shape, dev = codes.shape, codes.get_device()
     if len(shape) < 1:
@@ -822,6 +823,8 @@ def ckpt8_unpack(codes, exps, dtype=torch.bfloat16, x=None, stream=None):
     *rows, D = shape
     _int32(D)
     _need(exps, "exps", torch.uint8, (*rows, -(-D // 64)), dev)
+    if dtype is None:
+        dtype = x.dtype if isinstance(x, _Tensor) else torch.bfloat16
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
     with _on(dev, stream) as st:
