@@ -45,7 +45,7 @@ constexpr int kMaxCluster = 16;
 constexpr int kSMs = 152;
 constexpr int kSteps = 128;      // bytes of a warp's 24 checkpoint steps, and what keeps its rows on 128
 constexpr int kForwardRegs = 128, kBackwardRegs = 128;  // of a thread
-constexpr uint32_t kWaitPolls = 1u << 20;  // of a cluster's mbarrier, about 0.1 s, before the wait gives up
+constexpr uint32_t kWaitPolls = 1u << 18;  // of a cluster's mbarrier, about 1 s, before the wait gives up
 static_assert(kChan == ckpt8::kGroup, "a warp's channels are one checkpoint group");
 
 struct GlrArgs {
