@@ -153,16 +153,16 @@ __device__ __forceinline__ float at_most(float v, float top) {  // NaN stays NaN
 // m sigmoid(g) x with one special function less than its factors take: sigmoid(g)
 // = w / d with w = e^g and d = 1 + w, and m / d = m2 / sqrt(d^2 m2).  From g = 26 on
 // sigmoid(g) is 1 in fp32, so g is stopped there and d^2 stays in range; a small w
-// keeps its digits down to e^-87.  m2 comes times 2^12, and times 2^24 under the
-// root, which keeps the root's digits down to m2 = 2^-126; the number added there
-// keeps its inverse finite at m2 = 0.  x comes last: nothing but the term itself
-// overflows.  (With 1 / d from e^-g, three instructions less a pair of channels, the
-// term was 0 from g = -44 on: 8 x 4096 x 1920 took 107.3 us in place of 110.6.)
+// keeps its digits down to e^-87.  d comes times 2^6 and m2 times 2^12, which keeps
+// the root's digits down to m2 = 2^-126; the number added under it keeps its inverse
+// finite at m2 = 0.  x comes last: nothing but the term itself overflows.  (With
+// 1 / d from e^-g, two instructions less a pair of channels, the term was 0 from g =
+// -44 on: 8 x 4096 x 1920 took 107.3 us in place of 110.6.)
 __device__ __forceinline__ float2 input_term(float2 e, float2 g, float2 x) {
   const float2 z = mul2(make_float2(at_most(g.x, 26.f), at_most(g.y, 26.f)), dup(kLog2e));
-  const float2 w = make_float2(ex2(z.x), ex2(z.y)), d = add2(w, dup(1.f));
+  const float2 w = make_float2(ex2(z.x), ex2(z.y)), d = fma2(w, dup(64.f), dup(64.f));
   const float2 m2 = mul2(e, fma2(e, dup(-4096.f), dup(8192.f)));
-  const float2 q = mul2(mul2(d, d), fma2(m2, dup(4096.f), dup(1.17549435e-38f)));
+  const float2 q = fma2(mul2(d, d), m2, dup(1.17549435e-38f));
   return mul2(mul2(mul2(w, m2), make_float2(rsq(q.x), rsq(q.y))), x);
 }
 
