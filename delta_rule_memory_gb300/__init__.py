@@ -555,6 +555,7 @@ _DTYPES = {torch.float32: SDM_DTYPE_F32, torch.bfloat16: SDM_DTYPE_BF16}
 
 
 _Tensor = torch.Tensor
+_INT_END = 1 << 31      # ctypes cuts larger sizes off to the C ABI's 32 bits
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -632,12 +633,6 @@ def _act(t, name: str, dtype=None, shape=None, index=None) -> int:
     return ld
 
 
-def _int32(*sizes):
-    """Refuse sizes that the C ABI's ints do not hold: ctypes would cut them off."""
-    if max(sizes) >= 1 << 31:
-        raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
-
-
 def _need(t, name: str, dtype, shape, index: int):
     """A contiguous tensor; shape None: any."""
     if isinstance(t, _Tensor) and _plain(t, dtype, t.shape if shape is None else shape, index):
@@ -666,7 +661,8 @@ def _glr_checks(state, x, r, g, rate, reset, lens, dev_err, like=None):
         raise ValueError("x must be [B,T,D]" if like is None else "dy must be [B,T,D]")
     dt, dev = first.dtype, first.get_device()
     B, T, D = shape
-    _int32(B, T, D)
+    if D >= _INT_END or T >= _INT_END or B >= _INT_END:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(shape)}")
     lx = lr = lg = 0
     if x is not None or like is None:
         lx = D if _plain(x, dt, shape, dev) else _act(x, "x", dt, shape, dev)
@@ -799,7 +795,8 @@ def ckpt8_pack(x, codes=None, exps=None, dev_err=None, stream=None):
     ld = _act(x, "x")
     shape, dev = x.shape, x.get_device()
     *rows, D = shape
-    _int32(D)
+    if D >= _INT_END:
+        raise ValueError(f"D must be below 2^31, got {D}")
     if dev_err is not None:
         _need(dev_err, "dev_err", torch.int32, None, dev)
     with _on(dev, stream) as st:
@@ -821,7 +818,8 @@ def ckpt8_unpack(codes, exps, dtype=None, x=None, stream=None):
     if len(shape) < 1:
         raise ValueError("codes must be [..., D]")
     *rows, D = shape
-    _int32(D)
+    if D >= _INT_END:
+        raise ValueError(f"D must be below 2^31, got {D}")
     _need(exps, "exps", torch.uint8, (*rows, -(-D // 64)), dev)
     if dtype is None:
         dtype = x.dtype if isinstance(x, _Tensor) else torch.bfloat16
