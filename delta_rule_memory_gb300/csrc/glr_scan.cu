@@ -15,14 +15,15 @@
 // fixed by the sizes.
 //
 // What bounds it (8 x 4096 x 1920 in bf16, one GB300): the forward moves 8 bytes an
-// element and takes 106.5 us, 70% of the measured copy bandwidth; its walk over
-// memory alone takes 84 us.  A pair of channels costs 72 instructions, ten of them
+// element and takes 110.6 us, 67% of the measured copy bandwidth; its walk over
+// memory alone takes 84 us.  A pair of channels costs 77 instructions, ten of them
 // special functions, and 128 registers a thread leave four warps to an SM's
-// scheduler, which issues in 62% of the cycles: latency between dependent
+// scheduler, which issues in 63% of the cycles: latency between dependent
 // instructions and in the exchange of runs, not memory, is what is left.  Runs of 8
-// tokens in 96 registers have more warps, but exchange twice as often: 108.5 us,
-// and 304 in place of 215 for one sequence of 32768 x 3840.  The backward (14.5
-// bytes) takes 201 us (67%) for the same reason, at 1.8 times the instructions.
+// tokens in 96 registers have more warps, but exchange twice as often: 108.5 us
+// where runs of 16 took 106.5, and 304 in place of 215 for one sequence of 32768 x
+// 3840.  The backward (14.5 bytes) takes 206 us (65%) for the same reason, at 1.8
+// times the instructions.
 #include <initializer_list>
 #include <type_traits>
 
@@ -336,8 +337,9 @@ __device__ __forceinline__ Run join(const Run &q, const Run &p) {
 }
 
 // In front of a CTA's shared memory; then the warps' rows; then, in a cluster, the CTAs' runs.
-// (Rows that begin on 128 bytes are copied faster: 111 us at 16 behind a multiple, 108.5
-// at 32 or 64, 106.5 at 0; fp32, 4 x 4096 x 1920: 100, 94 and 90.)
+// (Rows that begin on 128 bytes are copied faster: the forward of 8 x 4096 x 1920 took
+// 111 us at 16 behind a multiple, 108.5 at 32 or 64, 106.5 at 0; fp32, 4 x 4096 x 1920:
+// 100, 94 and 90.)
 struct alignas(128) Runs {
   float4 warp[2][kWarps][32];
   uint64_t full[2];  // mbarriers: every CTA's run of a step has arrived in its half of the CTAs' runs
@@ -510,11 +512,11 @@ __device__ __forceinline__ bool put_codes(const GlrArgs &a, unsigned char *q, ui
 
 // ---- forward ----
 // K8: also the 8-bit checkpoints of x, r and g.  CUTS: with reset flags.
-// 8 x 4096 x 1920 in bf16: 106.5 us (70% of the measured copy bandwidth); with the
-// carry 108.5; with checkpoints as well 178 (11.55 bytes an element, 60%: their
-// maxima, codes and exponents nearly double the instructions).  1 x 32768 x 3840, one
-// sequence over clusters of 9: 215 us (69%); 2 x 8192 x 3840 with resets: 116
-// (64%); fp32, 4 x 4096 x 1920: 90 (82%).
+// 8 x 4096 x 1920 in bf16: 110.6 us (67% of the measured copy bandwidth); with the
+// carry 112; with checkpoints as well 185 (11.55 bytes an element, 58%: their
+// maxima, codes and exponents are three quarters more instructions).  1 x 32768 x 3840,
+// one sequence over clusters of 9: 223 us (67%); 2 x 8192 x 3840 with resets: 119
+// (62%); fp32, 4 x 4096 x 1920: 91.6 (81%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kForwardRegs) glr_forward_kernel(const GlrArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -715,9 +717,9 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs a) {
 // e_t = a_t dh_t, the gradient that reaches h_{t-1}: dh_t = dy_t + e_{t+1}.
 // K8: x, r and g come from their checkpoints.  A run is the 8 tokens between two
 // kept states, so the states inside it are recomputed in registers and cost no
-// memory.  8 x 4096 x 1920 in bf16: 201 us (67% of the measured copy bandwidth),
-// from checkpoints 207 (11.55 bytes an element, 52%: decoding takes the time of the
-// bytes it saves); 1 x 32768 x 3840: 396 (68%); 2 x 8192 x 3840 with resets: 228
+// memory.  8 x 4096 x 1920 in bf16: 206 us (65% of the measured copy bandwidth),
+// from checkpoints 208 (11.55 bytes an element, 52%: decoding takes the time of the
+// bytes it saves); 1 x 32768 x 3840: 408 (66%); 2 x 8192 x 3840 with resets: 228
 // (59%); fp32, 4 x 4096 x 1920: 156 (85%).
 template <class E, bool VEC, bool K8, bool CUTS>
 __global__ void __maxnreg__(kBackwardRegs) glr_backward_kernel(const GlrArgs a) {
@@ -968,10 +970,17 @@ constexpr size_t backward_smem(bool keep8) {
 // once, however few CTAs an SM has (it then waits for memory and for the runs of others);
 // beyond that, between the grid's share of the GPU and whole waves of it times as long.
 // Clusters of more than two CTAs find room on 148 of the 152 SMs.  Measured for 8 x 4096 x 1920
-// in bf16, forward: 125 us with 2 CTAs (81% of one wave), 134 with 3, 117 with 4, 125
-// with 5, 122 with 6, 120 with 8, 136 with 9; backward: 220, 255, 208, 231, 220, 222 and 228;
-// 1 x 32768 x 3840, forward: 250 with 8, 229 with 9.  (Today's kernels are about 8%
-// faster at each.)
+// in bf16, forward: 121 us with 2 CTAs (81% of one wave), 119 with 3, 111 with 4, 119
+// with 5, 116 with 6, 115 with 8, 132 with 9; backward: 216, 241, 206, 230, 217, 218 and 224;
+// 1 x 32768 x 3840, forward: 293 with 4, 248 with 8, 223 with 9; backward: 587, 441, 407.
+// More than 8 CTAs only where all of them have room by that count and the walk with 8 has
+// more than 16 steps.  The count is too high for large clusters where they would nearly
+// fill the GPU: without the second condition 8 x 3000 x 480 backward took 72 us in
+// place of 55 and 4 x 8192 x 963 forward 136 in place of 105, and without either
+// 12 x 512 x 1285 in fp32 backward 94 in place of 63.  What the second one costs: few
+// channels at up to 8192 (backward 4096) tokens would be faster with 16 CTAs, 1 x 4096 x
+// 480 by 18.4 us in place of 22.5 and 29 in place of 41, 1 x 6000 x 64 forward by 20.5
+// in place of 30.7.
 int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
   const int64_t columns = static_cast<int64_t>(B) * ((D + kChan - 1) / kChan);
   const int tile = run * kWarps;
@@ -981,7 +990,6 @@ int cluster_size(int B, int T, int D, int run, int regs, size_t smem) {
     if (cs > 1 && (cs - 1) * tile >= T) break;
     const int per_sm = min(65536 / (32 * regs) / kWarps, static_cast<int>((227 << 10) / (cluster_bytes(cs) + smem + 1024)));
     const int64_t room = (cs > 2 ? kSMs - 4 : kSMs) * per_sm, ctas = columns * cs;
-    // large clusters pay only where the walk is long and they fill the GPU
     if (cs > 8 && (ctas > room || T <= 16 * 8 * tile)) break;
     const int64_t waves = (ctas + room - 1) / room, steps = (T + tile * cs - 1) / (tile * cs);
     const double share = static_cast<double>(ctas) / room;

@@ -507,7 +507,8 @@ SDM_API int sse_scan(float *state, const float *route_logits, int topk, const fl
  *   L_t = -rate sigmoid(r_t),  a_t = exp(L_t),  m_t = sqrt(1 - a_t^2)
  *   h_t = a_t h_{t-1} + m_t sigmoid(g_t) x_t,   y_t = h_t
  * r is the logit of the recurrence gate, g of the input gate; m_t keeps the
- * state's variance at that of the input whatever the decay.
+ * state's variance at that of the input whatever the decay.  (A token that
+ * resets has the same m_t, not 1.)
  *
  * state    : fp32 [B,D], h_0.   state_out : fp32 [B,D], h_T; may be `state`
  *            itself (the state continues in place), must not overlap it else.
@@ -531,6 +532,8 @@ SDM_API int sse_scan(float *state, const float *route_logits, int topk, const fl
  * NaN and infinite x, r, g and states are not looked for: they run through the
  * arithmetic, into the states of their channel and sequence only, up to the next
  * reset (an infinite state may go on as a NaN).  The state, its decays and their products are fp32; y is rounded once, to nearest even.
+ * Decays and sigmoids are right relative to themselves (to 2^-22 and their exponent's
+ * roundings) however small they are, down to fp32's smallest normal number.
  * Limits: B, T, D >= 0, B < 65536, T < 2^30, D < 2^24; D <= ld < 2^27.  x, r, g, y
  *         aligned to their element; state, rate 4-byte.  Any B, T or D of 0
  *         is allowed (T = 0 copies the state).
@@ -576,7 +579,8 @@ SDM_API size_t glr_scan_backward_workspace_size(int B, int T, int D);
  *   dx = dh m s_g,   dg = dh m s_g (1 - s_g) x
  *   dL = a dh (h_{t-1} - (a / m) s_g x),  dr = -rate s_r (1 - s_r) dL
  *   drate = sum over b and t of -s_r dL,   dL/dh_0 = a_1 dh_1
- * (h_{t-1} as the forward used it: 0 where token t resets).  Where m_t^2
+ * (h_{t-1} as the forward used it: 0 where token t resets; 1 - s is a
+ * difference in fp32, 0 for logits above 17).  Where m_t^2
  * underflows (rate 0, say) the term with a / m, which has no limit there, is
  * left out.
  *
