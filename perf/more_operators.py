@@ -130,6 +130,7 @@ def prepare(case, seed):
         P = case["P"]
         s["pool"] = 0.3 * normal(P, H, dk, dv)
         s["slots"] = torch.randperm(P, generator=gen, device="cuda")[:B].to(torch.int32)
+        s["y"] = torch.empty((B, T, H, dv), dtype=torch.bfloat16, device="cuda")
         return s
     s["h0"] = 0.3 * normal(B, H, dk, dv)
     s["hT"] = torch.empty_like(s["h0"])
@@ -253,7 +254,7 @@ def _plain_step(s):
         S = S + k * (s["beta"][:, t, :, None] * e)[..., None, :]
         y.append((S * q).sum(-2))
     s["pool"][at] = S
-    return {"y": torch.stack(y, 1).to(torch.bfloat16), "pool": s["pool"]}
+    return {"y": s["y"].copy_(torch.stack(y, 1)), "pool": s["pool"]}
 
 
 def _plain_route(s):
@@ -297,7 +298,7 @@ def run(state):
         return {"gdn": _plain_gdn, "step": _plain_step, "route": _plain_route}[case["op"]](s)
     import delta_rule_memory_gb300 as sdm
     if case["op"] == "step":
-        y = sdm.gdn_step(s["pool"], s["q"], s["k"], s["v"], s["la"], s["beta"], slots=s["slots"])
+        y = sdm.gdn_step(s["pool"], s["q"], s["k"], s["v"], s["la"], s["beta"], slots=s["slots"], y=s["y"])
         return {"y": y, "pool": s["pool"]}
     if case["op"] == "gdn":
         y, saved = sdm.gdn_train(s["h0"], s["q"], s["k"], s["v"], s["la"], s["beta"], reset=s["reset"], lens=s["lens"],
