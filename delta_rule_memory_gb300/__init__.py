@@ -27,6 +27,8 @@ __all__ = [
     "sdm_scan_chunked_workspace_size",
     "gdn_scan", "gdn_scan_workspace_size", "gdn2_scan", "gdn2_scan_workspace_size", "sse_scan", "sse_scan_workspace_size",
     "glr_scan", "glr_scan_train", "glr_scan_carry_size", "glr_scan_backward", "glr_scan_backward_workspace_size",
+    "gdn_train", "gdn_train_saved_size", "gdn_backward", "gdn_backward_workspace_size", "gdn_step",
+    "route_sort", "route_sort_workspace_size", "route_gather", "route_combine", "route_combine_backward",
     "ckpt8_pack", "ckpt8_unpack", "SDM_RESID_SHARED", "SDM_RESID_PERSLOT", "SSE_WRITE_ADDITIVE", "SSE_WRITE_DELTA",
     "SDM_RESID_ADDITIVE", "SDM_DEVERR_INDEX_RANGE", "SDM_DEVERR_INDEX_REPEAT", "SDM_DEVERR_NONFINITE",
     "SDM_DEVERR_TIMEOUT", "SDM_DEVERR_RATE", "SDM_ERR_DEVICE",
@@ -77,6 +79,17 @@ _SIGNATURES = {
     "glr_scan_backward_workspace_size": (_SZ, [_I, _I, _I]),
     "glr_scan_backward": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P,
                                _L, _P, _P, _SZ, _P, _P]),
+    "gdn_train_saved_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "gdn_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "gdn_train": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P, _P]),
+    "gdn_backward": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _SZ, _P, _I, _I, _I, _I, _I, _I, _P, _L, _P,
+                          _L, _P, _L, _P, _P, _P, _SZ, _P, _P]),
+    "gdn_step": (_I, [_P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "route_sort_workspace_size": (_SZ, [_L, _I, _I]),
+    "route_sort": (_I, [_P, _L, _I, _I, _P, _P, _P, _P, _SZ, _P, _P]),
+    "route_gather": (_I, [_P, _L, _I, _P, _P, _L, _I, _I, _I, _P, _P]),
+    "route_combine": (_I, [_P, _I, _P, _P, _L, _I, _I, _P, _P]),
+    "route_combine_backward": (_I, [_P, _L, _I, _P, _P, _P, _P, _L, _I, _I, _I, _P, _P, _P]),
     "ckpt8_pack": (_I, [_P, _L, _I, _L, _I, _P, _P, _P, _P]),
     "ckpt8_unpack": (_I, [_P, _P, _L, _I, _P, _L, _I, _P]),
 }
@@ -835,3 +848,271 @@ def ckpt8_unpack(codes, exps, dtype=None, x=None, stream=None):
     if rc:
         _check("ckpt8_unpack", rc)
     return x
+
+
+def _heads(t, name: str, shape, index: int) -> int:
+    """Check bf16 [B,T,heads,d] whose heads and channels are contiguous within a
+    token and whose tokens lie at one distance (column slices of one projection
+    will do); returns that distance in elements."""
+    ld = shape[2] * shape[3]
+    if _plain(t, torch.bfloat16, shape, index):
+        return ld
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    B, T, heads, d = shape
+    if not t.numel():
+        return ld
+    if (d > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != d):
+        raise ValueError(f"{name}'s heads and channels must be contiguous within a token")
+    step = t.stride(1) if T > 1 else t.stride(0) if B > 1 else ld
+    if step < ld or (B > 1 and t.stride(0) != T * step):
+        raise ValueError(f"{name}'s tokens must lie at one distance of at least {ld} elements")
+    return step
+
+
+def _gdn_checks(state, name, q, k, v, log_alpha, beta, reset, lens, dev_err, pool=False):
+    """Common checks of the gdn_train, gdn_backward and gdn_step calls."""
+    if not isinstance(state, _Tensor) or not state.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if state.dim() != 4:
+        raise ValueError(f"{name} must be {'[P,H,dk,dv]' if pool else '[B,H,dk,dv]'}")
+    for t, n in ((q, "q"), (v, "v")):
+        if not isinstance(t, _Tensor) or not t.is_cuda:
+            raise TypeError(f"{n} must be a CUDA tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{n} must be [B,T,{'Hk,dk' if n == 'q' else 'H,dv'}]")
+    dev = state.get_device()
+    P, H, dk, dv = state.shape
+    B, T, Hk = q.shape[:3]
+    if max(P, B, T, Hk, H, dk, dv) >= _INT_END:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(state.shape)} and {tuple(q.shape)}")
+    if not pool and P != B:
+        raise ValueError(f"{name} must be [B,H,dk,dv] with B = {B}, got {tuple(state.shape)}")
+    _need(state, name, torch.float32, None, dev)
+    lq, lk, lv = _heads(q, "q", (B, T, Hk, dk), dev), _heads(k, "k", (B, T, Hk, dk), dev), _heads(v, "v", (B, T, H, dv), dev)
+    _need(log_alpha, "log_alpha", torch.float32, (B, T, H), dev)
+    _need(beta, "beta", torch.float32, (B, T, H), dev)
+    if reset is not None:
+        if isinstance(reset, _Tensor) and reset.dtype is torch.bool:
+            reset = reset.view(torch.uint8)
+        _need(reset, "reset", torch.uint8, (B, T), dev)
+    if lens is not None:
+        _need(lens, "lens", torch.int32, (B,), dev)
+    if dev_err is not None:
+        _need(dev_err, "dev_err", torch.int32, None, dev)
+    return B, T, Hk, H, dk, dv, dev, lq, lk, lv, reset
+
+
+def gdn_train_saved_size(B: int, T: int, Hk: int, H: int, dk: int, dv: int) -> int:
+    return int(lib().gdn_train_saved_size(B, T, Hk, H, dk, dv))
+
+
+def gdn_train(state, q, k, v, log_alpha, beta, reset=None, lens=None, y=None, state_out=None, saved=None, dev_err=None,
+              stream=None):
+    """Gated delta rule, chunked, keeping what gdn_backward needs: S~ =
+    exp(log_alpha_t) S, S = S~ + beta_t k_t (v_t - S~^T k_t)^T, y_t = S^T q_t.
+    q, k: bf16 [B,T,Hk,dk], v: bf16 [B,T,H,dv] (column slices of one projection
+    will do), H a multiple of Hk: value head h reads key head h // (H // Hk);
+    log_alpha, beta: fp32 [B,T,H]; reset: uint8 or bool [B,T], 1 where a new
+    sequence starts inside a row; lens: int32 [B], tokens that exist.  Updates
+    `state` fp32 [B,H,dk,dv] in place, or leaves it and writes `state_out`
+    where that is given.  Returns (y, saved): y bf16 [B,T,H,dv], whose rows
+    behind lens are 0, or as they were in a `y` that was given; saved uint8, for
+    gdn_backward with the same inputs."""
+    B, T, Hk, H, dk, dv, dev, lq, lk, lv, reset = _gdn_checks(state, "state", q, k, v, log_alpha, beta, reset, lens, dev_err)
+    with _on(dev, stream) as st:
+        y = _out(y, "y", torch.bfloat16, (B, T, H, dv), dev, lens)
+        state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
+        if saved is None:
+            saved = torch.empty(gdn_train_saved_size(B, T, Hk, H, dk, dv), dtype=torch.uint8, device=dev)
+        else:
+            _need(saved, "saved", torch.uint8, None, dev)
+        rc = lib().gdn_train(state.data_ptr(), state_out.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv,
+                             log_alpha.data_ptr(), beta.data_ptr(), _ptr(reset), _ptr(lens), B, T, Hk, H, dk, dv,
+                             y.data_ptr(), saved.data_ptr(), saved.numel(), _ptr(dev_err), st)
+    if rc:
+        _check("gdn_train", rc)
+    return y, saved
+
+
+def gdn_backward_workspace_size(B: int, T: int, Hk: int, H: int, dk: int, dv: int) -> int:
+    return int(lib().gdn_backward_workspace_size(B, T, Hk, H, dk, dv))
+
+
+def gdn_backward(dstate, q, k, v, log_alpha, beta, saved, dy, reset=None, lens=None, grads=None, dstate_out=None,
+                 workspace=None, dev_err=None, stream=None):
+    """Gradients of gdn_train, given its inputs and `saved`; dy bf16 [B,T,H,dv].
+    `dstate` fp32 [B,H,dk,dv] holds dL/dS_T and becomes dL/dS_0 (or stays, with
+    `dstate_out` given).  `grads`: optional (dq, dk, dv) to write, which may be
+    column slices of one buffer.  Returns (dq, dk, dv, dlog_alpha, dbeta), the
+    last two fp32 [B,T,H]; rows behind lens are 0, or as they were in given
+    ones.  Heads that share q and k have their gradients summed."""
+    B, T, Hk, H, dk, dv, dev, lq, lk, lv, reset = _gdn_checks(dstate, "dstate", q, k, v, log_alpha, beta, reset, lens,
+                                                              dev_err)
+    _need(saved, "saved", torch.uint8, None, dev)
+    _need(dy, "dy", torch.bfloat16, (B, T, H, dv), dev)
+    with _on(dev, stream) as st:
+        if grads is None:
+            dq, dk_, dv_ = (_out(None, "", torch.bfloat16, t.shape, dev, lens) for t in (q, k, v))
+            lds = Hk * dk, Hk * dk, H * dv
+        else:
+            dq, dk_, dv_ = grads
+            lds = [_heads(t, n, like.shape, dev) for t, n, like in ((dq, "dq", q), (dk_, "dk", k), (dv_, "dv", v))]
+        dla, dbeta = _out(None, "", torch.float32, (B, T, H), dev, lens), _out(None, "", torch.float32, (B, T, H), dev, lens)
+        dstate_out = dstate if dstate_out is None else _out(dstate_out, "dstate_out", torch.float32, (B, H, dk, dv), dev)
+        if workspace is None:
+            workspace = torch.empty(gdn_backward_workspace_size(B, T, Hk, H, dk, dv), dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace, "workspace", torch.uint8, None, dev)
+        rc = lib().gdn_backward(dstate.data_ptr(), dstate_out.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(),
+                                lv, log_alpha.data_ptr(), beta.data_ptr(), _ptr(reset), _ptr(lens), saved.data_ptr(),
+                                saved.numel(), dy.data_ptr(), B, T, Hk, H, dk, dv, dq.data_ptr(), lds[0], dk_.data_ptr(),
+                                lds[1], dv_.data_ptr(), lds[2], dla.data_ptr(), dbeta.data_ptr(), workspace.data_ptr(),
+                                workspace.numel(), _ptr(dev_err), st)
+    if rc:
+        _check("gdn_backward", rc)
+    return dq, dk_, dv_, dla, dbeta
+
+
+def gdn_step(state, q, k, v, log_alpha, beta, slots=None, lens=None, y=None, dev_err=None, stream=None):
+    """The gated delta rule token by token, for decoding: B sequences advance by
+    T tokens (one, or a few drafted ones).  `state` fp32 [P,H,dk,dv] is a pool,
+    updated in place; slots: int32 [B], each sequence's state in it (None: state
+    b; negative: a sequence that does not exist; no slot twice); lens: int32
+    [B], tokens that exist.  q, k, v, log_alpha, beta as gdn_train's.  Returns y
+    bf16 [B,T,H,dv]; rows of what does not exist are 0, or as they were in a
+    `y` that was given."""
+    B, T, Hk, H, dk, dv, dev, lq, lk, lv, _ = _gdn_checks(state, "state", q, k, v, log_alpha, beta, None, lens, dev_err, True)
+    if slots is not None:
+        _need(slots, "slots", torch.int32, (B,), dev)
+    with _on(dev, stream) as st:
+        y = _out(y, "y", torch.bfloat16, (B, T, H, dv), dev, slots if lens is None else lens)
+        rc = lib().gdn_step(state.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv, log_alpha.data_ptr(),
+                            beta.data_ptr(), _ptr(slots), _ptr(lens), state.shape[0], B, T, Hk, H, dk, dv, y.data_ptr(),
+                            _ptr(dev_err), st)
+    if rc:
+        _check("gdn_step", rc)
+    return y
+
+
+def _matrix(t, name: str, dtype=None, shape=None, index=None) -> int:
+    ld = _act(t, name, dtype, shape, index)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows,D]")
+    if max(t.shape) >= _INT_END:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(t.shape)}")
+    return ld
+
+
+def _visits(place, name: str, index=None):
+    if not isinstance(place, _Tensor) or not place.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if place.dim() != 2:
+        raise ValueError(f"{name} must be [M,k]")
+    if max(place.shape) >= _INT_END:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(place.shape)}")
+    dev = place.get_device() if index is None else index
+    _need(place, name, torch.int32, None, dev)
+    return (*place.shape, dev)
+
+
+def route_sort_workspace_size(M: int, k: int, N: int) -> int:
+    return int(lib().route_sort_workspace_size(M, k, N))
+
+
+def route_sort(sel, N: int, order=None, place=None, offsets=None, workspace=None, dev_err=None, stream=None):
+    """The k visits of each of M tokens sorted by partition, those of one
+    partition in their order.  sel: int32 [M,k], partitions in [0, N), negative
+    where a visit is dropped.  Returns (order int32 [M k], the visit m k + r at
+    each place, -1 behind the last; place int32 [M,k], its inverse, -1 for a
+    dropped visit; offsets int32 [N+1], where each partition's places begin)."""
+    M, k, dev = _visits(sel, "sel")
+    N = int(N)
+    if not 0 <= N < _INT_END:
+        raise ValueError(f"N must be in [0, 2^31), got {N}")
+    if dev_err is not None:
+        _need(dev_err, "dev_err", torch.int32, None, dev)
+    with _on(dev, stream) as st:
+        order = _out(order, "order", torch.int32, (M * k,), dev)
+        place = _out(place, "place", torch.int32, (M, k), dev)
+        offsets = _out(offsets, "offsets", torch.int32, (N + 1,), dev)
+        size = 0
+        if workspace is not None:
+            _need(workspace, "workspace", torch.uint8, None, dev)
+            size = workspace.numel()
+        else:
+            size = route_sort_workspace_size(M, k, N)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        rc = lib().route_sort(sel.data_ptr(), M, k, N, order.data_ptr(), place.data_ptr(), offsets.data_ptr(),
+                              _ptr(workspace), size, _ptr(dev_err), st)
+    if rc:
+        _check("route_sort", rc)
+    return order, place, offsets
+
+
+def route_gather(x, place, offsets, rows=None, stream=None):
+    """Rows of x [M,D] (bf16 or fp32, rows at one distance) at their visits'
+    places: rows[place[m,r]] = x[m], [M k, D]; rows without a visit are 0.  Its
+    gradient is route_combine(drows, place)."""
+    ld = _matrix(x, "x")
+    M, D = x.shape
+    _, k, dev = _visits(place, "place", x.get_device())
+    _need(place, "place", torch.int32, (M, k), dev)
+    _need(offsets, "offsets", torch.int32, None, dev)
+    if not offsets.numel():
+        raise ValueError("offsets must be [N+1]")
+    with _on(dev, stream) as st:
+        rows = _out(rows, "rows", x.dtype, (M * k, D), dev)
+        rc = lib().route_gather(x.data_ptr(), ld, _DTYPES[x.dtype], place.data_ptr(), offsets.data_ptr(), M, k,
+                                offsets.numel() - 1, D, rows.data_ptr(), st)
+    if rc:
+        _check("route_gather", rc)
+    return rows
+
+
+def route_combine(rows, place, w=None, y=None, stream=None):
+    """The rows [M k, D] (bf16 or fp32) at each token's places times its weights
+    w fp32 [M,k] (None: 1), summed: y [M,D] of the rows' type."""
+    _matrix(rows, "rows")
+    M, k, dev = _visits(place, "place", rows.get_device())
+    D = rows.shape[1]
+    _need(rows, "rows", rows.dtype, (M * k, D), dev)
+    if w is not None:
+        _need(w, "w", torch.float32, (M, k), dev)
+    with _on(dev, stream) as st:
+        y = _out(y, "y", rows.dtype, (M, D), dev)
+        rc = lib().route_combine(rows.data_ptr(), _DTYPES[rows.dtype], place.data_ptr(), _ptr(w), M, k, D, y.data_ptr(), st)
+    if rc:
+        _check("route_combine", rc)
+    return y
+
+
+def route_combine_backward(dy, rows, place, w, offsets, drows=None, dw=None, stream=None):
+    """Gradients of route_combine: dy [M,D] (rows at one distance) and the rows
+    that it was given -> (drows [M k, D] of their type, 0 where there is no
+    visit; dw fp32 [M,k])."""
+    ld = _matrix(dy, "dy")
+    M, D = dy.shape
+    _, k, dev = _visits(place, "place", dy.get_device())
+    _need(place, "place", torch.int32, (M, k), dev)
+    _need(rows, "rows", dy.dtype, (M * k, D), dev)
+    _need(w, "w", torch.float32, (M, k), dev)
+    _need(offsets, "offsets", torch.int32, None, dev)
+    if not offsets.numel():
+        raise ValueError("offsets must be [N+1]")
+    with _on(dev, stream) as st:
+        drows = _out(drows, "drows", dy.dtype, (M * k, D), dev)
+        dw = _out(dw, "dw", torch.float32, (M, k), dev)
+        rc = lib().route_combine_backward(dy.data_ptr(), ld, _DTYPES[dy.dtype], rows.data_ptr(), place.data_ptr(),
+                                          w.data_ptr(), offsets.data_ptr(), M, k, offsets.numel() - 1, D,
+                                          drows.data_ptr(), dw.data_ptr(), st)
+    if rc:
+        _check("route_combine_backward", rc)
+    return drows, dw

@@ -1,0 +1,144 @@
+// mma.cuh - warp-level bf16 matrix products (mma.sync m16n8k16, fp32 sums) on
+// shared-memory tiles, for chains whose operands stay in registers.
+//
+// A tile is row-major bf16 with rows of a multiple of 128 bytes; the 16-byte
+// piece p of row r lies at piece p ^ (r & 7), so the eight rows that one
+// ldmatrix phase reads lie in different banks.
+//
+// Fragments (g = lane / 4, t = lane % 4): the accumulator of an m16n8 product
+// holds rows g and g + 8, columns 2t and 2t + 1.  Two neighbouring ones are, as
+// they stand, the A fragment of a k = 16 step, so a product's result feeds the
+// next product without leaving the registers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace sdm {
+namespace mma {
+
+// byte offset of 16-byte piece p of row r, rows of `rb` bytes
+__device__ __forceinline__ uint32_t piece(int r, int p, int rb) {
+  return static_cast<uint32_t>(r * rb + ((p ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+
+// B fragments of two n-tiles (n0 .. n0+15) and one k-step from tile[n][k]:
+// r[0], r[1] of the first, r[2], r[3] of the second
+__device__ __forceinline__ void b_rows(uint32_t tile, int rb, int n0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4(tile + piece(n0 + ((lane >> 4) << 3) + (lane & 7), (k0 >> 3) + ((lane >> 3) & 1), rb), r);
+}
+// the same from tile[k][n]
+__device__ __forceinline__ void b_cols(uint32_t tile, int rb, int n0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4_t(tile + piece(k0 + (((lane >> 3) & 1) << 3) + (lane & 7), (n0 >> 3) + (lane >> 4), rb), r);
+}
+// A fragment (rows m0 .. m0+15, one k-step) from tile[m][k] ...
+__device__ __forceinline__ void a_rows(uint32_t tile, int rb, int m0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4(tile + piece(m0 + (((lane >> 3) & 1) << 3) + (lane & 7), (k0 >> 3) + (lane >> 4), rb), r);
+}
+// ... and from tile[k][m]
+__device__ __forceinline__ void a_cols(uint32_t tile, int rb, int m0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4_t(tile + piece(k0 + ((lane >> 4) << 3) + (lane & 7), (m0 >> 3) + ((lane >> 3) & 1), rb), r);
+}
+
+// d += a b
+__device__ __forceinline__ void fma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float low2(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high2(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// x = s[0] + s[1] + ... in bf16, each the rounding of what the ones before
+// leave: two parts keep 16 bits of x, three keep all 24 (to 2^-26 relative).
+template <int N>
+__device__ __forceinline__ void split(float x0, float x1, uint32_t (&s)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    s[i] = pack2(x0, x1);
+    if (i + 1 < N) {
+      x0 -= low2(s[i]);
+      x1 -= high2(s[i]);
+    }
+  }
+}
+
+// The A fragments, in N parts, of one k-step of an accumulator's columns: c0
+// and c1 are its n-tiles 2 ks and 2 ks + 1.  a[part][register].
+template <int N>
+__device__ __forceinline__ void a_split(const float (&c0)[4], const float (&c1)[4], uint32_t (&a)[N][4]) {
+  uint32_t s[N];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < 2)
+      split<N>(c0[2 * i], c0[2 * i + 1], s);
+    else
+      split<N>(c1[2 * i - 4], c1[2 * i - 3], s);
+#pragma unroll
+    for (int n = 0; n < N; ++n) a[n][i] = s[n];
+  }
+}
+
+// transposes an 8x8 matrix of 16-bit elements held one row per four lanes
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// 16 bytes global -> shared, asynchronously; zeros where `live` is false (src
+// then only has to be a valid address)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// `rows` rows of `width` bf16 (row r at src + r * ld) into a tile of rows of rb
+// bytes, zeros behind `width` and from row `live` on.  vec: every row is
+// 16-byte aligned and width % 8 == 0 (asynchronous copies); else by elements.
+__device__ __forceinline__ void load_tile(unsigned char *tile, int rb, const uint16_t *src, int64_t ld, int rows,
+                                          int live, int width, bool vec, int tid, int threads) {
+  const int pieces = rb >> 4, all = rows * pieces;
+  for (int id = tid; id < all; id += threads) {
+    const int r = id / pieces, p = id - r * pieces;
+    unsigned char *dst = tile + piece(r, p, rb);
+    const int c = p * 8;
+    if (vec) {
+      const bool ok = r < live && c < width;
+      copy16(static_cast<uint32_t>(__cvta_generic_to_shared(dst)), ok ? src + r * ld + c : src, ok);
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (r < live) {
+        const uint16_t *s = src + r * ld + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < width) w[e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
+      }
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+}  // namespace mma
+}  // namespace sdm

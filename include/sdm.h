@@ -631,6 +631,123 @@ SDM_API int ckpt8_pack(const void *x, int64_t ld, int dtype, int64_t rows, int D
 SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows, int D, void *x, int64_t ld, int dtype,
                          void *stream);
 
+/*
+ * gdn_train, gdn_backward - training of the gated delta rule ([LAA] Eqs. 15-17,
+ * gdn_scan's recurrence with the decay given as its logarithm):
+ *   S~   = e^{log_alpha_t} S          (0 where token t resets)
+ *   E_t  = v_t - S~^T k_t
+ *   S    = S~ + beta_t k_t E_t^T,     y_t = S^T q_t
+ * Heads are grouped: value head h reads key head h / (H / Hk), whose q and k
+ * gradients are summed over its value heads, in order.
+ *
+ * state     : fp32 [B,H,dk,dv], S_0 (NULL: zero).  state_out : fp32 [B,H,dk,dv],
+ *             S_T; may be `state` itself, must not overlap it else.
+ * q, k      : bf16, token t of sequence b at ld * (b T + t) elements, there
+ *             [Hk,dk] contiguous; v : bf16, there [H,dv]; ld_q, ld_k >= Hk dk and
+ *             ld_v >= H dv, so they may be column slices of one projection.
+ * log_alpha : fp32 [B,T,H]; values below -200 (minus infinity among them)
+ *             count as -200, whose exponential is 0.   beta : fp32 [B,T,H];
+ *             magnitudes below 1e-18 count as 1e-18, by which dbeta has its limit.
+ * reset     : optional uint8 [B,T]; where it is not 0, the state is taken as 0
+ *             before token t (a new document starts in a packed row).
+ * lens      : optional int32 [B], 0 <= lens[b] <= T: only the first lens[b]
+ *             tokens exist; the rows behind them are neither read nor written.
+ *             Other values are clamped and set SDM_DEVERR_INDEX_RANGE.
+ * y         : bf16 [B,T,H,dv], contiguous.
+ * saved     : gdn_train_saved_size() bytes, 16-byte aligned, written by
+ *             gdn_train and read by gdn_backward with the same inputs and sizes: per
+ *             64 tokens of a head their decays, two triangular matrices, the state
+ *             and the residuals E (149 KB at dk = dv = 128).
+ *
+ * gdn_backward: dstate fp32 [B,H,dk,dv] = dL/dS_T (NULL: zero), dstate_out =
+ * dL/dS_0 (may be dstate itself); dy bf16 [B,T,H,dv]; dq, dk, dv bf16 laid out
+ * as q, k, v with distances of their own; dlog_alpha, dbeta fp32 [B,T,H]
+ * (dlog_alpha is 0 where a token resets).  Gradients must not overlap inputs
+ * or one another.  workspace : gdn_backward_workspace_size() bytes, 16-byte aligned; calls that
+ * share one must not overlap on the GPU.
+ *
+ * Both are deterministic.  Chunks of 64 tokens: one kernel for what a chunk
+ * needs of itself, one that runs the chunks in order (16 value columns a warp, the state in its
+ * registers), and in the backward one for the sums over value columns.  States, sums and
+ * decays are fp32 (the sums of log_alpha wider); y, dq, dk and dv are rounded once, to nearest even.
+ * NaN and infinities are not looked for: they spread over their chunk and the
+ * tokens behind it (in the backward, before it).
+ * Limits: 1 <= dk <= 128, 1 <= dv <= 1024, H a multiple of Hk; B, H < 65536,
+ *         T < 2^30, B T < 2^31, B H ceil(T/64) ceil(dv/16) < 2^31; distances < 2^27.  Pointers aligned to their
+ *         element.  Any B, T or H of 0 is allowed (T = 0 copies the state).
+ */
+SDM_API size_t gdn_train_saved_size(int B, int T, int Hk, int H, int dk, int dv);
+SDM_API size_t gdn_backward_workspace_size(int B, int T, int Hk, int H, int dk, int dv);
+SDM_API int gdn_train(const float *state, float *state_out, const uint16_t *q, int64_t ld_q, const uint16_t *k,
+                      int64_t ld_k, const uint16_t *v, int64_t ld_v, const float *log_alpha, const float *beta,
+                      const uint8_t *reset, const int32_t *lens, int B, int T, int Hk, int H, int dk, int dv,
+                      uint16_t *y, void *saved, size_t saved_bytes, int32_t *dev_err, void *stream);
+SDM_API int gdn_backward(const float *dstate, float *dstate_out, const uint16_t *q, int64_t ld_q, const uint16_t *k,
+                         int64_t ld_k, const uint16_t *v, int64_t ld_v, const float *log_alpha, const float *beta,
+                         const uint8_t *reset, const int32_t *lens, const void *saved, size_t saved_bytes,
+                         const uint16_t *dy, int B, int T, int Hk, int H, int dk, int dv, uint16_t *dq, int64_t ld_dq,
+                         uint16_t *dk_out, int64_t ld_dk, uint16_t *dv_out, int64_t ld_dv, float *dlog_alpha,
+                         float *dbeta, void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/*
+ * gdn_step - the same recurrence, token by token, for decoding: B sequences
+ * advance by T tokens (one, or a few that were drafted), each on its own state
+ * out of a pool.
+ *
+ * state : fp32 [P,H,dk,dv], in place.
+ * slots : optional int32 [B], the state of each sequence (NULL: state b, P >= B).
+ *         A negative slot marks a sequence that does not exist: nothing of it is
+ *         read or written.  So does a slot outside the pool (SDM_DEVERR_INDEX_RANGE) and one that a
+ *         sequence before it names (SDM_DEVERR_INDEX_REPEAT; the first one runs).
+ * lens  : optional int32 [B], the tokens of each sequence that exist, as above.
+ * q, k, v, log_alpha, beta, y, limits : as gdn_train's (log_alpha is not clamped: e^-inf is 0;
+ *         beta is taken as it is; T < 2^20); rows of y of tokens that do not exist keep their bits.
+ */
+SDM_API int gdn_step(float *state, const uint16_t *q, int64_t ld_q, const uint16_t *k, int64_t ld_k, const uint16_t *v,
+                     int64_t ld_v, const float *log_alpha, const float *beta, const int32_t *slots,
+                     const int32_t *lens, int P, int B, int T, int Hk, int H, int dk, int dv, uint16_t *y,
+                     int32_t *dev_err, void *stream);
+
+/*
+ * route_sort - the visits of a routed layer ([SSE] "SSE routes tokens into
+ * shared-parameter state partitions") sorted by partition: token m makes the
+ * k visits m k + r to the partitions sel[m,r].
+ *
+ * sel     : int32 [M,k]; a negative value drops the visit, one of N or more
+ *           also sets SDM_DEVERR_INDEX_RANGE.  Values need not be distinct.
+ * order   : int32 [M k] out: the visit at each place, partitions in order,
+ *           visits of one in theirs; -1 behind the last.
+ * place   : int32 [M,k] out, the inverse: each visit's place, -1 if dropped.
+ * offsets : int32 [N+1] out: partition p has the places offsets[p] up to offsets[p+1].
+ * workspace : route_sort_workspace_size() bytes, 4-byte aligned (NULL where 0).
+ * Limits: 0 <= k <= 32, 0 <= N <= 1024, M k < 2^31 - 4096.
+ */
+SDM_API size_t route_sort_workspace_size(int64_t M, int k, int N);
+SDM_API int route_sort(const int32_t *sel, int64_t M, int k, int N, int32_t *order, int32_t *place, int32_t *offsets,
+                       void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/*
+ * route_gather           rows[place[m,r]] = x[m]; rows without a visit are 0
+ * route_combine          y[m] = sum over r of w[m,r] rows[place[m,r]], r in order
+ * route_combine_backward drows[place[m,r]] = w[m,r] dy[m] (0 without a visit),
+ *                        dw[m,r] = dy[m] . rows[place[m,r]] (0 if dropped)
+ * The gradient of route_gather is route_combine without weights.
+ *
+ * x, dy   : [M,D] of `dtype`, rows at ld >= D elements.  rows, drows : [M k, D],
+ *           y : [M,D], contiguous, of the same dtype.  w, dw : fp32 [M,k] (w
+ *           NULL: 1).  place, offsets : as route_sort wrote them (a place
+ *           outside [0, M k) counts as dropped; offsets[N] says where the rows without a visit begin).
+ * Sums are fp32, rounded once.  Outputs must not overlap inputs.
+ * Limits: as route_sort; D < 2^24, ld < 2^27.  Pointers aligned to their element.
+ */
+SDM_API int route_gather(const void *x, int64_t ld_x, int dtype, const int32_t *place, const int32_t *offsets, int64_t M,
+                         int k, int N, int D, void *rows, void *stream);
+SDM_API int route_combine(const void *rows, int dtype, const int32_t *place, const float *w, int64_t M, int k, int D,
+                          void *y, void *stream);
+SDM_API int route_combine_backward(const void *dy, int64_t ld_dy, int dtype, const void *rows, const int32_t *place,
+                                   const float *w, const int32_t *offsets, int64_t M, int k, int N, int D, void *drows,
+                                   float *dw, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
