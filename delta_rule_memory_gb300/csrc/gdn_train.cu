@@ -52,6 +52,7 @@ using namespace mma;
 
 constexpr int kC = 64;                  // tokens of a chunk
 constexpr int kTile = kC * kC * 2;      // bytes of one bf16 [64][64] tile
+constexpr int kTri = 10 * 512;          // ... of a lower triangular one: its ten 16 x 16 blocks
 constexpr int kLd = kC + 4;             // fp32 rows of the solve: 16-byte aligned, 4 banks apart
 constexpr int kScal = 6 * kC;           // gam, tail, beta, l (two floats), document number
 constexpr float kTinyBeta = 1e-18f;     // stands for a smaller |beta|, so that dZ / beta is the limit
@@ -64,14 +65,14 @@ struct Gdn {
   const uint8_t *reset;
   const int32_t *lens;
   int B, T, Hk, H, dk, dv, n;  // n: chunks of a sequence
-  int vec_qk, vec_v, vec_dy;   // rows of q, k / v / dy can be copied by 16 bytes
-  int vec_y;                   // y (or dv) can be written by pairs
+  int by_qk, by_v, by_dy;      // bytes by which rows of q and k / v / dy can be copied (load_tile)
+  int pair_y, pair_qk;         // y (or dv) / dq and dk can be written by pairs
   float *scal;                 // [units][kScal]
-  unsigned char *t3, *m3;      // [units][3][64][64] bf16 tiles, swizzled (lower blocks)
+  unsigned char *t3, *m3;      // [units][3] triangles
   float *s;                    // [units][16-column tiles][dk tiles of 8][lane][4]: S at the chunk's start
-  float *e;                    // [units][64][dv]
+  float *e;                    // [units][tiles][token tiles of 8][lane][4]: E
   float *g;                    // as s, n + 1 a sequence: G at chunk c's start, G_T behind the last
-  float *dz;                   // [units][64][dv]
+  float *dz;                   // as e: dZ
   const float *state_in;
   float *state_out;
   uint16_t *y, *odq, *odk, *odv;
@@ -79,6 +80,40 @@ struct Gdn {
   float *pdq, *pdk;            // [B,T,H,dk] where several heads share a key head
   int32_t *err;
 };
+
+// A triangle: 16 x 16 blocks row by row, each as four 8 x 8 of 8 rows of 16 bytes
+__device__ __forceinline__ constexpr int block_at(int i, int j) { return (i * (i + 1) / 2 + j) * 512; }
+// B fragments (two n-tiles, one k-step) of block (n, k), B[k][n] = tri[n][k] ...
+__device__ __forceinline__ void tri_rows(uint32_t tri, int n, int k, int lane, uint32_t (&r)[4]) {
+  ldsm4(tri + block_at(n, k) + lane * 16, r);
+}
+// ... and of block (k, n), B[k][n] = tri[k][n]
+__device__ __forceinline__ void tri_cols(uint32_t tri, int n, int k, int lane, uint32_t (&r)[4]) {
+  ldsm4_t(tri + block_at(k, n) + ((lane & 8) << 5) + ((lane & 16) << 3) + (lane & 7) * 16, r);
+}
+
+// A sum of many terms as two floats: to about 2^-46 of the largest partial sum
+struct Wide {
+  float hi, lo;
+};
+__device__ __forceinline__ Wide operator+(Wide a, Wide b) {
+  const float s = a.hi + b.hi, d = s - a.hi;
+  const float l = ((a.hi - (s - d)) + (b.hi - d)) + (a.lo + b.lo), hi = s + l;
+  return {hi, l - (hi - s)};
+}
+__device__ __forceinline__ Wide operator-(Wide a, Wide b) { return a + Wide{-b.hi, -b.lo}; }
+__device__ __forceinline__ Wide shfl(Wide x, int lane) {
+  return {__shfl_sync(kFull, x.hi, lane), __shfl_sync(kFull, x.lo, lane)};
+}
+// sums up to each of a warp's lanes
+__device__ __forceinline__ Wide running(Wide x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Wide y{__shfl_up_sync(kFull, x.hi, o), __shfl_up_sync(kFull, x.lo, o)};
+    if (lane >= o) x = y + x;
+  }
+  return x;
+}
 
 __device__ __forceinline__ int length_of(const Gdn &a, int b) {
   return a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
@@ -95,10 +130,10 @@ __device__ __forceinline__ void store_parts3(unsigned char *tiles, uint32_t off,
   for (int i = 0; i < 4; ++i) split<3>(x[2 * i], x[2 * i + 1], s[i]);
 #pragma unroll
   for (int p = 0; p < 3; ++p)
-    *reinterpret_cast<uint4 *>(tiles + p * kTile + off) = make_uint4(s[0][p], s[1][p], s[2][p], s[3][p]);
+    *reinterpret_cast<uint4 *>(tiles + p * kTri + off) = make_uint4(s[0][p], s[1][p], s[2][p], s[3][p]);
 }
 
-// the lower blocks of an fp32 [64][kLd] matrix as three tiles
+// the lower blocks of an fp32 [64][kLd] matrix as three triangles
 __device__ __forceinline__ void write_tiles(const float *x, unsigned char *tiles, int tid) {
   for (int id = tid; id < kC * 8; id += kPrepThreads) {
     const int i = id >> 3, p = id & 7;
@@ -106,7 +141,7 @@ __device__ __forceinline__ void write_tiles(const float *x, unsigned char *tiles
     float v[8];
     *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x + i * kLd + p * 8);
     *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(x + i * kLd + p * 8 + 4);
-    store_parts3(tiles, piece(i, p, 128), v);
+    store_parts3(tiles, block_at(i >> 4, p >> 1) + ((i >> 3) & 1) * 256 + (p & 1) * 128 + (i & 7) * 16, v);
   }
 }
 
@@ -199,43 +234,39 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
   if (live <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.T + c * kC;
   const int hk = h / (a.H / a.Hk);
-  load_tile(sK, rb, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, kC, live, a.dk, a.vec_qk, tid, kPrepThreads);
-  load_tile(sQ, rb, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, kC, live, a.dk, a.vec_qk, tid, kPrepThreads);
+  load_tile<rb, kPrepThreads>(sK, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+  load_tile<rb, kPrepThreads>(sQ, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
   cp_async_commit();
   float *out = a.scal + u * kScal;
   if (w == 0) {
-    // l in units of log2, summed in 64 bits and kept as two floats: a strong
-    // decay early in the chunk costs the later, weak ones nothing
-    double x[2];
+    // l in units of log2, as two floats: a strong decay early in the chunk costs
+    // the later, weak ones nothing
+    Wide x[2];
     bool r[2];
     float be[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
       const bool ok = m < live;
-      const float la = ok ? a.la[(tok + m) * a.H + h] : 0.f;
-      x[i] = static_cast<double>(la < kLeastLog ? kLeastLog : la) * 1.4426950408889634;
+      float la = ok ? a.la[(tok + m) * a.H + h] : 0.f;
+      if (la < kLeastLog) la = kLeastLog;
+      const float hi = la * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596303e-8
+      x[i] = running({hi, fmaf(la, 1.44269502f, -hi) + la * 1.92596303e-8f}, lane);
       r[i] = ok && a.reset && a.reset[tok + m] != 0;
       be[i] = ok ? a.beta[(tok + m) * a.H + h] : 0.f;
       if (fabsf(be[i]) < kTinyBeta) be[i] = copysignf(kTinyBeta, be[i]);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(kFull, x[i], o);
-        if (lane >= o) x[i] += y;
-      }
     }
-    x[1] += __shfl_sync(kFull, x[0], 31);
-    const double end = __shfl_sync(kFull, x[1], 31);
+    x[1] = shfl(x[0], 31) + x[1];
+    const Wide end = shfl(x[1], 31);
     const uint32_t b0 = __ballot_sync(kFull, r[0]), b1 = __ballot_sync(kFull, r[1]);
     const uint32_t upto = 0xffffffffu >> (31 - lane);
     const int seg[2] = {__popc(b0 & upto), __popc(b0) + __popc(b1 & upto)}, last = __popc(b0) + __popc(b1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
-      const float hi = static_cast<float>(x[i]), lo = static_cast<float>(x[i] - hi);
-      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(hi + lo) : 0.f,
-                          seg[i] == last ? umma::ex2_approx(static_cast<float>(end - x[i])) : 0.f,
-                          be[i], hi, lo, __int_as_float(seg[i])};
+      const Wide rest = end - x[i];
+      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(x[i].hi) : 0.f, seg[i] == last ? umma::ex2_approx(rest.hi) : 0.f,
+                          be[i], x[i].hi, x[i].lo, __int_as_float(seg[i])};
 #pragma unroll
       for (int e = 0; e < 6; ++e) {
         sc[e * kC + m] = v[e];
@@ -283,163 +314,296 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
     }
   }
   __syncthreads();
-  write_tiles(sX, a.m3 + u * (3 * kTile), tid);
+  write_tiles(sX, a.m3 + u * (3 * kTri), tid);
   __syncthreads();
   invert(sL, sX, zt, tid);
-  write_tiles(sX, a.t3 + u * (3 * kTile), tid);
+  write_tiles(sX, a.t3 + u * (3 * kTri), tid);
 }
 
 // ---------------------------------------------------------------------------
-// The chains.
+// The chains.  A CTA has W tiles of 16 value columns of one head, each with two
+// warps: the first does what the next chunk waits for (Z, E and the state's
+// update), the second everything else (copies of the next chunk's tiles, y,
+// the products with dy, what is kept for later).  A tile's state lives in shared memory as its three
+// bf16 parts, which are all 24 bits of it, in the order of the A fragments that every
+// product with it takes; so the loops over the key channels need not be unrolled over
+// registers and stay small enough for the instruction caches.
 // ---------------------------------------------------------------------------
-constexpr int kWarps = 4;  // warps of a CTA, 16 value columns each
-
-template <int NK, int PM>  // PM: parts of M
-struct Stage {
+template <int NK, int PM, int W>  // PM: parts of M
+struct Chain {
   static constexpr int rb = NK * 32;
-  static constexpr int K = 0, Q = K + kC * rb, T = Q + kC * rb, M = T + 3 * kTile, V = M + PM * kTile,
-                       sc = V + kC * 128, size = sc + 3 * kC * 4;
+  static constexpr int K = 0, Q = K + kC * rb, T = Q + kC * rb, M = T + 3 * kTri, V = M + PM * kTri, sc = V + kC * 128,
+                       stage = sc + 3 * kC * 4;
+  static constexpr int state = 2 * stage, tokens = state + W * NK * 3 * 512, size = tokens + W * 8 * 512;
 };
 
-// copies of chunk c's tiles into one stage; cols: the value columns' tensor
-template <int NK, int PM>
+// the second warps' copies of a chunk's tiles; cols: the value columns' tensor
+template <int NK, int PM, int W>
 __device__ __forceinline__ void load_stage(unsigned char *st, const Gdn &a, int64_t u, int64_t tok, int h, int col0,
-                                           int live, const uint16_t *cols, int64_t ld_cols, bool vec_cols, int tid,
-                                           int threads) {
-  using L = Stage<NK, PM>;
+                                           int live, const uint16_t *cols, int64_t ld_cols, int by_cols, int tid) {
+  using L = Chain<NK, PM, W>;
+  constexpr int threads = 32 * W;
   const int hk = h / (a.H / a.Hk);
-  load_tile(st + L::K, L::rb, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, kC, live, a.dk, a.vec_qk, tid, threads);
-  load_tile(st + L::Q, L::rb, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, kC, live, a.dk, a.vec_qk, tid, threads);
-  load_tile(st + L::V, 128, cols + tok * ld_cols + h * a.dv + col0, ld_cols, kC, live, min(64, a.dv - col0), vec_cols,
-            tid, threads);
-  const unsigned char *t3 = a.t3 + u * (3 * kTile), *m3 = a.m3 + u * (3 * kTile);
+  load_tile<L::rb, threads>(st + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+  load_tile<L::rb, threads>(st + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  load_tile<128, threads>(st + L::V, cols + tok * ld_cols + h * a.dv + col0, ld_cols, live, min(16 * W, a.dv - col0),
+                          by_cols, tid);
+  const unsigned char *t3 = a.t3 + u * (3 * kTri), *m3 = a.m3 + u * (3 * kTri);
   const uint32_t dT = smem_u32(st + L::T), dM = smem_u32(st + L::M), ds = smem_u32(st + L::sc);
-  for (int id = tid; id < 3 * kTile / 16; id += threads) {
-    // of each tile's 64 rows of 8 pieces only the lower blocks hold anything
-    const int r = (id >> 3) & 63, p = (id & 7) ^ (r & 7);
-    if (p > 2 * (r >> 4) + 1) continue;
-    copy16(dT + id * 16, t3 + id * 16, true);
-    if (id < PM * (kTile / 16)) copy16(dM + id * 16, m3 + id * 16, true);
-  }
+#pragma unroll 8
+  for (int id = tid; id < 3 * kTri / 16; id += threads) copy_async<16>(dT + id * 16, t3 + id * 16, true);
+#pragma unroll 8
+  for (int id = tid; id < PM * kTri / 16; id += threads) copy_async<16>(dM + id * 16, m3 + id * 16, true);
   const float *sc = a.scal + u * kScal;
-  for (int id = tid; id < 3 * kC / 4; id += threads) copy16(ds + id * 16, sc + id * 4, true);
+  for (int id = tid; id < 3 * kC / 4; id += threads) copy_async<16>(ds + id * 16, sc + id * 4, true);
   cp_async_commit();
 }
 
-// S^T of one warp's 16 columns: its registers and a [dk][dv] matrix
+// S^T of 16 columns and 8 NT rows of a [dk][dv] matrix as an accumulator, and back
 template <int NT>
-__device__ __forceinline__ void read_state(const float *m, int dk, int dv, int col, int lane, float (&S)[NT][4]) {
+__device__ __forceinline__ void read_state(const float *m, int row, int dk, int dv, int col, int lane, float (&S)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 8 * nt + 2 * t + (e & 1), c = col + g + 8 * (e >> 1);
+      const int r = row + 8 * nt + 2 * t + (e & 1), c = col + g + 8 * (e >> 1);
       S[nt][e] = m && r < dk && c < dv ? m[static_cast<int64_t>(r) * dv + c] : 0.f;
     }
 }
 template <int NT>
-__device__ __forceinline__ void write_state(float *m, int dk, int dv, int col, int lane, const float (&S)[NT][4]) {
+__device__ __forceinline__ void write_state(float *m, int row, int dk, int dv, int col, int lane, const float (&S)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 8 * nt + 2 * t + (e & 1), c = col + g + 8 * (e >> 1);
+      const int r = row + 8 * nt + 2 * t + (e & 1), c = col + g + 8 * (e >> 1);
       if (r < dk && c < dv) m[static_cast<int64_t>(r) * dv + c] = S[nt][e];
     }
 }
-// ... and its fragments in a row, 16 bytes a lane
-template <int NT>
-__device__ __forceinline__ void keep_state(float *m, int lane, const float (&S)[NT][4]) {
+// accumulators in a row, 16 bytes a lane
+template <int N>
+__device__ __forceinline__ void put(float4 *m, int lane, const float (&x)[N][4]) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-    reinterpret_cast<float4 *>(m)[nt * 32 + lane] = make_float4(S[nt][0], S[nt][1], S[nt][2], S[nt][3]);
+  for (int i = 0; i < N; ++i) m[i * 32 + lane] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+}
+template <int N>
+__device__ __forceinline__ void get(const float4 *m, int lane, float (&x)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float4 v = m[i * 32 + lane];
+    x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void clear(float (&x)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+}
+// the parts of a k-step's A fragments of a state, and the state that they are
+__device__ __forceinline__ void put_parts(uint4 *m, int lane, const float (&c0)[4], const float (&c1)[4]) {
+  uint32_t s[3][4];
+  a_split<3>(c0, c1, s);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) m[p * 32 + lane] = make_uint4(s[p][0], s[p][1], s[p][2], s[p][3]);
+}
+__device__ __forceinline__ void get_parts(const uint4 *m, int lane, uint32_t (&s)[3][4]) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const uint4 v = m[p * 32 + lane];
+    s[p][0] = v.x, s[p][1] = v.y, s[p][2] = v.z, s[p][3] = v.w;
+  }
+}
+__device__ __forceinline__ void join(const uint32_t (&s)[3][4], float (&c0)[4], float (&c1)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float(&c)[4] = i < 2 ? c0 : c1;
+    c[2 * (i & 1)] = low2(s[0][i]) + (low2(s[1][i]) + low2(s[2][i]));
+    c[2 * (i & 1) + 1] = high2(s[0][i]) + (high2(s[1][i]) + high2(s[2][i]));
+  }
+}
+// x[nt][.] *= f[token]: a token-wise factor on an accumulator whose columns are tokens
+template <int N>
+__device__ __forceinline__ void scale_tokens(float (&x)[N][4], const float *f, int t) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 v = *reinterpret_cast<const float2 *>(f + 8 * i + 2 * t);
+    x[i][0] *= v.x, x[i][1] *= v.y, x[i][2] *= v.x, x[i][3] *= v.y;
+  }
 }
 
-// a warp's [16 columns][64 tokens] accumulator into fp32 [64][dv]
-__device__ __forceinline__ void keep_tokens(float *m, int dv, int col, int lane, const float (&x)[8][4]) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 8 * nt + 2 * t + (e & 1), c = col + g + 8 * (e >> 1);
-      if (c < dv) m[i * dv + c] = x[nt][e];
-    }
-}
-
-// d[n] += the product of A's parts and B's parts, n-tiles 2 np and 2 np + 1, whose
-// part numbers sum up to less than max(PA, PB): what the others hold is below the last bit kept
+// d (the leading parts' product) and l (the others') += A B for n-tiles 2 np and
+// 2 np + 1, over the parts whose numbers sum up to less than max(PA, PB): what
+// the others hold is below the last bit kept.  The tensor cores cut sums off
+// where an addition would round; kept apart, the many small products do so
+// at their own size.
 template <int PA, int PB, int N>
-__device__ __forceinline__ void products(float (&d)[N][4], int np, const uint32_t (&a)[PA][4], const uint32_t (&b)[PB][4]) {
+__device__ __forceinline__ void products(float (&d)[N][4], float (&l)[N][4], int np, const uint32_t (&a)[PA][4],
+                                         const uint32_t (&b)[PB][4]) {
   constexpr int most = PA > PB ? PA : PB;
 #pragma unroll
   for (int i = 0; i < PA; ++i)
 #pragma unroll
     for (int j = 0; j < PB; ++j)
       if (i + j < most) {
-        fma16816(d[2 * np], a[i], b[j][0], b[j][1]);
-        fma16816(d[2 * np + 1], a[i], b[j][2], b[j][3]);
+        float(&to)[N][4] = i + j == 0 ? d : l;
+        fma16816(to[2 * np], a[i], b[j][0], b[j][1]);
+        fma16816(to[2 * np + 1], a[i], b[j][2], b[j][3]);
+      }
+}
+template <int N>
+__device__ __forceinline__ void add(float (&d)[N][4], const float (&l)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[i][e] += l[i][e];
+}
+
+// the three parts of an accumulator over 64 tokens, as A fragments of its four k-steps
+__device__ __forceinline__ void split_tokens(const float (&x)[8][4], uint32_t (&a)[4][3][4]) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) a_split<3>(x[2 * ks], x[2 * ks + 1], a[ks]);
+}
+
+// acc = A B for n-tiles 4 quad .. 4 quad + 3, B = tile[token][n] exact, over 64
+// tokens: the small parts first
+template <int RB>
+__device__ __forceinline__ void quad_product(uint32_t tile, int quad, const uint32_t (&a)[4][3][4], int lane,
+                                             float (&acc)[4][4]) {
+  uint32_t r[4][2][4];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) b_cols(tile, RB, 32 * quad + 16 * x, 16 * ks, lane, r[ks][x]);
+  clear(acc);
+#pragma unroll
+  for (int p = 2; p >= 0; --p)
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        fma16816(acc[2 * x], a[ks][p], r[ks][x][0], r[ks][x][1]);
+        fma16816(acc[2 * x + 1], a[ks][p], r[ks][x][2], r[ks][x][3]);
       }
 }
 
+// state <- factor state + sign acc for n-tiles 4 quad .. 4 quad + 3; x: its new values
+__device__ __forceinline__ void update_quad(uint4 *parts, int quad, int lane, float factor, float sign,
+                                            const float (&acc)[4][4], float (&x)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint4 *m = parts + (2 * quad + i) * 96;
+    uint32_t s[3][4];
+    get_parts(m, lane, s);
+    join(s, x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[2 * i + j][e] = fmaf(factor, x[2 * i + j][e], sign * acc[2 * i + j][e]);
+    put_parts(m, lane, x[2 * i], x[2 * i + 1]);
+  }
+}
+
+// d = the state's product with tile[token][key channel]
 template <int NK>
-__global__ void __launch_bounds__(kWarps * 32, 1) gdn_chain(const Gdn a) {
-  using L = Stage<NK, 2>;
+__device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile, int lane, float (&d)[8][4]) {
+  float l[8][4];
+  clear(d);
+  clear(l);
+#pragma unroll 2
+  for (int ks = 0; ks < NK; ++ks) {
+    uint32_t s[3][4], r[4][4];
+    get_parts(parts + ks * 96, lane, s);
+#pragma unroll
+    for (int np = 0; np < 4; ++np) b_rows(tile, NK * 32, 16 * np, 16 * ks, lane, r[np]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        float(&to)[8][4] = p == 0 ? d : l;
+        fma16816(to[2 * np], s[p], r[np][0], r[np][1]);
+        fma16816(to[2 * np + 1], s[p], r[np][2], r[np][3]);
+      }
+  }
+  add(d, l);
+}
+
+// d = X T^T (BACK: X T), X [16 columns][64 tokens] in three parts, T a triangle in three
+template <bool BACK>
+__device__ __forceinline__ void triangle_product(const float (&x)[8][4], uint32_t tri, int lane, float (&d)[8][4]) {
+  float l[8][4];
+  clear(d);
+  clear(l);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    uint32_t a[3][4];
+    a_split<3>(x[2 * ks], x[2 * ks + 1], a);
+#pragma unroll
+    for (int np = BACK ? 0 : ks; np < (BACK ? ks + 1 : 4); ++np) {
+      uint32_t r[3][4];
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        BACK ? tri_cols(tri + p * kTri, np, ks, lane, r[p]) : tri_rows(tri + p * kTri, np, ks, lane, r[p]);
+      products(d, l, np, a, r);
+    }
+  }
+  add(d, l);
+}
+
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id + 1) : "memory"); }
+
+// a state's parts from and to a [dk][dv] matrix
+template <int NK>
+__device__ __forceinline__ void load_state(uint4 *parts, const float *m, int dk, int dv, int col, int lane) {
+#pragma unroll 1
+  for (int ks = 0; ks < NK; ++ks) {
+    float x[2][4];
+    read_state<2>(m, 16 * ks, dk, dv, col, lane, x);
+    put_parts(parts + ks * 96, lane, x[0], x[1]);
+  }
+}
+template <int NK>
+__device__ __forceinline__ void store_state(const uint4 *parts, float *m, int dk, int dv, int col, int lane) {
+#pragma unroll 1
+  for (int ks = 0; ks < NK; ++ks) {
+    uint32_t s[3][4];
+    float x[2][4];
+    get_parts(parts + ks * 96, lane, s);
+    join(s, x[0], x[1]);
+    write_state<2>(m, 16 * ks, dk, dv, col, lane, x);
+  }
+}
+
+template <int NK, int W>
+__global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
+  using L = Chain<NK, 2, W>;
   constexpr int NT = 2 * NK, rb = L::rb;
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, threads = blockDim.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int tiles = (a.dv + 15) >> 4, groups = (tiles + kWarps - 1) / kWarps;
+  const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const bool second = tid >= 32 * W;
+  const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
   const int64_t bh = blockIdx.x / groups;
-  const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * kWarps), col = col0 + 16 * w;
+  const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
   const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
   const int len = length_of(a, b), n = (len + kC - 1) / kC;
   const int64_t tok = static_cast<int64_t>(b) * a.T;
-  if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-  const bool mine = col < a.dv;  // else the warp only helps with the copies
+  const bool mine = col < a.dv;  // else the warps only help with the copies
+  uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96;
+  float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;
 
-  float S[NT][4];
-  read_state<NT>(a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane, S);
-  if (n > 0)
-    load_stage<NK, 2>(sm, a, bh * a.n, tok, h, col0, min(len, kC), a.v, a.ld_v, a.vec_v, tid, threads);
-  for (int c = 0; c < n; ++c) {
-    const int64_t u = bh * a.n + c;
-    if (c + 1 < n) {
-      load_stage<NK, 2>(sm + ((c + 1) & 1) * L::size, a, u + 1, tok + (c + 1) * kC, h, col0, min(len - (c + 1) * kC, kC),
-                        a.v, a.ld_v, a.vec_v, tid, threads);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
-    __syncthreads();
-    if (mine) {
-      unsigned char *st = sm + (c & 1) * L::size;
-      const uint32_t uK = smem_u32(st + L::K), uQ = smem_u32(st + L::Q), uT = smem_u32(st + L::T),
-                     uM = smem_u32(st + L::M), uV = smem_u32(st + L::V);
+  if (!second) {
+    if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
+    load_state<NK>(hS, a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane);
+    for (int c = 0; c < n; ++c) {
+      __syncthreads();
+      if (!mine) continue;
+      unsigned char *st = sm + (c & 1) * L::stage;
+      const uint32_t uK = smem_u32(st + L::K), uV = smem_u32(st + L::V);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
-      keep_state<NT>(a.s + (u * tiles + (col >> 4)) * (NT * 128), lane, S);
-      // S^T K^T and S^T Q^T
-      float E[8][4], Y[8][4], Z[8][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) E[i][e] = Y[i][e] = Z[i][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        uint32_t s[3][4];
-        a_split<3>(S[2 * ks], S[2 * ks + 1], s);
-        const uint32_t s2[2][4] = {{s[0][0], s[0][1], s[0][2], s[0][3]}, {s[1][0], s[1][1], s[1][2], s[1][3]}};
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t r[1][4];
-          b_rows(uK, rb, 16 * np, 16 * ks, lane, r[0]);
-          products(Z, np, s, r);
-          b_rows(uQ, rb, 16 * np, 16 * ks, lane, r[0]);
-          products(Y, np, s2, r);
-        }
-      }
-      // Z^T = V^T - gam S^T K^T; gam S^T Q^T
+      float Z[8][4], E[8][4];
+      state_product<NK>(hS, uK, lane, Z);
+      // Z^T = V^T - gam S^T K^T
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t v[4];
@@ -451,151 +615,190 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gdn_chain(const Gdn a) {
           const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * nt + 2 * t);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float gg = e & 1 ? gm.y : gm.x;
             const uint32_t vv = v[2 * x + (e >> 1)];
-            Z[nt][e] = fmaf(-gg, Z[nt][e], e & 1 ? high2(vv) : low2(vv));
-            Y[nt][e] *= gg;
+            Z[nt][e] = fmaf(e & 1 ? -gm.y : -gm.x, Z[nt][e], e & 1 ? high2(vv) : low2(vv));
           }
         }
       }
-      // E^T = Z^T T^T
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t z[3][4];
-        a_split<3>(Z[2 * ks], Z[2 * ks + 1], z);
-#pragma unroll
-        for (int np = ks; np < 4; ++np) {
-          uint32_t r[3][4];
-#pragma unroll
-          for (int p = 0; p < 3; ++p) b_rows(uT + p * kTile, 128, 16 * np, 16 * ks, lane, r[p]);
-          products(E, np, z, r);
-        }
-      }
-      keep_tokens(a.e + u * kC * a.dv, a.dv, col, lane, E);
-      // U = beta E;  Y^T += U^T M^T;  S^T = gam_C S^T + (tail U)^T K
+      triangle_product<false>(Z, smem_u32(st + L::T), lane, E);
+      put(hE, lane, E);
+      pair_sync(w);  // E is there, S has been read
+      // S^T = gam_C S^T + (tail U)^T K
+      scale_tokens(E, beta, t);
+      scale_tokens(E, tail, t);
+      uint32_t ut[4][3][4];
+      split_tokens(E, ut);
       const float end = gam[kC - 1];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[nt][e] *= end;
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) E[nt][e] *= e & 1 ? be.y : be.x;
+#pragma unroll 1
+      for (int q = 0; q < NK / 2; ++q) {
+        float acc[4][4], x[4][4];
+        quad_product<rb>(uK, q, ut, lane, acc);
+        update_quad(hS, q, lane, end, 1.f, acc, x);
       }
+    }
+    if (mine) store_state<NK>(hS, a.state_out + bh * a.dk * a.dv, a.dk, a.dv, col, lane);
+    return;
+  }
+
+  const int ltid = tid - 32 * W;
+  if (n > 0) load_stage<NK, 2, W>(sm, a, bh * a.n, tok, h, col0, min(len, kC), a.v, a.ld_v, a.by_v, ltid);
+  for (int c = 0; c < n; ++c) {
+    const int64_t u = bh * a.n + c;
+    cp_async_wait<0>();
+    __syncthreads();
+    if (c + 1 < n)
+      load_stage<NK, 2, W>(sm + ((c + 1) & 1) * L::stage, a, u + 1, tok + (c + 1) * kC, h, col0,
+                           min(len - (c + 1) * kC, kC), a.v, a.ld_v, a.by_v, ltid);
+    if (!mine) continue;
+    unsigned char *st = sm + (c & 1) * L::stage;
+    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(st + L::M);
+    const float *gam = reinterpret_cast<const float *>(st + L::sc), *beta = gam + 2 * kC;
+    float Y[8][4], E[8][4];
+    clear(Y);
+    {  // Y^T = gam S^T Q^T; S is kept
+      float4 *kept = reinterpret_cast<float4 *>(a.s) + (u * tiles + (col >> 4)) * (NT * 32);
+#pragma unroll 2
+      for (int ks = 0; ks < NK; ++ks) {
+        uint32_t s[3][4], r[4][4];
+        float x[2][4];
+        get_parts(hS + ks * 96, lane, s);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t us[2][4];
-        a_split<2>(E[2 * ks], E[2 * ks + 1], us);
+        for (int np = 0; np < 4; ++np) b_rows(uQ, rb, 16 * np, 16 * ks, lane, r[np]);
+        join(s, x[0], x[1]);
+        put(kept + 64 * ks, lane, x);
 #pragma unroll
-        for (int np = ks; np < 4; ++np) {
-          uint32_t r[2][4];
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) b_rows(uM + p * kTile, 128, 16 * np, 16 * ks, lane, r[p]);
-          products(Y, np, us, r);
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float2 tl = *reinterpret_cast<const float2 *>(tail + 8 * (2 * ks + x) + 2 * t);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) E[2 * ks + x][e] *= e & 1 ? tl.y : tl.x;
-        }
-        uint32_t ut[3][4];
-        a_split<3>(E[2 * ks], E[2 * ks + 1], ut);
-#pragma unroll
-        for (int np = 0; np < NK; ++np) {
-          uint32_t r[1][4];
-          b_cols(uK, rb, 16 * np, 16 * ks, lane, r[0]);
-          products(S, np, ut, r);
-        }
-      }
-      // y, rounded once: pairs of tokens turned into pairs of columns
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const int i = c * kC + 8 * nt + g;
-        uint16_t *row = a.y + ((tok + i) * a.H + h) * a.dv;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t v = transpose8(pack2(Y[nt][2 * x], Y[nt][2 * x + 1]));
-          const int cc = col + 8 * x + 2 * t;
-          if (i >= len) continue;
-          if (a.vec_y && cc + 1 < a.dv) {
-            *reinterpret_cast<uint32_t *>(row + cc) = v;
-          } else {
-            if (cc < a.dv) row[cc] = static_cast<uint16_t>(v);
-            if (cc + 1 < a.dv) row[cc + 1] = static_cast<uint16_t>(v >> 16);
+          for (int np = 0; np < 4; ++np) {
+            fma16816(Y[2 * np], s[p], r[np][0], r[np][1]);
+            fma16816(Y[2 * np + 1], s[p], r[np][2], r[np][3]);
           }
+      }
+      scale_tokens(Y, gam, t);
+    }
+    pair_sync(w);
+    get(hE, lane, E);
+    put(reinterpret_cast<float4 *>(a.e) + (u * tiles + (col >> 4)) * 256, lane, E);
+    scale_tokens(E, beta, t);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {  // += U^T M^T
+      uint32_t us[2][4];
+      a_split<2>(E[2 * ks], E[2 * ks + 1], us);
+#pragma unroll
+      for (int np = ks; np < 4; ++np) {
+        uint32_t r[2][4];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, np, ks, lane, r[p]);
+        products(Y, Y, np, us, r);
+      }
+    }
+    // y, rounded once: pairs of tokens turned into pairs of columns
+    uint16_t *yc = a.y + (tok * a.H + h) * a.dv + col + 2 * t;
+    const int left = a.dv - col - 2 * t;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const int i = c * kC + 8 * nt + g;
+      uint16_t *row = yc + i * (static_cast<int64_t>(a.H) * a.dv);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t v = transpose8(pack2(Y[nt][2 * x], Y[nt][2 * x + 1]));
+        if (i >= len) continue;
+        if (a.pair_y) {
+          if (8 * x < left) *reinterpret_cast<uint32_t *>(row + 8 * x) = v;
+        } else {
+          if (8 * x < left) row[8 * x] = static_cast<uint16_t>(v);
+          if (8 * x + 1 < left) row[8 * x + 1] = static_cast<uint16_t>(v >> 16);
         }
       }
     }
-    __syncthreads();
   }
-  if (mine) write_state<NT>(a.state_out + bh * a.dk * a.dv, a.dk, a.dv, col, lane, S);
 }
 
-template <int NK>
-__global__ void __launch_bounds__(kWarps * 32, 1) gdn_chain_back(const Gdn a) {
-  using L = Stage<NK, 3>;
+template <int NK, int W>
+__global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
+  using L = Chain<NK, 3, W>;
   constexpr int NT = 2 * NK, rb = L::rb;
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, threads = blockDim.x, w = tid >> 5, lane = tid & 31, t = lane & 3;
-  const int tiles = (a.dv + 15) >> 4, groups = (tiles + kWarps - 1) / kWarps;
+  const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, t = lane & 3;
+  const bool second = tid >= 32 * W;
+  const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
   const int64_t bh = blockIdx.x / groups;
-  const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * kWarps), col = col0 + 16 * w;
+  const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
   const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
   const int len = length_of(a, b), n = (len + kC - 1) / kC;
   const int64_t tok = static_cast<int64_t>(b) * a.T, ld_y = static_cast<int64_t>(a.H) * a.dv;
-  if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   const bool mine = col < a.dv;
+  uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96;
+  float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
 
-  float S[NT][4];  // G^T
-  read_state<NT>(a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane, S);
-  float *kept = a.g + (bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 128);
-  const int64_t step = static_cast<int64_t>(tiles) * (NT * 128);
-  if (mine) keep_state<NT>(kept + n * step, lane, S);
-  if (n > 0)
-    load_stage<NK, 3>(sm + ((n - 1) & 1) * L::size, a, bh * a.n + n - 1, tok + (n - 1) * kC, h, col0,
-                      min(len - (n - 1) * kC, kC), a.dy, ld_y, a.vec_dy, tid, threads);
-  for (int c = n - 1; c >= 0; --c) {
-    const int64_t u = bh * a.n + c;
-    if (c > 0) {
-      load_stage<NK, 3>(sm + ((c - 1) & 1) * L::size, a, u - 1, tok + (c - 1) * kC, h, col0, kC, a.dy, ld_y, a.vec_dy, tid,
-                        threads);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
-    __syncthreads();
-    if (mine) {
-      unsigned char *st = sm + (c & 1) * L::size;
-      const uint32_t uK = smem_u32(st + L::K), uQ = smem_u32(st + L::Q), uT = smem_u32(st + L::T),
-                     uM = smem_u32(st + L::M), uY = smem_u32(st + L::V);
+  if (!second) {
+    if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
+    load_state<NK>(hG, a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane);
+    float4 *kept = reinterpret_cast<float4 *>(a.g) + (bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 32);
+    const int64_t step = static_cast<int64_t>(tiles) * (NT * 32);
+    if (mine)
+#pragma unroll 1
+      for (int ks = 0; ks < NK; ++ks) {
+        uint32_t s[3][4];
+        float x[2][4];
+        get_parts(hG + ks * 96, lane, s);
+        join(s, x[0], x[1]);
+        put(kept + n * step + ks * 64, lane, x);
+      }
+    for (int c = n - 1; c >= 0; --c) {
+      __syncthreads();
+      if (!mine) continue;
+      unsigned char *st = sm + (c & 1) * L::stage;
+      const uint32_t uK = smem_u32(st + L::K);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
       // dU^T = tail G^T K^T + dY^T M
       float U[8][4], Z[8][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) U[i][e] = Z[i][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        uint32_t s[3][4];
-        a_split<3>(S[2 * ks], S[2 * ks + 1], s);
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t r[1][4];
-          b_rows(uK, rb, 16 * np, 16 * ks, lane, r[0]);
-          products(U, np, s, r);
-        }
+      state_product<NK>(hG, uK, lane, U);
+      scale_tokens(U, tail, t);
+      pair_sync(w);  // dY^T M is there, G has been read
+      get(hZ, lane, Z);
+      add(U, Z);
+      scale_tokens(U, beta, t);
+      triangle_product<true>(U, smem_u32(st + L::T), lane, Z);  // dZ^T
+      put(hZ, lane, Z);
+      // G^T = gam_C G^T + (gam dY)^T Q, by the second warp, - (gam dZ)^T K
+      scale_tokens(Z, gam, t);
+      uint32_t zt[4][3][4];
+      split_tokens(Z, zt);
+      pair_sync(w);
+      float4 *to = kept + c * step;
+#pragma unroll 1
+      for (int q = 0; q < NK / 2; ++q) {
+        float acc[4][4], x[4][4];
+        quad_product<rb>(uK, q, zt, lane, acc);
+        update_quad(hG, q, lane, 1.f, -1.f, acc, x);
+        put(to + q * 128, lane, x);
       }
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 tl = *reinterpret_cast<const float2 *>(tail + 8 * nt + 2 * t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) U[nt][e] *= e & 1 ? tl.y : tl.x;
-      }
-      uint32_t y[4][1][4];
+    }
+    if (mine) store_state<NK>(hG, a.state_out + bh * a.dk * a.dv, a.dk, a.dv, col, lane);
+    return;
+  }
+
+  const int ltid = tid - 32 * W;
+  if (n > 0)
+    load_stage<NK, 3, W>(sm + ((n - 1) & 1) * L::stage, a, bh * a.n + n - 1, tok + (n - 1) * kC, h, col0,
+                         min(len - (n - 1) * kC, kC), a.dy, ld_y, a.by_dy, ltid);
+  for (int c = n - 1; c >= 0; --c) {
+    const int64_t u = bh * a.n + c;
+    cp_async_wait<0>();
+    __syncthreads();
+    if (c > 0)
+      load_stage<NK, 3, W>(sm + ((c - 1) & 1) * L::stage, a, u - 1, tok + (c - 1) * kC, h, col0, kC, a.dy, ld_y, a.by_dy,
+                           ltid);
+    if (!mine) continue;
+    unsigned char *st = sm + (c & 1) * L::stage;
+    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(st + L::M), uY = smem_u32(st + L::V);
+    const float *gam = reinterpret_cast<const float *>(st + L::sc);
+    uint32_t y[4][1][4];
+    {
+      float R[8][4], l[8][4];
+      clear(R);
+      clear(l);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         a_cols(uY, 128, 16 * w, 16 * ks, lane, y[ks][0]);
@@ -603,91 +806,82 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gdn_chain_back(const Gdn a) {
         for (int np = 0; np <= ks; ++np) {
           uint32_t r[3][4];
 #pragma unroll
-          for (int p = 0; p < 3; ++p) b_cols(uM + p * kTile, 128, 16 * np, 16 * ks, lane, r[p]);
-          products(U, np, y[ks], r);
+          for (int p = 0; p < 3; ++p) tri_cols(uM + p * kTri, np, ks, lane, r[p]);
+          products(R, l, np, y[ks], r);
         }
       }
-      // dZ^T = (beta dU)^T T
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) U[nt][e] *= e & 1 ? be.y : be.x;
-      }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t x[3][4];
-        a_split<3>(U[2 * ks], U[2 * ks + 1], x);
-#pragma unroll
-        for (int np = 0; np <= ks; ++np) {
-          uint32_t r[3][4];
-#pragma unroll
-          for (int p = 0; p < 3; ++p) b_cols(uT + p * kTile, 128, 16 * np, 16 * ks, lane, r[p]);
-          products(Z, np, x, r);
-        }
-      }
-      keep_tokens(a.dz + u * kC * a.dv, a.dv, col, lane, Z);
-      // G^T = gam_C G^T + (gam dY)^T Q - (gam dZ)^T K
-      const float end = gam[kC - 1];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[nt][e] *= end;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        float d[2][4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * (2 * ks + x) + 2 * t);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float gg = e & 1 ? gm.y : gm.x;
-            const uint32_t v = y[ks][0][2 * x + (e >> 1)];
-            d[x][e] = gg * (e & 1 ? high2(v) : low2(v));
-            Z[2 * ks + x][e] *= -gg;
-          }
-        }
-        uint32_t dy3[3][4], dz3[3][4];
-        a_split<3>(d[0], d[1], dy3);
-        a_split<3>(Z[2 * ks], Z[2 * ks + 1], dz3);
-#pragma unroll
-        for (int np = 0; np < NK; ++np) {
-          uint32_t r[1][4];
-          b_cols(uQ, rb, 16 * np, 16 * ks, lane, r[0]);
-          products(S, np, dy3, r);
-          b_cols(uK, rb, 16 * np, 16 * ks, lane, r[0]);
-          products(S, np, dz3, r);
-        }
-      }
-      keep_state<NT>(kept + c * step, lane, S);
+      add(R, l);
+      put(hZ, lane, R);
     }
-    __syncthreads();
+    uint32_t d3[4][3][4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      float d[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * (2 * ks + x) + 2 * t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t v = y[ks][0][2 * x + (e >> 1)];
+          d[x][e] = e & 1 ? gm.y * high2(v) : gm.x * low2(v);
+        }
+      }
+      a_split<3>(d[0], d[1], d3[ks]);
+    }
+    pair_sync(w);
+    const float end = gam[kC - 1];
+#pragma unroll 1
+    for (int q = 0; q < NK / 2; ++q) {
+      float acc[4][4], x[4][4];
+      quad_product<rb>(uQ, q, d3, lane, acc);
+      update_quad(hG, q, lane, end, 1.f, acc, x);
+    }
+    pair_sync(w);
+    float Z[8][4];
+    get(hZ, lane, Z);
+    put(reinterpret_cast<float4 *>(a.dz) + (u * tiles + (col >> 4)) * 256, lane, Z);
   }
-  if (mine) write_state<NT>(a.state_out + bh * a.dk * a.dv, a.dk, a.dv, col, lane, S);
 }
 
 // ---------------------------------------------------------------------------
-// gdn_grad: the gradients of one chunk of one head.  Eight warps: warp (mi, nj)
-// has tokens 16 mi .. +15 and half nj of the key channels (of the tokens j, for X and
-// N).  The value columns come 64 at a time: E, dZ and the two states are read
-// as fp32, split into bf16 parts and stored as tiles.
+// gdn_grad: the gradients of one chunk of one head.  A warp has an eighth of
+// the key channels for 32 tokens, so each element of the two states is needed by
+// two warps only: straight from memory, where the chains left it in fragment
+// order, split into bf16 parts and turned (8 x 8 at a time) into the B
+// fragments of the sums over value columns.  U and dZ are shared: split once, into A fragments
+// in shared memory (an A fragment of U holds the B fragments of U^T).
+// Value columns come 128 at a time.
 // ---------------------------------------------------------------------------
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 
 template <int NK>
-struct GradSmem {
+struct Grad {
   static constexpr int rb = NK * 32;
-  static constexpr int K = 0, Q = K + kC * rb, Y = Q + kC * rb, U = Y + kTile, Z = U + 3 * kTile, S = Z + 2 * kTile,
-                       G = S + 3 * 64 * rb, sc = G + 2 * 64 * rb, size = sc + (kScal + 4 * kC + 16) * 4;
-  static constexpr int X = U, N = Z;  // once the value columns are done: X in three parts, N + N^T in two
+  static constexpr int K = 0, Q = K + kC * rb, Y = Q + kC * rb, V = Y + 2 * kTile, U = V + 2 * kTile,
+                       Z = U + 8 * 3 * 4 * 512, sc = Z + 8 * 2 * 4 * 512,
+                       size = sc + (kScal + 8 * 3 * kC + 8) * 4;
+  static constexpr int X = U, N = X + 3 * kTile;  // once the value columns are done: X in three parts, N + N^T in two
 };
+
+// lanes 4 x + t hold v[16]; the sums over x, two of them a lane (bits 3..1 of the value are the lane's bits 4..2)
+__device__ __forceinline__ void sum_rows(float (&v)[16], int lane) {
+#pragma unroll
+  for (int o = 16; o >= 4; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o / 2; ++i) {
+      const float send = up ? v[i] : v[i + o / 2], keep = up ? v[i + o / 2] : v[i];
+      v[i] = keep + __shfl_xor_sync(kFull, send, o);
+    }
+  }
+}
 
 template <int NK>
 __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
-  using L = GradSmem<NK>;
-  constexpr int rb = L::rb, NT = 2 * NK, NP = NK / 2;  // NP: pairs of n-tiles in half the key channels
+  using L = Grad<NK>;
+  constexpr int rb = L::rb, NT = 2 * NK, NW = NK / 4;  // NW: n-tiles of key channels a warp
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, mi = w & 3, nj = w >> 2;
+  const int tid = threadIdx.x, w = (tid >> 5) & 7, half = tid >> 8, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x, bh = u / a.n;
   const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
   const int live = min(length_of(a, b) - c * kC, kC);
@@ -696,211 +890,207 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
   const int hk = h / (a.H / a.Hk), tiles = (a.dv + 15) >> 4;
   float *sc = reinterpret_cast<float *>(sm + L::sc);
   float *gam = sc, *tail = sc + kC, *beta = sc + 2 * kC, *lh = sc + 3 * kC, *ll = sc + 4 * kC, *sg = sc + 5 * kC;
-  float *rowEZ = sc + kScal, *rowVZ = rowEZ + kC, *flow = rowVZ + kC /* [2][64] */, *red = flow + 2 * kC;
-  load_tile(sm + L::K, rb, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, kC, live, a.dk, a.vec_qk, tid, kGradThreads);
-  load_tile(sm + L::Q, rb, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, kC, live, a.dk, a.vec_qk, tid, kGradThreads);
-  for (int i = tid; i < kScal; i += kGradThreads) sc[i] = a.scal[u * kScal + i];
-  const uint32_t uK = smem_u32(sm + L::K), uQ = smem_u32(sm + L::Q), uY = smem_u32(sm + L::Y), uU = smem_u32(sm + L::U),
-                 uZ = smem_u32(sm + L::Z), uS = smem_u32(sm + L::S), uG = smem_u32(sm + L::G);
+  float *rows = sc + kScal /* [8][2][64]: dZ . E and v . dZ */, *flow = rows + 8 * 2 * kC /* [8][64] */,
+        *red = flow + 8 * kC;
+  load_tile<rb, kGradThreads>(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+  load_tile<rb, kGradThreads>(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
+  if (w >= tiles) rows[(2 * w + half) * kC + lane] = rows[(2 * w + half) * kC + 32 + lane] = 0.f;
+  uint4 *sU = reinterpret_cast<uint4 *>(sm + L::U), *sZ = reinterpret_cast<uint4 *>(sm + L::Z);
+  const uint32_t uY = smem_u32(sm + L::Y), uV = smem_u32(sm + L::V);
 
-  float dQ[2 * NP][4], dA[2 * NP][4], dK[2 * NP][4], X[4][4], N[4][4];
+  // m-tiles 2 half and 2 half + 1
+  float dQ[2][NW][4], dA[2][NW][4], dK[2][NW][4], X[2][4], N[2][4];
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dQ[i][e] = dA[i][e] = dK[i][e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) X[i][e] = N[i][e] = 0.f;
-  float ez = 0.f, vz = 0.f, anchor = 0.f;
-  const int row = tid >> 2, part = tid & 3;  // four threads a token, 16 columns each
-  __syncthreads();
+  for (int m = 0; m < 2; ++m) clear(dQ[m]), clear(dA[m]), clear(dK[m]);
+  clear(X);
+  clear(N);
+  float anchor = 0.f;
 
-  for (int c0 = 0; c0 < a.dv; c0 += 64) {
-    const int width = min(64, a.dv - c0);
-    load_tile(sm + L::Y, 128, a.dy + tok * ld_y + h * a.dv + c0, ld_y, kC, live, width, a.vec_dy, tid, kGradThreads);
+  for (int c0 = 0; c0 < a.dv; c0 += 128) {
+    const int nt_cols = min(8, tiles - (c0 >> 4));  // tiles of 16 columns in this piece
+    // half a tile of E and dZ
+    float E[4][4], Z[4][4];
+    if (w < nt_cols) {
+      const int64_t at = (u * tiles + (c0 >> 4) + w) * 256 + half * 128;
+      get(reinterpret_cast<const float4 *>(a.e) + at, lane, E);
+      get(reinterpret_cast<const float4 *>(a.dz) + at, lane, Z);
+    }
+    if (c0) __syncthreads();  // the piece before has been read
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int cx = c0 + 64 * x;
+      if (cx >= a.dv) continue;
+      load_tile<128, kGradThreads>(sm + L::Y + x * kTile, a.dy + tok * ld_y + h * a.dv + cx, ld_y, live, min(64, a.dv - cx),
+                                   a.by_dy, tid);
+      load_tile<128, kGradThreads>(sm + L::V + x * kTile, a.v + tok * a.ld_v + h * a.dv + cx, a.ld_v, live,
+                                   min(64, a.dv - cx), a.by_v, tid);
+    }
     cp_async_commit();
-    {  // E and dZ: U and dZ as tiles, dv, and the sums over a token's columns
-      const float *E = a.e + (u * kC + row) * a.dv + c0, *Z = a.dz + (u * kC + row) * a.dv + c0;
-      const uint16_t *V = a.v + (tok + row) * a.ld_v + h * a.dv + c0;
-      uint16_t *dV = a.odv + (tok + row) * a.ld_dv + h * a.dv + c0;
-      const float be = beta[row];
-      const bool vec = a.dv % 4 == 0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int cc = 16 * part + 8 * half;
-        float e[8], z[8];
-        if (vec && cc + 8 <= width) {
-#pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            *reinterpret_cast<float4 *>(e + i) = *reinterpret_cast<const float4 *>(E + cc + i);
-            *reinterpret_cast<float4 *>(z + i) = *reinterpret_cast<const float4 *>(Z + cc + i);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            e[i] = cc + i < width ? E[cc + i] : 0.f;
-            z[i] = cc + i < width ? Z[cc + i] : 0.f;
-          }
-        }
-        if (row < live) {
-          if (a.vec_v && cc + 8 <= width) {
-            const uint4 vv = *reinterpret_cast<const uint4 *>(V + cc);
-            const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vz += low2(vw[i]) * z[2 * i] + high2(vw[i]) * z[2 * i + 1];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (cc + i < width) vz += bf16_to_f32(V[cc + i]) * z[i];
-          }
-          if (a.vec_y && cc + 8 <= width) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint32_t *>(dV + cc + 2 * i) = pack2(z[2 * i], z[2 * i + 1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (cc + i < width) dV[cc + i] = static_cast<uint16_t>(pack2(z[i], 0.f));
-          }
-        }
-        uint32_t su[4][3], sz[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ez += e[2 * i] * z[2 * i] + e[2 * i + 1] * z[2 * i + 1];
-          split<3>(be * e[2 * i], be * e[2 * i + 1], su[i]);
-          split<2>(z[2 * i], z[2 * i + 1], sz[i]);
-        }
-        const uint32_t off = piece(row, cc >> 3, 128);
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-          *reinterpret_cast<uint4 *>(sm + L::U + p * kTile + off) = make_uint4(su[0][p], su[1][p], su[2][p], su[3][p]);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          *reinterpret_cast<uint4 *>(sm + L::Z + p * kTile + off) = make_uint4(sz[0][p], sz[1][p], sz[2][p], sz[3][p]);
-      }
-    }
-    // the states: S and G at the chunk's two ends as tiles [column][key channel]; <S, G_start>
-    {
-      const int ct0 = c0 >> 4;
-      const float4 *S = reinterpret_cast<const float4 *>(a.s) + (u * tiles + ct0) * (NT * 32);
-      const float4 *G0 = reinterpret_cast<const float4 *>(a.g) + ((bh * (a.n + 1) + c) * tiles + ct0) * (NT * 32);
-      const float4 *G1 = G0 + tiles * (NT * 32);
-#pragma unroll 4
-      for (int id = tid; id < 4 * NT * 32; id += kGradThreads) {
-        const int ct = id / (NT * 32), nt = (id >> 5) % NT;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f), x = s;
-        if (ct0 + ct < tiles) {
-          s = S[id];
-          x = G1[id];
-          const float4 y = G0[id];
-          anchor += (s.x * y.x + s.y * y.y) + (s.z * y.z + s.w * y.w);
-        }
-        const uint32_t o0 = piece(16 * ct + g, nt, rb) + 4 * t, o1 = piece(16 * ct + g + 8, nt, rb) + 4 * t;
-        uint32_t p0[3], p1[3], g0[2], g1[2];
-        split<3>(s.x, s.y, p0);
-        split<3>(s.z, s.w, p1);
-        split<2>(x.x, x.y, g0);
-        split<2>(x.z, x.w, g1);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          *reinterpret_cast<uint32_t *>(sm + L::S + p * 64 * rb + o0) = p0[p];
-          *reinterpret_cast<uint32_t *>(sm + L::S + p * 64 * rb + o1) = p1[p];
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          *reinterpret_cast<uint32_t *>(sm + L::G + p * 64 * rb + o0) = g0[p];
-          *reinterpret_cast<uint32_t *>(sm + L::G + p * 64 * rb + o1) = g1[p];
-        }
-      }
-    }
     cp_async_wait<0>();
     __syncthreads();
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t y[1][4], uu[2][4], z[2][4];
-      a_rows(uY, 128, 16 * mi, 16 * ks, lane, y[0]);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        a_rows(uU + p * kTile, 128, 16 * mi, 16 * ks, lane, uu[p]);
-        a_rows(uZ + p * kTile, 128, 16 * mi, 16 * ks, lane, z[p]);
-      }
-#pragma unroll
-      for (int np = 0; np < NP; ++np) {
-        const int n0 = nj * (NK * 8) + 16 * np;
-        uint32_t r[3][4];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) b_cols(uS + p * 64 * rb, rb, n0, 16 * ks, lane, r[p]);
-        products(dQ, np, y, r);
-        const uint32_t r2[2][4] = {{r[0][0], r[0][1], r[0][2], r[0][3]}, {r[1][0], r[1][1], r[1][2], r[1][3]}};
-        products(dA, np, z, r2);
-        uint32_t q[2][4];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) b_cols(uG + p * 64 * rb, rb, n0, 16 * ks, lane, q[p]);
-        products(dK, np, uu, q);
-      }
+    if (w < nt_cols) {
+      uint16_t *dvp = a.odv + tok * a.ld_dv + h * a.dv + c0 + 16 * w + 2 * t;
+      float sum[16];  // [dZ . E, v . dZ][n-tile][token of the pair]
 #pragma unroll
       for (int np = 0; np < 2; ++np) {
-        const int n0 = 32 * nj + 16 * np;
-        if (n0 > 16 * mi) continue;
-        uint32_t r[3][4];
+        uint32_t v[4], pu[3][4], pz[2][4];
+        ldsm4_t(uV + (w >> 2) * kTile +
+                    piece(32 * half + 16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), 2 * (w & 3) + ((lane >> 3) & 1), 128),
+                v);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) b_rows(uU + p * kTile, 128, n0, 16 * ks, lane, r[p]);
-        products(X, np, y, r);
-        const uint32_t r2[2][4] = {{r[0][0], r[0][1], r[0][2], r[0][3]}, {r[1][0], r[1][1], r[1][2], r[1][3]}};
-        products(N, np, z, r2);
+        for (int x = 0; x < 2; ++x) {
+          const int nt = 2 * np + x;
+          const float2 be = *reinterpret_cast<const float2 *>(beta + 32 * half + 8 * nt + 2 * t);
+          sum[2 * nt] = E[nt][0] * Z[nt][0] + E[nt][2] * Z[nt][2];
+          sum[2 * nt + 1] = E[nt][1] * Z[nt][1] + E[nt][3] * Z[nt][3];
+          sum[8 + 2 * nt] = low2(v[2 * x]) * Z[nt][0] + low2(v[2 * x + 1]) * Z[nt][2];
+          sum[8 + 2 * nt + 1] = high2(v[2 * x]) * Z[nt][1] + high2(v[2 * x + 1]) * Z[nt][3];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // columns 0..7 and 8..15 of the tile
+            uint32_t s3[3], s2[2];
+            split<3>(be.x * E[nt][2 * e], be.y * E[nt][2 * e + 1], s3);
+            split<2>(Z[nt][2 * e], Z[nt][2 * e + 1], s2);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) pu[p][x + 2 * e] = transpose8(s3[p]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) pz[p][x + 2 * e] = transpose8(s2[p]);
+            // dv is dZ rounded once, which is its first part
+            const int i = 32 * half + 8 * nt + g, left = a.dv - (c0 + 16 * w + 8 * e + 2 * t);
+            if (i < live) {
+              uint16_t *o = dvp + i * a.ld_dv + 8 * e;
+              const uint32_t z = pz[0][x + 2 * e];
+              if (a.pair_y) {
+                if (left > 0) *reinterpret_cast<uint32_t *>(o) = z;
+              } else {
+                if (left > 0) o[0] = static_cast<uint16_t>(z);
+                if (left > 1) o[1] = static_cast<uint16_t>(z >> 16);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          sU[((w * 3 + p) * 4 + 2 * half + np) * 32 + lane] = make_uint4(pu[p][0], pu[p][1], pu[p][2], pu[p][3]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          sZ[((w * 2 + p) * 4 + 2 * half + np) * 32 + lane] = make_uint4(pz[p][0], pz[p][1], pz[p][2], pz[p][3]);
       }
+      sum_rows(sum, lane);
+      float *to = rows + (w * 2 + (lane >> 4)) * kC + 32 * half + 8 * (2 * ((lane >> 3) & 1) + ((lane >> 2) & 1)) + 2 * t;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) to[i] = c0 ? to[i] + sum[i] : sum[i];
     }
     __syncthreads();
-  }
 
-  // sums over a token's columns and over the state
+    const float4 *S = reinterpret_cast<const float4 *>(a.s) + ((u * tiles + (c0 >> 4)) * NT + w * NW) * 32 + lane;
+    const float4 *G0 = reinterpret_cast<const float4 *>(a.g) +
+                       (((bh * (a.n + 1) + c) * tiles + (c0 >> 4)) * NT + w * NW) * 32 + lane;
+    const float4 *G1 = G0 + static_cast<int64_t>(tiles) * NT * 32;
+    float4 fs[NW], f0[NW], f1[NW];
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    ez += __shfl_xor_sync(kFull, ez, o);
-    vz += __shfl_xor_sync(kFull, vz, o);
-  }
-  if (part == 0) {
-    rowEZ[row] = ez;
-    rowVZ[row] = vz;
+    for (int x = 0; x < NW; ++x) {
+      fs[x] = S[x * 32], f1[x] = G1[x * 32];
+      if (half == 0) f0[x] = G0[x * 32];
+    }
+#pragma unroll 1
+    for (int kt = 0; kt < nt_cols; ++kt) {
+      uint32_t bs[NW][3][2], bg[NW][2][2];
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        if (half == 0) anchor += (fs[x].x * f0[x].x + fs[x].y * f0[x].y) + (fs[x].z * f0[x].z + fs[x].w * f0[x].w);
+        uint32_t p0[3], p1[3], q0[2], q1[2];
+        split<3>(fs[x].x, fs[x].y, p0);
+        split<3>(fs[x].z, fs[x].w, p1);
+        split<2>(f1[x].x, f1[x].y, q0);
+        split<2>(f1[x].z, f1[x].w, q1);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) bs[x][p][0] = transpose8(p0[p]), bs[x][p][1] = transpose8(p1[p]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) bg[x][p][0] = transpose8(q0[p]), bg[x][p][1] = transpose8(q1[p]);
+      }
+      if (kt + 1 < nt_cols) {
+        S += NT * 32, G0 += NT * 32, G1 += NT * 32;
+#pragma unroll
+        for (int x = 0; x < NW; ++x) {
+      fs[x] = S[x * 32], f1[x] = G1[x * 32];
+      if (half == 0) f0[x] = G0[x * 32];
+    }
+      }
+      uint32_t bu[3][2];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const uint4 v = sU[((kt * 3 + p) * 4 + (w >> 1)) * 32 + lane];
+        bu[p][0] = w & 1 ? v.y : v.x;
+        bu[p][1] = w & 1 ? v.w : v.z;
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int mt = 2 * half + m;
+        uint32_t y[4], uu[2][4], z[2][4];
+        a_rows(uY + (kt >> 2) * kTile, 128, 16 * mt, 16 * (kt & 3), lane, y);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint4 vu = sU[((kt * 3 + p) * 4 + mt) * 32 + lane], vz = sZ[((kt * 2 + p) * 4 + mt) * 32 + lane];
+          uu[p][0] = vu.x, uu[p][1] = vu.y, uu[p][2] = vu.z, uu[p][3] = vu.w;
+          z[p][0] = vz.x, z[p][1] = vz.y, z[p][2] = vz.z, z[p][3] = vz.w;
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int x = 0; x < NW; ++x) {
+            fma16816(dQ[m][x], y, bs[x][p][0], bs[x][p][1]);
+            // parts 0 0, 0 1 and 1 0
+            fma16816(dA[m][x], z[p >> 1], bs[x][p & 1][0], bs[x][p & 1][1]);
+            fma16816(dK[m][x], uu[p >> 1], bg[x][p & 1][0], bg[x][p & 1][1]);
+          }
+        if (mt >= (w >> 1))
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            fma16816(X[m], y, bu[p][0], bu[p][1]);
+            fma16816(N[m], z[p >> 1], bu[p & 1][0], bu[p & 1][1]);
+          }
+      }
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) anchor += __shfl_xor_sync(kFull, anchor, o);
-  if (lane == 0) red[w] = anchor;
+  if (lane == 0 && half == 0) red[w] = anchor;
+  __syncthreads();  // U has been read
 
-  const int i0 = 16 * mi + g;
 #pragma unroll
-  for (int nt = 0; nt < 2 * NP; ++nt)
+  for (int m = 0; m < 2; ++m) {
+    const int mt = 2 * half + m;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 8 * (e >> 1);
-      dQ[nt][e] *= gam[i];
-      dK[nt][e] = tail[i] * dK[nt][e] - gam[i] * dA[nt][e];
-    }
+    for (int x = 0; x < NW; ++x)
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    if (32 * nj + 8 * nt > 16 * mi + 15) continue;
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * mt + g + 8 * (e >> 1);
+        dQ[m][x][e] *= gam[i];
+        dK[m][x][e] = tail[i] * dK[m][x][e] - gam[i] * dA[m][x][e];
+      }
+    if (mt < (w >> 1)) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 8 * (e >> 1), j = 32 * nj + 8 * nt + 2 * t + (e & 1);
-      const bool on = j <= i && __float_as_int(sg[i]) == __float_as_int(sg[j]);
-      const float d = on ? umma::ex2_approx((lh[i] - lh[j]) + (ll[i] - ll[j])) : 0.f;
-      X[nt][e] = on ? d * X[nt][e] : 0.f;
-      N[nt][e] = on && j < i ? -d * N[nt][e] : 0.f;
-    }
+    for (int r = 0; r < 2; ++r) {
+      const int i = 16 * mt + g + 8 * r, j = 8 * w + 2 * t;
+      float xv[2], nv[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int i = i0 + 8 * x, j = 32 * nj + 8 * nt + 2 * t;
-      uint32_t s[3], m[2];
-      split<3>(X[nt][2 * x], X[nt][2 * x + 1], s);
-      split<2>(N[nt][2 * x], N[nt][2 * x + 1], m);
-      const uint32_t off = piece(i, j >> 3, 128) + 2 * (j & 7);
+      for (int e = 0; e < 2; ++e) {
+        const bool on = j + e <= i && __float_as_int(sg[i]) == __float_as_int(sg[j + e]);
+        const float d = on ? umma::ex2_approx((lh[i] - lh[j + e]) + (ll[i] - ll[j + e])) : 0.f;
+        xv[e] = on ? d * X[m][2 * r + e] : 0.f;
+        nv[e] = on && j + e < i ? -d * N[m][2 * r + e] : 0.f;
+      }
+      uint32_t sx[3], sn[2];
+      split<3>(xv[0], xv[1], sx);
+      split<2>(nv[0], nv[1], sn);
+      const uint32_t off = piece(i, w, 128) + 4 * t;
 #pragma unroll
-      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t *>(sm + L::X + p * kTile + off) = s[p];
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t *>(sm + L::X + p * kTile + off) = sx[p];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {  // N below the diagonal, N^T above it
         unsigned char *tile = sm + L::N + p * kTile;
-        const uint16_t lo = static_cast<uint16_t>(m[p]), hi = static_cast<uint16_t>(m[p] >> 16);
+        const uint16_t lo = static_cast<uint16_t>(sn[p]), hi = static_cast<uint16_t>(sn[p] >> 16);
         if (j <= i) {
           *reinterpret_cast<uint16_t *>(tile + off) = lo;
           *reinterpret_cast<uint16_t *>(tile + piece(j, i >> 3, 128) + 2 * (i & 7)) = lo;
@@ -913,117 +1103,134 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
     }
   }
   __syncthreads();
+  const uint32_t uK = smem_u32(sm + L::K), uQ = smem_u32(sm + L::Q), uX = smem_u32(sm + L::X), uN = smem_u32(sm + L::N);
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    uint32_t x[3][4], xt[2][4], m[2][4];
-    const bool low = ks <= mi, up = ks >= mi;
+    uint32_t bk[4], bq[4];  // of 16 key channels: this warp's, or with another's beside them
+    constexpr int share = 2 / NW;
+    b_cols(uK, rb, 16 * (w / share), 16 * ks, lane, bk);
+    b_cols(uQ, rb, 16 * (w / share), 16 * ks, lane, bq);
+    if (NW == 1 && (w & 1)) bk[0] = bk[2], bk[1] = bk[3], bq[0] = bq[2], bq[1] = bq[3];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) a_rows(smem_u32(sm + L::N + p * kTile), 128, 16 * mi, 16 * ks, lane, m[p]);
-    if (low)
+    for (int m = 0; m < 2; ++m) {
+      const int mt = 2 * half + m;
+      uint32_t f[4];
 #pragma unroll
-      for (int p = 0; p < 3; ++p) a_rows(smem_u32(sm + L::X + p * kTile), 128, 16 * mi, 16 * ks, lane, x[p]);
-    if (up)
+      for (int p = 0; p < 2; ++p) {
+        a_rows(uN + p * kTile, 128, 16 * mt, 16 * ks, lane, f);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) a_cols(smem_u32(sm + L::X + p * kTile), 128, 16 * mi, 16 * ks, lane, xt[p]);
-#pragma unroll
-    for (int np = 0; np < NP; ++np) {
-      const int n0 = nj * (NK * 8) + 16 * np;
-      uint32_t r[1][4];
-      b_cols(uK, rb, n0, 16 * ks, lane, r[0]);
-      products(dK, np, m, r);
-      if (low) products(dQ, np, x, r);
-      if (up) {
-        b_cols(uQ, rb, n0, 16 * ks, lane, r[0]);
-        products(dK, np, xt, r);
+        for (int x = 0; x < NW; ++x) fma16816(dK[m][x], f, bk[2 * x], bk[2 * x + 1]);
       }
+      if (ks <= mt)
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          a_rows(uX + p * kTile, 128, 16 * mt, 16 * ks, lane, f);
+#pragma unroll
+          for (int x = 0; x < NW; ++x) fma16816(dQ[m][x], f, bk[2 * x], bk[2 * x + 1]);
+        }
+      if (ks >= mt)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          a_cols(uX + p * kTile, 128, 16 * mt, 16 * ks, lane, f);
+#pragma unroll
+          for (int x = 0; x < NW; ++x) fma16816(dK[m][x], f, bq[2 * x], bq[2 * x + 1]);
+        }
     }
   }
-  // q . dq, then the outputs
-  float qd[2] = {0.f, 0.f};
+  // q . dq
 #pragma unroll
-  for (int nt = 0; nt < 2 * NP; ++nt)
+  for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint32_t v = *reinterpret_cast<const uint32_t *>(sm + L::Q + piece(i0 + 8 * x, nj * NK + nt, rb) + 4 * t);
-      qd[x] += low2(v) * dQ[nt][2 * x] + high2(v) * dQ[nt][2 * x + 1];
-    }
+    for (int r = 0; r < 2; ++r) {
+      const int i = 32 * half + 16 * m + g + 8 * r;
+      float qd = 0.f;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    qd[x] += __shfl_xor_sync(kFull, qd[x], 1);
-    qd[x] += __shfl_xor_sync(kFull, qd[x], 2);
-    if (t == 0) flow[nj * kC + i0 + 8 * x] = qd[x];
-  }
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int i = i0 + 8 * x;
-    if (i >= live) continue;
-#pragma unroll
-    for (int nt = 0; nt < 2 * NP; ++nt) {
-      const int cc = nj * (NK * 8) + 8 * nt + 2 * t;
-      if (cc >= a.dk) continue;
-      const float q0 = dQ[nt][2 * x], q1 = dQ[nt][2 * x + 1], k0 = dK[nt][2 * x], k1 = dK[nt][2 * x + 1];
-      if (a.pdq) {
-        const int64_t o = ((tok + i) * a.H + h) * a.dk + cc;
-        a.pdq[o] = q0;
-        a.pdk[o] = k0;
-        if (cc + 1 < a.dk) {
-          a.pdq[o + 1] = q1;
-          a.pdk[o + 1] = k1;
-        }
-      } else {
-        uint16_t *oq = a.odq + (tok + i) * a.ld_dq + h * a.dk + cc, *ok = a.odk + (tok + i) * a.ld_dk + h * a.dk + cc;
-        const uint32_t vq = pack2(q0, q1), vk = pack2(k0, k1);
-        if (a.vec_qk && cc + 1 < a.dk) {
-          *reinterpret_cast<uint32_t *>(oq) = vq;
-          *reinterpret_cast<uint32_t *>(ok) = vk;
-        } else {
-          oq[0] = static_cast<uint16_t>(vq);
-          ok[0] = static_cast<uint16_t>(vk);
-          if (cc + 1 < a.dk) {
-            oq[1] = static_cast<uint16_t>(vq >> 16);
-            ok[1] = static_cast<uint16_t>(vk >> 16);
-          }
-        }
+      for (int x = 0; x < NW; ++x) {
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(sm + L::Q + piece(i, w * NW + x, rb) + 4 * t);
+        qd += low2(v) * dQ[m][x][2 * r] + high2(v) * dQ[m][x][2 * r + 1];
       }
+      qd += __shfl_xor_sync(kFull, qd, 1);
+      qd += __shfl_xor_sync(kFull, qd, 2);
+      if (t == 0) flow[w * kC + i] = qd;
     }
-  }
   __syncthreads();
-  if (w == 0) {  // the decays' gradient: sums before each token, in 64 bits (they cancel)
-    double start = 0.0;
-    for (int i = 0; i < kGradThreads / 32; ++i) start += red[i];
-    double x[2], before[2];
+  if (tid < 32) {  // the decays' gradient: sums before each token (which cancel)
+    Wide x[2], before[2];
+    float ez[2];
     int seg[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
-      before[i] = x[i] = static_cast<double>(flow[m] + flow[kC + m]) - rowVZ[m];
-      seg[i] = __float_as_int(sg[m]);
+      Wide f{0.f, 0.f};
+      ez[i] = 0.f;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(kFull, x[i], o);
-        if (lane >= o) x[i] += y;
+      for (int e = 0; e < 8; ++e) {
+        f = f + Wide{flow[e * kC + m], 0.f} - Wide{rows[(2 * e + 1) * kC + m], 0.f};
+        ez[i] += rows[2 * e * kC + m];
       }
+      before[i] = f;
+      x[i] = running(f, lane);
+      seg[i] = __float_as_int(sg[m]);
     }
-    x[1] += __shfl_sync(kFull, x[0], 31);
+    x[1] = shfl(x[0], 31) + x[1];
     const uint32_t s0 = __ballot_sync(kFull, lane == 0 || seg[0] != __float_as_int(sg[max(lane - 1, 0)]));
     const uint32_t s1 = __ballot_sync(kFull, seg[1] != __float_as_int(sg[lane + 31]));
     before[0] = x[0] - before[0];  // sum over s < t
     before[1] = x[1] - before[1];
+    const uint32_t upto = 0xffffffffu >> (31 - lane);
+    Wide start{0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) start = start + Wide{red[i], 0.f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
       // the first token of this one's document
-      const uint32_t upto = 0xffffffffu >> (31 - lane);
       const int first = i == 0 ? 31 - __clz(s0 & upto) : (s1 & upto) ? 63 - __clz(s1 & upto) : 31 - __clz(s0);
-      const double p0 = __shfl_sync(kFull, before[0], first & 31), p1 = __shfl_sync(kFull, before[1], first & 31);
-      const double base = first < 32 ? p0 : p1;
+      const Wide p0 = shfl(before[0], first & 31), p1 = shfl(before[1], first & 31);
       if (m < live) {
-        const double v = (seg[i] == 0 ? start : 0.0) - (before[i] - base);
-        a.dla[(tok + m) * a.H + h] = static_cast<float>(v);
-        a.dbeta[(tok + m) * a.H + h] = rowEZ[m] / beta[m];
+        const Wide v = (seg[i] == 0 ? start : Wide{0.f, 0.f}) - (before[i] - (first < 32 ? p0 : p1));
+        a.dla[(tok + m) * a.H + h] = v.hi;
+        a.dbeta[(tok + m) * a.H + h] = ez[i] / beta[m];
       }
     }
   }
+  // dq and dk
+  const int64_t to_q = a.pdq ? static_cast<int64_t>(a.H) * a.dk : a.ld_dq, to_k = a.pdq ? to_q : a.ld_dk;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = 32 * half + 16 * m + g + 8 * r;
+      if (i >= live) continue;
+      const int64_t oq = (tok + i) * to_q + h * a.dk, ok = (tok + i) * to_k + h * a.dk;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        const int cc = 8 * (w * NW + x) + 2 * t;
+        if (cc >= a.dk) continue;
+        const float q0 = dQ[m][x][2 * r], q1 = dQ[m][x][2 * r + 1], k0 = dK[m][x][2 * r], k1 = dK[m][x][2 * r + 1];
+        if (a.pdq) {
+          a.pdq[oq + cc] = q0;
+          a.pdk[ok + cc] = k0;
+          if (cc + 1 < a.dk) {
+            a.pdq[oq + cc + 1] = q1;
+            a.pdk[ok + cc + 1] = k1;
+          }
+        } else {
+          const uint32_t vq = pack2(q0, q1), vk = pack2(k0, k1);
+          if (a.pair_qk) {
+            *reinterpret_cast<uint32_t *>(a.odq + oq + cc) = vq;
+            *reinterpret_cast<uint32_t *>(a.odk + ok + cc) = vk;
+          } else {
+            a.odq[oq + cc] = static_cast<uint16_t>(vq);
+            a.odk[ok + cc] = static_cast<uint16_t>(vk);
+            if (cc + 1 < a.dk) {
+              a.odq[oq + cc + 1] = static_cast<uint16_t>(vq >> 16);
+              a.odk[ok + cc + 1] = static_cast<uint16_t>(vk >> 16);
+            }
+          }
+        }
+      }
+    }
 }
 
 // dq and dk of key heads that several value heads share, heads in order
@@ -1071,14 +1278,14 @@ Layout layout_of(int B, int T, int Hk, int H, int dk, int dv) {
   const size_t units = static_cast<size_t>(l.units);
   l.scal = 0;
   l.t3 = up(l.scal + units * kScal * 4);
-  l.m3 = up(l.t3 + units * 3 * kTile);
-  l.s = up(l.m3 + units * 3 * kTile);
+  l.m3 = up(l.t3 + units * 3 * kTri);
+  l.s = up(l.m3 + units * 3 * kTri);
   l.e = up(l.s + units * l.state * 4);
-  l.saved = up(l.e + units * kC * dv * 4);
+  l.saved = up(l.e + units * l.tiles * 16 * kC * 4);
   const size_t part = Hk == H ? 0 : static_cast<size_t>(B) * T * H * dk * 4;
   l.g = 0;
   l.dz = up(static_cast<size_t>(B) * H * (l.n + 1) * l.state * 4);
-  l.pdq = up(l.dz + units * kC * dv * 4);
+  l.pdq = up(l.dz + units * l.tiles * 16 * kC * 4);
   l.pdk = up(l.pdq + part);
   l.work = up(l.pdk + part);
   return l;
@@ -1095,6 +1302,13 @@ int check_common(const char *what, const Gdn &a, const void *saved, size_t saved
     return set_error(SDM_ERR_ALIGN, "%s: a pointer is not aligned", what);
   if (saved_bytes < l.saved) return set_error(SDM_ERR_INVALID_ARG, "%s: saved holds %zu bytes, %zu needed", what, saved_bytes, l.saved);
   return SDM_OK;
+}
+
+// the bytes by which rows of `width` bf16 can be copied
+int row_bytes(const void *p, int64_t ld, int width) {
+  for (int n = 16; n > 2; n /= 2)
+    if (width * 2 % n == 0 && ld * 2 % n == 0 && aligned(p, n)) return n;
+  return 2;
 }
 
 void place_saved(Gdn &a, void *saved, const Layout &l) {
@@ -1115,24 +1329,41 @@ int launch(K kernel, const char *what, int64_t grid, int threads, int smem, cons
   return check_launch(what);
 }
 
+// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its
+// two warps then run on schedulers of their own), else two, else four, which share an SM's
+// tensor cores and the chunk's tiles.
+constexpr int kSms = 152;
+int chain_width(const Gdn &a, const Layout &l) {
+  const int64_t all = l.tiles * a.B * a.H;
+  return all <= kSms || l.tiles == 1 ? 1 : all <= 2 * kSms || l.tiles == 2 ? 2 : 4;
+}
+
+template <int NK, int W>
+int run_chain(const Gdn &a, const Layout &l, bool back, cudaStream_t st) {
+  const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
+  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, 64 * W, Chain<NK, 3, W>::size, a, st)
+              : launch(gdn_chain<NK, W>, "gdn_train", grid, 64 * W, Chain<NK, 2, W>::size, a, st);
+}
+template <int NK>
+int run_chain(const Gdn &a, const Layout &l, bool back, cudaStream_t st) {
+  const int w = chain_width(a, l);
+  return w == 1 ? run_chain<NK, 1>(a, l, back, st) : w == 2 ? run_chain<NK, 2>(a, l, back, st) : run_chain<NK, 4>(a, l, back, st);
+}
+
 template <int NK>
 int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
   if (l.units > 0) {
     const int rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, 2 * kC * NK * 32 + (2 * kC * kLd + kScal) * 4, a, st);
     if (rc != SDM_OK) return rc;
   }
-  const int64_t groups = (l.tiles + kWarps - 1) / kWarps;
-  return launch(gdn_chain<NK>, "gdn_train", groups * a.B * a.H, 32 * static_cast<int>(std::min<int64_t>(kWarps, l.tiles)),
-                2 * Stage<NK, 2>::size, a, st);
+  return run_chain<NK>(a, l, false, st);
 }
 
 template <int NK>
 int run_backward(const Gdn &a, const Layout &l, cudaStream_t st) {
-  const int64_t groups = (l.tiles + kWarps - 1) / kWarps;
-  int rc = launch(gdn_chain_back<NK>, "gdn_backward", groups * a.B * a.H,
-                  32 * static_cast<int>(std::min<int64_t>(kWarps, l.tiles)), 2 * Stage<NK, 3>::size, a, st);
+  int rc = run_chain<NK>(a, l, true, st);
   if (rc != SDM_OK || l.units == 0) return rc;
-  rc = launch(gdn_grad<NK>, "gdn_backward", l.units, kGradThreads, GradSmem<NK>::size, a, st);
+  rc = launch(gdn_grad<NK>, "gdn_backward", l.units, kGradThreads, Grad<NK>::size, a, st);
   if (rc != SDM_OK || !a.pdq) return rc;
   gdn_grad_heads<<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T), 256, 0, st>>>(a);
   return check_launch("gdn_backward");
@@ -1168,9 +1399,9 @@ extern "C" int gdn_train(const float *state, float *state_out, const uint16_t *q
   if (rc != SDM_OK) return rc;
   if (!aligned(y, 2)) return set_error(SDM_ERR_ALIGN, "gdn_train: a pointer is not aligned");
   if (B == 0 || H == 0) return SDM_OK;
-  a.vec_qk = dk % 8 == 0 && ld_q % 8 == 0 && ld_k % 8 == 0 && aligned(q, 16) && aligned(k, 16);
-  a.vec_v = dv % 8 == 0 && ld_v % 8 == 0 && aligned(v, 16);
-  a.vec_y = dv % 2 == 0 && aligned(y, 4);
+  a.by_qk = std::min(row_bytes(q, ld_q, dk), row_bytes(k, ld_k, dk));
+  a.by_v = row_bytes(v, ld_v, dv);
+  a.pair_y = dv % 2 == 0 && aligned(y, 4);
   place_saved(a, saved, l);
   return dk <= 64 ? run_train<4>(a, l, static_cast<cudaStream_t>(stream)) : run_train<8>(a, l, static_cast<cudaStream_t>(stream));
 }
@@ -1205,11 +1436,11 @@ extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16
   if (workspace_bytes < l.work)
     return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: workspace of %zu bytes, %zu needed", workspace_bytes, l.work);
   if (B == 0 || H == 0) return SDM_OK;
-  a.vec_qk = dk % 8 == 0 && ld_q % 8 == 0 && ld_k % 8 == 0 && aligned(q, 16) && aligned(k, 16) && ld_dq % 2 == 0 &&
-             ld_dk % 2 == 0 && aligned(dq, 4) && aligned(dk_out, 4);
-  a.vec_v = dv % 8 == 0 && ld_v % 8 == 0 && aligned(v, 16);
-  a.vec_dy = dv % 8 == 0 && aligned(dy, 16);
-  a.vec_y = dv % 2 == 0 && ld_dv % 2 == 0 && aligned(dv_out, 4);
+  a.by_qk = std::min(row_bytes(q, ld_q, dk), row_bytes(k, ld_k, dk));
+  a.by_v = row_bytes(v, ld_v, dv);
+  a.by_dy = row_bytes(dy, static_cast<int64_t>(H) * dv, dv);
+  a.pair_y = dv % 2 == 0 && ld_dv % 2 == 0 && aligned(dv_out, 4);
+  a.pair_qk = dk % 2 == 0 && ld_dq % 2 == 0 && ld_dk % 2 == 0 && aligned(dq, 4) && aligned(dk_out, 4);
   place_saved(a, const_cast<void *>(saved), l);
   unsigned char *p = static_cast<unsigned char *>(workspace);
   a.g = reinterpret_cast<float *>(p + l.g);

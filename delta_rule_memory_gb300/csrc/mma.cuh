@@ -56,8 +56,7 @@ __device__ __forceinline__ void a_cols(uint32_t tile, int rb, int m0, int k0, in
 
 // d += a b
 __device__ __forceinline__ void fma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -107,27 +106,47 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return d;
 }
 
-// 16 bytes global -> shared, asynchronously; zeros where `live` is false (src
-// then only has to be a valid address)
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
-  const int n = live ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// BYTES (4, 8 or 16) global -> shared, asynchronously; zeros where `live` is
+// false (src then only has to be a valid address)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live) {
+  const int n = live ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 
-// `rows` rows of `width` bf16 (row r at src + r * ld) into a tile of rows of rb
-// bytes, zeros behind `width` and from row `live` on.  vec: every row is
-// 16-byte aligned and width % 8 == 0 (asynchronous copies); else by elements.
-__device__ __forceinline__ void load_tile(unsigned char *tile, int rb, const uint16_t *src, int64_t ld, int rows,
-                                          int live, int width, bool vec, int tid, int threads) {
-  const int pieces = rb >> 4, all = rows * pieces;
-  for (int id = tid; id < all; id += threads) {
-    const int r = id / pieces, p = id - r * pieces;
-    unsigned char *dst = tile + piece(r, p, rb);
-    const int c = p * 8;
-    if (vec) {
-      const bool ok = r < live && c < width;
-      copy16(static_cast<uint32_t>(__cvta_generic_to_shared(dst)), ok ? src + r * ld + c : src, ok);
-    } else {
+template <int RB, int THREADS, int BYTES>
+__device__ __forceinline__ void load_tile_by(unsigned char *tile, const uint16_t *src, int64_t ld, int live, int width,
+                                             int tid) {
+  constexpr int pieces = RB / BYTES, most = 64 * pieces / THREADS;
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(tile));
+#pragma unroll(most <= 16 ? most : 8)
+  for (int i = 0; i < most; ++i) {
+    const int id = tid + i * THREADS, r = id / pieces, p = id % pieces;
+    const bool ok = r < live && p * (BYTES / 2) < width;
+    copy_async<BYTES>(base + piece(r, p * BYTES / 16, RB) + p * BYTES % 16, ok ? src + r * ld + p * (BYTES / 2) : src, ok);
+  }
+}
+
+// 64 rows of `width` bf16 (row r at src + r * ld) into a tile of rows of RB
+// bytes, zeros behind `width` and from row `live` on, by THREADS threads (a
+// power of two).  bytes: what divides the address, the distance and the width
+// of every row (16, 8 or 4: asynchronous copies of that size; else by elements).
+template <int RB, int THREADS>
+__device__ __forceinline__ void load_tile(unsigned char *tile, const uint16_t *src, int64_t ld, int live, int width,
+                                          int bytes, int tid) {
+  if (bytes == 16) {
+    load_tile_by<RB, THREADS, 16>(tile, src, ld, live, width, tid);
+  } else if (bytes == 8) {
+    load_tile_by<RB, THREADS, 8>(tile, src, ld, live, width, tid);
+  } else if (bytes == 4) {
+    load_tile_by<RB, THREADS, 4>(tile, src, ld, live, width, tid);
+  } else {
+    constexpr int pieces = RB / 16;
+    for (int id = tid; id < 64 * pieces; id += THREADS) {
+      const int r = id / pieces, c = id % pieces * 8;
       uint32_t w[4] = {0, 0, 0, 0};
       if (r < live) {
         const uint16_t *s = src + r * ld + c;
@@ -135,7 +154,7 @@ __device__ __forceinline__ void load_tile(unsigned char *tile, int rb, const uin
         for (int e = 0; e < 8; ++e)
           if (c + e < width) w[e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
       }
-      *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(tile + piece(r, c / 8, RB)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
