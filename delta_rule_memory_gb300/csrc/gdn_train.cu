@@ -38,6 +38,8 @@
 // Precision.  q, k, v and dy are exact in bf16.  What is not (S, G, T, M, Z, U, X) is taken in
 // three bf16 parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da, dbeta); in two parts,
 // 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
+#include <cuda.h>
+
 #include <algorithm>
 #include <climits>
 
@@ -51,7 +53,7 @@ namespace {
 using namespace mma;
 
 constexpr int kC = 64;                  // tokens of a chunk
-constexpr int kTile = kC * kC * 2;      // bytes of one bf16 [64][64] tile
+constexpr int kTile = kPanel;           // bytes of one bf16 [64][64] tile
 constexpr int kTri = 10 * 512;          // ... of a lower triangular one: its ten 16 x 16 blocks
 constexpr int kLd = kC + 4;             // fp32 rows of the solve: 16-byte aligned, 4 banks apart
 constexpr int kScal = 6 * kC;           // gam, tail, beta, l (two floats), document number
@@ -113,6 +115,23 @@ __device__ __forceinline__ Wide running(Wide x, int lane) {
     if (lane >= o) x = y + x;
   }
   return x;
+}
+
+// Tensor maps of q, k, v and dy as [token][head][channel], boxes of one panel;
+// set where rows can be copied by 16 bytes
+struct Maps {
+  CUtensorMap q, k, v, dy;
+};
+
+constexpr uint32_t kWaitLimit = 1u << 20;  // polls (about 0.1 s) before a wait gives up
+
+// Wait for a phase of copies.  One that gives up is reported and lets the
+// kernel run out, its later waits short.
+__device__ __forceinline__ void wait_copies(uint64_t *bar, uint32_t parity, uint32_t &limit, const Gdn &a) {
+  if (!umma::mbar_wait(smem_u32(bar), parity, limit)) {
+    report_timeout(a.err);
+    limit = 64;
+  }
 }
 
 __device__ __forceinline__ int length_of(const Gdn &a, int b) {
@@ -219,13 +238,26 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
   __syncthreads();
 }
 
+// one thread: tensor copies of K and Q, and `more` bytes of its own to come
 template <int NK>
-__global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
-  constexpr int rb = NK * 32;
+__device__ __forceinline__ void load_qk(const Maps &maps, unsigned char *sK, unsigned char *sQ, int hk, int64_t tok,
+                                        uint32_t bar, uint32_t more) {
+  umma::mbar_expect_tx(bar, 2 * (NK / 4) * kPanel + more);
+#pragma unroll
+  for (int p = 0; p < NK / 4; ++p) {
+    tensor_panel(smem_u32(sK) + p * kPanel, &maps.k, 64 * p, hk, static_cast<int>(tok), bar);
+    tensor_panel(smem_u32(sQ) + p * kPanel, &maps.q, 64 * p, hk, static_cast<int>(tok), bar);
+  }
+}
+
+template <int NK>
+__global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __grid_constant__ Maps maps) {
+  constexpr int panels = NK / 4;
   extern __shared__ __align__(1024) unsigned char sm[];
-  unsigned char *sK = sm, *sQ = sm + kC * rb;
-  float *sL = reinterpret_cast<float *>(sm + 2 * kC * rb), *sX = sL + kC * kLd, *sc = sX + kC * kLd;
+  unsigned char *sK = sm, *sQ = sm + panels * kPanel;
+  float *sL = reinterpret_cast<float *>(sm + 2 * panels * kPanel), *sX = sL + kC * kLd, *sc = sX + kC * kLd;
   float *zt = reinterpret_cast<float *>(sm);  // the K tile's place, once the products are formed
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sc + kScal);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x;
   const int64_t bh = u / a.n;
@@ -234,9 +266,17 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
   if (live <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.T + c * kC;
   const int hk = h / (a.H / a.Hk);
-  load_tile<rb, kPrepThreads>(sK, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-  load_tile<rb, kPrepThreads>(sQ, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-  cp_async_commit();
+  if (a.by_qk == 16) {
+    if (tid == 0) {
+      umma::mbar_init(smem_u32(bar), 1);
+      umma::fence_mbar_init();
+      load_qk<NK>(maps, sK, sQ, hk, tok, smem_u32(bar), 0);
+    }
+  } else {
+    load_tile<panels, kPrepThreads>(sK, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+    load_tile<panels, kPrepThreads>(sQ, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+    cp_async_commit();
+  }
   float *out = a.scal + u * kScal;
   if (w == 0) {
     // l in units of log2, as two floats: a strong decay early in the chunk costs
@@ -276,6 +316,15 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
   }
   cp_async_wait<0>();
   __syncthreads();
+  if (a.by_qk == 16) {
+    uint32_t limit = kWaitLimit;
+    wait_copies(bar, 0, limit, a);
+    if (live < kC) {
+      clear_rows<panels, kPrepThreads>(sK, live, tid);
+      clear_rows<panels, kPrepThreads>(sQ, live, tid);
+      __syncthreads();
+    }
+  }
 
   // K K^T and Q K^T, a warp 16 rows, up to its diagonal block
   float G[8][4], P[8][4];
@@ -287,13 +336,13 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
 #pragma unroll
   for (int ks = 0; ks < NK; ++ks) {
     uint32_t ak[4], aq[4];
-    a_rows(uK, rb, 16 * w, 16 * ks, lane, ak);
-    a_rows(uQ, rb, 16 * w, 16 * ks, lane, aq);
+    a_rows(uK, 16 * w, 16 * ks, lane, ak);
+    a_rows(uQ, 16 * w, 16 * ks, lane, aq);
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       if (np > w) continue;
       uint32_t r[4];
-      b_rows(uK, rb, 16 * np, 16 * ks, lane, r);
+      b_rows(uK, 16 * np, 16 * ks, lane, r);
       fma16816(G[2 * np], ak, r[0], r[1]);
       fma16816(G[2 * np + 1], ak, r[2], r[3]);
       fma16816(P[2 * np], aq, r[0], r[1]);
@@ -331,32 +380,50 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a) {
 // ---------------------------------------------------------------------------
 template <int NK, int PM, int W>  // PM: parts of M
 struct Chain {
-  static constexpr int rb = NK * 32;
-  static constexpr int K = 0, Q = K + kC * rb, T = Q + kC * rb, M = T + 3 * kTri, V = M + PM * kTri, sc = V + kC * 128,
-                       stage = sc + 3 * kC * 4;
-  static constexpr int state = 2 * stage, tokens = state + W * NK * 3 * 512, size = tokens + W * 8 * 512;
+  static constexpr int P = NK / 4;  // panels of K and Q
+  static constexpr int K = 0, Q = K + P * kPanel, V = Q + P * kPanel, T = V + kPanel, M = T + 3 * kTri, sc = M + PM * kTri,
+                       stage = (sc + 3 * kC * 4 + 1023) / 1024 * 1024;
+  static constexpr int state = 2 * stage, tokens = state + W * NK * 3 * 512, bars = tokens + W * 8 * 512, size = bars + 16;
 };
 
 // the second warps' copies of a chunk's tiles; cols: the value columns' tensor
 template <int NK, int PM, int W>
-__device__ __forceinline__ void load_stage(unsigned char *st, const Gdn &a, int64_t u, int64_t tok, int h, int col0,
-                                           int live, const uint16_t *cols, int64_t ld_cols, int by_cols, int tid) {
+__device__ __forceinline__ void load_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps, int64_t u,
+                                           int64_t tok, int h, int col0, int live, const uint16_t *cols, int64_t ld_cols,
+                                           int by_cols, const CUtensorMap *cols_map, int tid) {
   using L = Chain<NK, PM, W>;
   constexpr int threads = 32 * W;
-  const int hk = h / (a.H / a.Hk);
-  load_tile<L::rb, threads>(st + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-  load_tile<L::rb, threads>(st + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-  load_tile<128, threads>(st + L::V, cols + tok * ld_cols + h * a.dv + col0, ld_cols, live, min(16 * W, a.dv - col0),
-                          by_cols, tid);
-  const unsigned char *t3 = a.t3 + u * (3 * kTri), *m3 = a.m3 + u * (3 * kTri);
-  const uint32_t dT = smem_u32(st + L::T), dM = smem_u32(st + L::M), ds = smem_u32(st + L::sc);
-#pragma unroll 8
-  for (int id = tid; id < 3 * kTri / 16; id += threads) copy_async<16>(dT + id * 16, t3 + id * 16, true);
-#pragma unroll 8
-  for (int id = tid; id < PM * kTri / 16; id += threads) copy_async<16>(dM + id * 16, m3 + id * 16, true);
-  const float *sc = a.scal + u * kScal;
-  for (int id = tid; id < 3 * kC / 4; id += threads) copy_async<16>(ds + id * 16, sc + id * 4, true);
+  const int hk = h / (a.H / a.Hk), from = col0 & ~63;  // whole panels of value columns
+  if (tid == 0) {
+    const uint32_t mb = smem_u32(bar), more = (3 + PM) * kTri + 3 * kC * 4 + (by_cols == 16 ? kPanel : 0);
+    if (a.by_qk == 16)
+      load_qk<NK>(maps, st + L::K, st + L::Q, hk, tok, mb, more);
+    else
+      umma::mbar_expect_tx(mb, more);
+    if (by_cols == 16) tensor_panel(smem_u32(st + L::V), cols_map, from, h, static_cast<int>(tok), mb);
+    umma::bulk_g2s(smem_u32(st + L::T), a.t3 + u * (3 * kTri), 3 * kTri, mb);
+    umma::bulk_g2s(smem_u32(st + L::M), a.m3 + u * (3 * kTri), PM * kTri, mb);
+    umma::bulk_g2s(smem_u32(st + L::sc), a.scal + u * kScal, 3 * kC * 4, mb);
+  }
+  if (a.by_qk != 16) {
+    load_tile<L::P, threads>(st + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+    load_tile<L::P, threads>(st + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  }
+  if (by_cols != 16)
+    load_tile<1, threads>(st + L::V, cols + tok * ld_cols + h * a.dv + from, ld_cols, live, min(64, a.dv - from), by_cols, tid);
   cp_async_commit();
+}
+
+// the rows behind a chunk's last token, which tensor copies fill with whatever follows it
+template <int NK, int PM, int W>
+__device__ __forceinline__ void clear_stage(unsigned char *st, const Gdn &a, int live, int by_cols, int tid) {
+  using L = Chain<NK, PM, W>;
+  if (a.by_qk == 16) {
+    clear_rows<L::P, 32 * W>(st + L::K, live, tid);
+    clear_rows<L::P, 32 * W>(st + L::Q, live, tid);
+  }
+  if (by_cols == 16) clear_rows<1, 32 * W>(st + L::V, live, tid);
+  umma::fence_async_smem();
 }
 
 // S^T of 16 columns and 8 NT rows of a [dk][dv] matrix as an accumulator, and back
@@ -468,14 +535,13 @@ __device__ __forceinline__ void split_tokens(const float (&x)[8][4], uint32_t (&
 
 // acc = A B for n-tiles 4 quad .. 4 quad + 3, B = tile[token][n] exact, over 64
 // tokens: the small parts first
-template <int RB>
 __device__ __forceinline__ void quad_product(uint32_t tile, int quad, const uint32_t (&a)[4][3][4], int lane,
                                              float (&acc)[4][4]) {
   uint32_t r[4][2][4];
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) b_cols(tile, RB, 32 * quad + 16 * x, 16 * ks, lane, r[ks][x]);
+    for (int x = 0; x < 2; ++x) b_cols(tile, 32 * quad + 16 * x, 16 * ks, lane, r[ks][x]);
   clear(acc);
 #pragma unroll
   for (int p = 2; p >= 0; --p)
@@ -516,7 +582,7 @@ __device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile,
     uint32_t s[3][4], r[4][4];
     get_parts(parts + ks * 96, lane, s);
 #pragma unroll
-    for (int np = 0; np < 4; ++np) b_rows(tile, NK * 32, 16 * np, 16 * ks, lane, r[np]);
+    for (int np = 0; np < 4; ++np) b_rows(tile, 16 * np, 16 * ks, lane, r[np]);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
@@ -576,9 +642,9 @@ __device__ __forceinline__ void store_state(const uint4 *parts, float *m, int dk
 }
 
 template <int NK, int W>
-__global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
+__global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Chain<NK, 2, W>;
-  constexpr int NT = 2 * NK, rb = L::rb;
+  constexpr int NT = 2 * NK;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const bool second = tid >= 32 * W;
@@ -591,12 +657,23 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
   const bool mine = col < a.dv;  // else the warps only help with the copies
   uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96;
   float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;
+  const int vp = ((col0 & 63) >> 3) + 2 * w;  // the warp's pieces of the value columns' panel
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
+  if (tid == 0) {
+    umma::mbar_init(smem_u32(bars), 1);
+    umma::mbar_init(smem_u32(bars + 1), 1);
+    umma::fence_mbar_init();
+  }
+  __syncthreads();
+  uint32_t limit = kWaitLimit;
 
   if (!second) {
     if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
     load_state<NK>(hS, a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane);
     for (int c = 0; c < n; ++c) {
       __syncthreads();
+      wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
+      if (len - c * kC < kC) __syncthreads();  // the second warps clear rows
       if (!mine) continue;
       unsigned char *st = sm + (c & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K), uV = smem_u32(st + L::V);
@@ -608,7 +685,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
       for (int np = 0; np < 4; ++np) {
         uint32_t v[4];
         // tile[token][column]: rows of V^T are its columns
-        ldsm4_t(uV + piece(16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), 2 * w + ((lane >> 3) & 1), 128), v);
+        ldsm4_t(uV + piece(16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int nt = 2 * np + x;
@@ -632,7 +709,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
 #pragma unroll 1
       for (int q = 0; q < NK / 2; ++q) {
         float acc[4][4], x[4][4];
-        quad_product<rb>(uK, q, ut, lane, acc);
+        quad_product(uK, q, ut, lane, acc);
         update_quad(hS, q, lane, end, 1.f, acc, x);
       }
     }
@@ -641,16 +718,23 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
   }
 
   const int ltid = tid - 32 * W;
-  if (n > 0) load_stage<NK, 2, W>(sm, a, bh * a.n, tok, h, col0, min(len, kC), a.v, a.ld_v, a.by_v, ltid);
+  const auto load = [&](int c) {
+    load_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, bh * a.n + c, tok + c * kC, h, col0,
+                         min(len - c * kC, kC), a.v, a.ld_v, a.by_v, &maps.v, ltid);
+  };
+  if (n > 0) load(0);
   for (int c = 0; c < n; ++c) {
     const int64_t u = bh * a.n + c;
+    unsigned char *st = sm + (c & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
-    if (c + 1 < n)
-      load_stage<NK, 2, W>(sm + ((c + 1) & 1) * L::stage, a, u + 1, tok + (c + 1) * kC, h, col0,
-                           min(len - (c + 1) * kC, kC), a.v, a.ld_v, a.by_v, ltid);
+    if (c + 1 < n) load(c + 1);
+    wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
+    if (len - c * kC < kC) {
+      clear_stage<NK, 2, W>(st, a, len - c * kC, a.by_v, ltid);
+      __syncthreads();
+    }
     if (!mine) continue;
-    unsigned char *st = sm + (c & 1) * L::stage;
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(st + L::M);
     const float *gam = reinterpret_cast<const float *>(st + L::sc), *beta = gam + 2 * kC;
     float Y[8][4], E[8][4];
@@ -663,7 +747,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
         float x[2][4];
         get_parts(hS + ks * 96, lane, s);
 #pragma unroll
-        for (int np = 0; np < 4; ++np) b_rows(uQ, rb, 16 * np, 16 * ks, lane, r[np]);
+        for (int np = 0; np < 4; ++np) b_rows(uQ, 16 * np, 16 * ks, lane, r[np]);
         join(s, x[0], x[1]);
         put(kept + 64 * ks, lane, x);
 #pragma unroll
@@ -715,9 +799,9 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a) {
 }
 
 template <int NK, int W>
-__global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
+__global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Chain<NK, 3, W>;
-  constexpr int NT = 2 * NK, rb = L::rb;
+  constexpr int NT = 2 * NK;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, t = lane & 3;
   const bool second = tid >= 32 * W;
@@ -730,6 +814,15 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
   const bool mine = col < a.dv;
   uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96;
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
+  const int vc = (col0 & 63) + 16 * w;  // the warp's columns in the value columns' panel
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
+  if (tid == 0) {
+    umma::mbar_init(smem_u32(bars), 1);
+    umma::mbar_init(smem_u32(bars + 1), 1);
+    umma::fence_mbar_init();
+  }
+  __syncthreads();
+  uint32_t limit = kWaitLimit;
 
   if (!second) {
     if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
@@ -746,9 +839,12 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
         put(kept + n * step + ks * 64, lane, x);
       }
     for (int c = n - 1; c >= 0; --c) {
+      const int it = n - 1 - c;
       __syncthreads();
+      wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
+      if (len - c * kC < kC) __syncthreads();  // the second warps clear rows
       if (!mine) continue;
-      unsigned char *st = sm + (c & 1) * L::stage;
+      unsigned char *st = sm + (it & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
       // dU^T = tail G^T K^T + dY^T M
@@ -770,7 +866,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
 #pragma unroll 1
       for (int q = 0; q < NK / 2; ++q) {
         float acc[4][4], x[4][4];
-        quad_product<rb>(uK, q, zt, lane, acc);
+        quad_product(uK, q, zt, lane, acc);
         update_quad(hG, q, lane, 1.f, -1.f, acc, x);
         put(to + q * 128, lane, x);
       }
@@ -780,18 +876,25 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
   }
 
   const int ltid = tid - 32 * W;
-  if (n > 0)
-    load_stage<NK, 3, W>(sm + ((n - 1) & 1) * L::stage, a, bh * a.n + n - 1, tok + (n - 1) * kC, h, col0,
-                         min(len - (n - 1) * kC, kC), a.dy, ld_y, a.by_dy, ltid);
+  const auto load = [&](int c) {
+    const int s = (n - 1 - c) & 1;
+    load_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, bh * a.n + c, tok + c * kC, h, col0, min(len - c * kC, kC),
+                         a.dy, ld_y, a.by_dy, &maps.dy, ltid);
+  };
+  if (n > 0) load(n - 1);
   for (int c = n - 1; c >= 0; --c) {
+    const int it = n - 1 - c;
     const int64_t u = bh * a.n + c;
+    unsigned char *st = sm + (it & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
-    if (c > 0)
-      load_stage<NK, 3, W>(sm + ((c - 1) & 1) * L::stage, a, u - 1, tok + (c - 1) * kC, h, col0, kC, a.dy, ld_y, a.by_dy,
-                           ltid);
+    if (c > 0) load(c - 1);
+    wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
+    if (len - c * kC < kC) {
+      clear_stage<NK, 3, W>(st, a, len - c * kC, a.by_dy, ltid);
+      __syncthreads();
+    }
     if (!mine) continue;
-    unsigned char *st = sm + (c & 1) * L::stage;
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(st + L::M), uY = smem_u32(st + L::V);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
     uint32_t y[4][1][4];
@@ -801,7 +904,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
       clear(l);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        a_cols(uY, 128, 16 * w, 16 * ks, lane, y[ks][0]);
+        a_cols(uY, vc, 16 * ks, lane, y[ks][0]);
 #pragma unroll
         for (int np = 0; np <= ks; ++np) {
           uint32_t r[3][4];
@@ -833,7 +936,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
 #pragma unroll 1
     for (int q = 0; q < NK / 2; ++q) {
       float acc[4][4], x[4][4];
-      quad_product<rb>(uQ, q, d3, lane, acc);
+      quad_product(uQ, q, d3, lane, acc);
       update_quad(hG, q, lane, end, 1.f, acc, x);
     }
     pair_sync(w);
@@ -854,12 +957,15 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a) {
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 512;
 
+constexpr int kRing = 3;  // tiles of the states on their way
+
 template <int NK>
 struct Grad {
-  static constexpr int rb = NK * 32;
-  static constexpr int K = 0, Q = K + kC * rb, Y = Q + kC * rb, V = Y + 2 * kTile, U = V + 2 * kTile,
-                       Z = U + 8 * 3 * 4 * 512, sc = Z + 8 * 2 * 4 * 512,
-                       size = sc + (kScal + 8 * 3 * kC + 8) * 4;
+  static constexpr int P = NK / 4;
+  static constexpr int K = 0, Q = K + P * kPanel, Y = Q + P * kPanel, V = Y + 2 * kTile, U = V + 2 * kTile,
+                       Z = U + 8 * 3 * 4 * 512, ring = Z + 8 * 2 * 4 * 512, part = 2 * NK * 512 /* one state's tile */,
+                       sc = ring + kRing * 3 * part, bars = sc + (kScal + 8 * 3 * kC + 8) * 4,
+                       size = bars + (2 * kRing + 1) * 8;
   static constexpr int X = U, N = X + 3 * kTile;  // once the value columns are done: X in three parts, N + N^T in two
 };
 
@@ -877,9 +983,9 @@ __device__ __forceinline__ void sum_rows(float (&v)[16], int lane) {
 }
 
 template <int NK>
-__global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
+__global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Grad<NK>;
-  constexpr int rb = L::rb, NT = 2 * NK, NW = NK / 4;  // NW: n-tiles of key channels a warp
+  constexpr int NT = 2 * NK, NW = NK / 4;  // NW: n-tiles of key channels a warp
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, w = (tid >> 5) & 7, half = tid >> 8, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x, bh = u / a.n;
@@ -892,12 +998,64 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
   float *gam = sc, *tail = sc + kC, *beta = sc + 2 * kC, *lh = sc + 3 * kC, *ll = sc + 4 * kC, *sg = sc + 5 * kC;
   float *rows = sc + kScal /* [8][2][64]: dZ . E and v . dZ */, *flow = rows + 8 * 2 * kC /* [8][64] */,
         *red = flow + 8 * kC;
-  load_tile<rb, kGradThreads>(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-  load_tile<rb, kGradThreads>(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-  if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
+  const uint32_t uY = smem_u32(sm + L::Y), uV = smem_u32(sm + L::V);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + kRing, *tile_bar = empty + kRing;
+  const unsigned char *gS = reinterpret_cast<const unsigned char *>(a.s) + u * tiles * L::part,
+                      *gG = reinterpret_cast<const unsigned char *>(a.g) + (bh * (a.n + 1) + c) * tiles * L::part;
+  // one thread: the states' tile kt (S, G at the chunk's start and at its end) into the ring
+  const auto load_states = [&](int kt) {
+    const uint32_t mb = smem_u32(full + kt % kRing), to = smem_u32(sm + L::ring) + (kt % kRing) * 3 * L::part;
+    umma::mbar_expect_tx(mb, 3 * L::part);
+    umma::bulk_g2s(to, gS + kt * L::part, L::part, mb);
+    umma::bulk_g2s(to + L::part, gG + kt * L::part, L::part, mb);
+    umma::bulk_g2s(to + 2 * L::part, gG + (static_cast<int64_t>(tiles) + kt) * L::part, L::part, mb);
+  };
+  // the value columns' tiles from column c0 on
+  const auto load_columns = [&](int c0) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int cx = c0 + 64 * x;
+      if (cx >= a.dv) continue;
+      if (a.by_dy != 16)
+        load_tile<1, kGradThreads>(sm + L::Y + x * kTile, a.dy + tok * ld_y + h * a.dv + cx, ld_y, live, min(64, a.dv - cx),
+                                   a.by_dy, tid);
+      else if (tid == 0)
+        tensor_panel(uY + x * kTile, &maps.dy, cx, h, static_cast<int>(tok), smem_u32(tile_bar));
+      if (a.by_v != 16)
+        load_tile<1, kGradThreads>(sm + L::V + x * kTile, a.v + tok * a.ld_v + h * a.dv + cx, a.ld_v, live,
+                                   min(64, a.dv - cx), a.by_v, tid);
+      else if (tid == 0)
+        tensor_panel(uV + x * kTile, &maps.v, cx, h, static_cast<int>(tok), smem_u32(tile_bar));
+    }
+    cp_async_commit();
+  };
+  const auto column_bytes = [&](int c0) {
+    return static_cast<uint32_t>(((a.by_dy == 16) + (a.by_v == 16)) * (c0 + 64 < a.dv ? 2 : 1) * kPanel);
+  };
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      umma::mbar_init(smem_u32(full + i), 1);
+      umma::mbar_init(smem_u32(empty + i), kGradThreads / 32);
+    }
+    umma::mbar_init(smem_u32(tile_bar), 1);
+    umma::fence_mbar_init();
+    const uint32_t more = kScal * 4 + column_bytes(0);
+    if (a.by_qk == 16)
+      load_qk<NK>(maps, sm + L::K, sm + L::Q, hk, tok, smem_u32(tile_bar), more);
+    else
+      umma::mbar_expect_tx(smem_u32(tile_bar), more);
+    umma::bulk_g2s(smem_u32(sc), a.scal + u * kScal, kScal * 4, smem_u32(tile_bar));
+  }
+  if (a.by_qk != 16) {
+    load_tile<L::P, kGradThreads>(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+    load_tile<L::P, kGradThreads>(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  }
+  load_columns(0);
+  if (tid == 0)
+    for (int kt = 0; kt < min(kRing, tiles); ++kt) load_states(kt);
+  uint32_t limit = kWaitLimit;
   if (w >= tiles) rows[(2 * w + half) * kC + lane] = rows[(2 * w + half) * kC + 32 + lane] = 0.f;
   uint4 *sU = reinterpret_cast<uint4 *>(sm + L::U), *sZ = reinterpret_cast<uint4 *>(sm + L::Z);
-  const uint32_t uY = smem_u32(sm + L::Y), uV = smem_u32(sm + L::V);
 
   // m-tiles 2 half and 2 half + 1
   float dQ[2][NW][4], dA[2][NW][4], dK[2][NW][4], X[2][4], N[2][4];
@@ -916,19 +1074,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
       get(reinterpret_cast<const float4 *>(a.e) + at, lane, E);
       get(reinterpret_cast<const float4 *>(a.dz) + at, lane, Z);
     }
-    if (c0) __syncthreads();  // the piece before has been read
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int cx = c0 + 64 * x;
-      if (cx >= a.dv) continue;
-      load_tile<128, kGradThreads>(sm + L::Y + x * kTile, a.dy + tok * ld_y + h * a.dv + cx, ld_y, live, min(64, a.dv - cx),
-                                   a.by_dy, tid);
-      load_tile<128, kGradThreads>(sm + L::V + x * kTile, a.v + tok * a.ld_v + h * a.dv + cx, a.ld_v, live,
-                                   min(64, a.dv - cx), a.by_v, tid);
+    if (c0) {
+      __syncthreads();  // the piece before has been read
+      if (tid == 0) umma::mbar_expect_tx(smem_u32(tile_bar), column_bytes(c0));
+      load_columns(c0);
     }
-    cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
+    wait_copies(tile_bar, (c0 >> 7) & 1, limit, a);
+    if (live < kC) {
+      if (a.by_qk == 16 && c0 == 0) {
+        clear_rows<L::P, kGradThreads>(sm + L::K, live, tid);
+        clear_rows<L::P, kGradThreads>(sm + L::Q, live, tid);
+      }
+      for (int x = 0; x < 2; ++x) {
+        if (a.by_dy == 16) clear_rows<1, kGradThreads>(sm + L::Y + x * kTile, live, tid);
+        if (a.by_v == 16) clear_rows<1, kGradThreads>(sm + L::V + x * kTile, live, tid);
+      }
+      umma::fence_async_smem();
+      __syncthreads();
+    }
     if (w < nt_cols) {
       uint16_t *dvp = a.odv + tok * a.ld_dv + h * a.dv + c0 + 16 * w + 2 * t;
       float sum[16];  // [dZ . E, v . dZ][n-tile][token of the pair]
@@ -936,7 +1101,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
       for (int np = 0; np < 2; ++np) {
         uint32_t v[4], pu[3][4], pz[2][4];
         ldsm4_t(uV + (w >> 2) * kTile +
-                    piece(32 * half + 16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), 2 * (w & 3) + ((lane >> 3) & 1), 128),
+                    piece(32 * half + 16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), 2 * (w & 3) + ((lane >> 3) & 1)),
                 v);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -983,18 +1148,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
     }
     __syncthreads();
 
-    const float4 *S = reinterpret_cast<const float4 *>(a.s) + ((u * tiles + (c0 >> 4)) * NT + w * NW) * 32 + lane;
-    const float4 *G0 = reinterpret_cast<const float4 *>(a.g) +
-                       (((bh * (a.n + 1) + c) * tiles + (c0 >> 4)) * NT + w * NW) * 32 + lane;
-    const float4 *G1 = G0 + static_cast<int64_t>(tiles) * NT * 32;
-    float4 fs[NW], f0[NW], f1[NW];
-#pragma unroll
-    for (int x = 0; x < NW; ++x) {
-      fs[x] = S[x * 32], f1[x] = G1[x * 32];
-      if (half == 0) f0[x] = G0[x * 32];
-    }
 #pragma unroll 1
     for (int kt = 0; kt < nt_cols; ++kt) {
+      const int at = (c0 >> 4) + kt, slot = at % kRing;
+      const uint32_t parity = (at / kRing) & 1;
+      if (tid == 0 && at > 0 && at + kRing - 1 < tiles) {  // the slot of the tile before, once everyone has it
+        wait_copies(empty + (at - 1) % kRing, ((at - 1) / kRing) & 1, limit, a);
+        load_states(at + kRing - 1);
+      }
+      __syncwarp();
+      wait_copies(full + slot, parity, limit, a);
+      float4 fs[NW], f0[NW], f1[NW];
+      const float4 *from = reinterpret_cast<const float4 *>(sm + L::ring + slot * 3 * L::part) + w * NW * 32 + lane;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        fs[x] = from[x * 32], f1[x] = from[2 * NT * 32 + x * 32];
+        if (half == 0) f0[x] = from[NT * 32 + x * 32];
+      }
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(smem_u32(empty + slot));
       uint32_t bs[NW][3][2], bg[NW][2][2];
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
@@ -1009,14 +1181,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) bg[x][p][0] = transpose8(q0[p]), bg[x][p][1] = transpose8(q1[p]);
       }
-      if (kt + 1 < nt_cols) {
-        S += NT * 32, G0 += NT * 32, G1 += NT * 32;
-#pragma unroll
-        for (int x = 0; x < NW; ++x) {
-      fs[x] = S[x * 32], f1[x] = G1[x * 32];
-      if (half == 0) f0[x] = G0[x * 32];
-    }
-      }
       uint32_t bu[3][2];
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
@@ -1028,7 +1192,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
       for (int m = 0; m < 2; ++m) {
         const int mt = 2 * half + m;
         uint32_t y[4], uu[2][4], z[2][4];
-        a_rows(uY + (kt >> 2) * kTile, 128, 16 * mt, 16 * (kt & 3), lane, y);
+        a_rows(uY + (kt >> 2) * kTile, 16 * mt, 16 * (kt & 3), lane, y);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const uint4 vu = sU[((kt * 3 + p) * 4 + mt) * 32 + lane], vz = sZ[((kt * 2 + p) * 4 + mt) * 32 + lane];
@@ -1084,7 +1248,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
       uint32_t sx[3], sn[2];
       split<3>(xv[0], xv[1], sx);
       split<2>(nv[0], nv[1], sn);
-      const uint32_t off = piece(i, w, 128) + 4 * t;
+      const uint32_t off = piece(i, w) + 4 * t;
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t *>(sm + L::X + p * kTile + off) = sx[p];
 #pragma unroll
@@ -1093,11 +1257,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
         const uint16_t lo = static_cast<uint16_t>(sn[p]), hi = static_cast<uint16_t>(sn[p] >> 16);
         if (j <= i) {
           *reinterpret_cast<uint16_t *>(tile + off) = lo;
-          *reinterpret_cast<uint16_t *>(tile + piece(j, i >> 3, 128) + 2 * (i & 7)) = lo;
+          *reinterpret_cast<uint16_t *>(tile + piece(j, i >> 3) + 2 * (i & 7)) = lo;
         }
         if (j + 1 <= i) {
           *reinterpret_cast<uint16_t *>(tile + off + 2) = hi;
-          *reinterpret_cast<uint16_t *>(tile + piece(j + 1, i >> 3, 128) + 2 * (i & 7)) = hi;
+          *reinterpret_cast<uint16_t *>(tile + piece(j + 1, i >> 3) + 2 * (i & 7)) = hi;
         }
       }
     }
@@ -1108,8 +1272,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
   for (int ks = 0; ks < 4; ++ks) {
     uint32_t bk[4], bq[4];  // of 16 key channels: this warp's, or with another's beside them
     constexpr int share = 2 / NW;
-    b_cols(uK, rb, 16 * (w / share), 16 * ks, lane, bk);
-    b_cols(uQ, rb, 16 * (w / share), 16 * ks, lane, bq);
+    b_cols(uK, 16 * (w / share), 16 * ks, lane, bk);
+    b_cols(uQ, 16 * (w / share), 16 * ks, lane, bq);
     if (NW == 1 && (w & 1)) bk[0] = bk[2], bk[1] = bk[3], bq[0] = bq[2], bq[1] = bq[3];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -1117,21 +1281,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
       uint32_t f[4];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        a_rows(uN + p * kTile, 128, 16 * mt, 16 * ks, lane, f);
+        a_rows(uN + p * kTile, 16 * mt, 16 * ks, lane, f);
 #pragma unroll
         for (int x = 0; x < NW; ++x) fma16816(dK[m][x], f, bk[2 * x], bk[2 * x + 1]);
       }
       if (ks <= mt)
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-          a_rows(uX + p * kTile, 128, 16 * mt, 16 * ks, lane, f);
+          a_rows(uX + p * kTile, 16 * mt, 16 * ks, lane, f);
 #pragma unroll
           for (int x = 0; x < NW; ++x) fma16816(dQ[m][x], f, bk[2 * x], bk[2 * x + 1]);
         }
       if (ks >= mt)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          a_cols(uX + p * kTile, 128, 16 * mt, 16 * ks, lane, f);
+          a_cols(uX + p * kTile, 16 * mt, 16 * ks, lane, f);
 #pragma unroll
           for (int x = 0; x < NW; ++x) fma16816(dK[m][x], f, bq[2 * x], bq[2 * x + 1]);
         }
@@ -1146,7 +1310,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
       float qd = 0.f;
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
-        const uint32_t v = *reinterpret_cast<const uint32_t *>(sm + L::Q + piece(i, w * NW + x, rb) + 4 * t);
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(sm + L::Q + piece(i, w * NW + x) + 4 * t);
         qd += low2(v) * dQ[m][x][2 * r] + high2(v) * dQ[m][x][2 * r + 1];
       }
       qd += __shfl_xor_sync(kFull, qd, 1);
@@ -1161,15 +1325,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
-      Wide f{0.f, 0.f};
+      float f = 0.f;
       ez[i] = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f = f + Wide{flow[e * kC + m], 0.f} - Wide{rows[(2 * e + 1) * kC + m], 0.f};
+        f += flow[e * kC + m] - rows[(2 * e + 1) * kC + m];
         ez[i] += rows[2 * e * kC + m];
       }
-      before[i] = f;
-      x[i] = running(f, lane);
+      before[i] = {f, 0.f};
+      x[i] = running(before[i], lane);
       seg[i] = __float_as_int(sg[m]);
     }
     x[1] = shfl(x[0], 31) + x[1];
@@ -1178,9 +1342,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a) {
     before[0] = x[0] - before[0];  // sum over s < t
     before[1] = x[1] - before[1];
     const uint32_t upto = 0xffffffffu >> (31 - lane);
-    Wide start{0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) start = start + Wide{red[i], 0.f};
+    const Wide start{((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7])), 0.f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
@@ -1311,6 +1473,39 @@ int row_bytes(const void *p, int64_t ld, int width) {
   return 2;
 }
 
+// a tensor map of [tokens][heads][d] bf16, tokens ld elements apart, boxes of 64 tokens x 64 channels
+int make_map(CUtensorMap *map, const void *p, int64_t ld, int64_t tokens, int heads, int d) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<Encode>(f)
+               : nullptr;
+  }();
+  if (!encode) return set_error(SDM_ERR_CUDA, "gdn_train: the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, 1, kC}, steps[3] = {1, 1, 1};
+  if (encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return set_error(SDM_ERR_CUDA, "gdn_train: cuTensorMapEncodeTiled failed");
+  return SDM_OK;
+}
+
+int make_maps(Maps *m, const Gdn &a) {
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
+  int rc = SDM_OK;
+  if (tokens == 0) return rc;
+  if (a.by_qk == 16) rc = make_map(&m->q, a.q, a.ld_q, tokens, a.Hk, a.dk);
+  if (rc == SDM_OK && a.by_qk == 16) rc = make_map(&m->k, a.k, a.ld_k, tokens, a.Hk, a.dk);
+  if (rc == SDM_OK && a.by_v == 16) rc = make_map(&m->v, a.v, a.ld_v, tokens, a.H, a.dv);
+  if (rc == SDM_OK && a.dy && a.by_dy == 16) rc = make_map(&m->dy, a.dy, static_cast<int64_t>(a.H) * a.dv, tokens, a.H, a.dv);
+  return rc;
+}
+
 void place_saved(Gdn &a, void *saved, const Layout &l) {
   unsigned char *p = static_cast<unsigned char *>(saved);
   a.n = static_cast<int>(l.n);
@@ -1322,10 +1517,10 @@ void place_saved(Gdn &a, void *saved, const Layout &l) {
 }
 
 template <typename K>
-int launch(K kernel, const char *what, int64_t grid, int threads, int smem, const Gdn &a, cudaStream_t st) {
+int launch(K kernel, const char *what, int64_t grid, int threads, int smem, const Gdn &a, const Maps &maps, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  kernel<<<static_cast<unsigned>(grid), threads, smem, st>>>(a);
+  kernel<<<static_cast<unsigned>(grid), threads, smem, st>>>(a, maps);
   return check_launch(what);
 }
 
@@ -1339,37 +1534,46 @@ int chain_width(const Gdn &a, const Layout &l) {
 }
 
 template <int NK, int W>
-int run_chain(const Gdn &a, const Layout &l, bool back, cudaStream_t st) {
+int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
-  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, 64 * W, Chain<NK, 3, W>::size, a, st)
-              : launch(gdn_chain<NK, W>, "gdn_train", grid, 64 * W, Chain<NK, 2, W>::size, a, st);
+  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, 64 * W, Chain<NK, 3, W>::size, a, maps, st)
+              : launch(gdn_chain<NK, W>, "gdn_train", grid, 64 * W, Chain<NK, 2, W>::size, a, maps, st);
 }
 template <int NK>
-int run_chain(const Gdn &a, const Layout &l, bool back, cudaStream_t st) {
+int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int w = chain_width(a, l);
-  return w == 1 ? run_chain<NK, 1>(a, l, back, st) : w == 2 ? run_chain<NK, 2>(a, l, back, st) : run_chain<NK, 4>(a, l, back, st);
+  return w == 1 ? run_chain<NK, 1>(a, maps, l, back, st)
+         : w == 2 ? run_chain<NK, 2>(a, maps, l, back, st) : run_chain<NK, 4>(a, maps, l, back, st);
 }
 
 template <int NK>
 int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
+  Maps maps{};
+  int rc = make_maps(&maps, a);
+  if (rc != SDM_OK) return rc;
   if (l.units > 0) {
-    const int rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, 2 * kC * NK * 32 + (2 * kC * kLd + kScal) * 4, a, st);
+    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, 2 * kC * NK * 32 + (2 * kC * kLd + kScal) * 4 + 16, a, maps, st);
     if (rc != SDM_OK) return rc;
   }
-  return run_chain<NK>(a, l, false, st);
+  return run_chain<NK>(a, maps, l, false, st);
 }
 
 template <int NK>
 int run_backward(const Gdn &a, const Layout &l, cudaStream_t st) {
-  int rc = run_chain<NK>(a, l, true, st);
+  Maps maps{};
+  int rc = make_maps(&maps, a);
+  if (rc == SDM_OK) rc = run_chain<NK>(a, maps, l, true, st);
   if (rc != SDM_OK || l.units == 0) return rc;
-  rc = launch(gdn_grad<NK>, "gdn_backward", l.units, kGradThreads, Grad<NK>::size, a, st);
+  rc = launch(gdn_grad<NK>, "gdn_backward", l.units, kGradThreads, Grad<NK>::size, a, maps, st);
   if (rc != SDM_OK || !a.pdq) return rc;
   gdn_grad_heads<<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T), 256, 0, st>>>(a);
   return check_launch("gdn_backward");
 }
 
 }  // namespace
+
+SDM_STICKY_ACCESSOR(sticky_gdn_train)
+
 }  // namespace sdm
 
 using namespace sdm;

@@ -1,9 +1,10 @@
 // mma.cuh - warp-level bf16 matrix products (mma.sync m16n8k16, fp32 sums) on
 // shared-memory tiles, for chains whose operands stay in registers.
 //
-// A tile is row-major bf16 with rows of a multiple of 128 bytes; the 16-byte
-// piece p of row r lies at piece p ^ (r & 7), so the eight rows that one
-// ldmatrix phase reads lie in different banks.
+// A tile has 64 rows in panels of 64 columns, each panel row-major with rows of
+// 128 bytes and aligned to 1024; the 16-byte piece p of a panel's row r lies at
+// piece p ^ (r & 7), so the eight rows that one ldmatrix phase reads lie in
+// different banks (the layout that a tensor copy with the 128-byte swizzle writes).
 //
 // Fragments (g = lane / 4, t = lane % 4): the accumulator of an m16n8 product
 // holds rows g and g + 8, columns 2t and 2t + 1.  Two neighbouring ones are, as
@@ -18,9 +19,11 @@
 namespace sdm {
 namespace mma {
 
-// byte offset of 16-byte piece p of row r, rows of `rb` bytes
-__device__ __forceinline__ uint32_t piece(int r, int p, int rb) {
-  return static_cast<uint32_t>(r * rb + ((p ^ (r & 7)) << 4));
+constexpr int kPanel = 64 * 128;
+
+// byte offset of 16-byte piece p (of all panels) of row r
+__device__ __forceinline__ uint32_t piece(int r, int p) {
+  return static_cast<uint32_t>((p >> 3) * kPanel + r * 128 + (((p & 7) ^ (r & 7)) << 4));
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t saddr, uint32_t (&r)[4]) {
@@ -38,20 +41,20 @@ __device__ __forceinline__ void ldsm4_t(uint32_t saddr, uint32_t (&r)[4]) {
 
 // B fragments of two n-tiles (n0 .. n0+15) and one k-step from tile[n][k]:
 // r[0], r[1] of the first, r[2], r[3] of the second
-__device__ __forceinline__ void b_rows(uint32_t tile, int rb, int n0, int k0, int lane, uint32_t (&r)[4]) {
-  ldsm4(tile + piece(n0 + ((lane >> 4) << 3) + (lane & 7), (k0 >> 3) + ((lane >> 3) & 1), rb), r);
+__device__ __forceinline__ void b_rows(uint32_t tile, int n0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4(tile + piece(n0 + ((lane >> 4) << 3) + (lane & 7), (k0 >> 3) + ((lane >> 3) & 1)), r);
 }
 // the same from tile[k][n]
-__device__ __forceinline__ void b_cols(uint32_t tile, int rb, int n0, int k0, int lane, uint32_t (&r)[4]) {
-  ldsm4_t(tile + piece(k0 + (((lane >> 3) & 1) << 3) + (lane & 7), (n0 >> 3) + (lane >> 4), rb), r);
+__device__ __forceinline__ void b_cols(uint32_t tile, int n0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4_t(tile + piece(k0 + (((lane >> 3) & 1) << 3) + (lane & 7), (n0 >> 3) + (lane >> 4)), r);
 }
 // A fragment (rows m0 .. m0+15, one k-step) from tile[m][k] ...
-__device__ __forceinline__ void a_rows(uint32_t tile, int rb, int m0, int k0, int lane, uint32_t (&r)[4]) {
-  ldsm4(tile + piece(m0 + (((lane >> 3) & 1) << 3) + (lane & 7), (k0 >> 3) + (lane >> 4), rb), r);
+__device__ __forceinline__ void a_rows(uint32_t tile, int m0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4(tile + piece(m0 + (((lane >> 3) & 1) << 3) + (lane & 7), (k0 >> 3) + (lane >> 4)), r);
 }
 // ... and from tile[k][m]
-__device__ __forceinline__ void a_cols(uint32_t tile, int rb, int m0, int k0, int lane, uint32_t (&r)[4]) {
-  ldsm4_t(tile + piece(k0 + ((lane >> 4) << 3) + (lane & 7), (m0 >> 3) + ((lane >> 3) & 1), rb), r);
+__device__ __forceinline__ void a_cols(uint32_t tile, int m0, int k0, int lane, uint32_t (&r)[4]) {
+  ldsm4_t(tile + piece(k0 + ((lane >> 4) << 3) + (lane & 7), (m0 >> 3) + ((lane >> 3) & 1)), r);
 }
 
 // d += a b
@@ -117,34 +120,33 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool l
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 
-template <int RB, int THREADS, int BYTES>
+template <int PANELS, int THREADS, int BYTES>
 __device__ __forceinline__ void load_tile_by(unsigned char *tile, const uint16_t *src, int64_t ld, int live, int width,
                                              int tid) {
-  constexpr int pieces = RB / BYTES, most = 64 * pieces / THREADS;
+  constexpr int pieces = PANELS * 128 / BYTES;
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(tile));
-#pragma unroll(most <= 16 ? most : 8)
-  for (int i = 0; i < most; ++i) {
+#pragma unroll 8
+  for (int i = 0; i < 64 * pieces / THREADS; ++i) {
     const int id = tid + i * THREADS, r = id / pieces, p = id % pieces;
     const bool ok = r < live && p * (BYTES / 2) < width;
-    copy_async<BYTES>(base + piece(r, p * BYTES / 16, RB) + p * BYTES % 16, ok ? src + r * ld + p * (BYTES / 2) : src, ok);
+    copy_async<BYTES>(base + piece(r, p * BYTES / 16) + p * BYTES % 16, ok ? src + r * ld + p * (BYTES / 2) : src, ok);
   }
 }
 
-// 64 rows of `width` bf16 (row r at src + r * ld) into a tile of rows of RB
-// bytes, zeros behind `width` and from row `live` on, by THREADS threads (a
-// power of two).  bytes: what divides the address, the distance and the width
-// of every row (16, 8 or 4: asynchronous copies of that size; else by elements).
-template <int RB, int THREADS>
+// 64 rows of `width` bf16 (row r at src + r * ld) into a tile, zeros behind
+// `width` and from row `live` on, by THREADS threads (a power of two).  bytes:
+// what divides the address, the distance and the width of every row (8 or 4:
+// asynchronous copies of that size; else by elements).  Where it is 16, a
+// tensor copy does the same.
+template <int PANELS, int THREADS>
 __device__ __forceinline__ void load_tile(unsigned char *tile, const uint16_t *src, int64_t ld, int live, int width,
                                           int bytes, int tid) {
-  if (bytes == 16) {
-    load_tile_by<RB, THREADS, 16>(tile, src, ld, live, width, tid);
-  } else if (bytes == 8) {
-    load_tile_by<RB, THREADS, 8>(tile, src, ld, live, width, tid);
+  if (bytes >= 8) {
+    load_tile_by<PANELS, THREADS, 8>(tile, src, ld, live, width, tid);
   } else if (bytes == 4) {
-    load_tile_by<RB, THREADS, 4>(tile, src, ld, live, width, tid);
+    load_tile_by<PANELS, THREADS, 4>(tile, src, ld, live, width, tid);
   } else {
-    constexpr int pieces = RB / 16;
+    constexpr int pieces = PANELS * 8;
     for (int id = tid; id < 64 * pieces; id += THREADS) {
       const int r = id / pieces, c = id % pieces * 8;
       uint32_t w[4] = {0, 0, 0, 0};
@@ -154,9 +156,26 @@ __device__ __forceinline__ void load_tile(unsigned char *tile, const uint16_t *s
         for (int e = 0; e < 8; ++e)
           if (c + e < width) w[e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
       }
-      *reinterpret_cast<uint4 *>(tile + piece(r, c / 8, RB)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(tile + piece(r, c / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// rows `live` .. 63 of a tile to zero
+template <int PANELS, int THREADS>
+__device__ __forceinline__ void clear_rows(unsigned char *tile, int live, int tid) {
+  for (int id = live * PANELS * 8 + tid; id < 64 * PANELS * 8; id += THREADS)
+    *reinterpret_cast<uint4 *>(tile + piece(id / (PANELS * 8), id % (PANELS * 8))) = make_uint4(0, 0, 0, 0);
+}
+
+// a panel of a tensor map's [token][head][channel] (box: 64 tokens, one head, 64
+// channels), by one thread; completes its 8 KB on the mbarrier.  channel: a multiple of 64
+__device__ __forceinline__ void tensor_panel(uint32_t dst, const void *map, int channel, int head, int token, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          dst),
+      "l"(map), "r"(channel), "r"(head), "r"(token), "r"(mbar)
+      : "memory");
 }
 
 }  // namespace mma
