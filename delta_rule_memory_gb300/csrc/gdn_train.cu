@@ -52,6 +52,7 @@ namespace {
 
 using namespace mma;
 
+constexpr int kSms = 152;
 constexpr int kC = 64;                  // tokens of a chunk
 constexpr int kTile = kPanel;           // bytes of one bf16 [64][64] tile
 constexpr int kTri = 10 * 512;          // ... of a lower triangular one: its ten 16 x 16 blocks
@@ -142,6 +143,7 @@ __device__ __forceinline__ int length_of(const Gdn &a, int b) {
 // gdn_prep: decays, M and T of one chunk of one head.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 128;
+static_assert(2 * kC * kLd * 4 >= 4 * kPanel, "the tiles fit where L and X will be");
 
 __device__ __forceinline__ void store_parts3(unsigned char *tiles, uint32_t off, const float *x) {
   uint32_t s[4][3];
@@ -255,8 +257,8 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
   constexpr int panels = NK / 4;
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char *sK = sm, *sQ = sm + panels * kPanel;
-  float *sL = reinterpret_cast<float *>(sm + 2 * panels * kPanel), *sX = sL + kC * kLd, *sc = sX + kC * kLd;
-  float *zt = reinterpret_cast<float *>(sm);  // the K tile's place, once the products are formed
+  // L and X take the tiles' place once the products are formed
+  float *sL = reinterpret_cast<float *>(sm), *sX = sL + kC * kLd, *zt = sX + kC * kLd, *sc = zt + 32 * 36;
   uint64_t *bar = reinterpret_cast<uint64_t *>(sc + kScal);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x;
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
     }
   }
   const float *be = sc + 2 * kC, *lh = sc + 3 * kC, *ll = sc + 4 * kC, *sg = sc + 5 * kC;
+  __syncthreads();  // the tiles have been read
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt) {
     if (nt > 2 * w + 1) continue;
@@ -386,25 +389,46 @@ struct Chain {
   static constexpr int state = 2 * stage, tokens = state + W * NK * 3 * 512, bars = tokens + W * 8 * 512, size = bars + 16;
 };
 
-// the second warps' copies of a chunk's tiles; cols: the value columns' tensor
+// A chunk's tiles into a stage; cols: the value columns' tensor.  What tensor and
+// bulk copies bring is asked for by one lane of a warp of its own or, where a CTA
+// has four tiles and no room for another warp's registers, by one lane of each of
+// the second warps (a request holds its warp for a hundred cycles and more).
+template <int W>
+constexpr int kAskers = W < 4 ? 1 : 4;
+
 template <int NK, int PM, int W>
-__device__ __forceinline__ void load_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps, int64_t u,
-                                           int64_t tok, int h, int col0, int live, const uint16_t *cols, int64_t ld_cols,
-                                           int by_cols, const CUtensorMap *cols_map, int tid) {
+__device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps, int64_t u,
+                                              int64_t tok, int h, int col0, int by_cols, const CUtensorMap *cols_map, int who) {
   using L = Chain<NK, PM, W>;
-  constexpr int threads = 32 * W;
-  const int hk = h / (a.H / a.Hk), from = col0 & ~63;  // whole panels of value columns
-  if (tid == 0) {
-    const uint32_t mb = smem_u32(bar), more = (3 + PM) * kTri + 3 * kC * 4 + (by_cols == 16 ? kPanel : 0);
-    if (a.by_qk == 16)
-      load_qk<NK>(maps, st + L::K, st + L::Q, hk, tok, mb, more);
-    else
-      umma::mbar_expect_tx(mb, more);
-    if (by_cols == 16) tensor_panel(smem_u32(st + L::V), cols_map, from, h, static_cast<int>(tok), mb);
+  constexpr bool all = kAskers<W> == 1;
+  const uint32_t mb = smem_u32(bar);
+  const int hk = h / (a.H / a.Hk), token = static_cast<int>(tok);
+  const bool qk = a.by_qk == 16, cols = by_cols == 16;
+  const uint32_t part[4] = {qk ? L::P * kPanel : 0u, qk ? L::P * kPanel : 0u, 3 * kTri + (cols ? kPanel : 0u),
+                            PM * kTri + 3 * kC * 4u};
+  umma::mbar_expect_tx(mb, all ? part[0] + part[1] + part[2] + part[3] : part[who]);
+  if ((all || who == 0) && qk)
+#pragma unroll
+    for (int p = 0; p < L::P; ++p) tensor_panel(smem_u32(st + L::K) + p * kPanel, &maps.k, 64 * p, hk, token, mb);
+  if ((all || who == 1) && qk)
+#pragma unroll
+    for (int p = 0; p < L::P; ++p) tensor_panel(smem_u32(st + L::Q) + p * kPanel, &maps.q, 64 * p, hk, token, mb);
+  if (all || who == 2) {
     umma::bulk_g2s(smem_u32(st + L::T), a.t3 + u * (3 * kTri), 3 * kTri, mb);
+    if (cols) tensor_panel(smem_u32(st + L::V), cols_map, col0 & ~63, h, token, mb);
+  }
+  if (all || who == 3) {
     umma::bulk_g2s(smem_u32(st + L::M), a.m3 + u * (3 * kTri), PM * kTri, mb);
     umma::bulk_g2s(smem_u32(st + L::sc), a.scal + u * kScal, 3 * kC * 4, mb);
   }
+}
+// ... and the rest, by the second warps
+template <int NK, int PM, int W>
+__device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int64_t tok, int h, int col0, int live,
+                                           const uint16_t *cols, int64_t ld_cols, int by_cols, int tid) {
+  using L = Chain<NK, PM, W>;
+  constexpr int threads = 32 * W;
+  const int hk = h / (a.H / a.Hk), from = col0 & ~63;  // whole panels of value columns
   if (a.by_qk != 16) {
     load_tile<L::P, threads>(st + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
     load_tile<L::P, threads>(st + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
@@ -642,12 +666,12 @@ __device__ __forceinline__ void store_state(const uint4 *parts, float *m, int dk
 }
 
 template <int NK, int W>
-__global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Chain<NK, 2, W>;
   constexpr int NT = 2 * NK;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const bool second = tid >= 32 * W;
+  const int role = tid / (32 * W);
   const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
   const int64_t bh = blockIdx.x / groups;
   const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
@@ -660,16 +684,19 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a, const __grid
   const int vp = ((col0 & 63) >> 3) + 2 * w;  // the warp's pieces of the value columns' panel
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
   if (tid == 0) {
-    umma::mbar_init(smem_u32(bars), 1);
-    umma::mbar_init(smem_u32(bars + 1), 1);
+    umma::mbar_init(smem_u32(bars), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
     umma::fence_mbar_init();
   }
   __syncthreads();
   uint32_t limit = kWaitLimit;
 
-  if (!second) {
+  if (role == 0) {
     if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-    load_state<NK>(hS, a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane);
+    float S[NT][4];  // the state itself beside its parts
+    read_state<NT>(a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, 0, a.dk, a.dv, col, lane, S);
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) put_parts(hS + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
     for (int c = 0; c < n; ++c) {
       __syncthreads();
       wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
@@ -706,29 +733,54 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a, const __grid
       uint32_t ut[4][3][4];
       split_tokens(E, ut);
       const float end = gam[kC - 1];
-#pragma unroll 1
+#pragma unroll
       for (int q = 0; q < NK / 2; ++q) {
-        float acc[4][4], x[4][4];
+        float acc[4][4];
         quad_product(uK, q, ut, lane, acc);
-        update_quad(hS, q, lane, end, 1.f, acc, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[4 * q + i][e] = fmaf(end, S[4 * q + i][e], acc[i][e]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) put_parts(hS + (2 * q + i) * 96, lane, S[4 * q + 2 * i], S[4 * q + 2 * i + 1]);
       }
     }
-    if (mine) store_state<NK>(hS, a.state_out + bh * a.dk * a.dv, a.dk, a.dv, col, lane);
+    if (mine) write_state<NT>(a.state_out + bh * a.dk * a.dv, 0, a.dk, a.dv, col, lane, S);
     return;
   }
 
   const int ltid = tid - 32 * W;
-  const auto load = [&](int c) {
-    load_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, bh * a.n + c, tok + c * kC, h, col0,
-                         min(len - c * kC, kC), a.v, a.ld_v, a.by_v, &maps.v, ltid);
+  const auto request = [&](int c) {
+    if (lane == 0)
+      request_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, bh * a.n + c, tok + c * kC, h, col0, a.by_v,
+                              &maps.v, w);
+    __syncwarp();
   };
-  if (n > 0) load(0);
+  if (role == 2) {
+    for (int c = 0; c <= n; ++c) {
+      if (c > 0) __syncthreads();
+      if (c < n) request(c);
+      if (c > 0 && len - (c - 1) * kC < kC) __syncthreads();
+    }
+    return;
+  }
+
+  const auto copy = [&](int c) {
+    copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, tok + c * kC, h, col0, min(len - c * kC, kC), a.v, a.ld_v, a.by_v, ltid);
+  };
+  if (n > 0) {
+    if (kAskers<W> > 1) request(0);
+    copy(0);
+  }
   for (int c = 0; c < n; ++c) {
     const int64_t u = bh * a.n + c;
     unsigned char *st = sm + (c & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
-    if (c + 1 < n) load(c + 1);
+    if (c + 1 < n) {
+      if (kAskers<W> > 1) request(c + 1);
+      copy(c + 1);
+    }
     wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
       clear_stage<NK, 2, W>(st, a, len - c * kC, a.by_v, ltid);
@@ -799,12 +851,12 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain(const Gdn a, const __grid
 }
 
 template <int NK, int W>
-__global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_back(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Chain<NK, 3, W>;
   constexpr int NT = 2 * NK;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, t = lane & 3;
-  const bool second = tid >= 32 * W;
+  const int role = tid / (32 * W);
   const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
   const int64_t bh = blockIdx.x / groups;
   const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
@@ -817,14 +869,14 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a, const _
   const int vc = (col0 & 63) + 16 * w;  // the warp's columns in the value columns' panel
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
   if (tid == 0) {
-    umma::mbar_init(smem_u32(bars), 1);
-    umma::mbar_init(smem_u32(bars + 1), 1);
+    umma::mbar_init(smem_u32(bars), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
     umma::fence_mbar_init();
   }
   __syncthreads();
   uint32_t limit = kWaitLimit;
 
-  if (!second) {
+  if (role == 0) {
     if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
     load_state<NK>(hG, a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane);
     float4 *kept = reinterpret_cast<float4 *>(a.g) + (bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 32);
@@ -863,7 +915,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a, const _
       split_tokens(Z, zt);
       pair_sync(w);
       float4 *to = kept + c * step;
-#pragma unroll 1
+#pragma unroll 2
       for (int q = 0; q < NK / 2; ++q) {
         float acc[4][4], x[4][4];
         quad_product(uK, q, zt, lane, acc);
@@ -876,19 +928,40 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a, const _
   }
 
   const int ltid = tid - 32 * W;
-  const auto load = [&](int c) {
+  const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
-    load_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, bh * a.n + c, tok + c * kC, h, col0, min(len - c * kC, kC),
-                         a.dy, ld_y, a.by_dy, &maps.dy, ltid);
+    if (lane == 0)
+      request_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, bh * a.n + c, tok + c * kC, h, col0, a.by_dy, &maps.dy, w);
+    __syncwarp();
   };
-  if (n > 0) load(n - 1);
+  if (role == 2) {
+    for (int it = 0; it <= n; ++it) {
+      const int c = n - 1 - it;
+      if (it > 0) __syncthreads();
+      if (it < n) request(c);
+      if (it > 0 && len - (c + 1) * kC < kC) __syncthreads();
+    }
+    return;
+  }
+
+  const auto copy = [&](int c) {
+    copy_stage<NK, 3, W>(sm + ((n - 1 - c) & 1) * L::stage, a, tok + c * kC, h, col0, min(len - c * kC, kC), a.dy, ld_y,
+                         a.by_dy, ltid);
+  };
+  if (n > 0) {
+    if (kAskers<W> > 1) request(n - 1);
+    copy(n - 1);
+  }
   for (int c = n - 1; c >= 0; --c) {
     const int it = n - 1 - c;
     const int64_t u = bh * a.n + c;
     unsigned char *st = sm + (it & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
-    if (c > 0) load(c - 1);
+    if (c > 0) {
+      if (kAskers<W> > 1) request(c - 1);
+      copy(c - 1);
+    }
     wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
       clear_stage<NK, 3, W>(st, a, len - c * kC, a.by_dy, ltid);
@@ -933,7 +1006,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn_chain_back(const Gdn a, const _
     }
     pair_sync(w);
     const float end = gam[kC - 1];
-#pragma unroll 1
+#pragma unroll 2
     for (int q = 0; q < NK / 2; ++q) {
       float acc[4][4], x[4][4];
       quad_product(uQ, q, d3, lane, acc);
@@ -1051,8 +1124,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a, const _
     load_tile<L::P, kGradThreads>(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
   }
   load_columns(0);
-  if (tid == 0)
+  if (tid == 0) {
     for (int kt = 0; kt < min(kRing, tiles); ++kt) load_states(kt);
+    // what the chunk that is likely to follow here reads first, on its way into L2
+    const int64_t next = u + kSms;
+    if (next < static_cast<int64_t>(gridDim.x)) {
+      const uint32_t bytes = static_cast<uint32_t>(tiles) * 4096;
+      umma::prefetch_l2(a.e + next * tiles * 1024, bytes);
+      umma::prefetch_l2(a.dz + next * tiles * 1024, bytes);
+      umma::prefetch_l2(a.s + next * tiles * (NT * 128), static_cast<uint32_t>(tiles) * L::part);
+    }
+  }
   uint32_t limit = kWaitLimit;
   if (w >= tiles) rows[(2 * w + half) * kC + lane] = rows[(2 * w + half) * kC + 32 + lane] = 0.f;
   uint4 *sU = reinterpret_cast<uint4 *>(sm + L::U), *sZ = reinterpret_cast<uint4 *>(sm + L::Z);
@@ -1318,9 +1400,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a, const _
       if (t == 0) flow[w * kC + i] = qd;
     }
   __syncthreads();
-  if (tid < 32) {  // the decays' gradient: sums before each token (which cancel)
-    Wide x[2], before[2];
-    float ez[2];
+  if (tid < 32) {  // the decays' gradient: sums before each token
+    float x[2], before[2], ez[2];
     int seg[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -1332,26 +1413,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a, const _
         f += flow[e * kC + m] - rows[(2 * e + 1) * kC + m];
         ez[i] += rows[2 * e * kC + m];
       }
-      before[i] = {f, 0.f};
-      x[i] = running(before[i], lane);
+      before[i] = x[i] = f;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(kFull, x[i], o);
+        if (lane >= o) x[i] += y;
+      }
       seg[i] = __float_as_int(sg[m]);
     }
-    x[1] = shfl(x[0], 31) + x[1];
+    x[1] += __shfl_sync(kFull, x[0], 31);
     const uint32_t s0 = __ballot_sync(kFull, lane == 0 || seg[0] != __float_as_int(sg[max(lane - 1, 0)]));
     const uint32_t s1 = __ballot_sync(kFull, seg[1] != __float_as_int(sg[lane + 31]));
     before[0] = x[0] - before[0];  // sum over s < t
     before[1] = x[1] - before[1];
     const uint32_t upto = 0xffffffffu >> (31 - lane);
-    const Wide start{((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7])), 0.f};
+    const float start = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
       // the first token of this one's document
       const int first = i == 0 ? 31 - __clz(s0 & upto) : (s1 & upto) ? 63 - __clz(s1 & upto) : 31 - __clz(s0);
-      const Wide p0 = shfl(before[0], first & 31), p1 = shfl(before[1], first & 31);
+      const float p0 = __shfl_sync(kFull, before[0], first & 31), p1 = __shfl_sync(kFull, before[1], first & 31);
       if (m < live) {
-        const Wide v = (seg[i] == 0 ? start : Wide{0.f, 0.f}) - (before[i] - (first < 32 ? p0 : p1));
-        a.dla[(tok + m) * a.H + h] = v.hi;
+        a.dla[(tok + m) * a.H + h] = (seg[i] == 0 ? start : 0.f) - (before[i] - (first < 32 ? p0 : p1));
         a.dbeta[(tok + m) * a.H + h] = ez[i] / beta[m];
       }
     }
@@ -1527,7 +1611,6 @@ int launch(K kernel, const char *what, int64_t grid, int threads, int smem, cons
 // Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its
 // two warps then run on schedulers of their own), else two, else four, which share an SM's
 // tensor cores and the chunk's tiles.
-constexpr int kSms = 152;
 int chain_width(const Gdn &a, const Layout &l) {
   const int64_t all = l.tiles * a.B * a.H;
   return all <= kSms || l.tiles == 1 ? 1 : all <= 2 * kSms || l.tiles == 2 ? 2 : 4;
@@ -1536,8 +1619,8 @@ int chain_width(const Gdn &a, const Layout &l) {
 template <int NK, int W>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
-  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, 64 * W, Chain<NK, 3, W>::size, a, maps, st)
-              : launch(gdn_chain<NK, W>, "gdn_train", grid, 64 * W, Chain<NK, 2, W>::size, a, maps, st);
+  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 64 * W + 32 : 64 * W, Chain<NK, 3, W>::size, a, maps, st)
+              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 64 * W + 32 : 64 * W, Chain<NK, 2, W>::size, a, maps, st);
 }
 template <int NK>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
@@ -1552,7 +1635,7 @@ int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc != SDM_OK) return rc;
   if (l.units > 0) {
-    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, 2 * kC * NK * 32 + (2 * kC * kLd + kScal) * 4 + 16, a, maps, st);
+    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + 32 * 36 + kScal) * 4 + 16, a, maps, st);
     if (rc != SDM_OK) return rc;
   }
   return run_chain<NK>(a, maps, l, false, st);
