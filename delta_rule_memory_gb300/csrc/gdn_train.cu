@@ -54,7 +54,6 @@ using namespace mma;
 
 constexpr int kSms = 152;
 constexpr int kC = 64;                  // tokens of a chunk
-constexpr int kTile = kPanel;           // bytes of one bf16 [64][64] tile
 constexpr int kTri = 10 * 512;          // ... of a lower triangular one: its ten 16 x 16 blocks
 constexpr int kLd = kC + 4;             // fp32 rows of the solve: 16-byte aligned, 4 banks apart
 constexpr int kScal = 6 * kC;           // gam, tail, beta, l (two floats), document number
@@ -1020,399 +1019,417 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_bac
 }
 
 // ---------------------------------------------------------------------------
-// gdn_grad: the gradients of one chunk of one head.  A warp has an eighth of
-// the key channels for 32 tokens, so each element of the two states is needed by
-// two warps only: straight from memory, where the chains left it in fragment
-// order, split into bf16 parts and turned (8 x 8 at a time) into the B
-// fragments of the sums over value columns.  U and dZ are shared: split once, into A fragments
-// in shared memory (an A fragment of U holds the B fragments of U^T).
-// Value columns come 128 at a time.
+// gdn_grad: the gradients of one chunk of one head, on the tcgen05 tensor cores.
+// Transposed, every sum over value columns has the key channels or two times
+// the tokens as its M = 128 and the tokens as N:
+//   [dQ1 | dKa]^T [128 x 128] = S [dY | dZ]^T        dKb^T [128 x 64] = G (tail U)^T
+//   [X; N]        [128 x 64]  = [dY; dZ] U^T
+// and then, with X and N times their decays,
+//   dQ2^T = K^T X^T,   dKb^T += Q^T X + K^T (N^T + N),
+//   dQ = gam dQ1 + dQ2,   dK = dKb - gam dKa.
+// The value columns come 32 at a time: read as the chains left them (16 bytes a
+// lane, read ahead by a piece), split into bf16 parts and stored as the 8 x 8 cores of the
+// operands, where a warp's store is 128 bytes in a row.  All operands have their rows
+// of 8 along M or N (MN-major); X and N serve both ways as they lie.
+// A CTA needs half of an SM's shared memory, registers and tensor memory, so that one's
+// conversions run beside the other's products.
 // ---------------------------------------------------------------------------
-constexpr int kGradThreads = 512;
+constexpr int kGradThreads = 256;
 
-constexpr int kRing = 3;  // tiles of the states on their way
-
-template <int NK>
 struct Grad {
-  static constexpr int P = NK / 4;
-  static constexpr int K = 0, Q = K + P * kPanel, Y = Q + P * kPanel, V = Y + 2 * kTile, U = V + 2 * kTile,
-                       Z = U + 8 * 3 * 4 * 512, ring = Z + 8 * 2 * 4 * 512, part = 2 * NK * 512 /* one state's tile */,
-                       sc = ring + kRing * 3 * part, bars = sc + (kScal + 8 * 3 * kC + 8) * 4,
-                       size = bars + (2 * kRing + 1) * 8;
-  static constexpr int X = U, N = X + 3 * kTile;  // once the value columns are done: X in three parts, N + N^T in two
+  // a core row of 8 value columns: 16 cores where M or N is 128, 8 where it is 64
+  static constexpr int YZ = 0, Zl = YZ + 8192 /* zeros | the second part of dZ */, U = Zl + 8192, Ut = U + 3 * 4096,
+                       S = Ut + 2 * 4096, G = S + 3 * 8192, K = G + 2 * 8192, Q = K + 16384, sc = Q + 16384,
+                       rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */, flow = rows + 4 * kC * 4 /* [4][64] */,
+                       red = flow + 4 * kC * 4, bars = red + 32, size = bars + 16;
+  static constexpr int X = 0, N = X + 3 * 8192;  // once the value columns are done
+  static constexpr uint32_t dQ1 = 0, dKa = 64, dKb = 128, XN = 192, dQ2 = 192, columns = 256;  // tensor memory
 };
+static_assert(2 * (Grad::size + 1024) <= 228 * 1024, "two CTAs an SM");
 
-// lanes 4 x + t hold v[16]; the sums over x, two of them a lane (bits 3..1 of the value are the lane's bits 4..2)
-__device__ __forceinline__ void sum_rows(float (&v)[16], int lane) {
+// 64 rows of `width` bf16 as 8 x 8 cores [row / 8][column / 8], zeros from row `live` on
+__device__ __forceinline__ void load_cores(unsigned char *to, const uint16_t *src, int64_t ld, int live, int width, int by,
+                                           int tid) {
+#pragma unroll 4
+  for (int i = 0; i < kC * 16 / kGradThreads; ++i) {
+    // a warp: 8 rows, 4 pieces of 16 bytes of each
+    const int id = tid + i * kGradThreads, r = ((id >> 7) << 3) | (id & 7), p = (id >> 3) & 15, c = p * 8;
+    unsigned char *dst = to + (r >> 3) * 2048 + p * 128 + (r & 7) * 16;
+    const uint16_t *s = src + r * ld + c;
+    if (by == 16) {
+      const bool ok = r < live && c < width;
+      copy_async<16>(smem_u32(dst), ok ? s : src, ok);
+    } else if (by == 8) {
 #pragma unroll
-  for (int o = 16; o >= 4; o >>= 1) {
-    const bool up = lane & o;
+      for (int e = 0; e < 8; e += 4) {
+        const bool ok = r < live && c + e < width;
+        copy_async<8>(smem_u32(dst) + 2 * e, ok ? s + e : src, ok);
+      }
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (r < live)
 #pragma unroll
-    for (int i = 0; i < o / 2; ++i) {
-      const float send = up ? v[i] : v[i + o / 2], keep = up ? v[i + o / 2] : v[i];
-      v[i] = keep + __shfl_xor_sync(kFull, send, o);
+        for (int e = 0; e < 8; ++e)
+          if (c + e < width) w[e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
+// two neighbouring bf16 of a row, of which `left` exist
+__device__ __forceinline__ uint32_t load_pair(const uint16_t *p, int left, bool pairs) {
+  if (left <= 0) return 0;
+  if (pairs) return *reinterpret_cast<const uint32_t *>(p);
+  return p[0] | (left > 1 ? static_cast<uint32_t>(p[1]) << 16 : 0);
+}
+
+// lanes hold v[32]; the sum over the lanes of v[lane]
+__device__ __forceinline__ float sum_lanes(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(kFull, send, o);
+    }
+  }
+  return v[0];
+}
+
 template <int NK>
-__global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a, const __grid_constant__ Maps maps) {
-  using L = Grad<NK>;
-  constexpr int NT = 2 * NK, NW = NK / 4;  // NW: n-tiles of key channels a warp
+__global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
+  using L = Grad;
+  using namespace umma;
+  constexpr int NT = 2 * NK, NW = NT / 4;  // NW: 8-channel groups of the states a warp
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, w = (tid >> 5) & 7, half = tid >> 8, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, w = tid >> 5, quarter = w & 3, upper = w >> 2, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x, bh = u / a.n;
-  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
   const int live = min(length_of(a, b) - c * kC, kC);
   if (live <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.T + c * kC, ld_y = static_cast<int64_t>(a.H) * a.dv;
   const int hk = h / (a.H / a.Hk), tiles = (a.dv + 15) >> 4;
   float *sc = reinterpret_cast<float *>(sm + L::sc);
   float *gam = sc, *tail = sc + kC, *beta = sc + 2 * kC, *lh = sc + 3 * kC, *ll = sc + 4 * kC, *sg = sc + 5 * kC;
-  float *rows = sc + kScal /* [8][2][64]: dZ . E and v . dZ */, *flow = rows + 8 * 2 * kC /* [8][64] */,
-        *red = flow + 8 * kC;
-  const uint32_t uY = smem_u32(sm + L::Y), uV = smem_u32(sm + L::V);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::bars), *empty = full + kRing, *tile_bar = empty + kRing;
-  const unsigned char *gS = reinterpret_cast<const unsigned char *>(a.s) + u * tiles * L::part,
-                      *gG = reinterpret_cast<const unsigned char *>(a.g) + (bh * (a.n + 1) + c) * tiles * L::part;
-  // one thread: the states' tile kt (S, G at the chunk's start and at its end) into the ring
-  const auto load_states = [&](int kt) {
-    const uint32_t mb = smem_u32(full + kt % kRing), to = smem_u32(sm + L::ring) + (kt % kRing) * 3 * L::part;
-    umma::mbar_expect_tx(mb, 3 * L::part);
-    umma::bulk_g2s(to, gS + kt * L::part, L::part, mb);
-    umma::bulk_g2s(to + L::part, gG + kt * L::part, L::part, mb);
-    umma::bulk_g2s(to + 2 * L::part, gG + (static_cast<int64_t>(tiles) + kt) * L::part, L::part, mb);
-  };
-  // the value columns' tiles from column c0 on
-  const auto load_columns = [&](int c0) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int cx = c0 + 64 * x;
-      if (cx >= a.dv) continue;
-      if (a.by_dy != 16)
-        load_tile<1, kGradThreads>(sm + L::Y + x * kTile, a.dy + tok * ld_y + h * a.dv + cx, ld_y, live, min(64, a.dv - cx),
-                                   a.by_dy, tid);
-      else if (tid == 0)
-        tensor_panel(uY + x * kTile, &maps.dy, cx, h, static_cast<int>(tok), smem_u32(tile_bar));
-      if (a.by_v != 16)
-        load_tile<1, kGradThreads>(sm + L::V + x * kTile, a.v + tok * a.ld_v + h * a.dv + cx, a.ld_v, live,
-                                   min(64, a.dv - cx), a.by_v, tid);
-      else if (tid == 0)
-        tensor_panel(uV + x * kTile, &maps.v, cx, h, static_cast<int>(tok), smem_u32(tile_bar));
-    }
-    cp_async_commit();
-  };
-  const auto column_bytes = [&](int c0) {
-    return static_cast<uint32_t>(((a.by_dy == 16) + (a.by_v == 16)) * (c0 + 64 < a.dv ? 2 : 1) * kPanel);
-  };
-  if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      umma::mbar_init(smem_u32(full + i), 1);
-      umma::mbar_init(smem_u32(empty + i), kGradThreads / 32);
-    }
-    umma::mbar_init(smem_u32(tile_bar), 1);
-    umma::fence_mbar_init();
-    const uint32_t more = kScal * 4 + column_bytes(0);
-    if (a.by_qk == 16)
-      load_qk<NK>(maps, sm + L::K, sm + L::Q, hk, tok, smem_u32(tile_bar), more);
-    else
-      umma::mbar_expect_tx(smem_u32(tile_bar), more);
-    umma::bulk_g2s(smem_u32(sc), a.scal + u * kScal, kScal * 4, smem_u32(tile_bar));
-  }
-  if (a.by_qk != 16) {
-    load_tile<L::P, kGradThreads>(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-    load_tile<L::P, kGradThreads>(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-  }
-  load_columns(0);
-  if (tid == 0) {
-    for (int kt = 0; kt < min(kRing, tiles); ++kt) load_states(kt);
-    // what the chunk that is likely to follow here reads first, on its way into L2
-    const int64_t next = u + kSms;
-    if (next < static_cast<int64_t>(gridDim.x)) {
-      const uint32_t bytes = static_cast<uint32_t>(tiles) * 4096;
-      umma::prefetch_l2(a.e + next * tiles * 1024, bytes);
-      umma::prefetch_l2(a.dz + next * tiles * 1024, bytes);
-      umma::prefetch_l2(a.s + next * tiles * (NT * 128), static_cast<uint32_t>(tiles) * L::part);
-    }
-  }
-  uint32_t limit = kWaitLimit;
-  if (w >= tiles) rows[(2 * w + half) * kC + lane] = rows[(2 * w + half) * kC + 32 + lane] = 0.f;
-  uint4 *sU = reinterpret_cast<uint4 *>(sm + L::U), *sZ = reinterpret_cast<uint4 *>(sm + L::Z);
+  float *rows = reinterpret_cast<float *>(sm + L::rows), *flow = reinterpret_cast<float *>(sm + L::flow),
+        *red = reinterpret_cast<float *>(sm + L::red);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::bars);
+  uint32_t *holder = reinterpret_cast<uint32_t *>(bar + 1);
+  const uint32_t mb = smem_u32(bar);
 
-  // m-tiles 2 half and 2 half + 1
-  float dQ[2][NW][4], dA[2][NW][4], dK[2][NW][4], X[2][4], N[2][4];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) clear(dQ[m]), clear(dA[m]), clear(dK[m]);
-  clear(X);
-  clear(N);
-  float anchor = 0.f;
+  load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+  load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
+  cp_async_commit();
 
-  for (int c0 = 0; c0 < a.dv; c0 += 128) {
-    const int nt_cols = min(8, tiles - (c0 >> 4));  // tiles of 16 columns in this piece
-    // half a tile of E and dZ
-    float E[4][4], Z[4][4];
-    if (w < nt_cols) {
-      const int64_t at = (u * tiles + (c0 >> 4) + w) * 256 + half * 128;
+  // a piece's share of this thread, read ahead: of tile `upper` of the two, key channels 8 NW quarter .. and
+  // tokens 16 quarter .. + 15
+  float4 fs[NW], f0[NW], f1[NW];
+  float E[2][4], Z[2][4];
+  uint32_t yv[2][2], vv[2][2];  // dy and v [n-tile][columns 0..7, 8..15]: a row's pair a lane
+  const auto read = [&](int c0) {
+    const int ct = (c0 >> 4) + upper;
+    const bool on = ct < tiles;
+    const float4 *S = reinterpret_cast<const float4 *>(a.s) + ((u * tiles + ct) * NT + quarter * NW) * 32 + lane;
+    const float4 *G = reinterpret_cast<const float4 *>(a.g) + (((bh * (a.n + 1) + c) * tiles + ct) * NT + quarter * NW) * 32 + lane;
+    const float4 *G1 = G + static_cast<int64_t>(tiles) * NT * 32;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+      fs[x] = on ? S[x * 32] : zero;
+      f1[x] = on ? G1[x * 32] : zero;
+      f0[x] = on ? G[x * 32] : zero;
+    }
+    const int64_t at = ((u * tiles + ct) * 8 + 2 * quarter) * 32;
+    if (on) {
       get(reinterpret_cast<const float4 *>(a.e) + at, lane, E);
       get(reinterpret_cast<const float4 *>(a.dz) + at, lane, Z);
+    } else {
+      clear(E);
+      clear(Z);
     }
-    if (c0) {
-      __syncthreads();  // the piece before has been read
-      if (tid == 0) umma::mbar_expect_tx(smem_u32(tile_bar), column_bytes(c0));
-      load_columns(c0);
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    wait_copies(tile_bar, (c0 >> 7) & 1, limit, a);
-    if (live < kC) {
-      if (a.by_qk == 16 && c0 == 0) {
-        clear_rows<L::P, kGradThreads>(sm + L::K, live, tid);
-        clear_rows<L::P, kGradThreads>(sm + L::Q, live, tid);
-      }
-      for (int x = 0; x < 2; ++x) {
-        if (a.by_dy == 16) clear_rows<1, kGradThreads>(sm + L::Y + x * kTile, live, tid);
-        if (a.by_v == 16) clear_rows<1, kGradThreads>(sm + L::V + x * kTile, live, tid);
-      }
-      umma::fence_async_smem();
-      __syncthreads();
-    }
-    if (w < nt_cols) {
-      uint16_t *dvp = a.odv + tok * a.ld_dv + h * a.dv + c0 + 16 * w + 2 * t;
-      float sum[16];  // [dZ . E, v . dZ][n-tile][token of the pair]
 #pragma unroll
-      for (int np = 0; np < 2; ++np) {
-        uint32_t v[4], pu[3][4], pz[2][4];
-        ldsm4_t(uV + (w >> 2) * kTile +
-                    piece(32 * half + 16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), 2 * (w & 3) + ((lane >> 3) & 1)),
-                v);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int nt = 2 * np + x;
-          const float2 be = *reinterpret_cast<const float2 *>(beta + 32 * half + 8 * nt + 2 * t);
-          sum[2 * nt] = E[nt][0] * Z[nt][0] + E[nt][2] * Z[nt][2];
-          sum[2 * nt + 1] = E[nt][1] * Z[nt][1] + E[nt][3] * Z[nt][3];
-          sum[8 + 2 * nt] = low2(v[2 * x]) * Z[nt][0] + low2(v[2 * x + 1]) * Z[nt][2];
-          sum[8 + 2 * nt + 1] = high2(v[2 * x]) * Z[nt][1] + high2(v[2 * x + 1]) * Z[nt][3];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // columns 0..7 and 8..15 of the tile
-            uint32_t s3[3], s2[2];
-            split<3>(be.x * E[nt][2 * e], be.y * E[nt][2 * e + 1], s3);
-            split<2>(Z[nt][2 * e], Z[nt][2 * e + 1], s2);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) pu[p][x + 2 * e] = transpose8(s3[p]);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) pz[p][x + 2 * e] = transpose8(s2[p]);
-            // dv is dZ rounded once, which is its first part
-            const int i = 32 * half + 8 * nt + g, left = a.dv - (c0 + 16 * w + 8 * e + 2 * t);
-            if (i < live) {
-              uint16_t *o = dvp + i * a.ld_dv + 8 * e;
-              const uint32_t z = pz[0][x + 2 * e];
-              if (a.pair_y) {
-                if (left > 0) *reinterpret_cast<uint32_t *>(o) = z;
-              } else {
-                if (left > 0) o[0] = static_cast<uint16_t>(z);
-                if (left > 1) o[1] = static_cast<uint16_t>(z >> 16);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-          sU[((w * 3 + p) * 4 + 2 * half + np) * 32 + lane] = make_uint4(pu[p][0], pu[p][1], pu[p][2], pu[p][3]);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          sZ[((w * 2 + p) * 4 + 2 * half + np) * 32 + lane] = make_uint4(pz[p][0], pz[p][1], pz[p][2], pz[p][3]);
-      }
-      sum_rows(sum, lane);
-      float *to = rows + (w * 2 + (lane >> 4)) * kC + 32 * half + 8 * (2 * ((lane >> 3) & 1) + ((lane >> 2) & 1)) + 2 * t;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) to[i] = c0 ? to[i] + sum[i] : sum[i];
-    }
-    __syncthreads();
-
-#pragma unroll 1
-    for (int kt = 0; kt < nt_cols; ++kt) {
-      const int at = (c0 >> 4) + kt, slot = at % kRing;
-      const uint32_t parity = (at / kRing) & 1;
-      if (tid == 0 && at > 0 && at + kRing - 1 < tiles) {  // the slot of the tile before, once everyone has it
-        wait_copies(empty + (at - 1) % kRing, ((at - 1) / kRing) & 1, limit, a);
-        load_states(at + kRing - 1);
-      }
-      __syncwarp();
-      wait_copies(full + slot, parity, limit, a);
-      float4 fs[NW], f0[NW], f1[NW];
-      const float4 *from = reinterpret_cast<const float4 *>(sm + L::ring + slot * 3 * L::part) + w * NW * 32 + lane;
-#pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        fs[x] = from[x * 32], f1[x] = from[2 * NT * 32 + x * 32];
-        if (half == 0) f0[x] = from[NT * 32 + x * 32];
-      }
-      __syncwarp();
-      if (lane == 0) umma::mbar_arrive(smem_u32(empty + slot));
-      uint32_t bs[NW][3][2], bg[NW][2][2];
-#pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        if (half == 0) anchor += (fs[x].x * f0[x].x + fs[x].y * f0[x].y) + (fs[x].z * f0[x].z + fs[x].w * f0[x].w);
-        uint32_t p0[3], p1[3], q0[2], q1[2];
-        split<3>(fs[x].x, fs[x].y, p0);
-        split<3>(fs[x].z, fs[x].w, p1);
-        split<2>(f1[x].x, f1[x].y, q0);
-        split<2>(f1[x].z, f1[x].w, q1);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) bs[x][p][0] = transpose8(p0[p]), bs[x][p][1] = transpose8(p1[p]);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) bg[x][p][0] = transpose8(q0[p]), bg[x][p][1] = transpose8(q1[p]);
-      }
-      uint32_t bu[3][2];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const uint4 v = sU[((kt * 3 + p) * 4 + (w >> 1)) * 32 + lane];
-        bu[p][0] = w & 1 ? v.y : v.x;
-        bu[p][1] = w & 1 ? v.w : v.z;
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int mt = 2 * half + m;
-        uint32_t y[4], uu[2][4], z[2][4];
-        a_rows(uY + (kt >> 2) * kTile, 16 * mt, 16 * (kt & 3), lane, y);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint4 vu = sU[((kt * 3 + p) * 4 + mt) * 32 + lane], vz = sZ[((kt * 2 + p) * 4 + mt) * 32 + lane];
-          uu[p][0] = vu.x, uu[p][1] = vu.y, uu[p][2] = vu.z, uu[p][3] = vu.w;
-          z[p][0] = vz.x, z[p][1] = vz.y, z[p][2] = vz.z, z[p][3] = vz.w;
-        }
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-          for (int x = 0; x < NW; ++x) {
-            fma16816(dQ[m][x], y, bs[x][p][0], bs[x][p][1]);
-            // parts 0 0, 0 1 and 1 0
-            fma16816(dA[m][x], z[p >> 1], bs[x][p & 1][0], bs[x][p & 1][1]);
-            fma16816(dK[m][x], uu[p >> 1], bg[x][p & 1][0], bg[x][p & 1][1]);
-          }
-        if (mt >= (w >> 1))
-#pragma unroll
-          for (int p = 0; p < 3; ++p) {
-            fma16816(X[m], y, bu[p][0], bu[p][1]);
-            fma16816(N[m], z[p >> 1], bu[p & 1][0], bu[p & 1][1]);
-          }
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) anchor += __shfl_xor_sync(kFull, anchor, o);
-  if (lane == 0 && half == 0) red[w] = anchor;
-  __syncthreads();  // U has been read
-
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int mt = 2 * half + m;
-#pragma unroll
-    for (int x = 0; x < NW; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * mt + g + 8 * (e >> 1);
-        dQ[m][x][e] *= gam[i];
-        dK[m][x][e] = tail[i] * dK[m][x][e] - gam[i] * dA[m][x][e];
-      }
-    if (mt < (w >> 1)) continue;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = 16 * mt + g + 8 * r, j = 8 * w + 2 * t;
-      float xv[2], nv[2];
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bool on = j + e <= i && __float_as_int(sg[i]) == __float_as_int(sg[j + e]);
-        const float d = on ? umma::ex2_approx((lh[i] - lh[j + e]) + (ll[i] - ll[j + e])) : 0.f;
-        xv[e] = on ? d * X[m][2 * r + e] : 0.f;
-        nv[e] = on && j + e < i ? -d * N[m][2 * r + e] : 0.f;
+        const int i = 16 * quarter + 8 * x + g, cc = 16 * ct + 8 * e + 2 * t, left = i < live ? a.dv - cc : 0;
+        yv[x][e] = load_pair(a.dy + (tok + i) * ld_y + h * a.dv + cc, left, a.by_dy >= 4);
+        vv[x][e] = load_pair(a.v + (tok + i) * a.ld_v + h * a.dv + cc, left, a.by_v >= 4);
       }
-      uint32_t sx[3], sn[2];
-      split<3>(xv[0], xv[1], sx);
-      split<2>(nv[0], nv[1], sn);
-      const uint32_t off = piece(i, w) + 4 * t;
-#pragma unroll
-      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t *>(sm + L::X + p * kTile + off) = sx[p];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {  // N below the diagonal, N^T above it
-        unsigned char *tile = sm + L::N + p * kTile;
-        const uint16_t lo = static_cast<uint16_t>(sn[p]), hi = static_cast<uint16_t>(sn[p] >> 16);
-        if (j <= i) {
-          *reinterpret_cast<uint16_t *>(tile + off) = lo;
-          *reinterpret_cast<uint16_t *>(tile + piece(j, i >> 3) + 2 * (i & 7)) = lo;
-        }
-        if (j + 1 <= i) {
-          *reinterpret_cast<uint16_t *>(tile + off + 2) = hi;
-          *reinterpret_cast<uint16_t *>(tile + piece(j + 1, i >> 3) + 2 * (i & 7)) = hi;
-        }
-      }
-    }
+  };
+  read(0);
+
+  if (tid == 0) {
+    mbar_init(mb, 1);
+    fence_mbar_init();
   }
+  if (w == 0) tmem_alloc(smem_u32(holder), L::columns);
+  // the half of zeros beside dZ's second part
+  {
+    const int i = tid >> 6, o = tid & 63;
+    *reinterpret_cast<uint4 *>(sm + L::Zl + i * 2048 + o * 16) = make_uint4(0, 0, 0, 0);
+  }
+  cp_async_wait<0>();
+  tc_fence_before();
   __syncthreads();
-  const uint32_t uK = smem_u32(sm + L::K), uQ = smem_u32(sm + L::Q), uX = smem_u32(sm + L::X), uN = smem_u32(sm + L::N);
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  bool ok = true;
+  uint32_t phase = 0;
+  // every thread waits for the products asked for; then the CTA agrees
+  const auto products_done = [&]() {
+    ok = mbar_wait(mb, phase & 1, kWaitLimit);
+    ++phase;
+    tc_fence_before();
+    ok = __syncthreads_and(ok) != 0;
+    tc_fence_after();
+    return ok;
+  };
+  const uint32_t base = smem_u32(sm);
+  // A and B with rows of 8 along M and N; N = 64 and 128
+  const uint32_t id64 = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16), id128 = idesc_bf16_f32(128, 128) | (1u << 15) | (1u << 16);
+
+  float anchor = 0.f, ez[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, vz[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+  for (int c0 = 0; c0 < a.dv; c0 += 32) {
+    if (c0 && !products_done()) break;  // the piece before has been read
+    // ---- the states
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    uint32_t bk[4], bq[4];  // of 16 key channels: this warp's, or with another's beside them
-    constexpr int share = 2 / NW;
-    b_cols(uK, 16 * (w / share), 16 * ks, lane, bk);
-    b_cols(uQ, 16 * (w / share), 16 * ks, lane, bq);
-    if (NW == 1 && (w & 1)) bk[0] = bk[2], bk[1] = bk[3], bq[0] = bq[2], bq[1] = bq[3];
+    for (int x = 0; x < NW; ++x) {
+      anchor += (fs[x].x * f0[x].x + fs[x].y * f0[x].y) + (fs[x].z * f0[x].z + fs[x].w * f0[x].w);
+      uint32_t p0[3], p1[3], q0[2], q1[2];
+      split<3>(fs[x].x, fs[x].y, p0);
+      split<3>(fs[x].z, fs[x].w, p1);
+      split<2>(f1[x].x, f1[x].y, q0);
+      split<2>(f1[x].z, f1[x].w, q1);
+      unsigned char *o = sm + upper * 4096 + (quarter * NW + x) * 128 + lane * 4;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int mt = 2 * half + m;
-      uint32_t f[4];
+      for (int p = 0; p < 3; ++p) {
+        *reinterpret_cast<uint32_t *>(o + L::S + p * 8192) = p0[p];
+        *reinterpret_cast<uint32_t *>(o + L::S + p * 8192 + 2048) = p1[p];
+      }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        a_rows(uN + p * kTile, 16 * mt, 16 * ks, lane, f);
-#pragma unroll
-        for (int x = 0; x < NW; ++x) fma16816(dK[m][x], f, bk[2 * x], bk[2 * x + 1]);
+        *reinterpret_cast<uint32_t *>(o + L::G + p * 8192) = q0[p];
+        *reinterpret_cast<uint32_t *>(o + L::G + p * 8192 + 2048) = q1[p];
       }
-      if (ks <= mt)
+    }
+    // ---- U, tail U, dZ, dy; dv; the sums over value columns
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          a_rows(uX + p * kTile, 16 * mt, 16 * ks, lane, f);
+    for (int x = 0; x < 2; ++x) {
+      const int nt = 2 * quarter + x;
+      const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t), tl = *reinterpret_cast<const float2 *>(tail + 8 * nt + 2 * t);
 #pragma unroll
-          for (int x = 0; x < NW; ++x) fma16816(dQ[m][x], f, bk[2 * x], bk[2 * x + 1]);
+      for (int e = 0; e < 2; ++e) {  // columns 0..7 and 8..15 of the tile
+        const float e0 = E[x][2 * e], e1 = E[x][2 * e + 1], z0 = Z[x][2 * e], z1 = Z[x][2 * e + 1], u0 = be.x * e0, u1 = be.y * e1;
+        uint32_t su[3], st[2], sz[2];
+        split<3>(u0, u1, su);
+        split<2>(tl.x * u0, tl.y * u1, st);
+        split<2>(z0, z1, sz);
+        const uint32_t y = transpose8(yv[x][e]), v = transpose8(vv[x][e]);
+        ez[x][0] = fmaf(e0, z0, ez[x][0]);
+        ez[x][1] = fmaf(e1, z1, ez[x][1]);
+        vz[x][0] = fmaf(low2(v), z0, vz[x][0]);
+        vz[x][1] = fmaf(high2(v), z1, vz[x][1]);
+        const int row = 2 * upper + e;  // of the piece's four core rows
+        unsigned char *o = sm + nt * 128 + lane * 4;
+        *reinterpret_cast<uint32_t *>(o + L::YZ + row * 2048) = y;
+        *reinterpret_cast<uint32_t *>(o + L::YZ + row * 2048 + 1024) = sz[0];
+        *reinterpret_cast<uint32_t *>(o + L::Zl + row * 2048 + 1024) = sz[1];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t *>(o + L::U + p * 4096 + row * 1024) = su[p];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) *reinterpret_cast<uint32_t *>(o + L::Ut + p * 4096 + row * 1024) = st[p];
+        // dv is dZ rounded once, which is its first part
+        const uint32_t z = transpose8(sz[0]);
+        const int i = 8 * nt + g, cc = c0 + 16 * upper + 8 * e + 2 * t;
+        if (i < live) {
+          uint16_t *to = a.odv + (tok + i) * a.ld_dv + h * a.dv + cc;
+          if (a.pair_y) {
+            if (cc < a.dv) *reinterpret_cast<uint32_t *>(to) = z;
+          } else {
+            if (cc < a.dv) to[0] = static_cast<uint16_t>(z);
+            if (cc + 1 < a.dv) to[1] = static_cast<uint16_t>(z >> 16);
+          }
         }
-      if (ks >= mt)
+      }
+    }
+    if (c0 + 32 < a.dv) read(c0 + 32);
+    fence_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      const bool more = c0 > 0;
+      const uint64_t yz = smem_desc(base + L::YZ, 2048, 128), zl = smem_desc(base + L::Zl, 2048, 128),
+                     zln = smem_desc(base + L::Zl + 1024, 2048, 128);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          a_cols(uX + p * kTile, 16 * mt, 16 * ks, lane, f);
-#pragma unroll
-          for (int x = 0; x < NW; ++x) fma16816(dK[m][x], f, bq[2 * x], bq[2 * x + 1]);
-        }
+      for (int ks = 0; ks < 2; ++ks) {
+        const bool acc = more || ks > 0;
+        const uint64_t s0 = smem_desc(base + L::S + ks * 4096, 2048, 128), s1 = s0 + 512, s2 = s0 + 1024;
+        const uint64_t g0 = smem_desc(base + L::G + ks * 4096, 2048, 128), g1 = g0 + 512;
+        const uint64_t u0 = smem_desc(base + L::U + ks * 2048, 1024, 128), u1 = u0 + 256, u2 = u0 + 512;
+        const uint64_t t0 = smem_desc(base + L::Ut + ks * 2048, 1024, 128), t1 = t0 + 256;
+        const uint64_t b = yz + 256 * ks, bl = zl + 256 * ks, bz = zln + 256 * ks;
+        mma_bf16(tmem + L::dQ1, s0, b, id128, acc);
+        mma_bf16(tmem + L::dQ1, s1, b, id128, true);
+        mma_bf16(tmem + L::dQ1, s2, b, id64, true);
+        mma_bf16(tmem + L::dKa, s0, bz, id64, true);
+        mma_bf16(tmem + L::dKb, g0, t0, id64, acc);
+        mma_bf16(tmem + L::dKb, g0, t1, id64, true);
+        mma_bf16(tmem + L::dKb, g1, t0, id64, true);
+        mma_bf16(tmem + L::XN, b, u0, id64, acc);
+        mma_bf16(tmem + L::XN, b, u1, id64, true);
+        mma_bf16(tmem + L::XN, b, u2, id64, true);
+        mma_bf16(tmem + L::XN, bl, u0, id64, true);
+      }
+      mma_commit(mb);
     }
   }
-  // q . dq
+  // sums over the columns of 16 tokens, and over the state
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = 32 * half + 16 * m + g + 8 * r;
-      float qd = 0.f;
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        const uint32_t v = *reinterpret_cast<const uint32_t *>(sm + L::Q + piece(i, w * NW + x) + 4 * t);
-        qd += low2(v) * dQ[m][x][2 * r] + high2(v) * dQ[m][x][2 * r + 1];
+      for (int o = 4; o < 32; o <<= 1) {
+        ez[x][e] += __shfl_xor_sync(kFull, ez[x][e], o);
+        vz[x][e] += __shfl_xor_sync(kFull, vz[x][e], o);
       }
-      qd += __shfl_xor_sync(kFull, qd, 1);
-      qd += __shfl_xor_sync(kFull, qd, 2);
-      if (t == 0) flow[w * kC + i] = qd;
+      if (g == 0) {
+        const int i = 16 * quarter + 8 * x + 2 * t + e;
+        rows[(2 * upper) * kC + i] = ez[x][e];
+        rows[(2 * upper + 1) * kC + i] = vz[x][e];
+      }
     }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) anchor += __shfl_xor_sync(kFull, anchor, o);
+  if (lane == 0) red[w] = anchor;
+
+  if (ok && products_done()) {
+    // ---- X (lanes 0..63) and N (64..127) times their decays: row i, columns 32 upper ..
+    {
+      const bool is_n = quarter >= 2;
+      const int i = 32 * (quarter & 1) + lane;
+      const float li = lh[i], lli = ll[i];
+      const int si = __float_as_int(sg[i]);
+      unsigned char *to = sm + (i >> 3) * 1024 + (i & 7) * 16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int j0 = 32 * upper + 16 * half;
+        float x[16];
+        tmem_ld16(lanes + L::XN + j0, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + e;
+          const bool on = (is_n ? j < i : j <= i) && si == __float_as_int(sg[j]);
+          const float d = umma::ex2_approx((li - lh[j]) + (lli - ll[j]));
+          x[e] = on ? (is_n ? -d : d) * x[e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          uint32_t s[4][3];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) split<3>(x[e + 2 * p], x[e + 2 * p + 1], s[p]);
+          unsigned char *o = to + ((j0 + e) >> 3) * 128;
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            if (!(is_n && p == 2))
+              *reinterpret_cast<uint4 *>(o + (is_n ? L::N : L::X) + p * 8192) = make_uint4(s[0][p], s[1][p], s[2][p], s[3][p]);
+        }
+      }
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) {
+      const uint32_t idk = idesc_bf16_f32(128, 64) | (1u << 15);  // B with rows of 8 along its sum
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128), q = smem_desc(base + L::Q + ks * 4096, 2048, 128);
+        const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024), xc = smem_desc(base + L::X + ks * 2048, 1024, 128);
+        const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024), nc = smem_desc(base + L::N + ks * 2048, 1024, 128);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) mma_bf16(tmem + L::dQ2, k, xr + 512 * p, idk, ks > 0 || p > 0);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          mma_bf16(tmem + L::dKb, q, xc + 512 * p, id64, true);
+          mma_bf16(tmem + L::dKb, k, nr + 512 * p, idk, true);
+          mma_bf16(tmem + L::dKb, k, nc + 512 * p, id64, true);
+        }
+      }
+      mma_commit(mb);
+    }
+    if (products_done()) {
+      // ---- channel 32 quarter + lane, tokens 32 upper ..
+      const int ch = 32 * quarter + lane, i0 = 32 * upper;
+      const bool there = ch < a.dk;
+      float q[32];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[16], y[16];
+        tmem_ld16(lanes + L::dQ1 + i0 + 16 * half, x);
+        tmem_ld16(lanes + L::dQ2 + i0 + 16 * half, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int i = i0 + 16 * half + e;
+          const float v = fmaf(gam[i], x[e], y[e]);
+          if (there && i < live) {
+            if (a.pdq)
+              a.pdq[((tok + i) * a.H + h) * a.dk + ch] = v;
+            else
+              a.odq[(tok + i) * a.ld_dq + h * a.dk + ch] = static_cast<uint16_t>(pack2(v, 0.f));
+          }
+          q[16 * half + e] =
+              there ? v * bf16_to_f32(*reinterpret_cast<const uint16_t *>(sm + L::Q + (i >> 3) * 2048 + (ch >> 3) * 128 + (i & 7) * 16 + (ch & 7) * 2))
+                    : 0.f;
+        }
+      }
+      flow[quarter * kC + i0 + lane] = sum_lanes(q, lane);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[16], y[16];
+        tmem_ld16(lanes + L::dKb + i0 + 16 * half, x);
+        tmem_ld16(lanes + L::dKa + i0 + 16 * half, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int i = i0 + 16 * half + e;
+          const float v = fmaf(-gam[i], y[e], x[e]);
+          if (there && i < live) {
+            if (a.pdk)
+              a.pdk[((tok + i) * a.H + h) * a.dk + ch] = v;
+            else
+              a.odk[(tok + i) * a.ld_dk + h * a.dk + ch] = static_cast<uint16_t>(pack2(v, 0.f));
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
   __syncthreads();
-  if (tid < 32) {  // the decays' gradient: sums before each token
-    float x[2], before[2], ez[2];
+  tc_fence_after();
+  if (!ok) {  // a wait gave up: let the products asked for end (bounded), and report
+    if (tid == 0) {
+      mma_commit(mb);
+      report_timeout(a.err);
+    }
+    mbar_wait(mb, phase & 1, kWaitLimit);
+    __syncthreads();
+  }
+  if (w == 1) tmem_dealloc(tmem, L::columns);
+  if (w == 0) {  // the decays' gradient: sums before each token
+    float x[2], before[2], e2[2];
     int seg[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
-      float f = 0.f;
-      ez[i] = 0.f;
+      float f = -(rows[kC + m] + rows[3 * kC + m]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f += flow[e * kC + m] - rows[(2 * e + 1) * kC + m];
-        ez[i] += rows[2 * e * kC + m];
-      }
+      for (int e = 0; e < 4; ++e) f += flow[e * kC + m];
+      e2[i] = rows[m] + rows[2 * kC + m];
       before[i] = x[i] = f;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1436,47 +1453,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_grad(const Gdn a, const _
       const float p0 = __shfl_sync(kFull, before[0], first & 31), p1 = __shfl_sync(kFull, before[1], first & 31);
       if (m < live) {
         a.dla[(tok + m) * a.H + h] = (seg[i] == 0 ? start : 0.f) - (before[i] - (first < 32 ? p0 : p1));
-        a.dbeta[(tok + m) * a.H + h] = ez[i] / beta[m];
+        a.dbeta[(tok + m) * a.H + h] = e2[i] / beta[m];
       }
     }
   }
-  // dq and dk
-  const int64_t to_q = a.pdq ? static_cast<int64_t>(a.H) * a.dk : a.ld_dq, to_k = a.pdq ? to_q : a.ld_dk;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = 32 * half + 16 * m + g + 8 * r;
-      if (i >= live) continue;
-      const int64_t oq = (tok + i) * to_q + h * a.dk, ok = (tok + i) * to_k + h * a.dk;
-#pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        const int cc = 8 * (w * NW + x) + 2 * t;
-        if (cc >= a.dk) continue;
-        const float q0 = dQ[m][x][2 * r], q1 = dQ[m][x][2 * r + 1], k0 = dK[m][x][2 * r], k1 = dK[m][x][2 * r + 1];
-        if (a.pdq) {
-          a.pdq[oq + cc] = q0;
-          a.pdk[ok + cc] = k0;
-          if (cc + 1 < a.dk) {
-            a.pdq[oq + cc + 1] = q1;
-            a.pdk[ok + cc + 1] = k1;
-          }
-        } else {
-          const uint32_t vq = pack2(q0, q1), vk = pack2(k0, k1);
-          if (a.pair_qk) {
-            *reinterpret_cast<uint32_t *>(a.odq + oq + cc) = vq;
-            *reinterpret_cast<uint32_t *>(a.odk + ok + cc) = vk;
-          } else {
-            a.odq[oq + cc] = static_cast<uint16_t>(vq);
-            a.odk[ok + cc] = static_cast<uint16_t>(vk);
-            if (cc + 1 < a.dk) {
-              a.odq[oq + cc + 1] = static_cast<uint16_t>(vq >> 16);
-              a.odk[ok + cc + 1] = static_cast<uint16_t>(vk >> 16);
-            }
-          }
-        }
-      }
-    }
 }
 
 // dq and dk of key heads that several value heads share, heads in order
@@ -1647,7 +1627,10 @@ int run_backward(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc == SDM_OK) rc = run_chain<NK>(a, maps, l, true, st);
   if (rc != SDM_OK || l.units == 0) return rc;
-  rc = launch(gdn_grad<NK>, "gdn_backward", l.units, kGradThreads, Grad<NK>::size, a, maps, st);
+  const cudaError_t e = cudaFuncSetAttribute(gdn_grad<NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad::size);
+  if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "gdn_backward: %s", cudaGetErrorString(e));
+  gdn_grad<NK><<<static_cast<unsigned>(l.units), kGradThreads, Grad::size, st>>>(a);
+  rc = check_launch("gdn_backward");
   if (rc != SDM_OK || !a.pdq) return rc;
   gdn_grad_heads<<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T), 256, 0, st>>>(a);
   return check_launch("gdn_backward");
