@@ -1083,10 +1083,10 @@ __device__ __forceinline__ uint32_t load_pair(const uint16_t *p, int left, bool 
   return p[0] | (left > 1 ? static_cast<uint32_t>(p[1]) << 16 : 0);
 }
 
-// lanes hold v[32]; the sum over the lanes of v[lane]
-__device__ __forceinline__ float sum_lanes(float (&v)[32], int lane) {
+// lanes hold v[16]; the sum over the lanes of v[lane % 16]
+__device__ __forceinline__ float sum_lanes(float (&v)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
+  for (int o = 8; o >= 1; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -1094,7 +1094,7 @@ __device__ __forceinline__ float sum_lanes(float (&v)[32], int lane) {
       v[i] = keep + __shfl_xor_sync(kFull, send, o);
     }
   }
-  return v[0];
+  return v[0] + __shfl_xor_sync(kFull, v[0], 16);
 }
 
 template <int NK>
@@ -1313,7 +1313,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       const float li = lh[i], lli = ll[i];
       const int si = __float_as_int(sg[i]);
       unsigned char *to = sm + (i >> 3) * 1024 + (i & 7) * 16;
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int j0 = 32 * upper + 16 * half;
         float x[16];
@@ -1363,47 +1363,50 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     }
     if (products_done()) {
       // ---- channel 32 quarter + lane, tokens 32 upper ..
-      const int ch = 32 * quarter + lane, i0 = 32 * upper;
+      const int ch = 32 * quarter + lane;
       const bool there = ch < a.dk;
-      float q[32];
-#pragma unroll
+      const unsigned char *sq = sm + L::Q + (ch >> 3) * 128 + (ch & 7) * 2;
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
+        const int i0 = 32 * upper + 16 * half, n = there ? live - i0 : 0;
+        const float *gi = gam + i0;
         float x[16], y[16];
-        tmem_ld16(lanes + L::dQ1 + i0 + 16 * half, x);
-        tmem_ld16(lanes + L::dQ2 + i0 + 16 * half, y);
+        tmem_ld16(lanes + L::dQ1 + i0, x);
+        tmem_ld16(lanes + L::dQ2 + i0, y);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int i = i0 + 16 * half + e;
-          const float v = fmaf(gam[i], x[e], y[e]);
-          if (there && i < live) {
-            if (a.pdq)
-              a.pdq[((tok + i) * a.H + h) * a.dk + ch] = v;
-            else
-              a.odq[(tok + i) * a.ld_dq + h * a.dk + ch] = static_cast<uint16_t>(pack2(v, 0.f));
-          }
-          q[16 * half + e] =
-              there ? v * bf16_to_f32(*reinterpret_cast<const uint16_t *>(sm + L::Q + (i >> 3) * 2048 + (ch >> 3) * 128 + (i & 7) * 16 + (ch & 7) * 2))
-                    : 0.f;
+        for (int e = 0; e < 16; ++e) x[e] = fmaf(gi[e], x[e], y[e]);
+        if (a.pdq) {
+          float *o = a.pdq + ((tok + i0) * a.H + h) * a.dk + ch;
+#pragma unroll
+          for (int e = 0; e < 16; ++e, o += a.H * a.dk)
+            if (e < n) *o = x[e];
+        } else {
+          uint16_t *o = a.odq + (tok + i0) * a.ld_dq + h * a.dk + ch;
+#pragma unroll
+          for (int e = 0; e < 16; ++e, o += a.ld_dq)
+            if (e < n) *o = static_cast<uint16_t>(pack2(x[e], 0.f));
         }
-      }
-      flow[quarter * kC + i0 + lane] = sum_lanes(q, lane);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[16], y[16];
-        tmem_ld16(lanes + L::dKb + i0 + 16 * half, x);
-        tmem_ld16(lanes + L::dKa + i0 + 16 * half, y);
+        for (int e = 0; e < 16; ++e)
+          x[e] = there ? x[e] * bf16_to_f32(*reinterpret_cast<const uint16_t *>(sq + ((i0 + e) >> 3) * 2048 + (e & 7) * 16)) : 0.f;
+        const float f = sum_lanes(x, lane);
+        if (lane < 16) flow[quarter * kC + i0 + lane] = f;
+        tmem_ld16(lanes + L::dKb + i0, x);
+        tmem_ld16(lanes + L::dKa + i0, y);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int i = i0 + 16 * half + e;
-          const float v = fmaf(-gam[i], y[e], x[e]);
-          if (there && i < live) {
-            if (a.pdk)
-              a.pdk[((tok + i) * a.H + h) * a.dk + ch] = v;
-            else
-              a.odk[(tok + i) * a.ld_dk + h * a.dk + ch] = static_cast<uint16_t>(pack2(v, 0.f));
-          }
+        for (int e = 0; e < 16; ++e) x[e] = fmaf(-gi[e], y[e], x[e]);
+        if (a.pdk) {
+          float *o = a.pdk + ((tok + i0) * a.H + h) * a.dk + ch;
+#pragma unroll
+          for (int e = 0; e < 16; ++e, o += a.H * a.dk)
+            if (e < n) *o = x[e];
+        } else {
+          uint16_t *o = a.odk + (tok + i0) * a.ld_dk + h * a.dk + ch;
+#pragma unroll
+          for (int e = 0; e < 16; ++e, o += a.ld_dk)
+            if (e < n) *o = static_cast<uint16_t>(pack2(x[e], 0.f));
         }
       }
     }

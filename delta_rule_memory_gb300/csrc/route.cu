@@ -25,8 +25,9 @@ namespace {
 // 32 at a time: lanes of one partition find one another with match_any, their
 // order being the visits' own.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kBlock = 4096, kRun = kBlock / kSortWarps;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRun = 128, kBlock = kSortWarps * kRun;
 constexpr int kMaxParts = 1024;
+constexpr int kSumHere = 8192;  // counts (blocks x N) up to which each block sums those before it by itself
 
 struct SortArgs {
   const int32_t *sel;
@@ -35,26 +36,38 @@ struct SortArgs {
   int32_t *order, *place, *offsets;
   int32_t *counts;  // [blocks][N]: visits of a block to a partition; then those of the blocks before it
   int32_t *err;
+  int sum_here;
 };
 
-// the partition of visit i: N where it is dropped
-__device__ __forceinline__ int part_of(const SortArgs &a, int64_t i) {
-  const int p = i < a.visits ? a.sel[i] : -1;
-  if (p >= a.N && a.err) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-  return p >= 0 && p < a.N ? p : a.N;
+// the partitions of a warp's run of visits, N where there is none
+struct Run {
+  int p[kRun / 32];
+};
+__device__ __forceinline__ Run read_run(const SortArgs &a, int64_t first) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Run r;
+#pragma unroll
+  for (int o = 0; o < kRun / 32; ++o) {
+    const int64_t i = first + w * kRun + 32 * o + lane;
+    r.p[o] = i < a.visits ? a.sel[i] : -1;
+  }
+#pragma unroll
+  for (int o = 0; o < kRun / 32; ++o) {
+    if (r.p[o] >= a.N && a.err) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
+    if (r.p[o] < 0 || r.p[o] > a.N) r.p[o] = a.N;
+  }
+  return r;
 }
 
 // hist[warp][N]: each warp's visits to each partition
-__device__ __forceinline__ void count_visits(const SortArgs &a, int64_t first, int *hist) {
+__device__ __forceinline__ void count_visits(const SortArgs &a, const Run &r, int *hist) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kSortWarps * a.N; i += kSortThreads) hist[i] = 0;
   __syncthreads();
-  for (int o = 0; o < kRun; o += 32) {
-    const int64_t i = first + w * kRun + o + lane;
-    if (first + w * kRun + o >= a.visits) break;
-    const int p = part_of(a, i);
-    const uint32_t peers = __match_any_sync(kFull, p);
-    if (p < a.N && (peers & ((1u << lane) - 1)) == 0) hist[w * a.N + p] += __popc(peers);
+#pragma unroll
+  for (int o = 0; o < kRun / 32; ++o) {
+    const uint32_t peers = __match_any_sync(kFull, r.p[o]);
+    if (r.p[o] < a.N && (peers & ((1u << lane) - 1)) == 0) hist[w * a.N + r.p[o]] += __popc(peers);
     __syncwarp();
   }
   __syncthreads();
@@ -62,7 +75,7 @@ __device__ __forceinline__ void count_visits(const SortArgs &a, int64_t first, i
 
 __global__ void __launch_bounds__(kSortThreads) route_count(const SortArgs a) {
   extern __shared__ int hist[];
-  count_visits(a, static_cast<int64_t>(blockIdx.x) * kBlock, hist);
+  count_visits(a, read_run(a, static_cast<int64_t>(blockIdx.x) * kBlock), hist);
   for (int p = threadIdx.x; p < a.N; p += kSortThreads) {
     int n = 0;
     for (int w = 0; w < kSortWarps; ++w) n += hist[w * a.N + p];
@@ -89,14 +102,15 @@ __global__ void __launch_bounds__(32) route_scan(const SortArgs a) {
   if (lane == 0) a.counts[static_cast<int64_t>(a.blocks) * a.N + p] = before;
 }
 
-// places.  One block alone counts for itself (a.blocks == 1: a.counts unused)
+// places.  One block alone counts for itself; with few counts in all a block sums those of the blocks before it
 __global__ void __launch_bounds__(kSortThreads) route_place(const SortArgs a) {
   extern __shared__ int hist[];
-  int *start = hist + kSortWarps * a.N;  // [N + 1]
+  int *start = hist + kSortWarps * a.N, *ahead = start + a.N + 1;  // [N + 1], [N]
   __shared__ int sums[kSortWarps];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kBlock;
-  count_visits(a, first, hist);
+  const Run run = read_run(a, first);
+  count_visits(a, run, hist);
   // a partition's visits in the warps before, and its total
   for (int p = threadIdx.x; p < a.N; p += kSortThreads) {
     int n = 0;
@@ -105,7 +119,21 @@ __global__ void __launch_bounds__(kSortThreads) route_place(const SortArgs a) {
       hist[i * a.N + p] = n;
       n += x;
     }
-    start[p] = a.blocks == 1 ? n : a.counts[static_cast<int64_t>(a.blocks) * a.N + p];
+    int before = 0;
+    if (a.blocks > 1 && a.sum_here) {
+      n = 0;
+#pragma unroll 8
+      for (int b = 0; b < a.blocks; ++b) {
+        const int x = a.counts[b * a.N + p];
+        n += x;
+        before += b < static_cast<int>(blockIdx.x) ? x : 0;
+      }
+    } else if (a.blocks > 1) {
+      n = a.counts[static_cast<int64_t>(a.blocks) * a.N + p];
+      before = a.counts[static_cast<int64_t>(blockIdx.x) * a.N + p];
+    }
+    start[p] = n;
+    ahead[p] = before;
   }
   __syncthreads();
   // totals to starts: kMaxParts / kSortThreads partitions a thread
@@ -141,13 +169,13 @@ __global__ void __launch_bounds__(kSortThreads) route_place(const SortArgs a) {
     for (int p = threadIdx.x; p <= a.N; p += kSortThreads) a.offsets[p] = start[p];
   for (int i = threadIdx.x; i < kSortWarps * a.N; i += kSortThreads) {
     const int p = i % a.N;
-    hist[i] += start[p] + (a.blocks == 1 ? 0 : a.counts[static_cast<int64_t>(blockIdx.x) * a.N + p]);
+    hist[i] += start[p] + ahead[p];
   }
   __syncthreads();
-  for (int o = 0; o < kRun; o += 32) {
-    const int64_t i = first + w * kRun + o + lane;
-    if (first + w * kRun + o >= a.visits) break;
-    const int p = part_of(a, i);
+#pragma unroll
+  for (int o = 0; o < kRun / 32; ++o) {
+    const int64_t i = first + w * kRun + 32 * o + lane;
+    const int p = run.p[o];
     const uint32_t peers = __match_any_sync(kFull, p), below = peers & ((1u << lane) - 1);
     int at = -1;
     if (p < a.N) at = hist[w * a.N + p] + __popc(below);
@@ -239,80 +267,94 @@ __device__ __forceinline__ void clear_rest(const RowArgs &a, int pieces, int64_t
   }
 }
 
+// an item: a token and a stretch of 32 U pieces of its row
+struct Items {
+  int64_t first, step, all;
+  int each;  // stretches of a row
+};
+template <int U>
+__device__ __forceinline__ Items items_of(const RowArgs &a, int pieces) {
+  Items t;
+  t.each = (pieces + 32 * U - 1) / (32 * U);
+  t.first = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  t.step = static_cast<int64_t>(gridDim.x) * kRowWarps;
+  t.all = a.M * t.each;
+  return t;
+}
+
 template <int BYTES, int ES>
 __global__ void __launch_bounds__(kRowThreads) route_gather_kernel(const RowArgs a) {
   using R = typename Raw<BYTES>::type;
   constexpr int U = 4;
   const int lane = threadIdx.x & 31, pieces = a.D / (BYTES / ES);
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = static_cast<int64_t>(gridDim.x) * kRowWarps;
-  for (int64_t m = warp; m < a.M; m += warps) {
+  const Items t = items_of<U>(a, pieces);
+  for (int64_t it = t.first; it < t.all; it += t.step) {
+    const int64_t m = it / t.each;
+    const int c = static_cast<int>(it - m * t.each) * (32 * U) + lane;
     const int at = place_of(a, m, lane);
     const R *x = reinterpret_cast<const R *>(static_cast<const char *>(a.x) + m * a.ld * ES);
-    for (int c0 = 0; c0 < pieces; c0 += 32 * U) {
-      const int c = c0 + lane;
-      R v[U];
+    R v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (c + 32 * i < pieces) v[i] = x[c + 32 * i];
+    for (int r = 0; r < a.k; ++r) {
+      const int64_t j = __shfl_sync(kFull, at, r);
+      if (j < 0) continue;
+      R *o = static_cast<R *>(a.out) + j * pieces;
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (c + 32 * i < pieces) v[i] = x[c + 32 * i];
-      for (int r = 0; r < a.k; ++r) {
-        const int64_t j = __shfl_sync(kFull, at, r);
-        if (j < 0) continue;
-        R *o = static_cast<R *>(a.out) + j * pieces;
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (c + 32 * i < pieces) o[c + 32 * i] = v[i];
-      }
+        if (c + 32 * i < pieces) o[c + 32 * i] = v[i];
     }
   }
-  clear_rest<BYTES>(a, pieces, warp, warps, lane);
+  clear_rest<BYTES>(a, pieces, t.first, t.step, lane);
 }
 
-template <typename T, int BYTES>
+// V rows at a time, U pieces of each: eight loads on their way
+template <typename T, int BYTES, int V>
 __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const RowArgs a) {
   using R = typename Raw<BYTES>::type;
   using P = Piece<T, BYTES>;
-  constexpr int U = 2, V = 4;  // pieces of a row, rows at a time
+  constexpr int U = 8 / V;
   const int lane = threadIdx.x & 31, pieces = a.D / P::n;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = static_cast<int64_t>(gridDim.x) * kRowWarps;
-  for (int64_t m = warp; m < a.M; m += warps) {
+  const Items t = items_of<U>(a, pieces);
+  for (int64_t it = t.first; it < t.all; it += t.step) {
+    const int64_t m = it / t.each;
+    const int c = static_cast<int>(it - m * t.each) * (32 * U) + lane;
     const int at = place_of(a, m, lane);
     const float wt = lane >= a.k ? 0.f : a.w ? a.w[m * a.k + lane] : 1.f;
-    for (int c0 = 0; c0 < pieces; c0 += 32 * U) {
-      const int c = c0 + lane;
-      P sum[U];
+    P sum[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i)
 #pragma unroll
-        for (int e = 0; e < P::n; ++e) sum[i].v[e] = 0.f;
-      for (int r0 = 0; r0 < a.k; r0 += V) {
-        R v[V][U];
-        bool have[V];
-        float ww[V];
+      for (int e = 0; e < P::n; ++e) sum[i].v[e] = 0.f;
+    for (int r0 = 0; r0 < a.k; r0 += V) {
+      R v[V][U];
+      bool have[V];
+      float ww[V];
 #pragma unroll
-        for (int r = 0; r < V; ++r) {
-          const int64_t j = __shfl_sync(kFull, at, (r0 + r) & 31);
-          ww[r] = __shfl_sync(kFull, wt, (r0 + r) & 31);
-          have[r] = r0 + r < a.k && j >= 0;
-          const R *x = static_cast<const R *>(a.rows) + j * pieces;
+      for (int r = 0; r < V; ++r) {
+        const int64_t j = __shfl_sync(kFull, at, (r0 + r) & 31);
+        ww[r] = __shfl_sync(kFull, wt, (r0 + r) & 31);
+        have[r] = r0 + r < a.k && j >= 0;
+        const R *x = static_cast<const R *>(a.rows) + j * pieces;
 #pragma unroll
-          for (int i = 0; i < U; ++i)
-            if (have[r] && c + 32 * i < pieces) v[r][i] = x[c + 32 * i];
-        }
-#pragma unroll
-        for (int r = 0; r < V; ++r)
-#pragma unroll
-          for (int i = 0; i < U; ++i)
-            if (have[r] && c + 32 * i < pieces) {
-              const P x = unpack<T, BYTES>(v[r][i]);
-#pragma unroll
-              for (int e = 0; e < P::n; ++e) sum[i].v[e] = fmaf(ww[r], x.v[e], sum[i].v[e]);
-            }
+        for (int i = 0; i < U; ++i)
+          if (have[r] && c + 32 * i < pieces) v[r][i] = x[c + 32 * i];
       }
-      R *y = static_cast<R *>(a.out) + m * pieces;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (c + 32 * i < pieces) y[c + 32 * i] = pack<T, BYTES>(sum[i]);
+      for (int r = 0; r < V; ++r)
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (have[r] && c + 32 * i < pieces) {
+            const P x = unpack<T, BYTES>(v[r][i]);
+#pragma unroll
+            for (int e = 0; e < P::n; ++e) sum[i].v[e] = fmaf(ww[r], x.v[e], sum[i].v[e]);
+          }
     }
+    R *y = static_cast<R *>(a.out) + m * pieces;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (c + 32 * i < pieces) y[c + 32 * i] = pack<T, BYTES>(sum[i]);
   }
 }
 
@@ -384,9 +426,9 @@ int piece_bytes(int es, int64_t D, int64_t ld, std::initializer_list<const void 
   return es;
 }
 
-unsigned row_grid(int64_t M) {
-  // a token a warp; from 32 CTAs an SM on, warps take several
-  const int64_t n = (M + kRowWarps - 1) / kRowWarps;
+unsigned row_grid(int64_t items) {
+  // an item a warp; from 32 CTAs an SM on, warps take several
+  const int64_t n = (items + kRowWarps - 1) / kRowWarps;
   return static_cast<unsigned>(n < 1 ? 1 : n > 152 * 32 ? 152 * 32 : n);
 }
 
@@ -420,37 +462,42 @@ extern "C" int route_sort(const int32_t *sel, int64_t M, int k, int N, int32_t *
     return set_error(SDM_ERR_INVALID_ARG, "route_sort: workspace of %zu bytes needed", need);
   if (!aligned(sel, 4) || !aligned(order, 4) || !aligned(place, 4) || !aligned(offsets, 4) || !aligned(workspace, 4) || !aligned(dev_err, 4))
     return set_error(SDM_ERR_ALIGN, "route_sort: a pointer is not aligned");
-  SortArgs a{sel, M * k, N, static_cast<int>((M * k + kBlock - 1) / kBlock), order, place, offsets, static_cast<int32_t *>(workspace), dev_err};
+  SortArgs a{sel, M * k, N, static_cast<int>((M * k + kBlock - 1) / kBlock), order, place, offsets, static_cast<int32_t *>(workspace), dev_err, 0};
   if (a.blocks < 1) a.blocks = 1;
+  a.sum_here = static_cast<int64_t>(a.blocks) * N <= kSumHere;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int hist = kSortWarps * N * 4, smem = hist + (N + 1) * 4;
+  const int hist = kSortWarps * N * 4, smem = hist + (2 * N + 1) * 4;
   if (smem > 48 << 10)  // the limit is the kernel's, the same in every call
     for (const void *f : {reinterpret_cast<const void *>(route_count), reinterpret_cast<const void *>(route_place)}) {
-      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps * kMaxParts + kMaxParts + 1) * 4);
+      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps * kMaxParts + 2 * kMaxParts + 1) * 4);
       if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "route_sort: %s", cudaGetErrorString(e));
     }
   if (a.blocks > 1 && N > 0) {
     route_count<<<a.blocks, kSortThreads, hist, st>>>(a);
-    route_scan<<<N, 32, 0, st>>>(a);
+    if (!a.sum_here) route_scan<<<N, 32, 0, st>>>(a);
   }
   route_place<<<a.blocks, kSortThreads, smem, st>>>(a);
   return check_launch("route_sort");
 }
 
-#define SDM_ROWS(kernel, bytes)                                                      \
-  do {                                                                               \
-    const unsigned grid_ = row_grid(M);                                              \
-    if (dtype == SDM_DTYPE_F32) {                                                    \
-      if ((bytes) == 16) kernel<float, 16><<<grid_, kRowThreads, 0, st>>>(a);        \
-      else if ((bytes) == 8) kernel<float, 8><<<grid_, kRowThreads, 0, st>>>(a);     \
-      else kernel<float, 4><<<grid_, kRowThreads, 0, st>>>(a);                       \
-    } else {                                                                         \
-      if ((bytes) == 16) kernel<uint16_t, 16><<<grid_, kRowThreads, 0, st>>>(a);     \
-      else if ((bytes) == 8) kernel<uint16_t, 8><<<grid_, kRowThreads, 0, st>>>(a);  \
-      else if ((bytes) == 4) kernel<uint16_t, 4><<<grid_, kRowThreads, 0, st>>>(a);  \
-      else kernel<uint16_t, 2><<<grid_, kRowThreads, 0, st>>>(a);                    \
-    }                                                                                \
-  } while (0)
+namespace {
+
+// the kernel for an element type and a piece size: f(type tag, piece size tag)
+template <int N>
+struct Tag {
+  static constexpr int value = N;
+};
+template <typename F>
+void by_type(int dtype, int bytes, F f) {
+  if (dtype == SDM_DTYPE_F32)
+    bytes == 16 ? f(0.f, Tag<16>()) : bytes == 8 ? f(0.f, Tag<8>()) : f(0.f, Tag<4>());
+  else
+    bytes == 16 ? f(uint16_t(0), Tag<16>()) : bytes == 8 ? f(uint16_t(0), Tag<8>()) : bytes == 4 ? f(uint16_t(0), Tag<4>()) : f(uint16_t(0), Tag<2>());
+}
+// items of M rows in stretches of 32 u pieces
+int64_t items(int64_t M, int D, int es, int bytes, int u) { return M * ((D / (bytes / es) + 32 * u - 1) / (32 * u)); }
+
+}  // namespace
 
 extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_t *place, const int32_t *offsets, int64_t M,
                             int k, int N, int D, void *rows, void *stream) {
@@ -464,15 +511,9 @@ extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_
   RowArgs a{x, nullptr, rows, ld_x, place, offsets, nullptr, nullptr, M, k, N, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bytes = piece_bytes(es, D, ld_x, {x, rows});
-  const unsigned grid = row_grid(M);
-  if (bytes == 16)
-    es == 4 ? route_gather_kernel<16, 4><<<grid, kRowThreads, 0, st>>>(a) : route_gather_kernel<16, 2><<<grid, kRowThreads, 0, st>>>(a);
-  else if (bytes == 8)
-    es == 4 ? route_gather_kernel<8, 4><<<grid, kRowThreads, 0, st>>>(a) : route_gather_kernel<8, 2><<<grid, kRowThreads, 0, st>>>(a);
-  else if (bytes == 4)
-    es == 4 ? route_gather_kernel<4, 4><<<grid, kRowThreads, 0, st>>>(a) : route_gather_kernel<4, 2><<<grid, kRowThreads, 0, st>>>(a);
-  else
-    route_gather_kernel<2, 2><<<grid, kRowThreads, 0, st>>>(a);
+  by_type(dtype, bytes, [&](auto e, auto n) {
+    route_gather_kernel<n.value, sizeof e><<<row_grid(items(M, D, es, n.value, 4)), kRowThreads, 0, st>>>(a);
+  });
   return check_launch("route_gather");
 }
 
@@ -487,7 +528,15 @@ extern "C" int route_combine(const void *rows, int dtype, const int32_t *place, 
     return set_error(SDM_ERR_ALIGN, "route_combine: a pointer is not aligned");
   RowArgs a{nullptr, rows, y, D, place, nullptr, w, nullptr, M, k, 0, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SDM_ROWS(route_combine_kernel, piece_bytes(es, D, D, {rows, y}));
+  by_type(dtype, piece_bytes(es, D, D, {rows, y}), [&](auto e, auto n) {
+    using T = decltype(e);
+    if (k <= 1)
+      route_combine_kernel<T, n.value, 1><<<row_grid(items(M, D, es, n.value, 8)), kRowThreads, 0, st>>>(a);
+    else if (k == 2)
+      route_combine_kernel<T, n.value, 2><<<row_grid(items(M, D, es, n.value, 4)), kRowThreads, 0, st>>>(a);
+    else
+      route_combine_kernel<T, n.value, 4><<<row_grid(items(M, D, es, n.value, 2)), kRowThreads, 0, st>>>(a);
+  });
   return check_launch("route_combine");
 }
 
@@ -505,6 +554,8 @@ extern "C" int route_combine_backward(const void *dy, int64_t ld_dy, int dtype, 
     return set_error(SDM_ERR_ALIGN, "route_combine_backward: a pointer is not aligned");
   RowArgs a{dy, rows, drows, ld_dy, place, offsets, w, dw, M, k, N, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SDM_ROWS(route_combine_back_kernel, piece_bytes(es, D, ld_dy, {dy, rows, drows}));
+  by_type(dtype, piece_bytes(es, D, ld_dy, {dy, rows, drows}), [&](auto e, auto n) {
+    route_combine_back_kernel<decltype(e), n.value><<<row_grid(M), kRowThreads, 0, st>>>(a);
+  });
   return check_launch("route_combine_backward");
 }
