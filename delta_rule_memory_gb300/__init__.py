@@ -1001,25 +1001,31 @@ def gdn_step(state, q, k, v, log_alpha, beta, slots=None, lens=None, y=None, dev
     return y
 
 
-def _matrix(t, name: str, dtype=None, shape=None, index=None) -> int:
-    ld = _act(t, name, dtype, shape, index)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be [rows,D]")
-    if max(t.shape) >= _INT_END:
-        raise ValueError(f"sizes must be below 2^31, got {tuple(t.shape)}")
-    return ld
+def _matrix(t, name: str, shape=None, dtype=None, index=None) -> int:
+    """Check [rows,D] activations; returns their row distance."""
+    if not isinstance(t, _Tensor) or t.dim() != 2 or max(t.shape) >= _INT_END or not _plain(t, t.dtype, t.shape, t.get_device()):
+        if isinstance(t, _Tensor) and t.dim() != 2:
+            raise ValueError(f"{name} must be [rows,D]")
+        if isinstance(t, _Tensor) and max(t.shape) >= _INT_END:
+            raise ValueError(f"sizes must be below 2^31, got {tuple(t.shape)}")
+        return _act(t, name, dtype, shape, index)
+    if t.dtype not in _DTYPES or not t.is_cuda:
+        _act(t, name)
+    return t.shape[1]
 
 
-def _visits(place, name: str, index=None):
-    if not isinstance(place, _Tensor) or not place.is_cuda:
+def _visits(t, name: str, M=None, index=None):
+    """Check int32 [M,k]; returns M, k and the device's index."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if place.dim() != 2:
+    if t.dim() != 2:
         raise ValueError(f"{name} must be [M,k]")
-    if max(place.shape) >= _INT_END:
-        raise ValueError(f"sizes must be below 2^31, got {tuple(place.shape)}")
-    dev = place.get_device() if index is None else index
-    _need(place, name, torch.int32, None, dev)
-    return (*place.shape, dev)
+    shape = t.shape
+    if max(shape) >= _INT_END:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(shape)}")
+    dev = t.get_device() if index is None else index
+    _need(t, name, torch.int32, shape if M is None else (M, shape[1]), dev)
+    return shape[0], shape[1], dev
 
 
 def route_sort_workspace_size(M: int, k: int, N: int) -> int:
@@ -1063,8 +1069,7 @@ def route_gather(x, place, offsets, rows=None, stream=None):
     gradient is route_combine(drows, place)."""
     ld = _matrix(x, "x")
     M, D = x.shape
-    _, k, dev = _visits(place, "place", x.get_device())
-    _need(place, "place", torch.int32, (M, k), dev)
+    _, k, dev = _visits(place, "place", M, x.get_device())
     _need(offsets, "offsets", torch.int32, None, dev)
     if not offsets.numel():
         raise ValueError("offsets must be [N+1]")
@@ -1081,7 +1086,7 @@ def route_combine(rows, place, w=None, y=None, stream=None):
     """The rows [M k, D] (bf16 or fp32) at each token's places times its weights
     w fp32 [M,k] (None: 1), summed: y [M,D] of the rows' type."""
     _matrix(rows, "rows")
-    M, k, dev = _visits(place, "place", rows.get_device())
+    M, k, dev = _visits(place, "place", None, rows.get_device())
     D = rows.shape[1]
     _need(rows, "rows", rows.dtype, (M * k, D), dev)
     if w is not None:
@@ -1100,8 +1105,7 @@ def route_combine_backward(dy, rows, place, w, offsets, drows=None, dw=None, str
     visit; dw fp32 [M,k])."""
     ld = _matrix(dy, "dy")
     M, D = dy.shape
-    _, k, dev = _visits(place, "place", dy.get_device())
-    _need(place, "place", torch.int32, (M, k), dev)
+    _, k, dev = _visits(place, "place", M, dy.get_device())
     _need(rows, "rows", dy.dtype, (M * k, D), dev)
     _need(w, "w", torch.float32, (M, k), dev)
     _need(offsets, "offsets", torch.int32, None, dev)

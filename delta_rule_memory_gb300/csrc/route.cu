@@ -268,6 +268,8 @@ __device__ __forceinline__ void clear_rest(const RowArgs &a, int pieces, int64_t
 }
 
 // an item: a token and a stretch of 32 U pieces of its row
+template <int BYTES>
+constexpr int kStretch = BYTES == 16 ? 4 : 8;
 struct Items {
   int64_t first, step, all;
   int each;  // stretches of a row
@@ -285,7 +287,7 @@ __device__ __forceinline__ Items items_of(const RowArgs &a, int pieces) {
 template <int BYTES, int ES>
 __global__ void __launch_bounds__(kRowThreads) route_gather_kernel(const RowArgs a) {
   using R = typename Raw<BYTES>::type;
-  constexpr int U = 4;
+  constexpr int U = kStretch<BYTES>;
   const int lane = threadIdx.x & 31, pieces = a.D / (BYTES / ES);
   const Items t = items_of<U>(a, pieces);
   for (int64_t it = t.first; it < t.all; it += t.step) {
@@ -309,12 +311,15 @@ __global__ void __launch_bounds__(kRowThreads) route_gather_kernel(const RowArgs
   clear_rest<BYTES>(a, pieces, t.first, t.step, lane);
 }
 
-// V rows at a time, U pieces of each: eight loads on their way
-template <typename T, int BYTES, int V>
+// A row at a time, so that a thread needs few registers and an SM holds many
+// warps, and reads that leave no trace in the caches (nothing is read twice):
+// 16,384 x 4 rows of 3,840 bf16 in 101 us, 92% of the measured copy bandwidth, where
+// four rows at a time took 133 and cached reads of two rows 182
+template <typename T, int BYTES>
 __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const RowArgs a) {
   using R = typename Raw<BYTES>::type;
   using P = Piece<T, BYTES>;
-  constexpr int U = 8 / V;
+  constexpr int U = kStretch<BYTES>;
   const int lane = threadIdx.x & 31, pieces = a.D / P::n;
   const Items t = items_of<U>(a, pieces);
   for (int64_t it = t.first; it < t.all; it += t.step) {
@@ -327,42 +332,36 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const RowArg
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int e = 0; e < P::n; ++e) sum[i].v[e] = 0.f;
-    for (int r0 = 0; r0 < a.k; r0 += V) {
-      R v[V][U];
-      bool have[V];
-      float ww[V];
+    for (int r = 0; r < a.k; ++r) {
+      const int64_t j = __shfl_sync(kFull, at, r);
+      const float ww = __shfl_sync(kFull, wt, r);
+      if (j < 0) continue;
+      const R *x = static_cast<const R *>(a.rows) + j * pieces;
+      R v[U];
 #pragma unroll
-      for (int r = 0; r < V; ++r) {
-        const int64_t j = __shfl_sync(kFull, at, (r0 + r) & 31);
-        ww[r] = __shfl_sync(kFull, wt, (r0 + r) & 31);
-        have[r] = r0 + r < a.k && j >= 0;
-        const R *x = static_cast<const R *>(a.rows) + j * pieces;
+      for (int i = 0; i < U; ++i)
+        if (c + 32 * i < pieces) v[i] = __ldcs(x + c + 32 * i);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (have[r] && c + 32 * i < pieces) v[r][i] = x[c + 32 * i];
-      }
+      for (int i = 0; i < U; ++i)
+        if (c + 32 * i < pieces) {
+          const P y = unpack<T, BYTES>(v[i]);
 #pragma unroll
-      for (int r = 0; r < V; ++r)
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (have[r] && c + 32 * i < pieces) {
-            const P x = unpack<T, BYTES>(v[r][i]);
-#pragma unroll
-            for (int e = 0; e < P::n; ++e) sum[i].v[e] = fmaf(ww[r], x.v[e], sum[i].v[e]);
-          }
+          for (int e = 0; e < P::n; ++e) sum[i].v[e] = fmaf(ww, y.v[e], sum[i].v[e]);
+        }
     }
     R *y = static_cast<R *>(a.out) + m * pieces;
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (c + 32 * i < pieces) y[c + 32 * i] = pack<T, BYTES>(sum[i]);
+      if (c + 32 * i < pieces) __stcs(y + c + 32 * i, pack<T, BYTES>(sum[i]));
   }
 }
 
-template <typename T, int BYTES>
+// V rows at a time: as many as a token has, up to four
+template <typename T, int BYTES, int V>
 __global__ void __launch_bounds__(kRowThreads) route_combine_back_kernel(const RowArgs a) {
   using R = typename Raw<BYTES>::type;
   using P = Piece<T, BYTES>;
-  constexpr int U = 2, V = 4;
+  constexpr int U = 2;
   const int lane = threadIdx.x & 31, pieces = a.D / P::n;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = static_cast<int64_t>(gridDim.x) * kRowWarps;
   for (int64_t m = warp; m < a.M; m += warps) {
@@ -512,7 +511,7 @@ extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bytes = piece_bytes(es, D, ld_x, {x, rows});
   by_type(dtype, bytes, [&](auto e, auto n) {
-    route_gather_kernel<n.value, sizeof e><<<row_grid(items(M, D, es, n.value, 4)), kRowThreads, 0, st>>>(a);
+    route_gather_kernel<n.value, sizeof e><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0, st>>>(a);
   });
   return check_launch("route_gather");
 }
@@ -529,13 +528,7 @@ extern "C" int route_combine(const void *rows, int dtype, const int32_t *place, 
   RowArgs a{nullptr, rows, y, D, place, nullptr, w, nullptr, M, k, 0, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_type(dtype, piece_bytes(es, D, D, {rows, y}), [&](auto e, auto n) {
-    using T = decltype(e);
-    if (k <= 1)
-      route_combine_kernel<T, n.value, 1><<<row_grid(items(M, D, es, n.value, 8)), kRowThreads, 0, st>>>(a);
-    else if (k == 2)
-      route_combine_kernel<T, n.value, 2><<<row_grid(items(M, D, es, n.value, 4)), kRowThreads, 0, st>>>(a);
-    else
-      route_combine_kernel<T, n.value, 4><<<row_grid(items(M, D, es, n.value, 2)), kRowThreads, 0, st>>>(a);
+    route_combine_kernel<decltype(e), n.value><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0, st>>>(a);
   });
   return check_launch("route_combine");
 }
@@ -555,7 +548,10 @@ extern "C" int route_combine_backward(const void *dy, int64_t ld_dy, int dtype, 
   RowArgs a{dy, rows, drows, ld_dy, place, offsets, w, dw, M, k, N, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_type(dtype, piece_bytes(es, D, ld_dy, {dy, rows, drows}), [&](auto e, auto n) {
-    route_combine_back_kernel<decltype(e), n.value><<<row_grid(M), kRowThreads, 0, st>>>(a);
+    if (k <= 2)
+      route_combine_back_kernel<decltype(e), n.value, 2><<<row_grid(M), kRowThreads, 0, st>>>(a);
+    else
+      route_combine_back_kernel<decltype(e), n.value, 4><<<row_grid(M), kRowThreads, 0, st>>>(a);
   });
   return check_launch("route_combine_backward");
 }
