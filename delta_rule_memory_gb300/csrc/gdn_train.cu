@@ -372,21 +372,28 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 }
 
 // ---------------------------------------------------------------------------
-// The chains.  A CTA has W tiles of 16 value columns of one head, each with two
-// warps: the first does what the next chunk waits for (Z, E and the state's
-// update), the second everything else (copies of the next chunk's tiles, y,
-// the products with dy, what is kept for later).  A tile's state lives in shared memory as its three
-// bf16 parts, which are all 24 bits of it, in the order of the A fragments that every
-// product with it takes; so the loops over the key channels need not be unrolled over
-// registers and stay small enough for the instruction caches.
+// The chains.  A CTA has W tiles of 16 value columns of one head, each with three
+// warps.  Two do what the next chunk waits for, each with half of the key channels (the
+// sums with the state and its update) and with two of the four groups of 16 tokens (0
+// and 3, or 1 and 2, the same number of the triangle's blocks): sums over all channels and a
+// triangle's products meet in shared memory.  The third does everything else:
+// y, the products with dy, what is kept for later, copies.  A tile's state lives in shared
+// memory as its three bf16 parts, which are all 24 bits of it, in the order of the A
+// fragments that every product with it takes.
+// One warp a tile took 7.6 us a chunk at dk = dv = 128, a second one for what can wait and
+// copies by TMA 3.6 (5.0 where four tiles share an SM's tensor cores); this form 
+// FIGURES
 // ---------------------------------------------------------------------------
 template <int NK, int PM, int W>  // PM: parts of M
 struct Chain {
   static constexpr int P = NK / 4;  // panels of K and Q
-  static constexpr int K = 0, Q = K + P * kPanel, V = Q + P * kPanel, T = V + kPanel, M = T + 3 * kTri, sc = M + PM * kTri,
+  static constexpr int K = 0, Q = K + P * kPanel, V = Q + P * kPanel, T = V + kPanel, sc = T + 3 * kTri,
                        stage = (sc + 3 * kC * 4 + 1023) / 1024 * 1024;
-  static constexpr int state = 2 * stage, tokens = state + W * NK * 3 * 512, bars = tokens + W * 8 * 512, size = bars + 16;
+  // M is read early in a chunk only, so one place does
+  static constexpr int M = 2 * stage, state = M + PM * kTri, parts = state + W * NK * 3 * 512, tokens = parts + W * 4 * 3 * 512,
+                       bars = tokens + W * 8 * 512, size = bars + 32;
 };
+static_assert(Chain<8, 3, 4>::size <= kMaxSmem && Chain<8, 2, 4>::size <= kMaxSmem, "");
 
 // A chunk's tiles into a stage; cols: the value columns' tensor.  What tensor and
 // bulk copies bring is asked for by one lane of a warp of its own or, where a CTA
@@ -404,7 +411,7 @@ __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, 
   const int hk = h / (a.H / a.Hk), token = static_cast<int>(tok);
   const bool qk = a.by_qk == 16, cols = by_cols == 16;
   const uint32_t part[4] = {qk ? L::P * kPanel : 0u, qk ? L::P * kPanel : 0u, 3 * kTri + (cols ? kPanel : 0u),
-                            PM * kTri + 3 * kC * 4u};
+                            3 * kC * 4u};
   umma::mbar_expect_tx(mb, all ? part[0] + part[1] + part[2] + part[3] : part[who]);
   if ((all || who == 0) && qk)
 #pragma unroll
@@ -417,11 +424,15 @@ __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, 
     if (cols) tensor_panel(smem_u32(st + L::V), cols_map, col0 & ~63, h, token, mb);
   }
   if (all || who == 3) {
-    umma::bulk_g2s(smem_u32(st + L::M), a.m3 + u * (3 * kTri), PM * kTri, mb);
     umma::bulk_g2s(smem_u32(st + L::sc), a.scal + u * kScal, 3 * kC * 4, mb);
   }
 }
-// ... and the rest, by the second warps
+template <int PM>
+__device__ __forceinline__ void request_m(unsigned char *to, uint64_t *bar, const Gdn &a, int64_t u) {
+  umma::mbar_expect_tx(smem_u32(bar), PM * kTri);
+  umma::bulk_g2s(smem_u32(to), a.m3 + u * (3 * kTri), PM * kTri, smem_u32(bar));
+}
+// ... and the rest, by the third warps
 template <int NK, int PM, int W>
 __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int64_t tok, int h, int col0, int live,
                                            const uint16_t *cols, int64_t ld_cols, int by_cols, int tid) {
@@ -550,12 +561,6 @@ __device__ __forceinline__ void add(float (&d)[N][4], const float (&l)[N][4]) {
     for (int e = 0; e < 4; ++e) d[i][e] += l[i][e];
 }
 
-// the three parts of an accumulator over 64 tokens, as A fragments of its four k-steps
-__device__ __forceinline__ void split_tokens(const float (&x)[8][4], uint32_t (&a)[4][3][4]) {
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks) a_split<3>(x[2 * ks], x[2 * ks + 1], a[ks]);
-}
-
 // acc = A B for n-tiles 4 quad .. 4 quad + 3, B = tile[token][n] exact, over 64
 // tokens: the small parts first
 __device__ __forceinline__ void quad_product(uint32_t tile, int quad, const uint32_t (&a)[4][3][4], int lane,
@@ -594,18 +599,18 @@ __device__ __forceinline__ void update_quad(uint4 *parts, int quad, int lane, fl
   }
 }
 
-// d = the state's product with tile[token][key channel]
-template <int NK>
-__device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile, int lane, float (&d)[8][4]) {
+// d = the product of N k-steps of the state with tile[token][key channel], channels from k0 on
+template <int N>
+__device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile, int k0, int lane, float (&d)[8][4]) {
   float l[8][4];
   clear(d);
   clear(l);
-#pragma unroll 2
-  for (int ks = 0; ks < NK; ++ks) {
+#pragma unroll
+  for (int ks = 0; ks < N; ++ks) {
     uint32_t s[3][4], r[4][4];
     get_parts(parts + ks * 96, lane, s);
 #pragma unroll
-    for (int np = 0; np < 4; ++np) b_rows(tile, 16 * np, 16 * ks, lane, r[np]);
+    for (int np = 0; np < 4; ++np) b_rows(tile, 16 * np, k0 + 16 * ks, lane, r[np]);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
@@ -618,144 +623,195 @@ __device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile,
   add(d, l);
 }
 
-// d = X T^T (BACK: X T), X [16 columns][64 tokens] in three parts, T a triangle in three
+// A tile's two first warps x = 0 and 1 and their groups of 16 tokens, i = 0 and 1
+__device__ __forceinline__ int group_of(int x, int i) { return x == 0 ? (i ? 3 : 0) : 1 + i; }
+// of sums over all tokens: the own groups' n-tiles, and the other warp's through shared memory
+__device__ __forceinline__ void give_sums(float4 *m, int x, int lane, const float (&d)[8][4], float (&mine)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = i < 2 ? i : i + 4, b = i + 2;  // n-tiles of groups 0 and 3, of 1 and 2
+    m[(x ? a : b) * 32 + lane] = x ? make_float4(d[a][0], d[a][1], d[a][2], d[a][3]) : make_float4(d[b][0], d[b][1], d[b][2], d[b][3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine[i][e] = x ? d[b][e] : d[a][e];
+  }
+}
+__device__ __forceinline__ int tile_of(int x, int i) { return 2 * group_of(x, i >> 1) + (i & 1); }
+__device__ __forceinline__ void take_sums(const float4 *m, int x, int lane, float (&mine)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = m[tile_of(x, i) * 32 + lane];
+    mine[i][0] += v.x, mine[i][1] += v.y, mine[i][2] += v.z, mine[i][3] += v.w;
+  }
+}
+__device__ __forceinline__ void put_tiles(float4 *m, int x, int lane, const float (&mine)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[tile_of(x, i) * 32 + lane] = make_float4(mine[i][0], mine[i][1], mine[i][2], mine[i][3]);
+}
+__device__ __forceinline__ void put_groups(uint4 *parts, int x, int lane, const float (&mine)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) put_parts(parts + group_of(x, i) * 96, lane, mine[2 * i], mine[2 * i + 1]);
+}
+__device__ __forceinline__ void scale_groups(float (&mine)[4][4], int x, const float *f, int t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = *reinterpret_cast<const float2 *>(f + 8 * tile_of(x, i) + 2 * t);
+    mine[i][0] *= v.x, mine[i][1] *= v.y, mine[i][2] *= v.x, mine[i][3] *= v.y;
+  }
+}
+
+// the own groups of X T^T (BACK: X T), X's parts in shared memory, T a triangle in three parts
 template <bool BACK>
-__device__ __forceinline__ void triangle_product(const float (&x)[8][4], uint32_t tri, int lane, float (&d)[8][4]) {
-  float l[8][4];
-  clear(d);
-  clear(l);
+__device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tri, int x, int lane, float (&d)[4][4]) {
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    uint32_t a[3][4];
-    a_split<3>(x[2 * ks], x[2 * ks + 1], a);
+  for (int i = 0; i < 2; ++i) {
+    const int n = group_of(x, i), first = BACK ? n : 0, last = BACK ? 3 : n;
+    float h[2][4], l[2][4], m[2][4];  // parts 0 0; 0 1 and 1 0; 1 1, 0 2 and 2 0
+    clear(h);
+    clear(l);
+    clear(m);
+#pragma unroll 1
+    for (int ks = first; ks <= last; ++ks) {
+      uint32_t a[3][4], r[3][4];
+      get_parts(parts + ks * 96, lane, a);
 #pragma unroll
-    for (int np = BACK ? 0 : ks; np < (BACK ? ks + 1 : 4); ++np) {
-      uint32_t r[3][4];
+      for (int p = 0; p < 3; ++p) BACK ? tri_cols(tri + p * kTri, n, ks, lane, r[p]) : tri_rows(tri + p * kTri, n, ks, lane, r[p]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
-        BACK ? tri_cols(tri + p * kTri, np, ks, lane, r[p]) : tri_rows(tri + p * kTri, np, ks, lane, r[p]);
-      products(d, l, np, a, r);
+      for (int j = 0; j < 2; ++j) {
+        fma16816(m[j], a[1], r[1][2 * j], r[1][2 * j + 1]);
+        fma16816(l[j], a[0], r[1][2 * j], r[1][2 * j + 1]);
+        fma16816(h[j], a[0], r[0][2 * j], r[0][2 * j + 1]);
+        fma16816(m[j], a[0], r[2][2 * j], r[2][2 * j + 1]);
+        fma16816(l[j], a[1], r[0][2 * j], r[0][2 * j + 1]);
+        fma16816(m[j], a[2], r[0][2 * j], r[0][2 * j + 1]);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[2 * i + j][e] = h[j][e] + (l[j][e] + m[j][e]);
   }
-  add(d, l);
 }
 
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id + 1) : "memory"); }
-
-// a state's parts from and to a [dk][dv] matrix
-template <int NK>
-__device__ __forceinline__ void load_state(uint4 *parts, const float *m, int dk, int dv, int col, int lane) {
-#pragma unroll 1
-  for (int ks = 0; ks < NK; ++ks) {
-    float x[2][4];
-    read_state<2>(m, 16 * ks, dk, dv, col, lane, x);
-    put_parts(parts + ks * 96, lane, x[0], x[1]);
+// a tile's first two warps (64 threads), or all three (96), meet
+__device__ __forceinline__ void meet(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+// where a warp of a chain stands
+template <int W>
+struct Place {
+  int tid, role, w, lane, col0, col, b, h, len, n;
+  int64_t bh, tok;
+  bool mine;  // else the tile lies behind dv, and its warps only help with the copies
+  __device__ __forceinline__ explicit Place(const Gdn &a) {
+    tid = threadIdx.x, role = tid / (32 * W), w = (tid >> 5) % W, lane = tid & 31;
+    const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
+    bh = blockIdx.x / groups;
+    col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
+    b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+    len = length_of(a, b), n = (len + kC - 1) / kC;
+    tok = static_cast<int64_t>(b) * a.T;
+    mine = col < a.dv;
   }
-}
-template <int NK>
-__device__ __forceinline__ void store_state(const uint4 *parts, float *m, int dk, int dv, int col, int lane) {
-#pragma unroll 1
-  for (int ks = 0; ks < NK; ++ks) {
-    uint32_t s[3][4];
-    float x[2][4];
-    get_parts(parts + ks * 96, lane, s);
-    join(s, x[0], x[1]);
-    write_state<2>(m, 16 * ks, dk, dv, col, lane, x);
-  }
-}
+};
 
 template <int NK, int W>
-__global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(const Gdn a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Chain<NK, 2, W>;
-  constexpr int NT = 2 * NK;
+  constexpr int NT = 2 * NK, kOwn = 96 * W;  // kOwn: threads before the warp that asks for copies
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int role = tid / (32 * W);
-  const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
-  const int64_t bh = blockIdx.x / groups;
-  const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
-  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
-  const int len = length_of(a, b), n = (len + kC - 1) / kC;
-  const int64_t tok = static_cast<int64_t>(b) * a.T;
-  const bool mine = col < a.dv;  // else the warps only help with the copies
-  uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96;
-  float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;
-  const int vp = ((col0 & 63) >> 3) + 2 * w;  // the warp's pieces of the value columns' panel
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
+  const Place<W> me(a);
+  const int tid = me.tid, w = me.w, lane = me.lane, g = lane >> 2, t = lane & 3, n = me.n, len = me.len, col = me.col, h = me.h;
+  const int tiles = (a.dv + 15) >> 4;
+  uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96, *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
+  float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // half sums, then E
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);           // two stages, M
   if (tid == 0) {
     umma::mbar_init(smem_u32(bars), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 2), 1);
     umma::fence_mbar_init();
+    if (a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   }
   __syncthreads();
   uint32_t limit = kWaitLimit;
+  const int pair = 1 + w, three = 1 + W + w;  // barriers
 
-  if (role == 0) {
-    if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-    float S[NT][4];  // the state itself beside its parts
-    read_state<NT>(a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, 0, a.dk, a.dv, col, lane, S);
+  if (me.role < 2) {
+    const int x = me.role, vp = ((me.col0 & 63) >> 3) + 2 * w;  // vp: the tile's pieces of the value columns' panel
+    uint4 *own = hS + x * (NK / 2) * 96;
+    float S[NK][4];  // the own channels' state beside its parts
+    read_state<NK>(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * NK * 8, a.dk, a.dv, col, lane, S);
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) put_parts(hS + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
+    for (int ks = 0; ks < NK / 2; ++ks) put_parts(own + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
     for (int c = 0; c < n; ++c) {
       __syncthreads();
       wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
-      if (len - c * kC < kC) __syncthreads();  // the second warps clear rows
-      if (!mine) continue;
+      if (len - c * kC < kC) __syncthreads();  // the third warps clear rows
+      if (!me.mine) continue;
       unsigned char *st = sm + (c & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K), uV = smem_u32(st + L::V);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
-      float Z[8][4], E[8][4];
-      state_product<NK>(hS, uK, lane, Z);
+      float Z[4][4];
+      {
+        float d[8][4];
+        state_product<NK / 2>(own, uK, x * NK * 8, lane, d);
+        give_sums(hE, x, lane, d, Z);
+      }
+      meet(pair, 64);
+      take_sums(hE, x, lane, Z);
       // Z^T = V^T - gam S^T K^T
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t v[4];
         // tile[token][column]: rows of V^T are its columns
-        ldsm4_t(uV + piece(16 * np + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v);
+        ldsm4_t(uV + piece(16 * group_of(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int nt = 2 * np + x;
-          const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * nt + 2 * t);
+        for (int j = 0; j < 2; ++j) {
+          const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * tile_of(x, 2 * i + j) + 2 * t);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t vv = v[2 * x + (e >> 1)];
-            Z[nt][e] = fmaf(e & 1 ? -gm.y : -gm.x, Z[nt][e], e & 1 ? high2(vv) : low2(vv));
+            const uint32_t vv = v[2 * j + (e >> 1)];
+            Z[2 * i + j][e] = fmaf(e & 1 ? -gm.y : -gm.x, Z[2 * i + j][e], e & 1 ? high2(vv) : low2(vv));
           }
         }
       }
-      triangle_product<false>(Z, smem_u32(st + L::T), lane, E);
-      put(hE, lane, E);
-      pair_sync(w);  // E is there, S has been read
+      put_groups(hP, x, lane, Z);
+      meet(pair, 64);
+      float E[4][4];
+      triangle_product<false>(hP, smem_u32(st + L::T), x, lane, E);
+      put_tiles(hE, x, lane, E);
+      meet(three, 96);  // E is there, S and Z have been read
       // S^T = gam_C S^T + (tail U)^T K
-      scale_tokens(E, beta, t);
-      scale_tokens(E, tail, t);
+      scale_groups(E, x, beta, t);
+      scale_groups(E, x, tail, t);
+      put_groups(hP, x, lane, E);
+      meet(pair, 64);
       uint32_t ut[4][3][4];
-      split_tokens(E, ut);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) get_parts(hP + ks * 96, lane, ut[ks]);
       const float end = gam[kC - 1];
 #pragma unroll
-      for (int q = 0; q < NK / 2; ++q) {
+      for (int q = 0; q < NK / 4; ++q) {
         float acc[4][4];
-        quad_product(uK, q, ut, lane, acc);
+        quad_product(uK, x * (NK / 4) + q, ut, lane, acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) S[4 * q + i][e] = fmaf(end, S[4 * q + i][e], acc[i][e]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) put_parts(hS + (2 * q + i) * 96, lane, S[4 * q + 2 * i], S[4 * q + 2 * i + 1]);
+        for (int i = 0; i < 2; ++i) put_parts(own + (2 * q + i) * 96, lane, S[4 * q + 2 * i], S[4 * q + 2 * i + 1]);
       }
     }
-    if (mine) write_state<NT>(a.state_out + bh * a.dk * a.dv, 0, a.dk, a.dv, col, lane, S);
+    if (me.mine) write_state<NK>(a.state_out + me.bh * a.dk * a.dv, x * NK * 8, a.dk, a.dv, col, lane, S);
     return;
   }
 
-  const int ltid = tid - 32 * W;
+  const int ltid = tid - 64 * W;
   const auto request = [&](int c) {
     if (lane == 0)
-      request_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, bh * a.n + c, tok + c * kC, h, col0, a.by_v,
+      request_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0, a.by_v,
                               &maps.v, w);
     __syncwarp();
   };
-  if (role == 2) {
+  if (tid >= kOwn) {
     for (int c = 0; c <= n; ++c) {
       if (c > 0) __syncthreads();
       if (c < n) request(c);
@@ -765,14 +821,18 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(con
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, tok + c * kC, h, col0, min(len - c * kC, kC), a.v, a.ld_v, a.by_v, ltid);
+    copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v, a.by_v, ltid);
+  };
+  const auto ask_m = [&](int c) {
+    if (ltid == 0) request_m<2>(sm + L::M, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(0);
+    ask_m(0);
     copy(0);
   }
   for (int c = 0; c < n; ++c) {
-    const int64_t u = bh * a.n + c;
+    const int64_t u = me.bh * a.n + c;
     unsigned char *st = sm + (c & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
@@ -780,13 +840,14 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(con
       if (kAskers<W> > 1) request(c + 1);
       copy(c + 1);
     }
+    if (c > 0) ask_m(c);  // every third warp is done with the chunk before
     wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
       clear_stage<NK, 2, W>(st, a, len - c * kC, a.by_v, ltid);
       __syncthreads();
     }
-    if (!mine) continue;
-    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(st + L::M);
+    if (!me.mine) continue;
+    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::M);
     const float *gam = reinterpret_cast<const float *>(st + L::sc), *beta = gam + 2 * kC;
     float Y[8][4], E[8][4];
     clear(Y);
@@ -811,7 +872,8 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(con
       }
       scale_tokens(Y, gam, t);
     }
-    pair_sync(w);
+    wait_copies(bars + 2, c & 1, limit, a);
+    meet(three, 96);
     get(hE, lane, E);
     put(reinterpret_cast<float4 *>(a.e) + (u * tiles + (col >> 4)) * 256, lane, E);
     scale_tokens(E, beta, t);
@@ -828,7 +890,7 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(con
       }
     }
     // y, rounded once: pairs of tokens turned into pairs of columns
-    uint16_t *yc = a.y + (tok * a.H + h) * a.dv + col + 2 * t;
+    uint16_t *yc = a.y + (me.tok * a.H + h) * a.dv + col + 2 * t;
     const int left = a.dv - col - 2 * t;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
@@ -850,90 +912,104 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain(con
 }
 
 template <int NK, int W>
-__global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_back(const Gdn a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_back(const Gdn a, const __grid_constant__ Maps maps) {
   using L = Chain<NK, 3, W>;
-  constexpr int NT = 2 * NK;
+  constexpr int NT = 2 * NK, kOwn = 96 * W;
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, w = (tid >> 5) % W, lane = tid & 31, t = lane & 3;
-  const int role = tid / (32 * W);
-  const int tiles = (a.dv + 15) >> 4, groups = (tiles + W - 1) / W;
-  const int64_t bh = blockIdx.x / groups;
-  const int col0 = static_cast<int>(blockIdx.x - bh * groups) * (16 * W), col = col0 + 16 * w;
-  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
-  const int len = length_of(a, b), n = (len + kC - 1) / kC;
-  const int64_t tok = static_cast<int64_t>(b) * a.T, ld_y = static_cast<int64_t>(a.H) * a.dv;
-  const bool mine = col < a.dv;
-  uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96;
+  const Place<W> me(a);
+  const int tid = me.tid, w = me.w, lane = me.lane, t = lane & 3, n = me.n, len = me.len, col = me.col, h = me.h;
+  const int tiles = (a.dv + 15) >> 4;
+  const int64_t ld_y = static_cast<int64_t>(a.H) * a.dv;
+  uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96, *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
+  float4 *hX = reinterpret_cast<float4 *>(hP);                           // half sums, before the parts
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
-  const int vc = (col0 & 63) + 16 * w;  // the warp's columns in the value columns' panel
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
   if (tid == 0) {
     umma::mbar_init(smem_u32(bars), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 2), 1);
     umma::fence_mbar_init();
+    if (a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   }
   __syncthreads();
   uint32_t limit = kWaitLimit;
+  const int pair = 1 + w, three = 1 + W + w;
 
-  if (role == 0) {
-    if (a.err && a.lens && a.lens[b] != len && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-    load_state<NK>(hG, a.state_in ? a.state_in + bh * a.dk * a.dv : nullptr, a.dk, a.dv, col, lane);
-    float4 *kept = reinterpret_cast<float4 *>(a.g) + (bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 32);
+  if (me.role < 2) {
+    const int x = me.role;
+    uint4 *own = hG + x * (NK / 2) * 96;
+    float4 *kept = reinterpret_cast<float4 *>(a.g) + (me.bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 32) + x * NK * 32;
     const int64_t step = static_cast<int64_t>(tiles) * (NT * 32);
-    if (mine)
 #pragma unroll 1
-      for (int ks = 0; ks < NK; ++ks) {
-        uint32_t s[3][4];
-        float x[2][4];
-        get_parts(hG + ks * 96, lane, s);
-        join(s, x[0], x[1]);
-        put(kept + n * step + ks * 64, lane, x);
-      }
+    for (int ks = 0; ks < NK / 2; ++ks) {
+      float y[2][4];
+      read_state<2>(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * NK * 8 + 16 * ks, a.dk, a.dv, col, lane, y);
+      put_parts(own + ks * 96, lane, y[0], y[1]);
+      if (me.mine) put(kept + n * step + ks * 64, lane, y);
+    }
     for (int c = n - 1; c >= 0; --c) {
       const int it = n - 1 - c;
       __syncthreads();
       wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
-      if (len - c * kC < kC) __syncthreads();  // the second warps clear rows
-      if (!mine) continue;
+      if (len - c * kC < kC) __syncthreads();  // the third warps clear rows
+      if (!me.mine) continue;
       unsigned char *st = sm + (it & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
       // dU^T = tail G^T K^T + dY^T M
-      float U[8][4], Z[8][4];
-      state_product<NK>(hG, uK, lane, U);
-      scale_tokens(U, tail, t);
-      pair_sync(w);  // dY^T M is there, G has been read
-      get(hZ, lane, Z);
-      add(U, Z);
-      scale_tokens(U, beta, t);
-      triangle_product<true>(U, smem_u32(st + L::T), lane, Z);  // dZ^T
-      put(hZ, lane, Z);
-      // G^T = gam_C G^T + (gam dY)^T Q, by the second warp, - (gam dZ)^T K
-      scale_tokens(Z, gam, t);
+      float U[4][4], Z[4][4];
+      {
+        float d[8][4];
+        state_product<NK / 2>(own, uK, x * NK * 8, lane, d);
+        give_sums(hX, x, lane, d, U);
+      }
+      meet(three, 96);  // dY^T M is there, G has been read
+      take_sums(hX, x, lane, U);
+      scale_groups(U, x, tail, t);
+      take_sums(hZ, x, lane, U);
+      scale_groups(U, x, beta, t);
+      meet(pair, 64);  // the half sums have been read
+      put_groups(hP, x, lane, U);
+      meet(pair, 64);
+      triangle_product<true>(hP, smem_u32(st + L::T), x, lane, Z);  // dZ^T
+      put_tiles(hZ, x, lane, Z);
+      meet(three, 96);  // dZ is there, dU has been read, G = gam_C G + Q^T (gam dY)
+      // G^T -= (gam dZ)^T K
+      scale_groups(Z, x, gam, t);
+      put_groups(hP, x, lane, Z);
+      meet(pair, 64);
       uint32_t zt[4][3][4];
-      split_tokens(Z, zt);
-      pair_sync(w);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) get_parts(hP + ks * 96, lane, zt[ks]);
       float4 *to = kept + c * step;
-#pragma unroll 2
-      for (int q = 0; q < NK / 2; ++q) {
-        float acc[4][4], x[4][4];
-        quad_product(uK, q, zt, lane, acc);
-        update_quad(hG, q, lane, 1.f, -1.f, acc, x);
-        put(to + q * 128, lane, x);
+#pragma unroll
+      for (int q = 0; q < NK / 4; ++q) {
+        float acc[4][4], y[4][4];
+        quad_product(uK, x * (NK / 4) + q, zt, lane, acc);
+        update_quad(own, q, lane, 1.f, -1.f, acc, y);
+        put(to + q * 128, lane, y);
       }
     }
-    if (mine) store_state<NK>(hG, a.state_out + bh * a.dk * a.dv, a.dk, a.dv, col, lane);
+    if (me.mine)
+#pragma unroll 1
+      for (int ks = 0; ks < NK / 2; ++ks) {
+        uint32_t s[3][4];
+        float y[2][4];
+        get_parts(own + ks * 96, lane, s);
+        join(s, y[0], y[1]);
+        write_state<2>(a.state_out + me.bh * a.dk * a.dv, x * NK * 8 + 16 * ks, a.dk, a.dv, col, lane, y);
+      }
     return;
   }
 
-  const int ltid = tid - 32 * W;
+  const int ltid = tid - 64 * W, vc = (me.col0 & 63) + 16 * w;  // vc: the tile's columns in the value columns' panel
   const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
     if (lane == 0)
-      request_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, bh * a.n + c, tok + c * kC, h, col0, a.by_dy, &maps.dy, w);
+      request_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0, a.by_dy, &maps.dy, w);
     __syncwarp();
   };
-  if (role == 2) {
+  if (tid >= kOwn) {
     for (int it = 0; it <= n; ++it) {
       const int c = n - 1 - it;
       if (it > 0) __syncthreads();
@@ -944,16 +1020,20 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_bac
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 3, W>(sm + ((n - 1 - c) & 1) * L::stage, a, tok + c * kC, h, col0, min(len - c * kC, kC), a.dy, ld_y,
-                         a.by_dy, ltid);
+    copy_stage<NK, 3, W>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.dy, ld_y, a.by_dy,
+                         ltid);
+  };
+  const auto ask_m = [&](int c) {
+    if (ltid == 0) request_m<3>(sm + L::M, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(n - 1);
+    ask_m(n - 1);
     copy(n - 1);
   }
   for (int c = n - 1; c >= 0; --c) {
     const int it = n - 1 - c;
-    const int64_t u = bh * a.n + c;
+    const int64_t u = me.bh * a.n + c;
     unsigned char *st = sm + (it & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
@@ -962,15 +1042,15 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_bac
       copy(c - 1);
     }
     wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
+    wait_copies(bars + 2, it & 1, limit, a);
     if (len - c * kC < kC) {
       clear_stage<NK, 3, W>(st, a, len - c * kC, a.by_dy, ltid);
       __syncthreads();
     }
-    if (!mine) continue;
-    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(st + L::M), uY = smem_u32(st + L::V);
+    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::M), uY = smem_u32(st + L::V);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
     uint32_t y[4][1][4];
-    {
+    if (me.mine) {
       float R[8][4], l[8][4];
       clear(R);
       clear(l);
@@ -988,6 +1068,9 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_bac
       add(R, l);
       put(hZ, lane, R);
     }
+    meet(1 + 2 * W, 32 * W);  // the third warps: M has been read
+    if (c > 0) ask_m(c - 1);
+    if (!me.mine) continue;
     uint32_t d3[4][3][4];
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
@@ -1003,7 +1086,7 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_bac
       }
       a_split<3>(d[0], d[1], d3[ks]);
     }
-    pair_sync(w);
+    meet(three, 96);
     const float end = gam[kC - 1];
 #pragma unroll 2
     for (int q = 0; q < NK / 2; ++q) {
@@ -1011,7 +1094,7 @@ __global__ void __launch_bounds__(W < 4 ? 64 * W + 32 : 64 * W, 1) gdn_chain_bac
       quad_product(uQ, q, d3, lane, acc);
       update_quad(hG, q, lane, end, 1.f, acc, x);
     }
-    pair_sync(w);
+    meet(three, 96);
     float Z[8][4];
     get(hZ, lane, Z);
     put(reinterpret_cast<float4 *>(a.dz) + (u * tiles + (col >> 4)) * 256, lane, Z);
@@ -1602,8 +1685,8 @@ int chain_width(const Gdn &a, const Layout &l) {
 template <int NK, int W>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
-  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 64 * W + 32 : 64 * W, Chain<NK, 3, W>::size, a, maps, st)
-              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 64 * W + 32 : 64 * W, Chain<NK, 2, W>::size, a, maps, st);
+  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 3, W>::size, a, maps, st)
+              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 2, W>::size, a, maps, st);
 }
 template <int NK>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
