@@ -156,7 +156,8 @@ __device__ __forceinline__ void store_parts3(unsigned char *tiles, uint32_t off,
 // the lower blocks of an fp32 [64][kLd] matrix as three triangles
 __device__ __forceinline__ void write_tiles(const float *x, unsigned char *tiles, int tid) {
   for (int id = tid; id < kC * 8; id += kPrepThreads) {
-    const int i = id >> 3, p = id & 7;
+    // eight lanes, eight rows: 128 bytes in a row of the triangle
+    const int i = ((id >> 6) << 3) | (id & 7), p = (id >> 3) & 7;
     if (p > 2 * (i >> 4) + 1) continue;
     float v[8];
     *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x + i * kLd + p * 8);
@@ -599,13 +600,14 @@ __device__ __forceinline__ void update_quad(uint4 *parts, int quad, int lane, fl
   }
 }
 
-// d = the product of N k-steps of the state with tile[token][key channel], channels from k0 on
-template <int N>
+// d = the product of N k-steps of the state with tile[token][key channel],
+// channels from k0 on; U of them unrolled
+template <int N, int U>
 __device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile, int k0, int lane, float (&d)[8][4]) {
   float l[8][4];
   clear(d);
   clear(l);
-#pragma unroll
+#pragma unroll(U)
   for (int ks = 0; ks < N; ++ks) {
     uint32_t s[3][4], r[4][4];
     get_parts(parts + ks * 96, lane, s);
@@ -694,6 +696,9 @@ __device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tr
 
 // a tile's first two warps (64 threads), or all three (96), meet
 __device__ __forceinline__ void meet(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+// ... or only tell the others that they are there
+__device__ __forceinline__ void arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+
 // where a warp of a chain stands
 template <int W>
 struct Place {
@@ -752,7 +757,7 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
       float Z[4][4];
       {
         float d[8][4];
-        state_product<NK / 2>(own, uK, x * NK * 8, lane, d);
+        state_product<NK / 2, NK / 2>(own, uK, x * NK * 8, lane, d);
         give_sums(hE, x, lane, d, Z);
       }
       meet(pair, 64);
@@ -933,7 +938,7 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   }
   __syncthreads();
   uint32_t limit = kWaitLimit;
-  const int pair = 1 + w, three = 1 + W + w;
+  const int pair = 1 + w, three = 1 + W + w, read = 1 + 2 * W + w, thirds = 1 + 3 * W;
 
   if (me.role < 2) {
     const int x = me.role;
@@ -960,10 +965,11 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
       float U[4][4], Z[4][4];
       {
         float d[8][4];
-        state_product<NK / 2>(own, uK, x * NK * 8, lane, d);
+        state_product<NK / 2, 1>(own, uK, x * NK * 8, lane, d);
         give_sums(hX, x, lane, d, U);
       }
-      meet(three, 96);  // dY^T M is there, G has been read
+      arrive(read, 96);  // G has been read
+      meet(three, 96);   // dY^T M is there
       take_sums(hX, x, lane, U);
       scale_groups(U, x, tail, t);
       take_sums(hZ, x, lane, U);
@@ -982,7 +988,7 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) get_parts(hP + ks * 96, lane, zt[ks]);
       float4 *to = kept + c * step;
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < NK / 4; ++q) {
         float acc[4][4], y[4][4];
         quad_product(uK, x * (NK / 4) + q, zt, lane, acc);
@@ -1068,7 +1074,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
       add(R, l);
       put(hZ, lane, R);
     }
-    meet(1 + 2 * W, 32 * W);  // the third warps: M has been read
+    if (me.mine) arrive(three, 96);
+    meet(thirds, 32 * W);  // M has been read
     if (c > 0) ask_m(c - 1);
     if (!me.mine) continue;
     uint32_t d3[4][3][4];
@@ -1086,9 +1093,9 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
       }
       a_split<3>(d[0], d[1], d3[ks]);
     }
-    meet(three, 96);
+    meet(read, 96);
     const float end = gam[kC - 1];
-#pragma unroll 2
+#pragma unroll 1
     for (int q = 0; q < NK / 2; ++q) {
       float acc[4][4], x[4][4];
       quad_product(uQ, q, d3, lane, acc);
