@@ -1208,17 +1208,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   uint32_t *holder = reinterpret_cast<uint32_t *>(bar + 1);
   const uint32_t mb = smem_u32(bar);
 
-  load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-  load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-  if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
-  cp_async_commit();
-
   // a piece's share of this thread, read ahead: of tile `upper` of the two, key channels 8 NW quarter .. and
   // tokens 16 quarter .. + 15
   float4 fs[NW], f0[NW], f1[NW];
   float E[2][4], Z[2][4];
   uint32_t yv[2][2], vv[2][2];  // dy and v [n-tile][columns 0..7, 8..15]: a row's pair a lane
-  const auto read = [&](int c0) {
+  const auto read_states = [&](int c0) {
     const int ct = (c0 >> 4) + upper;
     const bool on = ct < tiles;
     const float4 *S = reinterpret_cast<const float4 *>(a.s) + ((u * tiles + ct) * NT + quarter * NW) * 32 + lane;
@@ -1231,6 +1226,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       f1[x] = on ? G1[x * 32] : zero;
       f0[x] = on ? G[x * 32] : zero;
     }
+  };
+  const auto read_tokens = [&](int c0) {
+    const int ct = (c0 >> 4) + upper;
+    const bool on = ct < tiles;
     const int64_t at = ((u * tiles + ct) * 8 + 2 * quarter) * 32;
     if (on) {
       get(reinterpret_cast<const float4 *>(a.e) + at, lane, E);
@@ -1248,7 +1247,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         vv[x][e] = load_pair(a.v + (tok + i) * a.ld_v + h * a.dv + cc, left, a.by_v >= 4);
       }
   };
-  read(0);
+  read_states(0);
+  load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+  load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
+  cp_async_commit();
+  read_tokens(0);
 
   if (tid == 0) {
     mbar_init(mb, 1);
@@ -1305,6 +1309,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         *reinterpret_cast<uint32_t *>(o + L::G + p * 8192 + 2048) = q1[p];
       }
     }
+    if (c0 + 32 < a.dv) read_states(c0 + 32);
     // ---- U, tail U, dZ, dy; dv; the sums over value columns
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -1345,7 +1350,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         }
       }
     }
-    if (c0 + 32 < a.dv) read(c0 + 32);
+    if (c0 + 32 < a.dv) read_tokens(c0 + 32);
     fence_async_smem();
     __syncthreads();
     if (tid == 0) {
