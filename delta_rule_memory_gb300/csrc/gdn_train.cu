@@ -25,19 +25,21 @@
 // (the first term only before the chunk's first reset, the sum from the document's start on).
 //
 // Kernels.  gdn_prep (every chunk by itself): the decays, T and M.  gdn_chain:
-// chunk after chunk, a warp owns 16 value columns and keeps S^T [16, dk] in its
-// accumulators; every product of a chunk takes the one before as its A operand
-// from registers (mma.cuh), so warps never wait for one another and only the chunk's
-// tiles, which are copied a chunk ahead, are shared.  gdn_chain_back: the same
-// with G, last chunk to first.  gdn_grad: everything that needs sums over the value columns,
-// every chunk by itself.
-// mma.sync and not tcgen05: a product here is 64 x 128 x 16..128 and feeds the next one; through tensor
-// memory each would be read back, split into bf16 parts and stored for the next,
-// which is what bounds the chunk form in gdn_chunk.cu (2.85 us a chunk).
+// chunk after chunk, three warps a tile of 16 value columns; every product of a
+// chunk takes the one before as its A operand from registers or as parts in shared memory
+// (mma.cuh), and the chunk's tiles are copied a chunk ahead.  gdn_chain_back: the same with G, last
+// chunk to first.  gdn_grad: everything that needs sums over the value columns, every
+// chunk by itself, on tcgen05.
+// The chains use mma.sync: a product there is 64 x 128 x 16 and feeds the next one, so through
+// tensor memory each would be read back, split into bf16 parts and stored before
+// the next could start, which is what bounds the chunk form in gdn_chunk.cu (2.85 us a chunk
+// for 64 columns, with two parts).
 //
 // Precision.  q, k, v and dy are exact in bf16.  What is not (S, G, T, M, Z, U, X) is taken in
-// three bf16 parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da, dbeta); in two parts,
-// 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
+// three bf16 parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da,
+// dbeta); in two parts, 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
+//
+// B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 86 us, gdn_chain 345, gdn_chain_back 397, gdn_grad 400.
 #include <cuda.h>
 
 #include <algorithm>
@@ -48,6 +50,9 @@
 #include "umma.cuh"
 
 namespace sdm {
+
+int test_drop_signal();  // gdn_chunk.cu: the SDM_TEST_DROP_SIGNAL test hook
+
 namespace {
 
 using namespace mma;
@@ -81,6 +86,7 @@ struct Gdn {
   float *dla, *dbeta;
   float *pdq, *pdk;            // [B,T,H,dk] where several heads share a key head
   int32_t *err;
+  int drop;                    // test hook: M is not asked for
 };
 
 // A triangle: 16 x 16 blocks row by row, each as four 8 x 8 of 8 rows of 16 bytes
@@ -124,13 +130,14 @@ struct Maps {
 };
 
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls (about 0.1 s) before a wait gives up
+constexpr uint32_t kShortLimit = 1u << 12;  // ... once one has: still far longer than a copy takes
 
 // Wait for a phase of copies.  One that gives up is reported and lets the
-// kernel run out, its later waits short.
+// kernel run to its end, its later waits short.
 __device__ __forceinline__ void wait_copies(uint64_t *bar, uint32_t parity, uint32_t &limit, const Gdn &a) {
   if (!umma::mbar_wait(smem_u32(bar), parity, limit)) {
     report_timeout(a.err);
-    limit = 64;
+    limit = kShortLimit;
   }
 }
 
@@ -381,9 +388,11 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 // y, the products with dy, what is kept for later, copies.  A tile's state lives in shared
 // memory as its three bf16 parts, which are all 24 bits of it, in the order of the A
 // fragments that every product with it takes.
-// One warp a tile took 7.6 us a chunk at dk = dv = 128, a second one for what can wait and
-// copies by TMA 3.6 (5.0 where four tiles share an SM's tensor cores); this form 
-// FIGURES
+// Bound by latency where a tile has an SM to itself (2.6 us a chunk forward, 3.4 backward at
+// dk = dv = 128; one warp a tile took 7.6 and 6.5, a second one for what can wait, with copies by TMA, 3.6 and 4.7).
+// Where four tiles share an SM (5.4 and 6.2 us a chunk) by shared memory, about 5,000 of 10,500 cycles, beside the
+// tensor cores, 5,500 cycles: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward
+// chain is a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
 template <int NK, int PM, int W>  // PM: parts of M
 struct Chain {
@@ -829,7 +838,7 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
     copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v, a.by_v, ltid);
   };
   const auto ask_m = [&](int c) {
-    if (ltid == 0) request_m<2>(sm + L::M, bars + 2, a, me.bh * a.n + c);
+    if (ltid == 0 && !a.drop) request_m<2>(sm + L::M, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(0);
@@ -1030,7 +1039,7 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
                          ltid);
   };
   const auto ask_m = [&](int c) {
-    if (ltid == 0) request_m<3>(sm + L::M, bars + 2, a, me.bh * a.n + c);
+    if (ltid == 0 && !a.drop) request_m<3>(sm + L::M, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(n - 1);
@@ -1122,7 +1131,10 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
 // operands, where a warp's store is 128 bytes in a row.  All operands have their rows
 // of 8 along M or N (MN-major); X and N serve both ways as they lie.
 // A CTA needs half of an SM's shared memory, registers and tensor memory, so that one's
-// conversions run beside the other's products.
+// conversions run beside the other's products.  A chunk's 320 KB are read and its 48 KB written at 3.7 TB/s;
+// what bounds it is the latency of each piece's loads, conversions and products in turn (29,000
+// cycles a chunk and SM, of them 12,000 of issue, 7,000 of products).  On mma.sync, with accumulators in registers and
+// one CTA an SM, it took 705 us in place of 400.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -1762,6 +1774,7 @@ extern "C" int gdn_train(const float *state, float *state_out, const uint16_t *q
   a.la = log_alpha; a.beta = beta; a.reset = reset; a.lens = lens;
   a.B = B; a.T = T; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv;
   a.state_in = state; a.state_out = state_out; a.y = y; a.err = dev_err;
+  a.drop = test_drop_signal();
   if (static_cast<int64_t>(B) * H > 0 && (!state_out || (T > 0 && !y))) return set_error(SDM_ERR_INVALID_ARG, "gdn_train: null pointer");
   const int rc = check_common("gdn_train", a, saved, saved_bytes, l);
   if (rc != SDM_OK) return rc;
@@ -1789,6 +1802,7 @@ extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16
   a.la = log_alpha; a.beta = beta; a.reset = reset; a.lens = lens;
   a.B = B; a.T = T; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv;
   a.state_in = dstate; a.state_out = dstate_out; a.err = dev_err;
+  a.drop = test_drop_signal();
   a.odq = dq; a.odk = dk_out; a.odv = dv_out; a.dla = dlog_alpha; a.dbeta = dbeta;
   if (static_cast<int64_t>(B) * H > 0 &&
       (!dstate_out || !workspace || (T > 0 && (!dy || !dq || !dk_out || !dv_out || !dlog_alpha || !dbeta))))

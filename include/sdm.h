@@ -60,8 +60,8 @@ extern "C" {
 #define SDM_ERR_DEVICE 6       /* sdm_check: a device-side error was recorded */
 
 /* Device-side error bits (OR-ed into *dev_err when dev_err != NULL). */
-#define SDM_DEVERR_INDEX_RANGE 1  /* a slot index outside [0, N) (skipped); a length of glr_scan outside [0, T] (clamped) */
-#define SDM_DEVERR_INDEX_REPEAT 2 /* a slot repeated within one token's write list */
+#define SDM_DEVERR_INDEX_RANGE 1  /* a slot index outside [0, N) (skipped), a partition of route_sort (dropped); a length outside [0, T] (clamped) */
+#define SDM_DEVERR_INDEX_REPEAT 2 /* a slot repeated within one token's write list, or within a gdn_step batch (skipped) */
 #define SDM_DEVERR_NONFINITE 4    /* a NaN or infinite score or logit; an 8-bit checkpoint group without codes */
 #define SDM_DEVERR_TIMEOUT 8      /* a bounded on-device wait gave up; outputs invalid */
 #define SDM_DEVERR_RATE 16        /* a decay rate of glr_scan below zero or not finite (taken as 0) */
@@ -85,8 +85,8 @@ extern "C" {
  *   SDM_SSE_PATH=recurrent|chunk    sse_scan: force the token-by-token or the
  *       chunked prefill path (shape rules permitting).
  *   SDM_TEST_DROP_SIGNAL=1          test hook: the chunked GDN, KDA, GDN2 and
- *       SSE chain kernels and the glr_scan kernels (where a sequence is split over a
- *       cluster) skip one internal signal, so a bounded on-device wait runs out
+ *       SSE chain kernels, those of gdn_train and gdn_backward, and the glr_scan kernels
+ *       (where a sequence is split over a cluster) skip one internal signal, so a bounded on-device wait runs out
  *       and the call reports SDM_DEVERR_TIMEOUT (its outputs are invalid; the
  *       CUDA context stays usable).  Never set in normal use.
  */
@@ -657,7 +657,7 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * saved     : gdn_train_saved_size() bytes, 16-byte aligned, written by
  *             gdn_train and read by gdn_backward with the same inputs and sizes: per
  *             64 tokens of a head their decays, two triangular matrices, the state
- *             and the residuals E (149 KB at dk = dv = 128).
+ *             and the residuals E (127.5 KB at dk = dv = 128).
  *
  * gdn_backward: dstate fp32 [B,H,dk,dv] = dL/dS_T (NULL: zero), dstate_out =
  * dL/dS_0 (may be dstate itself); dy bf16 [B,T,H,dv]; dq, dk, dv bf16 laid out
@@ -666,9 +666,11 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * or one another.  workspace : gdn_backward_workspace_size() bytes, 16-byte aligned; calls that
  * share one must not overlap on the GPU.
  *
+ * dev_err : optional; also SDM_DEVERR_TIMEOUT if a bounded wait gave up (outputs then invalid).
+ *
  * Both are deterministic.  Chunks of 64 tokens: one kernel for what a chunk
- * needs of itself, one that runs the chunks in order (16 value columns a warp, the state in its
- * registers), and in the backward one for the sums over value columns.  States, sums and
+ * needs of itself, one that runs the chunks in order (16 value columns to three warps), and in
+ * the backward one for the sums over value columns.  States, sums and
  * decays are fp32 (the sums of log_alpha wider); y, dq, dk and dv are rounded once, to nearest even.
  * NaN and infinities are not looked for: they spread over their chunk and the
  * tokens behind it (in the backward, before it).

@@ -264,6 +264,25 @@ def test_many_heads():
         check(c, c.run(sdm), *c.reference())
 
 
+@pytest.mark.parametrize("shape", [(1, 200, 1, 1, 128, 128), (3, 130, 1, 20, 64, 64)], ids=str)
+def test_a_wait_that_runs_out_is_reported(shape, monkeypatch):
+    """A copy that is never asked for: both calls end, report it, and the next ones are right."""
+    sdm = need_gpu()
+    c = Case(*shape, seed=40)
+    x = [*c.layout(c.q, c.k, c.v), *c.gates()]
+    _, saved = sdm.gdn_train(c.S0.cuda(), *x)
+    monkeypatch.setenv("SDM_TEST_DROP_SIGNAL", "1")
+    for call in (lambda e: sdm.gdn_train(c.S0.cuda(), *x, dev_err=e), lambda e: sdm.gdn_backward(c.dS.cuda(), *x, saved, c.dy.cuda(), dev_err=e)):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(err)
+        assert int(err) == sdm.SDM_DEVERR_TIMEOUT
+        with pytest.raises(sdm.SdmError):
+            sdm.sdm_check()
+    monkeypatch.delenv("SDM_TEST_DROP_SIGNAL")
+    check(c, c.run(sdm), *c.reference())
+    sdm.sdm_check()
+
+
 # ---- decoding ----
 
 @pytest.mark.parametrize("shape", [(1, 1, 1, 1, 1, 1), (3, 1, 2, 4, 128, 128), (2, 5, 2, 2, 100, 72), (4, 2, 1, 3, 64, 33),
