@@ -6,10 +6,12 @@
 // where y = e^a S^T q + beta (k . q) E, so both products with the state are taken of
 // the state before the token: one sum over the rows, and one barrier, a token.
 //
-// Bound by the state's bytes: read and written once a call, whatever T is.  A
-// CTA holds 32 columns of one head's state in registers: 8 lanes a row, 16 bytes each, 16
-// rows at a time (a column group of 32 makes 4 CTAs of a 128 x 128 state, so that one sequence's 16
-// heads already reach 64 SMs).
+// Bound by the state's bytes: read and written once a call, whatever T is (256
+// sequences of 16 heads of 128 x 128: 537 MB in 91 us, 87% of the measured copy bandwidth).  A
+// CTA holds 32 columns of one head's state in registers: 8 lanes a row, 16 bytes each, 16 rows at
+// a time.  A column group of 32 makes 4 CTAs of a 128 x 128 state, so that one sequence's 16
+// heads already reach 64 SMs; five CTAs an SM keep enough loads on their way (unbounded registers, 3 or 4 an SM: 113 us),
+// and nothing of the state is kept in the caches on its way through (cached: 107).
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -19,7 +21,7 @@
 namespace sdm {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 4 * kWarps;  // kRows: at a time
 constexpr int kCols = 32;
 
 struct StepArgs {
@@ -40,9 +42,9 @@ __device__ __forceinline__ float rows_sum(float x) {
 }
 
 template <int NR, bool VEC>  // NR: rows a thread
-__global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
-  __shared__ float part[2][4][2][kCols];  // token parity, warp, S^T k and S^T q
-  __shared__ float kq[2][4];
+__global__ void __launch_bounds__(kThreads, 5) gdn_step_kernel(const StepArgs a) {
+  __shared__ float part[2][kWarps][2][kCols];  // token parity, warp, S^T k and S^T q
+  __shared__ float kq[2][kWarps];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int64_t bh = blockIdx.x / a.groups;
   const int c0 = static_cast<int>(blockIdx.x - bh * a.groups) * kCols;
@@ -50,11 +52,8 @@ __global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
   int slot = b;
   if (a.slots) {
     slot = a.slots[b];
-    bool repeat = false;
-    for (int i = tid; i < b; i += kThreads) repeat |= a.slots[i] == slot;
-    repeat = __syncthreads_or(repeat) && slot >= 0;
-    if (slot < 0 || slot >= a.P || repeat) {  // the whole CTA
-      if (a.err && tid == 0 && slot >= 0) atomicOr(a.err, slot >= a.P ? SDM_DEVERR_INDEX_RANGE : SDM_DEVERR_INDEX_REPEAT);
+    if (slot < 0 || slot >= a.P) {  // the whole CTA
+      if (a.err && tid == 0 && slot >= 0) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
       return;
     }
   }
@@ -69,14 +68,22 @@ __global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
   float s[NR][4];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    const int r = r0 + 16 * i;
+    const int r = r0 + kRows * i;
     if (VEC) {
-      const float4 x = r < a.dk && c < a.dv ? *reinterpret_cast<const float4 *>(S + static_cast<int64_t>(r) * a.dv)
+      const float4 x = r < a.dk && c < a.dv ? __ldcs(reinterpret_cast<const float4 *>(S + static_cast<int64_t>(r) * a.dv))
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
       s[i][0] = x.x, s[i][1] = x.y, s[i][2] = x.z, s[i][3] = x.w;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[i][e] = r < a.dk && c + e < a.dv ? S[static_cast<int64_t>(r) * a.dv + e] : 0.f;
+    }
+  }
+  if (a.slots) {  // a slot that a sequence before this one names, looked for while the state is on its way
+    bool repeat = false;
+    for (int i = tid; i < b; i += kThreads) repeat |= a.slots[i] == slot;
+    if (__syncthreads_or(repeat)) {
+      if (a.err && tid == 0) atomicOr(a.err, SDM_DEVERR_INDEX_REPEAT);
+      return;
     }
   }
   for (int t = 0; t < T; ++t) {
@@ -85,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
     float k[NR], q[NR], v[4];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int r = r0 + 16 * i;
+      const int r = r0 + kRows * i;
       k[i] = r < a.dk ? bf16_to_f32(kp[r]) : 0.f;
       q[i] = r < a.dk ? bf16_to_f32(qp[r]) : 0.f;
     }
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
       pk[e] = rows_sum(pk[e]);
       pq[e] = rows_sum(pq[e]);
     }
-    float(&pt)[4][2][kCols] = part[t & 1];
+    float(&pt)[kWarps][2][kCols] = part[t & 1];
     if (lane < 8) {
       *reinterpret_cast<float4 *>(&pt[w][0][4 * lane]) = make_float4(pk[0], pk[1], pk[2], pk[3]);
       *reinterpret_cast<float4 *>(&pt[w][1][4 * lane]) = make_float4(pq[0], pq[1], pq[2], pq[3]);
@@ -117,14 +124,19 @@ __global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
     }
     __syncthreads();  // (the other parity's words are read up to the barrier before this one)
     float e4[4], y4[4];
-    dot = (kq[t & 1][0] + kq[t & 1][1]) + (kq[t & 1][2] + kq[t & 1][3]);
+    float p4[4] = {0.f, 0.f, 0.f, 0.f}, o4[4] = {0.f, 0.f, 0.f, 0.f};
+    dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      dot += kq[t & 1][i];
+      const float4 p = *reinterpret_cast<const float4 *>(&pt[i][0][4 * (lane & 7)]), o = *reinterpret_cast<const float4 *>(&pt[i][1][4 * (lane & 7)]);
+      p4[0] += p.x, p4[1] += p.y, p4[2] += p.z, p4[3] += p.w;
+      o4[0] += o.x, o4[1] += o.y, o4[2] += o.z, o4[3] += o.w;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int j = 4 * (lane & 7) + e;
-      const float p = (pt[0][0][j] + pt[1][0][j]) + (pt[2][0][j] + pt[3][0][j]);
-      const float o = (pt[0][1][j] + pt[1][1][j]) + (pt[2][1][j] + pt[3][1][j]);
-      e4[e] = beta * fmaf(-decay, p, v[e]);
-      y4[e] = fmaf(dot, e4[e], decay * o);
+      e4[e] = beta * fmaf(-decay, p4[e], v[e]);
+      y4[e] = fmaf(dot, e4[e], decay * o4[e]);
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i)
@@ -139,11 +151,11 @@ __global__ void __launch_bounds__(kThreads) gdn_step_kernel(const StepArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    const int r = r0 + 16 * i;
+    const int r = r0 + kRows * i;
     if (r >= a.dk) continue;
     if (VEC) {
       if (c < a.dv)
-        *reinterpret_cast<float4 *>(S + static_cast<int64_t>(r) * a.dv) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+        __stcs(reinterpret_cast<float4 *>(S + static_cast<int64_t>(r) * a.dv), make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -180,8 +192,8 @@ extern "C" int gdn_step(float *state, const uint16_t *q, int64_t ld_q, const uin
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool vec = dv % 4 == 0 && aligned(state, 16);
   if (dk <= 64)
-    vec ? gdn_step_kernel<4, true><<<grid, kThreads, 0, st>>>(a) : gdn_step_kernel<4, false><<<grid, kThreads, 0, st>>>(a);
+    vec ? gdn_step_kernel<64 / kRows, true><<<grid, kThreads, 0, st>>>(a) : gdn_step_kernel<64 / kRows, false><<<grid, kThreads, 0, st>>>(a);
   else
-    vec ? gdn_step_kernel<8, true><<<grid, kThreads, 0, st>>>(a) : gdn_step_kernel<8, false><<<grid, kThreads, 0, st>>>(a);
+    vec ? gdn_step_kernel<128 / kRows, true><<<grid, kThreads, 0, st>>>(a) : gdn_step_kernel<128 / kRows, false><<<grid, kThreads, 0, st>>>(a);
   return check_launch("gdn_step");
 }
