@@ -141,6 +141,13 @@ __device__ __forceinline__ void wait_copies(uint64_t *bar, uint32_t parity, uint
   }
 }
 
+// Before a kernel's first access to memory: the kernel before it in the stream
+// has ended and its results are there; the next one may be brought up.
+__device__ __forceinline__ void before_reading() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
 __device__ __forceinline__ int length_of(const Gdn &a, int b) {
   return a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
 }
@@ -270,7 +277,8 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x;
   const int64_t bh = u / a.n;
-  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  before_reading();
   const int live = min(length_of(a, b) - c * kC, kC);
   if (live <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.T + c * kC;
@@ -731,19 +739,20 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   using L = Chain<NK, 2, W>;
   constexpr int NT = 2 * NK, kOwn = 96 * W;  // kOwn: threads before the warp that asks for copies
   extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages, M
+  if (threadIdx.x == 0) {
+    umma::mbar_init(smem_u32(bars), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 2), 1);
+    umma::fence_mbar_init();
+  }
+  before_reading();
   const Place<W> me(a);
   const int tid = me.tid, w = me.w, lane = me.lane, g = lane >> 2, t = lane & 3, n = me.n, len = me.len, col = me.col, h = me.h;
   const int tiles = (a.dv + 15) >> 4;
   uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96, *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
   float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // half sums, then E
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);           // two stages, M
-  if (tid == 0) {
-    umma::mbar_init(smem_u32(bars), kAskers<W>);
-    umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
-    umma::mbar_init(smem_u32(bars + 2), 1);
-    umma::fence_mbar_init();
-    if (a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-  }
+  if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
   uint32_t limit = kWaitLimit;
   const int pair = 1 + w, three = 1 + W + w;  // barriers
@@ -930,6 +939,14 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   using L = Chain<NK, 3, W>;
   constexpr int NT = 2 * NK, kOwn = 96 * W;
   extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages, M
+  if (threadIdx.x == 0) {
+    umma::mbar_init(smem_u32(bars), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
+    umma::mbar_init(smem_u32(bars + 2), 1);
+    umma::fence_mbar_init();
+  }
+  before_reading();
   const Place<W> me(a);
   const int tid = me.tid, w = me.w, lane = me.lane, t = lane & 3, n = me.n, len = me.len, col = me.col, h = me.h;
   const int tiles = (a.dv + 15) >> 4;
@@ -937,14 +954,7 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96, *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
   float4 *hX = reinterpret_cast<float4 *>(hP);                           // half sums, before the parts
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
-  if (tid == 0) {
-    umma::mbar_init(smem_u32(bars), kAskers<W>);
-    umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
-    umma::mbar_init(smem_u32(bars + 2), 1);
-    umma::fence_mbar_init();
-    if (a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
-  }
+  if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
   uint32_t limit = kWaitLimit;
   const int pair = 1 + w, three = 1 + W + w, read = 1 + 2 * W + w, thirds = 1 + 3 * W;
@@ -1208,6 +1218,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   const int tid = threadIdx.x, w = tid >> 5, quarter = w & 3, upper = w >> 2, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x, bh = u / a.n;
   const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  before_reading();
   const int live = min(length_of(a, b) - c * kC, kC);
   if (live <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.T + c * kC, ld_y = static_cast<int64_t>(a.H) * a.dv;
@@ -1573,6 +1584,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
 __global__ void __launch_bounds__(256) gdn_grad_heads(const Gdn a) {
   const int group = a.H / a.Hk;
   const int64_t tok = blockIdx.x;
+  before_reading();
   if (static_cast<int>(tok % a.T) >= length_of(a, static_cast<int>(tok / a.T))) return;
   for (int i = threadIdx.x; i < a.Hk * a.dk; i += 256) {
     const int hk = i / a.dk, ch = i - hk * a.dk;
@@ -1690,12 +1702,25 @@ void place_saved(Gdn &a, void *saved, const Layout &l) {
   a.e = reinterpret_cast<float *>(p + l.e);
 }
 
-template <typename K>
-int launch(K kernel, const char *what, int64_t grid, int threads, int smem, const Gdn &a, const Maps &maps, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Every kernel here may be launched while the one before it in the stream still
+// runs (its own set-up then overlaps that one's end) and waits for it with before_reading().
+template <typename... A>
+int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
   if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  kernel<<<static_cast<unsigned>(grid), threads, smem, st>>>(a, maps);
-  return check_launch(what);
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(grid));
+  c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.dynamicSmemBytes = static_cast<size_t>(smem);
+  c.stream = st;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, kernel, args...);
+  if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return SDM_OK;
 }
 
 // Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its
@@ -1709,8 +1734,8 @@ int chain_width(const Gdn &a, const Layout &l) {
 template <int NK, int W>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
-  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 3, W>::size, a, maps, st)
-              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 2, W>::size, a, maps, st);
+  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 3, W>::size, st, a, maps)
+              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 2, W>::size, st, a, maps);
 }
 template <int NK>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
@@ -1725,7 +1750,7 @@ int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc != SDM_OK) return rc;
   if (l.units > 0) {
-    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + 32 * 36 + kScal) * 4 + 16, a, maps, st);
+    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + 32 * 36 + kScal) * 4 + 16, st, a, maps);
     if (rc != SDM_OK) return rc;
   }
   return run_chain<NK>(a, maps, l, false, st);
@@ -1737,13 +1762,9 @@ int run_backward(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc == SDM_OK) rc = run_chain<NK>(a, maps, l, true, st);
   if (rc != SDM_OK || l.units == 0) return rc;
-  const cudaError_t e = cudaFuncSetAttribute(gdn_grad<NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad::size);
-  if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "gdn_backward: %s", cudaGetErrorString(e));
-  gdn_grad<NK><<<static_cast<unsigned>(l.units), kGradThreads, Grad::size, st>>>(a);
-  rc = check_launch("gdn_backward");
+  rc = launch(gdn_grad<NK>, "gdn_backward", l.units, kGradThreads, Grad::size, st, a);
   if (rc != SDM_OK || !a.pdq) return rc;
-  gdn_grad_heads<<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T), 256, 0, st>>>(a);
-  return check_launch("gdn_backward");
+  return launch(gdn_grad_heads, "gdn_backward", static_cast<int64_t>(a.B) * a.T, 256, 0, st, a);
 }
 
 }  // namespace
