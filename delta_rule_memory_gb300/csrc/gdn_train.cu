@@ -1,13 +1,12 @@
-// gdn_train.cu - training of the gated delta rule: the chunked forward that
-// keeps what its backward needs, and the backward.
+// gdn_train.cu - training of the gated delta rule: the chunked forward that keeps what its backward needs, and
+// the backward.
 //
 // Per sequence and head, S [dk, dv]:
 //   S~ = e^{a_t} S (0 at a reset),  E_t = v_t - S~^T k_t,
 //   S_t = S~ + beta_t k_t E_t^T,    y_t = S_t^T q_t.
-// In a chunk of C = 64 tokens let l_i be the sum of the a's up to token i,
-// D_ij = e^{l_i - l_j} for j <= i in one document (else 0), gam_i = D from the
-// chunk's start (0 behind a reset), tail_j = D to its end.  With S the state at the
-// chunk's start, rows being tokens,
+// In a chunk of C = 64 tokens let l_i be the sum of the a's up to token i, D_ij = e^{l_i - l_j} for j <= i in
+// one document (else 0), gam_i = D from the chunk's start (0 behind a reset), tail_j = D to its end.  With S
+// the state at the chunk's start, rows being tokens,
 //   Z = V - gam K S,   E = T Z,   T = (I + strict(D o K K^T) diag(beta))^-1,
 //   U = beta E,   Y = gam Q S + M U,   M = D o Q K^T,
 //   S_end = gam_C S + K^T (tail U).
@@ -18,26 +17,23 @@
 //   X = D o dY U^T,   N = -strict(D) o dZ U^T,
 //   dQ = gam dY S^T + X K,
 //   dK = tail U G^T - gam dZ S^T + X^T Q + (N + N^T) K.
-// The decays' gradient needs no product of its own.  y and S_end are linear in
-// (S, V), so at every cut the gradient's inner product with the state behind it plus that with the
-// values to come is that of the outputs to come; with y_t . dy_t = q_t . dq_t:
+// The decays' gradient needs no product of its own.  y and S_end are linear in (S, V), so at every cut the
+// gradient's inner product with the state behind it plus that with the values to come is that of the outputs to
+// come; with y_t . dy_t = q_t . dq_t:
 //   da_t = <S, G_start> - sum over s < t of (q_s . dq_s - v_s . dv_s)
 // (the first term only before the chunk's first reset, the sum from the document's start on).
 //
-// Kernels.  gdn_prep (every chunk by itself): the decays, T and M.  gdn_chain:
-// chunk after chunk, three warps a tile of 16 value columns; every product of a
-// chunk takes the one before as its A operand from registers or as parts in shared memory
-// (mma.cuh), and the chunk's tiles are copied a chunk ahead.  gdn_chain_back: the same with G, last
-// chunk to first.  gdn_grad: everything that needs sums over the value columns, every
-// chunk by itself, on tcgen05.
-// The chains use mma.sync: a product there is 64 x 128 x 16 and feeds the next one, so through
-// tensor memory each would be read back, split into bf16 parts and stored before
-// the next could start, which is what bounds the chunk form in gdn_chunk.cu (2.85 us a chunk
-// for 64 columns, with two parts).
+// Kernels.  gdn_prep (every chunk by itself): the decays, T and M.  gdn_chain: chunk after chunk, three warps a
+// tile of 16 value columns; every product of a chunk takes the one before as its A operand from registers or as
+// parts in shared memory (mma.cuh), and the chunk's tiles are copied a chunk ahead.  gdn_chain_back: the same
+// with G, last chunk to first.  gdn_grad: everything that needs sums over the value columns, every chunk by
+// itself, on tcgen05. The chains use mma.sync: a product there is 64 x 128 x 16 and feeds the next one, so
+// through tensor memory each would be read back, split into bf16 parts and stored before the next could start,
+// which is what bounds the chunk form in gdn_chunk.cu (2.85 us a chunk for 64 columns, with two parts).
 //
-// Precision.  q, k, v and dy are exact in bf16.  What is not (S, G, T, M, Z, U, X) is taken in
-// three bf16 parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da,
-// dbeta); in two parts, 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
+// Precision.  q, k, v and dy are exact in bf16.  What is not (S, G, T, M, Z, U, X) is taken in three bf16
+// parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da, dbeta); in two parts,
+// 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
 //
 // B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 86 us, gdn_chain 345, gdn_chain_back 397, gdn_grad 400.
 #include <cuda.h>
@@ -123,8 +119,8 @@ __device__ __forceinline__ Wide running(Wide x, int lane) {
   return x;
 }
 
-// Tensor maps of q, k, v and dy as [token][head][channel], boxes of one panel;
-// set where rows can be copied by 16 bytes
+// Tensor maps of q, k, v and dy as [token][head][channel], boxes of one panel; set where rows can be copied by
+// 16 bytes
 struct Maps {
   CUtensorMap q, k, v, dy;
 };
@@ -132,8 +128,8 @@ struct Maps {
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls (about 0.1 s) before a wait gives up
 constexpr uint32_t kShortLimit = 1u << 12;  // ... once one has: still far longer than a copy takes
 
-// Wait for a phase of copies.  One that gives up is reported and lets the
-// kernel run to its end, its later waits short.
+// Wait for a phase of copies.  One that gives up is reported and lets the kernel run to its end, its later
+// waits short.
 __device__ __forceinline__ void wait_copies(uint64_t *bar, uint32_t parity, uint32_t &limit, const Gdn &a) {
   if (!umma::mbar_wait(smem_u32(bar), parity, limit)) {
     report_timeout(a.err);
@@ -141,8 +137,8 @@ __device__ __forceinline__ void wait_copies(uint64_t *bar, uint32_t parity, uint
   }
 }
 
-// Before a kernel's first access to memory: the kernel before it in the stream
-// has ended and its results are there; the next one may be brought up.
+// Before a kernel's first access to memory: the kernel before it in the stream has ended and its results are
+// there; the next one may be brought up.
 __device__ __forceinline__ void before_reading() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -205,9 +201,8 @@ __device__ __forceinline__ void strip(const float *a, int lda, const float *b, i
   }
 }
 
-// X = L^-1 for unit lower triangular L: the 16 x 16 diagonal blocks by
-// substitution (one a warp), then blocks joined two by two,
-// X21 = -X22 (L21 X11).  zt: 32 x 36 floats.
+// X = L^-1 for unit lower triangular L: the 16 x 16 diagonal blocks by substitution (one a warp), then blocks
+// joined two by two, X21 = -X22 (L21 X11).  zt: 32 x 36 floats.
 __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int tid) {
   const int w = tid >> 5, lane = tid & 31;
   if (lane < 16) {
@@ -235,7 +230,8 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
     *reinterpret_cast<float4 *>(z + r * 20 + c) = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
     __syncthreads();
     strip<1, 16>(X + (o + 16 + r) * kLd + o + 16, kLd, z + c, 20, acc);
-    *reinterpret_cast<float4 *>(X + (o + 16 + r) * kLd + o + c) = make_float4(-acc[0][0], -acc[0][1], -acc[0][2], -acc[0][3]);
+    *reinterpret_cast<float4 *>(X + (o + 16 + r) * kLd + o + c) = make_float4(-acc[0][0], -acc[0][1], -acc[0][2],
+        -acc[0][3]);
   }
   __syncthreads();
   {  // 32 -> 64
@@ -249,7 +245,8 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
     strip<2, 32>(X + (32 + r) * kLd + 32, kLd, zt + c, 36, acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float4 *>(X + (32 + r + i) * kLd + c) = make_float4(-acc[i][0], -acc[i][1], -acc[i][2], -acc[i][3]);
+      *reinterpret_cast<float4 *>(X + (32 + r + i) * kLd + c) = make_float4(-acc[i][0], -acc[i][1], -acc[i][2],
+          -acc[i][3]);
   }
   __syncthreads();
 }
@@ -277,7 +274,8 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x;
   const int64_t bh = u / a.n;
-  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H),
+      h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
   before_reading();
   const int live = min(length_of(a, b) - c * kC, kC);
   if (live <= 0) return;
@@ -296,8 +294,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
   }
   float *out = a.scal + u * kScal;
   if (w == 0) {
-    // l in units of log2, as two floats: a strong decay early in the chunk costs
-    // the later, weak ones nothing
+    // l in units of log2, as two floats: a strong decay early in the chunk costs the later, weak ones nothing
     Wide x[2];
     bool r[2];
     float be[2];
@@ -322,7 +319,8 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
       const Wide rest = end - x[i];
-      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(x[i].hi) : 0.f, seg[i] == last ? umma::ex2_approx(rest.hi) : 0.f,
+      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(x[i].hi) : 0.f, seg[i] == last ? umma::ex2_approx(rest.hi)
+          : 0.f,
                           be[i], x[i].hi, x[i].lo, __int_as_float(seg[i])};
 #pragma unroll
       for (int e = 0; e < 6; ++e) {
@@ -388,19 +386,17 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 }
 
 // ---------------------------------------------------------------------------
-// The chains.  A CTA has W tiles of 16 value columns of one head, each with three
-// warps.  Two do what the next chunk waits for, each with half of the key channels (the
-// sums with the state and its update) and with two of the four groups of 16 tokens (0
-// and 3, or 1 and 2, the same number of the triangle's blocks): sums over all channels and a
-// triangle's products meet in shared memory.  The third does everything else:
-// y, the products with dy, what is kept for later, copies.  A tile's state lives in shared
-// memory as its three bf16 parts, which are all 24 bits of it, in the order of the A
-// fragments that every product with it takes.
-// Bound by latency where a tile has an SM to itself (2.6 us a chunk forward, 3.4 backward at
-// dk = dv = 128; one warp a tile took 7.6 and 6.5, a second one for what can wait, with copies by TMA, 3.6 and 4.7).
-// Where four tiles share an SM (5.4 and 6.2 us a chunk) by shared memory, about 5,000 of 10,500 cycles, beside the
-// tensor cores, 5,500 cycles: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward
-// chain is a fifth slower, its instructions no longer at hand.
+// The chains.  A CTA has W tiles of 16 value columns of one head, each with three warps.  Two do what the next
+// chunk waits for, each with half of the key channels (the sums with the state and its update) and with two of
+// the four groups of 16 tokens (0 and 3, or 1 and 2, the same number of the triangle's blocks): sums over all
+// channels and a triangle's products meet in shared memory.  The third does everything else: y, the products
+// with dy, what is kept for later, copies.  A tile's state lives in shared memory as its three bf16 parts,
+// which are all 24 bits of it, in the order of the A fragments that every product with it takes. Bound by
+// latency where a tile has an SM to itself (2.6 us a chunk forward, 3.4 backward at dk = dv = 128; one warp a
+// tile took 7.6 and 6.5, a second one for what can wait, with copies by TMA, 3.6 and 4.7). Where four tiles
+// share an SM (5.4 and 6.2 us a chunk) by shared memory, about 5,000 of 10,500 cycles, beside the tensor cores,
+// 5,500 cycles: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward chain is
+// a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
 template <int NK, int PM, int W>  // PM: parts of M
 struct Chain {
@@ -408,21 +404,23 @@ struct Chain {
   static constexpr int K = 0, Q = K + P * kPanel, V = Q + P * kPanel, T = V + kPanel, sc = T + 3 * kTri,
                        stage = (sc + 3 * kC * 4 + 1023) / 1024 * 1024;
   // M is read early in a chunk only, so one place does
-  static constexpr int M = 2 * stage, state = M + PM * kTri, parts = state + W * NK * 3 * 512, tokens = parts + W * 4 * 3 * 512,
+  static constexpr int M = 2 * stage, state = M + PM * kTri, parts = state + W * NK * 3 * 512,
+      tokens = parts + W * 4 * 3 * 512,
                        bars = tokens + W * 8 * 512, size = bars + 32;
 };
 static_assert(Chain<8, 3, 4>::size <= kMaxSmem && Chain<8, 2, 4>::size <= kMaxSmem, "");
 
-// A chunk's tiles into a stage; cols: the value columns' tensor.  What tensor and
-// bulk copies bring is asked for by one lane of a warp of its own or, where a CTA
-// has four tiles and no room for another warp's registers, by one lane of each of
-// the second warps (a request holds its warp for a hundred cycles and more).
+// A chunk's tiles into a stage; cols: the value columns' tensor.  What tensor and bulk copies bring is asked
+// for by one lane of a warp of its own or, where a CTA has four tiles and no room for another warp's registers,
+// by one lane of each of the second warps (a request holds its warp for a hundred cycles and more).
 template <int W>
 constexpr int kAskers = W < 4 ? 1 : 4;
 
 template <int NK, int PM, int W>
-__device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps, int64_t u,
-                                              int64_t tok, int h, int col0, int by_cols, const CUtensorMap *cols_map, int who) {
+__device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps,
+    int64_t u,
+                                              int64_t tok, int h, int col0, int by_cols, const CUtensorMap *cols_map,
+                                                  int who) {
   using L = Chain<NK, PM, W>;
   constexpr bool all = kAskers<W> == 1;
   const uint32_t mb = smem_u32(bar);
@@ -462,7 +460,8 @@ __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int6
     load_tile<L::P, threads>(st + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
   }
   if (by_cols != 16)
-    load_tile<1, threads>(st + L::V, cols + tok * ld_cols + h * a.dv + from, ld_cols, live, min(64, a.dv - from), by_cols, tid);
+    load_tile<1, threads>(st + L::V, cols + tok * ld_cols + h * a.dv + from, ld_cols, live, min(64, a.dv - from),
+        by_cols, tid);
   cp_async_commit();
 }
 
@@ -480,7 +479,8 @@ __device__ __forceinline__ void clear_stage(unsigned char *st, const Gdn &a, int
 
 // S^T of 16 columns and 8 NT rows of a [dk][dv] matrix as an accumulator, and back
 template <int NT>
-__device__ __forceinline__ void read_state(const float *m, int row, int dk, int dv, int col, int lane, float (&S)[NT][4]) {
+__device__ __forceinline__ void read_state(const float *m, int row, int dk, int dv, int col, int lane,
+    float (&S)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -491,7 +491,8 @@ __device__ __forceinline__ void read_state(const float *m, int row, int dk, int 
     }
 }
 template <int NT>
-__device__ __forceinline__ void write_state(float *m, int row, int dk, int dv, int col, int lane, const float (&S)[NT][4]) {
+__device__ __forceinline__ void write_state(float *m, int row, int dk, int dv, int col, int lane,
+    const float (&S)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -552,11 +553,9 @@ __device__ __forceinline__ void scale_tokens(float (&x)[N][4], const float *f, i
   }
 }
 
-// d (the leading parts' product) and l (the others') += A B for n-tiles 2 np and
-// 2 np + 1, over the parts whose numbers sum up to less than max(PA, PB): what
-// the others hold is below the last bit kept.  The tensor cores cut sums off
-// where an addition would round; kept apart, the many small products do so
-// at their own size.
+// d (the leading parts' product) and l (the others') += A B for n-tiles 2 np and 2 np + 1, over the parts whose
+// numbers sum up to less than max(PA, PB): what the others hold is below the last bit kept.  The tensor cores
+// cut sums off where an addition would round; kept apart, the many small products do so at their own size.
 template <int PA, int PB, int N>
 __device__ __forceinline__ void products(float (&d)[N][4], float (&l)[N][4], int np, const uint32_t (&a)[PA][4],
                                          const uint32_t (&b)[PB][4]) {
@@ -579,8 +578,7 @@ __device__ __forceinline__ void add(float (&d)[N][4], const float (&l)[N][4]) {
     for (int e = 0; e < 4; ++e) d[i][e] += l[i][e];
 }
 
-// acc = A B for n-tiles 4 quad .. 4 quad + 3, B = tile[token][n] exact, over 64
-// tokens: the small parts first
+// acc = A B for n-tiles 4 quad .. 4 quad + 3, B = tile[token][n] exact, over 64 tokens: the small parts first
 __device__ __forceinline__ void quad_product(uint32_t tile, int quad, const uint32_t (&a)[4][3][4], int lane,
                                              float (&acc)[4][4]) {
   uint32_t r[4][2][4];
@@ -617,8 +615,8 @@ __device__ __forceinline__ void update_quad(uint4 *parts, int quad, int lane, fl
   }
 }
 
-// d = the product of N k-steps of the state with tile[token][key channel],
-// channels from k0 on; U of them unrolled
+// d = the product of N k-steps of the state with tile[token][key channel], channels from k0 on; U of them
+// unrolled
 template <int N, int U>
 __device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile, int k0, int lane, float (&d)[8][4]) {
   float l[8][4];
@@ -649,7 +647,8 @@ __device__ __forceinline__ void give_sums(float4 *m, int x, int lane, const floa
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int a = i < 2 ? i : i + 4, b = i + 2;  // n-tiles of groups 0 and 3, of 1 and 2
-    m[(x ? a : b) * 32 + lane] = x ? make_float4(d[a][0], d[a][1], d[a][2], d[a][3]) : make_float4(d[b][0], d[b][1], d[b][2], d[b][3]);
+    m[(x ? a : b) * 32 + lane] = x ? make_float4(d[a][0], d[a][1], d[a][2], d[a][3]) : make_float4(d[b][0], d[b][1],
+        d[b][2], d[b][3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) mine[i][e] = x ? d[b][e] : d[a][e];
   }
@@ -664,7 +663,8 @@ __device__ __forceinline__ void take_sums(const float4 *m, int x, int lane, floa
 }
 __device__ __forceinline__ void put_tiles(float4 *m, int x, int lane, const float (&mine)[4][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[tile_of(x, i) * 32 + lane] = make_float4(mine[i][0], mine[i][1], mine[i][2], mine[i][3]);
+  for (int i = 0; i < 4; ++i) m[tile_of(x, i) * 32 + lane] = make_float4(mine[i][0], mine[i][1], mine[i][2],
+      mine[i][3]);
 }
 __device__ __forceinline__ void put_groups(uint4 *parts, int x, int lane, const float (&mine)[4][4]) {
 #pragma unroll
@@ -693,7 +693,8 @@ __device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tr
       uint32_t a[3][4], r[3][4];
       get_parts(parts + ks * 96, lane, a);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) BACK ? tri_cols(tri + p * kTri, n, ks, lane, r[p]) : tri_rows(tri + p * kTri, n, ks, lane, r[p]);
+      for (int p = 0; p < 3; ++p) BACK ? tri_cols(tri + p * kTri, n, ks, lane, r[p]) : tri_rows(tri + p * kTri, n, ks,
+          lane, r[p]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         fma16816(m[j], a[1], r[1][2 * j], r[1][2 * j + 1]);
@@ -712,9 +713,11 @@ __device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tr
 }
 
 // a tile's first two warps (64 threads), or all three (96), meet
-__device__ __forceinline__ void meet(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void meet(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads)
+    : "memory"); }
 // ... or only tell the others that they are there
-__device__ __forceinline__ void arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id),
+    "r"(threads) : "memory"); }
 
 // where a warp of a chain stands
 template <int W>
@@ -735,7 +738,8 @@ struct Place {
 };
 
 template <int NK, int W>
-__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(const Gdn a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(const Gdn a,
+    const __grid_constant__ Maps maps) {
   using L = Chain<NK, 2, W>;
   constexpr int NT = 2 * NK, kOwn = 96 * W;  // kOwn: threads before the warp that asks for copies
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -748,9 +752,11 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   }
   before_reading();
   const Place<W> me(a);
-  const int tid = me.tid, w = me.w, lane = me.lane, g = lane >> 2, t = lane & 3, n = me.n, len = me.len, col = me.col, h = me.h;
+  const int tid = me.tid, w = me.w, lane = me.lane, g = lane >> 2, t = lane & 3, n = me.n, len = me.len, col = me.col,
+      h = me.h;
   const int tiles = (a.dv + 15) >> 4;
-  uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96, *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
+  uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96,
+      *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
   float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // half sums, then E
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
@@ -830,7 +836,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   const int ltid = tid - 64 * W;
   const auto request = [&](int c) {
     if (lane == 0)
-      request_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0, a.by_v,
+      request_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h,
+          me.col0, a.by_v,
                               &maps.v, w);
     __syncwarp();
   };
@@ -844,7 +851,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v, a.by_v, ltid);
+    copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v,
+        a.by_v, ltid);
   };
   const auto ask_m = [&](int c) {
     if (ltid == 0 && !a.drop) request_m<2>(sm + L::M, bars + 2, a, me.bh * a.n + c);
@@ -935,7 +943,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
 }
 
 template <int NK, int W>
-__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_back(const Gdn a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_back(const Gdn a,
+    const __grid_constant__ Maps maps) {
   using L = Chain<NK, 3, W>;
   constexpr int NT = 2 * NK, kOwn = 96 * W;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -951,7 +960,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   const int tid = me.tid, w = me.w, lane = me.lane, t = lane & 3, n = me.n, len = me.len, col = me.col, h = me.h;
   const int tiles = (a.dv + 15) >> 4;
   const int64_t ld_y = static_cast<int64_t>(a.H) * a.dv;
-  uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96, *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
+  uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96,
+      *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
   float4 *hX = reinterpret_cast<float4 *>(hP);                           // half sums, before the parts
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
@@ -967,7 +977,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
 #pragma unroll 1
     for (int ks = 0; ks < NK / 2; ++ks) {
       float y[2][4];
-      read_state<2>(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * NK * 8 + 16 * ks, a.dk, a.dv, col, lane, y);
+      read_state<2>(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * NK * 8 + 16 * ks, a.dk, a.dv, col,
+          lane, y);
       put_parts(own + ks * 96, lane, y[0], y[1]);
       if (me.mine) put(kept + n * step + ks * 64, lane, y);
     }
@@ -1031,7 +1042,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
     if (lane == 0)
-      request_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0, a.by_dy, &maps.dy, w);
+      request_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
+          a.by_dy, &maps.dy, w);
     __syncwarp();
   };
   if (tid >= kOwn) {
@@ -1045,7 +1057,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 3, W>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.dy, ld_y, a.by_dy,
+    copy_stage<NK, 3, W>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.dy,
+        ld_y, a.by_dy,
                          ltid);
   };
   const auto ask_m = [&](int c) {
@@ -1128,23 +1141,21 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
 }
 
 // ---------------------------------------------------------------------------
-// gdn_grad: the gradients of one chunk of one head, on the tcgen05 tensor cores.
-// Transposed, every sum over value columns has the key channels or two times
-// the tokens as its M = 128 and the tokens as N:
+// gdn_grad: the gradients of one chunk of one head, on the tcgen05 tensor cores. Transposed, every sum over
+// value columns has the key channels or two times the tokens as its M = 128 and the tokens as N:
 //   [dQ1 | dKa]^T [128 x 128] = S [dY | dZ]^T        dKb^T [128 x 64] = G (tail U)^T
 //   [X; N]        [128 x 64]  = [dY; dZ] U^T
 // and then, with X and N times their decays,
 //   dQ2^T = K^T X^T,   dKb^T += Q^T X + K^T (N^T + N),
 //   dQ = gam dQ1 + dQ2,   dK = dKb - gam dKa.
-// The value columns come 32 at a time: read as the chains left them (16 bytes a
-// lane, read ahead by a piece), split into bf16 parts and stored as the 8 x 8 cores of the
-// operands, where a warp's store is 128 bytes in a row.  All operands have their rows
-// of 8 along M or N (MN-major); X and N serve both ways as they lie.
-// A CTA needs half of an SM's shared memory, registers and tensor memory, so that one's
-// conversions run beside the other's products.  A chunk's 320 KB are read and its 48 KB written at 3.7 TB/s;
-// what bounds it is the latency of each piece's loads, conversions and products in turn (29,000
-// cycles a chunk and SM, of them 12,000 of issue, 7,000 of products).  On mma.sync, with accumulators in registers and
-// one CTA an SM, it took 705 us in place of 400.
+// The value columns come 32 at a time: read as the chains left them (16 bytes a lane, read ahead by a piece),
+// split into bf16 parts and stored as the 8 x 8 cores of the operands, where a warp's store is 128 bytes in a
+// row.  All operands have their rows of 8 along M or N (MN-major); X and N serve both ways as they lie. A CTA
+// needs half of an SM's shared memory, registers and tensor memory, so that one's conversions run beside the
+// other's products.  A chunk's 320 KB are read and its 48 KB written at 3.7 TB/s; what bounds it is the latency
+// of each piece's loads, conversions and products in turn (29,000 cycles a chunk and SM, of them 12,000 of
+// issue, 7,000 of products).  On mma.sync, with accumulators in registers and one CTA an SM, it took 705 us in
+// place of 400.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -1152,7 +1163,8 @@ struct Grad {
   // a core row of 8 value columns: 16 cores where M or N is 128, 8 where it is 64
   static constexpr int YZ = 0, Zl = YZ + 8192 /* zeros | the second part of dZ */, U = Zl + 8192, Ut = U + 3 * 4096,
                        S = Ut + 2 * 4096, G = S + 3 * 8192, K = G + 2 * 8192, Q = K + 16384, sc = Q + 16384,
-                       rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */, flow = rows + 4 * kC * 4 /* [4][64] */,
+                       rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */,
+                           flow = rows + 4 * kC * 4 /* [4][64] */,
                        red = flow + 4 * kC * 4, bars = red + 32, size = bars + 16;
   static constexpr int X = 0, N = X + 3 * 8192;  // once the value columns are done
   static constexpr uint32_t dQ1 = 0, dKa = 64, dKb = 128, XN = 192, dQ2 = 192, columns = 256;  // tensor memory
@@ -1160,7 +1172,8 @@ struct Grad {
 static_assert(2 * (Grad::size + 1024) <= 228 * 1024, "two CTAs an SM");
 
 // 64 rows of `width` bf16 as 8 x 8 cores [row / 8][column / 8], zeros from row `live` on
-__device__ __forceinline__ void load_cores(unsigned char *to, const uint16_t *src, int64_t ld, int live, int width, int by,
+__device__ __forceinline__ void load_cores(unsigned char *to, const uint16_t *src, int64_t ld, int live, int width,
+    int by,
                                            int tid) {
 #pragma unroll 4
   for (int i = 0; i < kC * 16 / kGradThreads; ++i) {
@@ -1215,9 +1228,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   using namespace umma;
   constexpr int NT = 2 * NK, NW = NT / 4;  // NW: 8-channel groups of the states a warp
   extern __shared__ __align__(1024) unsigned char sm[];
-  const int tid = threadIdx.x, w = tid >> 5, quarter = w & 3, upper = w >> 2, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, w = tid >> 5, quarter = w & 3, upper = w >> 2, lane = tid & 31, g = lane >> 2,
+      t = lane & 3;
   const int64_t u = blockIdx.x, bh = u / a.n;
-  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H),
+      h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
   before_reading();
   const int live = min(length_of(a, b) - c * kC, kC);
   if (live <= 0) return;
@@ -1306,7 +1321,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   };
   const uint32_t base = smem_u32(sm);
   // A and B with rows of 8 along M and N; N = 64 and 128
-  const uint32_t id64 = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16), id128 = idesc_bf16_f32(128, 128) | (1u << 15) | (1u << 16);
+  const uint32_t id64 = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16), id128 = idesc_bf16_f32(128,
+      128) | (1u << 15) | (1u << 16);
 
   float anchor = 0.f, ez[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, vz[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
   for (int c0 = 0; c0 < a.dv; c0 += 32) {
@@ -1337,10 +1353,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int nt = 2 * quarter + x;
-      const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t), tl = *reinterpret_cast<const float2 *>(tail + 8 * nt + 2 * t);
+      const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t),
+          tl = *reinterpret_cast<const float2 *>(tail + 8 * nt + 2 * t);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // columns 0..7 and 8..15 of the tile
-        const float e0 = E[x][2 * e], e1 = E[x][2 * e + 1], z0 = Z[x][2 * e], z1 = Z[x][2 * e + 1], u0 = be.x * e0, u1 = be.y * e1;
+        const float e0 = E[x][2 * e], e1 = E[x][2 * e + 1], z0 = Z[x][2 * e], z1 = Z[x][2 * e + 1], u0 = be.x * e0,
+            u1 = be.y * e1;
         uint32_t su[3], st[2], sz[2];
         split<3>(u0, u1, su);
         split<2>(tl.x * u0, tl.y * u1, st);
@@ -1453,7 +1471,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
 #pragma unroll
           for (int p = 0; p < 3; ++p)
             if (!(is_n && p == 2))
-              *reinterpret_cast<uint4 *>(o + (is_n ? L::N : L::X) + p * 8192) = make_uint4(s[0][p], s[1][p], s[2][p], s[3][p]);
+              *reinterpret_cast<uint4 *>(o + (is_n ? L::N : L::X) + p * 8192) = make_uint4(s[0][p], s[1][p], s[2][p],
+                  s[3][p]);
         }
       }
     }
@@ -1465,9 +1484,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       const uint32_t idk = idesc_bf16_f32(128, 64) | (1u << 15);  // B with rows of 8 along its sum
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128), q = smem_desc(base + L::Q + ks * 4096, 2048, 128);
-        const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024), xc = smem_desc(base + L::X + ks * 2048, 1024, 128);
-        const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024), nc = smem_desc(base + L::N + ks * 2048, 1024, 128);
+        const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128), q = smem_desc(base + L::Q + ks * 4096, 2048,
+            128);
+        const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024), xc = smem_desc(base + L::X + ks * 2048, 1024,
+            128);
+        const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024), nc = smem_desc(base + L::N + ks * 2048, 1024,
+            128);
 #pragma unroll
         for (int p = 0; p < 3; ++p) mma_bf16(tmem + L::dQ2, k, xr + 512 * p, idk, ks > 0 || p > 0);
 #pragma unroll
@@ -1580,22 +1602,38 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   }
 }
 
-// dq and dk of key heads that several value heads share, heads in order
+// dq and dk of key heads that several value heads share, heads in order; two channels a thread
 __global__ void __launch_bounds__(256) gdn_grad_heads(const Gdn a) {
-  const int group = a.H / a.Hk;
+  const int group = a.H / a.Hk, half = (a.dk + 1) / 2;
   const int64_t tok = blockIdx.x;
   before_reading();
   if (static_cast<int>(tok % a.T) >= length_of(a, static_cast<int>(tok / a.T))) return;
-  for (int i = threadIdx.x; i < a.Hk * a.dk; i += 256) {
-    const int hk = i / a.dk, ch = i - hk * a.dk;
-    const int64_t o = (tok * a.H + static_cast<int64_t>(hk) * group) * a.dk + ch;
-    float q = 0.f, k = 0.f;
+  const bool pairs = a.pair_qk;
+  for (int i = threadIdx.x; i < a.Hk * half; i += 256) {
+    const int hk = i / half, ch = 2 * (i - hk * half);
+    const int64_t from = (tok * a.H + static_cast<int64_t>(hk) * group) * a.dk + ch;
+    const bool two = ch + 1 < a.dk;
+    float2 q = make_float2(0.f, 0.f), k = q;
     for (int e = 0; e < group; ++e) {
-      q += a.pdq[o + static_cast<int64_t>(e) * a.dk];
-      k += a.pdk[o + static_cast<int64_t>(e) * a.dk];
+      const float *pq = a.pdq + from + static_cast<int64_t>(e) * a.dk,
+          *pk = a.pdk + from + static_cast<int64_t>(e) * a.dk;
+      if (pairs) {
+        const float2 x = *reinterpret_cast<const float2 *>(pq), y = *reinterpret_cast<const float2 *>(pk);
+        q.x += x.x, q.y += x.y, k.x += y.x, k.y += y.y;
+      } else {
+        q.x += pq[0], k.x += pk[0];
+        if (two) q.y += pq[1], k.y += pk[1];
+      }
     }
-    a.odq[tok * a.ld_dq + i] = static_cast<uint16_t>(pack2(q, 0.f));
-    a.odk[tok * a.ld_dk + i] = static_cast<uint16_t>(pack2(k, 0.f));
+    const uint32_t vq = pack2(q.x, q.y), vk = pack2(k.x, k.y);
+    uint16_t *oq = a.odq + tok * a.ld_dq + hk * a.dk + ch, *ok = a.odk + tok * a.ld_dk + hk * a.dk + ch;
+    if (pairs) {
+      *reinterpret_cast<uint32_t *>(oq) = vq;
+      *reinterpret_cast<uint32_t *>(ok) = vk;
+    } else {
+      oq[0] = static_cast<uint16_t>(vq), ok[0] = static_cast<uint16_t>(vk);
+      if (two) oq[1] = static_cast<uint16_t>(vq >> 16), ok[1] = static_cast<uint16_t>(vk >> 16);
+    }
   }
 }
 
@@ -1609,7 +1647,8 @@ struct Layout {
 };
 
 bool sizes_fit(int B, int T, int Hk, int H, int dk, int dv) {
-  return B >= 0 && T >= 0 && H >= 0 && Hk >= 0 && B < 65536 && H < 65536 && T < (1 << 30) && dk >= 1 && dk <= 128 && dv >= 1 &&
+  return B >= 0 && T >= 0 && H >= 0 && Hk >= 0 && B < 65536 && H < 65536 && T < (1 << 30) && dk >= 1 && dk <= 128 &&
+      dv >= 1 &&
          dv <= 1024 && (H == 0 || (Hk > 0 && H % Hk == 0)) &&
          static_cast<int64_t>(B) * H * ((T + kC - 1) / kC) * ((dv + 15) / 16) < INT_MAX &&
          static_cast<int64_t>(B) * H * ((dv + 15) / 16) < INT_MAX && static_cast<int64_t>(B) * T < INT_MAX;
@@ -1644,11 +1683,14 @@ int check_common(const char *what, const Gdn &a, const void *saved, size_t saved
     return set_error(SDM_ERR_INVALID_ARG, "%s: null pointer", what);
   if (a.ld_q < static_cast<int64_t>(a.Hk) * a.dk || a.ld_k < static_cast<int64_t>(a.Hk) * a.dk ||
       a.ld_v < static_cast<int64_t>(a.H) * a.dv || a.ld_q >= (1 << 27) || a.ld_k >= (1 << 27) || a.ld_v >= (1 << 27))
-    return set_error(SDM_ERR_SHAPE, "%s: a token's row must be at most 2^27 elements from the next and hold its heads", what);
+    return set_error(SDM_ERR_SHAPE, "%s: a token's row must be at most 2^27 elements from the next and hold its heads",
+        what);
   if (!aligned(a.q, 2) || !aligned(a.k, 2) || !aligned(a.v, 2) || !aligned(a.la, 4) || !aligned(a.beta, 4) ||
-      !aligned(a.lens, 4) || !aligned(a.err, 4) || !aligned(a.state_in, 4) || !aligned(a.state_out, 4) || !aligned(saved, 16))
+      !aligned(a.lens, 4) || !aligned(a.err, 4) || !aligned(a.state_in, 4) || !aligned(a.state_out, 4) ||
+          !aligned(saved, 16))
     return set_error(SDM_ERR_ALIGN, "%s: a pointer is not aligned", what);
-  if (saved_bytes < l.saved) return set_error(SDM_ERR_INVALID_ARG, "%s: saved holds %zu bytes, %zu needed", what, saved_bytes, l.saved);
+  if (saved_bytes < l.saved) return set_error(SDM_ERR_INVALID_ARG, "%s: saved holds %zu bytes, %zu needed", what,
+      saved_bytes, l.saved);
   return SDM_OK;
 }
 
@@ -1665,13 +1707,15 @@ int make_map(CUtensorMap *map, const void *p, int64_t ld, int64_t tokens, int he
   static const Encode encode = [] {
     void *f = nullptr;
     cudaDriverEntryPointQueryResult q;
-    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+        &q) == cudaSuccess &&
                    q == cudaDriverEntryPointSuccess
                ? reinterpret_cast<Encode>(f)
                : nullptr;
   }();
   if (!encode) return set_error(SDM_ERR_CUDA, "gdn_train: the driver has no cuTensorMapEncodeTiled");
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+      static_cast<cuuint64_t>(tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
   const cuuint32_t box[3] = {64, 1, kC}, steps[3] = {1, 1, 1};
   if (encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, steps,
@@ -1688,7 +1732,8 @@ int make_maps(Maps *m, const Gdn &a) {
   if (a.by_qk == 16) rc = make_map(&m->q, a.q, a.ld_q, tokens, a.Hk, a.dk);
   if (rc == SDM_OK && a.by_qk == 16) rc = make_map(&m->k, a.k, a.ld_k, tokens, a.Hk, a.dk);
   if (rc == SDM_OK && a.by_v == 16) rc = make_map(&m->v, a.v, a.ld_v, tokens, a.H, a.dv);
-  if (rc == SDM_OK && a.dy && a.by_dy == 16) rc = make_map(&m->dy, a.dy, static_cast<int64_t>(a.H) * a.dv, tokens, a.H, a.dv);
+  if (rc == SDM_OK && a.dy && a.by_dy == 16) rc = make_map(&m->dy, a.dy, static_cast<int64_t>(a.H) * a.dv, tokens, a.H,
+      a.dv);
   return rc;
 }
 
@@ -1702,11 +1747,12 @@ void place_saved(Gdn &a, void *saved, const Layout &l) {
   a.e = reinterpret_cast<float *>(p + l.e);
 }
 
-// Every kernel here may be launched while the one before it in the stream still
-// runs (its own set-up then overlaps that one's end) and waits for it with before_reading().
+// Every kernel here may be launched while the one before it in the stream still runs (its own set-up then
+// overlaps that one's end) and waits for it with before_reading().
 template <typename... A>
 int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, int smem, cudaStream_t st, A... args) {
-  cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+  cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+      : cudaSuccess;
   if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1723,9 +1769,8 @@ int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, in
   return SDM_OK;
 }
 
-// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its
-// two warps then run on schedulers of their own), else two, else four, which share an SM's
-// tensor cores and the chunk's tiles.
+// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its two warps then run on
+// schedulers of their own), else two, else four, which share an SM's tensor cores and the chunk's tiles.
 int chain_width(const Gdn &a, const Layout &l) {
   const int64_t all = l.tiles * a.B * a.H;
   return all <= kSms || l.tiles == 1 ? 1 : all <= 2 * kSms || l.tiles == 2 ? 2 : 4;
@@ -1734,8 +1779,10 @@ int chain_width(const Gdn &a, const Layout &l) {
 template <int NK, int W>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
-  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 3, W>::size, st, a, maps)
-              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 2, W>::size, st, a, maps);
+  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 3, W>::size,
+      st, a, maps)
+              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 2, W>::size, st, a,
+                  maps);
 }
 template <int NK>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
@@ -1750,7 +1797,8 @@ int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc != SDM_OK) return rc;
   if (l.units > 0) {
-    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + 32 * 36 + kScal) * 4 + 16, st, a, maps);
+    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + 32 * 36 + kScal) * 4 + 16, st, a,
+        maps);
     if (rc != SDM_OK) return rc;
   }
   return run_chain<NK>(a, maps, l, false, st);
@@ -1796,7 +1844,8 @@ extern "C" int gdn_train(const float *state, float *state_out, const uint16_t *q
   a.B = B; a.T = T; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv;
   a.state_in = state; a.state_out = state_out; a.y = y; a.err = dev_err;
   a.drop = test_drop_signal();
-  if (static_cast<int64_t>(B) * H > 0 && (!state_out || (T > 0 && !y))) return set_error(SDM_ERR_INVALID_ARG, "gdn_train: null pointer");
+  if (static_cast<int64_t>(B) * H > 0 && (!state_out || (T > 0 && !y))) return set_error(SDM_ERR_INVALID_ARG,
+      "gdn_train: null pointer");
   const int rc = check_common("gdn_train", a, saved, saved_bytes, l);
   if (rc != SDM_OK) return rc;
   if (!aligned(y, 2)) return set_error(SDM_ERR_ALIGN, "gdn_train: a pointer is not aligned");
@@ -1805,13 +1854,15 @@ extern "C" int gdn_train(const float *state, float *state_out, const uint16_t *q
   a.by_v = row_bytes(v, ld_v, dv);
   a.pair_y = dv % 2 == 0 && aligned(y, 4);
   place_saved(a, saved, l);
-  return dk <= 64 ? run_train<4>(a, l, static_cast<cudaStream_t>(stream)) : run_train<8>(a, l, static_cast<cudaStream_t>(stream));
+  return dk <= 64 ? run_train<4>(a, l, static_cast<cudaStream_t>(stream)) : run_train<8>(a, l,
+      static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16_t *q, int64_t ld_q, const uint16_t *k,
                             int64_t ld_k, const uint16_t *v, int64_t ld_v, const float *log_alpha, const float *beta,
                             const uint8_t *reset, const int32_t *lens, const void *saved, size_t saved_bytes,
-                            const uint16_t *dy, int B, int T, int Hk, int H, int dk, int dv, uint16_t *dq, int64_t ld_dq,
+                            const uint16_t *dy, int B, int T, int Hk, int H, int dk, int dv, uint16_t *dq,
+                                int64_t ld_dq,
                             uint16_t *dk_out, int64_t ld_dk, uint16_t *dv_out, int64_t ld_dv, float *dlog_alpha,
                             float *dbeta, void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream) {
   if (B < 0 || T < 0 || Hk < 0 || H < 0) return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: negative size");
@@ -1830,9 +1881,11 @@ extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16
     return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: null pointer");
   const int rc = check_common("gdn_backward", a, saved, saved_bytes, l);
   if (rc != SDM_OK) return rc;
-  if (ld_dq < static_cast<int64_t>(Hk) * dk || ld_dk < static_cast<int64_t>(Hk) * dk || ld_dv < static_cast<int64_t>(H) * dv ||
+  if (ld_dq < static_cast<int64_t>(Hk) * dk || ld_dk < static_cast<int64_t>(Hk) * dk ||
+      ld_dv < static_cast<int64_t>(H) * dv ||
       ld_dq >= (1 << 27) || ld_dk >= (1 << 27) || ld_dv >= (1 << 27))
-    return set_error(SDM_ERR_SHAPE, "gdn_backward: a token's row must be at most 2^27 elements from the next and hold its heads");
+    return set_error(SDM_ERR_SHAPE,
+        "gdn_backward: a token's row must be at most 2^27 elements from the next and hold its heads");
   if (!aligned(dy, 2) || !aligned(dq, 2) || !aligned(dk_out, 2) || !aligned(dv_out, 2) || !aligned(dlog_alpha, 4) ||
       !aligned(dbeta, 4) || !aligned(workspace, 16))
     return set_error(SDM_ERR_ALIGN, "gdn_backward: a pointer is not aligned");

@@ -1,15 +1,13 @@
-// mma.cuh - warp-level bf16 matrix products (mma.sync m16n8k16, fp32 sums) on
-// shared-memory tiles, for chains whose operands stay in registers.
+// mma.cuh - warp-level bf16 matrix products (mma.sync m16n8k16, fp32 sums) on shared-memory tiles, for chains
+// whose operands stay in registers.
 //
-// A tile has 64 rows in panels of 64 columns, each panel row-major with rows of
-// 128 bytes and aligned to 1024; the 16-byte piece p of a panel's row r lies at
-// piece p ^ (r & 7), so the eight rows that one ldmatrix phase reads lie in
-// different banks (the layout that a tensor copy with the 128-byte swizzle writes).
+// A tile has 64 rows in panels of 64 columns, each panel row-major with rows of 128 bytes and aligned to 1024;
+// the 16-byte piece p of a panel's row r lies at piece p ^ (r & 7), so the eight rows that one ldmatrix phase
+// reads lie in different banks (the layout that a tensor copy with the 128-byte swizzle writes).
 //
-// Fragments (g = lane / 4, t = lane % 4): the accumulator of an m16n8 product
-// holds rows g and g + 8, columns 2t and 2t + 1.  Two neighbouring ones are, as
-// they stand, the A fragment of a k = 16 step, so a product's result feeds the
-// next product without leaving the registers.
+// Fragments (g = lane / 4, t = lane % 4): the accumulator of an m16n8 product holds rows g and g + 8, columns
+// 2t and 2t + 1.  Two neighbouring ones are, as they stand, the A fragment of a k = 16 step, so a product's
+// result feeds the next product without leaving the registers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -39,8 +37,8 @@ __device__ __forceinline__ void ldsm4_t(uint32_t saddr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// B fragments of two n-tiles (n0 .. n0+15) and one k-step from tile[n][k]:
-// r[0], r[1] of the first, r[2], r[3] of the second
+// B fragments of two n-tiles (n0 .. n0+15) and one k-step from tile[n][k]: r[0], r[1] of the first, r[2], r[3]
+// of the second
 __device__ __forceinline__ void b_rows(uint32_t tile, int n0, int k0, int lane, uint32_t (&r)[4]) {
   ldsm4(tile + piece(n0 + ((lane >> 4) << 3) + (lane & 7), (k0 >> 3) + ((lane >> 3) & 1)), r);
 }
@@ -72,8 +70,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float low2(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high2(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// x = s[0] + s[1] + ... in bf16, each the rounding of what the ones before
-// leave: two parts keep 16 bits of x, three keep all 24 (to 2^-26 relative).
+// x = s[0] + s[1] + ... in bf16, each the rounding of what the ones before leave: two parts keep 16 bits of x,
+// three keep all 24 (to 2^-26 relative).
 template <int N>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&s)[N]) {
 #pragma unroll
@@ -86,8 +84,8 @@ __device__ __forceinline__ void split(float x0, float x1, uint32_t (&s)[N]) {
   }
 }
 
-// The A fragments, in N parts, of one k-step of an accumulator's columns: c0
-// and c1 are its n-tiles 2 ks and 2 ks + 1.  a[part][register].
+// The A fragments, in N parts, of one k-step of an accumulator's columns: c0 and c1 are its n-tiles 2 ks and 2
+// ks + 1.  a[part][register].
 template <int N>
 __device__ __forceinline__ void a_split(const float (&c0)[4], const float (&c1)[4], uint32_t (&a)[N][4]) {
   uint32_t s[N];
@@ -109,8 +107,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return d;
 }
 
-// BYTES (4, 8 or 16) global -> shared, asynchronously; zeros where `live` is
-// false (src then only has to be a valid address)
+// BYTES (4, 8 or 16) global -> shared, asynchronously; zeros where `live` is false (src then only has to be a
+// valid address)
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool live) {
   const int n = live ? BYTES : 0;
@@ -133,11 +131,9 @@ __device__ __forceinline__ void load_tile_by(unsigned char *tile, const uint16_t
   }
 }
 
-// 64 rows of `width` bf16 (row r at src + r * ld) into a tile, zeros behind
-// `width` and from row `live` on, by THREADS threads (a power of two).  bytes:
-// what divides the address, the distance and the width of every row (8 or 4:
-// asynchronous copies of that size; else by elements).  Where it is 16, a
-// tensor copy does the same.
+// 64 rows of `width` bf16 (row r at src + r * ld) into a tile, zeros behind `width` and from row `live` on, by
+// THREADS threads (a power of two).  bytes: what divides the address, the distance and the width of every row
+// (8 or 4: asynchronous copies of that size; else by elements).  Where it is 16, a tensor copy does the same.
 template <int PANELS, int THREADS>
 __device__ __forceinline__ void load_tile(unsigned char *tile, const uint16_t *src, int64_t ld, int live, int width,
                                           int bytes, int tid) {
@@ -168,9 +164,10 @@ __device__ __forceinline__ void clear_rows(unsigned char *tile, int live, int ti
     *reinterpret_cast<uint4 *>(tile + piece(id / (PANELS * 8), id % (PANELS * 8))) = make_uint4(0, 0, 0, 0);
 }
 
-// a panel of a tensor map's [token][head][channel] (box: 64 tokens, one head, 64
-// channels), by one thread; completes its 8 KB on the mbarrier.  channel: a multiple of 64
-__device__ __forceinline__ void tensor_panel(uint32_t dst, const void *map, int channel, int head, int token, uint32_t mbar) {
+// a panel of a tensor map's [token][head][channel] (box: 64 tokens, one head, 64 channels), by one thread;
+// completes its 8 KB on the mbarrier.  channel: a multiple of 64
+__device__ __forceinline__ void tensor_panel(uint32_t dst, const void *map, int channel, int head, int token,
+    uint32_t mbar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
           dst),

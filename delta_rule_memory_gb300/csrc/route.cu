@@ -1,15 +1,13 @@
 // route.cu - visits sorted by partition and back.
 //
-// Token m of M makes k visits, visit m k + r to partition sel[m, r].  A stable
-// counting sort gives each visit its place in the partition-sorted order;
-// gather copies every token's row to its visits' places (the partitions'
-// inputs), combine sums the rows at a token's places times its weights (the
-// partitions' outputs).  Either is the other's transpose: gather's gradient is
-// combine without weights, combine's is a weighted gather and a dot product a
-// visit.  Every sum is formed in a fixed order in fp32: no atomics.
+// Token m of M makes k visits, visit m k + r to partition sel[m, r].  A stable counting sort gives each visit
+// its place in the partition-sorted order; gather copies every token's row to its visits' places (the
+// partitions' inputs), combine sums the rows at a token's places times its weights (the partitions' outputs).
+// Either is the other's transpose: gather's gradient is combine without weights, combine's is a weighted gather
+// and a dot product a visit.  Every sum is formed in a fixed order in fp32: no atomics.
 //
-// All of them move bytes and nothing else.  A warp has a token: its row is
-// read (written) once and in whole lines, its places are k whole rows.
+// All of them move bytes and nothing else.  A warp has a token: its row is read (written) once and in whole
+// lines, its places are k whole rows.
 #include <climits>
 #include <initializer_list>
 
@@ -21,9 +19,8 @@ namespace sdm {
 namespace {
 
 // ---------------------------------------------------------------------------
-// The sort.  A block has kBlock visits, each of its warps a run of them, taken
-// 32 at a time: lanes of one partition find one another with match_any, their
-// order being the visits' own.
+// The sort.  A block has kBlock visits, each of its warps a run of them, taken 32 at a time: lanes of one
+// partition find one another with match_any, their order being the visits' own.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRun = 128, kBlock = kSortWarps * kRun;
 constexpr int kMaxParts = 1024;
@@ -311,10 +308,9 @@ __global__ void __launch_bounds__(kRowThreads) route_gather_kernel(const RowArgs
   clear_rest<BYTES>(a, pieces, t.first, t.step, lane);
 }
 
-// A row at a time, so that a thread needs few registers and an SM holds many
-// warps, and reads that leave no trace in the caches (nothing is read twice):
-// 16,384 x 4 rows of 3,840 bf16 in 101 us, 92% of the measured copy bandwidth, where
-// four rows at a time took 133 and cached reads of two rows 182
+// A row at a time, so that a thread needs few registers and an SM holds many warps, and reads that leave no
+// trace in the caches (nothing is read twice): 16,384 x 4 rows of 3,840 bf16 in 101 us, 92% of the measured
+// copy bandwidth, where four rows at a time took 133 and cached reads of two rows 182
 template <typename T, int BYTES>
 __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const RowArgs a) {
   using R = typename Raw<BYTES>::type;
@@ -363,7 +359,8 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_back_kernel(const R
   using P = Piece<T, BYTES>;
   constexpr int U = 2;
   const int lane = threadIdx.x & 31, pieces = a.D / P::n;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = static_cast<int64_t>(gridDim.x) * kRowWarps;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5),
+      warps = static_cast<int64_t>(gridDim.x) * kRowWarps;
   for (int64_t m = warp; m < a.M; m += warps) {
     const int at = place_of(a, m, lane);
     const float wt = lane < a.k ? a.w[m * a.k + lane] : 0.f;
@@ -388,7 +385,8 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_back_kernel(const R
         for (int r = 0; r < V; ++r)
 #pragma unroll
           for (int i = 0; i < U; ++i)
-            if (j[r] >= 0 && c + 32 * i < pieces) v[r][i] = (static_cast<const R *>(a.rows) + j[r] * pieces)[c + 32 * i];
+            if (j[r] >= 0 &&
+                c + 32 * i < pieces) v[r][i] = (static_cast<const R *>(a.rows) + j[r] * pieces)[c + 32 * i];
 #pragma unroll
         for (int r = 0; r < V; ++r)
 #pragma unroll
@@ -433,10 +431,12 @@ unsigned row_grid(int64_t items) {
 
 int check_rows(const char *what, int dtype, int64_t M, int k, int N, int D, int64_t ld) {
   if (M < 0 || k < 0 || N < 0 || D < 0) return set_error(SDM_ERR_INVALID_ARG, "%s: negative size", what);
-  if (dtype != SDM_DTYPE_F32 && dtype != SDM_DTYPE_BF16) return set_error(SDM_ERR_UNSUPPORTED, "%s: unknown dtype", what);
+  if (dtype != SDM_DTYPE_F32 && dtype != SDM_DTYPE_BF16) return set_error(SDM_ERR_UNSUPPORTED, "%s: unknown dtype",
+      what);
   if (k > 32 || N > kMaxParts || M >= (1ll << 31) || M * k >= (1ll << 31) - kBlock || D >= (1 << 24))
     return set_error(SDM_ERR_SHAPE, "%s: need k <= 32, N <= %d, M k < 2^31 - 4096, D < 2^24", what, kMaxParts);
-  if (ld < D || ld >= (1 << 27)) return set_error(SDM_ERR_SHAPE, "%s: rows must be at least D and less than 2^27 elements apart", what);
+  if (ld < D || ld >= (1 << 27)) return set_error(SDM_ERR_SHAPE,
+      "%s: rows must be at least D and less than 2^27 elements apart", what);
   return SDM_OK;
 }
 
@@ -455,20 +455,24 @@ extern "C" int route_sort(const int32_t *sel, int64_t M, int k, int N, int32_t *
                           void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream) {
   const int rc = check_rows("route_sort", SDM_DTYPE_F32, M, k, N, 0, 0);
   if (rc != SDM_OK) return rc;
-  if (!offsets || (M * k > 0 && (!sel || !order || !place))) return set_error(SDM_ERR_INVALID_ARG, "route_sort: null pointer");
+  if (!offsets || (M * k > 0 && (!sel || !order || !place))) return set_error(SDM_ERR_INVALID_ARG,
+      "route_sort: null pointer");
   const size_t need = route_sort_workspace_size(M, k, N);
   if (need && (!workspace || workspace_bytes < need))
     return set_error(SDM_ERR_INVALID_ARG, "route_sort: workspace of %zu bytes needed", need);
-  if (!aligned(sel, 4) || !aligned(order, 4) || !aligned(place, 4) || !aligned(offsets, 4) || !aligned(workspace, 4) || !aligned(dev_err, 4))
+  if (!aligned(sel, 4) || !aligned(order, 4) || !aligned(place, 4) || !aligned(offsets, 4) || !aligned(workspace, 4) ||
+      !aligned(dev_err, 4))
     return set_error(SDM_ERR_ALIGN, "route_sort: a pointer is not aligned");
-  SortArgs a{sel, M * k, N, static_cast<int>((M * k + kBlock - 1) / kBlock), order, place, offsets, static_cast<int32_t *>(workspace), dev_err, 0};
+  SortArgs a{sel, M * k, N, static_cast<int>((M * k + kBlock - 1) / kBlock), order, place, offsets,
+      static_cast<int32_t *>(workspace), dev_err, 0};
   if (a.blocks < 1) a.blocks = 1;
   a.sum_here = static_cast<int64_t>(a.blocks) * N <= kSumHere;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int hist = kSortWarps * N * 4, smem = hist + (2 * N + 1) * 4;
   if (smem > 48 << 10)  // the limit is the kernel's, the same in every call
     for (const void *f : {reinterpret_cast<const void *>(route_count), reinterpret_cast<const void *>(route_place)}) {
-      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps * kMaxParts + 2 * kMaxParts + 1) * 4);
+      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          (kSortWarps * kMaxParts + 2 * kMaxParts + 1) * 4);
       if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "route_sort: %s", cudaGetErrorString(e));
     }
   if (a.blocks > 1 && N > 0) {
@@ -491,14 +495,16 @@ void by_type(int dtype, int bytes, F f) {
   if (dtype == SDM_DTYPE_F32)
     bytes == 16 ? f(0.f, Tag<16>()) : bytes == 8 ? f(0.f, Tag<8>()) : f(0.f, Tag<4>());
   else
-    bytes == 16 ? f(uint16_t(0), Tag<16>()) : bytes == 8 ? f(uint16_t(0), Tag<8>()) : bytes == 4 ? f(uint16_t(0), Tag<4>()) : f(uint16_t(0), Tag<2>());
+    bytes == 16 ? f(uint16_t(0), Tag<16>()) : bytes == 8 ? f(uint16_t(0), Tag<8>()) : bytes == 4 ? f(uint16_t(0),
+        Tag<4>()) : f(uint16_t(0), Tag<2>());
 }
 // items of M rows in stretches of 32 u pieces
 int64_t items(int64_t M, int D, int es, int bytes, int u) { return M * ((D / (bytes / es) + 32 * u - 1) / (32 * u)); }
 
 }  // namespace
 
-extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_t *place, const int32_t *offsets, int64_t M,
+extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_t *place, const int32_t *offsets,
+    int64_t M,
                             int k, int N, int D, void *rows, void *stream) {
   const int rc = check_rows("route_gather", dtype, M, k, N, D, ld_x);
   if (rc != SDM_OK) return rc;
@@ -511,7 +517,8 @@ extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bytes = piece_bytes(es, D, ld_x, {x, rows});
   by_type(dtype, bytes, [&](auto e, auto n) {
-    route_gather_kernel<n.value, sizeof e><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0, st>>>(a);
+    route_gather_kernel<n.value, sizeof e><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0,
+        st>>>(a);
   });
   return check_launch("route_gather");
 }
@@ -528,13 +535,15 @@ extern "C" int route_combine(const void *rows, int dtype, const int32_t *place, 
   RowArgs a{nullptr, rows, y, D, place, nullptr, w, nullptr, M, k, 0, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_type(dtype, piece_bytes(es, D, D, {rows, y}), [&](auto e, auto n) {
-    route_combine_kernel<decltype(e), n.value><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0, st>>>(a);
+    route_combine_kernel<decltype(e), n.value><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0,
+        st>>>(a);
   });
   return check_launch("route_combine");
 }
 
 extern "C" int route_combine_backward(const void *dy, int64_t ld_dy, int dtype, const void *rows, const int32_t *place,
-                                      const float *w, const int32_t *offsets, int64_t M, int k, int N, int D, void *drows,
+                                      const float *w, const int32_t *offsets, int64_t M, int k, int N, int D,
+                                          void *drows,
                                       float *dw, void *stream) {
   const int rc = check_rows("route_combine_backward", dtype, M, k, N, D, ld_dy);
   if (rc != SDM_OK) return rc;

@@ -60,8 +60,8 @@ extern "C" {
 #define SDM_ERR_DEVICE 6       /* sdm_check: a device-side error was recorded */
 
 /* Device-side error bits (OR-ed into *dev_err when dev_err != NULL). */
-#define SDM_DEVERR_INDEX_RANGE 1  /* a slot index outside [0, N) (skipped), a partition of route_sort (dropped); a length outside [0, T] (clamped) */
-#define SDM_DEVERR_INDEX_REPEAT 2 /* a slot repeated within one token's write list, or within a gdn_step batch (skipped) */
+#define SDM_DEVERR_INDEX_RANGE 1  /* a slot or partition outside [0, N) (skipped); a length outside [0, T] (clamped) */
+#define SDM_DEVERR_INDEX_REPEAT 2 /* a slot repeated within a token's write list or a gdn_step batch */
 #define SDM_DEVERR_NONFINITE 4    /* a NaN or infinite score or logit; an 8-bit checkpoint group without codes */
 #define SDM_DEVERR_TIMEOUT 8      /* a bounded on-device wait gave up; outputs invalid */
 #define SDM_DEVERR_RATE 16        /* a decay rate of glr_scan below zero or not finite (taken as 0) */
