@@ -230,8 +230,8 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
     *reinterpret_cast<float4 *>(z + r * 20 + c) = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
     __syncthreads();
     strip<1, 16>(X + (o + 16 + r) * kLd + o + 16, kLd, z + c, 20, acc);
-    *reinterpret_cast<float4 *>(X + (o + 16 + r) * kLd + o + c) = make_float4(-acc[0][0], -acc[0][1], -acc[0][2],
-        -acc[0][3]);
+    *reinterpret_cast<float4 *>(X + (o + 16 + r) * kLd + o + c) =
+        make_float4(-acc[0][0], -acc[0][1], -acc[0][2], -acc[0][3]);
   }
   __syncthreads();
   {  // 32 -> 64
@@ -245,8 +245,8 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
     strip<2, 32>(X + (32 + r) * kLd + 32, kLd, zt + c, 36, acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float4 *>(X + (32 + r + i) * kLd + c) = make_float4(-acc[i][0], -acc[i][1], -acc[i][2],
-          -acc[i][3]);
+      *reinterpret_cast<float4 *>(X + (32 + r + i) * kLd + c) =
+          make_float4(-acc[i][0], -acc[i][1], -acc[i][2], -acc[i][3]);
   }
   __syncthreads();
 }
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
       const Wide rest = end - x[i];
-      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(x[i].hi) : 0.f, seg[i] == last ? umma::ex2_approx(rest.hi)
-          : 0.f,
+      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(x[i].hi) : 0.f,
+                          seg[i] == last ? umma::ex2_approx(rest.hi) : 0.f,
                           be[i], x[i].hi, x[i].lo, __int_as_float(seg[i])};
 #pragma unroll
       for (int e = 0; e < 6; ++e) {
@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 // which are all 24 bits of it, in the order of the A fragments that every product with it takes. Bound by
 // latency where a tile has an SM to itself (2.6 us a chunk forward, 3.4 backward at dk = dv = 128; one warp a
 // tile took 7.6 and 6.5, a second one for what can wait, with copies by TMA, 3.6 and 4.7). Where four tiles
-// share an SM (5.4 and 6.2 us a chunk) by shared memory, about 5,000 of 10,500 cycles, beside the tensor cores,
-// 5,500 cycles: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward chain is
+// share an SM (5.4 and 6.2 us a chunk) by shared memory and the tensor cores beside each other, about 5,900 of
+// 10,500 cycles each: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward chain is
 // a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
 template <int NK, int PM, int W>  // PM: parts of M
@@ -418,9 +418,8 @@ constexpr int kAskers = W < 4 ? 1 : 4;
 
 template <int NK, int PM, int W>
 __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps,
-    int64_t u,
-                                              int64_t tok, int h, int col0, int by_cols, const CUtensorMap *cols_map,
-                                                  int who) {
+                                              int64_t u, int64_t tok, int h, int col0, int by_cols,
+                                              const CUtensorMap *cols_map, int who) {
   using L = Chain<NK, PM, W>;
   constexpr bool all = kAskers<W> == 1;
   const uint32_t mb = smem_u32(bar);
@@ -1153,8 +1152,8 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
 // row.  All operands have their rows of 8 along M or N (MN-major); X and N serve both ways as they lie. A CTA
 // needs half of an SM's shared memory, registers and tensor memory, so that one's conversions run beside the
 // other's products.  A chunk's 320 KB are read and its 48 KB written at 3.7 TB/s; what bounds it is the latency
-// of each piece's loads, conversions and products in turn (29,000 cycles a chunk and SM, of them 12,000 of
-// issue, 7,000 of products).  On mma.sync, with accumulators in registers and one CTA an SM, it took 705 us in
+// of each piece's loads, conversions and products in turn (29,000 cycles a chunk and SM, of them 10,500
+// of issue, 4,000 of products).  On mma.sync, with accumulators in registers and one CTA an SM, it took 705 us in
 // place of 400.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
@@ -1164,8 +1163,7 @@ struct Grad {
   static constexpr int YZ = 0, Zl = YZ + 8192 /* zeros | the second part of dZ */, U = Zl + 8192, Ut = U + 3 * 4096,
                        S = Ut + 2 * 4096, G = S + 3 * 8192, K = G + 2 * 8192, Q = K + 16384, sc = Q + 16384,
                        rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */,
-                           flow = rows + 4 * kC * 4 /* [4][64] */,
-                       red = flow + 4 * kC * 4, bars = red + 32, size = bars + 16;
+                       flow = rows + 4 * kC * 4 /* [4][64] */, red = flow + 4 * kC * 4, bars = red + 32, size = bars + 16;
   static constexpr int X = 0, N = X + 3 * 8192;  // once the value columns are done
   static constexpr uint32_t dQ1 = 0, dKa = 64, dKb = 128, XN = 192, dQ2 = 192, columns = 256;  // tensor memory
 };
@@ -1255,7 +1253,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     const int ct = (c0 >> 4) + upper;
     const bool on = ct < tiles;
     const float4 *S = reinterpret_cast<const float4 *>(a.s) + ((u * tiles + ct) * NT + quarter * NW) * 32 + lane;
-    const float4 *G = reinterpret_cast<const float4 *>(a.g) + (((bh * (a.n + 1) + c) * tiles + ct) * NT + quarter * NW) * 32 + lane;
+    const float4 *G = reinterpret_cast<const float4 *>(a.g) +
+        (((bh * (a.n + 1) + c) * tiles + ct) * NT + quarter * NW) * 32 + lane;
     const float4 *G1 = G + static_cast<int64_t>(tiles) * NT * 32;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1321,8 +1320,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   };
   const uint32_t base = smem_u32(sm);
   // A and B with rows of 8 along M and N; N = 64 and 128
-  const uint32_t id64 = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16), id128 = idesc_bf16_f32(128,
-      128) | (1u << 15) | (1u << 16);
+  const uint32_t mn = (1u << 15) | (1u << 16);
+  const uint32_t id64 = idesc_bf16_f32(128, 64) | mn, id128 = idesc_bf16_f32(128, 128) | mn;
 
   float anchor = 0.f, ez[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, vz[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
   for (int c0 = 0; c0 < a.dv; c0 += 32) {
@@ -1484,10 +1483,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       const uint32_t idk = idesc_bf16_f32(128, 64) | (1u << 15);  // B with rows of 8 along its sum
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128), q = smem_desc(base + L::Q + ks * 4096, 2048,
-            128);
-        const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024), xc = smem_desc(base + L::X + ks * 2048, 1024,
-            128);
+        const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128);
+        const uint64_t q = smem_desc(base + L::Q + ks * 4096, 2048, 128);
+        const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024);
+        const uint64_t xc = smem_desc(base + L::X + ks * 2048, 1024, 128);
         const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024), nc = smem_desc(base + L::N + ks * 2048, 1024,
             128);
 #pragma unroll
@@ -1529,7 +1528,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          x[e] = there ? x[e] * bf16_to_f32(*reinterpret_cast<const uint16_t *>(sq + ((i0 + e) >> 3) * 2048 + (e & 7) * 16)) : 0.f;
+          x[e] = there ? x[e] * bf16_to_f32(*reinterpret_cast<const uint16_t *>(sq + ((i0 + e) >> 3) * 2048 +
+                                                                              (e & 7) * 16)) : 0.f;
         const float f = sum_lanes(x, lane);
         if (lane < 16) flow[quarter * kC + i0 + lane] = f;
         tmem_ld16(lanes + L::dKb + i0, x);
@@ -1891,12 +1891,17 @@ extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16
     return set_error(SDM_ERR_ALIGN, "gdn_backward: a pointer is not aligned");
   if (workspace_bytes < l.work)
     return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: workspace of %zu bytes, %zu needed", workspace_bytes, l.work);
-  if (B == 0 || H == 0) return SDM_OK;
+  if (B == 0 || (H == 0 && (T == 0 || Hk == 0))) return SDM_OK;
   a.by_qk = std::min(row_bytes(q, ld_q, dk), row_bytes(k, ld_k, dk));
   a.by_v = row_bytes(v, ld_v, dv);
   a.by_dy = row_bytes(dy, static_cast<int64_t>(H) * dv, dv);
   a.pair_y = dv % 2 == 0 && ld_dv % 2 == 0 && aligned(dv_out, 4);
   a.pair_qk = dk % 2 == 0 && ld_dq % 2 == 0 && ld_dk % 2 == 0 && aligned(dq, 4) && aligned(dk_out, 4);
+  if (H == 0) {  // key heads that no value head reads: sums of nothing
+    if (!dq || !dk_out) return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: null pointer");
+    return launch(gdn_grad_heads, "gdn_backward", static_cast<int64_t>(B) * T, 256, 0,
+                  static_cast<cudaStream_t>(stream), a);
+  }
   place_saved(a, const_cast<void *>(saved), l);
   unsigned char *p = static_cast<unsigned char *>(workspace);
   a.g = reinterpret_cast<float *>(p + l.g);

@@ -653,7 +653,7 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * lens      : optional int32 [B], 0 <= lens[b] <= T: only the first lens[b]
  *             tokens exist; the rows behind them are neither read nor written.
  *             Other values are clamped and set SDM_DEVERR_INDEX_RANGE.
- * y         : bf16 [B,T,H,dv], contiguous.
+ * y         : bf16 [B,T,H,dv], contiguous.  Outputs overlap no input.
  * saved     : gdn_train_saved_size() bytes, 16-byte aligned, written by
  *             gdn_train and read by gdn_backward with the same inputs and sizes: per
  *             64 tokens of a head their decays, two triangular matrices, the state

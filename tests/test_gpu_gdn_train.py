@@ -264,6 +264,119 @@ def test_many_heads():
         check(c, c.run(sdm), *c.reference())
 
 
+def test_capture_behind_other_streams():
+    """Captured where the call follows copies and a join with another stream, and others follow it."""
+    sdm = need_gpu()
+    c, e = Case(2, 140, 1, 2, 64, 64, seed=14), Case(2, 140, 1, 2, 64, 64, seed=15)
+    new = [x.clone() for x in itertools.chain(*e.run(sdm))]
+    x = [*c.layout(c.q, c.k, c.v), *c.gates()]
+    S, dS, dy = c.S0.cuda(), c.dS.cuda(), c.dy.cuda()
+    inputs = (*x, S, dS, dy)
+    stage = [t.cuda() for t in (e.q, e.k, e.v, e.la, e.beta, e.S0, e.dS, e.dy)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for t, n in zip(inputs[:4], stage[:4]):
+                t.copy_(n)
+        for t, n in zip(inputs[4:], stage[4:]):
+            t.copy_(n)
+        torch.cuda.current_stream().wait_stream(side)
+        ST, d0 = torch.empty_like(S), torch.empty_like(S)
+        y, saved = sdm.gdn_train(S, *x, state_out=ST)
+        g = sdm.gdn_backward(dS, *x, saved, dy, dstate_out=d0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            copies = [t.clone() for t in (y, ST, d0, *g)]
+            for t in inputs:
+                t.zero_()           # the next replay's copies bring them back
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(copies, new))
+
+
+def test_two_streams_at_once():
+    """Calls that share their inputs, on two streams that run beside one another."""
+    sdm = need_gpu()
+    c = Case(2, 700, 2, 4, 128, 128, seed=16)
+    x, want = [*c.layout(c.q, c.k, c.v), *c.gates()], None
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    S, dS, dy = c.S0.cuda(), c.dS.cuda(), c.dy.cuda()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for st in streams:
+            ST, d0 = torch.empty_like(S), torch.empty_like(S)
+            st.wait_stream(torch.cuda.current_stream())
+            y, saved = sdm.gdn_train(S, *x, state_out=ST, stream=st)
+            outs.append((y, ST, d0, *sdm.gdn_backward(dS, *x, saved, dy, dstate_out=d0, stream=st)))
+    torch.cuda.synchronize()
+    want = list(itertools.chain(*c.run(sdm)))
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+@pytest.mark.parametrize("dims", [(3, 130, 3, 3, 48, 48), (3, 130, 3, 3, 128, 72)], ids=str)
+def test_nan_stays_in_its_sequence_and_head(dims):
+    """What one sequence or one head holds does not reach the others, whose tokens share its tiles' copies."""
+    sdm = need_gpu()
+    c = Case(*dims, seed=17)
+    want = c.run(sdm)
+    for t in (c.q, c.k, c.v, c.la, c.beta, c.dy):
+        t[1] = float("nan")
+        t[2, :, 1] = float("nan")
+    got = c.run(sdm)
+    for a, b in zip(itertools.chain(*got), itertools.chain(*want)):
+        heads = 1 if a.shape[1] == dims[3] and a.dim() == 4 and a.dtype == torch.float32 else 2
+        assert torch.equal(a[0], b[0])
+        rows = (a[2], b[2]) if heads == 1 else (a[2].transpose(0, 1), b[2].transpose(0, 1))
+        assert all(torch.equal(rows[0][h], rows[1][h]) for h in (0, 2))
+
+
+def test_no_value_heads():
+    """No value head reads the key heads: their gradients are 0."""
+    sdm = need_gpu()
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    q, v, gate = torch.randn(2, 70, 2, 24, **bf), torch.zeros(2, 70, 0, 16, **bf), torch.zeros(2, 70, 0, device="cuda")
+    state = torch.zeros(2, 0, 24, 16, device="cuda")
+    y, saved = sdm.gdn_train(state, q, q, v, gate, gate)
+    grads = [torch.full_like(q, 3.0), torch.full_like(q, 3.0), torch.zeros_like(v)]
+    lens = torch.tensor([70, 5], dtype=torch.int32, device="cuda")
+    sdm.gdn_backward(state, q, q, v, gate, gate, saved, y, grads=grads, lens=lens)
+    for g in grads[:2]:
+        assert bool((g[0] == 0).all()) and bool((g[1, :5] == 0).all()) and bool((g[1, 5:] == 3.0).all())
+
+
+def test_offsets_past_32_bits():
+    """Tokens 2^20 elements apart, 2^32 elements in all; a pool of more than 2^31 elements."""
+    sdm = need_gpu()
+    c = Case(1, 4097, 1, 1, 64, 64, seed=18)
+    want = list(itertools.chain(*c.run(sdm)))
+    p = torch.empty(4097, 1 << 20, dtype=torch.bfloat16, device="cuda")
+    x = []
+    for i, t in enumerate((c.q, c.k, c.v)):
+        s = p[:, 64 * i:64 * i + 64].view(1, 4097, 1, 64)
+        s.copy_(t)
+        x.append(s)
+    grads = [p[:, 64 * i:64 * i + 64].view(1, 4097, 1, 64) for i in (3, 4, 5)]
+    S, d = c.S0.cuda(), c.dS.cuda()
+    y, saved = sdm.gdn_train(S, *x, *c.gates())
+    got = (y, S, d, *sdm.gdn_backward(d, *x, *c.gates(), saved, c.dy.cuda(), grads=grads))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del p, x, grads
+    c = Case(2, 1, 1, 1, 128, 128, seed=19)
+    pool = torch.empty((1 << 17) + 2, 1, 128, 128, device="cuda")
+    slots = torch.tensor([(1 << 17) + 1, 0], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = c.S0.cuda()
+    y = sdm.gdn_step(pool, *c.layout(c.q, c.k, c.v), *c.gates(), slots=slots)
+    f = ref.forward(c.S0, c.q, c.k, c.v, c.la, c.beta)
+    close16(y, f[0], "y")
+    close32(pool[slots.long()], f[1], "state")
+
+
 @pytest.mark.parametrize("shape", [(1, 200, 1, 1, 128, 128), (3, 130, 1, 20, 64, 64)], ids=str)
 def test_a_wait_that_runs_out_is_reported(shape, monkeypatch):
     """A copy that is never asked for: both calls end, report it, and the next ones are right."""

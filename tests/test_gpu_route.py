@@ -113,6 +113,31 @@ def test_places_outside_the_rows_are_dropped():
     assert bool((sdm.route_combine(rows, place)[1] == 0).all())
 
 
+def test_offsets_past_32_bits():
+    """Rows of more than 2^32 elements in all, and tokens 2^26 elements apart."""
+    sdm = need_gpu()
+    M, k, D = 33000, 2, 1 << 16
+    sel = torch.zeros(M, k, dtype=torch.int32, device="cuda")
+    sel[:, 1] = 1
+    _, place, offsets = sdm.route_sort(sel, 2)
+    x = torch.empty(M, D, dtype=torch.bfloat16, device="cuda")
+    x[:] = (torch.arange(M, device="cuda") % 16)[:, None]
+    rows = sdm.route_gather(x, place, offsets)
+    assert bool((rows[:M, ::4095] == x[:, ::4095]).all()) and bool((rows[M:, ::4095] == x[:, ::4095]).all())
+    y = sdm.route_combine(rows, place)
+    assert bool((y[:, ::4095] == 2 * x[:, ::4095]).all())
+    del y
+    w = torch.full((M, k), 0.5, device="cuda")
+    drows, dw = sdm.route_combine_backward(x, rows, place, w, offsets)
+    assert bool((drows[:, ::4095] == 0.5 * rows[:, ::4095]).all())
+    assert torch.equal(dw, (x[:, :1].float() ** 2 * D).expand(M, k))       # whole numbers below 2^24
+    del drows, rows
+    far = torch.empty(70, 1 << 26, dtype=torch.bfloat16, device="cuda")[:, :40]
+    far.copy_(x[:70, :40])
+    p = torch.arange(70, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    assert torch.equal(sdm.route_gather(far, p, torch.tensor([0, 70], dtype=torch.int32, device="cuda")), x[:70, :40])
+
+
 def test_graph_and_stream():
     sdm = need_gpu()
     sel = [visits(300, 2, 5, s).cuda() for s in (1, 2)]
