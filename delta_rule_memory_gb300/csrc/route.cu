@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_back_kernel(const R
   for (int64_t m = warp; m < a.M; m += warps) {
     const int at = place_of(a, m, lane);
     const float wt = lane < a.k ? a.w[m * a.k + lane] : 0.f;
-    const R *dy = reinterpret_cast<const R *>(static_cast<const char *>(a.x) + m * a.ld * static_cast<int64_t>(sizeof(T)));
+    const R *dy = reinterpret_cast<const R *>(static_cast<const T *>(a.x) + m * a.ld);
     for (int r0 = 0; r0 < a.k; r0 += V) {
       int64_t j[V];
       float ww[V], dot[V];
