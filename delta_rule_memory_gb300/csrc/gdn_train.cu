@@ -386,11 +386,11 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 }
 
 // ---------------------------------------------------------------------------
-// The chains.  A CTA has W tiles of 16 value columns of one head, each with three warps.  Two do what the next
-// chunk waits for, each with half of the key channels (the sums with the state and its update) and with two of
-// the four groups of 16 tokens (0 and 3, or 1 and 2, the same number of the triangle's blocks): sums over all
-// channels and a triangle's products meet in shared memory.  The third does everything else: y, the products
-// with dy, what is kept for later, copies.  A tile's state lives in shared memory as its three bf16 parts,
+// The chains.  A CTA has W tiles of 16 value columns of one head, each with M + H warps.  M (two or four) do
+// what the next chunk waits for, each with its share of the key channels (the sums with the state and its
+// update) and of the four groups of 16 tokens (of two warps, 0 and 3, or 1 and 2, the same number of the
+// triangle's blocks): sums over all channels and a triangle's products meet in shared memory.  The H others do
+// everything else: y, the products with dy, what is kept for later, copies.  A tile's state lives in shared memory as its three bf16 parts,
 // which are all 24 bits of it, in the order of the A fragments that every product with it takes. Bound by
 // latency where a tile has an SM to itself (2.6 us a chunk forward, 3.4 backward at dk = dv = 128; one warp a
 // tile took 7.6 and 6.5, a second one for what can wait, with copies by TMA, 3.6 and 4.7). Where four tiles
@@ -398,17 +398,19 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 // 10,500 cycles each: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward chain is
 // a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
-template <int NK, int PM, int W>  // PM: parts of M
+template <int NK, int PM, int W, int M, int H>  // PM: parts of the chunk's M
 struct Chain {
   static constexpr int P = NK / 4;  // panels of K and Q
   static constexpr int K = 0, Q = K + P * kPanel, V = Q + P * kPanel, T = V + kPanel, sc = T + 3 * kTri,
                        stage = (sc + 3 * kC * 4 + 1023) / 1024 * 1024;
   // M is read early in a chunk only, so one place does
-  static constexpr int M = 2 * stage, state = M + PM * kTri, parts = state + W * NK * 3 * 512,
-      tokens = parts + W * 4 * 3 * 512,
-                       bars = tokens + W * 8 * 512, size = bars + 32;
+  static constexpr int Mq = 2 * stage, state = Mq + PM * kTri, parts = state + W * NK * 3 * 512,
+                       tokens = parts + W * 4 * 3 * 512, sums = tokens + W * 8 * 512,
+                       bars = sums + (M == 4 ? W * 4 * 8 * 512 : 0), size = bars + 32;
 };
-static_assert(Chain<8, 3, 4>::size <= kMaxSmem && Chain<8, 2, 4>::size <= kMaxSmem, "");
+static_assert(Chain<8, 3, 4, 2, 1>::size <= kMaxSmem && Chain<8, 3, 2, 4, 2>::size <= kMaxSmem, "");
+template <int W, int M, int H>
+constexpr int kChainThreads = 32 * W * (M + H) + (W < 4 ? 32 : 0);
 
 // A chunk's tiles into a stage; cols: the value columns' tensor.  What tensor and bulk copies bring is asked
 // for by one lane of a warp of its own or, where a CTA has four tiles and no room for another warp's registers,
@@ -416,11 +418,11 @@ static_assert(Chain<8, 3, 4>::size <= kMaxSmem && Chain<8, 2, 4>::size <= kMaxSm
 template <int W>
 constexpr int kAskers = W < 4 ? 1 : 4;
 
-template <int NK, int PM, int W>
+template <int NK, int PM, int W, int M, int H>
 __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps,
                                               int64_t u, int64_t tok, int h, int col0, int by_cols,
                                               const CUtensorMap *cols_map, int who) {
-  using L = Chain<NK, PM, W>;
+  using L = Chain<NK, PM, W, M, H>;
   constexpr bool all = kAskers<W> == 1;
   const uint32_t mb = smem_u32(bar);
   const int hk = h / (a.H / a.Hk), token = static_cast<int>(tok);
@@ -447,12 +449,12 @@ __device__ __forceinline__ void request_m(unsigned char *to, uint64_t *bar, cons
   umma::mbar_expect_tx(smem_u32(bar), PM * kTri);
   umma::bulk_g2s(smem_u32(to), a.m3 + u * (3 * kTri), PM * kTri, smem_u32(bar));
 }
-// ... and the rest, by the third warps
-template <int NK, int PM, int W>
+// ... and the rest, by the helping warps
+template <int NK, int PM, int W, int M, int H>
 __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int64_t tok, int h, int col0, int live,
                                            const uint16_t *cols, int64_t ld_cols, int by_cols, int tid) {
-  using L = Chain<NK, PM, W>;
-  constexpr int threads = 32 * W;
+  using L = Chain<NK, PM, W, M, H>;
+  constexpr int threads = 32 * W * H;
   const int hk = h / (a.H / a.Hk), from = col0 & ~63;  // whole panels of value columns
   if (a.by_qk != 16) {
     load_tile<L::P, threads>(st + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
@@ -465,14 +467,14 @@ __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int6
 }
 
 // the rows behind a chunk's last token, which tensor copies fill with whatever follows it
-template <int NK, int PM, int W>
+template <int NK, int PM, int W, int M, int H>
 __device__ __forceinline__ void clear_stage(unsigned char *st, const Gdn &a, int live, int by_cols, int tid) {
-  using L = Chain<NK, PM, W>;
+  using L = Chain<NK, PM, W, M, H>;
   if (a.by_qk == 16) {
-    clear_rows<L::P, 32 * W>(st + L::K, live, tid);
-    clear_rows<L::P, 32 * W>(st + L::Q, live, tid);
+    clear_rows<L::P, 32 * W * H>(st + L::K, live, tid);
+    clear_rows<L::P, 32 * W * H>(st + L::Q, live, tid);
   }
-  if (by_cols == 16) clear_rows<1, 32 * W>(st + L::V, live, tid);
+  if (by_cols == 16) clear_rows<1, 32 * W * H>(st + L::V, live, tid);
   umma::fence_async_smem();
 }
 
@@ -521,15 +523,17 @@ __device__ __forceinline__ void clear(float (&x)[N][4]) {
   for (int i = 0; i < N; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 }
 // the parts of a k-step's A fragments of a state, and the state that they are
+template <int N = 3>
 __device__ __forceinline__ void put_parts(uint4 *m, int lane, const float (&c0)[4], const float (&c1)[4]) {
-  uint32_t s[3][4];
-  a_split<3>(c0, c1, s);
+  uint32_t s[N][4];
+  a_split<N>(c0, c1, s);
 #pragma unroll
-  for (int p = 0; p < 3; ++p) m[p * 32 + lane] = make_uint4(s[p][0], s[p][1], s[p][2], s[p][3]);
+  for (int p = 0; p < N; ++p) m[p * 32 + lane] = make_uint4(s[p][0], s[p][1], s[p][2], s[p][3]);
 }
-__device__ __forceinline__ void get_parts(const uint4 *m, int lane, uint32_t (&s)[3][4]) {
+template <int N>
+__device__ __forceinline__ void get_parts(const uint4 *m, int lane, uint32_t (&s)[N][4]) {
 #pragma unroll
-  for (int p = 0; p < 3; ++p) {
+  for (int p = 0; p < N; ++p) {
     const uint4 v = m[p * 32 + lane];
     s[p][0] = v.x, s[p][1] = v.y, s[p][2] = v.z, s[p][3] = v.w;
   }
@@ -577,32 +581,34 @@ __device__ __forceinline__ void add(float (&d)[N][4], const float (&l)[N][4]) {
     for (int e = 0; e < 4; ++e) d[i][e] += l[i][e];
 }
 
-// acc = A B for n-tiles 4 quad .. 4 quad + 3, B = tile[token][n] exact, over 64 tokens: the small parts first
-__device__ __forceinline__ void quad_product(uint32_t tile, int quad, const uint32_t (&a)[4][3][4], int lane,
-                                             float (&acc)[4][4]) {
-  uint32_t r[4][2][4];
+// acc = A B for X blocks of 16 columns, B = tile[token][column] exact, over 64 tokens: the small parts first
+template <int X>
+__device__ __forceinline__ void block_product(uint32_t tile, int block, const uint32_t (&a)[4][3][4], int lane,
+                                              float (&acc)[2 * X][4]) {
+  uint32_t r[4][X][4];
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) b_cols(tile, 32 * quad + 16 * x, 16 * ks, lane, r[ks][x]);
+    for (int x = 0; x < X; ++x) b_cols(tile, 16 * (block + x), 16 * ks, lane, r[ks][x]);
   clear(acc);
 #pragma unroll
   for (int p = 2; p >= 0; --p)
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < X; ++x) {
         fma16816(acc[2 * x], a[ks][p], r[ks][x][0], r[ks][x][1]);
         fma16816(acc[2 * x + 1], a[ks][p], r[ks][x][2], r[ks][x][3]);
       }
 }
 
-// state <- factor state + sign acc for n-tiles 4 quad .. 4 quad + 3; x: its new values
-__device__ __forceinline__ void update_quad(uint4 *parts, int quad, int lane, float factor, float sign,
-                                            const float (&acc)[4][4], float (&x)[4][4]) {
+// state <- factor state + sign acc for X blocks of 16 channels; x: its new values
+template <int X>
+__device__ __forceinline__ void update_blocks(uint4 *parts, int block, int lane, float factor, float sign,
+                                              const float (&acc)[2 * X][4], float (&x)[2 * X][4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint4 *m = parts + (2 * quad + i) * 96;
+  for (int i = 0; i < X; ++i) {
+    uint4 *m = parts + (block + i) * 96;
     uint32_t s[3][4];
     get_parts(m, lane, s);
     join(s, x[2 * i], x[2 * i + 1]);
@@ -639,50 +645,76 @@ __device__ __forceinline__ void state_product(const uint4 *parts, uint32_t tile,
   add(d, l);
 }
 
-// A tile's two first warps x = 0 and 1 and their groups of 16 tokens, i = 0 and 1
-__device__ __forceinline__ int group_of(int x, int i) { return x == 0 ? (i ? 3 : 0) : 1 + i; }
-// of sums over all tokens: the own groups' n-tiles, and the other warp's through shared memory
-__device__ __forceinline__ void give_sums(float4 *m, int x, int lane, const float (&d)[8][4], float (&mine)[4][4]) {
+// Of the four groups of 16 tokens, the i-th of warp x of N that share them
+template <int N>
+__device__ __forceinline__ constexpr int group_of(int x, int i) {
+  return N == 1 ? i : N == 4 ? x : x == 0 ? (i ? 3 : 0) : 1 + i;
+}
+template <int N>
+__device__ __forceinline__ constexpr int tile_of(int x, int i) { return 2 * group_of<N>(x, i >> 1) + (i & 1); }
+// whether group n is one of warp x's
+template <int N>
+__device__ __forceinline__ constexpr bool has_group(int x, int n) {
+  return N == 1 || (N == 4 ? n == x : (n == 0 || n == 3) == (x == 0));
+}
+// Sums over all tokens, a part of them with each of M warps: the own groups' n-tiles, and the others' through
+// shared memory (of two warps eight tiles, each written by the one that does not keep it; of four all of them)
+template <int M>
+__device__ __forceinline__ void give_sums(float4 *m, int x, int lane, const float (&d)[8][4], float (&mine)[8 / M][4]) {
+  if constexpr (M == 4) {
+    put(m + x * 8 * 32, lane, d);
+    clear(mine);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int a = i < 2 ? i : i + 4, b = i + 2;  // n-tiles of groups 0 and 3, of 1 and 2
-    m[(x ? a : b) * 32 + lane] = x ? make_float4(d[a][0], d[a][1], d[a][2], d[a][3]) : make_float4(d[b][0], d[b][1],
-        d[b][2], d[b][3]);
+    for (int i = 0; i < 4; ++i) {
+      const int a = i < 2 ? i : i + 4, b = i + 2;  // n-tiles of groups 0 and 3, of 1 and 2
+      m[(x ? a : b) * 32 + lane] = x ? make_float4(d[a][0], d[a][1], d[a][2], d[a][3])
+                                     : make_float4(d[b][0], d[b][1], d[b][2], d[b][3]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) mine[i][e] = x ? d[b][e] : d[a][e];
+      for (int e = 0; e < 4; ++e) mine[i][e] = x ? d[b][e] : d[a][e];
+    }
   }
 }
-__device__ __forceinline__ int tile_of(int x, int i) { return 2 * group_of(x, i >> 1) + (i & 1); }
-__device__ __forceinline__ void take_sums(const float4 *m, int x, int lane, float (&mine)[4][4]) {
+template <int M, int N>
+__device__ __forceinline__ void add_tiles(const float4 *m, int x, int lane, float (&mine)[N][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = m[tile_of(x, i) * 32 + lane];
+  for (int i = 0; i < N; ++i) {
+    const float4 v = m[tile_of<M>(x, i) * 32 + lane];
     mine[i][0] += v.x, mine[i][1] += v.y, mine[i][2] += v.z, mine[i][3] += v.w;
   }
 }
-__device__ __forceinline__ void put_tiles(float4 *m, int x, int lane, const float (&mine)[4][4]) {
+template <int M>
+__device__ __forceinline__ void take_sums(const float4 *m, int x, int lane, float (&mine)[8 / M][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[tile_of(x, i) * 32 + lane] = make_float4(mine[i][0], mine[i][1], mine[i][2],
-      mine[i][3]);
+  for (int y = 0; y < (M == 4 ? 4 : 1); ++y) add_tiles<M>(m + y * 8 * 32, x, lane, mine);
 }
-__device__ __forceinline__ void put_groups(uint4 *parts, int x, int lane, const float (&mine)[4][4]) {
+template <int M, int N>
+__device__ __forceinline__ void put_tiles(float4 *m, int x, int lane, const float (&mine)[N][4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) put_parts(parts + group_of(x, i) * 96, lane, mine[2 * i], mine[2 * i + 1]);
+  for (int i = 0; i < N; ++i)
+    m[tile_of<M>(x, i) * 32 + lane] = make_float4(mine[i][0], mine[i][1], mine[i][2], mine[i][3]);
 }
-__device__ __forceinline__ void scale_groups(float (&mine)[4][4], int x, const float *f, int t) {
+template <int M>
+__device__ __forceinline__ void put_groups(uint4 *parts, int x, int lane, const float (&mine)[8 / M][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = *reinterpret_cast<const float2 *>(f + 8 * tile_of(x, i) + 2 * t);
+  for (int i = 0; i < 4 / M; ++i) put_parts(parts + group_of<M>(x, i) * 96, lane, mine[2 * i], mine[2 * i + 1]);
+}
+template <int M, int N>
+__device__ __forceinline__ void scale_groups(float (&mine)[N][4], int x, const float *f, int t) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 v = *reinterpret_cast<const float2 *>(f + 8 * tile_of<M>(x, i) + 2 * t);
     mine[i][0] *= v.x, mine[i][1] *= v.y, mine[i][2] *= v.x, mine[i][3] *= v.y;
   }
 }
 
 // the own groups of X T^T (BACK: X T), X's parts in shared memory, T a triangle in three parts
-template <bool BACK>
-__device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tri, int x, int lane, float (&d)[4][4]) {
+template <bool BACK, int M>
+__device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tri, int x, int lane,
+                                                 float (&d)[8 / M][4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = group_of(x, i), first = BACK ? n : 0, last = BACK ? 3 : n;
+  for (int i = 0; i < 4 / M; ++i) {
+    const int n = group_of<M>(x, i), first = BACK ? n : 0, last = BACK ? 3 : n;
     float h[2][4], l[2][4], m[2][4];  // parts 0 0; 0 1 and 1 0; 1 1, 0 2 and 2 0
     clear(h);
     clear(l);
@@ -711,7 +743,7 @@ __device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tr
   }
 }
 
-// a tile's first two warps (64 threads), or all three (96), meet
+// a tile's first M warps, or all of them, meet
 __device__ __forceinline__ void meet(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads)
     : "memory"); }
 // ... or only tell the others that they are there
@@ -721,7 +753,7 @@ __device__ __forceinline__ void arrive(int id, int threads) { asm volatile("bar.
 // where a warp of a chain stands
 template <int W>
 struct Place {
-  int tid, role, w, lane, col0, col, b, h, len, n;
+  int tid, role, w, lane, col0, col, b, h, len, n;  // role: which of the tile's warps
   int64_t bh, tok;
   bool mine;  // else the tile lies behind dv, and its warps only help with the copies
   __device__ __forceinline__ explicit Place(const Gdn &a) {
@@ -736,11 +768,12 @@ struct Place {
   }
 };
 
-template <int NK, int W>
-__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(const Gdn a,
+template <int NK, int W, int M, int H>
+__global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn a,
     const __grid_constant__ Maps maps) {
-  using L = Chain<NK, 2, W>;
-  constexpr int NT = 2 * NK, kOwn = 96 * W;  // kOwn: threads before the warp that asks for copies
+  using L = Chain<NK, 2, W, M, H>;
+  constexpr int NT = 2 * NK, kOwn = 32 * W * (M + H);  // kOwn: threads before the warp that asks for copies
+  constexpr int kBlocks = NK / M, X = kBlocks < 2 ? 1 : 2;        // blocks of 16 channels of a warp's; taken at once
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages, M
   if (threadIdx.x == 0) {
@@ -756,44 +789,48 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   const int tiles = (a.dv + 15) >> 4;
   uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96,
       *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
-  float4 *hE = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // half sums, then E
+  uint4 *hU = reinterpret_cast<uint4 *>(sm + L::tokens) + w * 8 * 32;  // U's first two parts
+  float4 *hX = M == 4 ? reinterpret_cast<float4 *>(sm + L::sums) + w * 32 * 32
+                      : reinterpret_cast<float4 *>(hU);  // partial sums, before U
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
   uint32_t limit = kWaitLimit;
-  const int pair = 1 + w, three = 1 + W + w;  // barriers
+  const int pair = 1 + w, all = 1 + W + w;  // barriers
 
-  if (me.role < 2) {
+  if (me.role < M) {
     const int x = me.role, vp = ((me.col0 & 63) >> 3) + 2 * w;  // vp: the tile's pieces of the value columns' panel
-    uint4 *own = hS + x * (NK / 2) * 96;
-    float S[NK][4];  // the own channels' state beside its parts
-    read_state<NK>(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * NK * 8, a.dk, a.dv, col, lane, S);
+    uint4 *own = hS + x * kBlocks * 96;
+    float S[2 * kBlocks][4];  // the own channels' state beside its parts
+    read_state(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
 #pragma unroll
-    for (int ks = 0; ks < NK / 2; ++ks) put_parts(own + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
+    for (int ks = 0; ks < kBlocks; ++ks) put_parts(own + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
     for (int c = 0; c < n; ++c) {
       __syncthreads();
       wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
-      if (len - c * kC < kC) __syncthreads();  // the third warps clear rows
+      if (len - c * kC < kC) __syncthreads();  // the helping warps clear rows
       if (!me.mine) continue;
       unsigned char *st = sm + (c & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K), uV = smem_u32(st + L::V);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
-      float Z[4][4];
+      const int64_t at = (me.bh * a.n + c) * tiles + (col >> 4);
+      put(reinterpret_cast<float4 *>(a.s) + at * (NT * 32) + x * kBlocks * 64, lane, S);
+      float Z[8 / M][4];
       {
         float d[8][4];
-        state_product<NK / 2, NK / 2>(own, uK, x * NK * 8, lane, d);
-        give_sums(hE, x, lane, d, Z);
+        state_product<kBlocks, kBlocks>(own, uK, x * kBlocks * 16, lane, d);
+        give_sums<M>(hX, x, lane, d, Z);
       }
-      meet(pair, 64);
-      take_sums(hE, x, lane, Z);
+      meet(pair, 32 * M);
+      take_sums<M>(hX, x, lane, Z);
       // Z^T = V^T - gam S^T K^T
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4 / M; ++i) {
         uint32_t v[4];
         // tile[token][column]: rows of V^T are its columns
-        ldsm4_t(uV + piece(16 * group_of(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v);
+        ldsm4_t(uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * tile_of(x, 2 * i + j) + 2 * t);
+          const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * tile_of<M>(x, 2 * i + j) + 2 * t);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t vv = v[2 * j + (e >> 1)];
@@ -801,48 +838,53 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
           }
         }
       }
-      put_groups(hP, x, lane, Z);
-      meet(pair, 64);
-      float E[4][4];
-      triangle_product<false>(hP, smem_u32(st + L::T), x, lane, E);
-      put_tiles(hE, x, lane, E);
-      meet(three, 96);  // E is there, S and Z have been read
+      put_groups<M>(hP, x, lane, Z);
+      meet(pair, 32 * M);
+      float E[8 / M][4];
+      triangle_product<false, M>(hP, smem_u32(st + L::T), x, lane, E);
+      put_tiles<M>(reinterpret_cast<float4 *>(a.e) + at * 256, x, lane, E);
+      scale_groups<M>(E, x, beta, t);
+#pragma unroll
+      for (int i = 0; i < 4 / M; ++i) put_parts<2>(hU + group_of<M>(x, i) * 64, lane, E[2 * i], E[2 * i + 1]);
+      meet(all, 32 * (M + H));  // U is there, S and Z have been read
       // S^T = gam_C S^T + (tail U)^T K
-      scale_groups(E, x, beta, t);
-      scale_groups(E, x, tail, t);
-      put_groups(hP, x, lane, E);
-      meet(pair, 64);
+      scale_groups<M>(E, x, tail, t);
+      put_groups<M>(hP, x, lane, E);
+      meet(pair, 32 * M);
       uint32_t ut[4][3][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) get_parts(hP + ks * 96, lane, ut[ks]);
       const float end = gam[kC - 1];
 #pragma unroll
-      for (int q = 0; q < NK / 4; ++q) {
-        float acc[4][4];
-        quad_product(uK, x * (NK / 4) + q, ut, lane, acc);
+      for (int q = 0; q < kBlocks; q += X) {
+        float acc[2 * X][4];
+        block_product<X>(uK, x * kBlocks + q, ut, lane, acc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2 * X; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) S[4 * q + i][e] = fmaf(end, S[4 * q + i][e], acc[i][e]);
+          for (int e = 0; e < 4; ++e) S[2 * q + i][e] = fmaf(end, S[2 * q + i][e], acc[i][e]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) put_parts(own + (2 * q + i) * 96, lane, S[4 * q + 2 * i], S[4 * q + 2 * i + 1]);
+        for (int i = 0; i < X; ++i) put_parts(own + (q + i) * 96, lane, S[2 * (q + i)], S[2 * (q + i) + 1]);
       }
     }
-    if (me.mine) write_state<NK>(a.state_out + me.bh * a.dk * a.dv, x * NK * 8, a.dk, a.dv, col, lane, S);
+    if (me.mine) write_state(a.state_out + me.bh * a.dk * a.dv, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
     return;
   }
 
-  const int ltid = tid - 64 * W;
+  // of four, those with many of the triangle's blocks run beside chain warps with few
+  const int ltid = tid - 32 * W * M, z = me.role - M, zg = H == 4 ? 3 - z : z;
   const auto request = [&](int c) {
     if (lane == 0)
-      request_stage<NK, 2, W>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h,
+      request_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h,
           me.col0, a.by_v,
                               &maps.v, w);
     __syncwarp();
   };
+  const auto ask_m = [&](int c) { if (!a.drop) request_m<2>(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
   if (tid >= kOwn) {
     for (int c = 0; c <= n; ++c) {
       if (c > 0) __syncthreads();
+      if (c > 0 && lane == 0) ask_m(c - 1);  // every helping warp is done with the chunk before
       if (c < n) request(c);
       if (c > 0 && len - (c - 1) * kC < kC) __syncthreads();
     }
@@ -850,19 +892,14 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 2, W>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v,
+    copy_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v,
         a.by_v, ltid);
-  };
-  const auto ask_m = [&](int c) {
-    if (ltid == 0 && !a.drop) request_m<2>(sm + L::M, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(0);
-    ask_m(0);
     copy(0);
   }
   for (int c = 0; c < n; ++c) {
-    const int64_t u = me.bh * a.n + c;
     unsigned char *st = sm + (c & 1) * L::stage;
     cp_async_wait<0>();
     __syncthreads();
@@ -870,61 +907,56 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
       if (kAskers<W> > 1) request(c + 1);
       copy(c + 1);
     }
-    if (c > 0) ask_m(c);  // every third warp is done with the chunk before
+    if (kAskers<W> > 1 && ltid == 0) ask_m(c);  // every helping warp is done with the chunk before
     wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
-      clear_stage<NK, 2, W>(st, a, len - c * kC, a.by_v, ltid);
+      clear_stage<NK, 2, W, M, H>(st, a, len - c * kC, a.by_v, ltid);
       __syncthreads();
     }
     if (!me.mine) continue;
-    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::M);
-    const float *gam = reinterpret_cast<const float *>(st + L::sc), *beta = gam + 2 * kC;
-    float Y[8][4], E[8][4];
+    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq);
+    const float *gam = reinterpret_cast<const float *>(st + L::sc);
+    float Y[8 / H][4];  // the own groups of tokens
     clear(Y);
-    {  // Y^T = gam S^T Q^T; S is kept
-      float4 *kept = reinterpret_cast<float4 *>(a.s) + (u * tiles + (col >> 4)) * (NT * 32);
-#pragma unroll 2
+    {  // Y^T = gam S^T Q^T
+#pragma unroll(2 * H)
       for (int ks = 0; ks < NK; ++ks) {
-        uint32_t s[3][4], r[4][4];
-        float x[2][4];
+        uint32_t s[2][4], r[4 / H][4];
         get_parts(hS + ks * 96, lane, s);
 #pragma unroll
-        for (int np = 0; np < 4; ++np) b_rows(uQ, 16 * np, 16 * ks, lane, r[np]);
-        join(s, x[0], x[1]);
-        put(kept + 64 * ks, lane, x);
+        for (int i = 0; i < 4 / H; ++i) b_rows(uQ, 16 * group_of<H>(zg, i), 16 * ks, lane, r[i]);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int np = 0; np < 4; ++np) {
-            fma16816(Y[2 * np], s[p], r[np][0], r[np][1]);
-            fma16816(Y[2 * np + 1], s[p], r[np][2], r[np][3]);
+          for (int i = 0; i < 4 / H; ++i) {
+            fma16816(Y[2 * i], s[p], r[i][0], r[i][1]);
+            fma16816(Y[2 * i + 1], s[p], r[i][2], r[i][3]);
           }
       }
-      scale_tokens(Y, gam, t);
+      scale_groups<H>(Y, zg, gam, t);
     }
     wait_copies(bars + 2, c & 1, limit, a);
-    meet(three, 96);
-    get(hE, lane, E);
-    put(reinterpret_cast<float4 *>(a.e) + (u * tiles + (col >> 4)) * 256, lane, E);
-    scale_tokens(E, beta, t);
+    meet(all, 32 * (M + H));
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {  // += U^T M^T
       uint32_t us[2][4];
-      a_split<2>(E[2 * ks], E[2 * ks + 1], us);
+      get_parts(hU + ks * 64, lane, us);
 #pragma unroll
-      for (int np = ks; np < 4; ++np) {
+      for (int i = 0; i < 4 / H; ++i) {
+        const int n = group_of<H>(zg, i);
+        if (n < ks) continue;
         uint32_t r[2][4];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, np, ks, lane, r[p]);
-        products(Y, Y, np, us, r);
+        for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, n, ks, lane, r[p]);
+        products(Y, Y, i, us, r);
       }
     }
     // y, rounded once: pairs of tokens turned into pairs of columns
     uint16_t *yc = a.y + (me.tok * a.H + h) * a.dv + col + 2 * t;
     const int left = a.dv - col - 2 * t;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const int i = c * kC + 8 * nt + g;
+    for (int nt = 0; nt < 8 / H; ++nt) {
+      const int i = c * kC + 8 * tile_of<H>(zg, nt) + g;
       uint16_t *row = yc + i * (static_cast<int64_t>(a.H) * a.dv);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -941,11 +973,12 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain(con
   }
 }
 
-template <int NK, int W>
-__global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_back(const Gdn a,
+template <int NK, int W, int M, int H>
+__global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(const Gdn a,
     const __grid_constant__ Maps maps) {
-  using L = Chain<NK, 3, W>;
-  constexpr int NT = 2 * NK, kOwn = 96 * W;
+  using L = Chain<NK, 3, W, M, H>;
+  constexpr int NT = 2 * NK, kOwn = 32 * W * (M + H);
+  constexpr int kBlocks = NK / M, X = kBlocks < 2 ? 1 : 2, XH = NK / H < 2 ? 1 : 2;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages, M
   if (threadIdx.x == 0) {
@@ -961,23 +994,25 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   const int64_t ld_y = static_cast<int64_t>(a.H) * a.dv;
   uint4 *hG = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96,
       *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
-  float4 *hX = reinterpret_cast<float4 *>(hP);                           // half sums, before the parts
+  float4 *hX = M == 4 ? reinterpret_cast<float4 *>(sm + L::sums) + w * 32 * 32
+                      : reinterpret_cast<float4 *>(hP);  // partial sums, before the parts
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
   uint32_t limit = kWaitLimit;
-  const int pair = 1 + w, three = 1 + W + w, read = 1 + 2 * W + w, thirds = 1 + 3 * W;
+  const int pair = 1 + w, all = 1 + W + w, read = 1 + 2 * W + w, helpers = 1 + 3 * W;
 
-  if (me.role < 2) {
+  if (me.role < M) {
     const int x = me.role;
-    uint4 *own = hG + x * (NK / 2) * 96;
-    float4 *kept = reinterpret_cast<float4 *>(a.g) + (me.bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 32) + x * NK * 32;
+    uint4 *own = hG + x * kBlocks * 96;
+    float4 *kept = reinterpret_cast<float4 *>(a.g) + (me.bh * (a.n + 1) * tiles + (col >> 4)) * (NT * 32) +
+        x * kBlocks * 64;
     const int64_t step = static_cast<int64_t>(tiles) * (NT * 32);
 #pragma unroll 1
-    for (int ks = 0; ks < NK / 2; ++ks) {
+    for (int ks = 0; ks < kBlocks; ++ks) {
       float y[2][4];
-      read_state<2>(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * NK * 8 + 16 * ks, a.dk, a.dv, col,
-          lane, y);
+      read_state(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, 16 * (x * kBlocks + ks), a.dk, a.dv, col,
+                 lane, y);
       put_parts(own + ks * 96, lane, y[0], y[1]);
       if (me.mine) put(kept + n * step + ks * 64, lane, y);
     }
@@ -985,63 +1020,64 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
       const int it = n - 1 - c;
       __syncthreads();
       wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
-      if (len - c * kC < kC) __syncthreads();  // the third warps clear rows
+      if (len - c * kC < kC) __syncthreads();  // the helping warps clear rows
       if (!me.mine) continue;
       unsigned char *st = sm + (it & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
       // dU^T = tail G^T K^T + dY^T M
-      float U[4][4], Z[4][4];
+      float U[8 / M][4], Z[8 / M][4];
       {
         float d[8][4];
-        state_product<NK / 2, 1>(own, uK, x * NK * 8, lane, d);
-        give_sums(hX, x, lane, d, U);
+        state_product<kBlocks, 1>(own, uK, x * kBlocks * 16, lane, d);
+        give_sums<M>(hX, x, lane, d, U);
       }
-      arrive(read, 96);  // G has been read
-      meet(three, 96);   // dY^T M is there
-      take_sums(hX, x, lane, U);
-      scale_groups(U, x, tail, t);
-      take_sums(hZ, x, lane, U);
-      scale_groups(U, x, beta, t);
-      meet(pair, 64);  // the half sums have been read
-      put_groups(hP, x, lane, U);
-      meet(pair, 64);
-      triangle_product<true>(hP, smem_u32(st + L::T), x, lane, Z);  // dZ^T
-      put_tiles(hZ, x, lane, Z);
-      meet(three, 96);  // dZ is there, dU has been read, G = gam_C G + Q^T (gam dY)
+      arrive(read, 32 * (M + H));  // G has been read
+      meet(all, 32 * (M + H));     // dY^T M is there
+      take_sums<M>(hX, x, lane, U);
+      scale_groups<M>(U, x, tail, t);
+      add_tiles<M>(hZ, x, lane, U);
+      scale_groups<M>(U, x, beta, t);
+      if (M == 2) meet(pair, 32 * M);  // the partial sums, which lie in the parts' place, have been read
+      put_groups<M>(hP, x, lane, U);
+      meet(pair, 32 * M);
+      triangle_product<true, M>(hP, smem_u32(st + L::T), x, lane, Z);  // dZ^T
+      put_tiles<M>(hZ, x, lane, Z);
+      meet(all, 32 * (M + H));  // dZ is there, dU has been read, G = gam_C G + Q^T (gam dY)
       // G^T -= (gam dZ)^T K
-      scale_groups(Z, x, gam, t);
-      put_groups(hP, x, lane, Z);
-      meet(pair, 64);
+      scale_groups<M>(Z, x, gam, t);
+      put_groups<M>(hP, x, lane, Z);
+      meet(pair, 32 * M);
       uint32_t zt[4][3][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) get_parts(hP + ks * 96, lane, zt[ks]);
       float4 *to = kept + c * step;
 #pragma unroll 1
-      for (int q = 0; q < NK / 4; ++q) {
-        float acc[4][4], y[4][4];
-        quad_product(uK, x * (NK / 4) + q, zt, lane, acc);
-        update_quad(own, q, lane, 1.f, -1.f, acc, y);
-        put(to + q * 128, lane, y);
+      for (int q = 0; q < kBlocks; q += X) {
+        float acc[2 * X][4], y[2 * X][4];
+        block_product<X>(uK, x * kBlocks + q, zt, lane, acc);
+        update_blocks<X>(own, q, lane, 1.f, -1.f, acc, y);
+        put(to + q * 64, lane, y);
       }
     }
     if (me.mine)
 #pragma unroll 1
-      for (int ks = 0; ks < NK / 2; ++ks) {
+      for (int ks = 0; ks < kBlocks; ++ks) {
         uint32_t s[3][4];
         float y[2][4];
         get_parts(own + ks * 96, lane, s);
         join(s, y[0], y[1]);
-        write_state<2>(a.state_out + me.bh * a.dk * a.dv, x * NK * 8 + 16 * ks, a.dk, a.dv, col, lane, y);
+        write_state(a.state_out + me.bh * a.dk * a.dv, 16 * (x * kBlocks + ks), a.dk, a.dv, col, lane, y);
       }
     return;
   }
 
-  const int ltid = tid - 64 * W, vc = (me.col0 & 63) + 16 * w;  // vc: the tile's columns in the value columns' panel
+  const int ltid = tid - 32 * W * M, z = me.role - M, zg = H == 4 ? 3 - z : z;
+  const int vc = (me.col0 & 63) + 16 * w;  // vc: the tile's columns in the value columns' panel
   const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
     if (lane == 0)
-      request_stage<NK, 3, W>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
+      request_stage<NK, 3, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
           a.by_dy, &maps.dy, w);
     __syncwarp();
   };
@@ -1056,12 +1092,12 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 3, W>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.dy,
+    copy_stage<NK, 3, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.dy,
         ld_y, a.by_dy,
                          ltid);
   };
   const auto ask_m = [&](int c) {
-    if (ltid == 0 && !a.drop) request_m<3>(sm + L::M, bars + 2, a, me.bh * a.n + c);
+    if (ltid == 0 && !a.drop) request_m<3>(sm + L::Mq, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(n - 1);
@@ -1081,32 +1117,34 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
     wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
     wait_copies(bars + 2, it & 1, limit, a);
     if (len - c * kC < kC) {
-      clear_stage<NK, 3, W>(st, a, len - c * kC, a.by_dy, ltid);
+      clear_stage<NK, 3, W, M, H>(st, a, len - c * kC, a.by_dy, ltid);
       __syncthreads();
     }
-    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::M), uY = smem_u32(st + L::V);
+    const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq), uY = smem_u32(st + L::V);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
     uint32_t y[4][1][4];
     if (me.mine) {
-      float R[8][4], l[8][4];
+      float R[8 / H][4], l[8 / H][4];  // the own groups of tokens
       clear(R);
       clear(l);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         a_cols(uY, vc, 16 * ks, lane, y[ks][0]);
 #pragma unroll
-        for (int np = 0; np <= ks; ++np) {
+        for (int i = 0; i < 4 / H; ++i) {
+          const int n = group_of<H>(zg, i);
+          if (n > ks) continue;
           uint32_t r[3][4];
 #pragma unroll
-          for (int p = 0; p < 3; ++p) tri_cols(uM + p * kTri, np, ks, lane, r[p]);
-          products(R, l, np, y[ks], r);
+          for (int p = 0; p < 3; ++p) tri_cols(uM + p * kTri, n, ks, lane, r[p]);
+          products(R, l, i, y[ks], r);
         }
       }
       add(R, l);
-      put(hZ, lane, R);
+      put_tiles<H>(hZ, zg, lane, R);
     }
-    if (me.mine) arrive(three, 96);
-    meet(thirds, 32 * W);  // M has been read
+    if (me.mine) arrive(all, 32 * (M + H));
+    meet(helpers, 32 * W * H);  // M has been read
     if (c > 0) ask_m(c - 1);
     if (!me.mine) continue;
     uint32_t d3[4][3][4];
@@ -1124,18 +1162,18 @@ __global__ void __launch_bounds__(W < 4 ? 96 * W + 32 : 96 * W, 1) gdn_chain_bac
       }
       a_split<3>(d[0], d[1], d3[ks]);
     }
-    meet(read, 96);
+    meet(read, 32 * (M + H));
     const float end = gam[kC - 1];
 #pragma unroll 1
-    for (int q = 0; q < NK / 2; ++q) {
-      float acc[4][4], x[4][4];
-      quad_product(uQ, q, d3, lane, acc);
-      update_quad(hG, q, lane, end, 1.f, acc, x);
+    for (int q = z * (NK / H); q < (z + 1) * (NK / H); q += XH) {
+      float acc[2 * XH][4], x[2 * XH][4];
+      block_product<XH>(uQ, q, d3, lane, acc);
+      update_blocks<XH>(hG, q, lane, end, 1.f, acc, x);
     }
-    meet(three, 96);
-    float Z[8][4];
-    get(hZ, lane, Z);
-    put(reinterpret_cast<float4 *>(a.dz) + (u * tiles + (col >> 4)) * 256, lane, Z);
+    meet(all, 32 * (M + H));
+    float4 *to = reinterpret_cast<float4 *>(a.dz) + (u * tiles + (col >> 4)) * 256 + lane;
+#pragma unroll
+    for (int i = 0; i < 8 / H; ++i) to[tile_of<H>(zg, i) * 32] = hZ[tile_of<H>(zg, i) * 32 + lane];
   }
 }
 
@@ -1769,26 +1807,26 @@ int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, in
   return SDM_OK;
 }
 
-// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its two warps then run on
-// schedulers of their own), else two, else four, which share an SM's tensor cores and the chunk's tiles.
+// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its warps, four for the chain, then
+// run on schedulers of their own), else two, else four, which share an SM's tensor cores and the chunk's tiles.
 int chain_width(const Gdn &a, const Layout &l) {
   const int64_t all = l.tiles * a.B * a.H;
   return all <= kSms || l.tiles == 1 ? 1 : all <= 2 * kSms || l.tiles == 2 ? 2 : 4;
 }
 
-template <int NK, int W>
+template <int NK, int W, int M, int H>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
-  return back ? launch(gdn_chain_back<NK, W>, "gdn_backward", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 3, W>::size,
-      st, a, maps)
-              : launch(gdn_chain<NK, W>, "gdn_train", grid, W < 4 ? 96 * W + 32 : 96 * W, Chain<NK, 2, W>::size, st, a,
-                  maps);
+  return back ? launch(gdn_chain_back<NK, W, M, H>, "gdn_backward", grid, kChainThreads<W, M, H>,
+                       Chain<NK, 3, W, M, H>::size, st, a, maps)
+              : launch(gdn_chain<NK, W, M, H>, "gdn_train", grid, kChainThreads<W, M, H>, Chain<NK, 2, W, M, H>::size,
+                       st, a, maps);
 }
 template <int NK>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int w = chain_width(a, l);
-  return w == 1 ? run_chain<NK, 1>(a, maps, l, back, st)
-         : w == 2 ? run_chain<NK, 2>(a, maps, l, back, st) : run_chain<NK, 4>(a, maps, l, back, st);
+  return w == 1 ? run_chain<NK, 1, 4, 4>(a, maps, l, back, st)
+         : w == 2 ? run_chain<NK, 2, 4, 2>(a, maps, l, back, st) : run_chain<NK, 4, 2, 1>(a, maps, l, back, st);
 }
 
 template <int NK>
