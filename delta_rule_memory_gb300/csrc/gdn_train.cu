@@ -130,11 +130,11 @@ constexpr uint32_t kShortLimit = 1u << 12;  // ... once one has: still far longe
 
 // Wait for a phase of copies.  One that gives up is reported and lets the kernel run to its end, its later
 // waits short.
-__device__ __forceinline__ void wait_copies(uint64_t *bar, uint32_t parity, uint32_t &limit, const Gdn &a) {
-  if (!umma::mbar_wait(smem_u32(bar), parity, limit)) {
-    report_timeout(a.err);
-    limit = kShortLimit;
-  }
+__device__ __forceinline__ bool wait_copies(uint64_t *bar, uint32_t parity, uint32_t &limit, const Gdn &a) {
+  if (umma::mbar_wait(smem_u32(bar), parity, limit)) return true;
+  report_timeout(a.err);
+  limit = kShortLimit;
+  return false;
 }
 
 // Before a kernel's first access to memory: the kernel before it in the stream has ended and its results are
@@ -405,10 +405,11 @@ struct Chain {
                        stage = (sc + 3 * kC * 4 + 1023) / 1024 * 1024;
   // M is read early in a chunk only, so one place does
   static constexpr int Mq = 2 * stage, state = Mq + PM * kTri, parts = state + W * NK * 3 * 512,
-                       tokens = parts + W * 4 * 3 * 512, sums = tokens + W * 8 * 512,
-                       bars = sums + (M == 4 ? W * 4 * 8 * 512 : 0), size = bars + 32;
+                       tokens = parts + W * 4 * 3 * 512, sums = tokens + (PM == 2 ? 2 : 1) * W * 8 * 512,
+                       bars = sums + (M == 4 ? W * 4 * 8 * 512 : 0), size = bars + 48;
 };
-static_assert(Chain<8, 3, 4, 2, 1>::size <= kMaxSmem && Chain<8, 3, 2, 4, 2>::size <= kMaxSmem, "");
+static_assert(Chain<8, 3, 4, 2, 1>::size <= kMaxSmem && Chain<8, 2, 4, 2, 1>::size <= kMaxSmem &&
+                  Chain<8, 2, 2, 4, 2>::size <= kMaxSmem, "");
 template <int W, int M, int H>
 constexpr int kChainThreads = 32 * W * (M + H) + (W < 4 ? 32 : 0);
 
@@ -775,11 +776,13 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   constexpr int NT = 2 * NK, kOwn = 32 * W * (M + H);  // kOwn: threads before the warp that asks for copies
   constexpr int kBlocks = NK / M, X = kBlocks < 2 ? 1 : 2;        // blocks of 16 channels of a warp's; taken at once
   extern __shared__ __align__(1024) unsigned char sm[];
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages, M
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages there, M there, two stages free
   if (threadIdx.x == 0) {
     umma::mbar_init(smem_u32(bars), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 2), 1);
+    umma::mbar_init(smem_u32(bars + 3), W * (M + H));
+    umma::mbar_init(smem_u32(bars + 4), W * (M + H));
     umma::fence_mbar_init();
   }
   before_reading();
@@ -789,13 +792,19 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   const int tiles = (a.dv + 15) >> 4;
   uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96,
       *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
-  uint4 *hU = reinterpret_cast<uint4 *>(sm + L::tokens) + w * 8 * 32;  // U's first two parts
-  float4 *hX = M == 4 ? reinterpret_cast<float4 *>(sm + L::sums) + w * 32 * 32
-                      : reinterpret_cast<float4 *>(hU);  // partial sums, before U
+  uint4 *hU2 = reinterpret_cast<uint4 *>(sm + L::tokens) + w * 8 * 32;  // U's first two parts, of two chunks
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
-  uint32_t limit = kWaitLimit;
-  const int pair = 1 + w, all = 1 + W + w;  // barriers
+  uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // who asks for copies outwaits the others
+  const int pair = 1 + w, all = 1 + W + w, ready = 1 + 2 * W + w;  // barriers
+  const bool together = a.by_qk != 16 || a.by_v != 16;  // tiles that the helping warps copy: all warps meet for them
+  const auto done = [&](int c) {  // this warp has read the chunk's stage
+    __syncwarp();
+    if (lane == 0) umma::mbar_arrive(smem_u32(bars + 3 + (c & 1)));
+  };
+  // ... and so have all others; where that is not seen, nothing more is asked for
+  bool ask = true;
+  const auto wait_done = [&](int c) { ask = ask && wait_copies(bars + 3 + (c & 1), (c >> 1) & 1, limit, a); };
 
   if (me.role < M) {
     const int x = me.role, vp = ((me.col0 & 63) >> 3) + 2 * w;  // vp: the tile's pieces of the value columns' panel
@@ -804,11 +813,18 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     read_state(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
 #pragma unroll
     for (int ks = 0; ks < kBlocks; ++ks) put_parts(own + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
+    if (me.mine && n > 0) arrive(ready, 32 * (M + H));  // the state's parts are there
     for (int c = 0; c < n; ++c) {
-      __syncthreads();
+      if (together) __syncthreads();
       wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
       if (len - c * kC < kC) __syncthreads();  // the helping warps clear rows
-      if (!me.mine) continue;
+      if (!me.mine) {
+        done(c);
+        continue;
+      }
+      uint4 *hU = hU2 + (c & 1) * W * 8 * 32;
+      float4 *hX = M == 4 ? reinterpret_cast<float4 *>(sm + L::sums) + w * 32 * 32
+                          : reinterpret_cast<float4 *>(hU);  // partial sums, before U
       unsigned char *st = sm + (c & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K), uV = smem_u32(st + L::V);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
@@ -866,6 +882,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
 #pragma unroll
         for (int i = 0; i < X; ++i) put_parts(own + (q + i) * 96, lane, S[2 * (q + i)], S[2 * (q + i) + 1]);
       }
+      if (c + 1 < n) arrive(ready, 32 * (M + H));
+      done(c);
     }
     if (me.mine) write_state(a.state_out + me.bh * a.dk * a.dv, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
     return;
@@ -874,17 +892,18 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   // of four, those with many of the triangle's blocks run beside chain warps with few
   const int ltid = tid - 32 * W * M, z = me.role - M, zg = H == 4 ? 3 - z : z;
   const auto request = [&](int c) {
-    if (lane == 0)
+    if (lane == 0 && ask)
       request_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h,
           me.col0, a.by_v,
                               &maps.v, w);
     __syncwarp();
   };
-  const auto ask_m = [&](int c) { if (!a.drop) request_m<2>(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
+  const auto ask_m = [&](int c) { if (ask && !a.drop) request_m<2>(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
   if (tid >= kOwn) {
     for (int c = 0; c <= n; ++c) {
-      if (c > 0) __syncthreads();
-      if (c > 0 && lane == 0) ask_m(c - 1);  // every helping warp is done with the chunk before
+      if (c > 0 && together) __syncthreads();
+      if (c > 1) wait_done(c - 2);
+      if (lane == 0 && c != 1 && n > 0) ask_m(c == 0 ? 0 : c - 1);  // of chunk 0 at once
       if (c < n) request(c);
       if (c > 0 && len - (c - 1) * kC < kC) __syncthreads();
     }
@@ -896,24 +915,35 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
         a.by_v, ltid);
   };
   if (n > 0) {
-    if (kAskers<W> > 1) request(0);
-    copy(0);
+    if (kAskers<W> > 1) {
+      request(0);
+      if (ltid == 0) ask_m(0);
+    }
+    if (together) copy(0);
   }
   for (int c = 0; c < n; ++c) {
     unsigned char *st = sm + (c & 1) * L::stage;
-    cp_async_wait<0>();
-    __syncthreads();
-    if (c + 1 < n) {
-      if (kAskers<W> > 1) request(c + 1);
-      copy(c + 1);
+    if (together) {
+      cp_async_wait<0>();
+      __syncthreads();
+      if (c + 1 < n) copy(c + 1);
     }
-    if (kAskers<W> > 1 && ltid == 0) ask_m(c);  // every helping warp is done with the chunk before
+    if (kAskers<W> > 1 && c > 0) {
+      wait_done(c - 1);
+      if (ltid == 0) ask_m(c);
+    }
+    if (kAskers<W> > 1 && c + 1 < n) request(c + 1);
     wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
       clear_stage<NK, 2, W, M, H>(st, a, len - c * kC, a.by_v, ltid);
       __syncthreads();
     }
-    if (!me.mine) continue;
+    if (!me.mine) {
+      done(c);
+      continue;
+    }
+    const uint4 *hU = hU2 + (c & 1) * W * 8 * 32;
+    meet(ready, 32 * (M + H));
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
     float Y[8 / H][4];  // the own groups of tokens
@@ -951,22 +981,28 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
         products(Y, Y, i, us, r);
       }
     }
+    done(c);
     // y, rounded once: pairs of tokens turned into pairs of columns
+    uint32_t v[8 / H][2];
+#pragma unroll
+    for (int i = 0; i < 8 / H; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) v[i][x] = transpose8(pack2(Y[i][2 * x], Y[i][2 * x + 1]));
     uint16_t *yc = a.y + (me.tok * a.H + h) * a.dv + col + 2 * t;
     const int left = a.dv - col - 2 * t;
+    const int64_t ld_y = static_cast<int64_t>(a.H) * a.dv;
 #pragma unroll
     for (int nt = 0; nt < 8 / H; ++nt) {
       const int i = c * kC + 8 * tile_of<H>(zg, nt) + g;
-      uint16_t *row = yc + i * (static_cast<int64_t>(a.H) * a.dv);
+      if (i >= len) continue;
+      uint16_t *row = yc + i * ld_y;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t v = transpose8(pack2(Y[nt][2 * x], Y[nt][2 * x + 1]));
-        if (i >= len) continue;
         if (a.pair_y) {
-          if (8 * x < left) *reinterpret_cast<uint32_t *>(row + 8 * x) = v;
+          if (8 * x < left) *reinterpret_cast<uint32_t *>(row + 8 * x) = v[nt][x];
         } else {
-          if (8 * x < left) row[8 * x] = static_cast<uint16_t>(v);
-          if (8 * x + 1 < left) row[8 * x + 1] = static_cast<uint16_t>(v >> 16);
+          if (8 * x < left) row[8 * x] = static_cast<uint16_t>(v[nt][x]);
+          if (8 * x + 1 < left) row[8 * x + 1] = static_cast<uint16_t>(v[nt][x] >> 16);
         }
       }
     }
@@ -980,11 +1016,13 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   constexpr int NT = 2 * NK, kOwn = 32 * W * (M + H);
   constexpr int kBlocks = NK / M, X = kBlocks < 2 ? 1 : 2, XH = NK / H < 2 ? 1 : 2;
   extern __shared__ __align__(1024) unsigned char sm[];
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages, M
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages there, M there, two stages free
   if (threadIdx.x == 0) {
     umma::mbar_init(smem_u32(bars), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 2), 1);
+    umma::mbar_init(smem_u32(bars + 3), W * (M + H));
+    umma::mbar_init(smem_u32(bars + 4), W * (M + H));
     umma::fence_mbar_init();
   }
   before_reading();
@@ -999,8 +1037,15 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
-  uint32_t limit = kWaitLimit;
+  uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // who asks for copies outwaits the others
   const int pair = 1 + w, all = 1 + W + w, read = 1 + 2 * W + w, helpers = 1 + 3 * W;
+  const bool together = a.by_qk != 16 || a.by_dy != 16;
+  const auto done = [&](int it) {
+    __syncwarp();
+    if (lane == 0) umma::mbar_arrive(smem_u32(bars + 3 + (it & 1)));
+  };
+  bool ask = true;
+  const auto wait_done = [&](int it) { ask = ask && wait_copies(bars + 3 + (it & 1), (it >> 1) & 1, limit, a); };
 
   if (me.role < M) {
     const int x = me.role;
@@ -1018,10 +1063,13 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
     }
     for (int c = n - 1; c >= 0; --c) {
       const int it = n - 1 - c;
-      __syncthreads();
+      if (together) __syncthreads();
       wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
       if (len - c * kC < kC) __syncthreads();  // the helping warps clear rows
-      if (!me.mine) continue;
+      if (!me.mine) {
+        done(it);
+        continue;
+      }
       unsigned char *st = sm + (it & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
@@ -1030,6 +1078,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       {
         float d[8][4];
         state_product<kBlocks, 1>(own, uK, x * kBlocks * 16, lane, d);
+        if (M == 2) meet(pair, 32 * M);  // the parts, in whose place the sums go, have been read
         give_sums<M>(hX, x, lane, d, U);
       }
       arrive(read, 32 * (M + H));  // G has been read
@@ -1059,6 +1108,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
         update_blocks<X>(own, q, lane, 1.f, -1.f, acc, y);
         put(to + q * 64, lane, y);
       }
+      done(it);
     }
     if (me.mine)
 #pragma unroll 1
@@ -1076,7 +1126,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   const int vc = (me.col0 & 63) + 16 * w;  // vc: the tile's columns in the value columns' panel
   const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
-    if (lane == 0)
+    if (lane == 0 && ask)
       request_stage<NK, 3, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
           a.by_dy, &maps.dy, w);
     __syncwarp();
@@ -1084,7 +1134,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   if (tid >= kOwn) {
     for (int it = 0; it <= n; ++it) {
       const int c = n - 1 - it;
-      if (it > 0) __syncthreads();
+      if (it > 0 && together) __syncthreads();
+      if (it > 1) wait_done(it - 2);
       if (it < n) request(c);
       if (it > 0 && len - (c + 1) * kC < kC) __syncthreads();
     }
@@ -1102,17 +1153,20 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   if (n > 0) {
     if (kAskers<W> > 1) request(n - 1);
     ask_m(n - 1);
-    copy(n - 1);
+    if (together) copy(n - 1);
   }
   for (int c = n - 1; c >= 0; --c) {
     const int it = n - 1 - c;
     const int64_t u = me.bh * a.n + c;
     unsigned char *st = sm + (it & 1) * L::stage;
-    cp_async_wait<0>();
-    __syncthreads();
-    if (c > 0) {
-      if (kAskers<W> > 1) request(c - 1);
-      copy(c - 1);
+    if (together) {
+      cp_async_wait<0>();
+      __syncthreads();
+      if (c > 0) copy(c - 1);
+    }
+    if (kAskers<W> > 1 && c > 0) {
+      if (it > 0) wait_done(it - 1);
+      request(c - 1);
     }
     wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
     wait_copies(bars + 2, it & 1, limit, a);
@@ -1146,7 +1200,10 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
     if (me.mine) arrive(all, 32 * (M + H));
     meet(helpers, 32 * W * H);  // M has been read
     if (c > 0) ask_m(c - 1);
-    if (!me.mine) continue;
+    if (!me.mine) {
+      done(it);
+      continue;
+    }
     uint32_t d3[4][3][4];
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
@@ -1170,6 +1227,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       block_product<XH>(uQ, q, d3, lane, acc);
       update_blocks<XH>(hG, q, lane, end, 1.f, acc, x);
     }
+    done(it);
     meet(all, 32 * (M + H));
     float4 *to = reinterpret_cast<float4 *>(a.dz) + (u * tiles + (col >> 4)) * 256 + lane;
 #pragma unroll
