@@ -411,13 +411,14 @@ struct Chain {
 static_assert(Chain<8, 3, 4, 2, 1>::size <= kMaxSmem && Chain<8, 2, 4, 2, 1>::size <= kMaxSmem &&
                   Chain<8, 2, 2, 4, 2>::size <= kMaxSmem, "");
 template <int W, int M, int H>
-constexpr int kChainThreads = 32 * W * (M + H) + (W < 4 ? 32 : 0);
+constexpr int kChainThreads = 32 * W * (M + H) + (W == 1 ? 32 : 0);
 
 // A chunk's tiles into a stage; cols: the value columns' tensor.  What tensor and bulk copies bring is asked
-// for by one lane of a warp of its own or, where a CTA has four tiles and no room for another warp's registers,
-// by one lane of each of the second warps (a request holds its warp for a hundred cycles and more).
+// for by one lane of a warp of its own or, where a CTA has more tiles than one, whose warps need its registers,
+// by one lane of each of the four helping warps (a request holds its warp for a hundred cycles and more; with
+// one tile they are what the chain waits for: 794 us in place of 750 backward at B = 1, T = 16384, H = 8).
 template <int W>
-constexpr int kAskers = W < 4 ? 1 : 4;
+constexpr int kAskers = W == 1 ? 1 : 4;
 
 template <int NK, int PM, int W, int M, int H>
 __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps,
@@ -425,6 +426,7 @@ __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, 
                                               const CUtensorMap *cols_map, int who) {
   using L = Chain<NK, PM, W, M, H>;
   constexpr bool all = kAskers<W> == 1;
+  static_assert(all || W * H == kAskers<W>, "");
   const uint32_t mb = smem_u32(bar);
   const int hk = h / (a.H / a.Hk), token = static_cast<int>(tok);
   const bool qk = a.by_qk == 16, cols = by_cols == 16;
@@ -547,16 +549,6 @@ __device__ __forceinline__ void join(const uint32_t (&s)[3][4], float (&c0)[4], 
     c[2 * (i & 1) + 1] = high2(s[0][i]) + (high2(s[1][i]) + high2(s[2][i]));
   }
 }
-// x[nt][.] *= f[token]: a token-wise factor on an accumulator whose columns are tokens
-template <int N>
-__device__ __forceinline__ void scale_tokens(float (&x)[N][4], const float *f, int t) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float2 v = *reinterpret_cast<const float2 *>(f + 8 * i + 2 * t);
-    x[i][0] *= v.x, x[i][1] *= v.y, x[i][2] *= v.x, x[i][3] *= v.y;
-  }
-}
-
 // d (the leading parts' product) and l (the others') += A B for n-tiles 2 np and 2 np + 1, over the parts whose
 // numbers sum up to less than max(PA, PB): what the others hold is below the last bit kept.  The tensor cores
 // cut sums off where an addition would round; kept apart, the many small products do so at their own size.
@@ -653,11 +645,6 @@ __device__ __forceinline__ constexpr int group_of(int x, int i) {
 }
 template <int N>
 __device__ __forceinline__ constexpr int tile_of(int x, int i) { return 2 * group_of<N>(x, i >> 1) + (i & 1); }
-// whether group n is one of warp x's
-template <int N>
-__device__ __forceinline__ constexpr bool has_group(int x, int n) {
-  return N == 1 || (N == 4 ? n == x : (n == 0 || n == 3) == (x == 0));
-}
 // Sums over all tokens, a part of them with each of M warps: the own groups' n-tiles, and the others' through
 // shared memory (of two warps eight tiles, each written by the one that does not keep it; of four all of them)
 template <int M>
@@ -745,11 +732,13 @@ __device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tr
 }
 
 // a tile's first M warps, or all of them, meet
-__device__ __forceinline__ void meet(int id, int threads) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads)
-    : "memory"); }
+__device__ __forceinline__ void meet(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
 // ... or only tell the others that they are there
-__device__ __forceinline__ void arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id),
-    "r"(threads) : "memory"); }
+__device__ __forceinline__ void arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
 
 // where a warp of a chain stands
 template <int W>
@@ -795,7 +784,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   uint4 *hU2 = reinterpret_cast<uint4 *>(sm + L::tokens) + w * 8 * 32;  // U's first two parts, of two chunks
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
-  uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // who asks for copies outwaits the others
+  uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // a warp that only asks for copies outwaits the others
   const int pair = 1 + w, all = 1 + W + w, ready = 1 + 2 * W + w;  // barriers
   const bool together = a.by_qk != 16 || a.by_v != 16;  // tiles that the helping warps copy: all warps meet for them
   const auto done = [&](int c) {  // this warp has read the chunk's stage
@@ -836,27 +825,28 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
         state_product<kBlocks, kBlocks>(own, uK, x * kBlocks * 16, lane, d);
         give_sums<M>(hX, x, lane, d, Z);
       }
+      uint32_t v[4 / M][4];
+#pragma unroll
+      for (int i = 0; i < 4 / M; ++i)  // tile[token][column]: rows of V^T are its columns
+        ldsm4_t(uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v[i]);
       meet(pair, 32 * M);
       take_sums<M>(hX, x, lane, Z);
       // Z^T = V^T - gam S^T K^T
 #pragma unroll
       for (int i = 0; i < 4 / M; ++i) {
-        uint32_t v[4];
-        // tile[token][column]: rows of V^T are its columns
-        ldsm4_t(uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float2 gm = *reinterpret_cast<const float2 *>(gam + 8 * tile_of<M>(x, 2 * i + j) + 2 * t);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t vv = v[2 * j + (e >> 1)];
+            const uint32_t vv = v[i][2 * j + (e >> 1)];
             Z[2 * i + j][e] = fmaf(e & 1 ? -gm.y : -gm.x, Z[2 * i + j][e], e & 1 ? high2(vv) : low2(vv));
           }
         }
       }
+      float E[8 / M][4];
       put_groups<M>(hP, x, lane, Z);
       meet(pair, 32 * M);
-      float E[8 / M][4];
       triangle_product<false, M>(hP, smem_u32(st + L::T), x, lane, E);
       put_tiles<M>(reinterpret_cast<float4 *>(a.e) + at * 256, x, lane, E);
       scale_groups<M>(E, x, beta, t);
@@ -893,9 +883,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   const int ltid = tid - 32 * W * M, z = me.role - M, zg = H == 4 ? 3 - z : z;
   const auto request = [&](int c) {
     if (lane == 0 && ask)
-      request_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC, h,
-          me.col0, a.by_v,
-                              &maps.v, w);
+      request_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC,
+                                    h, me.col0, a.by_v, &maps.v, ltid >> 5);
     __syncwarp();
   };
   const auto ask_m = [&](int c) { if (ask && !a.drop) request_m<2>(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
@@ -911,8 +900,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v, a.ld_v,
-        a.by_v, ltid);
+    copy_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v,
+                               a.ld_v, a.by_v, ltid);
   };
   if (n > 0) {
     if (kAskers<W> > 1) {
@@ -928,22 +917,24 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       __syncthreads();
       if (c + 1 < n) copy(c + 1);
     }
-    if (kAskers<W> > 1 && c > 0) {
-      wait_done(c - 1);
-      if (ltid == 0) ask_m(c);
-    }
-    if (kAskers<W> > 1 && c + 1 < n) request(c + 1);
     wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
       clear_stage<NK, 2, W, M, H>(st, a, len - c * kC, a.by_v, ltid);
       __syncthreads();
+    }
+    if (me.mine) meet(ready, 32 * (M + H));
+    if (kAskers<W> > 1) {
+      if (c > 0) {
+        wait_done(c - 1);
+        if (ltid == 0) ask_m(c);
+      }
+      if (c + 1 < n) request(c + 1);
     }
     if (!me.mine) {
       done(c);
       continue;
     }
     const uint4 *hU = hU2 + (c & 1) * W * 8 * 32;
-    meet(ready, 32 * (M + H));
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
     float Y[8 / H][4];  // the own groups of tokens
@@ -966,19 +957,38 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       scale_groups<H>(Y, zg, gam, t);
     }
     wait_copies(bars + 2, c & 1, limit, a);
-    meet(all, 32 * (M + H));
+    if constexpr (H == 4) {  // += U^T M^T, M's fragments read before U is there
+      uint32_t r[4][2][4], us[4][2][4];
+      float l[2][4];
+      clear(l);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {  // += U^T M^T
-      uint32_t us[2][4];
-      get_parts(hU + ks * 64, lane, us);
+      for (int ks = 0; ks < 4; ++ks)
+        if (ks <= zg)
 #pragma unroll
-      for (int i = 0; i < 4 / H; ++i) {
-        const int n = group_of<H>(zg, i);
-        if (n < ks) continue;
-        uint32_t r[2][4];
+          for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, zg, ks, lane, r[ks][p]);
+      meet(all, 32 * (M + H));
 #pragma unroll
-        for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, n, ks, lane, r[p]);
-        products(Y, Y, i, us, r);
+      for (int ks = 0; ks < 4; ++ks)
+        if (ks <= zg) get_parts(hU + ks * 64, lane, us[ks]);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        if (ks <= zg) products(Y, l, 0, us[ks], r[ks]);
+      add(Y, l);
+    } else {
+      meet(all, 32 * (M + H));
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t us[2][4];
+        get_parts(hU + ks * 64, lane, us);
+#pragma unroll
+        for (int i = 0; i < 4 / H; ++i) {
+          const int n = group_of<H>(zg, i);
+          if (n < ks) continue;
+          uint32_t r[2][4];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, n, ks, lane, r[p]);
+          products(Y, Y, i, us, r);
+        }
       }
     }
     done(c);
@@ -1037,7 +1047,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   float4 *hZ = reinterpret_cast<float4 *>(sm + L::tokens) + w * 8 * 32;  // dY^T M, then dZ^T
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
-  uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // who asks for copies outwaits the others
+  uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // a warp that only asks for copies outwaits the others
   const int pair = 1 + w, all = 1 + W + w, read = 1 + 2 * W + w, helpers = 1 + 3 * W;
   const bool together = a.by_qk != 16 || a.by_dy != 16;
   const auto done = [&](int it) {
@@ -1077,7 +1087,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       float U[8 / M][4], Z[8 / M][4];
       {
         float d[8][4];
-        state_product<kBlocks, 1>(own, uK, x * kBlocks * 16, lane, d);
+        state_product<kBlocks, W < 4 ? kBlocks : 1>(own, uK, x * kBlocks * 16, lane, d);
         if (M == 2) meet(pair, 32 * M);  // the parts, in whose place the sums go, have been read
         give_sums<M>(hX, x, lane, d, U);
       }
@@ -1128,7 +1138,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
     const int s = (n - 1 - c) & 1;
     if (lane == 0 && ask)
       request_stage<NK, 3, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
-          a.by_dy, &maps.dy, w);
+          a.by_dy, &maps.dy, ltid >> 5);
     __syncwarp();
   };
   if (tid >= kOwn) {
@@ -1143,9 +1153,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 3, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.dy,
-        ld_y, a.by_dy,
-                         ltid);
+    copy_stage<NK, 3, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC),
+                               a.dy, ld_y, a.by_dy, ltid);
   };
   const auto ask_m = [&](int c) {
     if (ltid == 0 && !a.drop) request_m<3>(sm + L::Mq, bars + 2, a, me.bh * a.n + c);
@@ -1163,10 +1172,6 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       cp_async_wait<0>();
       __syncthreads();
       if (c > 0) copy(c - 1);
-    }
-    if (kAskers<W> > 1 && c > 0) {
-      if (it > 0) wait_done(it - 1);
-      request(c - 1);
     }
     wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
     wait_copies(bars + 2, it & 1, limit, a);
@@ -1197,10 +1202,16 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       add(R, l);
       put_tiles<H>(hZ, zg, lane, R);
     }
+    const auto next = [&] {  // the next chunk's copies, once the stage is free
+      if (kAskers<W> == 1 || c == 0) return;
+      if (it > 0) wait_done(it - 1);
+      request(c - 1);
+    };
     if (me.mine) arrive(all, 32 * (M + H));
     meet(helpers, 32 * W * H);  // M has been read
     if (c > 0) ask_m(c - 1);
     if (!me.mine) {
+      next();
       done(it);
       continue;
     }
@@ -1219,6 +1230,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       }
       a_split<3>(d[0], d[1], d3[ks]);
     }
+    next();
     meet(read, 32 * (M + H));
     const float end = gam[kC - 1];
 #pragma unroll 1
@@ -1324,9 +1336,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, w = tid >> 5, quarter = w & 3, upper = w >> 2, lane = tid & 31, g = lane >> 2,
       t = lane & 3;
-  const int64_t u = blockIdx.x, bh = u / a.n;
-  const int c = static_cast<int>(u - bh * a.n), b = static_cast<int>(bh / a.H),
-      h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  const unsigned heads = static_cast<unsigned>(a.B) * a.H;
+  const int c = static_cast<int>(blockIdx.x / heads), bh32 = static_cast<int>(blockIdx.x % heads), b = bh32 / a.H, h = bh32 - b * a.H;
+  const int64_t bh = bh32, u = bh * a.n + c;
   before_reading();
   const int live = min(length_of(a, b) - c * kC, kC);
   if (live <= 0) return;
