@@ -1271,7 +1271,8 @@ struct Grad {
   static constexpr int YZ = 0, Zl = YZ + 8192 /* zeros | the second part of dZ */, U = Zl + 8192, Ut = U + 3 * 4096,
                        S = Ut + 2 * 4096, G = S + 3 * 8192, K = G + 2 * 8192, Q = K + 16384, sc = Q + 16384,
                        rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */,
-                       flow = rows + 4 * kC * 4 /* [4][64] */, red = flow + 4 * kC * 4, bars = red + 32, size = bars + 16;
+                       flow = rows + 4 * kC * 4 /* [4][64] */, red = flow + 4 * kC * 4, bars = red + 32, size = bars + 32;
+  static constexpr int stage = K;  // a piece of the states, until K and Q take its place
   static constexpr int X = 0, N = X + 3 * 8192;  // once the value columns are done
   static constexpr uint32_t dQ1 = 0, dKa = 64, dKb = 128, XN = 192, dQ2 = 192, columns = 256;  // tensor memory
 };
@@ -1349,28 +1350,27 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   float *rows = reinterpret_cast<float *>(sm + L::rows), *flow = reinterpret_cast<float *>(sm + L::flow),
         *red = reinterpret_cast<float *>(sm + L::red);
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::bars);
-  uint32_t *holder = reinterpret_cast<uint32_t *>(bar + 1);
-  const uint32_t mb = smem_u32(bar);
+  uint32_t *holder = reinterpret_cast<uint32_t *>(bar + 2);
+  const uint32_t mb = smem_u32(bar), full = smem_u32(bar + 1), base = smem_u32(sm);
 
-  // a piece's share of this thread, read ahead: of tile `upper` of the two, key channels 8 NW quarter .. and
-  // tokens 16 quarter .. + 15
-  float4 fs[NW], f0[NW], f1[NW];
+  // Two tiles of S at the chunk's start and G at its end by bulk copies, a piece ahead; the rest of a piece into
+  // registers: of tile `upper` of the two, key channels 8 NW quarter .. and tokens 16 quarter .. + 15
+  const auto ask_states = [&](int c0) {
+    const int ct = c0 >> 4;
+    const uint32_t bytes = min(2, tiles - ct) * NT * 512;
+    mbar_expect_tx(full, 2 * bytes);
+    bulk_g2s(base + L::stage, a.s + (u * tiles + ct) * (NT * 128), bytes, full);
+    bulk_g2s(base + L::stage + NT * 1024, a.g + ((bh * (a.n + 1) + c + 1) * tiles + ct) * (NT * 128), bytes, full);
+  };
+  float4 f0[NW];
   float E[2][4], Z[2][4];
   uint32_t yv[2][2], vv[2][2];  // dy and v [n-tile][columns 0..7, 8..15]: a row's pair a lane
-  const auto read_states = [&](int c0) {
+  const auto read_start = [&](int c0) {  // G at the chunk's start
     const int ct = (c0 >> 4) + upper;
-    const bool on = ct < tiles;
-    const float4 *S = reinterpret_cast<const float4 *>(a.s) + ((u * tiles + ct) * NT + quarter * NW) * 32 + lane;
     const float4 *G = reinterpret_cast<const float4 *>(a.g) +
         (((bh * (a.n + 1) + c) * tiles + ct) * NT + quarter * NW) * 32 + lane;
-    const float4 *G1 = G + static_cast<int64_t>(tiles) * NT * 32;
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int x = 0; x < NW; ++x) {
-      fs[x] = on ? S[x * 32] : zero;
-      f1[x] = on ? G1[x * 32] : zero;
-      f0[x] = on ? G[x * 32] : zero;
-    }
+    for (int x = 0; x < NW; ++x) f0[x] = ct < tiles ? G[x * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   const auto read_tokens = [&](int c0) {
     const int ct = (c0 >> 4) + upper;
@@ -1392,17 +1392,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         vv[x][e] = load_pair(a.v + (tok + i) * a.ld_v + h * a.dv + cc, left, a.by_v >= 4);
       }
   };
-  read_states(0);
-  load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-  load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  if (tid == 0) {
+    mbar_init(mb, 1);
+    mbar_init(full, 1);
+    fence_mbar_init();
+    ask_states(0);
+  }
+  read_start(0);
   if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
   cp_async_commit();
   read_tokens(0);
 
-  if (tid == 0) {
-    mbar_init(mb, 1);
-    fence_mbar_init();
-  }
   if (w == 0) tmem_alloc(smem_u32(holder), L::columns);
   // the half of zeros beside dZ's second part
   {
@@ -1415,18 +1415,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   tc_fence_after();
   const uint32_t tmem = *holder;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-  bool ok = true;
+  bool ok = true, there = true;
   uint32_t phase = 0;
   // every thread waits for the products asked for; then the CTA agrees
   const auto products_done = [&]() {
-    ok = mbar_wait(mb, phase & 1, kWaitLimit);
+    ok = mbar_wait(mb, phase & 1, kWaitLimit) && there;
     ++phase;
     tc_fence_before();
     ok = __syncthreads_and(ok) != 0;
     tc_fence_after();
     return ok;
   };
-  const uint32_t base = smem_u32(sm);
   // A and B with rows of 8 along M and N; N = 64 and 128
   const uint32_t mn = (1u << 15) | (1u << 16);
   const uint32_t id64 = idesc_bf16_f32(128, 64) | mn, id128 = idesc_bf16_f32(128, 128) | mn;
@@ -1435,14 +1434,20 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   for (int c0 = 0; c0 < a.dv; c0 += 32) {
     if (c0 && !products_done()) break;  // the piece before has been read
     // ---- the states
+    there = mbar_wait(full, (c0 >> 5) & 1, kWaitLimit) && there;
 #pragma unroll
     for (int x = 0; x < NW; ++x) {
-      anchor += (fs[x].x * f0[x].x + fs[x].y * f0[x].y) + (fs[x].z * f0[x].z + fs[x].w * f0[x].w);
+      float4 fs = make_float4(0.f, 0.f, 0.f, 0.f), f1 = fs;
+      if ((c0 >> 4) + upper < tiles) {
+        const float4 *st = reinterpret_cast<const float4 *>(sm + L::stage) + (upper * NT + quarter * NW + x) * 32 + lane;
+        fs = st[0], f1 = st[NT * 64];
+      }
+      anchor += (fs.x * f0[x].x + fs.y * f0[x].y) + (fs.z * f0[x].z + fs.w * f0[x].w);
       uint32_t p0[3], p1[3], q0[2], q1[2];
-      split<3>(fs[x].x, fs[x].y, p0);
-      split<3>(fs[x].z, fs[x].w, p1);
-      split<2>(f1[x].x, f1[x].y, q0);
-      split<2>(f1[x].z, f1[x].w, q1);
+      split<3>(fs.x, fs.y, p0);
+      split<3>(fs.z, fs.w, p1);
+      split<2>(f1.x, f1.y, q0);
+      split<2>(f1.z, f1.w, q1);
       unsigned char *o = sm + upper * 4096 + (quarter * NW + x) * 128 + lane * 4;
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
@@ -1455,7 +1460,21 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         *reinterpret_cast<uint32_t *>(o + L::G + p * 8192 + 2048) = q1[p];
       }
     }
-    if (c0 + 32 < a.dv) read_states(c0 + 32);
+    if (c0 + 32 < a.dv) {
+      read_start(c0 + 32);
+      if (w == 0) {  // once every warp has read the stage
+        asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        if (lane == 0) ask_states(c0 + 32);
+        __syncwarp();
+      } else {
+        asm volatile("bar.arrive 1, 256;\n" ::: "memory");
+      }
+    } else {
+      __syncthreads();
+      load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+      load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+      cp_async_commit();
+    }
     // ---- U, tail U, dZ, dy; dv; the sums over value columns
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -1548,6 +1567,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   for (int o = 16; o; o >>= 1) anchor += __shfl_xor_sync(kFull, anchor, o);
   if (lane == 0) red[w] = anchor;
 
+  cp_async_wait<0>();
   if (ok && products_done()) {
     // ---- X (lanes 0..63) and N (64..127) times their decays: row i, columns 32 upper ..
     {
