@@ -1469,11 +1469,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       } else {
         asm volatile("bar.arrive 1, 256;\n" ::: "memory");
       }
-    } else {
-      __syncthreads();
-      load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-      load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-      cp_async_commit();
     }
     // ---- U, tail U, dZ, dy; dv; the sums over value columns
 #pragma unroll
@@ -1547,6 +1542,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       mma_commit(mb);
     }
   }
+  load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+  load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+  cp_async_commit();
   // sums over the columns of 16 tokens, and over the state
 #pragma unroll
   for (int x = 0; x < 2; ++x)
