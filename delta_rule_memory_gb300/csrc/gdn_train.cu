@@ -23,9 +23,9 @@
 //   da_t = <S, G_start> - sum over s < t of (q_s . dq_s - v_s . dv_s)
 // (the first term only before the chunk's first reset, the sum from the document's start on).
 //
-// Kernels.  gdn_prep (every chunk by itself): the decays, T and M.  gdn_chain: chunk after chunk, three warps a
-// tile of 16 value columns; every product of a chunk takes the one before as its A operand from registers or as
-// parts in shared memory (mma.cuh), and the chunk's tiles are copied a chunk ahead.  gdn_chain_back: the same
+// Kernels.  gdn_prep (every chunk by itself): the decays, T and M.  gdn_chain: chunk after chunk, three to eight
+// warps a tile of 16 value columns; every product of a chunk takes the one before as its A operand from registers
+// or as parts in shared memory (mma.cuh), and the chunk's tiles are copied a chunk ahead.  gdn_chain_back: the same
 // with G, last chunk to first.  gdn_grad: everything that needs sums over the value columns, every chunk by
 // itself, on tcgen05. The chains use mma.sync: a product there is 64 x 128 x 16 and feeds the next one, so
 // through tensor memory each would be read back, split into bf16 parts and stored before the next could start,
@@ -35,7 +35,7 @@
 // parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da, dbeta); in two parts,
 // 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
 //
-// B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 86 us, gdn_chain 345, gdn_chain_back 397, gdn_grad 400.
+// B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 86 us, gdn_chain 318, gdn_chain_back 383, gdn_grad 360.
 #include <cuda.h>
 
 #include <algorithm>
@@ -390,13 +390,15 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 // what the next chunk waits for, each with its share of the key channels (the sums with the state and its
 // update) and of the four groups of 16 tokens (of two warps, 0 and 3, or 1 and 2, the same number of the
 // triangle's blocks): sums over all channels and a triangle's products meet in shared memory.  The H others do
-// everything else: y, the products with dy, what is kept for later, copies.  A tile's state lives in shared memory as its three bf16 parts,
-// which are all 24 bits of it, in the order of the A fragments that every product with it takes. Bound by
-// latency where a tile has an SM to itself (2.6 us a chunk forward, 3.4 backward at dk = dv = 128; one warp a
-// tile took 7.6 and 6.5, a second one for what can wait, with copies by TMA, 3.6 and 4.7). Where four tiles
-// share an SM (5.4 and 6.2 us a chunk) by shared memory and the tensor cores beside each other, about 5,900 of
-// 10,500 cycles each: mma.sync runs at 600 TFLOP/s.  Loops are kept small: unrolled four times the backward chain is
-// a fifth slower, its instructions no longer at hand.
+// everything else: y, the products with dy, copies.  Warps meet by named barriers, only where one needs what
+// another wrote; a stage of copies is asked for again once all have left it.  A tile's state lives in shared
+// memory as its three bf16 parts, which are all 24 bits of it, in the order of the A fragments that every
+// product with it takes.
+// Bound by latency where a tile has an SM to itself (M = H = 4; 1.75 us a chunk forward, 1.96 backward at dk =
+// dv = 128; M = 2 and H = 1, all warps meeting once a chunk, took 2.6 and 3.4, one warp for everything 7.6 and
+// 6.5).  Where four tiles share an SM (M = 2, H = 1; 5.0 and 6.0 us a chunk) by the tensor cores, about 6,000 of
+// 9,700 and 6,500 of 11,700 cycles, and shared memory beside them: mma.sync runs at 600 TFLOP/s.  Loops are kept
+// small: unrolled four times the backward chain is a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
 template <int NK, int PM, int W, int M, int H>  // PM: parts of the chunk's M
 struct Chain {
@@ -828,7 +830,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       uint32_t v[4 / M][4];
 #pragma unroll
       for (int i = 0; i < 4 / M; ++i)  // tile[token][column]: rows of V^T are its columns
-        ldsm4_t(uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v[i]);
+        ldsm4_t(uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)),
+                v[i]);
       meet(pair, 32 * M);
       take_sums<M>(hX, x, lane, Z);
       // Z^T = V^T - gam S^T K^T
@@ -1255,14 +1258,14 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
 // and then, with X and N times their decays,
 //   dQ2^T = K^T X^T,   dKb^T += Q^T X + K^T (N^T + N),
 //   dQ = gam dQ1 + dQ2,   dK = dKb - gam dKa.
-// The value columns come 32 at a time: read as the chains left them (16 bytes a lane, read ahead by a piece),
-// split into bf16 parts and stored as the 8 x 8 cores of the operands, where a warp's store is 128 bytes in a
-// row.  All operands have their rows of 8 along M or N (MN-major); X and N serve both ways as they lie. A CTA
+// The value columns come 32 at a time, as the chains left them, read ahead by a piece: the states of two kinds by
+// bulk copies (through registers alone, whose loads wait for one another at the door, 404 us in place of 360),
+// the rest 16 bytes a lane.  They are split into bf16 parts and stored as the 8 x 8 cores of the operands, where
+// a warp's store is 128 bytes in a row.  K and Q come last, in the states' place.  All operands have their rows of 8 along M or N (MN-major); X and N serve both ways as they lie. A CTA
 // needs half of an SM's shared memory, registers and tensor memory, so that one's conversions run beside the
-// other's products.  A chunk's 320 KB are read and its 48 KB written at 3.7 TB/s; what bounds it is the latency
-// of each piece's loads, conversions and products in turn (29,000 cycles a chunk and SM, of them 10,500
-// of issue, 4,000 of products).  On mma.sync, with accumulators in registers and one CTA an SM, it took 705 us in
-// place of 400.
+// other's products.  A chunk's 320 KB are read and its 48 KB written at 4.2 TB/s; what bounds it is the latency
+// of each piece's loads, conversions and products in turn (26,000 cycles a chunk and SM, of them 10,200 of issue
+// and 4,000 of products).  On mma.sync, with accumulators in registers and one CTA an SM, it took 705 us.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -1271,7 +1274,8 @@ struct Grad {
   static constexpr int YZ = 0, Zl = YZ + 8192 /* zeros | the second part of dZ */, U = Zl + 8192, Ut = U + 3 * 4096,
                        S = Ut + 2 * 4096, G = S + 3 * 8192, K = G + 2 * 8192, Q = K + 16384, sc = Q + 16384,
                        rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */,
-                       flow = rows + 4 * kC * 4 /* [4][64] */, red = flow + 4 * kC * 4, bars = red + 32, size = bars + 32;
+                       flow = rows + 4 * kC * 4 /* [4][64] */, red = flow + 4 * kC * 4,
+                       bars = red + 32, size = bars + 32;
   static constexpr int stage = K;  // a piece of the states, until K and Q take its place
   static constexpr int X = 0, N = X + 3 * 8192;  // once the value columns are done
   static constexpr uint32_t dQ1 = 0, dKa = 64, dKb = 128, XN = 192, dQ2 = 192, columns = 256;  // tensor memory
@@ -1895,8 +1899,9 @@ int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, in
   return SDM_OK;
 }
 
-// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (its warps, four for the chain, then
-// run on schedulers of their own), else two, else four, which share an SM's tensor cores and the chunk's tiles.
+// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (1.75 us a chunk forward), else two
+// (3.0), else four (5.0), which share an SM's tensor cores and the chunk's tiles; two turns of the SMs with half
+// as many would take 3.5 and 6.0.
 int chain_width(const Gdn &a, const Layout &l) {
   const int64_t all = l.tiles * a.B * a.H;
   return all <= kSms || l.tiles == 1 ? 1 : all <= 2 * kSms || l.tiles == 2 ? 2 : 4;

@@ -669,7 +669,7 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * dev_err : optional; also SDM_DEVERR_TIMEOUT if a bounded wait gave up (outputs then invalid).
  *
  * Both are deterministic.  Chunks of 64 tokens: one kernel for what a chunk
- * needs of itself, one that runs the chunks in order (16 value columns to three warps), and in
+ * needs of itself, one that runs the chunks in order (16 value columns to three to eight warps), and in
  * the backward one for the sums over value columns.  States, sums and
  * decays are fp32 (the sums of log_alpha wider); y, dq, dk and dv are rounded once, to nearest even.
  * NaN and infinities are not looked for: they spread over their chunk and the
