@@ -1261,11 +1261,12 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
 // The value columns come 32 at a time, as the chains left them, read ahead by a piece: the states of two kinds by
 // bulk copies (through registers alone, whose loads wait for one another at the door, 404 us in place of 360),
 // the rest 16 bytes a lane.  They are split into bf16 parts and stored as the 8 x 8 cores of the operands, where
-// a warp's store is 128 bytes in a row.  K and Q come last, in the states' place.  All operands have their rows of 8 along M or N (MN-major); X and N serve both ways as they lie. A CTA
-// needs half of an SM's shared memory, registers and tensor memory, so that one's conversions run beside the
-// other's products.  A chunk's 320 KB are read and its 48 KB written at 4.2 TB/s; what bounds it is the latency
-// of each piece's loads, conversions and products in turn (26,000 cycles a chunk and SM, of them 10,200 of issue
-// and 4,000 of products).  On mma.sync, with accumulators in registers and one CTA an SM, it took 705 us.
+// a warp's store is 128 bytes in a row.  K and Q come last, in the states' place.  All operands have their rows
+// of 8 along M or N (MN-major); X and N serve both ways as they lie.  A CTA needs half of an SM's shared memory,
+// registers and tensor memory, so that one's conversions run beside the other's products.  A chunk's 320 KB are
+// read and its 48 KB written at 4.2 TB/s; what bounds it is the latency of each piece's loads, conversions and
+// products in turn (26,000 cycles a chunk and SM, of them 10,200 of issue and 4,000 of products).  On mma.sync,
+// with accumulators in registers and one CTA an SM, it took 705 us.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -1342,7 +1343,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   const int tid = threadIdx.x, w = tid >> 5, quarter = w & 3, upper = w >> 2, lane = tid & 31, g = lane >> 2,
       t = lane & 3;
   const unsigned heads = static_cast<unsigned>(a.B) * a.H;
-  const int c = static_cast<int>(blockIdx.x / heads), bh32 = static_cast<int>(blockIdx.x % heads), b = bh32 / a.H, h = bh32 - b * a.H;
+  // chunk by chunk: what the backward chains wrote last, and is still in L2, comes first
+  const int c = static_cast<int>(blockIdx.x / heads), bh32 = static_cast<int>(blockIdx.x % heads);
+  const int b = bh32 / a.H, h = bh32 - b * a.H;
   const int64_t bh = bh32, u = bh * a.n + c;
   before_reading();
   const int live = min(length_of(a, b) - c * kC, kC);
@@ -1443,7 +1446,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     for (int x = 0; x < NW; ++x) {
       float4 fs = make_float4(0.f, 0.f, 0.f, 0.f), f1 = fs;
       if ((c0 >> 4) + upper < tiles) {
-        const float4 *st = reinterpret_cast<const float4 *>(sm + L::stage) + (upper * NT + quarter * NW + x) * 32 + lane;
+        const float4 *st =
+            reinterpret_cast<const float4 *>(sm + L::stage) + (upper * NT + quarter * NW + x) * 32 + lane;
         fs = st[0], f1 = st[NT * 64];
       }
       anchor += (fs.x * f0[x].x + fs.y * f0[x].y) + (fs.z * f0[x].z + fs.w * f0[x].w);

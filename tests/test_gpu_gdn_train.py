@@ -377,7 +377,7 @@ def test_offsets_past_32_bits():
     close32(pool[slots.long()], f[1], "state")
 
 
-@pytest.mark.parametrize("shape", [(1, 200, 1, 1, 128, 128), (3, 130, 1, 20, 64, 64)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 200, 1, 1, 128, 128), (3, 130, 1, 20, 64, 64), (4, 130, 1, 20, 64, 64)], ids=str)
 def test_a_wait_that_runs_out_is_reported(shape, monkeypatch):
     """A copy that is never asked for: both calls end, report it, and the next ones are right."""
     sdm = need_gpu()
