@@ -202,8 +202,9 @@ __device__ __forceinline__ void strip(const float *a, int lda, const float *b, i
 }
 
 // X = L^-1 for unit lower triangular L: the 16 x 16 diagonal blocks by substitution (one a warp), then blocks
-// joined two by two, X21 = -X22 (L21 X11).  zt: 32 x 36 floats.
-__device__ __forceinline__ void invert(const float *L, float *X, float *zt, int tid) {
+// joined two by two, X21 = -X22 (L21 X11), whose inner products lie in L's upper right quarter.
+__device__ __forceinline__ void invert(float *L, float *X, int tid) {
+  float *zt = L + 32;
   const int w = tid >> 5, lane = tid & 31;
   if (lane < 16) {
     const int o = 16 * w;
@@ -226,10 +227,10 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
     const int pr = tid >> 6, r = (tid >> 2) & 15, c = (tid & 3) * 4, o = 32 * pr;
     float acc[1][4];
     strip<1, 16>(L + (o + 16 + r) * kLd + o, kLd, X + o * kLd + o + c, kLd, acc);
-    float *z = zt + pr * 16 * 20;
-    *reinterpret_cast<float4 *>(z + r * 20 + c) = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+    float *z = zt + pr * 16 * kLd;
+    *reinterpret_cast<float4 *>(z + r * kLd + c) = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
     __syncthreads();
-    strip<1, 16>(X + (o + 16 + r) * kLd + o + 16, kLd, z + c, 20, acc);
+    strip<1, 16>(X + (o + 16 + r) * kLd + o + 16, kLd, z + c, kLd, acc);
     *reinterpret_cast<float4 *>(X + (o + 16 + r) * kLd + o + c) =
         make_float4(-acc[0][0], -acc[0][1], -acc[0][2], -acc[0][3]);
   }
@@ -240,9 +241,9 @@ __device__ __forceinline__ void invert(const float *L, float *X, float *zt, int 
     strip<2, 32>(L + (32 + r) * kLd, kLd, X + c, kLd, acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float4 *>(zt + (r + i) * 36 + c) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4 *>(zt + (r + i) * kLd + c) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     __syncthreads();
-    strip<2, 32>(X + (32 + r) * kLd + 32, kLd, zt + c, 36, acc);
+    strip<2, 32>(X + (32 + r) * kLd + 32, kLd, zt + c, kLd, acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       *reinterpret_cast<float4 *>(X + (32 + r + i) * kLd + c) =
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char *sK = sm, *sQ = sm + panels * kPanel;
   // L and X take the tiles' place once the products are formed
-  float *sL = reinterpret_cast<float *>(sm), *sX = sL + kC * kLd, *zt = sX + kC * kLd, *sc = zt + 32 * 36;
+  float *sL = reinterpret_cast<float *>(sm), *sX = sL + kC * kLd, *sc = sX + kC * kLd;
   uint64_t *bar = reinterpret_cast<uint64_t *>(sc + kScal);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t u = blockIdx.x;
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
   __syncthreads();
   write_tiles(sX, a.m3 + u * (3 * kTri), tid);
   __syncthreads();
-  invert(sL, sX, zt, tid);
+  invert(sL, sX, tid);
   write_tiles(sX, a.t3 + u * (3 * kTri), tid);
 }
 
@@ -1932,7 +1933,7 @@ int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc != SDM_OK) return rc;
   if (l.units > 0) {
-    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + 32 * 36 + kScal) * 4 + 16, st, a,
+    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + kScal) * 4 + 16, st, a,
         maps);
     if (rc != SDM_OK) return rc;
   }
