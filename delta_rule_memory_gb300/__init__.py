@@ -82,8 +82,8 @@ _SIGNATURES = {
     "gdn_train_saved_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "gdn_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "gdn_train": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P, _P]),
-    "gdn_backward": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _SZ, _P, _I, _I, _I, _I, _I, _I, _P, _L, _P,
-                          _L, _P, _L, _P, _P, _P, _SZ, _P, _P]),
+    "gdn_backward": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _SZ, _P, _I, _I, _I, _I, _I, _I, _P, _L,
+                          _P, _L, _P, _L, _P, _P, _P, _SZ, _P, _P]),
     "gdn_step": (_I, [_P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "route_sort_workspace_size": (_SZ, [_L, _I, _I]),
     "route_sort": (_I, [_P, _L, _I, _I, _P, _P, _P, _P, _SZ, _P, _P]),
@@ -895,7 +895,8 @@ def _gdn_checks(state, name, q, k, v, log_alpha, beta, reset, lens, dev_err, poo
     if not pool and P != B:
         raise ValueError(f"{name} must be [B,H,dk,dv] with B = {B}, got {tuple(state.shape)}")
     _need(state, name, torch.float32, None, dev)
-    lq, lk, lv = _heads(q, "q", (B, T, Hk, dk), dev), _heads(k, "k", (B, T, Hk, dk), dev), _heads(v, "v", (B, T, H, dv), dev)
+    lq, lk = _heads(q, "q", (B, T, Hk, dk), dev), _heads(k, "k", (B, T, Hk, dk), dev)
+    lv = _heads(v, "v", (B, T, H, dv), dev)
     _need(log_alpha, "log_alpha", torch.float32, (B, T, H), dev)
     _need(beta, "beta", torch.float32, (B, T, H), dev)
     if reset is not None:
@@ -925,7 +926,8 @@ def gdn_train(state, q, k, v, log_alpha, beta, reset=None, lens=None, y=None, st
     where that is given.  Returns (y, saved): y bf16 [B,T,H,dv], whose rows
     behind lens are 0, or as they were in a `y` that was given; saved uint8, for
     gdn_backward with the same inputs."""
-    B, T, Hk, H, dk, dv, dev, lq, lk, lv, reset = _gdn_checks(state, "state", q, k, v, log_alpha, beta, reset, lens, dev_err)
+    B, T, Hk, H, dk, dv, dev, lq, lk, lv, reset = _gdn_checks(state, "state", q, k, v, log_alpha, beta, reset, lens,
+                                                              dev_err)
     with _on(dev, stream) as st:
         y = _out(y, "y", torch.bfloat16, (B, T, H, dv), dev, lens)
         state_out = state if state_out is None else _out(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
@@ -933,8 +935,8 @@ def gdn_train(state, q, k, v, log_alpha, beta, reset=None, lens=None, y=None, st
             saved = torch.empty(gdn_train_saved_size(B, T, Hk, H, dk, dv), dtype=torch.uint8, device=dev)
         else:
             _need(saved, "saved", torch.uint8, None, dev)
-        rc = lib().gdn_train(state.data_ptr(), state_out.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv,
-                             log_alpha.data_ptr(), beta.data_ptr(), _ptr(reset), _ptr(lens), B, T, Hk, H, dk, dv,
+        rc = lib().gdn_train(state.data_ptr(), state_out.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(),
+                             lv, log_alpha.data_ptr(), beta.data_ptr(), _ptr(reset), _ptr(lens), B, T, Hk, H, dk, dv,
                              y.data_ptr(), saved.data_ptr(), saved.numel(), _ptr(dev_err), st)
     if rc:
         _check("gdn_train", rc)
@@ -964,17 +966,20 @@ def gdn_backward(dstate, q, k, v, log_alpha, beta, saved, dy, reset=None, lens=N
         else:
             dq, dk_, dv_ = grads
             lds = [_heads(t, n, like.shape, dev) for t, n, like in ((dq, "dq", q), (dk_, "dk", k), (dv_, "dv", v))]
-        dla, dbeta = _out(None, "", torch.float32, (B, T, H), dev, lens), _out(None, "", torch.float32, (B, T, H), dev, lens)
-        dstate_out = dstate if dstate_out is None else _out(dstate_out, "dstate_out", torch.float32, (B, H, dk, dv), dev)
+        dla, dbeta = (_out(None, "", torch.float32, (B, T, H), dev, lens) for _ in range(2))
+        if dstate_out is None:
+            dstate_out = dstate
+        else:
+            _need(dstate_out, "dstate_out", torch.float32, (B, H, dk, dv), dev)
         if workspace is None:
             workspace = torch.empty(gdn_backward_workspace_size(B, T, Hk, H, dk, dv), dtype=torch.uint8, device=dev)
         else:
             _need(workspace, "workspace", torch.uint8, None, dev)
-        rc = lib().gdn_backward(dstate.data_ptr(), dstate_out.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(),
-                                lv, log_alpha.data_ptr(), beta.data_ptr(), _ptr(reset), _ptr(lens), saved.data_ptr(),
-                                saved.numel(), dy.data_ptr(), B, T, Hk, H, dk, dv, dq.data_ptr(), lds[0], dk_.data_ptr(),
-                                lds[1], dv_.data_ptr(), lds[2], dla.data_ptr(), dbeta.data_ptr(), workspace.data_ptr(),
-                                workspace.numel(), _ptr(dev_err), st)
+        rc = lib().gdn_backward(dstate.data_ptr(), dstate_out.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk,
+                                v.data_ptr(), lv, log_alpha.data_ptr(), beta.data_ptr(), _ptr(reset), _ptr(lens),
+                                saved.data_ptr(), saved.numel(), dy.data_ptr(), B, T, Hk, H, dk, dv, dq.data_ptr(),
+                                lds[0], dk_.data_ptr(), lds[1], dv_.data_ptr(), lds[2], dla.data_ptr(),
+                                dbeta.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_err), st)
     if rc:
         _check("gdn_backward", rc)
     return dq, dk_, dv_, dla, dbeta
@@ -988,14 +993,15 @@ def gdn_step(state, q, k, v, log_alpha, beta, slots=None, lens=None, y=None, dev
     [B], tokens that exist.  q, k, v, log_alpha, beta as gdn_train's.  Returns y
     bf16 [B,T,H,dv]; rows of what does not exist are 0, or as they were in a
     `y` that was given."""
-    B, T, Hk, H, dk, dv, dev, lq, lk, lv, _ = _gdn_checks(state, "state", q, k, v, log_alpha, beta, None, lens, dev_err, True)
+    B, T, Hk, H, dk, dv, dev, lq, lk, lv, _ = _gdn_checks(state, "state", q, k, v, log_alpha, beta, None, lens,
+                                                          dev_err, True)
     if slots is not None:
         _need(slots, "slots", torch.int32, (B,), dev)
     with _on(dev, stream) as st:
         y = _out(y, "y", torch.bfloat16, (B, T, H, dv), dev, slots if lens is None else lens)
-        rc = lib().gdn_step(state.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv, log_alpha.data_ptr(),
-                            beta.data_ptr(), _ptr(slots), _ptr(lens), state.shape[0], B, T, Hk, H, dk, dv, y.data_ptr(),
-                            _ptr(dev_err), st)
+        rc = lib().gdn_step(state.data_ptr(), q.data_ptr(), lq, k.data_ptr(), lk, v.data_ptr(), lv,
+                            log_alpha.data_ptr(), beta.data_ptr(), _ptr(slots), _ptr(lens), state.shape[0], B, T, Hk,
+                            H, dk, dv, y.data_ptr(), _ptr(dev_err), st)
     if rc:
         _check("gdn_step", rc)
     return y
@@ -1003,7 +1009,8 @@ def gdn_step(state, q, k, v, log_alpha, beta, slots=None, lens=None, y=None, dev
 
 def _matrix(t, name: str, shape=None, dtype=None, index=None) -> int:
     """Check [rows,D] activations; returns their row distance."""
-    if not isinstance(t, _Tensor) or t.dim() != 2 or max(t.shape) >= _INT_END or not _plain(t, t.dtype, t.shape, t.get_device()):
+    if (not isinstance(t, _Tensor) or t.dim() != 2 or max(t.shape) >= _INT_END
+            or not _plain(t, t.dtype, t.shape, t.get_device())):
         if isinstance(t, _Tensor) and t.dim() != 2:
             raise ValueError(f"{name} must be [rows,D]")
         if isinstance(t, _Tensor) and max(t.shape) >= _INT_END:
@@ -1093,7 +1100,8 @@ def route_combine(rows, place, w=None, y=None, stream=None):
         _need(w, "w", torch.float32, (M, k), dev)
     with _on(dev, stream) as st:
         y = _out(y, "y", rows.dtype, (M, D), dev)
-        rc = lib().route_combine(rows.data_ptr(), _DTYPES[rows.dtype], place.data_ptr(), _ptr(w), M, k, D, y.data_ptr(), st)
+        rc = lib().route_combine(rows.data_ptr(), _DTYPES[rows.dtype], place.data_ptr(), _ptr(w), M, k, D,
+                                 y.data_ptr(), st)
     if rc:
         _check("route_combine", rc)
     return y
