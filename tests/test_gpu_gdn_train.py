@@ -377,6 +377,16 @@ def test_offsets_past_32_bits():
     close32(pool[slots.long()], f[1], "state")
 
 
+@pytest.mark.parametrize("B", [1, 2, 4])
+def test_odd_rows_of_many_heads(B):
+    """Rows that no tensor copy takes, one, two and four tiles of columns a CTA, tiles behind the last column."""
+    sdm = need_gpu()
+    c = Case(B, 200, 15, 15, 36, 129, seed=50 + B, reset=0.02, lens=[200, 150, 1, 128][:B], fused=True, offset=1)
+    check(c, c.run(sdm), *c.reference())
+    aligned = Case(B, 200, 15, 15, 40, 136, seed=60 + B, reset=0.02, lens=[193, 192, 0, 65][:B])
+    check(aligned, aligned.run(sdm), *aligned.reference())
+
+
 @pytest.mark.parametrize("shape", [(1, 200, 1, 1, 128, 128), (3, 130, 1, 20, 64, 64), (4, 130, 1, 20, 64, 64)], ids=str)
 def test_a_wait_that_runs_out_is_reported(shape, monkeypatch):
     """A copy that is never asked for: both calls end, report it, and the next ones are right."""
