@@ -1095,8 +1095,10 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
         if (M == 2) meet(pair, 32 * M);  // the parts, in whose place the sums go, have been read
         give_sums<M>(hX, x, lane, d, U);
       }
-      arrive(read, 32 * (M + H));  // G has been read
-      meet(all, 32 * (M + H));     // dY^T M is there
+      meet(all, 32 * (M + H));  // dY^T M is there
+      // G has been read.  Told only behind the meeting: a helping warp meets at `all` again once it is past `read`,
+      // so every main warp has to have left that barrier's phase by then, or the helper would be counted in its place
+      arrive(read, 32 * (M + H));
       take_sums<M>(hX, x, lane, U);
       scale_groups<M>(U, x, tail, t);
       add_tiles<M>(hZ, x, lane, U);
