@@ -24,6 +24,10 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kRun = 128, kBlock = kSortWarps * kRun;
 constexpr int kMaxParts = 1024;
+// shared memory of the two kernels of N partitions, all of it dynamic: what decides whether a launch needs the raised
+// limit is then the launch's own size
+constexpr int count_smem(int N) { return kSortWarps * N * 4; }
+constexpr int place_smem(int N) { return count_smem(N) + (2 * N + 1 + kSortWarps) * 4; }
 constexpr int kSumHere = 8192;  // counts (blocks x N) up to which each block sums those before it by itself
 
 struct SortArgs {
@@ -102,8 +106,7 @@ __global__ void __launch_bounds__(32) route_scan(const SortArgs a) {
 // places.  One block alone counts for itself; with few counts in all a block sums those of the blocks before it
 __global__ void __launch_bounds__(kSortThreads) route_place(const SortArgs a) {
   extern __shared__ int hist[];
-  int *start = hist + kSortWarps * a.N, *ahead = start + a.N + 1;  // [N + 1], [N]
-  __shared__ int sums[kSortWarps];
+  int *start = hist + kSortWarps * a.N, *ahead = start + a.N + 1, *sums = ahead + a.N;  // [N + 1], [N], [warps]
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kBlock;
   const Run run = read_run(a, first);
@@ -468,18 +471,16 @@ extern "C" int route_sort(const int32_t *sel, int64_t M, int k, int N, int32_t *
   if (a.blocks < 1) a.blocks = 1;
   a.sum_here = static_cast<int64_t>(a.blocks) * N <= kSumHere;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int hist = kSortWarps * N * 4, smem = hist + (2 * N + 1) * 4;
-  if (smem > 48 << 10)  // the limit is the kernel's, the same in every call
+  if (place_smem(N) > 48 << 10)  // the limit is the kernel's, the same in every call
     for (const void *f : {reinterpret_cast<const void *>(route_count), reinterpret_cast<const void *>(route_place)}) {
-      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-          (kSortWarps * kMaxParts + 2 * kMaxParts + 1) * 4);
+      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, place_smem(kMaxParts));
       if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "route_sort: %s", cudaGetErrorString(e));
     }
   if (a.blocks > 1 && N > 0) {
-    route_count<<<a.blocks, kSortThreads, hist, st>>>(a);
+    route_count<<<a.blocks, kSortThreads, count_smem(N), st>>>(a);
     if (!a.sum_here) route_scan<<<N, 32, 0, st>>>(a);
   }
-  route_place<<<a.blocks, kSortThreads, smem, st>>>(a);
+  route_place<<<a.blocks, kSortThreads, place_smem(N), st>>>(a);
   return check_launch("route_sort");
 }
 
