@@ -17,11 +17,11 @@
 //   X = D o dY U^T,   N = -strict(D) o dZ U^T,
 //   dQ = gam dY S^T + X K,
 //   dK = tail U G^T - gam dZ S^T + X^T Q + (N + N^T) K.
-// The decays' gradient needs no product of its own.  y and S_end are linear in (S, V), so at every cut the
-// gradient's inner product with the state behind it plus that with the values to come is that of the outputs to
-// come; with y_t . dy_t = q_t . dq_t:
-//   da_t = <S, G_start> - sum over s < t of (q_s . dq_s - v_s . dv_s)
-// (the first term only before the chunk's first reset, the sum from the document's start on).
+// The decays' gradient is the sum of what passes token t's decay, each term with that decay in it:
+//   da_t = gam_C <S, G> + sum over i >= t of gam_i (q_i . S dY_i - k_i . S dZ_i)
+//        + sum over j < t of tail_j k_j . G U_j + sum over i >= t > j of (X_ij q_i . k_j + N_ij k_i . k_j).
+// (A running sum of q . dq - v . dv taken off <S, G_start> is the same and needs no product of its own, but its
+// terms do not get smaller with the decay: at e^-8 a token their difference is 5e-4 off, at e^-16 half of it.)
 //
 // Kernels.  gdn_prep (every chunk by itself): the decays, T and M.  gdn_chain: chunk after chunk, three to eight
 // warps a tile of 16 value columns; every product of a chunk takes the one before as its A operand from registers
@@ -1256,16 +1256,18 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
 // ---------------------------------------------------------------------------
 // gdn_grad: the gradients of one chunk of one head, on the tcgen05 tensor cores. Transposed, every sum over
 // value columns has the key channels or two times the tokens as its M = 128 and the tokens as N:
-//   [dQ1 | dKa]^T [128 x 128] = S [dY | dZ]^T        dKb^T [128 x 64] = G (tail U)^T
-//   [X; N]        [128 x 64]  = [dY; dZ] U^T
-// and then, with X and N times their decays,
-//   dQ2^T = K^T X^T,   dKb^T += Q^T X + K^T (N^T + N),
-//   dQ = gam dQ1 + dQ2,   dK = dKb - gam dKa.
-// The value columns come 32 at a time, as the chains left them, read ahead by a piece: the states of two kinds by
-// bulk copies (through registers alone, whose loads wait for one another at the door, 404 us in place of 360),
-// the rest 16 bytes a lane.  They are split into bf16 parts and stored as the 8 x 8 cores of the operands, where
-// a warp's store is 128 bytes in a row.  K and Q come last, in the states' place.  All operands have their rows
-// of 8 along M or N (MN-major); X and N serve both ways as they lie.  A CTA needs half of an SM's shared memory,
+//   [dQ | dKa]^T [128 x 128] = S [dY | dZ]^T        dK^T [128 x 64] = G U^T
+//   [X; N]       [128 x 64]  = [dY; dZ] U^T
+// and then, with X and N times their decays, dQ <- gam dQ and dK <- tail dK - gam dKa written back,
+//   dQ^T += K^T X^T,   dK^T += Q^T X + K^T (N^T + N),   [QK; KK] [128 x 64] = [Q; K] K^T,
+// the last in X's and N's place, for the decays' gradient.
+// The value columns come 32 at a time, as the chains left them, read ahead by a piece: S by bulk copies (through
+// registers alone, whose loads wait for one another at the door, 404 us in place of 360), the rest 16 bytes a
+// lane.  They are split into bf16 parts and stored as the 8 x 8 cores of the operands, where a warp's store is
+// 128 bytes in a row.  K and Q come last, in the states' place, while X and N are converted.  The operands of the
+// sums over value columns have their rows of 8 along M or N (MN-major); X, N, K and Q serve both ways as they lie.
+// With dk <= 64 the products' upper 64 channels are whatever lies behind S and G; rows of a product do not mix,
+// and those are not read.  A CTA needs half of an SM's shared memory,
 // registers and tensor memory, so that one's conversions run beside the other's products.  A chunk's 320 KB are
 // read and its 48 KB written at 4.2 TB/s; what bounds it is the latency of each piece's loads, conversions and
 // products in turn (26,000 cycles a chunk and SM, of them 10,200 of issue and 4,000 of products).  On mma.sync,
@@ -1275,14 +1277,17 @@ constexpr int kGradThreads = 256;
 
 struct Grad {
   // a core row of 8 value columns: 16 cores where M or N is 128, 8 where it is 64
-  static constexpr int YZ = 0, Zl = YZ + 8192 /* zeros | the second part of dZ */, U = Zl + 8192, Ut = U + 3 * 4096,
-                       S = Ut + 2 * 4096, G = S + 3 * 8192, K = G + 2 * 8192, Q = K + 16384, sc = Q + 16384,
-                       rows = sc + kScal * 4 /* [2][2][64]: dZ . E and v . dZ */,
-                       flow = rows + 4 * kC * 4 /* [4][64] */, red = flow + 4 * kC * 4,
+  static constexpr int YZ = 0, Z1 = YZ + 8192 /* zeros | the second part of dZ */, Z2 = Z1 + 8192, U = Z2 + 8192,
+                       S = U + 3 * 4096, G = S + 3 * 8192, stage = G + 3 * 8192 /* S, a piece ahead */,
+                       sc = stage + 16384, rows = sc + kScal * 4 /* [2][64]: dZ . E */,
+                       into = rows + 2 * kC * 4 /* [4][64]: gam (q . S dY - k . S dZ) */,
+                       out = into + 4 * kC * 4 /* [4][64]: tail k . G U */,
+                       inner = out + 4 * kC * 4 /* [8][64]: pairs of tokens */, red = inner + 8 * kC * 4,
                        bars = red + 32, size = bars + 32;
-  static constexpr int stage = K;  // a piece of the states, until K and Q take its place
-  static constexpr int X = 0, N = X + 3 * 8192;  // once the value columns are done
-  static constexpr uint32_t dQ1 = 0, dKa = 64, dKb = 128, XN = 192, dQ2 = 192, columns = 256;  // tensor memory
+  // once the value columns are done
+  static constexpr int X = 0, N = X + 3 * 8192, Q = N + 3 * 8192, K = Q + 16384;
+  static constexpr uint32_t dQ = 0, dKa = 64, dK = 128, XN = 192, QKK = 192, columns = 256;  // tensor memory
+  static_assert(K + 16384 <= stage, "");
 };
 static_assert(2 * (Grad::size + 1024) <= 228 * 1024, "two CTAs an SM");
 
@@ -1357,30 +1362,30 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   const int hk = h / (a.H / a.Hk), tiles = (a.dv + 15) >> 4;
   float *sc = reinterpret_cast<float *>(sm + L::sc);
   float *gam = sc, *tail = sc + kC, *beta = sc + 2 * kC, *lh = sc + 3 * kC, *ll = sc + 4 * kC, *sg = sc + 5 * kC;
-  float *rows = reinterpret_cast<float *>(sm + L::rows), *flow = reinterpret_cast<float *>(sm + L::flow),
+  float *rows = reinterpret_cast<float *>(sm + L::rows), *into = reinterpret_cast<float *>(sm + L::into),
+        *out = reinterpret_cast<float *>(sm + L::out), *inner = reinterpret_cast<float *>(sm + L::inner),
         *red = reinterpret_cast<float *>(sm + L::red);
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::bars);
   uint32_t *holder = reinterpret_cast<uint32_t *>(bar + 2);
   const uint32_t mb = smem_u32(bar), full = smem_u32(bar + 1), base = smem_u32(sm);
 
-  // Two tiles of S at the chunk's start and G at its end by bulk copies, a piece ahead; the rest of a piece into
-  // registers: of tile `upper` of the two, key channels 8 NW quarter .. and tokens 16 quarter .. + 15
+  // Two tiles of S at the chunk's start by bulk copies, a piece ahead; the rest of a piece into registers: of tile
+  // `upper` of the two, key channels 8 NW quarter .. and tokens 16 quarter .. + 15
   const auto ask_states = [&](int c0) {
     const int ct = c0 >> 4;
     const uint32_t bytes = min(2, tiles - ct) * NT * 512;
-    mbar_expect_tx(full, 2 * bytes);
+    mbar_expect_tx(full, bytes);
     bulk_g2s(base + L::stage, a.s + (u * tiles + ct) * (NT * 128), bytes, full);
-    bulk_g2s(base + L::stage + NT * 1024, a.g + ((bh * (a.n + 1) + c + 1) * tiles + ct) * (NT * 128), bytes, full);
   };
-  float4 f0[NW];
+  float4 f1[NW];
   float E[2][4], Z[2][4];
-  uint32_t yv[2][2], vv[2][2];  // dy and v [n-tile][columns 0..7, 8..15]: a row's pair a lane
-  const auto read_start = [&](int c0) {  // G at the chunk's start
+  uint32_t yv[2][2];  // dy [n-tile][columns 0..7, 8..15]: a row's pair a lane
+  const auto read_end = [&](int c0) {  // G at the chunk's end
     const int ct = (c0 >> 4) + upper;
     const float4 *G = reinterpret_cast<const float4 *>(a.g) +
-        (((bh * (a.n + 1) + c) * tiles + ct) * NT + quarter * NW) * 32 + lane;
+        (((bh * (a.n + 1) + c + 1) * tiles + ct) * NT + quarter * NW) * 32 + lane;
 #pragma unroll
-    for (int x = 0; x < NW; ++x) f0[x] = ct < tiles ? G[x * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < NW; ++x) f1[x] = ct < tiles ? G[x * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   const auto read_tokens = [&](int c0) {
     const int ct = (c0 >> 4) + upper;
@@ -1399,7 +1404,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       for (int e = 0; e < 2; ++e) {
         const int i = 16 * quarter + 8 * x + g, cc = 16 * ct + 8 * e + 2 * t, left = i < live ? a.dv - cc : 0;
         yv[x][e] = load_pair(a.dy + (tok + i) * ld_y + h * a.dv + cc, left, a.by_dy >= 4);
-        vv[x][e] = load_pair(a.v + (tok + i) * a.ld_v + h * a.dv + cc, left, a.by_v >= 4);
       }
   };
   if (tid == 0) {
@@ -1408,16 +1412,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     fence_mbar_init();
     ask_states(0);
   }
-  read_start(0);
+  read_end(0);
   if (tid < kScal / 4) copy_async<16>(smem_u32(sc) + tid * 16, a.scal + u * kScal + tid * 4, true);
   cp_async_commit();
   read_tokens(0);
 
   if (w == 0) tmem_alloc(smem_u32(holder), L::columns);
-  // the half of zeros beside dZ's second part
+  // the halves of zeros beside dZ's second and third part
   {
     const int i = tid >> 6, o = tid & 63;
-    *reinterpret_cast<uint4 *>(sm + L::Zl + i * 2048 + o * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4 *>(sm + L::Z1 + i * 2048 + o * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4 *>(sm + L::Z2 + i * 2048 + o * 16) = make_uint4(0, 0, 0, 0);
   }
   cp_async_wait<0>();
   tc_fence_before();
@@ -1440,39 +1445,33 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
   const uint32_t mn = (1u << 15) | (1u << 16);
   const uint32_t id64 = idesc_bf16_f32(128, 64) | mn, id128 = idesc_bf16_f32(128, 128) | mn;
 
-  float anchor = 0.f, ez[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, vz[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+  float anchor = 0.f, ez[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
   for (int c0 = 0; c0 < a.dv; c0 += 32) {
     if (c0 && !products_done()) break;  // the piece before has been read
     // ---- the states
     there = mbar_wait(full, (c0 >> 5) & 1, kWaitLimit) && there;
 #pragma unroll
     for (int x = 0; x < NW; ++x) {
-      float4 fs = make_float4(0.f, 0.f, 0.f, 0.f), f1 = fs;
-      if ((c0 >> 4) + upper < tiles) {
-        const float4 *st =
-            reinterpret_cast<const float4 *>(sm + L::stage) + (upper * NT + quarter * NW + x) * 32 + lane;
-        fs = st[0], f1 = st[NT * 64];
-      }
-      anchor += (fs.x * f0[x].x + fs.y * f0[x].y) + (fs.z * f0[x].z + fs.w * f0[x].w);
-      uint32_t p0[3], p1[3], q0[2], q1[2];
+      float4 fs = make_float4(0.f, 0.f, 0.f, 0.f);
+      if ((c0 >> 4) + upper < tiles)
+        fs = reinterpret_cast<const float4 *>(sm + L::stage)[(upper * NT + quarter * NW + x) * 32 + lane];
+      anchor += (fs.x * f1[x].x + fs.y * f1[x].y) + (fs.z * f1[x].z + fs.w * f1[x].w);
+      uint32_t p0[3], p1[3], q0[3], q1[3];
       split<3>(fs.x, fs.y, p0);
       split<3>(fs.z, fs.w, p1);
-      split<2>(f1.x, f1.y, q0);
-      split<2>(f1.z, f1.w, q1);
+      split<3>(f1[x].x, f1[x].y, q0);
+      split<3>(f1[x].z, f1[x].w, q1);
       unsigned char *o = sm + upper * 4096 + (quarter * NW + x) * 128 + lane * 4;
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
         *reinterpret_cast<uint32_t *>(o + L::S + p * 8192) = p0[p];
         *reinterpret_cast<uint32_t *>(o + L::S + p * 8192 + 2048) = p1[p];
-      }
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
         *reinterpret_cast<uint32_t *>(o + L::G + p * 8192) = q0[p];
         *reinterpret_cast<uint32_t *>(o + L::G + p * 8192 + 2048) = q1[p];
       }
     }
     if (c0 + 32 < a.dv) {
-      read_start(c0 + 32);
+      read_end(c0 + 32);
       if (w == 0) {  // once every warp has read the stage
         asm volatile("bar.sync 1, 256;\n" ::: "memory");
         if (lane == 0) ask_states(c0 + 32);
@@ -1481,34 +1480,28 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         asm volatile("bar.arrive 1, 256;\n" ::: "memory");
       }
     }
-    // ---- U, tail U, dZ, dy; dv; the sums over value columns
+    // ---- U, dZ, dy; dv; the sums over value columns
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int nt = 2 * quarter + x;
-      const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t),
-          tl = *reinterpret_cast<const float2 *>(tail + 8 * nt + 2 * t);
+      const float2 be = *reinterpret_cast<const float2 *>(beta + 8 * nt + 2 * t);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // columns 0..7 and 8..15 of the tile
-        const float e0 = E[x][2 * e], e1 = E[x][2 * e + 1], z0 = Z[x][2 * e], z1 = Z[x][2 * e + 1], u0 = be.x * e0,
-            u1 = be.y * e1;
-        uint32_t su[3], st[2], sz[2];
-        split<3>(u0, u1, su);
-        split<2>(tl.x * u0, tl.y * u1, st);
-        split<2>(z0, z1, sz);
-        const uint32_t y = transpose8(yv[x][e]), v = transpose8(vv[x][e]);
+        const float e0 = E[x][2 * e], e1 = E[x][2 * e + 1], z0 = Z[x][2 * e], z1 = Z[x][2 * e + 1];
+        uint32_t su[3], sz[3];
+        split<3>(be.x * e0, be.y * e1, su);
+        split<3>(z0, z1, sz);
+        const uint32_t y = transpose8(yv[x][e]);
         ez[x][0] = fmaf(e0, z0, ez[x][0]);
         ez[x][1] = fmaf(e1, z1, ez[x][1]);
-        vz[x][0] = fmaf(low2(v), z0, vz[x][0]);
-        vz[x][1] = fmaf(high2(v), z1, vz[x][1]);
         const int row = 2 * upper + e;  // of the piece's four core rows
         unsigned char *o = sm + nt * 128 + lane * 4;
         *reinterpret_cast<uint32_t *>(o + L::YZ + row * 2048) = y;
         *reinterpret_cast<uint32_t *>(o + L::YZ + row * 2048 + 1024) = sz[0];
-        *reinterpret_cast<uint32_t *>(o + L::Zl + row * 2048 + 1024) = sz[1];
+        *reinterpret_cast<uint32_t *>(o + L::Z1 + row * 2048 + 1024) = sz[1];
+        *reinterpret_cast<uint32_t *>(o + L::Z2 + row * 2048 + 1024) = sz[2];
 #pragma unroll
         for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t *>(o + L::U + p * 4096 + row * 1024) = su[p];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) *reinterpret_cast<uint32_t *>(o + L::Ut + p * 4096 + row * 1024) = st[p];
         // dv is dZ rounded once, which is its first part
         const uint32_t z = transpose8(sz[0]);
         const int i = 8 * nt + g, cc = c0 + 16 * upper + 8 * e + 2 * t;
@@ -1528,67 +1521,67 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     __syncthreads();
     if (tid == 0) {
       const bool more = c0 > 0;
-      const uint64_t yz = smem_desc(base + L::YZ, 2048, 128), zl = smem_desc(base + L::Zl, 2048, 128),
-                     zln = smem_desc(base + L::Zl + 1024, 2048, 128);
+      const uint64_t yz = smem_desc(base + L::YZ, 2048, 128), z1 = smem_desc(base + L::Z1, 2048, 128),
+                     z2 = smem_desc(base + L::Z2, 2048, 128);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const bool acc = more || ks > 0;
         const uint64_t s0 = smem_desc(base + L::S + ks * 4096, 2048, 128), s1 = s0 + 512, s2 = s0 + 1024;
-        const uint64_t g0 = smem_desc(base + L::G + ks * 4096, 2048, 128), g1 = g0 + 512;
+        const uint64_t g0 = smem_desc(base + L::G + ks * 4096, 2048, 128), g1 = g0 + 512, g2 = g0 + 1024;
         const uint64_t u0 = smem_desc(base + L::U + ks * 2048, 1024, 128), u1 = u0 + 256, u2 = u0 + 512;
-        const uint64_t t0 = smem_desc(base + L::Ut + ks * 2048, 1024, 128), t1 = t0 + 256;
-        const uint64_t b = yz + 256 * ks, bl = zl + 256 * ks, bz = zln + 256 * ks;
-        mma_bf16(tmem + L::dQ1, s0, b, id128, acc);
-        mma_bf16(tmem + L::dQ1, s1, b, id128, true);
-        mma_bf16(tmem + L::dQ1, s2, b, id64, true);
-        mma_bf16(tmem + L::dKa, s0, bz, id64, true);
-        mma_bf16(tmem + L::dKb, g0, t0, id64, acc);
-        mma_bf16(tmem + L::dKb, g0, t1, id64, true);
-        mma_bf16(tmem + L::dKb, g1, t0, id64, true);
+        // b1, b2: dZ's second and third part alone
+        const uint64_t b = yz + 256 * ks, l1 = z1 + 256 * ks, l2 = z2 + 256 * ks, b1 = l1 + 64, b2 = l2 + 64;
+        mma_bf16(tmem + L::dQ, s0, b, id128, acc);
+        mma_bf16(tmem + L::dQ, s1, b, id128, true);
+        mma_bf16(tmem + L::dQ, s2, b, id128, true);
+        mma_bf16(tmem + L::dKa, s0, b1, id64, true);
+        mma_bf16(tmem + L::dKa, s1, b1, id64, true);
+        mma_bf16(tmem + L::dKa, s0, b2, id64, true);
+        mma_bf16(tmem + L::dK, g0, u0, id64, acc);
+        mma_bf16(tmem + L::dK, g0, u1, id64, true);
+        mma_bf16(tmem + L::dK, g1, u0, id64, true);
+        mma_bf16(tmem + L::dK, g1, u1, id64, true);
+        mma_bf16(tmem + L::dK, g0, u2, id64, true);
+        mma_bf16(tmem + L::dK, g2, u0, id64, true);
         mma_bf16(tmem + L::XN, b, u0, id64, acc);
         mma_bf16(tmem + L::XN, b, u1, id64, true);
         mma_bf16(tmem + L::XN, b, u2, id64, true);
-        mma_bf16(tmem + L::XN, bl, u0, id64, true);
+        mma_bf16(tmem + L::XN, l1, u0, id64, true);
+        mma_bf16(tmem + L::XN, l1, u1, id64, true);
+        mma_bf16(tmem + L::XN, l2, u0, id64, true);
       }
       mma_commit(mb);
     }
   }
-  load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
-  load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
-  cp_async_commit();
   // sums over the columns of 16 tokens, and over the state
 #pragma unroll
   for (int x = 0; x < 2; ++x)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        ez[x][e] += __shfl_xor_sync(kFull, ez[x][e], o);
-        vz[x][e] += __shfl_xor_sync(kFull, vz[x][e], o);
-      }
-      if (g == 0) {
-        const int i = 16 * quarter + 8 * x + 2 * t + e;
-        rows[(2 * upper) * kC + i] = ez[x][e];
-        rows[(2 * upper + 1) * kC + i] = vz[x][e];
-      }
+      for (int o = 4; o < 32; o <<= 1) ez[x][e] += __shfl_xor_sync(kFull, ez[x][e], o);
+      if (g == 0) rows[upper * kC + 16 * quarter + 8 * x + 2 * t + e] = ez[x][e];
     }
 #pragma unroll
   for (int o = 16; o; o >>= 1) anchor += __shfl_xor_sync(kFull, anchor, o);
   if (lane == 0) red[w] = anchor;
 
-  cp_async_wait<0>();
   if (ok && products_done()) {
+    load_cores(sm + L::K, a.k + tok * a.ld_k + hk * a.dk, a.ld_k, live, a.dk, a.by_qk, tid);
+    load_cores(sm + L::Q, a.q + tok * a.ld_q + hk * a.dk, a.ld_q, live, a.dk, a.by_qk, tid);
+    cp_async_commit();
     // ---- X (lanes 0..63) and N (64..127) times their decays: row i, columns 32 upper ..
+    const bool is_n = quarter >= 2;
+    float pair[2][16];  // they stay, for the decays' gradient
     {
-      const bool is_n = quarter >= 2;
       const int i = 32 * (quarter & 1) + lane;
       const float li = lh[i], lli = ll[i];
       const int si = __float_as_int(sg[i]);
-      unsigned char *to = sm + (i >> 3) * 1024 + (i & 7) * 16;
-#pragma unroll 1
+      unsigned char *to = sm + (is_n ? L::N : L::X) + (i >> 3) * 1024 + (i & 7) * 16;
+#pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int j0 = 32 * upper + 16 * half;
-        float x[16];
+        float(&x)[16] = pair[half];
         tmem_ld16(lanes + L::XN + j0, x);
         tmem_ld_wait();
 #pragma unroll
@@ -1606,52 +1599,117 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
           unsigned char *o = to + ((j0 + e) >> 3) * 128;
 #pragma unroll
           for (int p = 0; p < 3; ++p)
-            if (!(is_n && p == 2))
-              *reinterpret_cast<uint4 *>(o + (is_n ? L::N : L::X) + p * 8192) = make_uint4(s[0][p], s[1][p], s[2][p],
-                  s[3][p]);
+            *reinterpret_cast<uint4 *>(o + p * 8192) = make_uint4(s[0][p], s[1][p], s[2][p], s[3][p]);
         }
       }
     }
+    cp_async_wait<0>();
     fence_async_smem();
+    __syncthreads();
+    // ---- channel 32 quarter + lane, tokens 32 upper ..: what comes from the states, and its part in the decays' gradient
+    const int ch = 32 * quarter + lane;
+    const bool mine = ch < a.dk;
+    {
+      const unsigned char *sk = sm + L::K + (ch >> 3) * 128 + (ch & 7) * 2;
+      const auto key = [&](int i) {
+        return bf16_to_f32(*reinterpret_cast<const uint16_t *>(sk + (i >> 3) * 2048 + (i & 7) * 16));
+      };
+      const auto query = [&](int i) {
+        return bf16_to_f32(*reinterpret_cast<const uint16_t *>(sk + (L::Q - L::K) + (i >> 3) * 2048 + (i & 7) * 16));
+      };
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int i0 = 32 * upper + 16 * half;
+        const float *gi = gam + i0, *ti = tail + i0;
+        float x[16], y[16], f[16];
+        tmem_ld16(lanes + L::dQ + i0, x);
+        tmem_ld16(lanes + L::dKa + i0, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] *= gi[e];
+          y[e] *= gi[e];
+          f[e] = mine ? query(i0 + e) * x[e] - key(i0 + e) * y[e] : 0.f;
+        }
+        tmem_st16(lanes + L::dQ + i0, x);
+        const float a0 = sum_lanes(f, lane);
+        if (lane < 16) into[quarter * kC + i0 + lane] = a0;
+        tmem_ld16(lanes + L::dK + i0, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float d = ti[e] * x[e];
+          f[e] = mine ? key(i0 + e) * d : 0.f;
+          x[e] = d - y[e];
+        }
+        tmem_st16(lanes + L::dK + i0, x);
+        const float b0 = sum_lanes(f, lane);
+        if (lane < 16) out[quarter * kC + i0 + lane] = b0;
+      }
+      tmem_st_wait();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (tid == 0) {
       const uint32_t idk = idesc_bf16_f32(128, 64) | (1u << 15);  // B with rows of 8 along its sum
 #pragma unroll
+      for (int ks = 0; ks < NK; ++ks)  // A and B with rows of 8 along their sum
+        mma_bf16(tmem + L::QKK, smem_desc(base + L::Q + ks * 256, 128, 2048), smem_desc(base + L::K + ks * 256, 128, 2048),
+                 idesc_bf16_f32(128, 64), ks > 0);
+#pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128);
         const uint64_t q = smem_desc(base + L::Q + ks * 4096, 2048, 128);
         const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024);
         const uint64_t xc = smem_desc(base + L::X + ks * 2048, 1024, 128);
-        const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024), nc = smem_desc(base + L::N + ks * 2048, 1024,
-            128);
+        const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024);
+        const uint64_t nc = smem_desc(base + L::N + ks * 2048, 1024, 128);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) mma_bf16(tmem + L::dQ2, k, xr + 512 * p, idk, ks > 0 || p > 0);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          mma_bf16(tmem + L::dKb, q, xc + 512 * p, id64, true);
-          mma_bf16(tmem + L::dKb, k, nr + 512 * p, idk, true);
-          mma_bf16(tmem + L::dKb, k, nc + 512 * p, id64, true);
+        for (int p = 0; p < 3; ++p) {
+          mma_bf16(tmem + L::dQ, k, xr + 512 * p, idk, true);
+          mma_bf16(tmem + L::dK, q, xc + 512 * p, id64, true);
+          mma_bf16(tmem + L::dK, k, nr + 512 * p, idk, true);
+          mma_bf16(tmem + L::dK, k, nc + 512 * p, id64, true);
         }
       }
       mma_commit(mb);
     }
     if (products_done()) {
-      // ---- channel 32 quarter + lane, tokens 32 upper ..
-      const int ch = 32 * quarter + lane;
-      const bool there = ch < a.dk;
-      const unsigned char *sq = sm + L::Q + (ch >> 3) * 128 + (ch & 7) * 2;
+      // ---- the pairs: of row i, the sums over j < t of its terms, which belong to the tokens t <= i
+      if (upper <= (quarter & 1)) {
+        const bool below = upper < (quarter & 1);  // i >= 32 > j, else i and j in the same half
+        float *to = inner + w * kC;
+        float sum = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[16];
+          tmem_ld16(lanes + L::QKK + 32 * upper + 16 * half, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float term = pair[half][e] * x[e];
+            x[e] = below || 16 * half + e <= lane ? sum : 0.f;
+            sum += term;
+          }
+          const float f = sum_lanes(x, lane);
+          if (lane < 16) to[32 * upper + 16 * half + lane] = f;
+        }
+        if (below) {  // tokens t >= 32: rows from t on, all of their terms
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_down_sync(kFull, sum, o);
+            if (lane + o < 32) sum += y;
+          }
+          to[32 + lane] = sum;
+        }
+      }
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        const int i0 = 32 * upper + 16 * half, n = there ? live - i0 : 0;
-        const float *gi = gam + i0;
-        float x[16], y[16];
-        tmem_ld16(lanes + L::dQ1 + i0, x);
-        tmem_ld16(lanes + L::dQ2 + i0, y);
+        const int i0 = 32 * upper + 16 * half, n = mine ? live - i0 : 0;
+        float x[16];
+        tmem_ld16(lanes + L::dQ + i0, x);
         tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = fmaf(gi[e], x[e], y[e]);
         if (a.pdq) {
           float *o = a.pdq + ((tok + i0) * a.H + h) * a.dk + ch;
 #pragma unroll
@@ -1663,17 +1721,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
           for (int e = 0; e < 16; ++e, o += a.ld_dq)
             if (e < n) *o = static_cast<uint16_t>(pack2(x[e], 0.f));
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          x[e] = there ? x[e] * bf16_to_f32(*reinterpret_cast<const uint16_t *>(sq + ((i0 + e) >> 3) * 2048 +
-                                                                              (e & 7) * 16)) : 0.f;
-        const float f = sum_lanes(x, lane);
-        if (lane < 16) flow[quarter * kC + i0 + lane] = f;
-        tmem_ld16(lanes + L::dKb + i0, x);
-        tmem_ld16(lanes + L::dKa + i0, y);
+        tmem_ld16(lanes + L::dK + i0, x);
         tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = fmaf(-gi[e], y[e], x[e]);
         if (a.pdk) {
           float *o = a.pdk + ((tok + i0) * a.H + h) * a.dk + ch;
 #pragma unroll
@@ -1700,40 +1749,38 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     __syncthreads();
   }
   if (w == 1) tmem_dealloc(tmem, L::columns);
-  if (w == 0) {  // the decays' gradient: sums before each token
-    float x[2], before[2], e2[2];
-    int seg[2];
+  if (w == 0) {  // the decays' gradient.  No sum is formed as a difference: what it leaves out may be far larger
+    float x[2], y[2];  // what passes the decays up to a token from the states, and on to the state behind it
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
-      float f = -(rows[kC + m] + rows[3 * kC + m]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f += flow[e * kC + m];
-      e2[i] = rows[m] + rows[2 * kC + m];
-      before[i] = x[i] = f;
+      x[i] = (into[m] + into[kC + m]) + (into[2 * kC + m] + into[3 * kC + m]);
+      y[i] = (out[m] + out[kC + m]) + (out[2 * kC + m] + out[3 * kC + m]);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(kFull, x[i], o);
-        if (lane >= o) x[i] += y;
+        const float xx = __shfl_down_sync(kFull, x[i], o), yy = __shfl_up_sync(kFull, y[i], o);
+        if (lane + o < 32) x[i] += xx;  // over the tokens from this one on
+        if (lane >= o) y[i] += yy;      // up to this one
       }
-      seg[i] = __float_as_int(sg[m]);
     }
-    x[1] += __shfl_sync(kFull, x[0], 31);
-    const uint32_t s0 = __ballot_sync(kFull, lane == 0 || seg[0] != __float_as_int(sg[max(lane - 1, 0)]));
-    const uint32_t s1 = __ballot_sync(kFull, seg[1] != __float_as_int(sg[lane + 31]));
-    before[0] = x[0] - before[0];  // sum over s < t
-    before[1] = x[1] - before[1];
-    const uint32_t upto = 0xffffffffu >> (31 - lane);
-    const float start = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+    x[0] += __shfl_sync(kFull, x[1], 0);
+    const float half = __shfl_sync(kFull, y[0], 31);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float last = __shfl_up_sync(kFull, y[i], 1);
+      y[i] = (lane ? last : 0.f) + (i ? half : 0.f);  // over those before it
+    }
+    const float state =
+        gam[kC - 1] * (((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7])));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
-      // the first token of this one's document
-      const int first = i == 0 ? 31 - __clz(s0 & upto) : (s1 & upto) ? 63 - __clz(s1 & upto) : 31 - __clz(s0);
-      const float p0 = __shfl_sync(kFull, before[0], first & 31), p1 = __shfl_sync(kFull, before[1], first & 31);
+      // of the warps that had rows 0..31 / 32..63 of X and N beside columns 0..31 (0, 2 / 1, 3) and 32..63 (- / 5, 7)
+      const float *p = inner + m + (i ? 4 * kC : 0);
+      const float pairs = (p[i * kC] + p[(2 + i) * kC]) + (inner[kC + m] + inner[3 * kC + m]);
       if (m < live) {
-        a.dla[(tok + m) * a.H + h] = (seg[i] == 0 ? start : 0.f) - (before[i] - (first < 32 ? p0 : p1));
-        a.dbeta[(tok + m) * a.H + h] = e2[i] / beta[m];
+        a.dla[(tok + m) * a.H + h] = state + ((x[i] + y[i]) + pairs);
+        a.dbeta[(tok + m) * a.H + h] = (rows[m] + rows[kC + m]) / beta[m];
       }
     }
   }
@@ -2031,7 +2078,6 @@ extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16
     return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: workspace of %zu bytes, %zu needed", workspace_bytes, l.work);
   if (B == 0 || (H == 0 && (T == 0 || Hk == 0))) return SDM_OK;
   a.by_qk = std::min(row_bytes(q, ld_q, dk), row_bytes(k, ld_k, dk));
-  a.by_v = row_bytes(v, ld_v, dv);
   a.by_dy = row_bytes(dy, static_cast<int64_t>(H) * dv, dv);
   a.pair_y = dv % 2 == 0 && ld_dv % 2 == 0 && aligned(dv_out, 4);
   a.pair_qk = dk % 2 == 0 && ld_dq % 2 == 0 && ld_dk % 2 == 0 && aligned(dq, 4) && aligned(dk_out, 4);
