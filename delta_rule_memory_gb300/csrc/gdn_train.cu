@@ -32,8 +32,7 @@
 // which is what bounds the chunk form in gdn_chunk.cu (2.85 us a chunk for 64 columns, with two parts).
 //
 // Precision.  q, k, v and dy are exact in bf16.  What is not (S, G, T, M, Z, U, X) is taken in three bf16
-// parts, all 24 bits of it, wherever the result reaches an fp32 output (the states, da, dbeta); in two parts,
-// 16 bits, where it only reaches y or dk, which are rounded to bf16's 8.
+// parts, all 24 bits of it; y, dq, dk and dv are rounded to bf16 once, from fp32 sums.
 //
 // B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 86 us, gdn_chain 318, gdn_chain_back 383, gdn_grad 360.
 #include <cuda.h>
@@ -401,18 +400,20 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 // 9,700 and 6,500 of 11,700 cycles, and shared memory beside them: mma.sync runs at 600 TFLOP/s.  Loops are kept
 // small: unrolled four times the backward chain is a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
-template <int NK, int PM, int W, int M, int H>  // PM: parts of the chunk's M
+template <int NK, bool BACK, int W, int M, int H>
 struct Chain {
   static constexpr int P = NK / 4;  // panels of K and Q
   static constexpr int K = 0, Q = K + P * kPanel, V = Q + P * kPanel, T = V + kPanel, sc = T + 3 * kTri,
                        stage = (sc + 3 * kC * 4 + 1023) / 1024 * 1024;
+  // places of U: with one, the main warps wait until the helping ones have read the chunk before's
+  static constexpr int places = !BACK && W < 4 ? 2 : 1;
   // M is read early in a chunk only, so one place does
-  static constexpr int Mq = 2 * stage, state = Mq + PM * kTri, parts = state + W * NK * 3 * 512,
-                       tokens = parts + W * 4 * 3 * 512, sums = tokens + (PM == 2 ? 2 : 1) * W * 8 * 512,
-                       bars = sums + (M == 4 ? W * 4 * 8 * 512 : 0), size = bars + 48;
+  static constexpr int Mq = 2 * stage, state = Mq + 3 * kTri, parts = state + W * NK * 3 * 512,
+                       tokens = parts + W * 4 * 3 * 512, sums = tokens + places * W * 8 * 512,
+                       bars = sums + (M == 4 ? W * 4 * 8 * 512 : 0), size = bars + 48 + W * 8;
 };
-static_assert(Chain<8, 3, 4, 2, 1>::size <= kMaxSmem && Chain<8, 2, 4, 2, 1>::size <= kMaxSmem &&
-                  Chain<8, 2, 2, 4, 2>::size <= kMaxSmem, "");
+static_assert(Chain<8, true, 4, 2, 1>::size <= kMaxSmem && Chain<8, false, 4, 2, 1>::size <= kMaxSmem &&
+                  Chain<8, false, 2, 4, 2>::size <= kMaxSmem, "");
 template <int W, int M, int H>
 constexpr int kChainThreads = 32 * W * (M + H) + (W == 1 ? 32 : 0);
 
@@ -423,11 +424,11 @@ constexpr int kChainThreads = 32 * W * (M + H) + (W == 1 ? 32 : 0);
 template <int W>
 constexpr int kAskers = W == 1 ? 1 : 4;
 
-template <int NK, int PM, int W, int M, int H>
+template <int NK, bool BACK, int W, int M, int H>
 __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, const Gdn &a, const Maps &maps,
                                               int64_t u, int64_t tok, int h, int col0, int by_cols,
                                               const CUtensorMap *cols_map, int who) {
-  using L = Chain<NK, PM, W, M, H>;
+  using L = Chain<NK, BACK, W, M, H>;
   constexpr bool all = kAskers<W> == 1;
   static_assert(all || W * H == kAskers<W>, "");
   const uint32_t mb = smem_u32(bar);
@@ -450,16 +451,15 @@ __device__ __forceinline__ void request_stage(unsigned char *st, uint64_t *bar, 
     umma::bulk_g2s(smem_u32(st + L::sc), a.scal + u * kScal, 3 * kC * 4, mb);
   }
 }
-template <int PM>
 __device__ __forceinline__ void request_m(unsigned char *to, uint64_t *bar, const Gdn &a, int64_t u) {
-  umma::mbar_expect_tx(smem_u32(bar), PM * kTri);
-  umma::bulk_g2s(smem_u32(to), a.m3 + u * (3 * kTri), PM * kTri, smem_u32(bar));
+  umma::mbar_expect_tx(smem_u32(bar), 3 * kTri);
+  umma::bulk_g2s(smem_u32(to), a.m3 + u * (3 * kTri), 3 * kTri, smem_u32(bar));
 }
 // ... and the rest, by the helping warps
-template <int NK, int PM, int W, int M, int H>
+template <int NK, bool BACK, int W, int M, int H>
 __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int64_t tok, int h, int col0, int live,
                                            const uint16_t *cols, int64_t ld_cols, int by_cols, int tid) {
-  using L = Chain<NK, PM, W, M, H>;
+  using L = Chain<NK, BACK, W, M, H>;
   constexpr int threads = 32 * W * H;
   const int hk = h / (a.H / a.Hk), from = col0 & ~63;  // whole panels of value columns
   if (a.by_qk != 16) {
@@ -473,9 +473,9 @@ __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int6
 }
 
 // the rows behind a chunk's last token, which tensor copies fill with whatever follows it
-template <int NK, int PM, int W, int M, int H>
+template <int NK, bool BACK, int W, int M, int H>
 __device__ __forceinline__ void clear_stage(unsigned char *st, const Gdn &a, int live, int by_cols, int tid) {
-  using L = Chain<NK, PM, W, M, H>;
+  using L = Chain<NK, BACK, W, M, H>;
   if (a.by_qk == 16) {
     clear_rows<L::P, 32 * W * H>(st + L::K, live, tid);
     clear_rows<L::P, 32 * W * H>(st + L::Q, live, tid);
@@ -529,17 +529,15 @@ __device__ __forceinline__ void clear(float (&x)[N][4]) {
   for (int i = 0; i < N; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 }
 // the parts of a k-step's A fragments of a state, and the state that they are
-template <int N = 3>
 __device__ __forceinline__ void put_parts(uint4 *m, int lane, const float (&c0)[4], const float (&c1)[4]) {
-  uint32_t s[N][4];
-  a_split<N>(c0, c1, s);
+  uint32_t s[3][4];
+  a_split<3>(c0, c1, s);
 #pragma unroll
-  for (int p = 0; p < N; ++p) m[p * 32 + lane] = make_uint4(s[p][0], s[p][1], s[p][2], s[p][3]);
+  for (int p = 0; p < 3; ++p) m[p * 32 + lane] = make_uint4(s[p][0], s[p][1], s[p][2], s[p][3]);
 }
-template <int N>
-__device__ __forceinline__ void get_parts(const uint4 *m, int lane, uint32_t (&s)[N][4]) {
+__device__ __forceinline__ void get_parts(const uint4 *m, int lane, uint32_t (&s)[3][4]) {
 #pragma unroll
-  for (int p = 0; p < N; ++p) {
+  for (int p = 0; p < 3; ++p) {
     const uint4 v = m[p * 32 + lane];
     s[p][0] = v.x, s[p][1] = v.y, s[p][2] = v.z, s[p][3] = v.w;
   }
@@ -764,17 +762,19 @@ struct Place {
 template <int NK, int W, int M, int H>
 __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn a,
     const __grid_constant__ Maps maps) {
-  using L = Chain<NK, 2, W, M, H>;
+  using L = Chain<NK, false, W, M, H>;
   constexpr int NT = 2 * NK, kOwn = 32 * W * (M + H);  // kOwn: threads before the warp that asks for copies
   constexpr int kBlocks = NK / M, X = kBlocks < 2 ? 1 : 2;        // blocks of 16 channels of a warp's; taken at once
   extern __shared__ __align__(1024) unsigned char sm[];
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages there, M there, two stages free
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);  // two stages there, M there, two stages free, ...
+  uint64_t *read = bars + 6;                                     // ... each tile's U read
   if (threadIdx.x == 0) {
     umma::mbar_init(smem_u32(bars), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 1), kAskers<W>);
     umma::mbar_init(smem_u32(bars + 2), 1);
     umma::mbar_init(smem_u32(bars + 3), W * (M + H));
     umma::mbar_init(smem_u32(bars + 4), W * (M + H));
+    for (int i = 0; i < W; ++i) umma::mbar_init(smem_u32(read + i), H);
     umma::fence_mbar_init();
   }
   before_reading();
@@ -784,7 +784,9 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   const int tiles = (a.dv + 15) >> 4;
   uint4 *hS = reinterpret_cast<uint4 *>(sm + L::state) + w * NK * 96,
       *hP = reinterpret_cast<uint4 *>(sm + L::parts) + w * 4 * 96;
-  uint4 *hU2 = reinterpret_cast<uint4 *>(sm + L::tokens) + w * 8 * 32;  // U's first two parts, of two chunks
+  const auto place = [&](int c) {  // U^T, in fp32
+    return reinterpret_cast<float4 *>(sm + L::tokens) + ((c % L::places) * W + w) * 8 * 32;
+  };
   if (tid == 0 && a.err && a.lens && a.lens[me.b] != len) atomicOr(a.err, SDM_DEVERR_INDEX_RANGE);
   __syncthreads();
   uint32_t limit = tid < kOwn ? kWaitLimit : 4 * kWaitLimit;  // a warp that only asks for copies outwaits the others
@@ -814,9 +816,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
         done(c);
         continue;
       }
-      uint4 *hU = hU2 + (c & 1) * W * 8 * 32;
-      float4 *hX = M == 4 ? reinterpret_cast<float4 *>(sm + L::sums) + w * 32 * 32
-                          : reinterpret_cast<float4 *>(hU);  // partial sums, before U
+      float4 *hU = place(c);
+      float4 *hX = M == 4 ? reinterpret_cast<float4 *>(sm + L::sums) + w * 32 * 32 : hU;  // partial sums, before U
       unsigned char *st = sm + (c & 1) * L::stage;
       const uint32_t uK = smem_u32(st + L::K), uV = smem_u32(st + L::V);
       const float *gam = reinterpret_cast<const float *>(st + L::sc), *tail = gam + kC, *beta = tail + kC;
@@ -826,6 +827,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       {
         float d[8][4];
         state_product<kBlocks, kBlocks>(own, uK, x * kBlocks * 16, lane, d);
+        if (L::places == 1 && c > 0) wait_copies(read + w, (c - 1) & 1, limit, a);
         give_sums<M>(hX, x, lane, d, Z);
       }
       uint32_t v[4 / M][4];
@@ -854,8 +856,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       triangle_product<false, M>(hP, smem_u32(st + L::T), x, lane, E);
       put_tiles<M>(reinterpret_cast<float4 *>(a.e) + at * 256, x, lane, E);
       scale_groups<M>(E, x, beta, t);
-#pragma unroll
-      for (int i = 0; i < 4 / M; ++i) put_parts<2>(hU + group_of<M>(x, i) * 64, lane, E[2 * i], E[2 * i + 1]);
+      put_tiles<M>(hU, x, lane, E);
       meet(all, 32 * (M + H));  // U is there, S and Z have been read
       // S^T = gam_C S^T + (tail U)^T K
       scale_groups<M>(E, x, tail, t);
@@ -887,11 +888,11 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   const int ltid = tid - 32 * W * M, z = me.role - M, zg = H == 4 ? 3 - z : z;
   const auto request = [&](int c) {
     if (lane == 0 && ask)
-      request_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC,
+      request_stage<NK, false, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC,
                                     h, me.col0, a.by_v, &maps.v, ltid >> 5);
     __syncwarp();
   };
-  const auto ask_m = [&](int c) { if (ask && !a.drop) request_m<2>(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
+  const auto ask_m = [&](int c) { if (ask && !a.drop) request_m(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
   if (tid >= kOwn) {
     for (int c = 0; c <= n; ++c) {
       if (c > 0 && together) __syncthreads();
@@ -904,7 +905,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 2, W, M, H>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v,
+    copy_stage<NK, false, W, M, H>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v,
                                a.ld_v, a.by_v, ltid);
   };
   if (n > 0) {
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     }
     wait_copies(bars + (c & 1), (c >> 1) & 1, limit, a);
     if (len - c * kC < kC) {
-      clear_stage<NK, 2, W, M, H>(st, a, len - c * kC, a.by_v, ltid);
+      clear_stage<NK, false, W, M, H>(st, a, len - c * kC, a.by_v, ltid);
       __syncthreads();
     }
     if (me.mine) meet(ready, 32 * (M + H));
@@ -938,7 +939,17 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       done(c);
       continue;
     }
-    const uint4 *hU = hU2 + (c & 1) * W * 8 * 32;
+    const float4 *hU = place(c);
+    const auto get_u = [&](int ks, uint32_t(&us)[3][4]) {
+      float u[2][4];
+      get(hU + ks * 64, lane, u);
+      a_split<3>(u[0], u[1], us);
+    };
+    const auto done_u = [&] {  // this warp has read U
+      if (L::places > 1) return;
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(smem_u32(read + w));
+    };
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
     float Y[8 / H][4];  // the own groups of tokens
@@ -946,12 +957,12 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     {  // Y^T = gam S^T Q^T
 #pragma unroll(2 * H)
       for (int ks = 0; ks < NK; ++ks) {
-        uint32_t s[2][4], r[4 / H][4];
+        uint32_t s[3][4], r[4 / H][4];
         get_parts(hS + ks * 96, lane, s);
 #pragma unroll
         for (int i = 0; i < 4 / H; ++i) b_rows(uQ, 16 * group_of<H>(zg, i), 16 * ks, lane, r[i]);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < 3; ++p)
 #pragma unroll
           for (int i = 0; i < 4 / H; ++i) {
             fma16816(Y[2 * i], s[p], r[i][0], r[i][1]);
@@ -962,18 +973,19 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     }
     wait_copies(bars + 2, c & 1, limit, a);
     if constexpr (H == 4) {  // += U^T M^T, M's fragments read before U is there
-      uint32_t r[4][2][4], us[4][2][4];
+      uint32_t r[4][3][4], us[4][3][4];
       float l[2][4];
       clear(l);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         if (ks <= zg)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, zg, ks, lane, r[ks][p]);
+          for (int p = 0; p < 3; ++p) tri_rows(uM + p * kTri, zg, ks, lane, r[ks][p]);
       meet(all, 32 * (M + H));
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        if (ks <= zg) get_parts(hU + ks * 64, lane, us[ks]);
+        if (ks <= zg) get_u(ks, us[ks]);
+      done_u();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         if (ks <= zg) products(Y, l, 0, us[ks], r[ks]);
@@ -982,15 +994,16 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       meet(all, 32 * (M + H));
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        uint32_t us[2][4];
-        get_parts(hU + ks * 64, lane, us);
+        uint32_t us[3][4];
+        get_u(ks, us);
+        if (ks == 3) done_u();
 #pragma unroll
         for (int i = 0; i < 4 / H; ++i) {
           const int n = group_of<H>(zg, i);
           if (n < ks) continue;
-          uint32_t r[2][4];
+          uint32_t r[3][4];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) tri_rows(uM + p * kTri, n, ks, lane, r[p]);
+          for (int p = 0; p < 3; ++p) tri_rows(uM + p * kTri, n, ks, lane, r[p]);
           products(Y, Y, i, us, r);
         }
       }
@@ -1026,7 +1039,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
 template <int NK, int W, int M, int H>
 __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(const Gdn a,
     const __grid_constant__ Maps maps) {
-  using L = Chain<NK, 3, W, M, H>;
+  using L = Chain<NK, true, W, M, H>;
   constexpr int NT = 2 * NK, kOwn = 32 * W * (M + H);
   constexpr int kBlocks = NK / M, X = kBlocks < 2 ? 1 : 2, XH = NK / H < 2 ? 1 : 2;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -1143,7 +1156,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
     if (lane == 0 && ask)
-      request_stage<NK, 3, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
+      request_stage<NK, true, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
           a.by_dy, &maps.dy, ltid >> 5);
     __syncwarp();
   };
@@ -1159,11 +1172,11 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, 3, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC),
+    copy_stage<NK, true, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC),
                                a.dy, ld_y, a.by_dy, ltid);
   };
   const auto ask_m = [&](int c) {
-    if (ltid == 0 && !a.drop) request_m<3>(sm + L::Mq, bars + 2, a, me.bh * a.n + c);
+    if (ltid == 0 && !a.drop) request_m(sm + L::Mq, bars + 2, a, me.bh * a.n + c);
   };
   if (n > 0) {
     if (kAskers<W> > 1) request(n - 1);
@@ -1182,7 +1195,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
     wait_copies(bars + (it & 1), (it >> 1) & 1, limit, a);
     wait_copies(bars + 2, it & 1, limit, a);
     if (len - c * kC < kC) {
-      clear_stage<NK, 3, W, M, H>(st, a, len - c * kC, a.by_dy, ltid);
+      clear_stage<NK, true, W, M, H>(st, a, len - c * kC, a.by_dy, ltid);
       __syncthreads();
     }
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq), uY = smem_u32(st + L::V);
@@ -1965,9 +1978,9 @@ template <int NK, int W, int M, int H>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
   const int64_t grid = (l.tiles + W - 1) / W * a.B * a.H;
   return back ? launch(gdn_chain_back<NK, W, M, H>, "gdn_backward", grid, kChainThreads<W, M, H>,
-                       Chain<NK, 3, W, M, H>::size, st, a, maps)
-              : launch(gdn_chain<NK, W, M, H>, "gdn_train", grid, kChainThreads<W, M, H>, Chain<NK, 2, W, M, H>::size,
-                       st, a, maps);
+                       Chain<NK, true, W, M, H>::size, st, a, maps)
+              : launch(gdn_chain<NK, W, M, H>, "gdn_train", grid, kChainThreads<W, M, H>,
+                       Chain<NK, false, W, M, H>::size, st, a, maps);
 }
 template <int NK>
 int run_chain(const Gdn &a, const Maps &maps, const Layout &l, bool back, cudaStream_t st) {
