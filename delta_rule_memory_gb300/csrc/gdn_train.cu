@@ -952,8 +952,9 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     };
     const uint32_t uQ = smem_u32(st + L::Q), uM = smem_u32(sm + L::Mq);
     const float *gam = reinterpret_cast<const float *>(st + L::sc);
-    float Y[8 / H][4];  // the own groups of tokens
+    float Y[8 / H][4], l[8 / H][4];  // the own groups of tokens; small products apart
     clear(Y);
+    clear(l);
     {  // Y^T = gam S^T Q^T
 #pragma unroll(2 * H)
       for (int ks = 0; ks < NK; ++ks) {
@@ -965,17 +966,18 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
         for (int p = 0; p < 3; ++p)
 #pragma unroll
           for (int i = 0; i < 4 / H; ++i) {
-            fma16816(Y[2 * i], s[p], r[i][0], r[i][1]);
-            fma16816(Y[2 * i + 1], s[p], r[i][2], r[i][3]);
+            float(&to)[8 / H][4] = p == 0 ? Y : l;
+            fma16816(to[2 * i], s[p], r[i][0], r[i][1]);
+            fma16816(to[2 * i + 1], s[p], r[i][2], r[i][3]);
           }
       }
+      add(Y, l);
+      clear(l);
       scale_groups<H>(Y, zg, gam, t);
     }
     wait_copies(bars + 2, c & 1, limit, a);
     if constexpr (H == 4) {  // += U^T M^T, M's fragments read before U is there
       uint32_t r[4][3][4], us[4][3][4];
-      float l[2][4];
-      clear(l);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         if (ks <= zg)
@@ -1004,9 +1006,10 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
           uint32_t r[3][4];
 #pragma unroll
           for (int p = 0; p < 3; ++p) tri_rows(uM + p * kTri, n, ks, lane, r[p]);
-          products(Y, Y, i, us, r);
+          products(Y, l, i, us, r);
         }
       }
+      add(Y, l);
     }
     done(c);
     // y, rounded once: pairs of tokens turned into pairs of columns
@@ -1271,9 +1274,12 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
 // value columns has the key channels or two times the tokens as its M = 128 and the tokens as N:
 //   [dQ | dKa]^T [128 x 128] = S [dY | dZ]^T        dK^T [128 x 64] = G U^T
 //   [X; N]       [128 x 64]  = [dY; dZ] U^T
-// and then, with X and N times their decays, dQ <- gam dQ and dK <- tail dK - gam dKa written back,
-//   dQ^T += K^T X^T,   dK^T += Q^T X + K^T (N^T + N),   [QK; KK] [128 x 64] = [Q; K] K^T,
-// the last in X's and N's place, for the decays' gradient.
+// and then, with X and N times their decays,
+//   [QK; KK] [128 x 64] = [Q; K] K^T,   dQ2^T = K^T X^T,   dK2^T = Q^T X + K^T (N^T + N),
+//   dQ = gam dQ + dQ2,   dK = (tail dK - gam dKa) + dK2,
+// QK and KK for the decays' gradient and, like dQ2, in X's and N's place; dK2 in dKa's.  The tensor cores cut a
+// sum off at each product, towards 0, so a sum with fewer products behind it is nearer: with dQ2 and dK2 on top of
+// dQ and dK those were 5.9e-7 and 8.5e-7 off.
 // The value columns come 32 at a time, as the chains left them, read ahead by a piece: S by bulk copies (through
 // registers alone, whose loads wait for one another at the door, 404 us in place of 360), the rest 16 bytes a
 // lane.  They are split into bf16 parts and stored as the 8 x 8 cores of the operands, where a warp's store is
@@ -1299,7 +1305,8 @@ struct Grad {
                        bars = red + 32, size = bars + 32;
   // once the value columns are done
   static constexpr int X = 0, N = X + 3 * 8192, Q = N + 3 * 8192, K = Q + 16384;
-  static constexpr uint32_t dQ = 0, dKa = 64, dK = 128, XN = 192, QKK = 192, columns = 256;  // tensor memory
+  static constexpr uint32_t dQ = 0, dKa = 64, dK = 128, XN = 192, columns = 256;  // tensor memory
+  static constexpr uint32_t QKK = XN, dQ2 = XN, dK2 = dKa;
   static_assert(K + 16384 <= stage, "");
 };
 static_assert(2 * (Grad::size + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -1618,7 +1625,16 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     }
     cp_async_wait<0>();
     fence_async_smem();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    if (tid == 0) {
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks)  // A and B with rows of 8 along their sum
+        mma_bf16(tmem + L::QKK, smem_desc(base + L::Q + ks * 256, 128, 2048), smem_desc(base + L::K + ks * 256, 128, 2048),
+                 idesc_bf16_f32(128, 64), ks > 0);
+      mma_commit(mb);
+    }
     // ---- channel 32 quarter + lane, tokens 32 upper ..: what comes from the states, and its part in the decays' gradient
     const int ch = 32 * quarter + lane;
     const bool mine = ch < a.dk;
@@ -1640,11 +1656,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          x[e] *= gi[e];
           y[e] *= gi[e];
-          f[e] = mine ? query(i0 + e) * x[e] - key(i0 + e) * y[e] : 0.f;
+          f[e] = mine ? query(i0 + e) * (gi[e] * x[e]) - key(i0 + e) * y[e] : 0.f;
         }
-        tmem_st16(lanes + L::dQ + i0, x);
         const float a0 = sum_lanes(f, lane);
         if (lane < 16) into[quarter * kC + i0 + lane] = a0;
         tmem_ld16(lanes + L::dK + i0, x);
@@ -1661,34 +1675,23 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
       }
       tmem_st_wait();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (tid == 0) {
-      const uint32_t idk = idesc_bf16_f32(128, 64) | (1u << 15);  // B with rows of 8 along its sum
-#pragma unroll
-      for (int ks = 0; ks < NK; ++ks)  // A and B with rows of 8 along their sum
-        mma_bf16(tmem + L::QKK, smem_desc(base + L::Q + ks * 256, 128, 2048), smem_desc(base + L::K + ks * 256, 128, 2048),
-                 idesc_bf16_f32(128, 64), ks > 0);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128);
-        const uint64_t q = smem_desc(base + L::Q + ks * 4096, 2048, 128);
-        const uint64_t xr = smem_desc(base + L::X + ks * 256, 128, 1024);
-        const uint64_t xc = smem_desc(base + L::X + ks * 2048, 1024, 128);
-        const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024);
-        const uint64_t nc = smem_desc(base + L::N + ks * 2048, 1024, 128);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          mma_bf16(tmem + L::dQ, k, xr + 512 * p, idk, true);
-          mma_bf16(tmem + L::dK, q, xc + 512 * p, id64, true);
-          mma_bf16(tmem + L::dK, k, nr + 512 * p, idk, true);
-          mma_bf16(tmem + L::dK, k, nc + 512 * p, id64, true);
-        }
-      }
-      mma_commit(mb);
-    }
     if (products_done()) {
+      const uint32_t idk = idesc_bf16_f32(128, 64) | (1u << 15);  // B with rows of 8 along its sum
+      if (tid == 0) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t k = smem_desc(base + L::K + ks * 4096, 2048, 128);
+            const uint64_t q = smem_desc(base + L::Q + ks * 4096, 2048, 128);
+            const uint64_t xc = smem_desc(base + L::X + ks * 2048, 1024, 128);
+            const uint64_t nr = smem_desc(base + L::N + ks * 256, 128, 1024);
+            const uint64_t nc = smem_desc(base + L::N + ks * 2048, 1024, 128);
+            mma_bf16(tmem + L::dK2, q, xc + 512 * p, id64, p < 2 || ks > 0);
+            mma_bf16(tmem + L::dK2, k, nr + 512 * p, idk, true);
+            mma_bf16(tmem + L::dK2, k, nc + 512 * p, id64, true);
+          }
+      }
       // ---- the pairs: of row i, the sums over j < t of its terms, which belong to the tokens t <= i
       if (upper <= (quarter & 1)) {
         const bool below = upper < (quarter & 1);  // i >= 32 > j, else i and j in the same half
@@ -1717,12 +1720,30 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
           to[32 + lane] = sum;
         }
       }
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      if (tid == 0) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16(tmem + L::dQ2, smem_desc(base + L::K + ks * 4096, 2048, 128),
+                     smem_desc(base + L::X + ks * 256, 128, 1024) + 512 * p, idk, p < 2 || ks > 0);
+        mma_commit(mb);
+      }
+    }
+    if (ok && products_done()) {
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int i0 = 32 * upper + 16 * half, n = mine ? live - i0 : 0;
-        float x[16];
+        const float *gi = gam + i0;
+        float x[16], y[16];
         tmem_ld16(lanes + L::dQ + i0, x);
+        tmem_ld16(lanes + L::dQ2 + i0, y);
         tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = fmaf(gi[e], x[e], y[e]);
         if (a.pdq) {
           float *o = a.pdq + ((tok + i0) * a.H + h) * a.dk + ch;
 #pragma unroll
@@ -1735,7 +1756,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
             if (e < n) *o = static_cast<uint16_t>(pack2(x[e], 0.f));
         }
         tmem_ld16(lanes + L::dK + i0, x);
+        tmem_ld16(lanes + L::dK2 + i0, y);
         tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] += y[e];
         if (a.pdk) {
           float *o = a.pdk + ((tok + i0) * a.H + h) * a.dk + ch;
 #pragma unroll
