@@ -118,6 +118,21 @@ __device__ __forceinline__ Wide running(Wide x, int lane) {
   return x;
 }
 
+// 2^x: ex2.approx of the upper float, 2^-22 relative, and what the lower one adds to first order (it is below
+// 2^-24 of the upper one, which is at most 2^15 here).  The upper one alone is off by that: 7e-7 of the result at
+// e^-20, twice that for a difference of two of them in 32 bits
+__device__ __forceinline__ float exp2_wide(Wide x) {
+  const float e = umma::ex2_approx(x.hi);
+  return fmaf(e, x.lo * 0.693147181f, e);
+}
+
+// the decay from token j to a later token i: their sums' difference with its rounding, which is exact where no decay
+// in between is above 1
+__device__ __forceinline__ float decay_between(Wide i, Wide j) {
+  const float hi = i.hi - j.hi;
+  return exp2_wide({hi, ((i.hi - hi) - j.hi) + (i.lo - j.lo)});
+}
+
 // Tensor maps of q, k, v and dy as [token][head][channel], boxes of one panel; set where rows can be copied by
 // 16 bytes
 struct Maps {
@@ -319,8 +334,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
     for (int i = 0; i < 2; ++i) {
       const int m = lane + 32 * i;
       const Wide rest = end - x[i];
-      const float v[6] = {seg[i] == 0 ? umma::ex2_approx(x[i].hi) : 0.f,
-                          seg[i] == last ? umma::ex2_approx(rest.hi) : 0.f,
+      const float v[6] = {seg[i] == 0 ? exp2_wide(x[i]) : 0.f, seg[i] == last ? exp2_wide(rest) : 0.f,
                           be[i], x[i].hi, x[i].lo, __int_as_float(seg[i])};
 #pragma unroll
       for (int e = 0; e < 6; ++e) {
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * w + g + 8 * (e >> 1), j = 8 * nt + 2 * t + (e & 1);
       const bool on = j <= i && __float_as_int(sg[i]) == __float_as_int(sg[j]);
-      const float d = on ? umma::ex2_approx((lh[i] - lh[j]) + (ll[i] - ll[j])) : 0.f;
+      const float d = on ? decay_between({lh[i], ll[i]}, {lh[j], ll[j]}) : 0.f;
       sL[i * kLd + j] = on && j < i ? d * G[nt][e] * be[j] : 0.f;
       sX[i * kLd + j] = on ? d * P[nt][e] : 0.f;
     }
@@ -1595,7 +1609,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     float pair[2][16];  // they stay, for the decays' gradient
     {
       const int i = 32 * (quarter & 1) + lane;
-      const float li = lh[i], lli = ll[i];
+      const Wide li{lh[i], ll[i]};
       const int si = __float_as_int(sg[i]);
       unsigned char *to = sm + (is_n ? L::N : L::X) + (i >> 3) * 1024 + (i & 7) * 16;
 #pragma unroll
@@ -1608,7 +1622,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
         for (int e = 0; e < 16; ++e) {
           const int j = j0 + e;
           const bool on = (is_n ? j < i : j <= i) && si == __float_as_int(sg[j]);
-          const float d = umma::ex2_approx((li - lh[j]) + (lli - ll[j]));
+          const float d = decay_between(li, {lh[j], ll[j]});
           x[e] = on ? (is_n ? -d : d) * x[e] : 0.f;
         }
 #pragma unroll

@@ -71,7 +71,7 @@ __device__ __forceinline__ float low2(uint32_t v) { return __uint_as_float(v << 
 __device__ __forceinline__ float high2(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // x = s[0] + s[1] + ... in bf16, each the rounding of what the ones before leave: two parts keep 16 bits of x,
-// three keep all 24 (to 2^-26 relative).
+// three keep all 24 (to 2^-26 relative) as long as they are not below bf16's least step: to 2^-134 absolute.
 template <int N>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&s)[N]) {
 #pragma unroll
