@@ -818,7 +818,10 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     const int x = me.role, vp = ((me.col0 & 63) >> 3) + 2 * w;  // vp: the tile's pieces of the value columns' panel
     uint4 *own = hS + x * kBlocks * 96;
     float S[2 * kBlocks][4];  // the own channels' state beside its parts
-    read_state(a.state_in ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
+    // a row that starts with a reset does not read it: gam would be 0, but does not take a NaN away.  (Resets further on
+    // multiply by 0.  The same there, where a chunk's first token resets, made every chunk 0.1 us longer.)
+    const bool given = a.state_in && !(a.reset && n > 0 && a.reset[me.tok] != 0);
+    read_state(given ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
 #pragma unroll
     for (int ks = 0; ks < kBlocks; ++ks) put_parts(own + ks * 96, lane, S[2 * ks], S[2 * ks + 1]);
     if (me.mine && n > 0) arrive(ready, 32 * (M + H));  // the state's parts are there

@@ -649,7 +649,9 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  *             count as -200, whose exponential is 0.   beta : fp32 [B,T,H];
  *             magnitudes below 1e-18 count as 1e-18, by which dbeta has its limit.
  * reset     : optional uint8 [B,T]; where it is not 0, the state is taken as 0
- *             before token t (a new document starts in a packed row).
+ *             before token t (a new document starts in a packed row).  A row that
+ *             starts with one does not read `state`, which need not have been set; later
+ *             ones have finite states to cut off (see below for NaN).
  * lens      : optional int32 [B], 0 <= lens[b] <= T: only the first lens[b]
  *             tokens exist; the rows behind them are neither read nor written.
  *             Other values are clamped and set SDM_DEVERR_INDEX_RANGE.
@@ -672,8 +674,9 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * needs of itself, one that runs the chunks in order (16 value columns to three to eight warps), and in
  * the backward one for the sums over value columns.  States, sums and
  * decays are fp32 (the sums of log_alpha wider); y, dq, dk and dv are rounded once, to nearest even.
- * NaN and infinities are not looked for: they spread over their chunk and the
- * tokens behind it (in the backward, before it).
+ * NaN and infinities are not looked for: they spread over the 64 tokens of their chunk
+ * and the tokens of the row behind it, other documents' among them (in the backward, over
+ * those before it).  They do not reach other sequences or heads.
  * Limits: 1 <= dk <= 128, 1 <= dv <= 1024, H a multiple of Hk; B, H < 65536,
  *         T < 2^30, B T < 2^31, B H ceil(T/64) ceil(dv/16) < 2^31; distances < 2^27.  Pointers aligned to their
  *         element.  Any B, T or H of 0 is allowed (T = 0 copies the state).
