@@ -1107,6 +1107,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
                  lane, y);
       put_parts(own + ks * 96, lane, y[0], y[1]);
       if (me.mine) put(kept + n * step + ks * 64, lane, y);
+      // without a token its bits go on as they are: the parts do not hold infinities
+      if (n == 0) write_state(a.state_out + me.bh * a.dk * a.dv, 16 * (x * kBlocks + ks), a.dk, a.dv, col, lane, y);
     }
     for (int c = n - 1; c >= 0; --c) {
       const int it = n - 1 - c;
@@ -1159,7 +1161,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
       }
       done(it);
     }
-    if (me.mine)
+    if (me.mine && n > 0)
 #pragma unroll 1
       for (int ks = 0; ks < kBlocks; ++ks) {
         uint32_t s[3][4];
