@@ -70,9 +70,8 @@ __global__ void __launch_bounds__(kThreads, 5) gdn_step_kernel(const StepArgs a)
   for (int i = 0; i < NR; ++i) {
     const int r = r0 + kRows * i;
     if (VEC) {
-      const float4 x = r < a.dk &&
-          c < a.dv ? __ldcs(reinterpret_cast<const float4 *>(S + static_cast<int64_t>(r) * a.dv))
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < a.dk && c < a.dv) x = __ldcs(reinterpret_cast<const float4 *>(S + static_cast<int64_t>(r) * a.dv));
       s[i][0] = x.x, s[i][1] = x.y, s[i][2] = x.z, s[i][3] = x.w;
     } else {
 #pragma unroll
@@ -130,8 +129,8 @@ __global__ void __launch_bounds__(kThreads, 5) gdn_step_kernel(const StepArgs a)
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
       dot += kq[t & 1][i];
-      const float4 p = *reinterpret_cast<const float4 *>(&pt[i][0][4 * (lane & 7)]),
-          o = *reinterpret_cast<const float4 *>(&pt[i][1][4 * (lane & 7)]);
+      const float4 p = *reinterpret_cast<const float4 *>(&pt[i][0][4 * (lane & 7)]);
+      const float4 o = *reinterpret_cast<const float4 *>(&pt[i][1][4 * (lane & 7)]);
       p4[0] += p.x, p4[1] += p.y, p4[2] += p.z, p4[3] += p.w;
       o4[0] += o.x, o4[1] += o.y, o4[2] += o.z, o4[3] += o.w;
     }
@@ -157,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 5) gdn_step_kernel(const StepArgs a)
     if (r >= a.dk) continue;
     if (VEC) {
       if (c < a.dv)
-        __stcs(reinterpret_cast<float4 *>(S + static_cast<int64_t>(r) * a.dv), make_float4(s[i][0], s[i][1], s[i][2],
-            s[i][3]));
+        __stcs(reinterpret_cast<float4 *>(S + static_cast<int64_t>(r) * a.dv),
+               make_float4(s[i][0], s[i][1], s[i][2], s[i][3]));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -173,37 +172,32 @@ __global__ void __launch_bounds__(kThreads, 5) gdn_step_kernel(const StepArgs a)
 using namespace sdm;
 
 extern "C" int gdn_step(float *state, const uint16_t *q, int64_t ld_q, const uint16_t *k, int64_t ld_k,
-    const uint16_t *v,
-                        int64_t ld_v, const float *log_alpha, const float *beta, const int32_t *slots,
-                        const int32_t *lens, int P, int B, int T, int Hk, int H, int dk, int dv, uint16_t *y,
-                        int32_t *dev_err, void *stream) {
+                        const uint16_t *v, int64_t ld_v, const float *log_alpha, const float *beta,
+                        const int32_t *slots, const int32_t *lens, int P, int B, int T, int Hk, int H, int dk, int dv,
+                        uint16_t *y, int32_t *dev_err, void *stream) {
   if (P < 0 || B < 0 || T < 0 || Hk < 0 || H < 0) return set_error(SDM_ERR_INVALID_ARG, "gdn_step: negative size");
-  if (B >= 65536 || H >= 65536 || T >= (1 << 20) || dk < 1 || dk > 128 || dv < 1 || dv > 1024 || (H > 0 && (Hk == 0 ||
-      H % Hk != 0)) ||
+  if (B >= 65536 || H >= 65536 || T >= (1 << 20) || dk < 1 || dk > 128 || dv < 1 || dv > 1024 ||
+      (H > 0 && (Hk == 0 || H % Hk != 0)) ||
       static_cast<int64_t>(B) * H * ((dv + kCols - 1) / kCols) > INT_MAX)
     return set_error(SDM_ERR_SHAPE, "gdn_step: sizes beyond the limits");
   if (!slots && P < B) return set_error(SDM_ERR_SHAPE, "gdn_step: %d states for %d sequences", P, B);
   if (ld_q < static_cast<int64_t>(Hk) * dk || ld_k < static_cast<int64_t>(Hk) * dk ||
-      ld_v < static_cast<int64_t>(H) * dv ||
-      ld_q >= (1 << 27) || ld_k >= (1 << 27) || ld_v >= (1 << 27))
+      ld_v < static_cast<int64_t>(H) * dv || ld_q >= (1 << 27) || ld_k >= (1 << 27) || ld_v >= (1 << 27))
     return set_error(SDM_ERR_SHAPE,
-        "gdn_step: a token's row must be at most 2^27 elements from the next and hold its heads");
+                     "gdn_step: a token's row must be at most 2^27 elements from the next and hold its heads");
   if (B == 0 || T == 0 || H == 0) return SDM_OK;
   if ((!state && P > 0) || !q || !k || !v || !log_alpha || !beta || !y)
     return set_error(SDM_ERR_INVALID_ARG, "gdn_step: null pointer");
   if (!aligned(state, 4) || !aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(log_alpha, 4) ||
       !aligned(beta, 4) || !aligned(y, 2) || !aligned(slots, 4) || !aligned(lens, 4) || !aligned(dev_err, 4))
     return set_error(SDM_ERR_ALIGN, "gdn_step: a pointer is not aligned");
-  StepArgs a{state, q, k, v, ld_q, ld_k, ld_v, log_alpha, beta, slots, lens, P, B, T, Hk, H, dk, dv,
-      (dv + kCols - 1) / kCols, y, dev_err};
+  StepArgs a{state, q, k, v, ld_q, ld_k, ld_v, log_alpha, beta, slots, lens,
+             P, B, T, Hk, H, dk, dv, (dv + kCols - 1) / kCols, y, dev_err};
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(B) * H * a.groups);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool vec = dv % 4 == 0 && aligned(state, 16);
-  if (dk <= 64)
-    vec ? gdn_step_kernel<64 / kRows, true><<<grid, kThreads, 0, st>>>(a) : gdn_step_kernel<64 / kRows, false><<<grid,
-        kThreads, 0, st>>>(a);
-  else
-    vec ? gdn_step_kernel<128 / kRows, true><<<grid, kThreads, 0, st>>>(a) : gdn_step_kernel<128 / kRows, false><<<grid,
-        kThreads, 0, st>>>(a);
+  auto kernel = vec ? gdn_step_kernel<128 / kRows, true> : gdn_step_kernel<128 / kRows, false>;
+  if (dk <= 64) kernel = vec ? gdn_step_kernel<64 / kRows, true> : gdn_step_kernel<64 / kRows, false>;
+  kernel<<<grid, kThreads, 0, st>>>(a);
   return check_launch("gdn_step");
 }

@@ -92,7 +92,7 @@ __device__ __forceinline__ void tri_rows(uint32_t tri, int n, int k, int lane, u
 }
 // ... and of block (k, n), B[k][n] = tri[k][n]
 __device__ __forceinline__ void tri_cols(uint32_t tri, int n, int k, int lane, uint32_t (&r)[4]) {
-  ldsm4_t(tri + block_at(k, n) + ((lane & 8) << 5) + ((lane & 16) << 3) + (lane & 7) * 16, r);
+  ldsm_x4_trans(tri + block_at(k, n) + ((lane & 8) << 5) + ((lane & 16) << 3) + (lane & 7) * 16, r);
 }
 
 // A sum of many terms as two floats: to about 2^-46 of the largest partial sum
@@ -482,7 +482,7 @@ __device__ __forceinline__ void copy_stage(unsigned char *st, const Gdn &a, int6
   }
   if (by_cols != 16)
     load_tile<1, threads>(st + L::V, cols + tok * ld_cols + h * a.dv + from, ld_cols, live, min(64, a.dv - from),
-        by_cols, tid);
+                          by_cols, tid);
   cp_async_commit();
 }
 
@@ -501,7 +501,7 @@ __device__ __forceinline__ void clear_stage(unsigned char *st, const Gdn &a, int
 // S^T of 16 columns and 8 NT rows of a [dk][dv] matrix as an accumulator, and back
 template <int NT>
 __device__ __forceinline__ void read_state(const float *m, int row, int dk, int dv, int col, int lane,
-    float (&S)[NT][4]) {
+                                           float (&S)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -513,7 +513,7 @@ __device__ __forceinline__ void read_state(const float *m, int row, int dk, int 
 }
 template <int NT>
 __device__ __forceinline__ void write_state(float *m, int row, int dk, int dv, int col, int lane,
-    const float (&S)[NT][4]) {
+                                            const float (&S)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -727,8 +727,8 @@ __device__ __forceinline__ void triangle_product(const uint4 *parts, uint32_t tr
       uint32_t a[3][4], r[3][4];
       get_parts(parts + ks * 96, lane, a);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) BACK ? tri_cols(tri + p * kTri, n, ks, lane, r[p]) : tri_rows(tri + p * kTri, n, ks,
-          lane, r[p]);
+      for (int p = 0; p < 3; ++p)
+        BACK ? tri_cols(tri + p * kTri, n, ks, lane, r[p]) : tri_rows(tri + p * kTri, n, ks, lane, r[p]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         fma16816(m[j], a[1], r[1][2 * j], r[1][2 * j + 1]);
@@ -818,8 +818,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
     const int x = me.role, vp = ((me.col0 & 63) >> 3) + 2 * w;  // vp: the tile's pieces of the value columns' panel
     uint4 *own = hS + x * kBlocks * 96;
     float S[2 * kBlocks][4];  // the own channels' state beside its parts
-    // a row that starts with a reset does not read it: gam would be 0, but does not take a NaN away.  (Resets further on
-    // multiply by 0.  The same there, where a chunk's first token resets, made every chunk 0.1 us longer.)
+    // a row that starts with a reset does not read it: gam would be 0, but does not take a NaN away.  (Resets further
+    // on multiply by 0.  The same there, where a chunk's first token resets, made every chunk 0.1 us longer.)
     const bool given = a.state_in && !(a.reset && n > 0 && a.reset[me.tok] != 0);
     read_state(given ? a.state_in + me.bh * a.dk * a.dv : nullptr, x * kBlocks * 16, a.dk, a.dv, col, lane, S);
 #pragma unroll
@@ -850,8 +850,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
       uint32_t v[4 / M][4];
 #pragma unroll
       for (int i = 0; i < 4 / M; ++i)  // tile[token][column]: rows of V^T are its columns
-        ldsm4_t(uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)),
-                v[i]);
+        ldsm_x4_trans(
+            uV + piece(16 * group_of<M>(x, i) + (((lane >> 4) & 1) << 3) + (lane & 7), vp + ((lane >> 3) & 1)), v[i]);
       meet(pair, 32 * M);
       take_sums<M>(hX, x, lane, Z);
       // Z^T = V^T - gam S^T K^T
@@ -905,8 +905,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
   const int ltid = tid - 32 * W * M, z = me.role - M, zg = H == 4 ? 3 - z : z;
   const auto request = [&](int c) {
     if (lane == 0 && ask)
-      request_stage<NK, false, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c, me.tok + c * kC,
-                                    h, me.col0, a.by_v, &maps.v, ltid >> 5);
+      request_stage<NK, false, W, M, H>(sm + (c & 1) * L::stage, bars + (c & 1), a, maps, me.bh * a.n + c,
+                                        me.tok + c * kC, h, me.col0, a.by_v, &maps.v, ltid >> 5);
     __syncwarp();
   };
   const auto ask_m = [&](int c) { if (ask && !a.drop) request_m(sm + L::Mq, bars + 2, a, me.bh * a.n + c); };
@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain(const Gdn
 
   const auto copy = [&](int c) {
     copy_stage<NK, false, W, M, H>(sm + (c & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC), a.v,
-                               a.ld_v, a.by_v, ltid);
+                                   a.ld_v, a.by_v, ltid);
   };
   if (n > 0) {
     if (kAskers<W> > 1) {
@@ -1178,8 +1178,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   const auto request = [&](int c) {
     const int s = (n - 1 - c) & 1;
     if (lane == 0 && ask)
-      request_stage<NK, true, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h, me.col0,
-          a.by_dy, &maps.dy, ltid >> 5);
+      request_stage<NK, true, W, M, H>(sm + s * L::stage, bars + s, a, maps, me.bh * a.n + c, me.tok + c * kC, h,
+                                       me.col0, a.by_dy, &maps.dy, ltid >> 5);
     __syncwarp();
   };
   if (tid >= kOwn) {
@@ -1194,8 +1194,8 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
   }
 
   const auto copy = [&](int c) {
-    copy_stage<NK, true, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0, min(len - c * kC, kC),
-                               a.dy, ld_y, a.by_dy, ltid);
+    copy_stage<NK, true, W, M, H>(sm + ((n - 1 - c) & 1) * L::stage, a, me.tok + c * kC, h, me.col0,
+                                  min(len - c * kC, kC), a.dy, ld_y, a.by_dy, ltid);
   };
   const auto ask_m = [&](int c) {
     if (ltid == 0 && !a.drop) request_m(sm + L::Mq, bars + 2, a, me.bh * a.n + c);
@@ -1332,8 +1332,7 @@ static_assert(2 * (Grad::size + 1024) <= 228 * 1024, "two CTAs an SM");
 
 // 64 rows of `width` bf16 as 8 x 8 cores [row / 8][column / 8], zeros from row `live` on
 __device__ __forceinline__ void load_cores(unsigned char *to, const uint16_t *src, int64_t ld, int live, int width,
-    int by,
-                                           int tid) {
+                                           int by, int tid) {
 #pragma unroll 4
   for (int i = 0; i < kC * 16 / kGradThreads; ++i) {
     // a warp: 8 rows, 4 pieces of 16 bytes of each
@@ -1650,11 +1649,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) gdn_grad(const Gdn a) {
     if (tid == 0) {
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks)  // A and B with rows of 8 along their sum
-        mma_bf16(tmem + L::QKK, smem_desc(base + L::Q + ks * 256, 128, 2048), smem_desc(base + L::K + ks * 256, 128, 2048),
-                 idesc_bf16_f32(128, 64), ks > 0);
+        mma_bf16(tmem + L::QKK, smem_desc(base + L::Q + ks * 256, 128, 2048),
+                 smem_desc(base + L::K + ks * 256, 128, 2048), idesc_bf16_f32(128, 64), ks > 0);
       mma_commit(mb);
     }
-    // ---- channel 32 quarter + lane, tokens 32 upper ..: what comes from the states, and its part in the decays' gradient
+    // ---- channel 32 quarter + lane, tokens 32 upper ..: what comes from the states, its part in the decays' gradient
     const int ch = 32 * quarter + lane;
     const bool mine = ch < a.dk;
     {
@@ -1888,8 +1887,7 @@ struct Layout {
 
 bool sizes_fit(int B, int T, int Hk, int H, int dk, int dv) {
   return B >= 0 && T >= 0 && H >= 0 && Hk >= 0 && B < 65536 && H < 65536 && T < (1 << 30) && dk >= 1 && dk <= 128 &&
-      dv >= 1 &&
-         dv <= 1024 && (H == 0 || (Hk > 0 && H % Hk == 0)) &&
+         dv >= 1 && dv <= 1024 && (H == 0 || (Hk > 0 && H % Hk == 0)) &&
          static_cast<int64_t>(B) * H * ((T + kC - 1) / kC) * ((dv + 15) / 16) < INT_MAX &&
          static_cast<int64_t>(B) * H * ((dv + 15) / 16) < INT_MAX && static_cast<int64_t>(B) * T < INT_MAX;
 }
@@ -1927,10 +1925,10 @@ int check_common(const char *what, const Gdn &a, const void *saved, size_t saved
         what);
   if (!aligned(a.q, 2) || !aligned(a.k, 2) || !aligned(a.v, 2) || !aligned(a.la, 4) || !aligned(a.beta, 4) ||
       !aligned(a.lens, 4) || !aligned(a.err, 4) || !aligned(a.state_in, 4) || !aligned(a.state_out, 4) ||
-          !aligned(saved, 16))
+      !aligned(saved, 16))
     return set_error(SDM_ERR_ALIGN, "%s: a pointer is not aligned", what);
-  if (saved_bytes < l.saved) return set_error(SDM_ERR_INVALID_ARG, "%s: saved holds %zu bytes, %zu needed", what,
-      saved_bytes, l.saved);
+  if (saved_bytes < l.saved)
+    return set_error(SDM_ERR_INVALID_ARG, "%s: saved holds %zu bytes, %zu needed", what, saved_bytes, l.saved);
   return SDM_OK;
 }
 
@@ -1947,11 +1945,8 @@ int make_map(CUtensorMap *map, const void *p, int64_t ld, int64_t tokens, int he
   static const Encode encode = [] {
     void *f = nullptr;
     cudaDriverEntryPointQueryResult q;
-    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-        &q) == cudaSuccess &&
-                   q == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<Encode>(f)
-               : nullptr;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(f) : nullptr;
   }();
   if (!encode) return set_error(SDM_ERR_CUDA, "gdn_train: the driver has no cuTensorMapEncodeTiled");
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
@@ -1972,8 +1967,8 @@ int make_maps(Maps *m, const Gdn &a) {
   if (a.by_qk == 16) rc = make_map(&m->q, a.q, a.ld_q, tokens, a.Hk, a.dk);
   if (rc == SDM_OK && a.by_qk == 16) rc = make_map(&m->k, a.k, a.ld_k, tokens, a.Hk, a.dk);
   if (rc == SDM_OK && a.by_v == 16) rc = make_map(&m->v, a.v, a.ld_v, tokens, a.H, a.dv);
-  if (rc == SDM_OK && a.dy && a.by_dy == 16) rc = make_map(&m->dy, a.dy, static_cast<int64_t>(a.H) * a.dv, tokens, a.H,
-      a.dv);
+  if (rc == SDM_OK && a.dy && a.by_dy == 16)
+    rc = make_map(&m->dy, a.dy, static_cast<int64_t>(a.H) * a.dv, tokens, a.H, a.dv);
   return rc;
 }
 
@@ -1991,8 +1986,8 @@ void place_saved(Gdn &a, void *saved, const Layout &l) {
 // overlaps that one's end) and waits for it with before_reading().
 template <typename... A>
 int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, int smem, cudaStream_t st, A... args) {
-  cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
-      : cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  if (smem > (48 << 10)) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(SDM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -2038,8 +2033,7 @@ int run_train(const Gdn &a, const Layout &l, cudaStream_t st) {
   int rc = make_maps(&maps, a);
   if (rc != SDM_OK) return rc;
   if (l.units > 0) {
-    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + kScal) * 4 + 16, st, a,
-        maps);
+    rc = launch(gdn_prep<NK>, "gdn_train", l.units, kPrepThreads, (2 * kC * kLd + kScal) * 4 + 16, st, a, maps);
     if (rc != SDM_OK) return rc;
   }
   return run_chain<NK>(a, maps, l, false, st);
@@ -2085,8 +2079,8 @@ extern "C" int gdn_train(const float *state, float *state_out, const uint16_t *q
   a.B = B; a.T = T; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv;
   a.state_in = state; a.state_out = state_out; a.y = y; a.err = dev_err;
   a.drop = test_drop_signal();
-  if (static_cast<int64_t>(B) * H > 0 && (!state_out || (T > 0 && !y))) return set_error(SDM_ERR_INVALID_ARG,
-      "gdn_train: null pointer");
+  if (static_cast<int64_t>(B) * H > 0 && (!state_out || (T > 0 && !y)))
+    return set_error(SDM_ERR_INVALID_ARG, "gdn_train: null pointer");
   const int rc = check_common("gdn_train", a, saved, saved_bytes, l);
   if (rc != SDM_OK) return rc;
   if (!aligned(y, 2)) return set_error(SDM_ERR_ALIGN, "gdn_train: a pointer is not aligned");
@@ -2095,17 +2089,17 @@ extern "C" int gdn_train(const float *state, float *state_out, const uint16_t *q
   a.by_v = row_bytes(v, ld_v, dv);
   a.pair_y = dv % 2 == 0 && aligned(y, 4);
   place_saved(a, saved, l);
-  return dk <= 64 ? run_train<4>(a, l, static_cast<cudaStream_t>(stream)) : run_train<8>(a, l,
-      static_cast<cudaStream_t>(stream));
+  return dk <= 64 ? run_train<4>(a, l, static_cast<cudaStream_t>(stream))
+                  : run_train<8>(a, l, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16_t *q, int64_t ld_q, const uint16_t *k,
                             int64_t ld_k, const uint16_t *v, int64_t ld_v, const float *log_alpha, const float *beta,
                             const uint8_t *reset, const int32_t *lens, const void *saved, size_t saved_bytes,
                             const uint16_t *dy, int B, int T, int Hk, int H, int dk, int dv, uint16_t *dq,
-                                int64_t ld_dq,
-                            uint16_t *dk_out, int64_t ld_dk, uint16_t *dv_out, int64_t ld_dv, float *dlog_alpha,
-                            float *dbeta, void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream) {
+                            int64_t ld_dq, uint16_t *dk_out, int64_t ld_dk, uint16_t *dv_out, int64_t ld_dv,
+                            float *dlog_alpha, float *dbeta, void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                            void *stream) {
   if (B < 0 || T < 0 || Hk < 0 || H < 0) return set_error(SDM_ERR_INVALID_ARG, "gdn_backward: negative size");
   if (!sizes_fit(B, T, Hk, H, dk, dv)) return set_error(SDM_ERR_SHAPE, "gdn_backward: sizes beyond the limits");
   const Layout l = layout_of(B, T, Hk, H, dk, dv);
@@ -2123,10 +2117,9 @@ extern "C" int gdn_backward(const float *dstate, float *dstate_out, const uint16
   const int rc = check_common("gdn_backward", a, saved, saved_bytes, l);
   if (rc != SDM_OK) return rc;
   if (ld_dq < static_cast<int64_t>(Hk) * dk || ld_dk < static_cast<int64_t>(Hk) * dk ||
-      ld_dv < static_cast<int64_t>(H) * dv ||
-      ld_dq >= (1 << 27) || ld_dk >= (1 << 27) || ld_dv >= (1 << 27))
+      ld_dv < static_cast<int64_t>(H) * dv || ld_dq >= (1 << 27) || ld_dk >= (1 << 27) || ld_dv >= (1 << 27))
     return set_error(SDM_ERR_SHAPE,
-        "gdn_backward: a token's row must be at most 2^27 elements from the next and hold its heads");
+                     "gdn_backward: a token's row must be at most 2^27 elements from the next and hold its heads");
   if (!aligned(dy, 2) || !aligned(dq, 2) || !aligned(dk_out, 2) || !aligned(dv_out, 2) || !aligned(dlog_alpha, 4) ||
       !aligned(dbeta, 4) || !aligned(workspace, 16))
     return set_error(SDM_ERR_ALIGN, "gdn_backward: a pointer is not aligned");

@@ -14,8 +14,12 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "umma.cuh"
+
 namespace sdm {
 namespace mma {
+
+using umma::ldsm_x4_trans;
 
 constexpr int kPanel = 64 * 128;
 
@@ -30,12 +34,6 @@ __device__ __forceinline__ void ldsm4(uint32_t saddr, uint32_t (&r)[4]) {
                : "r"(saddr)
                : "memory");
 }
-__device__ __forceinline__ void ldsm4_t(uint32_t saddr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(saddr)
-               : "memory");
-}
 
 // B fragments of two n-tiles (n0 .. n0+15) and one k-step from tile[n][k]: r[0], r[1] of the first, r[2], r[3]
 // of the second
@@ -44,7 +42,7 @@ __device__ __forceinline__ void b_rows(uint32_t tile, int n0, int k0, int lane, 
 }
 // the same from tile[k][n]
 __device__ __forceinline__ void b_cols(uint32_t tile, int n0, int k0, int lane, uint32_t (&r)[4]) {
-  ldsm4_t(tile + piece(k0 + (((lane >> 3) & 1) << 3) + (lane & 7), (n0 >> 3) + (lane >> 4)), r);
+  ldsm_x4_trans(tile + piece(k0 + (((lane >> 3) & 1) << 3) + (lane & 7), (n0 >> 3) + (lane >> 4)), r);
 }
 // A fragment (rows m0 .. m0+15, one k-step) from tile[m][k] ...
 __device__ __forceinline__ void a_rows(uint32_t tile, int m0, int k0, int lane, uint32_t (&r)[4]) {
@@ -52,7 +50,7 @@ __device__ __forceinline__ void a_rows(uint32_t tile, int m0, int k0, int lane, 
 }
 // ... and from tile[k][m]
 __device__ __forceinline__ void a_cols(uint32_t tile, int m0, int k0, int lane, uint32_t (&r)[4]) {
-  ldsm4_t(tile + piece(k0 + ((lane >> 4) << 3) + (lane & 7), (m0 >> 3) + ((lane >> 3) & 1)), r);
+  ldsm_x4_trans(tile + piece(k0 + ((lane >> 4) << 3) + (lane & 7), (m0 >> 3) + ((lane >> 3) & 1)), r);
 }
 
 // d += a b
@@ -167,10 +165,10 @@ __device__ __forceinline__ void clear_rows(unsigned char *tile, int live, int ti
 // a panel of a tensor map's [token][head][channel] (box: 64 tokens, one head, 64 channels), by one thread;
 // completes its 8 KB on the mbarrier.  channel: a multiple of 64
 __device__ __forceinline__ void tensor_panel(uint32_t dst, const void *map, int channel, int head, int token,
-    uint32_t mbar) {
+                                             uint32_t mbar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
-          dst),
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n" ::"r"(dst),
       "l"(map), "r"(channel), "r"(head), "r"(token), "r"(mbar)
       : "memory");
 }

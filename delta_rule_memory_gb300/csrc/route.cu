@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_back_kernel(const R
         for (int r = 0; r < V; ++r)
 #pragma unroll
           for (int i = 0; i < U; ++i)
-            if (j[r] >= 0 &&
-                c + 32 * i < pieces) v[r][i] = (static_cast<const R *>(a.rows) + j[r] * pieces)[c + 32 * i];
+            if (j[r] >= 0 && c + 32 * i < pieces)
+              v[r][i] = (static_cast<const R *>(a.rows) + j[r] * pieces)[c + 32 * i];
 #pragma unroll
         for (int r = 0; r < V; ++r)
 #pragma unroll
@@ -434,12 +434,12 @@ unsigned row_grid(int64_t items) {
 
 int check_rows(const char *what, int dtype, int64_t M, int k, int N, int D, int64_t ld) {
   if (M < 0 || k < 0 || N < 0 || D < 0) return set_error(SDM_ERR_INVALID_ARG, "%s: negative size", what);
-  if (dtype != SDM_DTYPE_F32 && dtype != SDM_DTYPE_BF16) return set_error(SDM_ERR_UNSUPPORTED, "%s: unknown dtype",
-      what);
+  if (dtype != SDM_DTYPE_F32 && dtype != SDM_DTYPE_BF16)
+    return set_error(SDM_ERR_UNSUPPORTED, "%s: unknown dtype", what);
   if (k > 32 || N > kMaxParts || M >= (1ll << 31) || M * k >= (1ll << 31) - kBlock || D >= (1 << 24))
     return set_error(SDM_ERR_SHAPE, "%s: need k <= 32, N <= %d, M k < 2^31 - 4096, D < 2^24", what, kMaxParts);
-  if (ld < D || ld >= (1 << 27)) return set_error(SDM_ERR_SHAPE,
-      "%s: rows must be at least D and less than 2^27 elements apart", what);
+  if (ld < D || ld >= (1 << 27))
+    return set_error(SDM_ERR_SHAPE, "%s: rows must be at least D and less than 2^27 elements apart", what);
   return SDM_OK;
 }
 
@@ -458,8 +458,8 @@ extern "C" int route_sort(const int32_t *sel, int64_t M, int k, int N, int32_t *
                           void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream) {
   const int rc = check_rows("route_sort", SDM_DTYPE_F32, M, k, N, 0, 0);
   if (rc != SDM_OK) return rc;
-  if (!offsets || (M * k > 0 && (!sel || !order || !place))) return set_error(SDM_ERR_INVALID_ARG,
-      "route_sort: null pointer");
+  if (!offsets || (M * k > 0 && (!sel || !order || !place)))
+    return set_error(SDM_ERR_INVALID_ARG, "route_sort: null pointer");
   const size_t need = route_sort_workspace_size(M, k, N);
   if (need && (!workspace || workspace_bytes < need))
     return set_error(SDM_ERR_INVALID_ARG, "route_sort: workspace of %zu bytes needed", need);
@@ -496,8 +496,10 @@ void by_type(int dtype, int bytes, F f) {
   if (dtype == SDM_DTYPE_F32)
     bytes == 16 ? f(0.f, Tag<16>()) : bytes == 8 ? f(0.f, Tag<8>()) : f(0.f, Tag<4>());
   else
-    bytes == 16 ? f(uint16_t(0), Tag<16>()) : bytes == 8 ? f(uint16_t(0), Tag<8>()) : bytes == 4 ? f(uint16_t(0),
-        Tag<4>()) : f(uint16_t(0), Tag<2>());
+    bytes == 16  ? f(uint16_t(0), Tag<16>())
+    : bytes == 8 ? f(uint16_t(0), Tag<8>())
+    : bytes == 4 ? f(uint16_t(0), Tag<4>())
+                 : f(uint16_t(0), Tag<2>());
 }
 // items of M rows in stretches of 32 u pieces
 int64_t items(int64_t M, int D, int es, int bytes, int u) { return M * ((D / (bytes / es) + 32 * u - 1) / (32 * u)); }
@@ -505,8 +507,7 @@ int64_t items(int64_t M, int D, int es, int bytes, int u) { return M * ((D / (by
 }  // namespace
 
 extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_t *place, const int32_t *offsets,
-    int64_t M,
-                            int k, int N, int D, void *rows, void *stream) {
+                            int64_t M, int k, int N, int D, void *rows, void *stream) {
   const int rc = check_rows("route_gather", dtype, M, k, N, D, ld_x);
   if (rc != SDM_OK) return rc;
   if (M == 0 || k == 0 || D == 0) return SDM_OK;
@@ -518,8 +519,8 @@ extern "C" int route_gather(const void *x, int64_t ld_x, int dtype, const int32_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bytes = piece_bytes(es, D, ld_x, {x, rows});
   by_type(dtype, bytes, [&](auto e, auto n) {
-    route_gather_kernel<n.value, sizeof e><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0,
-        st>>>(a);
+    const unsigned grid = row_grid(items(M, D, es, n.value, kStretch<n.value>));
+    route_gather_kernel<n.value, sizeof e><<<grid, kRowThreads, 0, st>>>(a);
   });
   return check_launch("route_gather");
 }
@@ -536,16 +537,15 @@ extern "C" int route_combine(const void *rows, int dtype, const int32_t *place, 
   RowArgs a{nullptr, rows, y, D, place, nullptr, w, nullptr, M, k, 0, D};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   by_type(dtype, piece_bytes(es, D, D, {rows, y}), [&](auto e, auto n) {
-    route_combine_kernel<decltype(e), n.value><<<row_grid(items(M, D, es, n.value, kStretch<n.value>)), kRowThreads, 0,
-        st>>>(a);
+    const unsigned grid = row_grid(items(M, D, es, n.value, kStretch<n.value>));
+    route_combine_kernel<decltype(e), n.value><<<grid, kRowThreads, 0, st>>>(a);
   });
   return check_launch("route_combine");
 }
 
 extern "C" int route_combine_backward(const void *dy, int64_t ld_dy, int dtype, const void *rows, const int32_t *place,
                                       const float *w, const int32_t *offsets, int64_t M, int k, int N, int D,
-                                          void *drows,
-                                      float *dw, void *stream) {
+                                      void *drows, float *dw, void *stream) {
   const int rc = check_rows("route_combine_backward", dtype, M, k, N, D, ld_dy);
   if (rc != SDM_OK) return rc;
   if (M == 0 || k == 0) return SDM_OK;
