@@ -34,7 +34,8 @@
 // Precision.  q, k, v and dy are exact in bf16.  What is not (S, G, T, M, Z, U, X) is taken in three bf16
 // parts, all 24 bits of it; y, dq, dk and dv are rounded to bf16 once, from fp32 sums.
 //
-// B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 86 us, gdn_chain 318, gdn_chain_back 383, gdn_grad 360.
+// B = 4, T = 4096, H = 16, dk = dv = 128: gdn_prep 89 us, gdn_chain 344 (with two parts behind y 318),
+// gdn_chain_back 384, gdn_grad 419.
 #include <cuda.h>
 
 #include <algorithm>
@@ -408,10 +409,10 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep(const Gdn a, const __gr
 // another wrote; a stage of copies is asked for again once all have left it.  A tile's state lives in shared
 // memory as its three bf16 parts, which are all 24 bits of it, in the order of the A fragments that every
 // product with it takes.
-// Bound by latency where a tile has an SM to itself (M = H = 4; 1.75 us a chunk forward, 1.96 backward at dk =
+// Bound by latency where a tile has an SM to itself (M = H = 4; 1.9 us a chunk forward, 2.0 backward at dk =
 // dv = 128; M = 2 and H = 1, all warps meeting once a chunk, took 2.6 and 3.4, one warp for everything 7.6 and
-// 6.5).  Where four tiles share an SM (M = 2, H = 1; 5.0 and 6.0 us a chunk) by the tensor cores, about 6,000 of
-// 9,700 and 6,500 of 11,700 cycles, and shared memory beside them: mma.sync runs at 600 TFLOP/s.  Loops are kept
+// 6.5).  Where four tiles share an SM (M = 2, H = 1; 5.4 and 6.0 us a chunk) by the tensor cores, about 6,500 of
+// 10,500 and of 11,700 cycles, and shared memory beside them: mma.sync runs at 600 TFLOP/s.  Loops are kept
 // small: unrolled four times the backward chain is a fifth slower, its instructions no longer at hand.
 // ---------------------------------------------------------------------------
 template <int NK, bool BACK, int W, int M, int H>
@@ -1299,17 +1300,18 @@ __global__ void __launch_bounds__(kChainThreads<W, M, H>, 1) gdn_chain_back(cons
 // QK and KK for the decays' gradient and, like dQ2, in X's and N's place; dK2 in dKa's.  The tensor cores cut a
 // sum off at each product, towards 0, so a sum with fewer products behind it is nearer: with dQ2 and dK2 on top of
 // dQ and dK those were 5.9e-7 and 8.5e-7 off.
-// The value columns come 32 at a time, as the chains left them, read ahead by a piece: S by bulk copies (through
-// registers alone, whose loads wait for one another at the door, 404 us in place of 360), the rest 16 bytes a
-// lane.  They are split into bf16 parts and stored as the 8 x 8 cores of the operands, where a warp's store is
-// 128 bytes in a row.  K and Q come last, in the states' place, while X and N are converted.  The operands of the
-// sums over value columns have their rows of 8 along M or N (MN-major); X, N, K and Q serve both ways as they lie.
+// The value columns come 32 at a time, as the chains left them, read ahead by a piece: S by bulk copies, G and the
+// rest 16 bytes a lane (a copy of G too would not leave room for a second CTA an SM; states through registers
+// alone, whose loads wait for one another at the door, took 404 us where copies took 360).  They are split into
+// bf16 parts and stored as the 8 x 8 cores of the operands, where a warp's store is 128 bytes in a row.  K and Q
+// come last, in the states' place, while X and N are converted.  The operands of the sums over value columns have
+// their rows of 8 along M or N (MN-major); X, N, K and Q serve both ways as they lie.
 // With dk <= 64 the products' upper 64 channels are whatever lies behind S and G; rows of a product do not mix,
-// and those are not read.  A CTA needs half of an SM's shared memory,
-// registers and tensor memory, so that one's conversions run beside the other's products.  A chunk's 320 KB are
-// read and its 48 KB written at 4.2 TB/s; what bounds it is the latency of each piece's loads, conversions and
-// products in turn (26,000 cycles a chunk and SM, of them 10,200 of issue and 4,000 of products).  On mma.sync,
-// with accumulators in registers and one CTA an SM, it took 705 us.
+// and those are not read.  A CTA needs half of an SM's shared memory, registers and tensor memory, so that one's
+// conversions run beside the other's products.  A chunk's 240 KB are read and its 48 KB written at 2.8 TB/s; what
+// bounds it is the latency of each piece's loads, conversions and products in turn (30,000 cycles a chunk and SM,
+// of them 12,100 of issue and about 7,000 of products).  On mma.sync, with accumulators in registers and one CTA
+// an SM, it took 705 us, where this form, with two parts behind dk and the decays' gradient by a difference, took 360.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -2004,9 +2006,9 @@ int launch(void (*kernel)(A...), const char *what, int64_t grid, int threads, in
   return SDM_OK;
 }
 
-// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (1.75 us a chunk forward), else two
-// (3.0), else four (5.0), which share an SM's tensor cores and the chunk's tiles; two turns of the SMs with half
-// as many would take 3.5 and 6.0.
+// Tiles of 16 columns a CTA: one where every tile can have an SM of its own (1.9 us a chunk forward), else two
+// (3.4), else four (5.4), which share an SM's tensor cores and the chunk's tiles; two turns of the SMs with half
+// as many would take 3.8 and 6.7.
 int chain_width(const Gdn &a, const Layout &l) {
   const int64_t all = l.tiles * a.B * a.H;
   return all <= kSms || l.tiles == 1 ? 1 : all <= 2 * kSms || l.tiles == 2 ? 2 : 4;

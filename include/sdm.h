@@ -659,7 +659,7 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * saved     : gdn_train_saved_size() bytes, 16-byte aligned, written by
  *             gdn_train and read by gdn_backward with the same inputs and sizes: per
  *             64 tokens of a head their decays, two triangular matrices, the state
- *             and the residuals E (127.5 KB at dk = dv = 128).
+ *             and the residuals E (127.5 KB at dk = dv = 128).  The backward does not read v again.
  *
  * gdn_backward: dstate fp32 [B,H,dk,dv] = dL/dS_T (NULL: zero), dstate_out =
  * dL/dS_0 (may be dstate itself); dy bf16 [B,T,H,dv]; dq, dk, dv bf16 laid out
@@ -673,7 +673,9 @@ SDM_API int ckpt8_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
  * Both are deterministic.  Chunks of 64 tokens: one kernel for what a chunk
  * needs of itself, one that runs the chunks in order (16 value columns to three to eight warps), and in
  * the backward one for the sums over value columns.  States, sums and
- * decays are fp32 (the sums of log_alpha wider); y, dq, dk and dv are rounded once, to nearest even.
+ * decays are fp32 (the sums of log_alpha wider), and what enters the tensor cores is taken in three
+ * bf16 parts, 24 bits; y, dq, dk and dv are rounded once, to nearest even.  dlog_alpha is summed from
+ * terms that each pass the token's decay, so it is as exact, relative to itself, at strong decays as at weak ones.
  * NaN and infinities are not looked for: they spread over the 64 tokens of their chunk
  * and the tokens of the row behind it, other documents' among them (in the backward, over
  * those before it).  They do not reach other sequences or heads.
